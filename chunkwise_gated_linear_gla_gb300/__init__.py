@@ -14,5 +14,8 @@ from .binding import (  # noqa: F401
     gla_fwd_workspace_size, gla_host_release, gla_pair_combine, gla_pair_scan, gla_segment_pair,
     gla_segment_pair_workspace_size, gla_status_string, gla_version, make_params, pair_combine, pair_scan,
     segment_pair,
+    GLA_NORM_L2, GLA_NORM_NONE, GLA_NORM_RMS, delta_backward, delta_forward, gla_delta_bwd,
+    gla_delta_bwd_workspace_size, gla_delta_fwd, gla_delta_fwd_workspace_size, gla_qk_norm_rope,
+    gla_qk_norm_rope_bwd, gla_qk_norm_rope_bwd_workspace_size, qk_norm_rope_backward, qk_norm_rope_forward,
 )
-from .autograd import gla_attention  # noqa: F401,E402
+from .autograd import delta_attention, gla_attention, qk_norm_rope  # noqa: F401,E402

@@ -7,6 +7,12 @@ both passes runs in the library's kernels.
 Gradients reach q, k, v (in their dtype: the library returns fp32 gradients, cast here),
 log_g and S0 (fp32), for every gate mode but the bilinear one. Nothing is kept from the
 forward pass but its inputs: the backward recomputes the chunk states (gla_bwd's design).
+
+    O, ST = delta_attention(q, k, v, log_g, beta, S0)     # the gated delta rule
+    q, k = qk_norm_rope(q, k, norm="l2", inv_freq=f)      # norms of q and k, position rotation
+
+delta_attention's backward runs gla_delta_bwd and qk_norm_rope's gla_qk_norm_rope_bwd; both
+keep their inputs only.
 """
 from __future__ import annotations
 
@@ -42,7 +48,66 @@ def _function():
     return GLAFunction
 
 
+def _delta_function():
+    import torch
+
+    class DeltaFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, log_g, beta, S0, scale, path):
+            O, ST = _b.delta_forward(q, k, v, log_g, beta, S0, scale=scale, path=path)
+            ctx.scale, ctx.path = scale, path
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(q, k, v, log_g, beta, S0)
+            return O, ST
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dO, dST):
+            q, k, v, log_g, beta, S0 = ctx.saved_tensors
+            if dO is None and dST is None:
+                return (None,) * 8
+            dO = torch.zeros_like(v) if dO is None else dO.to(q.dtype).contiguous()
+            dST = None if dST is None else dST.to(torch.float32).contiguous()
+            want = ctx.needs_input_grad
+            g = _b.delta_backward(q, k, v, log_g, beta, S0, dO, dST, scale=ctx.scale,
+                                  want_dS0=S0 is not None and want[5], path=ctx.path)
+            return (*(x if w else None for x, w in zip(g, want)), None, None)
+
+    return DeltaFunction
+
+
+def _qk_function():
+    import torch
+
+    class QkNormRopeFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, w_q, w_k, inv_freq, positions, norm, eps, start, interleaved):
+            qo, ko = _b.qk_norm_rope_forward(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved)
+            ctx.how = norm, eps, start, interleaved
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(q, k, w_q, w_k, inv_freq, positions)
+            return qo, ko
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dqo, dko):
+            q, k, w_q, w_k, inv_freq, positions = ctx.saved_tensors
+            if dqo is None and dko is None:
+                return (None,) * 10
+            norm, eps, start, interleaved = ctx.how
+            want = ctx.needs_input_grad
+            dense = lambda g, x: (torch.zeros(x.shape, dtype=x.dtype, device=x.device) if g is None
+                                  else g.to(x.dtype).contiguous())
+            g = _b.qk_norm_rope_backward(q, k, dense(dqo, q), None if k is None else dense(dko, k), norm, w_q, w_k,
+                                         eps, inv_freq, positions, start, interleaved)
+            return (*(x if w else None for x, w in zip(g, want)), None, None, None, None, None, None)
+
+    return QkNormRopeFunction
+
+
 _FN = None
+_DELTA = None
+_QK = None
 
 
 def gla_attention(q, k, v, log_g=None, S0=None, gate=None):
@@ -52,3 +117,21 @@ def gla_attention(q, k, v, log_g=None, S0=None, gate=None):
     if _FN is None:
         _FN = _function()
     return _FN.apply(q, k, v, log_g, S0, gate)
+
+
+def delta_attention(q, k, v, log_g, beta, S0=None, scale=None, path=_b.GLA_PATH_AUTO):
+    """(O, S_T) of the gated delta rule (binding.delta_forward), differentiable once in q, k, v, log_g, beta
+    and S0. The inputs must be contiguous device tensors."""
+    global _DELTA
+    if _DELTA is None:
+        _DELTA = _delta_function()
+    return _DELTA.apply(q, k, v, log_g, beta, S0, scale, path)
+
+
+def qk_norm_rope(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv_freq=None, positions=None, start=0,
+                 interleaved=False):
+    """binding.qk_norm_rope_forward, differentiable once in q, k and the weights."""
+    global _QK
+    if _QK is None:
+        _QK = _qk_function()
+    return _QK.apply(q, k, w_q, w_k, inv_freq, positions, norm, eps, start, interleaved)

@@ -16,6 +16,7 @@ from . import build as _build
 GLA_OK, GLA_ERR_INVALID_ARG, GLA_ERR_UNSUPPORTED, GLA_ERR_CUDA, GLA_ERR_WORKSPACE, GLA_ERR_TIMEOUT = range(6)
 GLA_BF16, GLA_FP32 = 0, 1
 GLA_GATE_NONE, GLA_GATE_HEAD_SCALAR, GLA_GATE_PER_KEY, GLA_GATE_TOKEN_SCALAR, GLA_GATE_BILINEAR = 0, 1, 2, 3, 4
+GLA_NORM_NONE, GLA_NORM_L2, GLA_NORM_RMS = 0, 1, 2
 GLA_PATH_AUTO, GLA_PATH_TENSOR, GLA_PATH_SIMT, GLA_PATH_STAGED, GLA_PATH_FUSED, GLA_PATH_SPLIT = 0, 1, 2, 3, 4, 5
 
 # Every symbol include/gla.h declares.
@@ -24,7 +25,9 @@ EXPORTED = ("gla_fwd", "gla_fwd_ex", "gla_fwd_workspace_size", "gla_fwd_num_stag
             "gla_version", "gla_fwd_noalloc", "gla_fwd_host", "gla_host_release", "gla_bwd",
             "gla_bwd_workspace_size", "gla_bwd_num_stages", "gla_bwd_stage", "gla_bwd_stage_name",
             "gla_segment_pair_workspace_size", "gla_segment_pair",
-            "gla_pair_scan", "gla_pair_combine", "gla_selftest_bounded_wait")
+            "gla_pair_scan", "gla_pair_combine", "gla_selftest_bounded_wait",
+            "gla_delta_fwd", "gla_delta_fwd_workspace_size", "gla_delta_bwd", "gla_delta_bwd_workspace_size",
+            "gla_qk_norm_rope", "gla_qk_norm_rope_bwd", "gla_qk_norm_rope_bwd_workspace_size")
 
 
 class GlaError(RuntimeError):
@@ -60,6 +63,53 @@ class gla_bwd_params(ctypes.Structure):
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("path", ctypes.c_int),
         ("log_b", ctypes.c_void_p), ("grad_log_b", ctypes.c_void_p),
+    ]
+
+
+class gla_delta_params(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("log_g", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("S0", ctypes.c_void_p),
+        ("O", ctypes.c_void_p), ("ST", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("T", ctypes.c_int),
+        ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("scale", ctypes.c_float),
+        ("dtype", ctypes.c_int), ("path", ctypes.c_int),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class gla_delta_bwd_params(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("log_g", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("S0", ctypes.c_void_p),
+        ("grad_O", ctypes.c_void_p), ("grad_ST", ctypes.c_void_p),
+        ("grad_q", ctypes.c_void_p), ("grad_k", ctypes.c_void_p), ("grad_v", ctypes.c_void_p),
+        ("grad_log_g", ctypes.c_void_p), ("grad_beta", ctypes.c_void_p), ("grad_S0", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("T", ctypes.c_int),
+        ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("scale", ctypes.c_float),
+        ("dtype", ctypes.c_int), ("path", ctypes.c_int),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class gla_qk_norm_params(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("q_stride", ctypes.c_longlong * 3), ("k_stride", ctypes.c_longlong * 3),
+        ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p),
+        ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("start", ctypes.c_longlong),
+        ("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("T", ctypes.c_int),
+        ("d", ctypes.c_int), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("norm", ctypes.c_int),
+        ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+    ]
+
+
+class gla_qk_norm_grads(ctypes.Structure):
+    _fields_ = [
+        ("grad_q_out", ctypes.c_void_p), ("grad_k_out", ctypes.c_void_p),
+        ("grad_q", ctypes.c_void_p), ("grad_k", ctypes.c_void_p),
+        ("q_stride", ctypes.c_longlong * 3), ("k_stride", ctypes.c_longlong * 3),
+        ("grad_w_q", ctypes.c_void_p), ("grad_w_k", ctypes.c_void_p),
     ]
 
 
@@ -130,6 +180,16 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.gla_selftest_bounded_wait.argtypes = [ctypes.c_uint, i, vp]
         lib.gla_pair_combine.restype = st
         lib.gla_pair_combine.argtypes = [vp, vp, vp, vp, i, i, i, i, vp]
+        D, DB = ctypes.POINTER(gla_delta_params), ctypes.POINTER(gla_delta_bwd_params)
+        N, NG = ctypes.POINTER(gla_qk_norm_params), ctypes.POINTER(gla_qk_norm_grads)
+        for name, restype, argtypes in (
+                ("gla_delta_fwd", st, [D, vp]), ("gla_delta_fwd_workspace_size", ctypes.c_size_t, [D]),
+                ("gla_delta_bwd", st, [DB, vp]), ("gla_delta_bwd_workspace_size", ctypes.c_size_t, [DB]),
+                ("gla_qk_norm_rope", st, [N, vp, vp, vp]),
+                ("gla_qk_norm_rope_bwd", st, [N, NG, vp, ctypes.c_size_t, vp]),
+                ("gla_qk_norm_rope_bwd_workspace_size", ctypes.c_size_t, [N])):
+            f = getattr(lib, name)
+            f.restype, f.argtypes = restype, argtypes
         _lib = lib
         return lib
 
@@ -453,3 +513,286 @@ def pair_combine(log_Gamma2, S2, log_Gamma1, S1, stream=None):
     B, H, dk, dv = S1.shape
     gla_pair_combine(log_Gamma2, S2, log_Gamma1, S1, B, H, dk, dv, stream)
     return log_Gamma1, S1
+
+
+# ---------------------------------------------------------------- the gated delta rule
+
+def gla_delta_fwd(p: gla_delta_params, stream=None, check=True) -> int:
+    s = load().gla_delta_fwd(ctypes.byref(p), _stream(stream))
+    if check:
+        _check(s, "gla_delta_fwd")
+    return s
+
+
+def gla_delta_fwd_workspace_size(p: gla_delta_params) -> int:
+    return load().gla_delta_fwd_workspace_size(ctypes.byref(p))
+
+
+def gla_delta_bwd(p: gla_delta_bwd_params, stream=None, check=True) -> int:
+    s = load().gla_delta_bwd(ctypes.byref(p), _stream(stream))
+    if check:
+        _check(s, "gla_delta_bwd")
+    return s
+
+
+def gla_delta_bwd_workspace_size(p: gla_delta_bwd_params) -> int:
+    return load().gla_delta_bwd_workspace_size(ctypes.byref(p))
+
+
+def _refuse(what):
+    raise GlaError(GLA_ERR_INVALID_ARG, what)
+
+
+def _dense(t, shape, dtype, device, what):
+    """A contiguous tensor of this shape, type and device (the C ABI sees pointers only)."""
+    if t.shape != shape:
+        _refuse(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype != dtype:
+        _refuse(f"{what} is {t.dtype}, not {dtype}")
+    if t.device != device:
+        _refuse(f"{what} is on {t.device}, not on {device}")
+    if not t.is_contiguous():
+        _refuse(f"{what} is not contiguous")
+
+
+def _dtype_code(t, what):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return GLA_BF16
+    if t.dtype == torch.float32:
+        return GLA_FP32
+    _refuse(f"{what} is {t.dtype}, not bfloat16 or float32")
+
+
+def _on_gpu(t, what):
+    if not t.is_cuda:
+        _refuse(f"{what} is on {t.device}, not on a GPU")
+
+
+class _here:
+    """The tensors' device made current for a call (nothing to do when it is already)."""
+    __slots__ = ("dev", "was")
+
+    def __init__(self, device):
+        self.dev, self.was = device.index, None
+
+    def __enter__(self):
+        import torch
+        if torch.cuda.current_device() != self.dev:
+            self.was = torch.cuda.current_device()
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.was is not None:
+            import torch
+            torch.cuda.set_device(self.was)
+
+
+def _used_on(stream, device, *tensors):
+    """Tensors allocated here but used on another stream than the current one are not reused
+    before that stream is done with them."""
+    if stream is None:
+        return
+    import torch
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    if s != torch.cuda.current_stream(device):
+        s.wait_stream(torch.cuda.current_stream(device))
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
+def _delta_shapes(q, k, v, log_g, beta, S0):
+    import torch
+    if q.dim() != 4 or v.dim() != 4:
+        _refuse("q and v have four dimensions: [B,Hk,T,dk] and [B,H,T,dv]")
+    B, Hk, T, dk = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    code, dt, dev = _dtype_code(q, "q"), q.dtype, q.device
+    if Hk == 0 or H % Hk:
+        _refuse(f"{H} heads of v do not divide over {Hk} of q and k")
+    _dense(q, (B, Hk, T, dk), dt, dev, "q")
+    _dense(k, (B, Hk, T, dk), dt, dev, "k")
+    _dense(v, (B, H, T, dv), dt, dev, "v")
+    _dense(beta, (B, H, T), dt, dev, "beta")
+    if log_g is not None:
+        _dense(log_g, (B, H, T), torch.float32, dev, "log_g")
+    if S0 is not None:
+        _dense(S0, (B, H, dk, dv), torch.float32, dev, "S0")
+    return B, H, Hk, T, dk, dv, code, dt, dev
+
+
+def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, path=GLA_PATH_AUTO, stream=None,
+                  O=None, ST=None):
+    """The gated delta rule's forward pass (gla_delta_fwd), outputs and workspace from torch.
+
+    q, k [B,Hk,T,dk], v [B,H,T,dv], beta [B,H,T] (bf16 or fp32, one type); log_g fp32 [B,H,T] or
+    None; S0 fp32 [B,H,dk,dv] or None; scale defaults to dk^-0.5. Returns (O, S_T). A decoding
+    loop passes ST=S0 to carry the state in place. With `stream` the outputs may be used there,
+    and on other streams after it.
+    """
+    import torch
+    B, H, Hk, T, dk, dv, code, dt, dev = _delta_shapes(q, k, v, log_g, beta, S0)
+    if O is not None:
+        _dense(O, (B, H, T, dv), dt, dev, "O")
+    if ST is not None:
+        _dense(ST, (B, H, dk, dv), torch.float32, dev, "ST")
+    _on_gpu(q, "q")
+    if B == 0:
+        _refuse("an empty batch")
+    with _here(dev):
+        new = []
+        if O is None:
+            O = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+            new.append(O)
+        if ST is None and want_state:
+            ST = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+            new.append(ST)
+        p = gla_delta_params(_ptr(q), _ptr(k), _ptr(v), _ptr(log_g), _ptr(beta), _ptr(S0), _ptr(O), _ptr(ST),
+                             B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path)
+        n = gla_delta_fwd_workspace_size(p)
+        if n:
+            ws = _aligned_workspace(n, dev)
+            new.append(ws)
+            p.workspace, p.workspace_bytes = ws.data_ptr(), n
+        _used_on(stream, dev, *new)
+        gla_delta_fwd(p, stream)
+    return O, ST
+
+
+def delta_backward(q, k, v, log_g, beta, S0, dO, dST=None, scale=None, want_dS0=True, path=GLA_PATH_AUTO, stream=None):
+    """The gated delta rule's gradients (gla_delta_bwd): (dq, dk, dv, dlog_g, dbeta, dS0); dq, dk, dv
+    and dbeta in the inputs' type, dlog_g and dS0 fp32, dlog_g None without log_g and dS0 None
+    unless wanted (it is defined without S0 too, a zero state)."""
+    import torch
+    B, H, Hk, T, dk, dv, code, dt, dev = _delta_shapes(q, k, v, log_g, beta, S0)
+    _dense(dO, (B, H, T, dv), dt, dev, "dO")
+    if dST is not None:
+        _dense(dST, (B, H, dk, dv), torch.float32, dev, "dST")
+    _on_gpu(q, "q")
+    if B == 0:
+        _refuse("an empty batch")
+    with _here(dev):
+        gq, gk, gv, gb = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(beta)
+        gg = None if log_g is None else torch.empty_like(log_g)
+        gS = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if want_dS0 else None
+        p = gla_delta_bwd_params(_ptr(q), _ptr(k), _ptr(v), _ptr(log_g), _ptr(beta), _ptr(S0), _ptr(dO), _ptr(dST),
+                                 _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gg), _ptr(gb), _ptr(gS),
+                                 B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path)
+        n = gla_delta_bwd_workspace_size(p)
+        ws = _aligned_workspace(n, dev)
+        if n:
+            p.workspace, p.workspace_bytes = ws.data_ptr(), n
+        _used_on(stream, dev, gq, gk, gv, gg, gb, gS, ws)
+        gla_delta_bwd(p, stream)
+    return gq, gk, gv, gg, gb, gS
+
+
+# ---------------------------------------------------------------- norms of q and k, and the rotation
+
+_NORMS = {None: GLA_NORM_NONE, "l2": GLA_NORM_L2, "rms": GLA_NORM_RMS}
+
+
+def gla_qk_norm_rope(p: gla_qk_norm_params, q_out, k_out, stream=None, check=True) -> int:
+    s = load().gla_qk_norm_rope(ctypes.byref(p), _ptr(q_out), _ptr(k_out), _stream(stream))
+    if check:
+        _check(s, "gla_qk_norm_rope")
+    return s
+
+
+def gla_qk_norm_rope_bwd(p: gla_qk_norm_params, g: gla_qk_norm_grads, workspace=None, stream=None, check=True) -> int:
+    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    s = load().gla_qk_norm_rope_bwd(ctypes.byref(p), ctypes.byref(g), _ptr(workspace), n, _stream(stream))
+    if check:
+        _check(s, "gla_qk_norm_rope_bwd")
+    return s
+
+
+def gla_qk_norm_rope_bwd_workspace_size(p: gla_qk_norm_params) -> int:
+    return load().gla_qk_norm_rope_bwd_workspace_size(ctypes.byref(p))
+
+
+def _strides(t):
+    """(batch, head, token) strides; those of dimensions of one are never stepped and count as 0."""
+    n, s = t.shape, t.stride()
+    return tuple(s[i] if n[i] > 1 else 0 for i in range(3))
+
+
+def _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved):
+    import torch
+    if norm not in _NORMS:
+        _refuse(f"norm is None, 'l2' or 'rms', not {norm!r}")
+    if q.dim() != 4:
+        _refuse("q has four dimensions: [B,H,T,d]")
+    B, H, T, d = q.shape
+    code, dev = _dtype_code(q, "q"), q.device
+    Hk = 0
+    if k is not None:
+        if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, T, d):
+            _refuse(f"k has shape {tuple(k.shape)}, not [{B},Hk,{T},{d}]")
+        if k.dtype != q.dtype or k.device != dev:
+            _refuse("k has another type or device than q")
+        Hk = k.shape[1]
+    for t, what in ((q, "q"), (k, "k")):
+        if t is not None and t.stride(3) != 1 and d > 1:
+            _refuse(f"the last dimension of {what} is not contiguous")
+    for w, what in ((w_q, "w_q"), (w_k, "w_k")):
+        if w is not None:
+            _dense(w, (d,), torch.float32, dev, what)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _dense(inv_freq, (rot // 2,), torch.float64, dev, "inv_freq")
+    if positions is not None:
+        _dense(positions, (B, T), torch.int64, dev, "positions")
+    _on_gpu(q, "q")
+    return gla_qk_norm_params(_ptr(q), _ptr(k), _strides(q), (0, 0, 0) if k is None else _strides(k), _ptr(w_q),
+                              _ptr(w_k), _ptr(inv_freq), _ptr(positions), start, B, H, Hk, T, d, rot,
+                              1 if interleaved else 0, _NORMS[norm], eps, code)
+
+
+def qk_norm_rope_forward(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv_freq=None, positions=None, start=0,
+                         interleaved=False, stream=None):
+    """Norm, weight and position rotation of every row of q [B,H,T,d] and k [B,Hk,T,d] (or None) in
+    one pass (gla_qk_norm_rope). Inputs may be strided views, the last dimension contiguous;
+    returns dense (q', k'). inv_freq: fp64 [rot/2], radians per position (None: no rotation);
+    positions: int64 [B,T], else start + t."""
+    import torch
+    p = _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved)
+    with _here(q.device):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        _used_on(stream, q.device, qo, ko)
+        gla_qk_norm_rope(p, qo, ko, stream)
+    return qo, ko
+
+
+def _rows_like(t):
+    """An uninitialised tensor for t's gradient: token-major as a projection's slices are, when t is
+    such a view, else dense."""
+    import torch
+    if t.is_contiguous() or t.stride(1) >= t.stride(2):
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    B, H, T, d = t.shape
+    return torch.empty((B, T, H, d), dtype=t.dtype, device=t.device).transpose(1, 2)
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, norm="l2", w_q=None, w_k=None, eps=1e-6, inv_freq=None,
+                          positions=None, start=0, interleaved=False, stream=None):
+    """Gradients of qk_norm_rope_forward: (dq, dk, dw_q, dw_k); dq and dk in the inputs' type (token-major
+    where the input is a token-major view), the weights' fp32, None where there is no input."""
+    import torch
+    p = _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved)
+    _dense(dq_out, q.shape, q.dtype, q.device, "dq_out")
+    if k is not None:
+        _dense(dk_out, k.shape, k.dtype, k.device, "dk_out")
+    with _here(q.device):
+        gq, gk = _rows_like(q), None if k is None else _rows_like(k)
+        gwq = None if w_q is None else torch.empty_like(w_q)
+        gwk = None if w_k is None or k is None else torch.empty_like(w_k)
+        g = gla_qk_norm_grads(_ptr(dq_out), _ptr(dk_out) if k is not None else None, _ptr(gq), _ptr(gk),
+                              _strides(gq), (0, 0, 0) if k is None else _strides(gk), _ptr(gwq), _ptr(gwk))
+        ws = _aligned_workspace(gla_qk_norm_rope_bwd_workspace_size(p), q.device)
+        _used_on(stream, q.device, gq, gk, gwq, gwk, ws)
+        gla_qk_norm_rope_bwd(p, g, ws, stream)
+    return gq, gk, gwq, gwk

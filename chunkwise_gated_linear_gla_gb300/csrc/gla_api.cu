@@ -402,6 +402,15 @@ gla_status plan_workspace(const gla_fwd_params* p, size_t* bytes)
     return st;
 }
 
+gla_status device_ready(int* sms)
+{
+    DevCache* c = dev_cache();
+    if (!c) return GLA_ERR_CUDA;
+    if (c->major != 10 || c->minor != 3) return GLA_ERR_UNSUPPORTED;   // built for sm_103a only
+    *sms = c->sms;
+    return GLA_OK;
+}
+
 int* device_status_ptr()
 {
     DevCache* c = dev_cache();

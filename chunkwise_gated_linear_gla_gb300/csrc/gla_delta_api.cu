@@ -1,0 +1,228 @@
+// The C ABI of the gated delta rule: argument checks, the choice of form, workspace layout and
+// launch order. No arithmetic of the method happens here.
+#include <cmath>
+#include <cstring>
+
+#include "gla_delta_internal.h"
+
+namespace gla {
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Range { uintptr_t lo, hi; };
+Range rng(const void* p, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return p ? Range{a, a + bytes} : Range{0, 0};
+}
+bool overlap(Range a, Range b) {
+    if (a.lo == a.hi || b.lo == b.hi) return false;
+    return a.lo < b.hi && b.lo < a.hi;
+}
+
+gla_status check_sizes(int B, int H, int Hk, int T, int dk, int dv, float scale, int dtype, int path)
+{
+    if (B <= 0 || H <= 0 || Hk <= 0 || T < 0 || dk <= 0 || dv <= 0) return GLA_ERR_INVALID_ARG;
+    if (H % Hk != 0 || dk % 16 != 0 || dv % 16 != 0) return GLA_ERR_INVALID_ARG;
+    if (dtype != GLA_BF16 && dtype != GLA_FP32) return GLA_ERR_INVALID_ARG;
+    if (path != GLA_PATH_AUTO && path != GLA_PATH_TENSOR && path != GLA_PATH_SIMT) return GLA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return GLA_ERR_INVALID_ARG;
+    if ((long long)B * H > (1LL << 30)) return GLA_ERR_INVALID_ARG;
+    if (dk > kDeltaMaxDk || dv > (1 << 20)) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+struct DeltaPlan {
+    int path = GLA_PATH_SIMT;
+    size_t ws = 0;
+};
+
+gla_status plan_fwd(const gla_delta_params* p, DeltaPlan& pl)
+{
+    if (!p) return GLA_ERR_INVALID_ARG;
+    gla_status st = check_sizes(p->B, p->H, p->Hk, p->T, p->dk, p->dv, p->scale, p->dtype, p->path);
+    if (st != GLA_OK) return st;
+    if (p->path == GLA_PATH_TENSOR) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+gla_status check_fwd(const gla_delta_params* p)
+{
+    if (p->T > 0 && (!p->q || !p->k || !p->v || !p->beta || !p->O)) return GLA_ERR_INVALID_ARG;
+    for (const void* x : {p->q, p->k, p->v, (const void*)p->O, (const void*)p->S0, (const void*)p->ST})
+        if (!aligned(x, 16)) return GLA_ERR_INVALID_ARG;
+    const size_t e = p->dtype == GLA_BF16 ? 2 : 4;
+    if (!aligned(p->log_g, 4) || !aligned(p->beta, e) || !aligned(p->workspace, 256)) return GLA_ERR_INVALID_ARG;
+    const size_t BHT = (size_t)p->B * p->H * p->T, nk = (size_t)p->B * p->Hk * p->T * p->dk * e;
+    const size_t ns = (size_t)p->B * p->H * p->dk * p->dv * 4;
+    const Range O = rng(p->O, BHT * p->dv * e), ST = rng(p->ST, ns), S0 = rng(p->S0, ns);
+    const Range in[] = {rng(p->q, nk), rng(p->k, nk), rng(p->v, BHT * p->dv * e), rng(p->log_g, BHT * 4),
+                        rng(p->beta, BHT * e)};
+    for (const Range& r : in)
+        if (overlap(O, r) || overlap(ST, r)) return GLA_ERR_INVALID_ARG;
+    if (overlap(O, S0) || overlap(O, ST)) return GLA_ERR_INVALID_ARG;
+    if (overlap(ST, S0) && (const void*)p->ST != (const void*)p->S0) return GLA_ERR_INVALID_ARG;
+    return GLA_OK;
+}
+
+struct DeltaBwdPlan {
+    int path = GLA_PATH_SIMT;
+    int tiles = 0;
+    size_t off_keep = 0, off_pq = 0, off_pk = 0, off_pg = 0, off_pb = 0, off_scr = 0;
+    size_t ws = 0;
+};
+
+gla_status plan_bwd(const gla_delta_bwd_params* p, DeltaBwdPlan& pl)
+{
+    if (!p) return GLA_ERR_INVALID_ARG;
+    gla_status st = check_sizes(p->B, p->H, p->Hk, p->T, p->dk, p->dv, p->scale, p->dtype, p->path);
+    if (st != GLA_OK) return st;
+    if (p->path == GLA_PATH_TENSOR) return GLA_ERR_UNSUPPORTED;
+    if (p->T == 0) return GLA_OK;
+    const size_t BH = (size_t)p->B * p->H, T = p->T;
+    const size_t dkp = p->dk <= 64 ? 64 : p->dk <= 128 ? 128 : 256;
+    size_t off = 0;
+    auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
+    pl.tiles = (p->dv + kDeltaBwdTile - 1) / kDeltaBwdTile;
+    pl.off_keep = take(BH * ((T + kDeltaKeep - 1) / kDeltaKeep) * p->dk * p->dv * 4);
+    pl.off_pq = take(pl.tiles * BH * T * p->dk * 4);
+    pl.off_pk = take(pl.tiles * BH * T * p->dk * 4);
+    pl.off_pg = take(pl.tiles * BH * T * 4);
+    pl.off_pb = take(pl.tiles * BH * T * 4);
+    pl.off_scr = take(pl.tiles * BH * kDeltaKeep * dkp * kDeltaBwdTile * 4);
+    pl.ws = off;
+    return GLA_OK;
+}
+
+gla_status check_bwd(const gla_delta_bwd_params* p)
+{
+    if (p->T > 0 && (!p->q || !p->k || !p->v || !p->beta || !p->grad_O || !p->grad_q || !p->grad_k || !p->grad_v))
+        return GLA_ERR_INVALID_ARG;
+    if (p->grad_log_g && !p->log_g && p->T > 0) return GLA_ERR_INVALID_ARG;
+    for (const void* x : {p->q, p->k, p->v, p->grad_O, (const void*)p->S0, (const void*)p->grad_ST,
+                          (const void*)p->grad_q, (const void*)p->grad_k, (const void*)p->grad_v,
+                          (const void*)p->grad_S0})
+        if (!aligned(x, 16)) return GLA_ERR_INVALID_ARG;
+    const size_t e = p->dtype == GLA_BF16 ? 2 : 4;
+    if (!aligned(p->log_g, 4) || !aligned(p->grad_log_g, 4) || !aligned(p->beta, e) || !aligned(p->grad_beta, e) ||
+        !aligned(p->workspace, 256))
+        return GLA_ERR_INVALID_ARG;
+    const size_t BHT = (size_t)p->B * p->H * p->T, nk = (size_t)p->B * p->Hk * p->T * p->dk * e;
+    const size_t nv = BHT * p->dv * e, ns = (size_t)p->B * p->H * p->dk * p->dv * 4;
+    const Range in[] = {rng(p->q, nk), rng(p->k, nk), rng(p->v, nv), rng(p->log_g, BHT * 4), rng(p->beta, BHT * e),
+                        rng(p->S0, ns), rng(p->grad_O, nv), rng(p->grad_ST, ns)};
+    const Range out[] = {rng(p->grad_q, nk), rng(p->grad_k, nk), rng(p->grad_v, nv), rng(p->grad_log_g, BHT * 4),
+                         rng(p->grad_beta, BHT * e), rng(p->grad_S0, ns)};
+    const int no = sizeof(out) / sizeof(out[0]);
+    for (int i = 0; i < no; ++i) {
+        for (const Range& r : in)
+            if (overlap(out[i], r)) return GLA_ERR_INVALID_ARG;
+        for (int j = i + 1; j < no; ++j)
+            if (overlap(out[i], out[j])) return GLA_ERR_INVALID_ARG;
+    }
+    return GLA_OK;
+}
+
+DeltaStep step_args(const gla_delta_params* p, int sms)
+{
+    DeltaStep a;
+    a.q = p->q; a.k = p->k; a.v = p->v; a.log_g = p->log_g; a.beta = p->beta;
+    a.S0 = p->S0; a.O = p->O; a.ST = p->ST; a.keep = nullptr;
+    a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.dv = p->dv;
+    a.scale = p->scale; a.dtype = p->dtype; a.sms = sms;
+    return a;
+}
+
+}  // namespace
+}  // namespace gla
+
+using namespace gla;
+
+extern "C" {
+
+size_t gla_delta_fwd_workspace_size(const gla_delta_params* p)
+{
+    DeltaPlan pl;
+    return plan_fwd(p, pl) == GLA_OK ? pl.ws : 0;
+}
+
+gla_status gla_delta_fwd(const gla_delta_params* p, cudaStream_t stream)
+{
+    DeltaPlan pl;
+    gla_status st = plan_fwd(p, pl);
+    if (st != GLA_OK) return st;
+    st = check_fwd(p);
+    if (st != GLA_OK) return st;
+    int sms = 0;
+    st = device_ready(&sms);
+    if (st != GLA_OK) return st;
+    if (pl.ws > 0 && (!p->workspace || p->workspace_bytes < pl.ws)) return GLA_ERR_WORKSPACE;
+    cudaError_t e = cudaSuccess;
+    if (p->T == 0) {
+        const size_t ns = (size_t)p->B * p->H * p->dk * p->dv * 4;
+        if (p->ST && p->ST != p->S0)
+            e = p->S0 ? cudaMemcpyAsync(p->ST, p->S0, ns, cudaMemcpyDeviceToDevice, stream)
+                      : cudaMemsetAsync(p->ST, 0, ns, stream);
+    } else {
+        e = launch_delta_step(step_args(p, sms), stream);
+    }
+    return e == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+}
+
+size_t gla_delta_bwd_workspace_size(const gla_delta_bwd_params* p)
+{
+    DeltaBwdPlan pl;
+    return plan_bwd(p, pl) == GLA_OK ? pl.ws : 0;
+}
+
+gla_status gla_delta_bwd(const gla_delta_bwd_params* p, cudaStream_t stream)
+{
+    DeltaBwdPlan pl;
+    gla_status st = plan_bwd(p, pl);
+    if (st != GLA_OK) return st;
+    st = check_bwd(p);
+    if (st != GLA_OK) return st;
+    int sms = 0;
+    st = device_ready(&sms);
+    if (st != GLA_OK) return st;
+    if (pl.ws > 0 && (!p->workspace || p->workspace_bytes < pl.ws)) return GLA_ERR_WORKSPACE;
+    cudaError_t e = cudaSuccess;
+    if (p->T == 0) {
+        const size_t ns = (size_t)p->B * p->H * p->dk * p->dv * 4;
+        if (p->grad_S0)
+            e = p->grad_ST ? cudaMemcpyAsync(p->grad_S0, p->grad_ST, ns, cudaMemcpyDeviceToDevice, stream)
+                           : cudaMemsetAsync(p->grad_S0, 0, ns, stream);
+        return e == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+    auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+    DeltaStep a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = p->q; a.k = p->k; a.v = p->v; a.log_g = p->log_g; a.beta = p->beta; a.S0 = p->S0;
+    a.keep = f(pl.off_keep);
+    a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.dv = p->dv;
+    a.scale = p->scale; a.dtype = p->dtype; a.sms = sms;
+    e = launch_delta_step(a, stream);
+    if (e == cudaSuccess) {
+        DeltaBwdStep w;
+        w.q = p->q; w.k = p->k; w.v = p->v; w.log_g = p->log_g; w.beta = p->beta;
+        w.keep = f(pl.off_keep); w.dO = p->grad_O; w.dST = p->grad_ST; w.dv_out = p->grad_v; w.dS0 = p->grad_S0;
+        w.part_q = f(pl.off_pq); w.part_k = f(pl.off_pk); w.part_g = f(pl.off_pg); w.part_b = f(pl.off_pb);
+        w.scratch = f(pl.off_scr);
+        w.B = p->B; w.H = p->H; w.Hk = p->Hk; w.T = p->T; w.dk = p->dk; w.dv = p->dv;
+        w.scale = p->scale; w.dtype = p->dtype;
+        e = launch_delta_bwd_step(w, stream);
+    }
+    if (e == cudaSuccess) {
+        DeltaBwdSum w;
+        w.part_q = f(pl.off_pq); w.part_k = f(pl.off_pk); w.part_g = f(pl.off_pg); w.part_b = f(pl.off_pb);
+        w.dq = p->grad_q; w.dk_out = p->grad_k; w.dlog_g = p->grad_log_g; w.dbeta = p->grad_beta;
+        w.tiles = pl.tiles; w.B = p->B; w.H = p->H; w.Hk = p->Hk; w.T = p->T; w.dk = p->dk;
+        w.dtype = p->dtype; w.sms = sms;
+        e = launch_delta_bwd_sum(w, stream);
+    }
+    return e == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -87,6 +87,9 @@ gla_status validate_pointers(const gla_fwd_params* p, bool device);
 // not looked at); the status of validate_args or of planning.
 gla_status plan_workspace(const gla_fwd_params* p, size_t* bytes);
 
+// Whether the current device runs this build (GLA_OK), and its multiprocessors.
+gla_status device_ready(int* sms);
+
 // Device status word (per device), written by kernels whose bounded waits run out.
 int* device_status_ptr();   // nullptr on failure
 

@@ -386,6 +386,135 @@ int gla_bwd_num_stages(const gla_bwd_params* p);
 gla_status gla_bwd_stage(const gla_bwd_params* p, int stage, cudaStream_t stream);
 const char* gla_bwd_stage_name(const gla_bwd_params* p, int stage);
 
+/*
+ * gla_delta_fwd — the gated delta rule. Where the pass above only adds k_t^T v_t to the
+ * decayed state, the delta rule first takes out what the state already answers for k_t
+ * (the recurrence of gated delta networks, whose chunk kernels the FlashQLA talk describes):
+ *
+ *     S~_t = alpha_t S_{t-1},   u_t = beta_t (v_t - k_t S~_t),
+ *     S_t  = S~_t + k_t^T u_t,  o_t = scale q_t S_t,
+ *
+ * alpha_t = exp(log_g_t) one value per token and head (<= 1; -inf, a full reset, is allowed),
+ * beta_t in [0, 1]. Keys are meant to have unit 2-norm (gla_qk_norm_rope makes such rows):
+ * then no step grows the state. H / Hk value heads share one head of q and k (head h reads
+ * h / (H / Hk)). A token with beta = 0 and log_g = 0 leaves the state as it is: that is how a
+ * padded row is passed over.
+ *   GLA_PATH_SIMT    the recurrent form on CUDA cores, token by token, the state in registers:
+ *                    single tokens (decoding; bound by the state's bytes), a few tokens,
+ *                    fp32 inputs and other shapes; dk <= 256.
+ *   GLA_PATH_AUTO    the form that is faster for the sizes.
+ * dk and dv are multiples of 16, q, k, v, O, S0 and ST 16-byte aligned, `scale` finite. ST may
+ * equal S0 (the state carried in place). Other outputs may not overlap inputs. T = 0 copies S0
+ * to ST. Ownership, asynchrony and the workspace are as for gla_fwd_ex.
+ */
+typedef struct {
+    const void* q;          /* [B,Hk,T,dk] dtype */
+    const void* k;          /* [B,Hk,T,dk] dtype */
+    const void* v;          /* [B,H,T,dv] dtype */
+    const float* log_g;     /* [B,H,T] log(alpha_t), or NULL (alpha = 1) */
+    const void* beta;       /* [B,H,T] dtype */
+    const float* S0;        /* [B,H,dk,dv] or NULL (zero) */
+    void* O;                /* [B,H,T,dv] dtype, written */
+    float* ST;              /* [B,H,dk,dv] or NULL (not written); may equal S0 */
+    int B, H, Hk, T, dk, dv;
+    float scale;            /* of the output, commonly dk^-0.5 */
+    gla_dtype dtype;
+    int path;               /* gla_path: AUTO, TENSOR or SIMT */
+    void* workspace;        /* gla_delta_fwd_workspace_size() bytes, 256-byte aligned */
+    size_t workspace_bytes;
+} gla_delta_params;
+
+gla_status gla_delta_fwd(const gla_delta_params* p, cudaStream_t stream);
+/* Bytes of workspace (0 if none, or for invalid parameters); pointers are not looked at. */
+size_t gla_delta_fwd_workspace_size(const gla_delta_params* p);
+
+/*
+ * gla_delta_bwd — the gradients of a scalar loss through gla_delta_fwd, given grad_O and
+ * grad_ST (NULL: zero): grad_q and grad_k (summed over the heads that share a row), grad_v and
+ * grad_beta in `dtype`, each rounded once from fp32; grad_log_g and grad_S0 fp32 (any of
+ * grad_log_g, grad_beta, grad_S0 may be NULL; grad_log_g must be without log_g). Nothing of
+ * the forward call is needed but its inputs. Forms, alignment, ownership and asynchrony as for
+ * the forward call; results are bitwise reproducible.
+ */
+typedef struct {
+    const void* q; const void* k; const void* v; const float* log_g; const void* beta;
+    const float* S0;
+    const void* grad_O;     /* [B,H,T,dv] dtype */
+    const float* grad_ST;   /* [B,H,dk,dv] or NULL */
+    void* grad_q;           /* [B,Hk,T,dk] dtype */
+    void* grad_k;           /* [B,Hk,T,dk] dtype */
+    void* grad_v;           /* [B,H,T,dv] dtype */
+    float* grad_log_g;      /* [B,H,T] or NULL */
+    void* grad_beta;        /* [B,H,T] dtype, or NULL */
+    float* grad_S0;         /* [B,H,dk,dv] or NULL */
+    int B, H, Hk, T, dk, dv;
+    float scale;
+    gla_dtype dtype;
+    int path;
+    void* workspace;        /* gla_delta_bwd_workspace_size() bytes, 256-byte aligned */
+    size_t workspace_bytes;
+} gla_delta_bwd_params;
+
+gla_status gla_delta_bwd(const gla_delta_bwd_params* p, cudaStream_t stream);
+size_t gla_delta_bwd_workspace_size(const gla_delta_bwd_params* p);
+
+/*
+ * gla_qk_norm_rope — the rows of q and k of every head on their way to an attention call, in
+ * one pass: norm, weight, rotation by position, and the dense [B,heads,T,d] layout.
+ *     n(x) = sqrt(sum x^2 + eps)  (GLA_NORM_L2: unit rows, what the delta rule wants)
+ *          = sqrt(mean x^2 + eps) (GLA_NORM_RMS)   or 1 (GLA_NORM_NONE)
+ *     y = R(pos) (w (.) x / n(x)),
+ * w per value (NULL: 1). R turns the pairs of the first `rot` values (a multiple of 16, 0: no
+ * rotation) by pos * inv_freq[i] radians: pair i is (2i, 2i+1) when `interleaved`, else
+ * (i, i + rot/2). The angle is taken modulo a turn in 64-bit integers, so far positions lose
+ * nothing. Position of token t of row b: positions[b,t], or start + t when positions is NULL;
+ * any 64-bit value. Inputs are read through strides in elements (batch, head, token; the last
+ * dimension contiguous), every row starting on 16 bytes; strides may be zero or negative.
+ * d is a multiple of 16 up to 256. Hk = 0 with k = NULL takes q alone.
+ */
+typedef enum { GLA_NORM_NONE = 0, GLA_NORM_L2 = 1, GLA_NORM_RMS = 2 } gla_norm;
+
+typedef struct {
+    const void* q;              /* [B,H,T,d] through q_stride, dtype */
+    const void* k;              /* [B,Hk,T,d] through k_stride, dtype */
+    long long q_stride[3], k_stride[3];
+    const float* w_q;           /* [d] or NULL */
+    const float* w_k;           /* [d] or NULL */
+    const double* inv_freq;     /* [rot/2], device memory; NULL iff rot == 0 */
+    const long long* positions; /* [B,T], device memory, or NULL */
+    long long start;
+    int B, H, Hk, T, d, rot;
+    int interleaved;
+    int norm;                   /* gla_norm */
+    float eps;                  /* >= 0 */
+    gla_dtype dtype;
+} gla_qk_norm_params;
+
+/* q_out [B,H,T,d] and k_out [B,Hk,T,d], dense, 16-byte aligned, apart from every input. */
+gla_status gla_qk_norm_rope(const gla_qk_norm_params* p, void* q_out, void* k_out, cudaStream_t stream);
+
+/*
+ * gla_qk_norm_rope_bwd — its gradients, from grad_q_out and grad_k_out (dense): grad_q and
+ * grad_k in `dtype` through strides of their own (they may be slices of one tensor, each row
+ * apart from every other), grad_w_q and grad_w_k fp32 [d] (NULL: not wanted; must be NULL
+ * without the weight). The workspace holds the weights' partial sums:
+ * gla_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned, 0 without weights. Results are
+ * bitwise reproducible on one device.
+ */
+typedef struct {
+    const void* grad_q_out;
+    const void* grad_k_out;
+    void* grad_q;
+    void* grad_k;
+    long long q_stride[3], k_stride[3];
+    float* grad_w_q;
+    float* grad_w_k;
+} gla_qk_norm_grads;
+
+gla_status gla_qk_norm_rope_bwd(const gla_qk_norm_params* p, const gla_qk_norm_grads* g, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+size_t gla_qk_norm_rope_bwd_workspace_size(const gla_qk_norm_params* p);
+
 /* Synchronises `stream`, then reads and clears the library's device status
  * word for the current device. GLA_ERR_TIMEOUT if a kernel gave up on a
  * bounded wait since the last call, GLA_ERR_CUDA if the stream reports an
