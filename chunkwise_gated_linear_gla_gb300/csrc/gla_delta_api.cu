@@ -33,8 +33,19 @@ gla_status check_sizes(int B, int H, int Hk, int T, int dk, int dv, float scale,
     return GLA_OK;
 }
 
+// Whether the chunk form takes these sizes: bf16, keys of one or two 64-key slabs, dv in halves
+// of its 128-column tile; grid dimensions and TMA coordinates within their types.
+bool chunk_shape_ok(int B, int H, int T, int dk, int dv, int dtype)
+{
+    const long long nch = ((long long)T + kChunk - 1) / kChunk;
+    return dtype == GLA_BF16 && (dk == 64 || dk == 128) && dv % 64 == 0 && (long long)B * H <= 65535 &&
+           (long long)B * H * nch < (1LL << 31) && (long long)B * H * T < (1LL << 40);
+}
+
 struct DeltaPlan {
     int path = GLA_PATH_SIMT;
+    int nch = 0;
+    size_t off_th = 0, off_tl = 0, off_p = 0, off_g = 0;
     size_t ws = 0;
 };
 
@@ -43,7 +54,20 @@ gla_status plan_fwd(const gla_delta_params* p, DeltaPlan& pl)
     if (!p) return GLA_ERR_INVALID_ARG;
     gla_status st = check_sizes(p->B, p->H, p->Hk, p->T, p->dk, p->dv, p->scale, p->dtype, p->path);
     if (st != GLA_OK) return st;
-    if (p->path == GLA_PATH_TENSOR) return GLA_ERR_UNSUPPORTED;
+    const bool ok = chunk_shape_ok(p->B, p->H, p->T, p->dk, p->dv, p->dtype);
+    if (p->path == GLA_PATH_TENSOR && !ok) return GLA_ERR_UNSUPPORTED;
+    if (p->T == 0 || !ok || p->path == GLA_PATH_SIMT) return GLA_OK;
+    if (p->path == GLA_PATH_AUTO && p->T < kDeltaChunkMinT) return GLA_OK;
+    pl.path = GLA_PATH_TENSOR;
+    pl.nch = (p->T + kChunk - 1) / kChunk;
+    const size_t nc = (size_t)p->B * p->H * pl.nch;
+    size_t off = 0;
+    auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
+    pl.off_th = take(nc * kChunk * kChunk * 2);
+    pl.off_tl = take(nc * kChunk * kChunk * 2);
+    pl.off_p = take(nc * kChunk * kChunk * 2);
+    pl.off_g = take(nc * 4 * kChunk * 4);
+    pl.ws = off;
     return GLA_OK;
 }
 
@@ -164,6 +188,23 @@ gla_status gla_delta_fwd(const gla_delta_params* p, cudaStream_t stream)
         if (p->ST && p->ST != p->S0)
             e = p->S0 ? cudaMemcpyAsync(p->ST, p->S0, ns, cudaMemcpyDeviceToDevice, stream)
                       : cudaMemsetAsync(p->ST, 0, ns, stream);
+    } else if (pl.path == GLA_PATH_TENSOR) {
+        uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+        int* status = device_status_ptr();
+        DeltaPrep a;
+        a.q = p->q; a.k = p->k; a.log_g = p->log_g; a.beta = p->beta;
+        a.t_hi = ws + pl.off_th; a.t_lo = ws + pl.off_tl; a.p_hi = ws + pl.off_p; a.p_lo = nullptr;
+        a.gates = reinterpret_cast<float*>(ws + pl.off_g);
+        a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.nch = pl.nch; a.scale = p->scale;
+        e = launch_delta_prep(a, status, stream);
+        if (e == cudaSuccess) {
+            DeltaChain w;
+            w.q = p->q; w.k = p->k; w.v = p->v; w.t_hi = a.t_hi; w.t_lo = a.t_lo; w.p_hi = a.p_hi; w.gates = a.gates;
+            w.S0 = p->S0; w.O = p->O; w.ST = p->ST;
+            w.B = p->B; w.H = p->H; w.Hk = p->Hk; w.T = p->T; w.dk = p->dk; w.dv = p->dv; w.nch = pl.nch;
+            w.scale = p->scale;
+            e = launch_delta_chain(w, status, stream);
+        }
     } else {
         e = launch_delta_step(step_args(p, sms), stream);
     }

@@ -1,0 +1,102 @@
+// Device helpers shared by the chunk form's kernels of the gated delta rule.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "gla_internal.h"
+#include "sm100.cuh"
+#include "tma_host.h"
+
+namespace gla {
+namespace delta {
+
+constexpr int C = kChunk;
+constexpr int SLAB = C * 128;                     // 64 rows of 128 bytes: one swizzled TMA box
+constexpr uint64_t kTimeoutNs = 2000000000ull;    // per wait
+
+// Bounded wait. When it runs out (or another thread's has) the caller goes on without waiting:
+// every role keeps its sequence of arrivals, so the CTA ends; the status word reports it.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status, int code)
+{
+    if (sm100::mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = sm100::globaltimer();
+    while (!sm100::mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return;
+        if (sm100::globaltimer() - t0 > kTimeoutNs) {
+            *abort_flag = 1;
+            atomicExch(status, code);
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// a b + c on two fp32 values in one packed instruction (each half rounds as fmaf).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// x in two bf16 parts: hi = bf16(x), lo = bf16(x - hi); |x - hi - lo| <= 2^-18 |x|.
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo)
+{
+    hi = sm100::pack_bf16(x.x, x.y);
+    const float2 r = fma2(make_float2(bf_lo(hi), bf_hi(hi)), make_float2(-1.f, -1.f), x);
+    lo = sm100::pack_bf16(r.x, r.y);
+}
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo)
+{
+    split2(make_float2(x0, x1), hi, lo);
+}
+
+// Shared-memory accesses by 32-bit address. A pointer into the aligned dynamic buffer is generic
+// to the compiler, and a generic load may not pass a generic store; these stay in order among
+// the volatile statements around them (waits, fences) and overlap freely otherwise.
+__device__ __forceinline__ float4 lds4(uint32_t a)
+{
+    float4 f;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(a));
+    return f;
+}
+__device__ __forceinline__ float lds1(uint32_t a)
+{
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a));
+    return f;
+}
+__device__ __forceinline__ void sts_bf16(uint32_t a, float x)
+{
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(*reinterpret_cast<const uint16_t*>(&h)));
+}
+
+// Row-major [rows][cols] bf16 with a batch dimension, in boxes of 64 columns x 64 rows.
+inline bool map_rows(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t batch)
+{
+    const uint64_t dims[3] = {cols, rows, batch}, str[2] = {cols * 2, cols * rows * 2};
+    const uint32_t box[3] = {64, C, 1};
+    return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace delta
+}  // namespace gla

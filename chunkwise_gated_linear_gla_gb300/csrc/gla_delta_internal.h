@@ -11,6 +11,7 @@
 namespace gla {
 
 constexpr int kDeltaMaxDk = 256;    // widest keys of the recurrent form (its state rows per thread)
+constexpr int kDeltaChunkMinT = 32; // AUTO: shortest call that the chunk form takes
 constexpr int kDeltaKeep = 16;      // recurrent backward: tokens between two kept states
 
 // The recurrent form (gla_delta_step.cu): the recurrence token by token, the state tile in
@@ -51,5 +52,30 @@ struct DeltaBwdSum {
     int sms;
 };
 cudaError_t launch_delta_bwd_sum(const DeltaBwdSum& a, cudaStream_t s);
+
+// The chunk form (bf16, dk in {64, 128}, dv a multiple of 64), 64-token chunks on tcgen05.
+// Prep (gla_delta_prep.cu), chunk by chunk in parallel: with G the running sum of log_g in the
+// chunk, A[i][j] = beta_i (k_i . k_j) exp(G_i - G_j) for j < i, it writes
+//   t_hi, t_lo [BH][nch][64][64] bf16: (I + A)^-1 diag(beta) in two parts (about 17 bits),
+//   p_hi (, p_lo when non-null)      : scale (q_i . k_j) exp(G_i - G_j) for j <= i, else 0,
+//   gates [BH][nch][4][64] fp32      : beta, exp(G), exp(G_end - G), -exp(G).
+struct DeltaPrep {
+    const void* q; const void* k; const float* log_g; const void* beta;
+    void* t_hi; void* t_lo; void* p_hi; void* p_lo; float* gates;
+    int B, H, Hk, T, dk, nch;
+    float scale;
+};
+cudaError_t launch_delta_prep(const DeltaPrep& a, int* status, cudaStream_t s);
+
+// The serial pass over the chunks (gla_delta_chain.cu), the state in registers and tensor
+// memory, one CTA per head and 128 columns of dv.
+struct DeltaChain {
+    const void* q; const void* k; const void* v;
+    const void* t_hi; const void* t_lo; const void* p_hi; const float* gates;
+    const float* S0; void* O; float* ST;
+    int B, H, Hk, T, dk, dv, nch;
+    float scale;
+};
+cudaError_t launch_delta_chain(const DeltaChain& a, int* status, cudaStream_t s);
 
 }  // namespace gla

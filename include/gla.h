@@ -402,6 +402,11 @@ const char* gla_bwd_stage_name(const gla_bwd_params* p, int stage);
  *   GLA_PATH_SIMT    the recurrent form on CUDA cores, token by token, the state in registers:
  *                    single tokens (decoding; bound by the state's bytes), a few tokens,
  *                    fp32 inputs and other shapes; dk <= 256.
+ *   GLA_PATH_TENSOR  the chunk form on the tensor cores (bf16, dk 64 or 128, dv a multiple of
+ *                    64, B H <= 65535; else GLA_ERR_UNSUPPORTED): 64-token chunks, the
+ *                    corrections u of a chunk through the inverse of a unit triangular matrix.
+ *                    What feeds the state is kept to 17 bits (pairs of bf16) and summed in
+ *                    fp32: S_T is good to about 3e-6, O to its bf16 rounding.
  *   GLA_PATH_AUTO    the form that is faster for the sizes.
  * dk and dv are multiples of 16, q, k, v, O, S0 and ST 16-byte aligned, `scale` finite. ST may
  * equal S0 (the state carried in place). Other outputs may not overlap inputs. T = 0 copies S0
