@@ -93,6 +93,11 @@ gla_status check_fwd(const gla_delta_params* p)
 struct DeltaBwdPlan {
     int path = GLA_PATH_SIMT;
     int tiles = 0;
+    int nch = 0;
+    // chunk form: prep's T and P in two parts, gates; the sweeps' states, U and what dV's rounding left
+    size_t off_th = 0, off_tl = 0, off_ph = 0, off_pl = 0, off_g = 0, off_sh = 0, off_sl = 0, off_uh = 0, off_ul = 0,
+           off_dh = 0, off_dl = 0, off_xl = 0;
+    // recurrent form; part_q and part_k also serve the chunk form when heads share keys
     size_t off_keep = 0, off_pq = 0, off_pk = 0, off_pg = 0, off_pb = 0, off_scr = 0;
     size_t ws = 0;
 };
@@ -102,12 +107,30 @@ gla_status plan_bwd(const gla_delta_bwd_params* p, DeltaBwdPlan& pl)
     if (!p) return GLA_ERR_INVALID_ARG;
     gla_status st = check_sizes(p->B, p->H, p->Hk, p->T, p->dk, p->dv, p->scale, p->dtype, p->path);
     if (st != GLA_OK) return st;
-    if (p->path == GLA_PATH_TENSOR) return GLA_ERR_UNSUPPORTED;
+    const bool ok = chunk_shape_ok(p->B, p->H, p->T, p->dk, p->dv, p->dtype);
+    if (p->path == GLA_PATH_TENSOR && !ok) return GLA_ERR_UNSUPPORTED;
     if (p->T == 0) return GLA_OK;
     const size_t BH = (size_t)p->B * p->H, T = p->T;
     const size_t dkp = p->dk <= 64 ? 64 : p->dk <= 128 ? 128 : 256;
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
+    if (ok && p->path != GLA_PATH_SIMT) {
+        pl.path = GLA_PATH_TENSOR;
+        pl.nch = (p->T + kChunk - 1) / kChunk;
+        const size_t nc = BH * pl.nch, cc = nc * kChunk * kChunk * 2, st = nc * p->dk * p->dv * 2, u = nc * kChunk * p->dv * 2;
+        pl.off_th = take(cc); pl.off_tl = take(cc); pl.off_ph = take(cc); pl.off_pl = take(cc);
+        pl.off_g = take(nc * 8 * kChunk * 4);
+        pl.off_sh = take(st); pl.off_sl = take(st); pl.off_dh = take(st); pl.off_dl = take(st);
+        pl.off_uh = take(u); pl.off_ul = take(u);
+        pl.off_xl = take(BH * T * p->dv * 2);
+        if (p->H != p->Hk) {
+            pl.tiles = 1;
+            pl.off_pq = take(BH * T * p->dk * 4);
+            pl.off_pk = take(BH * T * p->dk * 4);
+        }
+        pl.ws = off;
+        return GLA_OK;
+    }
     pl.tiles = (p->dv + kDeltaBwdTile - 1) / kDeltaBwdTile;
     pl.off_keep = take(BH * ((T + kDeltaKeep - 1) / kDeltaKeep) * p->dk * p->dv * 4);
     pl.off_pq = take(pl.tiles * BH * T * p->dk * 4);
@@ -158,6 +181,55 @@ DeltaStep step_args(const gla_delta_params* p, int sms)
     return a;
 }
 
+// The chunk form of the backward: prep, the two sweeps, the gradients, and the sum over heads
+// that share keys.
+gla_status bwd_chunks(const gla_delta_bwd_params* p, const DeltaBwdPlan& pl, int sms, cudaStream_t stream)
+{
+    uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+    int* status = device_status_ptr();
+    if (!status) return GLA_ERR_CUDA;
+    float* gates = reinterpret_cast<float*>(ws + pl.off_g);
+    DeltaPrep a;
+    a.q = p->q; a.k = p->k; a.log_g = p->log_g; a.beta = p->beta;
+    a.t_hi = ws + pl.off_th; a.t_lo = ws + pl.off_tl; a.p_hi = ws + pl.off_ph; a.p_lo = ws + pl.off_pl; a.gates = gates;
+    a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.nch = pl.nch; a.scale = p->scale;
+    a.beta_floor = 0x1p-40f;
+    cudaError_t e = launch_delta_prep(a, status, stream);
+    DeltaSweep w;
+    w.q = p->q; w.k = p->k; w.v = p->v;
+    w.t_hi = a.t_hi; w.t_lo = a.t_lo; w.p_hi = a.p_hi; w.p_lo = a.p_lo; w.gates = gates;
+    w.S_in = p->S0; w.S_out = nullptr;
+    w.s_hi = ws + pl.off_sh; w.s_lo = ws + pl.off_sl; w.u_hi = ws + pl.off_uh; w.u_lo = ws + pl.off_ul;
+    w.x_hi = p->grad_v; w.x_lo = ws + pl.off_xl;
+    w.B = p->B; w.H = p->H; w.Hk = p->Hk; w.T = p->T; w.dk = p->dk; w.dv = p->dv; w.nch = pl.nch;
+    w.scale = p->scale; w.reverse = false;
+    if (e == cudaSuccess) e = launch_delta_sweep(w, status, stream);
+    w.v = p->grad_O; w.S_in = p->grad_ST; w.S_out = p->grad_S0;
+    w.s_hi = ws + pl.off_dh; w.s_lo = ws + pl.off_dl; w.reverse = true;
+    if (e == cudaSuccess) e = launch_delta_sweep(w, status, stream);
+    const bool shared = p->H != p->Hk;
+    DeltaGrads g;
+    g.q = p->q; g.k = p->k; g.dO = p->grad_O;
+    g.s_hi = ws + pl.off_sh; g.s_lo = ws + pl.off_sl; g.u_hi = w.u_hi; g.u_lo = w.u_lo;
+    g.d_hi = w.s_hi; g.d_lo = w.s_lo; g.x_hi = p->grad_v; g.x_lo = w.x_lo;
+    g.log_g = p->log_g; g.gates = gates;
+    g.dq = p->grad_q; g.dk_out = p->grad_k;
+    g.part_q = shared ? reinterpret_cast<float*>(ws + pl.off_pq) : nullptr;
+    g.part_k = shared ? reinterpret_cast<float*>(ws + pl.off_pk) : nullptr;
+    g.dlog_g = p->grad_log_g; g.dbeta = p->grad_beta;
+    g.B = p->B; g.H = p->H; g.Hk = p->Hk; g.T = p->T; g.dk = p->dk; g.dv = p->dv; g.nch = pl.nch; g.scale = p->scale;
+    if (e == cudaSuccess) e = launch_delta_grads(g, status, stream);
+    if (e == cudaSuccess && shared) {
+        DeltaBwdSum u;
+        u.part_q = g.part_q; u.part_k = g.part_k; u.part_g = nullptr; u.part_b = nullptr;
+        u.dq = p->grad_q; u.dk_out = p->grad_k; u.dlog_g = nullptr; u.dbeta = nullptr;
+        u.tiles = 1; u.B = p->B; u.H = p->H; u.Hk = p->Hk; u.T = p->T; u.dk = p->dk;
+        u.dtype = p->dtype; u.sms = sms;
+        e = launch_delta_bwd_sum(u, stream);
+    }
+    return e == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace gla
 
@@ -196,6 +268,7 @@ gla_status gla_delta_fwd(const gla_delta_params* p, cudaStream_t stream)
         a.t_hi = ws + pl.off_th; a.t_lo = ws + pl.off_tl; a.p_hi = ws + pl.off_p; a.p_lo = nullptr;
         a.gates = reinterpret_cast<float*>(ws + pl.off_g);
         a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.nch = pl.nch; a.scale = p->scale;
+        a.beta_floor = 0.f;
         e = launch_delta_prep(a, status, stream);
         if (e == cudaSuccess) {
             DeltaChain w;
@@ -238,6 +311,7 @@ gla_status gla_delta_bwd(const gla_delta_bwd_params* p, cudaStream_t stream)
     }
     uint8_t* ws = static_cast<uint8_t*>(p->workspace);
     auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+    if (pl.path == GLA_PATH_TENSOR) return bwd_chunks(p, pl, sms, stream);
     DeltaStep a;
     std::memset(&a, 0, sizeof(a));
     a.q = p->q; a.k = p->k; a.v = p->v; a.log_g = p->log_g; a.beta = p->beta; a.S0 = p->S0;

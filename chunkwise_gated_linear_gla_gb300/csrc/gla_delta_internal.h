@@ -58,12 +58,15 @@ cudaError_t launch_delta_bwd_sum(const DeltaBwdSum& a, cudaStream_t s);
 // chunk, A[i][j] = beta_i (k_i . k_j) exp(G_i - G_j) for j < i, it writes
 //   t_hi, t_lo [BH][nch][64][64] bf16: (I + A)^-1 diag(beta) in two parts (about 17 bits),
 //   p_hi (, p_lo when non-null)      : scale (q_i . k_j) exp(G_i - G_j) for j <= i, else 0,
-//   gates [BH][nch][4][64] fp32      : beta, exp(G), exp(G_end - G), -exp(G).
+//   gates [BH][nch][4][64] fp32      : beta, exp(G), exp(G_end - G), -exp(G); with p_lo
+//                                      [BH][nch][8][64]: also exp(G - G_mid), exp(G_mid - G) and G
+//                                      in two floats.
 struct DeltaPrep {
     const void* q; const void* k; const float* log_g; const void* beta;
     void* t_hi; void* t_lo; void* p_hi; void* p_lo; float* gates;
     int B, H, Hk, T, dk, nch;
     float scale;
+    float beta_floor;   // > 0: smaller |beta| are taken as this (the backward divides by it)
 };
 cudaError_t launch_delta_prep(const DeltaPrep& a, int* status, cudaStream_t s);
 
@@ -77,5 +80,35 @@ struct DeltaChain {
     float scale;
 };
 cudaError_t launch_delta_chain(const DeltaChain& a, int* status, cudaStream_t s);
+
+// The backward's serial passes (gla_delta_bwd_chain.cu). Forward sweep: from S0, the state
+// entering every chunk and the chunk's U to the workspace. Reverse sweep: from dST, the
+// gradient of the state leaving every chunk, the gradient of V (rounded to bf16: the output)
+// and what that rounding left, and dS0. All in two bf16 parts; x_hi of the reverse sweep is the
+// caller's grad_v.
+//   s_hi, s_lo [BH][nch][dv][dk];  u_hi, u_lo [BH][nch][dv][64];  x_hi, x_lo [BH][T][dv]
+struct DeltaSweep {
+    const void* q; const void* k; const void* v;      // v: V, or dO in reverse
+    const void* t_hi; const void* t_lo; const void* p_hi; const void* p_lo; const float* gates;
+    const float* S_in; float* S_out;
+    void* s_hi; void* s_lo; void* u_hi; void* u_lo; void* x_hi; void* x_lo;
+    int B, H, Hk, T, dk, dv, nch;
+    float scale;
+    bool reverse;
+};
+cudaError_t launch_delta_sweep(const DeltaSweep& a, int* status, cudaStream_t s);
+
+// Chunk-parallel gradients (gla_delta_grads.cu) from the sweeps' results. dq, dk_out: bf16
+// [BH][T][dk] when part_q is null (H == Hk), else fp32 partials per head to part_q, part_k.
+struct DeltaGrads {
+    const void* q; const void* k; const void* dO;
+    const void* s_hi; const void* s_lo; const void* u_hi; const void* u_lo;
+    const void* d_hi; const void* d_lo; const void* x_hi; const void* x_lo;
+    const float* log_g; const float* gates;
+    void* dq; void* dk_out; float* part_q; float* part_k; float* dlog_g; void* dbeta;
+    int B, H, Hk, T, dk, dv, nch;
+    float scale;
+};
+cudaError_t launch_delta_grads(const DeltaGrads& a, int* status, cudaStream_t s);
 
 }  // namespace gla

@@ -125,7 +125,11 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
         const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta) + bh * a.T;
         const int t = t0 + 2 * lane;
         float x0 = lg && t < a.T ? lg[t] : 0.f, x1 = lg && t + 1 < a.T ? lg[t + 1] : 0.f;
-        const float b0 = t < a.T ? __bfloat162float(bp[t]) : 0.f, b1 = t + 1 < a.T ? __bfloat162float(bp[t + 1]) : 0.f;
+        float b0 = t < a.T ? __bfloat162float(bp[t]) : 0.f, b1 = t + 1 < a.T ? __bfloat162float(bp[t + 1]) : 0.f;
+        if (a.beta_floor > 0.f) {
+            if (t < a.T && fabsf(b0) < a.beta_floor) b0 = a.beta_floor;
+            if (t + 1 < a.T && fabsf(b1) < a.beta_floor) b1 = a.beta_floor;
+        }
         // below -1e5 exp() is zero whatever comes later
         const bool bad = __any_sync(~0u, x0 != x0 || x1 != x1);   // a NaN gate reaches the state through exp(G)
         x0 = fminf(fmaxf(x0, -1e5f), 1e5f);
@@ -153,11 +157,20 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
         be[i] = b0; be[i + 1] = b1;
         const float nan = __int_as_float(0x7fc00000);
         const float e0 = bad ? nan : expf(g0.h + g0.l), e1 = bad ? nan : expf(g1.h + g1.l);
-        float2* go = reinterpret_cast<float2*>(a.gates + (bh * a.nch + c) * 4 * C) + lane;
+        float2* go = reinterpret_cast<float2*>(a.gates + (bh * a.nch + c) * (a.p_lo ? 8 : 4) * C) + lane;
         go[0] = make_float2(b0, b1);
         go[C / 2] = make_float2(e0, e1);
         go[C] = make_float2(expf(minus(end, g0)), expf(minus(end, g1)));
         go[3 * C / 2] = make_float2(-e0, -e1);
+        if (a.p_lo) {
+            // for the gradients: the factors of exp(G_i - G_j) (zeros where the chunk's gate is too
+            // steep for them), and G
+            const bool near = m <= kRange;
+            go[2 * C] = near ? make_float2(fa[i], fa[i + 1]) : make_float2(0.f, 0.f);
+            go[5 * C / 2] = near ? make_float2(fb[i], fb[i + 1]) : make_float2(0.f, 0.f);
+            go[3 * C] = make_float2(g0.h, g1.h);
+            go[7 * C / 2] = make_float2(g0.l, g1.l);
+        }
     }
     tc_fence_before();
     __syncthreads();

@@ -439,7 +439,10 @@ size_t gla_delta_fwd_workspace_size(const gla_delta_params* p);
  * grad_beta in `dtype`, each rounded once from fp32; grad_log_g and grad_S0 fp32 (any of
  * grad_log_g, grad_beta, grad_S0 may be NULL; grad_log_g must be without log_g). Nothing of
  * the forward call is needed but its inputs. Forms, alignment, ownership and asynchrony as for
- * the forward call; results are bitwise reproducible.
+ * the forward call (AUTO takes the chunk form for every shape it can); results are bitwise
+ * reproducible. The workspace holds the state and its gradient at every chunk (chunk form,
+ * about 8 B H T dk dv / 64 bytes) or a state for every 16 tokens (recurrent form). The chunk
+ * form divides by beta: a |beta| below 2^-40 is taken as 2^-40.
  */
 typedef struct {
     const void* q; const void* k; const void* v; const float* log_g; const void* beta;
