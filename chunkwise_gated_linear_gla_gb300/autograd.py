@@ -66,8 +66,8 @@ def _delta_function():
             q, k, v, log_g, beta, S0 = ctx.saved_tensors
             if dO is None and dST is None:
                 return (None,) * 8
-            dO = torch.zeros_like(v) if dO is None else dO.to(q.dtype).contiguous()
-            dST = None if dST is None else dST.to(torch.float32).contiguous()
+            dO = torch.zeros_like(v) if dO is None else dO.contiguous()
+            dST = None if dST is None else dST.contiguous()
             want = ctx.needs_input_grad
             g = _b.delta_backward(q, k, v, log_g, beta, S0, dO, dST, scale=ctx.scale,
                                   want_dS0=S0 is not None and want[5], path=ctx.path)
@@ -97,7 +97,7 @@ def _qk_function():
             norm, eps, start, interleaved = ctx.how
             want = ctx.needs_input_grad
             dense = lambda g, x: (torch.zeros(x.shape, dtype=x.dtype, device=x.device) if g is None
-                                  else g.to(x.dtype).contiguous())
+                                  else g.contiguous())
             g = _b.qk_norm_rope_backward(q, k, dense(dqo, q), None if k is None else dense(dko, k), norm, w_q, w_k,
                                          eps, inv_freq, positions, start, interleaved)
             return (*(x if w else None for x, w in zip(g, want)), None, None, None, None, None, None)
@@ -122,6 +122,9 @@ def gla_attention(q, k, v, log_g=None, S0=None, gate=None):
 def delta_attention(q, k, v, log_g, beta, S0=None, scale=None, path=_b.GLA_PATH_AUTO):
     """(O, S_T) of the gated delta rule (binding.delta_forward), differentiable once in q, k, v, log_g, beta
     and S0. The inputs must be contiguous device tensors."""
+    import torch
+    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in (q, k, v, log_g, beta, S0)):
+        return _b.delta_forward(q, k, v, log_g, beta, S0, scale=scale, path=path)
     global _DELTA
     if _DELTA is None:
         _DELTA = _delta_function()
@@ -131,6 +134,9 @@ def delta_attention(q, k, v, log_g, beta, S0=None, scale=None, path=_b.GLA_PATH_
 def qk_norm_rope(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv_freq=None, positions=None, start=0,
                  interleaved=False):
     """binding.qk_norm_rope_forward, differentiable once in q, k and the weights."""
+    import torch
+    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in (q, k, w_q, w_k)):
+        return _b.qk_norm_rope_forward(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved)
     global _QK
     if _QK is None:
         _QK = _qk_function()

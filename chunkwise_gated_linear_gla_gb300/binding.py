@@ -569,23 +569,25 @@ def _on_gpu(t, what):
         _refuse(f"{what} is on {t.device}, not on a GPU")
 
 
-class _here:
-    """The tensors' device made current for a call (nothing to do when it is already)."""
-    __slots__ = ("dev", "was")
-
-    def __init__(self, device):
-        self.dev, self.was = device.index, None
-
-    def __enter__(self):
-        import torch
-        if torch.cuda.current_device() != self.dev:
-            self.was = torch.cuda.current_device()
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.was is not None:
-            import torch
-            torch.cuda.set_device(self.was)
+def _launch(f, name, p, device, stream, *tensors):
+    """Calls f(byref(p), stream) with the tensors' device current; raises on an error. `tensors`
+    (may be None) were allocated for this call and are used on `stream`."""
+    import torch
+    index = device.index
+    was = torch._C._cuda_getDevice()
+    if was != index:
+        torch.cuda.set_device(index)
+    try:
+        if stream is None:
+            s = f(ctypes.byref(p), torch._C._cuda_getCurrentRawStream(index))
+        else:
+            _used_on(stream, device, *tensors)
+            s = f(ctypes.byref(p), _stream(stream))
+    finally:
+        if was != index:
+            torch.cuda.set_device(was)
+    if s != GLA_OK:
+        raise GlaError(s, name)
 
 
 def _used_on(stream, device, *tensors):
@@ -640,23 +642,19 @@ def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, pa
     _on_gpu(q, "q")
     if B == 0:
         _refuse("an empty batch")
-    with _here(dev):
-        new = []
-        if O is None:
-            O = torch.empty((B, H, T, dv), dtype=dt, device=dev)
-            new.append(O)
-        if ST is None and want_state:
-            ST = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-            new.append(ST)
-        p = gla_delta_params(_ptr(q), _ptr(k), _ptr(v), _ptr(log_g), _ptr(beta), _ptr(S0), _ptr(O), _ptr(ST),
-                             B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path)
-        n = gla_delta_fwd_workspace_size(p)
-        if n:
-            ws = _aligned_workspace(n, dev)
-            new.append(ws)
-            p.workspace, p.workspace_bytes = ws.data_ptr(), n
-        _used_on(stream, dev, *new)
-        gla_delta_fwd(p, stream)
+    lib = _lib or load()
+    if O is None:
+        O = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+    if ST is None and want_state:
+        ST = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    p = gla_delta_params(_ptr(q), _ptr(k), _ptr(v), _ptr(log_g), _ptr(beta), _ptr(S0), _ptr(O), _ptr(ST),
+                         B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path)
+    n = lib.gla_delta_fwd_workspace_size(ctypes.byref(p))
+    ws = None
+    if n:
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        p.workspace, p.workspace_bytes = ws.data_ptr(), n
+    _launch(lib.gla_delta_fwd, "gla_delta_fwd", p, dev, stream, O, ST, ws)
     return O, ST
 
 
@@ -672,19 +670,19 @@ def delta_backward(q, k, v, log_g, beta, S0, dO, dST=None, scale=None, want_dS0=
     _on_gpu(q, "q")
     if B == 0:
         _refuse("an empty batch")
-    with _here(dev):
-        gq, gk, gv, gb = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(beta)
-        gg = None if log_g is None else torch.empty_like(log_g)
-        gS = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if want_dS0 else None
-        p = gla_delta_bwd_params(_ptr(q), _ptr(k), _ptr(v), _ptr(log_g), _ptr(beta), _ptr(S0), _ptr(dO), _ptr(dST),
-                                 _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gg), _ptr(gb), _ptr(gS),
-                                 B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path)
-        n = gla_delta_bwd_workspace_size(p)
-        ws = _aligned_workspace(n, dev)
-        if n:
-            p.workspace, p.workspace_bytes = ws.data_ptr(), n
-        _used_on(stream, dev, gq, gk, gv, gg, gb, gS, ws)
-        gla_delta_bwd(p, stream)
+    lib = _lib or load()
+    gq, gk, gv, gb = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(beta)
+    gg = None if log_g is None else torch.empty_like(log_g)
+    gS = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if want_dS0 else None
+    p = gla_delta_bwd_params(_ptr(q), _ptr(k), _ptr(v), _ptr(log_g), _ptr(beta), _ptr(S0), _ptr(dO), _ptr(dST),
+                             _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gg), _ptr(gb), _ptr(gS),
+                             B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path)
+    n = lib.gla_delta_bwd_workspace_size(ctypes.byref(p))
+    ws = None
+    if n:
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        p.workspace, p.workspace_bytes = ws.data_ptr(), n
+    _launch(lib.gla_delta_bwd, "gla_delta_bwd", p, dev, stream, gq, gk, gv, gg, gb, gS, ws)
     return gq, gk, gv, gg, gb, gS
 
 
@@ -714,8 +712,8 @@ def gla_qk_norm_rope_bwd_workspace_size(p: gla_qk_norm_params) -> int:
 
 def _strides(t):
     """(batch, head, token) strides; those of dimensions of one are never stepped and count as 0."""
-    n, s = t.shape, t.stride()
-    return tuple(s[i] if n[i] > 1 else 0 for i in range(3))
+    (a, b, c, _), (x, y, z, _) = t.shape, t.stride()
+    return x if a > 1 else 0, y if b > 1 else 0, z if c > 1 else 0
 
 
 def _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved):
@@ -759,11 +757,11 @@ def qk_norm_rope_forward(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv
     positions: int64 [B,T], else start + t."""
     import torch
     p = _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved)
-    with _here(q.device):
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _used_on(stream, q.device, qo, ko)
-        gla_qk_norm_rope(p, qo, ko, stream)
+    lib, dev = _lib or load(), q.device
+    qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    ko = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=dev)
+    po, pk = _ptr(qo), _ptr(ko)
+    _launch(lambda r, s: lib.gla_qk_norm_rope(r, po, pk, s), "gla_qk_norm_rope", p, dev, stream, qo, ko)
     return qo, ko
 
 
@@ -777,6 +775,15 @@ def _rows_like(t):
     return torch.empty((B, T, H, d), dtype=t.dtype, device=t.device).transpose(1, 2)
 
 
+def _here_size(f, p, device):
+    """A workspace size that depends on the device's multiprocessors."""
+    import torch
+    if torch._C._cuda_getDevice() == device.index:
+        return f(ctypes.byref(p))
+    with torch.cuda.device(device):
+        return f(ctypes.byref(p))
+
+
 def qk_norm_rope_backward(q, k, dq_out, dk_out, norm="l2", w_q=None, w_k=None, eps=1e-6, inv_freq=None,
                           positions=None, start=0, interleaved=False, stream=None):
     """Gradients of qk_norm_rope_forward: (dq, dk, dw_q, dw_k); dq and dk in the inputs' type (token-major
@@ -786,13 +793,18 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, norm="l2", w_q=None, w_k=None, e
     _dense(dq_out, q.shape, q.dtype, q.device, "dq_out")
     if k is not None:
         _dense(dk_out, k.shape, k.dtype, k.device, "dk_out")
-    with _here(q.device):
-        gq, gk = _rows_like(q), None if k is None else _rows_like(k)
-        gwq = None if w_q is None else torch.empty_like(w_q)
-        gwk = None if w_k is None or k is None else torch.empty_like(w_k)
-        g = gla_qk_norm_grads(_ptr(dq_out), _ptr(dk_out) if k is not None else None, _ptr(gq), _ptr(gk),
-                              _strides(gq), (0, 0, 0) if k is None else _strides(gk), _ptr(gwq), _ptr(gwk))
-        ws = _aligned_workspace(gla_qk_norm_rope_bwd_workspace_size(p), q.device)
-        _used_on(stream, q.device, gq, gk, gwq, gwk, ws)
-        gla_qk_norm_rope_bwd(p, g, ws, stream)
+    lib, dev = _lib or load(), q.device
+    gq, gk = _rows_like(q), None if k is None else _rows_like(k)
+    gwq = None if w_q is None else torch.empty_like(w_q)
+    gwk = None if w_k is None or k is None else torch.empty_like(w_k)
+    g = gla_qk_norm_grads(_ptr(dq_out), None if k is None else _ptr(dk_out), _ptr(gq), _ptr(gk), _strides(gq),
+                          (0, 0, 0) if k is None else _strides(gk), _ptr(gwq), _ptr(gwk))
+    n, ws = 0, None
+    if gwq is not None or gwk is not None:
+        n = _here_size(lib.gla_qk_norm_rope_bwd_workspace_size, p, dev)
+        if n:
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    pw = _ptr(ws)
+    _launch(lambda r, s: lib.gla_qk_norm_rope_bwd(r, ctypes.byref(g), pw, n, s), "gla_qk_norm_rope_bwd", p, dev, stream,
+            gq, gk, gwq, gwk, ws)
     return gq, gk, gwq, gwk

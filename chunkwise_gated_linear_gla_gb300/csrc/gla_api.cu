@@ -27,6 +27,13 @@ DevCache* dev_cache()
 {
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64) return nullptr;
+    // A thread that has made no CUDA call yet (an autograd worker whose allocations came from a
+    // cache) has no context current, and encoding a tensor map needs one.
+    static thread_local int bound = -1;
+    if (bound != d) {
+        if (cudaSetDevice(d) != cudaSuccess) return nullptr;
+        bound = d;
+    }
     std::lock_guard<std::mutex> lk(g_mu);
     DevCache& c = g_dev[d];
     if (!c.init) {

@@ -45,7 +45,7 @@ bool chunk_shape_ok(int B, int H, int T, int dk, int dv, int dtype)
 struct DeltaPlan {
     int path = GLA_PATH_SIMT;
     int nch = 0;
-    size_t off_th = 0, off_tl = 0, off_p = 0, off_g = 0;
+    size_t off_th = 0, off_tl = 0, off_p = 0, off_pl = 0, off_g = 0;
     size_t ws = 0;
 };
 
@@ -66,6 +66,7 @@ gla_status plan_fwd(const gla_delta_params* p, DeltaPlan& pl)
     pl.off_th = take(nc * kChunk * kChunk * 2);
     pl.off_tl = take(nc * kChunk * kChunk * 2);
     pl.off_p = take(nc * kChunk * kChunk * 2);
+    pl.off_pl = take(nc * kChunk * kChunk * 2);
     pl.off_g = take(nc * 4 * kChunk * 4);
     pl.ws = off;
     return GLA_OK;
@@ -193,7 +194,7 @@ gla_status bwd_chunks(const gla_delta_bwd_params* p, const DeltaBwdPlan& pl, int
     a.q = p->q; a.k = p->k; a.log_g = p->log_g; a.beta = p->beta;
     a.t_hi = ws + pl.off_th; a.t_lo = ws + pl.off_tl; a.p_hi = ws + pl.off_ph; a.p_lo = ws + pl.off_pl; a.gates = gates;
     a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.nch = pl.nch; a.scale = p->scale;
-    a.beta_floor = 0x1p-40f;
+    a.grads = true; a.beta_floor = 0x1p-40f;
     cudaError_t e = launch_delta_prep(a, status, stream);
     DeltaSweep w;
     w.q = p->q; w.k = p->k; w.v = p->v;
@@ -265,14 +266,14 @@ gla_status gla_delta_fwd(const gla_delta_params* p, cudaStream_t stream)
         int* status = device_status_ptr();
         DeltaPrep a;
         a.q = p->q; a.k = p->k; a.log_g = p->log_g; a.beta = p->beta;
-        a.t_hi = ws + pl.off_th; a.t_lo = ws + pl.off_tl; a.p_hi = ws + pl.off_p; a.p_lo = nullptr;
+        a.t_hi = ws + pl.off_th; a.t_lo = ws + pl.off_tl; a.p_hi = ws + pl.off_p; a.p_lo = ws + pl.off_pl;
         a.gates = reinterpret_cast<float*>(ws + pl.off_g);
         a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.nch = pl.nch; a.scale = p->scale;
-        a.beta_floor = 0.f;
+        a.grads = false; a.beta_floor = 0.f;
         e = launch_delta_prep(a, status, stream);
         if (e == cudaSuccess) {
             DeltaChain w;
-            w.q = p->q; w.k = p->k; w.v = p->v; w.t_hi = a.t_hi; w.t_lo = a.t_lo; w.p_hi = a.p_hi; w.gates = a.gates;
+            w.q = p->q; w.k = p->k; w.v = p->v; w.t_hi = a.t_hi; w.t_lo = a.t_lo; w.p_hi = a.p_hi; w.p_lo = a.p_lo; w.gates = a.gates;
             w.S0 = p->S0; w.O = p->O; w.ST = p->ST;
             w.B = p->B; w.H = p->H; w.Hk = p->Hk; w.T = p->T; w.dk = p->dk; w.dv = p->dv; w.nch = pl.nch;
             w.scale = p->scale;

@@ -11,11 +11,11 @@
 //
 //     S -> bf16 parts | K S | R -> parts | T R | l U -> parts | K^T (l U) | S
 //
-// What feeds the state (S, R, U, T) goes into the products in two bf16 parts, hi + lo, K is
-// and V are exact: two products for K S, K^T U and T V (off the chain), three for T R, about
-// 2^-17 per step, so the fp32
-// state is good to 1e-5. O is rounded to bf16 at the end, so its products take Q and both parts
-// of S, but P and U in one; their own commit lies off the chain, and so does the drain of O on four other warps.
+// Every operand that is not an input (S, R, U, T, P) goes into the products in two bf16 parts,
+// hi + lo, good to 2^-17; K, V and Q are exact: two products for K S, K^T U, Q S and T V, three for
+// T R and P U. So the fp32 state is good to 3e-6, and O to its last rounding: with one part of P
+// and U it was not (keys that repeat make P U a sum of cancelling terms: 7.5e-3 where all keys
+// are the same). Q S, T V and P U run off the chain, and so does the drain of O on four other warps.
 //
 // Bound by the chain's latency (the products are 0.4 us of it per chunk at dk = dv = 128).
 //
@@ -42,7 +42,7 @@ template <int DK>
 struct CL {
     static constexpr int KB = (DK / 64) * SLAB;
     static constexpr int K_OFF = 0, Q_OFF = KB, V_OFF = 2 * KB, TH_OFF = V_OFF + 2 * SLAB, TL_OFF = TH_OFF + SLAB,
-                         P_OFF = TL_OFF + SLAB, G_OFF = P_OFF + SLAB;
+                         P_OFF = TL_OFF + SLAB, PL_OFF = P_OFF + SLAB, G_OFF = PL_OFF + SLAB;
     static constexpr int STAGE = G_OFF + 1024;
     static constexpr int BYTES = G_OFF + 4 * C * 4;       // of one stage's loads, all of dv present
     static constexpr int O_OFF = NST * STAGE;             // [2 halves of dv][64 tokens][64] bf16
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(NT, 1)
 gla_delta_chain_kernel(DeltaChain a, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmTh,
                        const __grid_constant__ CUtensorMap tmTl, const __grid_constant__ CUtensorMap tmP,
+                       const __grid_constant__ CUtensorMap tmPl,
                        const __grid_constant__ CUtensorMap tmO, int* status)
 {
     using L = CL<DK>;
@@ -82,9 +83,10 @@ gla_delta_chain_kernel(DeltaChain a, const __grid_constant__ CUtensorMap tmK, co
     uint64_t* d_full = s_ready + 5;         // the increment formed
     uint64_t* o_full = s_ready + 6;         // Q S and P U formed
     uint64_t* o_empty = s_ready + 7;        // O read out (4 warps)
-    uint64_t* fin = s_ready + 8;
-    uint32_t* holder = reinterpret_cast<uint32_t*>(s_ready + 9);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(s_ready + 10);
+    uint64_t* p_ready = s_ready + 8;        // U's own parts written, for P U (8 warps)
+    uint64_t* fin = s_ready + 9;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(s_ready + 10);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(s_ready + 11);
 
     const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32, wg = warp / 4;
     const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
@@ -98,7 +100,7 @@ gla_delta_chain_kernel(DeltaChain a, const __grid_constant__ CUtensorMap tmK, co
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 5);
         }
-        for (int i = 0; i < 9; ++i) mbar_init(&s_ready[i], (i == 0 || i == 2 || i == 4) ? 8 : i == 7 ? 4 : 1);
+        for (int i = 0; i < 10; ++i) mbar_init(&s_ready[i], (i == 0 || i == 2 || i == 4 || i == 8) ? 8 : i == 7 ? 4 : 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -133,6 +135,7 @@ gla_delta_chain_kernel(DeltaChain a, const __grid_constant__ CUtensorMap tmK, co
 #pragma unroll
                 for (int i = 0; i < DK / 64; ++i) tma_load_3d(sb + L::Q_OFF + i * SLAB, &tmQ, &full[st], 64 * i, t0, bk);
                 tma_load_3d(sb + L::P_OFF, &tmP, &full[st], 0, 0, at);
+                tma_load_3d(sb + L::PL_OFF, &tmPl, &full[st], 0, 0, at);
                 if (m + NST < n) {
                     // the next stages' tiles on their way into L2
                     const int t1 = t0 + NST * C, a1 = at + NST;
@@ -147,6 +150,7 @@ gla_delta_chain_kernel(DeltaChain a, const __grid_constant__ CUtensorMap tmK, co
                         prefetch_l2_tile_3d(&tmTh, 0, 0, a1);
                         prefetch_l2_tile_3d(&tmTl, 0, 0, a1);
                         prefetch_l2_tile_3d(&tmP, 0, 0, a1);
+                        prefetch_l2_tile_3d(&tmPl, 0, 0, a1);
                     }
                 }
             }
@@ -168,6 +172,7 @@ gla_delta_chain_kernel(DeltaChain a, const __grid_constant__ CUtensorMap tmK, co
                 const uint64_t dTh = sdesc(sb + L::TH_OFF, 16, 1024, kSwizzle128);
                 const uint64_t dTl = sdesc(sb + L::TL_OFF, 16, 1024, kSwizzle128);
                 const uint64_t dP = sdesc(sb + L::P_OFF, 16, 1024, kSwizzle128);
+                const uint64_t dPl = sdesc(sb + L::PL_OFF, 16, 1024, kSwizzle128);
                 const uint64_t dKn = sdesc(sb + L::K_OFF, SLAB, 1024, kSwizzle128);   // keys along N
                 const uint64_t dV = sdesc(sb + L::V_OFF, SLAB, 1024, kSwizzle128);    // dv along M
                 wait(&full[st], (m / NST) & 1, abort_flag, status, ERR_MMA);
@@ -231,11 +236,19 @@ gla_delta_chain_kernel(DeltaChain a, const __grid_constant__ CUtensorMap tmK, co
                         mma_ts(tm + L::tD, tm + L::tRl + kk * 8, dKn + o, idS, 1);
                     }
                     mma_commit(d_full);
-                    // (P U)^T: U's high part lies in the first 16 columns of each group's half of X
+                }
+                wait(p_ready, ph, abort_flag, status, ERR_MMA);
+                __syncwarp();
+                tc_fence_after();
+                if (elect_one()) {
+                    // (P U)^T: U's parts lie in X, 16 columns of 32 tokens each
 #pragma unroll
-                    for (int kk = 0; kk < C / 16; ++kk)
-                        mma_ts(tm + L::tOp, tm + L::tX + (kk >> 1) * 32 + (kk & 1) * 8, dP + ((kk * 32) >> 4), id64,
-                               kk > 0);
+                    for (int kk = 0; kk < C / 16; ++kk) {
+                        const uint32_t u = tm + L::tX + (kk >> 1) * 32 + (kk & 1) * 8;
+                        mma_ts(tm + L::tOp, u, dP + ((kk * 32) >> 4), id64, kk > 0);
+                        mma_ts(tm + L::tOp, u + 16, dP + ((kk * 32) >> 4), id64, 1);
+                        mma_ts(tm + L::tOp, u, dPl + ((kk * 32) >> 4), id64, 1);
+                    }
                     mma_commit(o_full);
                     mma_commit(&empty[st]);
                 }
@@ -309,23 +322,29 @@ gla_delta_chain_kernel(DeltaChain a, const __grid_constant__ CUtensorMap tmK, co
                 for (int i = 0; i < 8; ++i) g[i] = lds4(gt + (2 * C + i0 + 4 * i) * 4);   // l
                 wait(u_full, ph, abort_flag, status, ERR_EPI);
                 tc_fence_after();
-                uint32_t x[32], u[16];
+                uint32_t x[32];
                 tmem_ld32(tm + lb + L::tX + i0, x);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    u[2 * i] = pack_bf16(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]));
-                    u[2 * i + 1] = pack_bf16(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
                     split2(mul2(make_float2(g[i].x, g[i].y), f2(x[4 * i], x[4 * i + 1])), hi[2 * i], lo[2 * i]);
                     split2(mul2(make_float2(g[i].z, g[i].w), f2(x[4 * i + 2], x[4 * i + 3])), hi[2 * i + 1], lo[2 * i + 1]);
                 }
                 tmem_st16(tm + lb + L::tRh + i0 / 2, hi);
                 tmem_st16(tm + lb + L::tRl + i0 / 2, lo);
-                tmem_st16(tm + lb + L::tX + i0, u);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(u_ready);
+                // U's own parts, off the chain: the increment's products run meanwhile
+#pragma unroll
+                for (int i = 0; i < 16; ++i) split2(f2(x[2 * i], x[2 * i + 1]), hi[i], lo[i]);
+                tmem_st16(tm + lb + L::tX + i0, hi);
+                tmem_st16(tm + lb + L::tX + i0 + 16, lo);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready);
             }
             wait(d_full, ph, abort_flag, status, ERR_EPI);
             tc_fence_after();
@@ -405,13 +424,13 @@ gla_delta_chain_kernel(DeltaChain a, const __grid_constant__ CUtensorMap tmK, co
 }
 
 template <int DK>
-cudaError_t launch_dk(const DeltaChain& a, const CUtensorMap (&m)[7], int* status, cudaStream_t s)
+cudaError_t launch_dk(const DeltaChain& a, const CUtensorMap (&m)[8], int* status, cudaStream_t s)
 {
     using L = CL<DK>;
     cudaError_t e = cudaFuncSetAttribute(gla_delta_chain_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
     const dim3 g((a.dv + DVT - 1) / DVT, (unsigned)(a.B * a.H));
-    gla_delta_chain_kernel<DK><<<g, NT, L::SMEM, s>>>(a, m[0], m[1], m[2], m[3], m[4], m[5], m[6], status);
+    gla_delta_chain_kernel<DK><<<g, NT, L::SMEM, s>>>(a, m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], status);
     return cudaGetLastError();
 }
 
@@ -420,15 +439,16 @@ cudaError_t launch_dk(const DeltaChain& a, const CUtensorMap (&m)[7], int* statu
 cudaError_t launch_delta_chain(const DeltaChain& a, int* status, cudaStream_t s)
 {
     const uint64_t bk = (uint64_t)a.B * a.Hk, bh = (uint64_t)a.B * a.H, nc = bh * a.nch;
-    CUtensorMap m[7];
+    CUtensorMap m[8];
     if (!map_rows(&m[0], a.k, a.dk, a.T, bk) || !map_rows(&m[1], a.q, a.dk, a.T, bk) ||
         !map_rows(&m[2], a.v, a.dv, a.T, bh) || !map_rows(&m[3], a.t_hi, C, C, nc) ||
-        !map_rows(&m[4], a.t_lo, C, C, nc) || !map_rows(&m[5], a.p_hi, C, C, nc))
+        !map_rows(&m[4], a.t_lo, C, C, nc) || !map_rows(&m[5], a.p_hi, C, C, nc) ||
+        !map_rows(&m[6], a.p_lo, C, C, nc))
         return cudaErrorInvalidValue;
     {   // O: staged without a swizzle
         const uint64_t dims[3] = {(uint64_t)a.dv, (uint64_t)a.T, bh}, str[2] = {(uint64_t)a.dv * 2, (uint64_t)a.dv * a.T * 2};
         const uint32_t box[3] = {64, C, 1};
-        if (!make_tmap(&m[6], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.O, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+        if (!make_tmap(&m[7], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.O, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE))
             return cudaErrorInvalidValue;
     }
     return a.dk == 64 ? launch_dk<64>(a, m, status, s) : launch_dk<128>(a, m, status, s);

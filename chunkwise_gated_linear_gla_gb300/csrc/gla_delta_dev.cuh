@@ -57,7 +57,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return d;
 }
 
-// x in two bf16 parts: hi = bf16(x), lo = bf16(x - hi); |x - hi - lo| <= 2^-18 |x|.
+// x in two bf16 parts: hi = bf16(x), lo = bf16(x - hi); |x - hi - lo| <= 2^-17 |x|.
 __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo)
 {
     hi = sm100::pack_bf16(x.x, x.y);

@@ -57,8 +57,8 @@ cudaError_t launch_delta_bwd_sum(const DeltaBwdSum& a, cudaStream_t s);
 // Prep (gla_delta_prep.cu), chunk by chunk in parallel: with G the running sum of log_g in the
 // chunk, A[i][j] = beta_i (k_i . k_j) exp(G_i - G_j) for j < i, it writes
 //   t_hi, t_lo [BH][nch][64][64] bf16: (I + A)^-1 diag(beta) in two parts (about 17 bits),
-//   p_hi (, p_lo when non-null)      : scale (q_i . k_j) exp(G_i - G_j) for j <= i, else 0,
-//   gates [BH][nch][4][64] fp32      : beta, exp(G), exp(G_end - G), -exp(G); with p_lo
+//   p_hi, p_lo                       : scale (q_i . k_j) exp(G_i - G_j) for j <= i, else 0,
+//   gates [BH][nch][4][64] fp32      : beta, exp(G), exp(G_end - G), -exp(G); with grads
 //                                      [BH][nch][8][64]: also exp(G - G_mid), exp(G_mid - G) and G
 //                                      in two floats.
 struct DeltaPrep {
@@ -66,6 +66,7 @@ struct DeltaPrep {
     void* t_hi; void* t_lo; void* p_hi; void* p_lo; float* gates;
     int B, H, Hk, T, dk, nch;
     float scale;
+    bool grads;         // for the backward
     float beta_floor;   // > 0: smaller |beta| are taken as this (the backward divides by it)
 };
 cudaError_t launch_delta_prep(const DeltaPrep& a, int* status, cudaStream_t s);
@@ -74,7 +75,7 @@ cudaError_t launch_delta_prep(const DeltaPrep& a, int* status, cudaStream_t s);
 // memory, one CTA per head and 128 columns of dv.
 struct DeltaChain {
     const void* q; const void* k; const void* v;
-    const void* t_hi; const void* t_lo; const void* p_hi; const float* gates;
+    const void* t_hi; const void* t_lo; const void* p_hi; const void* p_lo; const float* gates;
     const float* S0; void* O; float* ST;
     int B, H, Hk, T, dk, dv, nch;
     float scale;

@@ -157,12 +157,12 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
         be[i] = b0; be[i + 1] = b1;
         const float nan = __int_as_float(0x7fc00000);
         const float e0 = bad ? nan : expf(g0.h + g0.l), e1 = bad ? nan : expf(g1.h + g1.l);
-        float2* go = reinterpret_cast<float2*>(a.gates + (bh * a.nch + c) * (a.p_lo ? 8 : 4) * C) + lane;
+        float2* go = reinterpret_cast<float2*>(a.gates + (bh * a.nch + c) * (a.grads ? 8 : 4) * C) + lane;
         go[0] = make_float2(b0, b1);
         go[C / 2] = make_float2(e0, e1);
         go[C] = make_float2(expf(minus(end, g0)), expf(minus(end, g1)));
         go[3 * C / 2] = make_float2(-e0, -e1);
-        if (a.p_lo) {
+        if (a.grads) {
             // for the gradients: the factors of exp(G_i - G_j) (zeros where the chunk's gate is too
             // steep for them), and G
             const bool near = m <= kRange;
@@ -233,14 +233,14 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
         } else {
             const long long at = ((bh * a.nch + c) * C + i) * C + c0;
             uint4* ph = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.p_hi) + at);
-            uint4* pl = a.p_lo ? reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.p_lo) + at) : nullptr;
+            uint4* pl = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.p_lo) + at);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t h8[4], l8[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split2(x[8 * j + 2 * e], x[8 * j + 2 * e + 1], h8[e], l8[e]);
                 ph[j] = make_uint4(h8[0], h8[1], h8[2], h8[3]);
-                if (pl) pl[j] = make_uint4(l8[0], l8[1], l8[2], l8[3]);
+                pl[j] = make_uint4(l8[0], l8[1], l8[2], l8[3]);
             }
         }
     }
