@@ -13,10 +13,14 @@
 // tiles are fewer than the SMs they narrow to 32 columns so that more SMs pull (the launcher).
 #include <cuda_bf16.h>
 
+#include "gla_delta_dev.cuh"
 #include "gla_delta_internal.h"
 
 namespace gla {
 namespace {
+
+using delta::fma2;
+using delta::mul2;
 
 constexpr int NT = 256;
 constexpr int NW = NT / 32;
@@ -86,13 +90,18 @@ __global__ void __launch_bounds__(NT) gla_delta_step_kernel(DeltaStep a)
     const bool in = col < a.dv;           // dv is a multiple of 16: a group of four is in or out
     const int row0 = r * RPT;
 
-    float4 S[RPT];
+    float2 S[RPT][2];
     const size_t sbase = (size_t)bh * a.dk * a.dv + col;
 #pragma unroll
     for (int i = 0; i < RPT; ++i)
-        S[i] = a.S0 && in && row0 + i < a.dk
-                   ? __ldcs(reinterpret_cast<const float4*>(a.S0 + sbase + (size_t)(row0 + i) * a.dv))
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    {
+        const float4 x = a.S0 && in && row0 + i < a.dk
+                             ? __ldcs(reinterpret_cast<const float4*>(a.S0 + sbase + (size_t)(row0 + i) * a.dv))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        S[i][0] = make_float2(x.x, x.y);
+        S[i][1] = make_float2(x.z, x.w);
+    }
+    auto row4 = [&](int i) { return make_float4(S[i][0].x, S[i][0].y, S[i][1].x, S[i][1].y); };
 
     const E* gq = static_cast<const E*>(a.q) + (size_t)bk * a.T * a.dk;
     const E* gk = static_cast<const E*>(a.k) + (size_t)bk * a.T * a.dk;
@@ -128,24 +137,28 @@ __global__ void __launch_bounds__(NT) gla_delta_step_kernel(DeltaStep a)
             float* kp = a.keep + ((size_t)bh * nkeep + t0 / kDeltaKeep) * a.dk * a.dv + col;
 #pragma unroll
             for (int i = 0; i < RPT; ++i)
-                if (row0 + i < a.dk) *reinterpret_cast<float4*>(kp + (size_t)(row0 + i) * a.dv) = S[i];
+                if (row0 + i < a.dk) *reinterpret_cast<float4*>(kp + (size_t)(row0 + i) * a.dv) = row4(i);
         }
         for (int t = 0; t < n; ++t) {
             float kr[RPT];
-            float4 ks = make_float4(0.f, 0.f, 0.f, 0.f), qs = ks;
+            float4 ks, qs;
             float qk = 0.f;
             read_row<RPT>(&sk[t][row0], kr);
             {
                 float qr[RPT];
                 read_row<RPT>(&sq[t][row0], qr);
+                float2 kp[2] = {}, qp[2] = {};
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                    ks.x = fmaf(kr[i], S[i].x, ks.x); ks.y = fmaf(kr[i], S[i].y, ks.y);
-                    ks.z = fmaf(kr[i], S[i].z, ks.z); ks.w = fmaf(kr[i], S[i].w, ks.w);
-                    qs.x = fmaf(qr[i], S[i].x, qs.x); qs.y = fmaf(qr[i], S[i].y, qs.y);
-                    qs.z = fmaf(qr[i], S[i].z, qs.z); qs.w = fmaf(qr[i], S[i].w, qs.w);
+                    const float2 kk = make_float2(kr[i], kr[i]), qq = make_float2(qr[i], qr[i]);
+                    kp[0] = fma2(kk, S[i][0], kp[0]);
+                    kp[1] = fma2(kk, S[i][1], kp[1]);
+                    qp[0] = fma2(qq, S[i][0], qp[0]);
+                    qp[1] = fma2(qq, S[i][1], qp[1]);
                     qk = fmaf(qr[i], kr[i], qk);
                 }
+                ks = make_float4(kp[0].x, kp[0].y, kp[1].x, kp[1].y);
+                qs = make_float4(qp[0].x, qp[0].y, qp[1].x, qp[1].y);
             }
             // the row groups of one warp, then the warps through shared memory
 #pragma unroll
@@ -178,10 +191,12 @@ __global__ void __launch_bounds__(NT) gla_delta_step_kernel(DeltaStep a)
             if (in) read_row<4>(&sv[t][4 * c], vv);
             const float4 u = make_float4(be * (vv[0] - al * ks.x), be * (vv[1] - al * ks.y),
                                          be * (vv[2] - al * ks.z), be * (vv[3] - al * ks.w));
+            const float2 u0 = make_float2(u.x, u.y), u1 = make_float2(u.z, u.w), aa = make_float2(al, al);
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
-                S[i].x = fmaf(kr[i], u.x, al * S[i].x); S[i].y = fmaf(kr[i], u.y, al * S[i].y);
-                S[i].z = fmaf(kr[i], u.z, al * S[i].z); S[i].w = fmaf(kr[i], u.w, al * S[i].w);
+                const float2 kk = make_float2(kr[i], kr[i]);
+                S[i][0] = fma2(kk, u0, mul2(aa, S[i][0]));
+                S[i][1] = fma2(kk, u1, mul2(aa, S[i][1]));
             }
             if (go && r == 0 && in)
                 store4(go + (size_t)(t0 + t) * a.dv + col,
@@ -193,12 +208,149 @@ __global__ void __launch_bounds__(NT) gla_delta_step_kernel(DeltaStep a)
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
             if (row0 + i < a.dk)
-                __stcs(reinterpret_cast<float4*>(a.ST + sbase + (size_t)(row0 + i) * a.dv), S[i]);
+                __stcs(reinterpret_cast<float4*>(a.ST + sbase + (size_t)(row0 + i) * a.dv), row4(i));
+    }
+}
+
+__device__ __forceinline__ void cp16(void* dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+// The same recurrence for several tokens: nothing but the block's token loads is shared between
+// warps, so no barrier stands between two tokens. A warp owns four columns; lane (r, c) holds rows
+// r RPT .. of one of them, and a token's two sums cross eight lanes in four shuffle steps (about
+// 250 cycles a token at dk = 64, 1000 in the kernel above, whose warps meet at every token). Its
+// state accesses are 16 bytes a row and warp, the reason why single tokens take the other kernel.
+template <typename E, int DK>
+__global__ void __launch_bounds__(256) gla_delta_tokens_kernel(DeltaStep a)
+{
+    constexpr int NT = 256, NW = 8, CT = 32, RPT = DK / 8, V = 16 / sizeof(E);
+    __shared__ __align__(16) E sq[2][TB][DK], sk[2][TB][DK], sv[2][TB][CT];
+    __shared__ float sal[2][TB], sbe[2][TB], sqk[2][TB];
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, c = lane & 3, r = lane >> 2;
+    const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H;
+    const int bk = b * a.Hk + h / (a.H / a.Hk);
+    const int c0 = blockIdx.y * CT, col = c0 + 4 * warp + c;
+    const bool in = col < a.dv;
+    const int row0 = r * RPT;
+
+    const E* gq = static_cast<const E*>(a.q) + (size_t)bk * a.T * a.dk;
+    const E* gk = static_cast<const E*>(a.k) + (size_t)bk * a.T * a.dk;
+    const E* gv = static_cast<const E*>(a.v) + (size_t)bh * a.T * a.dv;
+    E* go = a.O ? static_cast<E*>(a.O) + (size_t)bh * a.T * a.dv : nullptr;
+    const int nkeep = (a.T + kDeltaKeep - 1) / kDeltaKeep;
+
+    // tokens t0 .. of the sequence on their way to buffer f
+    auto fetch = [&](int t0, int f) {
+        const int n = min(TB, a.T - t0);
+        for (int i = tid; i < n * (DK / V); i += NT) {
+            const int t = i / (DK / V), x = i % (DK / V) * V;
+            if (x < a.dk) {
+                cp16(&sq[f][t][x], gq + (size_t)(t0 + t) * a.dk + x);
+                cp16(&sk[f][t][x], gk + (size_t)(t0 + t) * a.dk + x);
+            }
+        }
+        for (int i = tid; i < n * (CT / V); i += NT) {
+            const int t = i / (CT / V), x = i % (CT / V) * V;
+            if (c0 + x < a.dv) cp16(&sv[f][t][x], gv + (size_t)(t0 + t) * a.dv + c0 + x);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (tid < n) {
+            sal[f][tid] = a.log_g ? expf(a.log_g[(size_t)bh * a.T + t0 + tid]) : 1.f;
+            sbe[f][tid] = to_f(static_cast<const E*>(a.beta)[(size_t)bh * a.T + t0 + tid]);
+        }
+    };
+    if (a.dk < DK)   // keys past dk are zero in both buffers, for good
+        for (int i = tid; i < 2 * TB * (DK - a.dk); i += NT) {
+            const int x = a.dk + i % (DK - a.dk), t = i / (DK - a.dk);
+            (&sq[0][0][0])[t * DK + x] = E(0.f);
+            (&sk[0][0][0])[t * DK + x] = E(0.f);
+        }
+    fetch(0, 0);
+
+    float2 S[RPT / 2];
+    const size_t sbase = (size_t)bh * a.dk * a.dv + col;
+#pragma unroll
+    for (int i = 0; i < RPT / 2; ++i) {
+        const int x = row0 + 2 * i;      // dk is a multiple of 16: a pair is in or out
+        const bool ok = a.S0 && in && x < a.dk;
+        S[i].x = ok ? a.S0[sbase + (size_t)x * a.dv] : 0.f;
+        S[i].y = ok ? a.S0[sbase + (size_t)(x + 1) * a.dv] : 0.f;
+    }
+
+    for (int t0 = 0, f = 0; t0 < a.T; t0 += TB, f ^= 1) {
+        const int n = min(TB, a.T - t0);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        for (int t = warp; t < n; t += NW) {
+            float s = 0.f;
+            for (int x = lane; x < DK; x += 32) s = fmaf(to_f(sq[f][t][x]), to_f(sk[f][t][x]), s);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+            if (lane == 0) sqk[f][t] = s;
+        }
+        if (t0 + TB < a.T) fetch(t0 + TB, f ^ 1);
+        if (a.keep && in) {
+            float* kp = a.keep + ((size_t)bh * nkeep + t0 / kDeltaKeep) * a.dk * a.dv + col;
+#pragma unroll
+            for (int i = 0; i < RPT / 2; ++i)
+                if (row0 + 2 * i < a.dk) {
+                    kp[(size_t)(row0 + 2 * i) * a.dv] = S[i].x;
+                    kp[(size_t)(row0 + 2 * i + 1) * a.dv] = S[i].y;
+                }
+        }
+        __syncthreads();                 // q . k of every token
+        for (int t = 0; t < n; ++t) {
+            float k[RPT], q[RPT];
+            read_row<RPT>(&sk[f][t][row0], k);
+            read_row<RPT>(&sq[f][t][row0], q);
+            const float al = sal[f][t], be = sbe[f][t], qk = sqk[f][t], v = to_f(sv[f][t][4 * warp + c]);
+            float2 ks[2] = {}, qs[2] = {};
+#pragma unroll
+            for (int i = 0; i < RPT / 2; ++i) {
+                ks[i & 1] = fma2(make_float2(k[2 * i], k[2 * i + 1]), S[i], ks[i & 1]);
+                qs[i & 1] = fma2(make_float2(q[2 * i], q[2 * i + 1]), S[i], qs[i & 1]);
+            }
+            float x = (ks[0].x + ks[0].y) + (ks[1].x + ks[1].y), y = (qs[0].x + qs[0].y) + (qs[1].x + qs[1].y);
+            // eight row groups (lanes 4 apart): one half of the lanes sums k S, the other q S
+            const bool up = lane & 16;
+            const float sent = __shfl_xor_sync(~0u, up ? x : y, 16);
+            float m = (up ? y : x) + sent;
+            m += __shfl_xor_sync(~0u, m, 8);
+            m += __shfl_xor_sync(~0u, m, 4);
+            const float kS = __shfl_sync(~0u, m, c), qS = __shfl_sync(~0u, m, 16 + c);
+            const float u = in ? be * (v - al * kS) : 0.f;
+#pragma unroll
+            for (int i = 0; i < RPT / 2; ++i)
+                S[i] = fma2(make_float2(k[2 * i], k[2 * i + 1]), make_float2(u, u),
+                            mul2(make_float2(al, al), S[i]));
+            if (go && r == 0 && in) {
+                const float o = a.scale * fmaf(qk, u, al * qS);
+                if constexpr (sizeof(E) == 2) go[(size_t)(t0 + t) * a.dv + col] = __float2bfloat16_rn(o);
+                else go[(size_t)(t0 + t) * a.dv + col] = o;
+            }
+        }
+    }
+    if (a.ST && in) {
+#pragma unroll
+        for (int i = 0; i < RPT / 2; ++i)
+            if (row0 + 2 * i < a.dk) {
+                a.ST[sbase + (size_t)(row0 + 2 * i) * a.dv] = S[i].x;
+                a.ST[sbase + (size_t)(row0 + 2 * i + 1) * a.dv] = S[i].y;
+            }
     }
 }
 
 template <typename E, int DK>
 cudaError_t launch_dk(const DeltaStep& a, cudaStream_t s) {
+    // Beyond a few tokens the barriers between them cost more than the narrow state accesses (20
+    // tokens of 128 heads, dk = dv = 128: 29 us against 46; 3 tokens of 256 heads: 21 against 17).
+    if (a.T > 8) {
+        gla_delta_tokens_kernel<E, DK><<<dim3((unsigned)(a.B * a.H), (a.dv + 31) / 32), 256, 0, s>>>(a);
+        return cudaGetLastError();
+    }
     // A thread holds at least four rows and at most 32 of them of four columns.
     constexpr int WIDE = DK <= 128 ? 128 : 64, NARROW = DK == 64 ? 64 : 32;
     const unsigned BH = (unsigned)(a.B * a.H);

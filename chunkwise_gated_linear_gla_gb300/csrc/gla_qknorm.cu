@@ -30,7 +30,8 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int VEC = 8;        // values per lane
-constexpr int UNR = 4;        // heads in flight per thread
+constexpr int UNR = 4;        // heads in flight per thread (backward: 2, of two rows each)
+constexpr long long kBlocksPerSm = 16;
 
 struct QkArgs {
     const void* x[2]; void* y[2];                 // q, k (strided) and their results (dense)
@@ -44,8 +45,19 @@ struct QkArgs {
     int hsplit;                                   // heads (q's and k's in a row) per block
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[VEC]) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
+// Eight values as loaded, and as fp32: a row waits in its own type (half the registers in bf16).
+template <typename E> struct Raw;
+template <> struct Raw<__nv_bfloat16> { typedef uint4 type; };
+template <> struct Raw<float> { struct type { float4 a, b; }; };
+__device__ __forceinline__ uint4 fetch(const __nv_bfloat16* p) {
+    return p ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ Raw<float>::type fetch(const float* p) {
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    return p ? Raw<float>::type{__ldcs(reinterpret_cast<const float4*>(p)), __ldcs(reinterpret_cast<const float4*>(p) + 1)}
+             : Raw<float>::type{z, z};
+}
+__device__ __forceinline__ void unpack(const uint4& w, float (&x)[VEC]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -53,9 +65,8 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[VEC]) {
         x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[VEC]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ void unpack(const Raw<float>::type& w, float (&x)[VEC]) {
+    x[0] = w.a.x; x[1] = w.a.y; x[2] = w.a.z; x[3] = w.a.w; x[4] = w.b.x; x[5] = w.b.y; x[6] = w.b.z; x[7] = w.b.w;
 }
 __device__ __forceinline__ void save8(__nv_bfloat16* p, const float (&x)[VEC]) {
     uint32_t u[4];
@@ -123,22 +134,22 @@ __device__ __forceinline__ void rotate(float (&x)[VEC], const float (&cs)[VEC], 
 
 // One block: NT / LPR tokens by hsplit heads. BWD: dy, x -> dx and the weights' partials.
 template <typename E, int LPR, bool BWD>
-__global__ void __launch_bounds__(NT) gla_qk_norm_rope_kernel(QkArgs a)
+__global__ void __launch_bounds__(NT, BWD ? 2 : 3) gla_qk_norm_rope_kernel(QkArgs a)
 {
-    constexpr int RPB = NT / LPR;
+    constexpr int RPB = NT / LPR, U = BWD ? 2 : UNR;
     __shared__ unsigned long long turns[LPR * VEC / 2];
     __shared__ float red[BWD ? NT * VEC : 1];
     const int l = threadIdx.x % LPR, lo = l * VEC, row = threadIdx.x / LPR;
     const long long ntok = (long long)a.B * a.T;
-    const int nh = a.heads[0] + a.heads[1];
     const bool lane_in = lo < a.d;
     for (int i = threadIdx.x; i < a.rot / 2; i += NT) turns[i] = turn_units(a.inv_freq[i]);
     __syncthreads();
 
-    const int h0 = blockIdx.y * a.hsplit, h1 = min(nh, h0 + a.hsplit);
-    float dw[BWD ? 2 : 1][VEC];
+    // this block's heads of q (z = 0) and of k (z = 1)
+    const int h0 = blockIdx.y * a.hsplit, h1 = min(a.heads[0] + a.heads[1], h0 + a.hsplit);
+    float dw[2][VEC];
 #pragma unroll
-    for (int z = 0; z < (BWD ? 2 : 1); ++z)
+    for (int z = 0; z < 2; ++z)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) dw[z][j] = 0.f;
     const float invn = a.norm == GLA_NORM_RMS ? 1.f / (float)a.d : 1.f;
@@ -147,7 +158,7 @@ __global__ void __launch_bounds__(NT) gla_qk_norm_rope_kernel(QkArgs a)
         const long long tok = t0 + row;
         const bool on = lane_in && tok < ntok;
         const long long tk = tok < ntok ? tok : ntok - 1;
-        const long long b = tk / a.T, t = tk - b * a.T;
+        const long long b = ntok <= 0x7fffffff ? (unsigned)tk / (unsigned)a.T : tk / a.T, t = tk - b * a.T;
         float cs[VEC], sn[VEC];
         if (lo < a.rot) {
             const unsigned long long pos = (unsigned long long)(a.positions ? a.positions[tk] : a.start + t);
@@ -159,67 +170,59 @@ __global__ void __launch_bounds__(NT) gla_qk_norm_rope_kernel(QkArgs a)
                 sincospif((float)top * 4.6566128730773926e-10f, &sn[j], &cs[j]);   // 2^-31: half turns
             }
         }
-        for (int hb = h0; hb < h1; hb += UNR) {
-            float x[UNR][VEC], g[BWD ? UNR : 1][VEC];
 #pragma unroll
-            for (int u = 0; u < UNR; ++u) {
-                const int hh = hb + u, z = hh >= a.heads[0], h = z ? hh - a.heads[0] : hh;
+        for (int z = 0; z < 2; ++z) {
+            const int hb0 = max(0, h0 - (z ? a.heads[0] : 0)), hb1 = min(a.heads[z], h1 - (z ? a.heads[0] : 0));
+            if (hb0 >= hb1) continue;
+            const float* wz = lane_in ? a.w[z] : nullptr;
+            const E* xp = static_cast<const E*>(a.x[z]) + b * a.sx[z][0] + t * a.sx[z][2] + lo;
+            const long long dense = (b * a.heads[z] * a.T + t) * a.d + lo, hstep = (long long)a.T * a.d;
+            for (int hb = hb0; hb < hb1; hb += U) {
+                typename Raw<E>::type xr[U], gr[BWD ? U : 1];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) x[u][j] = 0.f;
-                if (hh < h1 && on)
-                    load8(static_cast<const E*>(a.x[z]) + b * a.sx[z][0] + h * a.sx[z][1] + t * a.sx[z][2] + lo, x[u]);
-                if constexpr (BWD) {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) g[u][j] = 0.f;
-                    if (hh < h1 && on)
-                        load8(static_cast<const E*>(a.dy[z]) + ((b * a.heads[z] + h) * a.T + t) * a.d + lo, g[u]);
+                for (int u = 0; u < U; ++u) {
+                    const bool ok = hb + u < hb1 && on;
+                    xr[u] = fetch(ok ? xp + (hb + u) * a.sx[z][1] : nullptr);
+                    if constexpr (BWD)
+                        gr[u] = fetch(ok ? static_cast<const E*>(a.dy[z]) + dense + (hb + u) * hstep : nullptr);
                 }
-            }
 #pragma unroll
-            for (int u = 0; u < UNR; ++u) {
-                const int hh = hb + u;
-                if (hh >= h1) break;
-                const int z = hh >= a.heads[0], h = z ? hh - a.heads[0] : hh;
-                float inv = 1.f;
-                if (a.norm != GLA_NORM_NONE) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) s = fmaf(x[u][j], x[u][j], s);
-                    inv = 1.f / sqrtf(fmaf(row_sum<LPR>(s), invn, a.eps));
-                }
-                float w[VEC];
-                if (a.w[z] && lane_in) {
-                    const float4 p = *reinterpret_cast<const float4*>(a.w[z] + lo);
-                    const float4 q = *reinterpret_cast<const float4*>(a.w[z] + lo + 4);
-                    w[0] = p.x; w[1] = p.y; w[2] = p.z; w[3] = p.w; w[4] = q.x; w[5] = q.y; w[6] = q.z; w[7] = q.w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) w[j] = 1.f;
-                }
-                if constexpr (!BWD) {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) x[u][j] *= inv * w[j];
-                    if (a.rot) rotate<LPR>(x[u], cs, sn, lo, a.rot, a.interleaved, 1.f);
-                    if (on) save8(static_cast<E*>(a.y[z]) + ((b * a.heads[z] + h) * a.T + t) * a.d + lo, x[u]);
-                } else {
-                    if (a.rot) rotate<LPR>(g[u], cs, sn, lo, a.rot, a.interleaved, -1.f);
-                    float s = 0.f;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        x[u][j] *= inv;                       // x^
-                        const float p = g[u][j] * x[u][j];
-                        if (z == 0) dw[0][j] += p;            // (rows past the last token hold zeros)
-                        else dw[1][j] += p;
-                        g[u][j] *= w[j];
-                        s = fmaf(g[u][j], x[u][j], s);
-                    }
+                for (int u = 0; u < U; ++u) {
+                    const int h = hb + u;
+                    if (h >= hb1) break;
+                    float x[VEC];
+                    unpack(xr[u], x);
+                    float inv = 1.f;
                     if (a.norm != GLA_NORM_NONE) {
-                        s = row_sum<LPR>(s) * invn;
+                        float s = 0.f;
 #pragma unroll
-                        for (int j = 0; j < VEC; ++j) g[u][j] = inv * fmaf(-x[u][j], s, g[u][j]);
+                        for (int j = 0; j < VEC; ++j) s = fmaf(x[j], x[j], s);
+                        inv = 1.f / sqrtf(fmaf(row_sum<LPR>(s), invn, a.eps));
                     }
-                    if (on)
-                        save8(static_cast<E*>(a.dx[z]) + b * a.sdx[z][0] + h * a.sdx[z][1] + t * a.sdx[z][2] + lo, g[u]);
+                    if constexpr (!BWD) {
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) x[j] *= wz ? inv * wz[lo + j] : inv;
+                        if (a.rot) rotate<LPR>(x, cs, sn, lo, a.rot, a.interleaved, 1.f);
+                        if (on) save8(static_cast<E*>(a.y[z]) + dense + h * hstep, x);
+                    } else {
+                        float g[VEC];
+                        unpack(gr[u], g);
+                        if (a.rot) rotate<LPR>(g, cs, sn, lo, a.rot, a.interleaved, -1.f);
+                        float s = 0.f;
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) {
+                            x[j] *= inv;                                    // x^
+                            dw[z][j] = fmaf(g[j], x[j], dw[z][j]);          // (rows past the last token hold zeros)
+                            if (wz) g[j] *= wz[lo + j];
+                            s = fmaf(g[j], x[j], s);
+                        }
+                        if (a.norm != GLA_NORM_NONE) {
+                            s = row_sum<LPR>(s) * invn;
+#pragma unroll
+                            for (int j = 0; j < VEC; ++j) g[j] = inv * fmaf(-x[j], s, g[j]);
+                        }
+                        if (on) save8(static_cast<E*>(a.dx[z]) + b * a.sdx[z][0] + h * a.sdx[z][1] + t * a.sdx[z][2] + lo, g);
+                    }
                 }
             }
         }
@@ -265,10 +268,11 @@ dim3 grid_of(const QkArgs& a, int lpr, int sms, bool bwd, int* hsplit)
 {
     const long long rows = NT / lpr, tg = ((long long)a.B * a.T + rows - 1) / rows;
     const int nh = a.heads[0] + a.heads[1];
-    // Few tokens: the heads are spread over blocks (each forms the token's angles again) until
-    // there are four blocks per SM; many: one block takes a token's every head.
+    // The heads are spread over blocks (each forms the token's angles again) until there are
+    // kBlocksPerSm blocks per SM, so that the last wave's idle SMs cost little: forward only, where
+    // blocks leave nothing behind.
     int split = 1;
-    while (split < nh && tg * split < 4LL * sms) split *= 2;
+    while (split < nh && tg * split < (bwd ? 4LL : kBlocksPerSm) * sms) split *= 2;
     if (split > nh) split = nh;
     *hsplit = (nh + split - 1) / split;
     const int gy = (nh + *hsplit - 1) / *hsplit;
