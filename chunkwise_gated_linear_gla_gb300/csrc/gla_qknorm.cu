@@ -7,8 +7,8 @@
 //
 // Bound by HBM: every row is read once and written once (backward: x and dy read, dx written).
 // A row is LPR lanes of eight values (16 bytes in bf16); a thread keeps its row of the batch and
-// takes that token's heads one after the other, so a token's angles are formed once per thread
-// and four heads' loads are in flight at a time. Reads go through strides (a fused projection's
+// takes that token's heads one after the other, so a token's angles are formed once per block
+// (in shared memory) and four heads' loads are in flight at a time. Reads go through strides (a fused projection's
 // [B,T,heads,d] slice), writes are dense [B,H,T,d].
 //
 // Angles: the caller's frequencies are radians per position in fp64. Each becomes a fraction of
@@ -104,31 +104,26 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// The rotation of this lane's eight values (dir = 1) or its transpose (dir = -1). Neighbouring
-// pairs lie in the lane; halves pair value i with i + rot / 2, `hop` lanes on.
+// The rotation of this lane's eight values. Neighbouring pairs lie in the lane; halves pair value
+// i with i + rot / 2, `hop` lanes on. The sines carry the sign that their place wants (and the
+// transpose's), lanes past `rot` have cosine one and sine zero.
 template <int LPR>
-__device__ __forceinline__ void rotate(float (&x)[VEC], const float (&cs)[VEC], const float (&sn)[VEC], int lo,
-                                       int rot, int interleaved, float dir)
+__device__ __forceinline__ void rotate(float (&x)[VEC], const float (&cs)[VEC], const float (&sn)[VEC], int from,
+                                       int interleaved)
 {
     if (interleaved) {
-        if (lo < rot) {
 #pragma unroll
-            for (int j = 0; j < VEC; j += 2) {
-                const float a = x[j], b = x[j + 1], s = dir * sn[j / 2];
-                x[j] = a * cs[j / 2] - b * s;
-                x[j + 1] = fmaf(b, cs[j / 2], a * s);
-            }
+        for (int j = 0; j < VEC; j += 2) {
+            const float a = x[j], b = x[j + 1], s = sn[j / 2];
+            x[j] = fmaf(a, cs[j / 2], -b * s);
+            x[j + 1] = fmaf(b, cs[j / 2], a * s);
         }
         return;
     }
-    const int hop = rot / (2 * VEC), l = threadIdx.x % LPR;
-    const bool low = lo < rot / 2, on = lo < rot;
-    const int from = on ? (low ? l + hop : l - hop) : l;
-    const float sg = low ? -dir : dir;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
         const float m = __shfl_sync(~0u, x[j], from, LPR);
-        if (on) x[j] = fmaf(x[j], cs[j], sg * sn[j] * m);
+        x[j] = fmaf(x[j], cs[j], sn[j] * m);
     }
 }
 
@@ -138,7 +133,10 @@ __global__ void __launch_bounds__(NT, BWD ? 2 : 3) gla_qk_norm_rope_kernel(QkArg
 {
     constexpr int RPB = NT / LPR, U = BWD ? 2 : UNR;
     __shared__ unsigned long long turns[LPR * VEC / 2];
-    __shared__ float red[BWD ? NT * VEC : 1];
+    // cosines and sines of the block's tokens; the weights' sums take their place at the end
+    __shared__ __align__(16) float trig[2][RPB][LPR * VEC / 2];
+    float* red = &trig[0][0][0];
+    static_assert(!BWD || sizeof(trig) >= NT * VEC * 4, "weights' sums");
     const int l = threadIdx.x % LPR, lo = l * VEC, row = threadIdx.x / LPR;
     const long long ntok = (long long)a.B * a.T;
     const bool lane_in = lo < a.d;
@@ -160,70 +158,99 @@ __global__ void __launch_bounds__(NT, BWD ? 2 : 3) gla_qk_norm_rope_kernel(QkArg
         const long long tk = tok < ntok ? tok : ntok - 1;
         const long long b = ntok <= 0x7fffffff ? (unsigned)tk / (unsigned)a.T : tk / a.T, t = tk - b * a.T;
         float cs[VEC], sn[VEC];
-        if (lo < a.rot) {
-            const unsigned long long pos = (unsigned long long)(a.positions ? a.positions[tk] : a.start + t);
-            const int first = a.interleaved ? lo / 2 : (lo < a.rot / 2 ? lo : lo - a.rot / 2);
+        if (a.rot) {
+            // one angle per token and pair, shared by the row's lanes (a pair's halves lie in two)
+            const int half = a.rot / 2;
+            __syncthreads();
+            for (int i = threadIdx.x; i < RPB * half; i += NT) {
+                const int rr = i / half, p = i - rr * half;
+                const long long tt = min(t0 + rr, ntok - 1);
+                const unsigned long long pos =
+                    (unsigned long long)(a.positions ? a.positions[tt] : a.start + (ntok <= 0x7fffffff ? (unsigned)tt % (unsigned)a.T : tt % a.T));
+                const int top = (int)(unsigned)((pos * turns[p]) >> 32);
+                sincospif((float)top * 4.6566128730773926e-10f, &trig[1][rr][p], &trig[0][rr][p]);   // 2^-31: half turns
+            }
+            __syncthreads();
+            const bool turned = lo < a.rot, low = lo < half;
+            const int first = !turned ? 0 : a.interleaved ? lo / 2 : low ? lo : lo - half;
+            const float sg = (a.interleaved || !low) != BWD ? 1.f : -1.f;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
+            for (int j = 0; j < VEC; j += 4) {
                 if (a.interleaved && j >= VEC / 2) break;
-                const int top = (int)(unsigned)((pos * turns[first + j]) >> 32);
-                sincospif((float)top * 4.6566128730773926e-10f, &sn[j], &cs[j]);   // 2^-31: half turns
+                const float4 c4 = *reinterpret_cast<const float4*>(&trig[0][row][first + j]);
+                const float4 s4 = *reinterpret_cast<const float4*>(&trig[1][row][first + j]);
+                const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    cs[j + e] = turned ? c[e] : 1.f;
+                    sn[j + e] = turned ? sg * s[e] : 0.f;
+                }
             }
         }
+        const int hop = a.rot / (2 * VEC);
+        const int from = lo < a.rot / 2 ? l + hop : lo < a.rot ? l - hop : l;   // the lane of the pairs' other halves
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const int hb0 = max(0, h0 - (z ? a.heads[0] : 0)), hb1 = min(a.heads[z], h1 - (z ? a.heads[0] : 0));
             if (hb0 >= hb1) continue;
-            const float* wz = lane_in ? a.w[z] : nullptr;
-            const E* xp = static_cast<const E*>(a.x[z]) + b * a.sx[z][0] + t * a.sx[z][2] + lo;
-            const long long dense = (b * a.heads[z] * a.T + t) * a.d + lo, hstep = (long long)a.T * a.d;
+            float w[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) w[j] = a.w[z] && lane_in ? a.w[z][lo + j] : 1.f;
+            const E* xp = static_cast<const E*>(a.x[z]) + b * a.sx[z][0] + hb0 * a.sx[z][1] + t * a.sx[z][2] + lo;
+            const long long hstep = (long long)a.T * a.d, dense = ((b * a.heads[z] + hb0) * a.T + t) * a.d + lo;
+            E* yp = BWD ? static_cast<E*>(a.dx[z]) + b * a.sdx[z][0] + hb0 * a.sdx[z][1] + t * a.sdx[z][2] + lo
+                        : static_cast<E*>(a.y[z]) + dense;
+            const E* gp = BWD ? static_cast<const E*>(a.dy[z]) + dense : nullptr;
+            const long long xstep = a.sx[z][1], ystep = BWD ? a.sdx[z][1] : hstep;
+            auto one = [&](const typename Raw<E>::type& xr, const typename Raw<E>::type& gr, E* out) {
+                float x[VEC];
+                unpack(xr, x);
+                float inv = 1.f;
+                if (a.norm != GLA_NORM_NONE) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) s = fmaf(x[j], x[j], s);
+                    inv = rsqrtf(fmaf(row_sum<LPR>(s), invn, a.eps));
+                }
+                if constexpr (!BWD) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) x[j] *= inv * w[j];
+                    if (a.rot) rotate<LPR>(x, cs, sn, from, a.interleaved);
+                    if (on) save8(out, x);
+                } else {
+                    float g[VEC];
+                    unpack(gr, g);
+                    if (a.rot) rotate<LPR>(g, cs, sn, from, a.interleaved);
+                    float s = 0.f;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        x[j] *= inv;                                    // x^
+                        dw[z][j] = fmaf(g[j], x[j], dw[z][j]);          // (rows past the last token hold zeros)
+                        g[j] *= w[j];
+                        s = fmaf(g[j], x[j], s);
+                    }
+                    if (a.norm != GLA_NORM_NONE) {
+                        s = row_sum<LPR>(s) * invn;
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) g[j] = inv * fmaf(-x[j], s, g[j]);
+                    }
+                    if (on) save8(out, g);
+                }
+            };
             for (int hb = hb0; hb < hb1; hb += U) {
-                typename Raw<E>::type xr[U], gr[BWD ? U : 1];
+                typename Raw<E>::type xr[U], gr[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const bool ok = hb + u < hb1 && on;
-                    xr[u] = fetch(ok ? xp + (hb + u) * a.sx[z][1] : nullptr);
-                    if constexpr (BWD)
-                        gr[u] = fetch(ok ? static_cast<const E*>(a.dy[z]) + dense + (hb + u) * hstep : nullptr);
+                    xr[u] = fetch(ok ? xp + u * xstep : nullptr);
+                    if constexpr (BWD) gr[u] = fetch(ok ? gp + u * hstep : nullptr);
                 }
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = hb + u;
-                    if (h >= hb1) break;
-                    float x[VEC];
-                    unpack(xr[u], x);
-                    float inv = 1.f;
-                    if (a.norm != GLA_NORM_NONE) {
-                        float s = 0.f;
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) s = fmaf(x[j], x[j], s);
-                        inv = 1.f / sqrtf(fmaf(row_sum<LPR>(s), invn, a.eps));
-                    }
-                    if constexpr (!BWD) {
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) x[j] *= wz ? inv * wz[lo + j] : inv;
-                        if (a.rot) rotate<LPR>(x, cs, sn, lo, a.rot, a.interleaved, 1.f);
-                        if (on) save8(static_cast<E*>(a.y[z]) + dense + h * hstep, x);
-                    } else {
-                        float g[VEC];
-                        unpack(gr[u], g);
-                        if (a.rot) rotate<LPR>(g, cs, sn, lo, a.rot, a.interleaved, -1.f);
-                        float s = 0.f;
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) {
-                            x[j] *= inv;                                    // x^
-                            dw[z][j] = fmaf(g[j], x[j], dw[z][j]);          // (rows past the last token hold zeros)
-                            if (wz) g[j] *= wz[lo + j];
-                            s = fmaf(g[j], x[j], s);
-                        }
-                        if (a.norm != GLA_NORM_NONE) {
-                            s = row_sum<LPR>(s) * invn;
-#pragma unroll
-                            for (int j = 0; j < VEC; ++j) g[j] = inv * fmaf(-x[j], s, g[j]);
-                        }
-                        if (on) save8(static_cast<E*>(a.dx[z]) + b * a.sdx[z][0] + h * a.sdx[z][1] + t * a.sdx[z][2] + lo, g);
-                    }
-                }
+                for (int u = 0; u < U; ++u)
+                    if (hb + u < hb1) one(xr[u], gr[u], yp + u * ystep);
+                xp += U * xstep;
+                yp += U * ystep;
+                if constexpr (BWD) gp += U * hstep;
             }
         }
     }
