@@ -45,7 +45,7 @@ bool chunk_shape_ok(int B, int H, int T, int dk, int dv, int dtype)
 struct DeltaPlan {
     int path = GLA_PATH_SIMT;
     int nch = 0;
-    size_t off_th = 0, off_tl = 0, off_p = 0, off_pl = 0, off_g = 0;
+    size_t off_t = 0, off_p = 0, off_g = 0;
     size_t ws = 0;
 };
 
@@ -63,10 +63,8 @@ gla_status plan_fwd(const gla_delta_params* p, DeltaPlan& pl)
     const size_t nc = (size_t)p->B * p->H * pl.nch;
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
-    pl.off_th = take(nc * kChunk * kChunk * 2);
-    pl.off_tl = take(nc * kChunk * kChunk * 2);
-    pl.off_p = take(nc * kChunk * kChunk * 2);
-    pl.off_pl = take(nc * kChunk * kChunk * 2);
+    pl.off_t = take(nc * 2 * kChunk * kChunk * 2);
+    pl.off_p = take(nc * 2 * kChunk * kChunk * 2);
     pl.off_g = take(nc * 4 * kChunk * 4);
     pl.ws = off;
     return GLA_OK;
@@ -96,7 +94,7 @@ struct DeltaBwdPlan {
     int tiles = 0;
     int nch = 0;
     // chunk form: prep's T and P in two parts, gates; the sweeps' states, U and what dV's rounding left
-    size_t off_th = 0, off_tl = 0, off_ph = 0, off_pl = 0, off_g = 0, off_sh = 0, off_sl = 0, off_uh = 0, off_ul = 0,
+    size_t off_t = 0, off_p = 0, off_g = 0, off_sh = 0, off_sl = 0, off_uh = 0, off_ul = 0,
            off_dh = 0, off_dl = 0, off_xl = 0;
     // recurrent form; part_q and part_k also serve the chunk form when heads share keys
     size_t off_keep = 0, off_pq = 0, off_pk = 0, off_pg = 0, off_pb = 0, off_scr = 0;
@@ -118,8 +116,8 @@ gla_status plan_bwd(const gla_delta_bwd_params* p, DeltaBwdPlan& pl)
     if (ok && p->path != GLA_PATH_SIMT) {
         pl.path = GLA_PATH_TENSOR;
         pl.nch = (p->T + kChunk - 1) / kChunk;
-        const size_t nc = BH * pl.nch, cc = nc * kChunk * kChunk * 2, st = nc * p->dk * p->dv * 2, u = nc * kChunk * p->dv * 2;
-        pl.off_th = take(cc); pl.off_tl = take(cc); pl.off_ph = take(cc); pl.off_pl = take(cc);
+        const size_t nc = BH * pl.nch, cc = nc * 2 * kChunk * kChunk * 2, st = nc * p->dk * p->dv * 2, u = nc * kChunk * p->dv * 2;
+        pl.off_t = take(cc); pl.off_p = take(cc);
         pl.off_g = take(nc * 8 * kChunk * 4);
         pl.off_sh = take(st); pl.off_sl = take(st); pl.off_dh = take(st); pl.off_dl = take(st);
         pl.off_uh = take(u); pl.off_ul = take(u);
@@ -192,13 +190,13 @@ gla_status bwd_chunks(const gla_delta_bwd_params* p, const DeltaBwdPlan& pl, int
     float* gates = reinterpret_cast<float*>(ws + pl.off_g);
     DeltaPrep a;
     a.q = p->q; a.k = p->k; a.log_g = p->log_g; a.beta = p->beta;
-    a.t_hi = ws + pl.off_th; a.t_lo = ws + pl.off_tl; a.p_hi = ws + pl.off_ph; a.p_lo = ws + pl.off_pl; a.gates = gates;
+    a.t = ws + pl.off_t; a.p = ws + pl.off_p; a.gates = gates;
     a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.nch = pl.nch; a.scale = p->scale;
     a.grads = true; a.beta_floor = 0x1p-40f;
     cudaError_t e = launch_delta_prep(a, status, stream);
     DeltaSweep w;
     w.q = p->q; w.k = p->k; w.v = p->v;
-    w.t_hi = a.t_hi; w.t_lo = a.t_lo; w.p_hi = a.p_hi; w.p_lo = a.p_lo; w.gates = gates;
+    w.t = a.t; w.p = a.p; w.gates = gates;
     w.S_in = p->S0; w.S_out = nullptr;
     w.s_hi = ws + pl.off_sh; w.s_lo = ws + pl.off_sl; w.u_hi = ws + pl.off_uh; w.u_lo = ws + pl.off_ul;
     w.x_hi = p->grad_v; w.x_lo = ws + pl.off_xl;
@@ -266,14 +264,14 @@ gla_status gla_delta_fwd(const gla_delta_params* p, cudaStream_t stream)
         int* status = device_status_ptr();
         DeltaPrep a;
         a.q = p->q; a.k = p->k; a.log_g = p->log_g; a.beta = p->beta;
-        a.t_hi = ws + pl.off_th; a.t_lo = ws + pl.off_tl; a.p_hi = ws + pl.off_p; a.p_lo = ws + pl.off_pl;
+        a.t = ws + pl.off_t; a.p = ws + pl.off_p;
         a.gates = reinterpret_cast<float*>(ws + pl.off_g);
         a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.nch = pl.nch; a.scale = p->scale;
         a.grads = false; a.beta_floor = 0.f;
         e = launch_delta_prep(a, status, stream);
         if (e == cudaSuccess) {
             DeltaChain w;
-            w.q = p->q; w.k = p->k; w.v = p->v; w.t_hi = a.t_hi; w.t_lo = a.t_lo; w.p_hi = a.p_hi; w.p_lo = a.p_lo; w.gates = a.gates;
+            w.q = p->q; w.k = p->k; w.v = p->v; w.t = a.t; w.p = a.p; w.gates = a.gates;
             w.S0 = p->S0; w.O = p->O; w.ST = p->ST;
             w.B = p->B; w.H = p->H; w.Hk = p->Hk; w.T = p->T; w.dk = p->dk; w.dv = p->dv; w.nch = pl.nch;
             w.scale = p->scale;

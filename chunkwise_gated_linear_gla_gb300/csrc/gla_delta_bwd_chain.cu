@@ -33,9 +33,8 @@ __device__ __forceinline__ float2 f2(uint32_t a, uint32_t b) { return make_float
 template <int DK, bool REV>
 struct CL {
     static constexpr int KB = (DK / 64) * SLAB;
-    static constexpr int K_OFF = 0, V_OFF = KB, TH_OFF = V_OFF + 2 * SLAB, TL_OFF = TH_OFF + SLAB,
-                         Q_OFF = TL_OFF + SLAB, PH_OFF = Q_OFF + (REV ? KB : 0), PL_OFF = PH_OFF + (REV ? SLAB : 0),
-                         G_OFF = PL_OFF + (REV ? SLAB : 0);
+    static constexpr int K_OFF = 0, V_OFF = KB, T_OFF = V_OFF + 2 * SLAB, Q_OFF = T_OFF + 2 * SLAB,
+                         P_OFF = Q_OFF + (REV ? KB : 0), G_OFF = P_OFF + (REV ? 2 * SLAB : 0);
     static constexpr int STAGE = G_OFF + 1024;
     static constexpr int BYTES = G_OFF + 4 * C * 4;
     static constexpr int O_OFF = NST * STAGE;            // staging for the stores, 32 KB
@@ -49,7 +48,7 @@ struct CL {
 };
 
 struct Maps {
-    CUtensorMap k, v, th, tl, q, ph, pl;   // loads
+    CUtensorMap k, v, t, q, p;             // loads
     CUtensorMap sh, sl, xh, xl;            // stores: the state's parts; U's parts or dV's
 };
 
@@ -106,46 +105,44 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
 
     if (wg == 0) {
         regs_dec<56>();
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             int issued = 0;
-            for (int m = 0; m < n && !*abort_flag; ++m, ++issued) {
+            for (int m = 0; m < n; ++m, ++issued) {
+                if (__any_sync(~0u, *abort_flag)) break;
                 const int st = m % NST, c = chunk(m), t0 = c * C, at = bh * n + c;
                 if (m >= NST) wait(&empty[st], ((m / NST) - 1) & 1, abort_flag, status, ERR_TMA);
+                __syncwarp();
                 uint8_t* sb = sm + st * L::STAGE;
-                mbar_arrive_expect_tx(&full[st], L::BYTES - (wide ? 0 : SLAB));
-#pragma unroll
-                for (int i = 0; i < DK / 64; ++i) tma_load_3d(sb + L::K_OFF + i * SLAB, &mp.k, &full[st], 64 * i, t0, bk);
-                tma_load_3d(sb + L::V_OFF, &mp.v, &full[st], dv0, t0, bh);
-                if (wide) tma_load_3d(sb + L::V_OFF + SLAB, &mp.v, &full[st], dv0 + 64, t0, bh);
-                bulk_load(sb + L::G_OFF, a.gates + (size_t)at * 8 * C, 4 * C * 4, &full[st]);
-                tma_load_3d(sb + L::TH_OFF, &mp.th, &full[st], 0, 0, at);
-                tma_load_3d(sb + L::TL_OFF, &mp.tl, &full[st], 0, 0, at);
-                if (REV) {
-#pragma unroll
-                    for (int i = 0; i < DK / 64; ++i) tma_load_3d(sb + L::Q_OFF + i * SLAB, &mp.q, &full[st], 64 * i, t0, bk);
-                    tma_load_3d(sb + L::PH_OFF, &mp.ph, &full[st], 0, 0, at);
-                    tma_load_3d(sb + L::PL_OFF, &mp.pl, &full[st], 0, 0, at);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&full[st], L::BYTES);
+                    tma_load_4d(sb + L::V_OFF, &mp.v, &full[st], 0, t0, dv0 / 64, bh);   // (slabs past dv: zeros)
+                    tma_load_3d(sb + L::T_OFF, &mp.t, &full[st], 0, 0, at);
+                    if (REV) tma_load_3d(sb + L::P_OFF, &mp.p, &full[st], 0, 0, at);
+                    tma_load_4d(sb + L::K_OFF, &mp.k, &full[st], 0, t0, 0, bk);
+                    bulk_load(sb + L::G_OFF, a.gates + (size_t)at * 8 * C, 4 * C * 4, &full[st]);
+                    if (REV) tma_load_4d(sb + L::Q_OFF, &mp.q, &full[st], 0, t0, 0, bk);
                 }
-                if (m + NST < n) {
-                    const int c1 = chunk(m + NST), t1 = c1 * C, a1 = bh * n + c1;
-                    prefetch_l2_tile_3d(&mp.v, dv0, t1, bh);
-                    if (wide) prefetch_l2_tile_3d(&mp.v, dv0 + 64, t1, bh);
-                    if (blockIdx.x == 0) {
-#pragma unroll
-                        for (int i = 0; i < DK / 64; ++i) {
-                            prefetch_l2_tile_3d(&mp.k, 64 * i, t1, bk);
-                            if (REV) prefetch_l2_tile_3d(&mp.q, 64 * i, t1, bk);
-                        }
-                        prefetch_l2_tile_3d(&mp.th, 0, 0, a1);
-                        prefetch_l2_tile_3d(&mp.tl, 0, 0, a1);
-                        if (REV) {
-                            prefetch_l2_tile_3d(&mp.ph, 0, 0, a1);
-                            prefetch_l2_tile_3d(&mp.pl, 0, 0, a1);
-                        }
-                    }
-                }
+                __syncwarp();
             }
             for (int m = max(0, issued - NST); m < issued; ++m) wait(&full[m % NST], (m / NST) & 1, abort_flag, status, ERR_TMA);
+        } else if (warp == 2) {
+            // L2 prefetch, two chunks ahead of the loads
+            for (int m = 0; m + NST < n; ++m) {
+                if (__any_sync(~0u, *abort_flag)) break;
+                if (m >= NST) wait(&empty[m % NST], ((m / NST) - 1) & 1, abort_flag, status, ERR_TMA);
+                __syncwarp();
+                const int c1 = chunk(m + NST), t1 = c1 * C, a1 = bh * n + c1;
+                if (elect_one()) {
+                    prefetch_l2_tile_4d(&mp.v, 0, t1, dv0 / 64, bh);
+                    if (blockIdx.x == 0) {
+                        prefetch_l2_tile_3d(&mp.t, 0, 0, a1);
+                        prefetch_l2_tile_4d(&mp.k, 0, t1, 0, bk);
+                        if (REV) prefetch_l2_tile_4d(&mp.q, 0, t1, 0, bk);
+                        if (REV) prefetch_l2_tile_3d(&mp.p, 0, 0, a1);
+                    }
+                }
+                __syncwarp();
+            }
         } else if (warp == 1) {
             const uint32_t id64 = idesc_bf16(128, 64, false, false), id64n = idesc_bf16(128, 64, false, true);
             const uint32_t idS = idesc_bf16(128, DK, false, true);
@@ -159,10 +156,10 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
                 const uint64_t dQn = sdesc(sb + L::Q_OFF, SLAB, 1024, kSwizzle128);
                 const uint64_t dV = sdesc(sb + L::V_OFF, SLAB, 1024, kSwizzle128);    // dv along M
                 // T: forward as U^T = . T^T (rows along N, K-major), reverse as . T (columns along N)
-                const uint64_t dTh = sdesc(sb + L::TH_OFF, REV ? SLAB : 16, 1024, kSwizzle128);
-                const uint64_t dTl = sdesc(sb + L::TL_OFF, REV ? SLAB : 16, 1024, kSwizzle128);
-                const uint64_t dPh = sdesc(sb + L::PH_OFF, SLAB, 1024, kSwizzle128);
-                const uint64_t dPl = sdesc(sb + L::PL_OFF, SLAB, 1024, kSwizzle128);
+                const uint64_t dTh = sdesc(sb + L::T_OFF, REV ? SLAB : 16, 1024, kSwizzle128);
+                const uint64_t dTl = sdesc(sb + L::T_OFF + SLAB, REV ? SLAB : 16, 1024, kSwizzle128);
+                const uint64_t dPh = sdesc(sb + L::P_OFF, SLAB, 1024, kSwizzle128);
+                const uint64_t dPl = sdesc(sb + L::P_OFF + SLAB, SLAB, 1024, kSwizzle128);
                 constexpr uint32_t step = (REV ? 2048 : 32) >> 4;   // 16 tokens of T's contraction
                 wait(&full[st], (m / NST) & 1, abort_flag, status, ERR_MMA);
                 if (m > 0) wait(x_free, (m - 1) & 1, abort_flag, status, ERR_MMA);
@@ -495,15 +492,14 @@ cudaError_t launch_delta_sweep(const DeltaSweep& a, int* status, cudaStream_t s)
     const uint64_t bk = (uint64_t)a.B * a.Hk, bh = (uint64_t)a.B * a.H, nc = bh * a.nch;
     const auto w128 = CU_TENSOR_MAP_SWIZZLE_128B, w0 = CU_TENSOR_MAP_SWIZZLE_NONE;
     Maps m;
-    bool ok = map_rows(&m.k, a.k, a.dk, a.T, bk) && map_rows(&m.v, a.v, a.dv, a.T, bh) &&
-              map_rows(&m.th, a.t_hi, C, C, nc) && map_rows(&m.tl, a.t_lo, C, C, nc) &&
+    bool ok = map_slabs(&m.k, a.k, a.dk, a.T, bk, a.dk / 64) && map_slabs(&m.v, a.v, a.dv, a.T, bh, 2) &&
+              map_pair(&m.t, a.t, nc) &&
               map_box(&m.sh, a.s_hi, a.dk, a.dv, nc, 128, w128) && map_box(&m.sl, a.s_lo, a.dk, a.dv, nc, 128, w128);
     if (a.reverse)
-        ok = ok && map_rows(&m.q, a.q, a.dk, a.T, bk) && map_rows(&m.ph, a.p_hi, C, C, nc) &&
-             map_rows(&m.pl, a.p_lo, C, C, nc) && map_box(&m.xh, a.x_hi, a.dv, a.T, bh, C, w0) &&
+        ok = ok && map_slabs(&m.q, a.q, a.dk, a.T, bk, a.dk / 64) && map_pair(&m.p, a.p, nc) && map_box(&m.xh, a.x_hi, a.dv, a.T, bh, C, w0) &&
              map_box(&m.xl, a.x_lo, a.dv, a.T, bh, C, w0);
     else {
-        m.q = m.ph = m.pl = m.k;   // not read
+        m.q = m.p = m.k;   // not read
         ok = ok && map_box(&m.xh, a.u_hi, C, a.dv, nc, 128, w128) && map_box(&m.xl, a.u_lo, C, a.dv, nc, 128, w128);
     }
     if (!ok) return cudaErrorInvalidValue;

@@ -98,5 +98,20 @@ inline bool map_rows(CUtensorMap* m, const void* base, uint64_t cols, uint64_t r
     return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The same rows of `slabs` 64-column slabs in one box: each slab's 64 rows after the other's.
+inline bool map_slabs(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t batch, uint32_t slabs)
+{
+    const uint64_t dims[4] = {64, rows, cols / 64, batch}, str[3] = {cols * 2, 128, cols * rows * 2};
+    const uint32_t box[4] = {64, C, slabs, 1};
+    return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// The prep's 64 x 64 matrices, both parts in one box of 128 rows.
+inline bool map_pair(CUtensorMap* m, const void* base, uint64_t chunks)
+{
+    const uint64_t dims[3] = {C, 2 * C, chunks}, str[2] = {C * 2, 2 * C * C * 2};
+    const uint32_t box[3] = {C, 2 * C, 1};
+    return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 }  // namespace delta
 }  // namespace gla

@@ -56,14 +56,14 @@ cudaError_t launch_delta_bwd_sum(const DeltaBwdSum& a, cudaStream_t s);
 // The chunk form (bf16, dk in {64, 128}, dv a multiple of 64), 64-token chunks on tcgen05.
 // Prep (gla_delta_prep.cu), chunk by chunk in parallel: with G the running sum of log_g in the
 // chunk, A[i][j] = beta_i (k_i . k_j) exp(G_i - G_j) for j < i, it writes
-//   t_hi, t_lo [BH][nch][64][64] bf16: (I + A)^-1 diag(beta) in two parts (about 17 bits),
-//   p_hi, p_lo                       : scale (q_i . k_j) exp(G_i - G_j) for j <= i, else 0,
+//   t [BH][nch][2][64][64] bf16      : (I + A)^-1 diag(beta) in two parts (17 bits),
+//   p, the same                      : scale (q_i . k_j) exp(G_i - G_j) for j <= i, else 0,
 //   gates [BH][nch][4][64] fp32      : beta, exp(G), exp(G_end - G), -exp(G); with grads
 //                                      [BH][nch][8][64]: also exp(G - G_mid), exp(G_mid - G) and G
 //                                      in two floats.
 struct DeltaPrep {
     const void* q; const void* k; const float* log_g; const void* beta;
-    void* t_hi; void* t_lo; void* p_hi; void* p_lo; float* gates;
+    void* t; void* p; float* gates;
     int B, H, Hk, T, dk, nch;
     float scale;
     bool grads;         // for the backward
@@ -75,7 +75,7 @@ cudaError_t launch_delta_prep(const DeltaPrep& a, int* status, cudaStream_t s);
 // memory, one CTA per head and 128 columns of dv.
 struct DeltaChain {
     const void* q; const void* k; const void* v;
-    const void* t_hi; const void* t_lo; const void* p_hi; const void* p_lo; const float* gates;
+    const void* t; const void* p; const float* gates;
     const float* S0; void* O; float* ST;
     int B, H, Hk, T, dk, dv, nch;
     float scale;
@@ -90,7 +90,7 @@ cudaError_t launch_delta_chain(const DeltaChain& a, int* status, cudaStream_t s)
 //   s_hi, s_lo [BH][nch][dv][dk];  u_hi, u_lo [BH][nch][dv][64];  x_hi, x_lo [BH][T][dv]
 struct DeltaSweep {
     const void* q; const void* k; const void* v;      // v: V, or dO in reverse
-    const void* t_hi; const void* t_lo; const void* p_hi; const void* p_lo; const float* gates;
+    const void* t; const void* p; const float* gates;
     const float* S_in; float* S_out;
     void* s_hi; void* s_lo; void* u_hi; void* u_lo; void* x_hi; void* x_lo;
     int B, H, Hk, T, dk, dv, nch;

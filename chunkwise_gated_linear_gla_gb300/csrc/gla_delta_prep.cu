@@ -231,9 +231,8 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
             for (int j = 0; j < 32; j += 4)
                 *reinterpret_cast<float4*>(A + i * LD + c0 + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
         } else {
-            const long long at = ((bh * a.nch + c) * C + i) * C + c0;
-            uint4* ph = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.p_hi) + at);
-            uint4* pl = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.p_lo) + at);
+            uint4* ph = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.p) + ((bh * a.nch + c) * 2 * C + i) * C + c0);
+            uint4* pl = ph + C * C / 8;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t h8[4], l8[4];
@@ -318,9 +317,8 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
     {
         // T diag(beta) in two parts: a quarter of a row a thread, zero above the diagonal
         const int i = tid >> 2, c0 = (tid & 3) * 16;
-        const long long at = ((bh * a.nch + c) * C + i) * C + c0;
-        uint4* th = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.t_hi) + at);
-        uint4* tl = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.t_lo) + at);
+        uint4* th = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.t) + ((bh * a.nch + c) * 2 * C + i) * C + c0);
+        uint4* tl = th + C * C / 8;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint32_t h8[4], l8[4];
