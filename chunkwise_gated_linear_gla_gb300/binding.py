@@ -74,7 +74,7 @@ class gla_delta_params(ctypes.Structure):
         ("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("T", ctypes.c_int),
         ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("scale", ctypes.c_float),
         ("dtype", ctypes.c_int), ("path", ctypes.c_int),
-        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("force_segments", ctypes.c_int),
     ]
 
 
@@ -625,7 +625,7 @@ def _delta_shapes(q, k, v, log_g, beta, S0):
 
 
 def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, path=GLA_PATH_AUTO, stream=None,
-                  O=None, ST=None):
+                  O=None, ST=None, force_segments=0):
     """The gated delta rule's forward pass (gla_delta_fwd), outputs and workspace from torch.
 
     q, k [B,Hk,T,dk], v [B,H,T,dv], beta [B,H,T] (bf16 or fp32, one type); log_g fp32 [B,H,T] or
@@ -648,8 +648,8 @@ def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, pa
     if ST is None and want_state:
         ST = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
     p = gla_delta_params(_ptr(q), _ptr(k), _ptr(v), _ptr(log_g), _ptr(beta), _ptr(S0), _ptr(O), _ptr(ST),
-                         B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path)
-    n = lib.gla_delta_fwd_workspace_size(ctypes.byref(p))
+                         B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path, None, 0, force_segments)
+    n = 0 if T < 128 else _here_size(lib.gla_delta_fwd_workspace_size, p, dev)   # (two chunks at least: none below)
     ws = None
     if n:
         ws = torch.empty(n, dtype=torch.uint8, device=dev)

@@ -44,29 +44,52 @@ bool chunk_shape_ok(int B, int H, int T, int dk, int dv, int dtype)
 
 struct DeltaPlan {
     int path = GLA_PATH_SIMT;
-    int nch = 0;
-    size_t off_t = 0, off_p = 0, off_g = 0;
+    int nch = 0, cps = 0, nseg = 1;
+    size_t off_pair = 0, off_in = 0;
     size_t ws = 0;
 };
+
+// Segments of the sequence. The pass is serial over the chunks of a head's 128 dv columns, so few
+// heads leave SMs idle. Cut into n segments the pass takes two walks of nch / n chunks (the first, of
+// all segments but the last, has one more tile per head for the transitions) and a scan of about one
+// chunk's time per segment; n is as many as one wave of the first walk holds.
+int choose_segments(int units, int trans, int nch, int sms)
+{
+    int n = 1 + sms / (units + trans);
+    if (n > nch / 4) n = nch / 4;
+    if (n < 3) return 1;
+    return 2 * ((nch + n - 1) / n) + n + 6 < nch ? n : 1;
+}
 
 gla_status plan_fwd(const gla_delta_params* p, DeltaPlan& pl)
 {
     if (!p) return GLA_ERR_INVALID_ARG;
     gla_status st = check_sizes(p->B, p->H, p->Hk, p->T, p->dk, p->dv, p->scale, p->dtype, p->path);
     if (st != GLA_OK) return st;
+    if (p->force_segments < 0) return GLA_ERR_INVALID_ARG;
     const bool ok = chunk_shape_ok(p->B, p->H, p->T, p->dk, p->dv, p->dtype);
     if (p->path == GLA_PATH_TENSOR && !ok) return GLA_ERR_UNSUPPORTED;
     if (p->T == 0 || !ok || p->path == GLA_PATH_SIMT) return GLA_OK;
     if (p->path == GLA_PATH_AUTO && p->T < kDeltaChunkMinT) return GLA_OK;
     pl.path = GLA_PATH_TENSOR;
     pl.nch = (p->T + kChunk - 1) / kChunk;
-    const size_t nc = (size_t)p->B * p->H * pl.nch;
-    size_t off = 0;
-    auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
-    pl.off_t = take(nc * 2 * kChunk * kChunk * 2);
-    pl.off_p = take(nc * 2 * kChunk * kChunk * 2);
-    pl.off_g = take(nc * 4 * kChunk * 4);
-    pl.ws = off;
+    int sms = 0;
+    if (device_ready(&sms) != GLA_OK) sms = 152;
+    const int BH = p->B * p->H;
+    int n = p->force_segments > 0 ? p->force_segments
+                                  : choose_segments(BH * ((p->dv + kDvTile - 1) / kDvTile), BH, pl.nch, sms);
+    if (n > pl.nch) n = pl.nch;
+    if (n > 65535) n = 65535;
+    pl.cps = (pl.nch + n - 1) / n;
+    pl.nseg = (pl.nch + pl.cps - 1) / pl.cps;
+    if (pl.nseg > 1) {
+        const size_t st4 = (size_t)p->dk * p->dv * 4, m4 = (size_t)p->dk * p->dk * 4;
+        size_t off = 0;
+        auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
+        pl.off_pair = take((size_t)BH * (pl.nseg - 1) * (st4 + m4));
+        pl.off_in = take((size_t)BH * pl.nseg * st4);
+        pl.ws = off;
+    }
     return GLA_OK;
 }
 
@@ -192,7 +215,7 @@ gla_status bwd_chunks(const gla_delta_bwd_params* p, const DeltaBwdPlan& pl, int
     a.q = p->q; a.k = p->k; a.log_g = p->log_g; a.beta = p->beta;
     a.t = ws + pl.off_t; a.p = ws + pl.off_p; a.gates = gates;
     a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.nch = pl.nch; a.scale = p->scale;
-    a.grads = true; a.beta_floor = 0x1p-40f;
+    a.beta_floor = 0x1p-40f;
     cudaError_t e = launch_delta_prep(a, status, stream);
     DeltaSweep w;
     w.q = p->q; w.k = p->k; w.v = p->v;
@@ -262,21 +285,15 @@ gla_status gla_delta_fwd(const gla_delta_params* p, cudaStream_t stream)
     } else if (pl.path == GLA_PATH_TENSOR) {
         uint8_t* ws = static_cast<uint8_t*>(p->workspace);
         int* status = device_status_ptr();
-        DeltaPrep a;
-        a.q = p->q; a.k = p->k; a.log_g = p->log_g; a.beta = p->beta;
-        a.t = ws + pl.off_t; a.p = ws + pl.off_p;
-        a.gates = reinterpret_cast<float*>(ws + pl.off_g);
-        a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.nch = pl.nch; a.scale = p->scale;
-        a.grads = false; a.beta_floor = 0.f;
-        e = launch_delta_prep(a, status, stream);
-        if (e == cudaSuccess) {
-            DeltaChain w;
-            w.q = p->q; w.k = p->k; w.v = p->v; w.t = a.t; w.p = a.p; w.gates = a.gates;
-            w.S0 = p->S0; w.O = p->O; w.ST = p->ST;
-            w.B = p->B; w.H = p->H; w.Hk = p->Hk; w.T = p->T; w.dk = p->dk; w.dv = p->dv; w.nch = pl.nch;
-            w.scale = p->scale;
-            e = launch_delta_chain(w, status, stream);
-        }
+        if (!status) return GLA_ERR_CUDA;
+        DeltaChunks a;
+        a.q = p->q; a.k = p->k; a.v = p->v; a.log_g = p->log_g; a.beta = p->beta;
+        a.S0 = p->S0; a.O = p->O; a.ST = p->ST;
+        a.pair = pl.ws ? reinterpret_cast<float*>(ws + pl.off_pair) : nullptr;
+        a.seg_in = pl.ws ? reinterpret_cast<float*>(ws + pl.off_in) : nullptr;
+        a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.dv = p->dv;
+        a.nch = pl.nch; a.cps = pl.cps; a.nseg = pl.nseg; a.scale = p->scale;
+        e = launch_delta_chunks(a, status, stream);
     } else {
         e = launch_delta_step(step_args(p, sms), stream);
     }

@@ -69,6 +69,16 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
     split2(make_float2(x0, x1), hi, lo);
 }
 
+// A sum of floats kept with its rounding errors (Knuth's two-sum, renormalised).
+struct Two { float h, l; };
+__device__ __forceinline__ Two two_add(Two a, Two b)
+{
+    const float s = __fadd_rn(a.h, b.h), t = __fadd_rn(s, -a.h);
+    const float e = __fadd_rn(__fadd_rn(a.h, -__fadd_rn(s, -t)), __fadd_rn(b.h, -t)) + (a.l + b.l);
+    const float h = __fadd_rn(s, e);
+    return Two{h, __fadd_rn(e, -__fadd_rn(h, -s))};
+}
+
 // Shared-memory accesses by 32-bit address. A pointer into the aligned dynamic buffer is generic
 // to the compiler, and a generic load may not pass a generic store; these stay in order among
 // the volatile statements around them (waits, fences) and overlap freely otherwise.

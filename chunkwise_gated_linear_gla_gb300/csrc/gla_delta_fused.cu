@@ -1,0 +1,844 @@
+// gla_delta_fused: the whole chunk form of the gated delta rule in one kernel. Per 64-token chunk,
+// with G the running sum of log_g in the chunk, e = exp(G), l = exp(G_end - G), D_ij = exp(G_i - G_j):
+//
+//   L_ij = (k_i . k_j) D_ij (j < i),   T = (1 / beta + L)^-1,   P_ij = scale (q_i . k_j) D_ij (j <= i),
+//   R = -e K S,   U = T V + T R,   O = scale e (Q S) + P U,   S <- exp(G_end) S + K^T (l U).
+//
+// (U solves u_i = beta_i (v_i - e_i k_i S - sum_{j<i} L_ij u_j).) A CTA owns 128 columns of dv of one
+// head (and of one segment of the sequence) and walks the chunks; T and P never leave the SM.
+//
+// The chain (four warpgroups' warps 4-11, products by warp 1). Everything is transposed, dv along the
+// 128 tensor-memory lanes: the state, R and U are A operands read from tensor memory and a thread owns
+// one column of dv, so nothing of the chain passes through shared memory; the state itself stays in
+// fp32 registers. Every step comes in two halves (of the keys, or of the tokens), so that the
+// products of one run beside the register step of the other. Every operand that is not an input (S,
+// R, U, T, P) goes into the products in two bf16 parts, hi + lo, good to 2^-17; K, V and Q are exact:
+// two products for K S, K^T U, Q S and T V, three for T R and P U. So the fp32 state is good to 3e-6
+// and O to its last rounding (with one part of P and U it was not: where keys repeat, P U is a sum of
+// cancelling terms, 7.5e-3 off when all keys are the same).
+//
+// The prep (warps 16-23) runs one chunk ahead on the same SM: one product of 128 rows, K stacked on
+// Q, against K^T; the masked L and P; then T in place of L: 16-row diagonal blocks by forward
+// substitution in fp32, and twice the block rule, the inverse of [[X^-1, 0], [C, Y^-1]] has -Y C X
+// below, on mma.sync fragments in two parts (16 x 16 and 32 x 32 pieces, too small for a tcgen05
+// tile). G is summed in pairs of floats (48 bits), so a steep gate costs no precision; D is a product
+// of two factors around the chunk's middle while both stay within e^60, else one exponential per pair.
+//
+// Warps: 0 TMA, 1 products, 4-11 chain, 12-15 drain of O, 16-23 prep. Reads K, Q, V once
+// and writes O once; bound by the chain's latency, with the tensor pipe busy 2800 cycles a chunk.
+#include "gla_delta_dev.cuh"
+#include "gla_delta_internal.h"
+
+namespace gla {
+namespace {
+
+using namespace sm100;
+using namespace delta;
+
+constexpr int NT = 768;
+constexpr int NKQ = 3;            // K and Q stages: chunk m's, the next one's (read by the prep), one in flight
+constexpr int NV = 2;             // V stages, T and P buffers
+constexpr int NG = 4;             // gate slots (the drain is the last reader)
+constexpr int PF = 4;             // chunks between a tile's prefetch into L2 and its load
+constexpr int DVT = 128;          // dv columns per CTA
+constexpr int LDD = 20;           // row stride of the fp32 diagonal blocks
+constexpr float kRange = 60.f;    // |G - G_mid| up to which the two-factor form of D is used
+
+enum { ERR_TMA = 0x641, ERR_MMA = 0x642, ERR_EPI = 0x643, ERR_DRAIN = 0x644, ERR_PREP = 0x645 };
+
+__device__ __forceinline__ float2 f2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+
+template <int DK>
+struct FL {
+    static constexpr int KB = (DK / 64) * SLAB;
+    static constexpr int KQ_OFF = 0;                       // [NKQ][K, Q]
+    static constexpr int V_OFF = NKQ * 2 * KB;             // [NV]
+    static constexpr int TP_OFF = V_OFF + NV * 2 * SLAB;   // [NV][T, T_lo, P, P_lo]
+    static constexpr int O_OFF = TP_OFF + NV * 4 * SLAB;   // [2 halves of dv][64 tokens][64] bf16
+    static constexpr int GB = 8 * C * 4;                   // beta, e, l, -e, the factors of D, G in two floats
+    static constexpr int G_OFF = O_OFF + 2 * SLAB;
+    static constexpr int D_OFF = G_OFF + NG * GB;          // diagonal blocks of L beta, fp32
+    static constexpr int BAR_OFF = D_OFF + 4 * 16 * LDD * 4;
+    static constexpr int SMEM = BAR_OFF + 256 + 1024;
+    // tensor memory columns
+    static constexpr int tD = 0;                           // the state's increment, [dv][DK]
+    static constexpr int tSh = DK, tSl = tSh + DK / 2;     // the state's parts
+    static constexpr int tX = 2 * DK;                      // U; then its parts
+    static constexpr int tRh = tX + 64, tRl = tRh + 32;    // R's parts, then l U's
+    static constexpr int tOq = tRl + 32, tOp = tOq + 64;   // Q S, P U
+    // K S and the prep's product: at dk = 128 over the increment's two halves, which are read
+    // before the one is formed and not formed again before the other is read
+    static constexpr int tKs = DK == 128 ? tD : tOp + 64, tG = DK == 128 ? tD + 64 : tOp + 128;
+    static_assert(tG + 64 <= 512 && tOp + 64 <= 512 && tKs + 64 <= 512, "tensor memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct FusedArgs {
+    const float* log_g; const __nv_bfloat16* beta;
+    const float* S_in; float* S_out;      // + bh * s_bh + segment * s_seg
+    long long in_bh, in_seg, out_bh, out_seg;
+    int H, Hk, T, dv, nch, cps, nseg, tiles;
+    float scale;
+    int* status;
+};
+struct FusedMaps { CUtensorMap k, q, v, o; };
+
+// ---- mma.sync on 16-row pieces of a swizzled 64 x 64 bf16 matrix (128-byte rows)
+__device__ __forceinline__ uint32_t sw(uint32_t base, int row, int col8) { return base + row * 128 + ((col8 ^ (row & 7)) << 4); }
+__device__ __forceinline__ void ldm_a(uint32_t base, int r0, int k0, uint32_t (&a)[4])
+{
+    const int lane = threadIdx.x & 31;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(sw(base, r0 + (lane & 15), k0 / 8 + (lane >> 4))) : "memory");
+}
+__device__ __forceinline__ void ldm_b(uint32_t base, int k0, int n0, uint32_t (&b)[2])
+{
+    const int lane = threadIdx.x & 31;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+                 : "=r"(b[0]), "=r"(b[1]) : "r"(sw(base, k0 + (lane & 15), n0 / 8)) : "memory");
+}
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// X (16 x 8 at column n0 of the block) = -(Y C) Z for K-wide pieces: Y at (yr, yc), C at (yc, zc) and Z at
+// (zc, zc) of the matrix whose parts start at hi and hi + SLAB. Columns n0 .. n0 + 7 of the product.
+template <int K>
+__device__ __forceinline__ void block_rule(uint32_t hi, int yr, int yc, int zc, int n0, float (&x)[4])
+{
+    float w[K / 8][4];
+#pragma unroll
+    for (int i = 0; i < K / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[i][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; k += 16) {
+        uint32_t ah[4], al[4];
+        ldm_a(hi, yr, yc + k, ah);
+        ldm_a(hi + SLAB, yr, yc + k, al);
+#pragma unroll
+        for (int i = 0; i < K / 8; ++i) {
+            uint32_t bh[2], bl[2];
+            ldm_b(hi, yc + k, zc + 8 * i, bh);
+            ldm_b(hi + SLAB, yc + k, zc + 8 * i, bl);
+            mma16(w[i], ah, bh);
+            mma16(w[i], al, bh);
+            mma16(w[i], ah, bl);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; k += 16) {
+        uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            split2(-w[k / 8 + e][0], -w[k / 8 + e][1], ah[2 * e], al[2 * e]);
+            split2(-w[k / 8 + e][2], -w[k / 8 + e][3], ah[2 * e + 1], al[2 * e + 1]);
+        }
+        ldm_b(hi, zc + k, zc + n0, bh);
+        ldm_b(hi + SLAB, zc + k, zc + n0, bl);
+        mma16(x, ah, bh);
+        mma16(x, al, bh);
+        mma16(x, ah, bl);
+    }
+}
+// The 16 x 8 fragment to rows r0.., columns c0.. of both parts.
+__device__ __forceinline__ void put_fragment(uint32_t hi, int r0, int c0, const float (&x)[4])
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        uint32_t h, l;
+        split2(x[2 * e], x[2 * e + 1], h, l);
+        const uint32_t a = sw(hi, r0 + g + 8 * e, c0 / 8) + t * 4;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(h) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(a + SLAB), "r"(l) : "memory");
+    }
+}
+__device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// OUT: O is formed (and its loads, products and drain run). Without it the state alone, from zero, and
+// in the tiles after dv's the state that starts from the identity without V: the segment's transition.
+template <int DK, bool OUT>
+__global__ void __launch_bounds__(NT, 1)
+gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
+{
+    using L = FL<DK>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t s0 = smem_u32(sm);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR_OFF);
+    uint64_t* kq_full = bar;                // [NKQ]
+    uint64_t* kq_empty = bar + NKQ;         // [NKQ]
+    uint64_t* v_full = kq_empty + NKQ;      // [NV]
+    uint64_t* v_empty = v_full + NV;        // [NV]
+    uint64_t* s_ready = v_empty + NV;       // [2] state parts written (8 warps)
+    uint64_t* r_ready = s_ready + 2;        // [2] R's parts written (8 warps)
+    uint64_t* u_ready = s_ready + 4;        // [2] l U's parts written (8 warps)
+    uint64_t* p_ready = s_ready + 6;        // U's own parts written, for P U (8 warps)
+    uint64_t* g_read = s_ready + 7;         // the prep's product read (8 warps)
+    uint64_t* t_ready = s_ready + 8;        // [2] a chunk's T, P and gates written (8 warps), even and odd chunks
+    uint64_t* ks_full = s_ready + 10;       // K S formed
+    uint64_t* u_full = s_ready + 11;        // U formed
+    uint64_t* d_full = s_ready + 12;        // [2] the increment formed
+    uint64_t* o_full = s_ready + 14;        // Q S and P U formed
+    uint64_t* g_full = s_ready + 15;        // the prep's product formed
+    uint64_t* fin = s_ready + 16;
+    uint64_t* o_empty = s_ready + 17;       // O read out (4 warps)
+    uint32_t* holder = reinterpret_cast<uint32_t*>(s_ready + 18);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(s_ready + 19);
+
+    const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32, wg = warp / 4;
+    const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+    const int bk = b * a.Hk + h / (a.H / a.Hk);
+    const int seg = blockIdx.z, first = seg * a.cps, n = min(a.nch - first, a.cps);
+    const bool ident = !OUT && (int)blockIdx.x >= a.tiles;
+    const int dv0 = ident ? 0 : blockIdx.x * DVT;
+    const bool wide = dv0 + 64 < a.dv;      // the tile's second half is inside dv
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * NKQ + 2 * NV; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < 18; ++i) mbar_init(&s_ready[i], i < 10 ? 8 : i == 17 ? 4 : 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(holder, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *holder;
+    int* status = a.status;
+
+    if (wg == 0) {
+        regs_dec<40>();
+        if (warp == 0) {
+            // ------------------------------------------------------ TMA producer
+            int kq = 0, v = 0;
+            for (int m = 0; m < n; ++m) {
+                if (__any_sync(~0u, *abort_flag)) break;
+                const int t0 = (first + m) * C, st = m % NKQ;
+                if (m >= NKQ) wait(&kq_empty[st], ((m / NKQ) - 1) & 1, abort_flag, status, ERR_TMA);
+                __syncwarp();
+                if (elect_one()) {
+                    // K's and Q's slab of the same 64 keys side by side: 128 rows of one operand
+                    mbar_arrive_expect_tx(&kq_full[st], 2 * L::KB);
+                    uint8_t* sb = sm + L::KQ_OFF + st * 2 * L::KB;
+#pragma unroll
+                    for (int i = 0; i < DK / 64; ++i) {
+                        tma_load_3d(sb + 2 * i * SLAB, &mp.k, &kq_full[st], 64 * i, t0, bk);
+                        tma_load_3d(sb + (2 * i + 1) * SLAB, &mp.q, &kq_full[st], 64 * i, t0, bk);
+                    }
+                    if (m + PF < n) {
+                        // on their way into L2, PF chunks ahead
+                        const int t1 = t0 + PF * C;
+                        if (blockIdx.x == 0) {
+#pragma unroll
+                            for (int i = 0; i < DK / 64; ++i) {
+                                prefetch_l2_tile_3d(&mp.k, 64 * i, t1, bk);
+                                prefetch_l2_tile_3d(&mp.q, 64 * i, t1, bk);
+                            }
+                        }
+                        if (!ident) prefetch_l2_tile_4d(&mp.v, 0, t1, dv0 / 64, bh);
+                    }
+                }
+                __syncwarp();
+                ++kq;
+                if (ident) continue;
+                if (m >= NV) wait(&v_empty[m % NV], ((m / NV) - 1) & 1, abort_flag, status, ERR_TMA);
+                __syncwarp();
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&v_full[m % NV], 2 * SLAB);
+                    // (slabs past dv: zeros)
+                    tma_load_4d(sm + L::V_OFF + (m % NV) * 2 * SLAB, &mp.v, &v_full[m % NV], 0, t0, dv0 / 64, bh);
+                }
+                __syncwarp();
+                ++v;
+            }
+            for (int m = max(0, kq - NKQ); m < kq; ++m) wait(&kq_full[m % NKQ], (m / NKQ) & 1, abort_flag, status, ERR_TMA);
+            for (int m = max(0, v - NV); m < v; ++m) wait(&v_full[m % NV], (m / NV) & 1, abort_flag, status, ERR_TMA);
+        } else if (warp == 1) {
+            // ------------------------------------------------------ products
+            // The whole warp walks the loop and one elected lane issues, so that descriptors stay
+            // in uniform registers (issued from a divergent lane each product took 60 to 100
+            // cycles of moves, twice its time on the tensor cores).
+            const uint32_t id64 = idesc_bf16(128, 64, false, false), idS = idesc_bf16(128, DK, false, true);
+            const uint32_t idV = idesc_bf16(128, 64, true, false), idH = idesc_bf16(128, 64, false, true);
+            // chunk m's K on Q (128 rows) against K
+            auto gram = [&](int m) {
+                const int st = m % NKQ;
+                wait(&kq_full[st], (m / NKQ) & 1, abort_flag, status, ERR_MMA);
+                __syncwarp();
+                if (elect_one()) {
+                    const uint64_t d0 = sdesc(s0 + L::KQ_OFF + st * 2 * L::KB, 16, 1024, kSwizzle128);
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk) {
+                        const uint64_t d = d0 + (((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4);
+                        mma_ss(tm + L::tG, d, d, id64, kk > 0);
+                    }
+                    mma_commit(g_full);
+                }
+                __syncwarp();
+            };
+            if (n > 0) gram(0);
+            for (int m = 0; m < n; ++m) {
+                if (__any_sync(~0u, *abort_flag)) break;
+                const int st = m % NKQ, vt = m % NV;
+                const uint32_t sb = s0 + L::KQ_OFF + st * 2 * L::KB, tp = s0 + L::TP_OFF + vt * 4 * SLAB, ph = m & 1;
+                const uint64_t dK = sdesc(sb, 16, 1024, kSwizzle128), dQ = sdesc(sb + SLAB, 16, 1024, kSwizzle128);
+                const uint64_t dKn = sdesc(sb, 2 * SLAB, 1024, kSwizzle128);          // keys along N
+                const uint64_t dV = sdesc(s0 + L::V_OFF + vt * 2 * SLAB, SLAB, 1024, kSwizzle128);   // dv along M
+                const uint64_t dTh = sdesc(tp, 16, 1024, kSwizzle128), dTl = sdesc(tp + SLAB, 16, 1024, kSwizzle128);
+                const uint64_t dP = sdesc(tp + 2 * SLAB, 16, 1024, kSwizzle128), dPl = sdesc(tp + 3 * SLAB, 16, 1024, kSwizzle128);
+                // (K S)^T: A the state's parts, B = K (64 tokens by keys, K-major)
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    wait(&s_ready[part], ph, abort_flag, status, ERR_MMA);
+                    // (the first product's buffer: chunk 0's product has been read by then)
+                    if (part == 0 && m == 0) wait(g_read, 0, abort_flag, status, ERR_MMA);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = part * (DK / 32); kk < (part + 1) * (DK / 32); ++kk) {
+                            const uint64_t o = ((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4;
+                            mma_ts(tm + L::tKs, tm + L::tSh + kk * 8, dK + o, id64, kk > 0);
+                            mma_ts(tm + L::tKs, tm + L::tSl + kk * 8, dK + o, id64, 1);
+                        }
+                        if (part) mma_commit(ks_full);
+                    }
+                    __syncwarp();
+                }
+                // V^T T^T, both from shared memory, in the gap of R's register step
+                wait(&t_ready[m & 1], (m >> 1) & 1, abort_flag, status, ERR_MMA);
+                if (!ident) {
+                    wait(&v_full[vt], (m / NV) & 1, abort_flag, status, ERR_MMA);
+                    __syncwarp();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < C / 16; ++kk) {
+                            const uint64_t o = (kk * 32) >> 4, v = (kk * 2048) >> 4;
+                            mma_ss(tm + L::tX, dV + v, dTh + o, idV, kk > 0);
+                            mma_ss(tm + L::tX, dV + v, dTl + o, idV, 1);
+                        }
+                        mma_commit(&v_empty[vt]);
+                    }
+                    __syncwarp();
+                }
+                if (m + 1 < n) gram(m + 1);
+                // U^T += R^T T^T: B = T (rows i, columns j: K-major)
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    wait(&r_ready[part], ph, abort_flag, status, ERR_MMA);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 2 * part; kk < 2 * part + 2; ++kk) {
+                            const uint64_t o = (kk * 32) >> 4;
+                            mma_ts(tm + L::tX, tm + L::tRh + kk * 8, dTh + o, id64, !ident || kk > 0);
+                            mma_ts(tm + L::tX, tm + L::tRl + kk * 8, dTh + o, id64, 1);
+                            mma_ts(tm + L::tX, tm + L::tRh + kk * 8, dTl + o, id64, 1);
+                        }
+                        if (part) mma_commit(u_full);
+                    }
+                    __syncwarp();
+                }
+                if (OUT) {
+                    // (Q S)^T in the gap of U's register step
+                    if (m > 0) wait(o_empty, (m - 1) & 1, abort_flag, status, ERR_MMA);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < DK / 16; ++kk) {
+                            const uint64_t o = ((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4;
+                            mma_ts(tm + L::tOq, tm + L::tSh + kk * 8, dQ + o, id64, kk > 0);
+                            mma_ts(tm + L::tOq, tm + L::tSl + kk * 8, dQ + o, id64, 1);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (m + 1 < n) wait(g_read, (m + 1) & 1, abort_flag, status, ERR_MMA);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    wait(&u_ready[part], ph, abort_flag, status, ERR_MMA);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (elect_one()) {
+                        // the increment (l U)^T K: B = K with the keys along N (MN-major); the second
+                        // part's products one half of the keys after the other (dk = 128: a slab each)
+                        constexpr int NH = DK == 128 ? 2 : 1;
+#pragma unroll
+                        for (int nh = 0; nh < (part ? NH : 1); ++nh) {
+#pragma unroll
+                            for (int kk = 2 * part; kk < 2 * part + 2; ++kk) {
+                                const uint64_t o = (kk * 2048 + nh * 2 * SLAB) >> 4;
+                                const uint32_t id = part && NH == 2 ? idH : idS;
+                                mma_ts(tm + L::tD + nh * 64, tm + L::tRh + kk * 8, dKn + o, id, kk > 0);
+                                mma_ts(tm + L::tD + nh * 64, tm + L::tRl + kk * 8, dKn + o, id, 1);
+                            }
+                            if (part) mma_commit(&d_full[nh]);
+                        }
+                        if (part && NH == 1) mma_commit(&d_full[1]);
+                        if (part && !OUT) mma_commit(&kq_empty[st]);
+                    }
+                    __syncwarp();
+                }
+                if (OUT) {
+                    wait(p_ready, ph, abort_flag, status, ERR_MMA);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (elect_one()) {
+                        // (P U)^T: U's parts lie in X, eight columns each in the place of 16 tokens
+#pragma unroll
+                        for (int kk = 0; kk < C / 16; ++kk) {
+                            const uint32_t u = tm + L::tX + kk * 16;
+                            mma_ts(tm + L::tOp, u, dP + ((kk * 32) >> 4), id64, kk > 0);
+                            mma_ts(tm + L::tOp, u + 8, dP + ((kk * 32) >> 4), id64, 1);
+                            mma_ts(tm + L::tOp, u, dPl + ((kk * 32) >> 4), id64, 1);
+                        }
+                        mma_commit(o_full);
+                        mma_commit(&kq_empty[st]);
+                    }
+                    __syncwarp();
+                }
+            }
+            // no product may still run when the tensor memory is freed
+            if (elect_one()) mma_commit(fin);
+            __syncwarp();
+            mbar_wait(fin, 0, kTimeoutNs);
+        }
+    } else if (wg < 3) {
+        // ---------------------------------------------------------- the chain's register steps
+        // Group g owns, of part p, the keys p DK/2 + g DK/4 .. and the tokens 32 p + 16 g ..
+        regs_inc<128>();
+        constexpr int KP = DK / 4;                    // keys of one part
+        const int grp = wg - 1, d = (warp & 3) * 32 + lane;
+        const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
+        const int dvs = ident ? DK : a.dv;            // columns of the state's rows in memory
+        const bool in = dv0 + d < dvs;
+        const size_t sbase = (size_t)dv0 + d;
+        auto key = [&](int p) { return p * (DK / 2) + grp * KP; };
+        auto signal = [&](uint64_t* x) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x);
+        };
+        float2 s[2][KP / 2];
+        {
+            const float* S = a.S_in ? a.S_in + bh * a.in_bh + seg * a.in_seg : nullptr;
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int i = 0; i < KP / 2; ++i) {
+                    const int k = key(p) + 2 * i;
+                    if (!OUT) s[p][i] = make_float2(ident && k == d ? 1.f : 0.f, ident && k + 1 == d ? 1.f : 0.f);
+                    else s[p][i] = S && in ? make_float2(S[sbase + (size_t)k * a.dv], S[sbase + (size_t)(k + 1) * a.dv])
+                                           : make_float2(0.f, 0.f);
+                }
+        }
+        auto put_state = [&](int p) {
+            uint32_t hi[KP / 2], lo[KP / 2];
+#pragma unroll
+            for (int i = 0; i < KP / 2; ++i) split2(s[p][i], hi[i], lo[i]);
+#pragma unroll
+            for (int i = 0; i < KP / 2; i += 8) {
+                tmem_st8(tm + lb + L::tSh + key(p) / 2 + i, hi + i);
+                tmem_st8(tm + lb + L::tSl + key(p) / 2 + i, lo + i);
+            }
+            signal(&s_ready[p]);
+        };
+        if (n > 0) {
+            put_state(0);
+            put_state(1);
+        }
+        for (int m = 0; m < n; ++m) {
+            const uint32_t ph = m & 1;
+            const uint32_t gt = s0 + L::G_OFF + (m % NG) * L::GB;
+            wait(&t_ready[m & 1], (m >> 1) & 1, abort_flag, status, ERR_EPI);
+            const float gend = lds1(gt + (2 * C - 1) * 4);
+            // 16 tokens of part p times their gate (a row of the gates), in two parts, to R's place
+            auto put_tokens = [&](int p, const uint32_t (&x)[16], int row) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 e = lds4(gt + (row * C + p * 32 + grp * 16 + 4 * i) * 4);
+                    split2(mul2(make_float2(e.x, e.y), f2(x[4 * i], x[4 * i + 1])), hi[2 * i], lo[2 * i]);
+                    split2(mul2(make_float2(e.z, e.w), f2(x[4 * i + 2], x[4 * i + 3])), hi[2 * i + 1], lo[2 * i + 1]);
+                }
+                tmem_st8(tm + lb + L::tRh + p * 16 + grp * 8, hi);
+                tmem_st8(tm + lb + L::tRl + p * 16 + grp * 8, lo);
+            };
+            uint32_t x0[16], x1[16];
+            wait(ks_full, ph, abort_flag, status, ERR_EPI);
+            tc_fence_after();
+            tmem_ld16(tm + lb + L::tKs + grp * 16, x0);
+            tmem_ld16(tm + lb + L::tKs + 32 + grp * 16, x1);
+            tmem_wait_ld();
+            put_tokens(0, x0, 3);         // -e
+            signal(&r_ready[0]);
+            put_tokens(1, x1, 3);
+            signal(&r_ready[1]);
+            wait(u_full, ph, abort_flag, status, ERR_EPI);
+            tc_fence_after();
+            tmem_ld16(tm + lb + L::tX + grp * 16, x0);
+            tmem_ld16(tm + lb + L::tX + 32 + grp * 16, x1);
+            tmem_wait_ld();
+            put_tokens(0, x0, 2);         // l
+            signal(&u_ready[0]);
+            put_tokens(1, x1, 2);
+            signal(&u_ready[1]);
+            if (OUT) {
+                // U's own parts, off the chain: the increment's products run meanwhile
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        split2(p ? f2(x1[2 * i], x1[2 * i + 1]) : f2(x0[2 * i], x0[2 * i + 1]), hi[i], lo[i]);
+                    tmem_st8(tm + lb + L::tX + p * 32 + grp * 16, hi);
+                    tmem_st8(tm + lb + L::tX + p * 32 + grp * 16 + 8, lo);
+                }
+                signal(p_ready);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                wait(&d_full[p], ph, abort_flag, status, ERR_EPI);
+                tc_fence_after();
+                uint32_t x[KP];
+#pragma unroll
+                for (int c = 0; c < KP; c += 16)
+                    tmem_ld16(tm + lb + L::tD + key(p) + c, *reinterpret_cast<uint32_t(*)[16]>(x + c));
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < KP / 2; ++i)
+                    s[p][i] = fma2(make_float2(gend, gend), s[p][i], f2(x[2 * i], x[2 * i + 1]));
+                if (m + 1 < n) put_state(p);
+            }
+        }
+        // the state after the last segment; without O every segment's, a transition after the states
+        if (a.S_out && in && (!OUT || seg == a.nseg - 1)) {
+            float* S = a.S_out + bh * a.out_bh + seg * a.out_seg + (ident ? (size_t)DK * a.dv : 0);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int i = 0; i < KP / 2; ++i) {
+                    float* o = S + sbase + (size_t)(key(p) + 2 * i) * dvs;
+                    o[0] = s[p][i].x;
+                    o[dvs] = s[p][i].y;
+                }
+        }
+    } else if (wg == 3) {
+        // ---------------------------------------------------------- drain of O
+        regs_dec<56>();
+        if (OUT) {
+            const int d = (warp & 3) * 32 + lane;
+            const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t ob = s0 + L::O_OFF + (d >> 6) * SLAB + (d & 63) * 2;
+            const bool lead = threadIdx.x == 384;
+            for (int m = 0; m < n; ++m) {
+                const uint32_t gt = s0 + L::G_OFF + (m % NG) * L::GB + C * 4;   // e
+                wait(o_full, m & 1, abort_flag, status, ERR_DRAIN);
+                tc_fence_after();
+                // the tile's last store must have read it
+                if (lead) bulk_wait_read0();
+                named_bar_sync(1, 128);
+#pragma unroll
+                for (int c = 0; c < 64; c += 16) {
+                    uint32_t x[16], y[16];
+                    tmem_ld16(tm + lb + L::tOq + c, x);
+                    tmem_ld16(tm + lb + L::tOp + c, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 g = lds4(gt + (c + i) * 4);
+                        sts_bf16(ob + (c + i) * 128, fmaf(a.scale * g.x, __uint_as_float(x[i]), __uint_as_float(y[i])));
+                        sts_bf16(ob + (c + i + 1) * 128, fmaf(a.scale * g.y, __uint_as_float(x[i + 1]), __uint_as_float(y[i + 1])));
+                        sts_bf16(ob + (c + i + 2) * 128, fmaf(a.scale * g.z, __uint_as_float(x[i + 2]), __uint_as_float(y[i + 2])));
+                        sts_bf16(ob + (c + i + 3) * 128, fmaf(a.scale * g.w, __uint_as_float(x[i + 3]), __uint_as_float(y[i + 3])));
+                    }
+                }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_empty);
+                named_bar_sync(1, 128);
+                if (lead) {
+                    tma_store_3d(&mp.o, sm + L::O_OFF, dv0, (first + m) * C, bh);
+                    if (wide) tma_store_3d(&mp.o, sm + L::O_OFF + SLAB, dv0 + 64, (first + m) * C, bh);
+                    bulk_commit();
+                }
+            }
+            if (lead) bulk_wait0();
+        }
+    } else {
+        // ---------------------------------------------------------- prep, one chunk ahead
+        regs_dec<64>();
+        const int pw = warp - 16, quarter = warp & 3, c0 = (pw >> 2) * 32;
+        const int i = (quarter & 1) * 32 + lane;      // row of the chunk
+        const bool isP = quarter >= 2;
+        float* diag = reinterpret_cast<float*>(sm + L::D_OFF);
+        const float* lg = a.log_g ? a.log_g + (size_t)bh * a.T : nullptr;
+        const __nv_bfloat16* bp = a.beta + (size_t)bh * a.T;
+        float x0 = 0.f, x1 = 0.f, b0 = 0.f, b1 = 0.f;   // warp 16: the gates of two tokens of the next chunk
+        auto fetch = [&](int m) {
+            const int t = (first + m) * C + 2 * lane;
+            const bool p = t < a.T, q = t + 1 < a.T;    // tokens past T: no decay, beta 0
+            x0 = lg && p ? lg[t] : 0.f;
+            x1 = lg && q ? lg[t + 1] : 0.f;
+            b0 = p ? __bfloat162float(bp[t]) : 0.f;
+            b1 = q ? __bfloat162float(bp[t + 1]) : 0.f;
+        };
+        if (pw == 0 && n > 0) fetch(0);
+        for (int m = 0; m < n; ++m) {
+            float* gt = reinterpret_cast<float*>(sm + L::G_OFF + (m % NG) * L::GB);
+            const uint32_t tb = s0 + L::TP_OFF + (m % NV) * 4 * SLAB, pb = tb + 2 * SLAB;
+            if (pw == 0) {
+                // running sum of the gate over the chunk, two tokens a lane
+                const bool bad = __any_sync(~0u, x0 != x0 || x1 != x1);   // a NaN gate reaches the state through exp(G)
+                // below -1e5 exp() is zero whatever comes later
+                x0 = fminf(fmaxf(x0, -1e5f), 1e5f);
+                x1 = fminf(fmaxf(x1, -1e5f), 1e5f);
+                Two s = two_add(Two{x0, 0.f}, Two{x1, 0.f});
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const Two y = {__shfl_up_sync(~0u, s.h, o), __shfl_up_sync(~0u, s.l, o)};
+                    if (lane >= o) s = two_add(s, y);
+                }
+                const Two g1 = s, g0 = two_add(s, Two{-x1, 0.f});
+                const Two mid = {__shfl_sync(~0u, g1.h, 15), __shfl_sync(~0u, g1.l, 15)};   // G at token 31
+                const Two end = {__shfl_sync(~0u, g1.h, 31), __shfl_sync(~0u, g1.l, 31)};
+                auto minus = [](Two x, Two y) { return (x.h - y.h) + (x.l - y.l); };
+                const float d0 = minus(g0, mid), d1 = minus(g1, mid);
+                const bool near = __all_sync(~0u, fmaxf(fabsf(d0), fabsf(d1)) <= kRange);
+                const float nan = __int_as_float(0x7fc00000);
+                const float e0 = bad ? nan : expf(g0.h + g0.l), e1 = bad ? nan : expf(g1.h + g1.l);
+                float2* o = reinterpret_cast<float2*>(gt) + lane;
+                o[0] = make_float2(b0, b1);
+                o[C / 2] = make_float2(e0, e1);
+                o[C] = make_float2(expf(minus(end, g0)), expf(minus(end, g1)));
+                o[3 * C / 2] = make_float2(-e0, -e1);
+                // the factors of D (zeros where the gate is too steep for them) and G
+                o[2 * C] = near ? make_float2(expf(d0), expf(d1)) : make_float2(0.f, 0.f);
+                o[5 * C / 2] = near ? make_float2(expf(-d0), expf(-d1)) : make_float2(0.f, 0.f);
+                o[3 * C] = make_float2(g0.h, g1.h);
+                o[7 * C / 2] = make_float2(g0.l, g1.l);
+                if (m + 1 < n) fetch(m + 1);
+            }
+            named_bar_sync(2, 256);
+            wait(g_full, m & 1, abort_flag, status, ERR_PREP);
+            tc_fence_after();
+            uint32_t r[32];
+            tmem_ld32(tm + ((uint32_t)(quarter * 32) << 16) + L::tG + c0, r);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(g_read);
+            {
+                // tensor-memory lanes 0-63: rows of L; 64-127: rows of P
+                const bool near = gt[4 * C] != 0.f;
+                const float f = isP ? a.scale : 1.f;
+                const int last = isP ? i : i - 1;
+                const float fi = f * gt[4 * C + i], gh = gt[6 * C + i], gl = gt[7 * C + i], be = gt[i];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {          // eight columns at a time
+                    float x[8];
+                    const int cq = c0 + 8 * q;
+                    if (near) {
+                        const float4 u = *reinterpret_cast<const float4*>(gt + 5 * C + cq);
+                        const float4 v = *reinterpret_cast<const float4*>(gt + 5 * C + cq + 4);
+                        const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[8 * q + j]) * (fi * w[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            x[j] = f * __uint_as_float(r[8 * q + j]) * expf((gh - gt[6 * C + cq + j]) + (gl - gt[7 * C + cq + j]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = cq + j <= last ? x[j] : 0.f;
+                    const bool own = !isP && (cq >> 4) == (i >> 4);   // the row's diagonal block: to fp32, times beta
+                    uint32_t h8[4], l8[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split2(x[2 * e], x[2 * e + 1], h8[e], l8[e]);
+                    const uint32_t o = sw(isP ? pb : tb, i, cq / 8);
+                    if (own) {
+                        float* dd = diag + (i >> 4) * 16 * LDD + (i & 15) * LDD + (cq & 15);
+                        *reinterpret_cast<float4*>(dd) = make_float4(be * x[0], be * x[1], be * x[2], be * x[3]);
+                        *reinterpret_cast<float4*>(dd + 4) = make_float4(be * x[4], be * x[5], be * x[6], be * x[7]);
+                    } else {
+                        sts4(o, h8[0], h8[1], h8[2], h8[3]);
+                        sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
+                    }
+                }
+            }
+            named_bar_sync(2, 256);
+            if (pw < 4) {
+                // diagonal block `pw`: column cc of its inverse by forward substitution, a lane each
+                // (both half-warps; one stores the high parts, one the low)
+                const int cc = lane & 15;
+                const float* A = diag + pw * 16 * LDD;
+                float2 x[8];
+#pragma unroll
+                for (int ii = 0; ii < 16; ++ii) {
+                    float2 s0v = make_float2(ii == cc ? 1.f : 0.f, 0.f), s1v = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < ii; j += 4) {
+                        const float4 q = *reinterpret_cast<const float4*>(A + ii * LDD + j);
+                        if (j + 1 < ii) s0v = fma2(make_float2(-q.x, -q.y), x[j / 2], s0v);
+                        else s0v.x = fmaf(-q.x, x[j / 2].x, s0v.x);
+                        if (j + 3 < ii) s1v = fma2(make_float2(-q.z, -q.w), x[j / 2 + 1], s1v);
+                        else if (j + 2 < ii) s1v.x = fmaf(-q.z, x[j / 2 + 1].x, s1v.x);
+                    }
+                    const float v = (s0v.x + s0v.y) + (s1v.x + s1v.y);
+                    if (ii & 1) x[ii / 2].y = v;
+                    else x[ii / 2].x = v;
+                }
+                const float be = gt[16 * pw + cc];
+                const uint32_t o0 = tb + (lane >> 4) * SLAB;
+#pragma unroll
+                for (int ii = 0; ii < 16; ii += 2) {
+                    uint32_t hh, ll;
+                    split2(be * x[ii / 2].x, be * x[ii / 2].y, hh, ll);
+                    const uint32_t w = lane < 16 ? hh : ll;
+                    const int row = 16 * pw + ii, col = 16 * pw + cc;
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(sw(o0, row, col >> 3) + (col & 7) * 2), "h"((uint16_t)w) : "memory");
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(sw(o0, row + 1, col >> 3) + (col & 7) * 2), "h"((uint16_t)(w >> 16)) : "memory");
+                }
+            }
+            named_bar_sync(2, 256);
+            {
+                // 16 -> 32, eight columns a warp for each of the two pairs
+                float x[4];
+                const int o = 32 * (pw >> 1), n0 = (pw & 1) * 8;
+                if (pw < 4) block_rule<16>(tb, o + 16, o + 16, o, n0, x);
+                named_bar_sync(2, 256);
+                if (pw < 4) put_fragment(tb, o + 16, o + n0, x);
+            }
+            named_bar_sync(2, 256);
+            {
+                // 32 -> 64: 16 rows by eight columns a warp
+                float x[4];
+                const int r0 = 32 + (pw >> 2) * 16, n0 = (pw & 3) * 8;
+                block_rule<32>(tb, r0, 32, 0, n0, x);
+                named_bar_sync(2, 256);
+                put_fragment(tb, r0, n0, x);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&t_ready[m & 1]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// The states entering the segments: S_in[0] = S0, S_in[s + 1] = M_s S_in[s] + S*_s, with each segment's
+// (S* [dk][dv], M [dk][dk]) side by side. A block owns 32 columns of one head; 1.5 us a segment.
+template <int DK>
+__global__ void __launch_bounds__(256) gla_delta_scan_kernel(const float* __restrict__ S0, const float* __restrict__ pair,
+                                                             float* S_in, int dv, int nseg)
+{
+    __shared__ float s[2][DK][32];
+    const int bh = blockIdx.y, c = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+    const bool in = col < dv;
+    const size_t st = (size_t)DK * dv, step = st + DK * DK;
+    float* out = S_in + (size_t)bh * nseg * st + col;
+    for (int r = w; r < DK; r += 8) {
+        const float x = S0 && in ? S0[bh * st + (size_t)r * dv + col] : 0.f;
+        s[0][r][c] = x;
+        if (in) out[(size_t)r * dv] = x;
+    }
+    for (int g = 0; g + 1 < nseg; ++g) {
+        __syncthreads();
+        const float* p = pair + ((size_t)bh * (nseg - 1) + g) * step;
+        const float* M = p + st;
+        float y[DK / 8];
+#pragma unroll
+        for (int i = 0; i < DK / 8; ++i) y[i] = in ? p[(size_t)(w + 8 * i) * dv + col] : 0.f;
+        for (int j = 0; j < DK; j += 4) {
+            const float x0 = s[g & 1][j][c], x1 = s[g & 1][j + 1][c], x2 = s[g & 1][j + 2][c], x3 = s[g & 1][j + 3][c];
+#pragma unroll
+            for (int i = 0; i < DK / 8; ++i) {
+                const float4 f = *reinterpret_cast<const float4*>(M + (size_t)(w + 8 * i) * DK + j);
+                y[i] = fmaf(f.x, x0, fmaf(f.y, x1, fmaf(f.z, x2, fmaf(f.w, x3, y[i]))));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < DK / 8; ++i) {
+            s[(g + 1) & 1][w + 8 * i][c] = y[i];
+            if (in) out[(g + 1) * st + (size_t)(w + 8 * i) * dv] = y[i];
+        }
+    }
+}
+
+template <int DK, bool OUT>
+cudaError_t launch_pass(const FusedArgs& a, const FusedMaps& m, dim3 grid, cudaStream_t s)
+{
+    using L = FL<DK>;
+    cudaError_t e = cudaFuncSetAttribute(gla_delta_fused_kernel<DK, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    if (e != cudaSuccess) return e;
+    gla_delta_fused_kernel<DK, OUT><<<grid, NT, L::SMEM, s>>>(a, m);
+    return cudaGetLastError();
+}
+
+template <int DK>
+cudaError_t launch_dk(const DeltaChunks& p, const FusedMaps& m, int* status, cudaStream_t s)
+{
+    const unsigned BH = (unsigned)(p.B * p.H);
+    const long long st = (long long)p.dk * p.dv;
+    FusedArgs a;
+    a.log_g = p.log_g; a.beta = static_cast<const __nv_bfloat16*>(p.beta);
+    a.H = p.H; a.Hk = p.Hk; a.T = p.T; a.dv = p.dv; a.nch = p.nch; a.cps = p.cps; a.nseg = p.nseg;
+    a.tiles = (p.dv + DVT - 1) / DVT;
+    a.scale = p.scale; a.status = status;
+    const unsigned tiles = (unsigned)a.tiles;
+    if (p.nseg > 1) {
+        // every segment but the last: its state from zero and its transition
+        a.S_in = nullptr; a.in_bh = a.in_seg = 0;
+        a.S_out = p.pair; a.out_seg = st + (long long)p.dk * p.dk; a.out_bh = a.out_seg * (p.nseg - 1);
+        cudaError_t e = launch_pass<DK, false>(a, m, dim3(tiles + 1, BH, p.nseg - 1), s);
+        if (e != cudaSuccess) return e;
+        gla_delta_scan_kernel<DK><<<dim3((p.dv + 31) / 32, BH), 256, 0, s>>>(p.S0, p.pair, p.seg_in, p.dv, p.nseg);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        a.S_in = p.seg_in; a.in_bh = st * p.nseg; a.in_seg = st;
+    } else {
+        a.S_in = p.S0; a.in_bh = st; a.in_seg = 0;
+    }
+    a.S_out = p.ST; a.out_bh = st; a.out_seg = 0;
+    return launch_pass<DK, true>(a, m, dim3(tiles, BH, p.nseg), s);
+}
+
+}  // namespace
+
+cudaError_t launch_delta_chunks(const DeltaChunks& p, int* status, cudaStream_t s)
+{
+    const uint64_t bk = (uint64_t)p.B * p.Hk, bh = (uint64_t)p.B * p.H;
+    FusedMaps m;
+    if (!map_rows(&m.k, p.k, p.dk, p.T, bk) || !map_rows(&m.q, p.q, p.dk, p.T, bk) || !map_slabs(&m.v, p.v, p.dv, p.T, bh, 2))
+        return cudaErrorInvalidValue;
+    {   // O: staged without a swizzle
+        const uint64_t dims[3] = {(uint64_t)p.dv, (uint64_t)p.T, bh}, str[2] = {(uint64_t)p.dv * 2, (uint64_t)p.dv * p.T * 2};
+        const uint32_t box[3] = {64, C, 1};
+        if (!make_tmap(&m.o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.O, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+    }
+    return p.dk == 64 ? launch_dk<64>(p, m, status, s) : launch_dk<128>(p, m, status, s);
+}
+
+}  // namespace gla

@@ -54,33 +54,31 @@ struct DeltaBwdSum {
 cudaError_t launch_delta_bwd_sum(const DeltaBwdSum& a, cudaStream_t s);
 
 // The chunk form (bf16, dk in {64, 128}, dv a multiple of 64), 64-token chunks on tcgen05.
-// Prep (gla_delta_prep.cu), chunk by chunk in parallel: with G the running sum of log_g in the
+// The backward's prep (gla_delta_prep.cu), chunk by chunk in parallel: with G the running sum of log_g in the
 // chunk, A[i][j] = beta_i (k_i . k_j) exp(G_i - G_j) for j < i, it writes
 //   t [BH][nch][2][64][64] bf16      : (I + A)^-1 diag(beta) in two parts (17 bits),
 //   p, the same                      : scale (q_i . k_j) exp(G_i - G_j) for j <= i, else 0,
-//   gates [BH][nch][4][64] fp32      : beta, exp(G), exp(G_end - G), -exp(G); with grads
-//                                      [BH][nch][8][64]: also exp(G - G_mid), exp(G_mid - G) and G
-//                                      in two floats.
+//   gates [BH][nch][8][64] fp32      : beta, exp(G), exp(G_end - G), -exp(G), exp(G - G_mid),
+//                                      exp(G_mid - G) (both 0 where too steep) and G in two floats.
 struct DeltaPrep {
     const void* q; const void* k; const float* log_g; const void* beta;
     void* t; void* p; float* gates;
     int B, H, Hk, T, dk, nch;
     float scale;
-    bool grads;         // for the backward
     float beta_floor;   // > 0: smaller |beta| are taken as this (the backward divides by it)
 };
 cudaError_t launch_delta_prep(const DeltaPrep& a, int* status, cudaStream_t s);
 
-// The serial pass over the chunks (gla_delta_chain.cu), the state in registers and tensor
-// memory, one CTA per head and 128 columns of dv.
-struct DeltaChain {
-    const void* q; const void* k; const void* v;
-    const void* t; const void* p; const float* gates;
-    const float* S0; void* O; float* ST;
-    int B, H, Hk, T, dk, dv, nch;
+// The forward pass of the chunk form (gla_delta_fused.cu): one kernel, or with nseg > 1 segments of cps
+// chunks three: every segment's state from zero and its dk x dk transition (pair: [BH][nseg - 1] of
+// [dk][dv] and [dk][dk]), the states entering the segments (seg_in [BH][nseg][dk][dv]), and the pass.
+struct DeltaChunks {
+    const void* q; const void* k; const void* v; const float* log_g; const void* beta;
+    const float* S0; void* O; float* ST; float* pair; float* seg_in;
+    int B, H, Hk, T, dk, dv, nch, cps, nseg;
     float scale;
 };
-cudaError_t launch_delta_chain(const DeltaChain& a, int* status, cudaStream_t s);
+cudaError_t launch_delta_chunks(const DeltaChunks& a, int* status, cudaStream_t s);
 
 // The backward's serial passes (gla_delta_bwd_chain.cu). Forward sweep: from S0, the state
 // entering every chunk and the chunk's U to the workspace. Reverse sweep: from dST, the

@@ -1,5 +1,5 @@
-// gla_delta_prep: what the chunk form of the gated delta rule needs of every 64-token chunk and
-// does not depend on the state. Within a chunk the corrections u solve
+// gla_delta_prep: what the backward's sweeps (gla_delta_bwd_chain.cu) need of every 64-token chunk
+// and does not depend on the state; the forward pass forms the same on the fly (gla_delta_fused.cu). Within a chunk the corrections u solve
 //
 //     u_i = beta_i (v_i - exp(G_i) k_i S) - sum_{j<i} A_ij u_j,
 //     A_ij = beta_i (k_i . k_j) exp(G_i - G_j),
@@ -31,16 +31,6 @@ constexpr int LD = 68;            // row stride of the fp32 matrices: 16-byte ro
 constexpr float kRange = 60.f;    // |G - G_mid| up to which the two-factor form is used
 
 enum { ERR_LOAD = 0x601, ERR_MMA = 0x602 };
-
-// A sum of floats kept with its rounding errors (Knuth's two-sum, renormalised).
-struct Two { float h, l; };
-__device__ __forceinline__ Two two_add(Two a, Two b)
-{
-    const float s = __fadd_rn(a.h, b.h), t = __fadd_rn(s, -a.h);
-    const float e = __fadd_rn(__fadd_rn(a.h, -__fadd_rn(s, -t)), __fadd_rn(b.h, -t)) + (a.l + b.l);
-    const float h = __fadd_rn(s, e);
-    return Two{h, __fadd_rn(e, -__fadd_rn(h, -s))};
-}
 
 template <int DK>
 struct PL {
@@ -157,20 +147,18 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
         be[i] = b0; be[i + 1] = b1;
         const float nan = __int_as_float(0x7fc00000);
         const float e0 = bad ? nan : expf(g0.h + g0.l), e1 = bad ? nan : expf(g1.h + g1.l);
-        float2* go = reinterpret_cast<float2*>(a.gates + (bh * a.nch + c) * (a.grads ? 8 : 4) * C) + lane;
+        float2* go = reinterpret_cast<float2*>(a.gates + (bh * a.nch + c) * 8 * C) + lane;
         go[0] = make_float2(b0, b1);
         go[C / 2] = make_float2(e0, e1);
         go[C] = make_float2(expf(minus(end, g0)), expf(minus(end, g1)));
         go[3 * C / 2] = make_float2(-e0, -e1);
-        if (a.grads) {
-            // for the gradients: the factors of exp(G_i - G_j) (zeros where the chunk's gate is too
-            // steep for them), and G
-            const bool near = m <= kRange;
-            go[2 * C] = near ? make_float2(fa[i], fa[i + 1]) : make_float2(0.f, 0.f);
-            go[5 * C / 2] = near ? make_float2(fb[i], fb[i + 1]) : make_float2(0.f, 0.f);
-            go[3 * C] = make_float2(g0.h, g1.h);
-            go[7 * C / 2] = make_float2(g0.l, g1.l);
-        }
+        // for the gradients: the factors of exp(G_i - G_j) (zeros where the chunk's gate is too
+        // steep for them), and G
+        const bool near = m <= kRange;
+        go[2 * C] = near ? make_float2(fa[i], fa[i + 1]) : make_float2(0.f, 0.f);
+        go[5 * C / 2] = near ? make_float2(fb[i], fb[i + 1]) : make_float2(0.f, 0.f);
+        go[3 * C] = make_float2(g0.h, g1.h);
+        go[7 * C / 2] = make_float2(g0.l, g1.l);
     }
     tc_fence_before();
     __syncthreads();

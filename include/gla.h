@@ -406,7 +406,9 @@ const char* gla_bwd_stage_name(const gla_bwd_params* p, int stage);
  *                    64, B H <= 65535; else GLA_ERR_UNSUPPORTED): 64-token chunks, the
  *                    corrections u of a chunk through the inverse of a unit triangular matrix.
  *                    What feeds the state is kept to 17 bits (pairs of bf16) and summed in
- *                    fp32: S_T is good to about 3e-6, O to its bf16 rounding.
+ *                    fp32: S_T is good to about 3e-6, O to its bf16 rounding. With few heads the
+ *                    sequence is cut into segments: their states from zero and their dk x dk
+ *                    transitions first, then the states entering them, then the pass over all.
  *   GLA_PATH_AUTO    the form that is faster for the sizes.
  * dk and dv are multiples of 16, q, k, v, O, S0 and ST 16-byte aligned, `scale` finite. ST may
  * equal S0 (the state carried in place). Other outputs may not overlap inputs. T = 0 copies S0
@@ -427,6 +429,7 @@ typedef struct {
     int path;               /* gla_path: AUTO, TENSOR or SIMT */
     void* workspace;        /* gla_delta_fwd_workspace_size() bytes, 256-byte aligned */
     size_t workspace_bytes;
+    int force_segments;     /* chunk form: 0: the planner chooses the sequence split; n >= 1: n segments */
 } gla_delta_params;
 
 gla_status gla_delta_fwd(const gla_delta_params* p, cudaStream_t stream);

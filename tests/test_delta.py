@@ -133,7 +133,7 @@ def test_backward_refuses_before_launch(kw, want):
 
 
 def test_struct_layout():
-    assert ctypes.sizeof(bnd.gla_delta_params) == 8 * 8 + 9 * 4 + 4 + 16
+    assert ctypes.sizeof(bnd.gla_delta_params) == 8 * 8 + 9 * 4 + 4 + 16 + 8
     assert ctypes.sizeof(bnd.gla_delta_bwd_params) == 14 * 8 + 9 * 4 + 4 + 16
 
 
@@ -150,7 +150,12 @@ def test_python_checks_shapes():
 
 
 def test_plans_on_host():
-    """The chunk form needs its inverses, scores and gates: 25 KB a chunk and head; the recurrent none."""
+    """Workspace only for the segments of a cut sequence: a state and a transition each but the last, and a state
+    entering each."""
+    seg = 2 * (3 * (64 * 64 + 64 * 64) + 4 * 64 * 64) * 4     # H = 2, four segments
+    assert bnd.gla_delta_fwd_workspace_size(_params(T=500, force_segments=4)) == seg
+    assert bnd.gla_delta_fwd_workspace_size(_params(T=500, force_segments=1)) == 0
+    assert bnd.gla_delta_fwd(_params(T=500, force_segments=-1), 0, check=False) == 1
     assert bnd.gla_delta_fwd_workspace_size(_params(T=1)) == 0
     assert bnd.gla_delta_fwd_workspace_size(_params(T=500, dtype=gla.GLA_FP32)) == 0
     assert bnd.gla_delta_fwd_workspace_size(_params(T=500, dk=80)) == 0
@@ -184,6 +189,20 @@ def test_chunk_form_of_dependent_keys(keys, beta):
 @pytest.mark.parametrize("T,dk,dv", [(1, 128, 128), (1, 16, 16), (5, 64, 80), (17, 256, 64), (40, 48, 144), (2, 208, 128)])
 def test_recurrent_form(T, dk, dv, gate, dtype):
     check_forward(ref.make(2, 4, 2, T, dk, dv, dtype, seed=T, gate=gate)[0], path=gla.GLA_PATH_SIMT)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("segments", [2, 3, 7])
+@pytest.mark.parametrize("gate", ["sigmoid", "steep", "resets"])
+@pytest.mark.parametrize("dk,dv,T", [(128, 128, 430), (64, 192, 449), (128, 64, 131)])
+def test_cut_sequences(dk, dv, T, gate, segments):
+    x = ref.make(1, 2, 1, T, dk, dv, torch.bfloat16, seed=T, gate=gate, s0=segments != 3)[0]
+    O, S = ref.delta(*ref.f64(x), dk ** -0.5)
+    got_O, got_S = gla.delta_forward(*ref.cuda(x), path=gla.GLA_PATH_TENSOR, force_segments=segments)
+    torch.cuda.synchronize()
+    assert gla.gla_device_status() == 0
+    assert_close(to_np(got_O), to_np(O), torch.bfloat16, "O")
+    close(got_S, S, 6 * PARTS, "S_T")        # the transition's two-part operands too
 
 
 @pytest.mark.gpu
