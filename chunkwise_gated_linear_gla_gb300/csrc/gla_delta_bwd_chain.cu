@@ -75,7 +75,7 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
     uint64_t* y_ready = s_ready + 8;  // and written the parts of scale e dO (4 warps; reverse)
     uint64_t* fin = s_ready + 9;
     uint32_t* holder = reinterpret_cast<uint32_t*>(s_ready + 10);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(s_ready + 11);
+    const Abort abort_flag(s_ready + 11);
 
     const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32, wg = warp / 4;
     const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;

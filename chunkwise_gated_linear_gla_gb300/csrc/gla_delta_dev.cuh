@@ -14,15 +14,29 @@ constexpr int C = kChunk;
 constexpr int SLAB = C * 128;                     // 64 rows of 128 bytes: one swizzled TMA box
 constexpr uint64_t kTimeoutNs = 2000000000ull;    // per wait
 
-// Bounded wait. When it runs out (or another thread's has) the caller goes on without waiting:
-// every role keeps its sequence of arrivals, so the CTA ends; the status word reports it.
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status, int code)
+// A CTA's abort flag and the time at which its waits give up: between 4.3 and 8.6 seconds after its
+// start (the upper word of the nanosecond clock, two steps on).
+struct Abort {
+    volatile int* flag;
+    uint32_t deadline;
+    __device__ __forceinline__ explicit Abort(void* p) : flag(static_cast<volatile int*>(p)) {
+        asm volatile("mov.u32 %0, %%globaltimer_hi;" : "=r"(deadline));
+        deadline += 2;
+    }
+    __device__ __forceinline__ volatile int& operator*() const { return *flag; }
+};
+
+// Bounded wait. When it runs out the caller goes on without waiting: every role keeps its sequence of
+// arrivals, and all of a CTA's roles give up at the same time, so the CTA ends; the status word
+// reports it. The loop is short on purpose: it is copied to every wait, and code that pushes the
+// roles' steps out of the instruction caches costs them dearly.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, const Abort& abort_flag, int* status, int code)
 {
-    if (sm100::mbar_try_wait(bar, parity)) return;
-    const uint64_t t0 = sm100::globaltimer();
+#pragma unroll 1
     while (!sm100::mbar_try_wait(bar, parity)) {
-        if (*abort_flag) return;
-        if (sm100::globaltimer() - t0 > kTimeoutNs) {
+        uint32_t now;
+        asm volatile("mov.u32 %0, %%globaltimer_hi;" : "=r"(now));
+        if ((int)(now - abort_flag.deadline) >= 0) {
             *abort_flag = 1;
             atomicExch(status, code);
             return;

@@ -24,7 +24,7 @@
 // tile). G is summed in pairs of floats (48 bits), so a steep gate costs no precision; D is a product
 // of two factors around the chunk's middle while both stay within e^60, else one exponential per pair.
 //
-// Warps: 0 TMA, 1 products, 4-11 chain, 12-15 drain of O, 16-23 prep. Reads K, Q, V once
+// Warps: 0 TMA, 1 products, 3 gates, 4-11 chain, 12-15 drain of O, 16-23 prep. Reads K, Q, V once
 // and writes O once; bound by the chain's latency, with the tensor pipe busy 2800 cycles a chunk.
 #include "gla_delta_dev.cuh"
 #include "gla_delta_internal.h"
@@ -59,7 +59,7 @@ struct FL {
     static constexpr int G_OFF = O_OFF + 2 * SLAB;
     static constexpr int D_OFF = G_OFF + NG * GB;          // diagonal blocks of L beta, fp32
     static constexpr int BAR_OFF = D_OFF + 4 * 16 * LDD * 4;
-    static constexpr int SMEM = BAR_OFF + 256 + 1024;
+    static constexpr int SMEM = BAR_OFF + 320 + 1024;
     // tensor memory columns
     static constexpr int tD = 0;                           // the state's increment, [dv][DK]
     static constexpr int tSh = DK, tSl = tSh + DK / 2;     // the state's parts
@@ -191,8 +191,9 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
     uint64_t* g_full = s_ready + 15;        // the prep's product formed
     uint64_t* fin = s_ready + 16;
     uint64_t* o_empty = s_ready + 17;       // O read out (4 warps)
-    uint32_t* holder = reinterpret_cast<uint32_t*>(s_ready + 18);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(s_ready + 19);
+    uint64_t* gt_ready = s_ready + 18;      // [NG] a chunk's gates written
+    uint32_t* holder = reinterpret_cast<uint32_t*>(s_ready + 18 + NG);
+    const Abort abort_flag(s_ready + 19 + NG);
 
     const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32, wg = warp / 4;
     const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
@@ -204,7 +205,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * NKQ + 2 * NV; ++i) mbar_init(&bar[i], 1);
-        for (int i = 0; i < 18; ++i) mbar_init(&s_ready[i], i < 10 ? 8 : i == 17 ? 4 : 1);
+        for (int i = 0; i < 18 + NG; ++i) mbar_init(&s_ready[i], i < 10 ? 8 : i == 17 ? 4 : 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -219,7 +220,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
     int* status = a.status;
 
     if (wg == 0) {
-        regs_dec<40>();
+        regs_dec<48>();
         if (warp == 0) {
             // ------------------------------------------------------ TMA producer
             int kq = 0, v = 0;
@@ -265,6 +266,58 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
             }
             for (int m = max(0, kq - NKQ); m < kq; ++m) wait(&kq_full[m % NKQ], (m / NKQ) & 1, abort_flag, status, ERR_TMA);
             for (int m = max(0, v - NV); m < v; ++m) wait(&v_full[m % NV], (m / NV) & 1, abort_flag, status, ERR_TMA);
+        } else if (warp == 3) {
+            // ------------------------------------------------------ gates, up to NG - 1 chunks ahead
+            const float* lg = a.log_g ? a.log_g + (size_t)bh * a.T : nullptr;
+            const __nv_bfloat16* bp = a.beta + (size_t)bh * a.T;
+            float x0, x1, b0, b1;                           // two tokens of the next chunk
+            auto fetch = [&](int m) {
+                const int t = (first + m) * C + 2 * lane;
+                const bool p = t < a.T, q = t + 1 < a.T;    // tokens past T: no decay, beta 0
+                x0 = lg && p ? lg[t] : 0.f;
+                x1 = lg && q ? lg[t + 1] : 0.f;
+                b0 = p ? __bfloat162float(bp[t]) : 0.f;
+                b1 = q ? __bfloat162float(bp[t + 1]) : 0.f;
+            };
+            if (n > 0) fetch(0);
+            for (int m = 0; m < n; ++m) {
+                // the slot's last readers, chunk m - NG's register steps and drain, are done when the
+                // next chunk's increment is formed
+                if (m >= NG - 1) wait(&d_full[1], (m - NG + 1) & 1, abort_flag, status, ERR_PREP);
+                __syncwarp();
+                // running sum of the gate over the chunk
+                const bool bad = __any_sync(~0u, x0 != x0 || x1 != x1);   // a NaN gate reaches the state through exp(G)
+                // below -1e5 exp() is zero whatever comes later
+                x0 = fminf(fmaxf(x0, -1e5f), 1e5f);
+                x1 = fminf(fmaxf(x1, -1e5f), 1e5f);
+                Two s = two_add(Two{x0, 0.f}, Two{x1, 0.f});
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const Two y = {__shfl_up_sync(~0u, s.h, o), __shfl_up_sync(~0u, s.l, o)};
+                    if (lane >= o) s = two_add(s, y);
+                }
+                const Two g1 = s, g0 = two_add(s, Two{-x1, 0.f});
+                const Two mid = {__shfl_sync(~0u, g1.h, 15), __shfl_sync(~0u, g1.l, 15)};   // G at token 31
+                const Two end = {__shfl_sync(~0u, g1.h, 31), __shfl_sync(~0u, g1.l, 31)};
+                auto minus = [](Two x, Two y) { return (x.h - y.h) + (x.l - y.l); };
+                const float d0 = minus(g0, mid), d1 = minus(g1, mid);
+                const bool near = __all_sync(~0u, fmaxf(fabsf(d0), fabsf(d1)) <= kRange);
+                const float nan = __int_as_float(0x7fc00000);
+                const float e0 = bad ? nan : expf(g0.h + g0.l), e1 = bad ? nan : expf(g1.h + g1.l);
+                float2* o = reinterpret_cast<float2*>(sm + L::G_OFF + (m % NG) * L::GB) + lane;
+                o[0] = make_float2(b0, b1);
+                o[C / 2] = make_float2(e0, e1);
+                o[C] = make_float2(expf(minus(end, g0)), expf(minus(end, g1)));
+                o[3 * C / 2] = make_float2(-e0, -e1);
+                // the factors of D (zeros where the gate is too steep for them) and G
+                o[2 * C] = near ? make_float2(expf(d0), expf(d1)) : make_float2(0.f, 0.f);
+                o[5 * C / 2] = near ? make_float2(expf(-d0), expf(-d1)) : make_float2(0.f, 0.f);
+                o[3 * C] = make_float2(g0.h, g1.h);
+                o[7 * C / 2] = make_float2(g0.l, g1.l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&gt_ready[m % NG]);
+                if (m + 1 < n) fetch(m + 1);
+            }
         } else if (warp == 1) {
             // ------------------------------------------------------ products
             // The whole warp walks the loop and one elected lane issues, so that descriptors stay
@@ -540,7 +593,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
         }
     } else if (wg == 3) {
         // ---------------------------------------------------------- drain of O
-        regs_dec<56>();
+        regs_dec<48>();
         if (OUT) {
             const int d = (warp & 3) * 32 + lane;
             const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
@@ -553,7 +606,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 // the tile's last store must have read it
                 if (lead) bulk_wait_read0();
                 named_bar_sync(1, 128);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 64; c += 16) {
                     uint32_t x[16], y[16];
                     tmem_ld16(tm + lb + L::tOq + c, x);
@@ -588,99 +641,59 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
         const int i = (quarter & 1) * 32 + lane;      // row of the chunk
         const bool isP = quarter >= 2;
         float* diag = reinterpret_cast<float*>(sm + L::D_OFF);
-        const float* lg = a.log_g ? a.log_g + (size_t)bh * a.T : nullptr;
-        const __nv_bfloat16* bp = a.beta + (size_t)bh * a.T;
-        float x0 = 0.f, x1 = 0.f, b0 = 0.f, b1 = 0.f;   // warp 16: the gates of two tokens of the next chunk
-        auto fetch = [&](int m) {
-            const int t = (first + m) * C + 2 * lane;
-            const bool p = t < a.T, q = t + 1 < a.T;    // tokens past T: no decay, beta 0
-            x0 = lg && p ? lg[t] : 0.f;
-            x1 = lg && q ? lg[t + 1] : 0.f;
-            b0 = p ? __bfloat162float(bp[t]) : 0.f;
-            b1 = q ? __bfloat162float(bp[t + 1]) : 0.f;
-        };
-        if (pw == 0 && n > 0) fetch(0);
         for (int m = 0; m < n; ++m) {
-            float* gt = reinterpret_cast<float*>(sm + L::G_OFF + (m % NG) * L::GB);
+            const float* gt = reinterpret_cast<const float*>(sm + L::G_OFF + (m % NG) * L::GB);
             const uint32_t tb = s0 + L::TP_OFF + (m % NV) * 4 * SLAB, pb = tb + 2 * SLAB;
-            if (pw == 0) {
-                // running sum of the gate over the chunk, two tokens a lane
-                const bool bad = __any_sync(~0u, x0 != x0 || x1 != x1);   // a NaN gate reaches the state through exp(G)
-                // below -1e5 exp() is zero whatever comes later
-                x0 = fminf(fmaxf(x0, -1e5f), 1e5f);
-                x1 = fminf(fmaxf(x1, -1e5f), 1e5f);
-                Two s = two_add(Two{x0, 0.f}, Two{x1, 0.f});
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const Two y = {__shfl_up_sync(~0u, s.h, o), __shfl_up_sync(~0u, s.l, o)};
-                    if (lane >= o) s = two_add(s, y);
-                }
-                const Two g1 = s, g0 = two_add(s, Two{-x1, 0.f});
-                const Two mid = {__shfl_sync(~0u, g1.h, 15), __shfl_sync(~0u, g1.l, 15)};   // G at token 31
-                const Two end = {__shfl_sync(~0u, g1.h, 31), __shfl_sync(~0u, g1.l, 31)};
-                auto minus = [](Two x, Two y) { return (x.h - y.h) + (x.l - y.l); };
-                const float d0 = minus(g0, mid), d1 = minus(g1, mid);
-                const bool near = __all_sync(~0u, fmaxf(fabsf(d0), fabsf(d1)) <= kRange);
-                const float nan = __int_as_float(0x7fc00000);
-                const float e0 = bad ? nan : expf(g0.h + g0.l), e1 = bad ? nan : expf(g1.h + g1.l);
-                float2* o = reinterpret_cast<float2*>(gt) + lane;
-                o[0] = make_float2(b0, b1);
-                o[C / 2] = make_float2(e0, e1);
-                o[C] = make_float2(expf(minus(end, g0)), expf(minus(end, g1)));
-                o[3 * C / 2] = make_float2(-e0, -e1);
-                // the factors of D (zeros where the gate is too steep for them) and G
-                o[2 * C] = near ? make_float2(expf(d0), expf(d1)) : make_float2(0.f, 0.f);
-                o[5 * C / 2] = near ? make_float2(expf(-d0), expf(-d1)) : make_float2(0.f, 0.f);
-                o[3 * C] = make_float2(g0.h, g1.h);
-                o[7 * C / 2] = make_float2(g0.l, g1.l);
-                if (m + 1 < n) fetch(m + 1);
-            }
-            named_bar_sync(2, 256);
+            wait(&gt_ready[m % NG], (m / NG) & 1, abort_flag, status, ERR_PREP);
             wait(g_full, m & 1, abort_flag, status, ERR_PREP);
             tc_fence_after();
-            uint32_t r[32];
-            tmem_ld32(tm + ((uint32_t)(quarter * 32) << 16) + L::tG + c0, r);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(g_read);
             {
                 // tensor-memory lanes 0-63: rows of L; 64-127: rows of P
                 const bool near = gt[4 * C] != 0.f;
                 const float f = isP ? a.scale : 1.f;
                 const int last = isP ? i : i - 1;
                 const float fi = f * gt[4 * C + i], gh = gt[6 * C + i], gl = gt[7 * C + i], be = gt[i];
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q) {          // eight columns at a time
-                    float x[8];
                     const int cq = c0 + 8 * q;
+                    uint32_t r[8];
+                    tmem_ld8(tm + ((uint32_t)(quarter * 32) << 16) + L::tG + cq, r);
+                    const float* wf = gt + 5 * C + cq;
+                    const float4 u = *reinterpret_cast<const float4*>(wf), v = *reinterpret_cast<const float4*>(wf + 4);
+                    tmem_wait_ld();
+                    float2 x[4];
                     if (near) {
-                        const float4 u = *reinterpret_cast<const float4*>(gt + 5 * C + cq);
-                        const float4 v = *reinterpret_cast<const float4*>(gt + 5 * C + cq + 4);
-                        const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[8 * q + j]) * (fi * w[j]);
+                        const float2 ff = make_float2(fi, fi);
+                        x[0] = mul2(f2(r[0], r[1]), mul2(ff, make_float2(u.x, u.y)));
+                        x[1] = mul2(f2(r[2], r[3]), mul2(ff, make_float2(u.z, u.w)));
+                        x[2] = mul2(f2(r[4], r[5]), mul2(ff, make_float2(v.x, v.y)));
+                        x[3] = mul2(f2(r[6], r[7]), mul2(ff, make_float2(v.z, v.w)));
                     } else {
+                        auto D = [&](int j) { return f * expf((gh - gt[6 * C + cq + j]) + (gl - gt[7 * C + cq + j])); };
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            x[j] = f * __uint_as_float(r[8 * q + j]) * expf((gh - gt[6 * C + cq + j]) + (gl - gt[7 * C + cq + j]));
+                        for (int j = 0; j < 4; ++j) x[j] = mul2(f2(r[2 * j], r[2 * j + 1]), make_float2(D(2 * j), D(2 * j + 1)));
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = cq + j <= last ? x[j] : 0.f;
-                    const bool own = !isP && (cq >> 4) == (i >> 4);   // the row's diagonal block: to fp32, times beta
-                    uint32_t h8[4], l8[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) split2(x[2 * e], x[2 * e + 1], h8[e], l8[e]);
-                    const uint32_t o = sw(isP ? pb : tb, i, cq / 8);
-                    if (own) {
+                    for (int j = 0; j < 4; ++j) {
+                        x[j].x = cq + 2 * j <= last ? x[j].x : 0.f;
+                        x[j].y = cq + 2 * j + 1 <= last ? x[j].y : 0.f;
+                    }
+                    if (!isP && (cq >> 4) == (i >> 4)) {   // the row's diagonal block: to fp32, times beta
                         float* dd = diag + (i >> 4) * 16 * LDD + (i & 15) * LDD + (cq & 15);
-                        *reinterpret_cast<float4*>(dd) = make_float4(be * x[0], be * x[1], be * x[2], be * x[3]);
-                        *reinterpret_cast<float4*>(dd + 4) = make_float4(be * x[4], be * x[5], be * x[6], be * x[7]);
+                        *reinterpret_cast<float4*>(dd) = make_float4(be * x[0].x, be * x[0].y, be * x[1].x, be * x[1].y);
+                        *reinterpret_cast<float4*>(dd + 4) = make_float4(be * x[2].x, be * x[2].y, be * x[3].x, be * x[3].y);
                     } else {
+                        uint32_t h8[4], l8[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) split2(x[e], h8[e], l8[e]);
+                        const uint32_t o = sw(isP ? pb : tb, i, cq / 8);
                         sts4(o, h8[0], h8[1], h8[2], h8[3]);
                         sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
                     }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(g_read);
             }
             named_bar_sync(2, 256);
             if (pw < 4) {

@@ -77,7 +77,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     uint64_t* m_3 = bar + 5;     // products with dS^T done
     uint64_t* m_h = bar + 6;     // products of W and M done
     uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 7);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 8);
+    const Abort abort_flag(bar + 8);
     float* gt = reinterpret_cast<float*>(sm + L::G_OFF);
     float* rs = reinterpret_cast<float*>(sm + L::R_OFF);        // [4][64] row sums
     float* ss = rs + 4 * C;                                     // [4][64] k . (l U dS^T)

@@ -83,7 +83,7 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
     float* mx = be + C;                                    // [0]: max |G - G_mid|
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR_OFF);   // loaded, multiplied
     uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 2);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 3);
+    const Abort abort_flag(bar + 3);
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid % 32;
     const int c = blockIdx.x % a.nch, bhi = blockIdx.x / a.nch;
