@@ -18,10 +18,10 @@
 // cancelling terms, 7.5e-3 off when all keys are the same).
 //
 // The prep (warps 16-23) runs one chunk ahead on the same SM: one product of 128 rows, K stacked on
-// Q, against K^T; the masked L and P; then T in place of L: 16-row diagonal blocks by forward
-// substitution in fp32, and twice the block rule, the inverse of [[X^-1, 0], [C, Y^-1]] has -Y C X
-// below, on mma.sync fragments in two parts (16 x 16 and 32 x 32 pieces, too small for a tcgen05
-// tile). G is summed in pairs of floats (48 bits), so a steep gate costs no precision; D is a product
+// Q, against K^T; the masked L and P; then T in place of L: 8-row diagonal blocks by forward
+// substitution in fp32, then three times the block rule, the inverse of [[X^-1, 0], [C, Y^-1]] has -Y C X
+// below: once more in fp32, then on mma.sync fragments in two parts (16 x 16 and 32 x 32 pieces, too
+// small for a tcgen05 tile). G is summed in pairs of floats (48 bits), so a steep gate costs no precision; D is a product
 // of two factors around the chunk's middle while both stay within e^60, else one exponential per pair.
 //
 // Warps: 0 TMA, 1 products, 3 gates, 4-11 chain, 12-15 drain of O, 16-23 prep. Reads K, Q, V once
@@ -57,7 +57,8 @@ struct FL {
     static constexpr int O_OFF = TP_OFF + NV * 4 * SLAB;   // [2 halves of dv][64 tokens][64] bf16
     static constexpr int GB = 8 * C * 4;                   // beta, e, l, -e, the factors of D, G in two floats
     static constexpr int G_OFF = O_OFF + 2 * SLAB;
-    static constexpr int D_OFF = G_OFF + NG * GB;          // diagonal blocks of L beta, fp32
+    static constexpr int W_OFF = G_OFF + NG * GB;          // 32 rows of [32 values, their low parts]
+    static constexpr int D_OFF = W_OFF + 32 * 128;         // diagonal blocks of beta L, fp32
     static constexpr int BAR_OFF = D_OFF + 4 * 16 * LDD * 4;
     static constexpr int SMEM = BAR_OFF + 320 + 1024;
     // tensor memory columns
@@ -103,6 +104,24 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], con
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
+// c (16 x 8) += Y Z over K values: Y's rows from (yr, yc) of a matrix whose low parts lie ylo bytes
+// behind, or in the rows' other halves (ylo = 64); Z's from (zr, zc), low parts SLAB behind.
+template <int K>
+__device__ __forceinline__ void block_product(uint32_t y, int yr, int yc, uint32_t ylo, uint32_t z, int zr, int zc, float (&c)[4])
+{
+#pragma unroll
+    for (int k = 0; k < K; k += 16) {
+        uint32_t ah[4], al[4], bh[2], bl[2];
+        ldm_a(y, yr, yc + k, ah);
+        if (ylo == 64) ldm_a(y, yr, yc + k + 32, al);
+        else ldm_a(y + ylo, yr, yc + k, al);
+        ldm_b(z, zr + k, zc, bh);
+        ldm_b(z + SLAB, zr + k, zc, bl);
+        mma16(c, ah, bh);
+        mma16(c, al, bh);
+        mma16(c, ah, bl);
+    }
+}
 // X (16 x 8 at column n0 of the block) = -(Y C) Z for K-wide pieces: Y at (yr, yc), C at (yc, zc) and Z at
 // (zc, zc) of the matrix whose parts start at hi and hi + SLAB. Columns n0 .. n0 + 7 of the product.
 template <int K>
@@ -145,17 +164,18 @@ __device__ __forceinline__ void block_rule(uint32_t hi, int yr, int yc, int zc, 
         mma16(x, ah, bl);
     }
 }
-// The 16 x 8 fragment to rows r0.., columns c0.. of both parts.
-__device__ __forceinline__ void put_fragment(uint32_t hi, int r0, int c0, const float (&x)[4])
+// The 16 x 8 fragment times f to rows r0.., columns c0.. of both parts (the low one as above).
+__device__ __forceinline__ void put_fragment(uint32_t hi, int r0, int c0, uint32_t lo, const float (&x)[4], float f)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         uint32_t h, l;
-        split2(x[2 * e], x[2 * e + 1], h, l);
+        split2(f * x[2 * e], f * x[2 * e + 1], h, l);
         const uint32_t a = sw(hi, r0 + g + 8 * e, c0 / 8) + t * 4;
+        const uint32_t b = lo == 64 ? sw(hi, r0 + g + 8 * e, c0 / 8 + 4) + t * 4 : a + lo;
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(h) : "memory");
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(a + SLAB), "r"(l) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(b), "r"(l) : "memory");
     }
 }
 __device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
@@ -370,7 +390,8 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                     }
                     __syncwarp();
                 }
-                // V^T T^T, both from shared memory, in the gap of R's register step
+                // the next chunk's K on Q against K, then V^T T^T, in the gap of R's register step
+                if (m + 1 < n) gram(m + 1);
                 wait(&t_ready[m & 1], (m >> 1) & 1, abort_flag, status, ERR_MMA);
                 if (!ident) {
                     wait(&v_full[vt], (m / NV) & 1, abort_flag, status, ERR_MMA);
@@ -386,7 +407,6 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                     }
                     __syncwarp();
                 }
-                if (m + 1 < n) gram(m + 1);
                 // U^T += R^T T^T: B = T (rows i, columns j: K-major)
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
@@ -652,33 +672,38 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 const bool near = gt[4 * C] != 0.f;
                 const float f = isP ? a.scale : 1.f;
                 const int last = isP ? i : i - 1;
-                const float fi = f * gt[4 * C + i], gh = gt[6 * C + i], gl = gt[7 * C + i], be = gt[i];
+                const float fi = f * gt[4 * C + i], gh = gt[6 * C + i], gl = gt[7 * C + i];
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {          // eight columns at a time
-                    const int cq = c0 + 8 * q;
-                    uint32_t r[8];
-                    tmem_ld8(tm + ((uint32_t)(quarter * 32) << 16) + L::tG + cq, r);
+                for (int c = c0; c < c0 + 32; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tm + ((uint32_t)(quarter * 32) << 16) + L::tG + c, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {          // eight columns at a time
+                    const int cq = c + 8 * q;
                     const float* wf = gt + 5 * C + cq;
                     const float4 u = *reinterpret_cast<const float4*>(wf), v = *reinterpret_cast<const float4*>(wf + 4);
-                    tmem_wait_ld();
                     float2 x[4];
                     if (near) {
                         const float2 ff = make_float2(fi, fi);
-                        x[0] = mul2(f2(r[0], r[1]), mul2(ff, make_float2(u.x, u.y)));
-                        x[1] = mul2(f2(r[2], r[3]), mul2(ff, make_float2(u.z, u.w)));
-                        x[2] = mul2(f2(r[4], r[5]), mul2(ff, make_float2(v.x, v.y)));
-                        x[3] = mul2(f2(r[6], r[7]), mul2(ff, make_float2(v.z, v.w)));
+                        x[0] = mul2(f2(r[8 * q], r[8 * q + 1]), mul2(ff, make_float2(u.x, u.y)));
+                        x[1] = mul2(f2(r[8 * q + 2], r[8 * q + 3]), mul2(ff, make_float2(u.z, u.w)));
+                        x[2] = mul2(f2(r[8 * q + 4], r[8 * q + 5]), mul2(ff, make_float2(v.x, v.y)));
+                        x[3] = mul2(f2(r[8 * q + 6], r[8 * q + 7]), mul2(ff, make_float2(v.z, v.w)));
                     } else {
                         auto D = [&](int j) { return f * expf((gh - gt[6 * C + cq + j]) + (gl - gt[7 * C + cq + j])); };
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = mul2(f2(r[2 * j], r[2 * j + 1]), make_float2(D(2 * j), D(2 * j + 1)));
+                        for (int j = 0; j < 4; ++j) x[j] = mul2(f2(r[8 * q + 2 * j], r[8 * q + 2 * j + 1]), make_float2(D(2 * j), D(2 * j + 1)));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         x[j].x = cq + 2 * j <= last ? x[j].x : 0.f;
                         x[j].y = cq + 2 * j + 1 <= last ? x[j].y : 0.f;
                     }
-                    if (!isP && (cq >> 4) == (i >> 4)) {   // the row's diagonal block: to fp32, times beta
+                    if (!isP && (cq >> 4) == (i >> 4)) {
+                        // the row's diagonal block: to fp32, times beta in its 8-row halves (which are
+                        // solved), plain in the quarter below the diagonal (which enters the block rule)
+                        const float be = (cq >> 3) == (i >> 3) ? gt[i] : 1.f;
                         float* dd = diag + (i >> 4) * 16 * LDD + (i & 15) * LDD + (cq & 15);
                         *reinterpret_cast<float4*>(dd) = make_float4(be * x[0].x, be * x[0].y, be * x[1].x, be * x[1].y);
                         *reinterpret_cast<float4*>(dd + 4) = make_float4(be * x[2].x, be * x[2].y, be * x[3].x, be * x[3].y);
@@ -691,43 +716,72 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                         sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
                     }
                 }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(g_read);
             }
             named_bar_sync(2, 256);
             if (pw < 4) {
-                // diagonal block `pw`: column cc of its inverse by forward substitution, a lane each
-                // (both half-warps; one stores the high parts, one the low)
-                const int cc = lane & 15;
-                const float* A = diag + pw * 16 * LDD;
-                float2 x[8];
+                // The 16-row diagonal block `pw`, in place in fp32: its two 8-row halves by forward
+                // substitution, a lane per column, then the block rule, two outputs a lane.
+                const int cc = lane & 7, rr = lane >> 3, hb = rr & 1;
+                float* B = diag + pw * 16 * LDD;
+                float* A = B + hb * 8 * (LDD + 1);
+                float x[8];
 #pragma unroll
-                for (int ii = 0; ii < 16; ++ii) {
-                    float2 s0v = make_float2(ii == cc ? 1.f : 0.f, 0.f), s1v = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int j = 0; j < ii; j += 4) {
-                        const float4 q = *reinterpret_cast<const float4*>(A + ii * LDD + j);
-                        if (j + 1 < ii) s0v = fma2(make_float2(-q.x, -q.y), x[j / 2], s0v);
-                        else s0v.x = fmaf(-q.x, x[j / 2].x, s0v.x);
-                        if (j + 3 < ii) s1v = fma2(make_float2(-q.z, -q.w), x[j / 2 + 1], s1v);
-                        else if (j + 2 < ii) s1v.x = fmaf(-q.z, x[j / 2 + 1].x, s1v.x);
+                for (int ii = 0; ii < 8; ++ii) {
+                    float u = ii == cc ? 1.f : 0.f, v = 0.f;
+                    if (ii > 0) {
+                        const float4 q = *reinterpret_cast<const float4*>(A + ii * LDD);
+                        u = fmaf(-q.x, x[0], u);
+                        if (ii > 1) v = fmaf(-q.y, x[1], v);
+                        if (ii > 2) u = fmaf(-q.z, x[2], u);
+                        if (ii > 3) v = fmaf(-q.w, x[3], v);
                     }
-                    const float v = (s0v.x + s0v.y) + (s1v.x + s1v.y);
-                    if (ii & 1) x[ii / 2].y = v;
-                    else x[ii / 2].x = v;
+                    if (ii > 4) {
+                        const float4 q = *reinterpret_cast<const float4*>(A + ii * LDD + 4);
+                        u = fmaf(-q.x, x[4], u);
+                        if (ii > 5) v = fmaf(-q.y, x[5], v);
+                        if (ii > 6) u = fmaf(-q.z, x[6], u);
+                    }
+                    x[ii] = u + v;
                 }
-                const float be = gt[16 * pw + cc];
-                const uint32_t o0 = tb + (lane >> 4) * SLAB;
+                const float be = gt[16 * pw + 8 * hb + cc];
+                __syncwarp();                        // the half's rows are read
+                if (lane < 16) {
 #pragma unroll
-                for (int ii = 0; ii < 16; ii += 2) {
-                    uint32_t hh, ll;
-                    split2(be * x[ii / 2].x, be * x[ii / 2].y, hh, ll);
-                    const uint32_t w = lane < 16 ? hh : ll;
-                    const int row = 16 * pw + ii, col = 16 * pw + cc;
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(sw(o0, row, col >> 3) + (col & 7) * 2), "h"((uint16_t)w) : "memory");
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(sw(o0, row + 1, col >> 3) + (col & 7) * 2), "h"((uint16_t)(w >> 16)) : "memory");
+                    for (int ii = 0; ii < 8; ++ii) A[ii * LDD + cc] = be * x[ii];
                 }
+                __syncwarp();
+                float w[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {        // rows rr and rr + 4 of C Z
+                    const float z = B[k * LDD + cc];
+                    w[0] = fmaf(B[(8 + rr) * LDD + k], z, w[0]);
+                    w[1] = fmaf(B[(12 + rr) * LDD + k], z, w[1]);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {        // and of -Y (C Z)
+                    const float z = __shfl_sync(~0u, w[k >> 2], (k & 3) * 8 + cc);
+                    y[0] = fmaf(-B[(8 + rr) * LDD + 8 + k], z, y[0]);
+                    y[1] = fmaf(-B[(12 + rr) * LDD + 8 + k], z, y[1]);
+                }
+                __syncwarp();                        // C is read
+                B[(8 + rr) * LDD + cc] = y[0];
+                B[(12 + rr) * LDD + cc] = y[1];
+                __syncwarp();
+                const int row = lane >> 1, col = (lane & 1) * 8;
+                uint32_t h8[4], l8[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float4 q = *reinterpret_cast<const float4*>(B + row * LDD + col + 4 * e);
+                    split2(q.x, q.y, h8[2 * e], l8[2 * e]);
+                    split2(q.z, q.w, h8[2 * e + 1], l8[2 * e + 1]);
+                }
+                const uint32_t o = sw(tb, 16 * pw + row, 2 * pw + (lane & 1));
+                sts4(o, h8[0], h8[1], h8[2], h8[3]);
+                sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
             }
             named_bar_sync(2, 256);
             {
@@ -736,16 +790,21 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 const int o = 32 * (pw >> 1), n0 = (pw & 1) * 8;
                 if (pw < 4) block_rule<16>(tb, o + 16, o + 16, o, n0, x);
                 named_bar_sync(2, 256);
-                if (pw < 4) put_fragment(tb, o + 16, o + n0, x);
+                if (pw < 4) put_fragment(tb, o + 16, o + n0, SLAB, x, 1.f);
             }
             named_bar_sync(2, 256);
             {
-                // 32 -> 64: 16 rows by eight columns a warp
-                float x[4];
-                const int r0 = 32 + (pw >> 2) * 16, n0 = (pw & 3) * 8;
-                block_rule<32>(tb, r0, 32, 0, n0, x);
+                // 32 -> 64: 16 rows by eight columns a warp, Y C by way of shared memory
+                const int r0 = (pw >> 2) * 16, n0 = (pw & 3) * 8;
+                const uint32_t wb = s0 + L::W_OFF;
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                block_product<32>(tb, 32 + r0, 32, SLAB, tb, 32, n0, x);
+                put_fragment(wb, r0, n0, 64, x, -1.f);
                 named_bar_sync(2, 256);
-                put_fragment(tb, r0, n0, x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = 0.f;
+                block_product<32>(wb, r0, 0, 64, tb, 0, n0, x);
+                put_fragment(tb, 32 + r0, n0, SLAB, x, 1.f);
             }
             fence_proxy_async_smem();
             __syncwarp();
