@@ -661,66 +661,76 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
         const int i = (quarter & 1) * 32 + lane;      // row of the chunk
         const bool isP = quarter >= 2;
         float* diag = reinterpret_cast<float*>(sm + L::D_OFF);
+        // Of the warps' 32 x 32 pieces the one above the diagonal is zero, once and for all, the one below
+        // needs no mask.
+        const bool above = !(quarter & 1) && c0 > 0, below = (quarter & 1) && c0 == 0;
+        if (above)
+            for (int x = 0; x < NV * 2 * 4; ++x)
+                sts4(sw(s0 + L::TP_OFF + (x >> 3) * 4 * SLAB + (isP ? 2 * SLAB : 0) + ((x >> 2) & 1) * SLAB, i, 4 + (x & 3)), 0u, 0u, 0u, 0u);
         for (int m = 0; m < n; ++m) {
             const float* gt = reinterpret_cast<const float*>(sm + L::G_OFF + (m % NG) * L::GB);
             const uint32_t tb = s0 + L::TP_OFF + (m % NV) * 4 * SLAB, pb = tb + 2 * SLAB;
             wait(&gt_ready[m % NG], (m / NG) & 1, abort_flag, status, ERR_PREP);
             wait(g_full, m & 1, abort_flag, status, ERR_PREP);
             tc_fence_after();
-            {
+            if (!above) {
                 // tensor-memory lanes 0-63: rows of L; 64-127: rows of P
                 const bool near = gt[4 * C] != 0.f;
                 const float f = isP ? a.scale : 1.f;
-                const int last = isP ? i : i - 1;
-                const float fi = f * gt[4 * C + i], gh = gt[6 * C + i], gl = gt[7 * C + i];
+                const int last = below ? C : isP ? i : i - 1;
+                const float fi = f * gt[4 * C + i];
 #pragma unroll 1
                 for (int c = c0; c < c0 + 32; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(tm + ((uint32_t)(quarter * 32) << 16) + L::tG + c, r);
-                tmem_wait_ld();
+                    uint32_t r[16];
+                    tmem_ld16(tm + ((uint32_t)(quarter * 32) << 16) + L::tG + c, r);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {          // eight columns at a time
-                    const int cq = c + 8 * q;
-                    const float* wf = gt + 5 * C + cq;
-                    const float4 u = *reinterpret_cast<const float4*>(wf), v = *reinterpret_cast<const float4*>(wf + 4);
-                    float2 x[4];
-                    if (near) {
-                        const float2 ff = make_float2(fi, fi);
-                        x[0] = mul2(f2(r[8 * q], r[8 * q + 1]), mul2(ff, make_float2(u.x, u.y)));
-                        x[1] = mul2(f2(r[8 * q + 2], r[8 * q + 3]), mul2(ff, make_float2(u.z, u.w)));
-                        x[2] = mul2(f2(r[8 * q + 4], r[8 * q + 5]), mul2(ff, make_float2(v.x, v.y)));
-                        x[3] = mul2(f2(r[8 * q + 6], r[8 * q + 7]), mul2(ff, make_float2(v.z, v.w)));
-                    } else {
-                        auto D = [&](int j) { return f * expf((gh - gt[6 * C + cq + j]) + (gl - gt[7 * C + cq + j])); };
+                    for (int q = 0; q < 2; ++q) {          // eight columns at a time
+                        const int cq = c + 8 * q;
+                        float2 x[4];
+                        if (near) {
+                            const float4 u = *reinterpret_cast<const float4*>(gt + 5 * C + cq);
+                            const float4 v = *reinterpret_cast<const float4*>(gt + 5 * C + cq + 4);
+                            const float2 ff = make_float2(fi, fi);
+                            x[0] = mul2(f2(r[8 * q], r[8 * q + 1]), mul2(ff, make_float2(u.x, u.y)));
+                            x[1] = mul2(f2(r[8 * q + 2], r[8 * q + 3]), mul2(ff, make_float2(u.z, u.w)));
+                            x[2] = mul2(f2(r[8 * q + 4], r[8 * q + 5]), mul2(ff, make_float2(v.x, v.y)));
+                            x[3] = mul2(f2(r[8 * q + 6], r[8 * q + 7]), mul2(ff, make_float2(v.z, v.w)));
+                        } else {
+                            const float gh = gt[6 * C + i], gl = gt[7 * C + i];
+                            auto D = [&](int j) { return f * expf((gh - gt[6 * C + cq + j]) + (gl - gt[7 * C + cq + j])); };
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = mul2(f2(r[8 * q + 2 * j], r[8 * q + 2 * j + 1]), make_float2(D(2 * j), D(2 * j + 1)));
-                    }
+                            for (int j = 0; j < 4; ++j)
+                                x[j] = mul2(f2(r[8 * q + 2 * j], r[8 * q + 2 * j + 1]), make_float2(D(2 * j), D(2 * j + 1)));
+                        }
+                        if (!below) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x[j].x = cq + 2 * j <= last ? x[j].x : 0.f;
-                        x[j].y = cq + 2 * j + 1 <= last ? x[j].y : 0.f;
-                    }
-                    if (!isP && (cq >> 4) == (i >> 4)) {
-                        // the row's diagonal block: to fp32, times beta in its 8-row halves (which are
-                        // solved), plain in the quarter below the diagonal (which enters the block rule)
-                        const float be = (cq >> 3) == (i >> 3) ? gt[i] : 1.f;
-                        float* dd = diag + (i >> 4) * 16 * LDD + (i & 15) * LDD + (cq & 15);
-                        *reinterpret_cast<float4*>(dd) = make_float4(be * x[0].x, be * x[0].y, be * x[1].x, be * x[1].y);
-                        *reinterpret_cast<float4*>(dd + 4) = make_float4(be * x[2].x, be * x[2].y, be * x[3].x, be * x[3].y);
-                    } else {
-                        uint32_t h8[4], l8[4];
+                            for (int j = 0; j < 4; ++j) {
+                                x[j].x = cq + 2 * j <= last ? x[j].x : 0.f;
+                                x[j].y = cq + 2 * j + 1 <= last ? x[j].y : 0.f;
+                            }
+                        }
+                        if (!isP && !below && (cq >> 4) == (i >> 4)) {
+                            // the row's diagonal block: to fp32, times beta in its 8-row halves (which are
+                            // solved), plain in the quarter below the diagonal (which enters the block rule)
+                            const float be = (cq >> 3) == (i >> 3) ? gt[i] : 1.f;
+                            float* dd = diag + (i >> 4) * 16 * LDD + (i & 15) * LDD + (cq & 15);
+                            *reinterpret_cast<float4*>(dd) = make_float4(be * x[0].x, be * x[0].y, be * x[1].x, be * x[1].y);
+                            *reinterpret_cast<float4*>(dd + 4) = make_float4(be * x[2].x, be * x[2].y, be * x[3].x, be * x[3].y);
+                        } else {
+                            uint32_t h8[4], l8[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) split2(x[e], h8[e], l8[e]);
-                        const uint32_t o = sw(isP ? pb : tb, i, cq / 8);
-                        sts4(o, h8[0], h8[1], h8[2], h8[3]);
-                        sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
+                            for (int e = 0; e < 4; ++e) split2(x[e], h8[e], l8[e]);
+                            const uint32_t o = sw(isP ? pb : tb, i, cq / 8);
+                            sts4(o, h8[0], h8[1], h8[2], h8[3]);
+                            sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
+                        }
                     }
                 }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(g_read);
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(g_read);
             named_bar_sync(2, 256);
             if (pw < 4) {
                 // The 16-row diagonal block `pw`, in place in fp32: its two 8-row halves by forward
