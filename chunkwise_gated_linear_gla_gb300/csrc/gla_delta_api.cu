@@ -239,7 +239,7 @@ gla_status bwd_chunks(const gla_delta_bwd_params* p, const DeltaBwdPlan& pl, int
     g.part_q = shared ? reinterpret_cast<float*>(ws + pl.off_pq) : nullptr;
     g.part_k = shared ? reinterpret_cast<float*>(ws + pl.off_pk) : nullptr;
     g.dlog_g = p->grad_log_g; g.dbeta = p->grad_beta;
-    g.B = p->B; g.H = p->H; g.Hk = p->Hk; g.T = p->T; g.dk = p->dk; g.dv = p->dv; g.nch = pl.nch; g.scale = p->scale;
+    g.B = p->B; g.H = p->H; g.Hk = p->Hk; g.T = p->T; g.dk = p->dk; g.dv = p->dv; g.nch = pl.nch; g.sms = sms; g.scale = p->scale;
     if (e == cudaSuccess) e = launch_delta_grads(g, status, stream);
     if (e == cudaSuccess && shared) {
         DeltaBwdSum u;

@@ -15,7 +15,9 @@
 // dS^T (both halves of the result belong to one row and are added at the end), [W; M] on the left
 // of K, and transposed, hi over lo, on the left of [Q; K].
 //
-// One CTA per chunk and head. Bound by its loads: 240 KB per chunk at dk = dv = 128.
+// One persistent CTA per SM (the operands and accumulators fill its shared and tensor memory) walks
+// the chunks; the next chunk's dO, dV, U and S are loaded as soon as this one's are used. Bound by its
+// loads, 240 KB per chunk at dk = dv = 128, and the latency of its own steps, about equally.
 #include "gla_delta_dev.cuh"
 #include "gla_delta_internal.h"
 
@@ -42,10 +44,9 @@ struct GL {
     static constexpr int R_OFF = G_OFF + 8 * C * 4;           // row sums 4 x 64, state sums 4 x 64, 8 partials
     static constexpr int BAR_OFF = R_OFF + 8 * C * 4 + 64;
     static constexpr int SMEM = BAR_OFF + 128 + 1024;
-    static constexpr int W_OFF = XA_OFF;                      // [W; M] in two parts, once dO and dV are used
-    static constexpr int E_OFF = XB_OFF;                      // dK's partial rows (fp32), over dV_lo
-    static constexpr int LDE = DK + 4;
-    static_assert(64 * LDE * 4 <= 8 * SLAB, "exchange buffer over dV_lo and U");
+    static constexpr int W_OFF = XB_OFF;                      // [W; M] in two parts, once dV_lo is used
+    static constexpr int E_OFF = XB_OFF;                      // then dK's partial rows (fp32), when W is used
+    static_assert(64 * DK * 4 <= 4 * SLAB, "exchange buffer");
     static constexpr int t1 = 0, t2 = 128, t3 = 256, tH = 384, tH2 = 0;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -70,27 +71,27 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     const uint32_t s0 = smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR_OFF);
     uint64_t* b_qk = bar;        // Q, K, gates loaded
-    uint64_t* b_x = bar + 1;     // dO, dV, U loaded
-    uint64_t* b_s = bar + 2;     // S loaded
-    uint64_t* b_d = bar + 3;     // dS loaded
-    uint64_t* m_1 = bar + 4;     // products with U^T and S^T done
-    uint64_t* m_3 = bar + 5;     // products with dS^T done
-    uint64_t* m_h = bar + 6;     // products of W and M done
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 7);
-    const Abort abort_flag(bar + 8);
+    uint64_t* b_xa = bar + 1;    // dO, dV loaded
+    uint64_t* b_xb = bar + 2;    // dV_lo loaded
+    uint64_t* b_u = bar + 3;     // U loaded
+    uint64_t* b_s = bar + 4;     // S loaded
+    uint64_t* b_d = bar + 5;     // dS loaded
+    uint64_t* m_1 = bar + 6;     // products with U^T and S^T done
+    uint64_t* m_3 = bar + 7;     // products with dS^T done
+    uint64_t* m_h = bar + 8;     // products of W and M done
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 9);
+    const Abort abort_flag(bar + 10);
     float* gt = reinterpret_cast<float*>(sm + L::G_OFF);
     float* rs = reinterpret_cast<float*>(sm + L::R_OFF);        // [4][64] row sums
     float* ss = rs + 4 * C;                                     // [4][64] k . (l U dS^T)
     float* ip = ss + 4 * C;                                     // [8] warps' parts of <dS, S>
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid % 32;
-    const int c = blockIdx.x % a.nch, bh = blockIdx.x / a.nch;
-    const int b = bh / a.H, h = bh % a.H, bk = b * a.Hk + h / (a.H / a.Hk);
-    const int t0 = c * C, at = blockIdx.x;
     const int ntile = (a.dv + 127) / 128;
+    const int total = a.B * a.H * a.nch;
 
     if (tid == 0) {
-        for (int i = 0; i < 7; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < 9; ++i) mbar_init(&bar[i], 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -98,18 +99,48 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
         tmem_alloc(holder, 512);
         tmem_relinquish();
     }
-    for (int i = tid; i < 2 * SLAB / 16; i += NT)
-        *reinterpret_cast<uint4*>(sm + L::XB_OFF + (i / (SLAB / 16)) * 2 * SLAB + i % (SLAB / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    auto zero_slabs = [&]() {
+        for (int i = tid; i < 2 * SLAB / 16; i += NT)
+            *reinterpret_cast<uint4*>(sm + L::XB_OFF + (i / (SLAB / 16)) * 2 * SLAB + i % (SLAB / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    };
+    zero_slabs();
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *holder;
 
+    int it = 0, cnt = 0;                // chunks done, and tiles of dv: the barriers' phases
+    for (int at = blockIdx.x; at < total; at += gridDim.x, ++it) {
+    const int c = at % a.nch, bh = at / a.nch, t0 = c * C;
+    const int b = bh / a.H, h = bh % a.H, bk = b * a.Hk + h / (a.H / a.Hk);
+    auto load_s = [&](int chunk, int dv0) {
+        mbar_arrive_expect_tx(b_s, 2 * L::SB);
+#pragma unroll
+        for (int i = 0; i < L::NS; ++i) {
+            tma_load_3d(sm + L::S_OFF + i * 2 * SLAB, &mp.sh, b_s, 64 * i, dv0, chunk);
+            tma_load_3d(sm + L::S_OFF + L::SB + i * 2 * SLAB, &mp.sl, b_s, 64 * i, dv0, chunk);
+        }
+    };
+    // (tiles of dv that end inside the pair of slabs are filled with zeros)
+    auto load_xa = [&](int chunk, int dv0) {
+        mbar_arrive_expect_tx(b_xa, 4 * SLAB);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            tma_load_3d(sm + L::XA_OFF + 2 * i * SLAB, &mp.dO, b_xa, dv0 + 64 * i, chunk % a.nch * C, chunk / a.nch);
+            tma_load_3d(sm + L::XA_OFF + (2 * i + 1) * SLAB, &mp.xh, b_xa, dv0 + 64 * i, chunk % a.nch * C, chunk / a.nch);
+        }
+    };
+    auto load_u = [&](int chunk, int dv0) {
+        mbar_arrive_expect_tx(b_u, 4 * SLAB);
+        tma_load_3d(sm + L::U_OFF, &mp.uh, b_u, 0, dv0, chunk);
+        tma_load_3d(sm + L::U_OFF + 2 * SLAB, &mp.ul, b_u, 0, dv0, chunk);
+    };
+    const bool more = at + (int)gridDim.x < total;
     float inner = 0.f;
-    for (int vt = 0; vt < ntile; ++vt) {
+    for (int vt = 0; vt < ntile; ++vt, ++cnt) {
         const int dv0 = vt * 128;
-        const uint32_t ph = vt & 1;
+        const uint32_t ph = cnt & 1;
         if (warp == 0) {
             if (lane == 0) {
                 if (vt == 0) {
@@ -121,21 +152,14 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                     }
                     bulk_load(gt, a.gates + (size_t)at * 8 * C, 8 * C * 4, b_qk);
                 }
-                // (tiles of dv that end inside the pair of slabs are filled with zeros)
-                mbar_arrive_expect_tx(b_x, 10 * SLAB);
+                mbar_arrive_expect_tx(b_xb, 2 * SLAB);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    tma_load_3d(sm + L::XA_OFF + 2 * i * SLAB, &mp.dO, b_x, dv0 + 64 * i, t0, bh);
-                    tma_load_3d(sm + L::XA_OFF + (2 * i + 1) * SLAB, &mp.xh, b_x, dv0 + 64 * i, t0, bh);
-                    tma_load_3d(sm + L::XB_OFF + (2 * i + 1) * SLAB, &mp.xl, b_x, dv0 + 64 * i, t0, bh);
-                }
-                tma_load_3d(sm + L::U_OFF, &mp.uh, b_x, 0, dv0, at);
-                tma_load_3d(sm + L::U_OFF + 2 * SLAB, &mp.ul, b_x, 0, dv0, at);
-                mbar_arrive_expect_tx(b_s, 2 * L::SB);
-#pragma unroll
-                for (int i = 0; i < L::NS; ++i) {
-                    tma_load_3d(sm + L::S_OFF + i * 2 * SLAB, &mp.sh, b_s, 64 * i, dv0, at);
-                    tma_load_3d(sm + L::S_OFF + L::SB + i * 2 * SLAB, &mp.sl, b_s, 64 * i, dv0, at);
+                for (int i = 0; i < 2; ++i)
+                    tma_load_3d(sm + L::XB_OFF + (2 * i + 1) * SLAB, &mp.xl, b_xb, dv0 + 64 * i, t0, bh);
+                if (it == 0 || vt > 0) {              // (else they are there or on their way)
+                    load_xa(at, dv0);
+                    load_u(at, dv0);
+                    load_s(at, dv0);
                 }
             }
             __syncwarp();
@@ -143,7 +167,8 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             const uint64_t dU = sdesc(s0 + L::U_OFF, 2 * SLAB, 1024, kSwizzle128);
             const uint64_t dS = sdesc(s0 + L::S_OFF, 2 * SLAB, 1024, kSwizzle128);
             const uint32_t id1 = idesc_bf16(128, 64, false, true), id2 = idesc_bf16(128, DK, false, true);
-            wait(b_x, ph, abort_flag, status, ERR_LOAD);
+            wait(b_xa, ph, abort_flag, status, ERR_LOAD);
+            wait(b_u, ph, abort_flag, status, ERR_LOAD);
             __syncwarp();
             if (elect_one()) {
 #pragma unroll
@@ -151,7 +176,6 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                     const uint64_t o = ((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4, r = (kk * 2048) >> 4;
                     mma_ss(tm + L::t1, dXa + o, dU + r, id1, vt > 0 || kk > 0);
                     mma_ss(tm + L::t1, dXa + o, dU + (2 * SLAB >> 4) + r, id1, 1);
-                    mma_ss(tm + L::t1, dXb + o, dU + r, id1, 1);
                 }
             }
             wait(b_s, ph, abort_flag, status, ERR_LOAD);
@@ -162,33 +186,45 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                     const uint64_t o = ((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4, r = (kk * 2048) >> 4;
                     mma_ss(tm + L::t2, dXa + o, dS + r, id2, vt > 0 || kk > 0);
                     mma_ss(tm + L::t2, dXa + o, dS + (L::SB >> 4) + r, id2, 1);
+                }
+            }
+            wait(b_xb, ph, abort_flag, status, ERR_LOAD);
+            __syncwarp();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint64_t o = ((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4, r = (kk * 2048) >> 4;
+                    mma_ss(tm + L::t1, dXb + o, dU + r, id1, 1);
                     mma_ss(tm + L::t2, dXb + o, dS + r, id2, 1);
                 }
                 mma_commit(m_1);
             }
             __syncwarp();
         }
-        // <dS, S> of this tile: dS from global memory, S from the tiles
-        wait(b_s, ph, abort_flag, status, ERR_LOAD);
-        {
-            const int rows = min(128, a.dv - dv0);
-            const uint4* dh = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_hi) + ((size_t)at * a.dv + dv0) * DK);
-            const uint4* dl = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_lo) + ((size_t)at * a.dv + dv0) * DK);
-#pragma unroll 4
-            for (int i = tid; i < rows * (DK / 8); i += NT) {
-                const int r = i / (DK / 8), p = i % (DK / 8);
-                const uint4 x = dh[i], y = dl[i];
-                const uint32_t xx[4] = {x.x, x.y, x.z, x.w}, yy[4] = {y.x, y.y, y.z, y.w};
-                const uint32_t o = s0 + L::S_OFF + (p >> 3) * 2 * SLAB + r * 128 + (((p & 7) ^ (r & 7)) << 4);
-                float u[8], v[8];
-                load8(o, u);
-                load8(o + L::SB, v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    inner = fmaf(u[2 * e] + v[2 * e], bf_lo(xx[e]) + bf_lo(yy[e]), inner);
-                    inner = fmaf(u[2 * e + 1] + v[2 * e + 1], bf_hi(xx[e]) + bf_hi(yy[e]), inner);
+        if (warp == 1) {
+            // dS on its way into L2 (more tiles than these would only queue before the loads)
+            if (elect_one())
+                for (int i = 0; i < L::NS; ++i) {
+                    prefetch_l2_tile_3d(&mp.dh, 64 * i, dv0, at);
+                    prefetch_l2_tile_3d(&mp.dl, 64 * i, dv0, at);
                 }
-            }
+            __syncwarp();
+        }
+        // S of this tile to registers, for <dS, S> (dS takes its place)
+        constexpr int NP = 128 * DK / 8 / NT;        // pieces of eight keys a thread
+        auto piece = [&](int p) {
+            const int i = tid + p * NT, r = i / (DK / 8), k = i % (DK / 8);
+            return s0 + L::S_OFF + (k >> 3) * 2 * SLAB + r * 128 + (((k & 7) ^ (r & 7)) << 4);
+        };
+        float sv[NP][8];
+        wait(b_s, ph, abort_flag, status, ERR_LOAD);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            float v[8];
+            load8(piece(p), sv[p]);
+            load8(piece(p) + L::SB, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sv[p][e] += v[e];
         }
         wait(m_1, ph, abort_flag, status, ERR_MMA);
         __syncthreads();            // S is read by everyone: dS may take its place
@@ -200,6 +236,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                     tma_load_3d(sm + L::S_OFF + i * 2 * SLAB, &mp.dh, b_d, 64 * i, dv0, at);
                     tma_load_3d(sm + L::S_OFF + L::SB + i * 2 * SLAB, &mp.dl, b_d, 64 * i, dv0, at);
                 }
+                if (more && vt == ntile - 1) load_xa(at + gridDim.x, 0);   // (the next chunk's)
             }
             __syncwarp();
             const uint64_t dU = sdesc(s0 + L::U_OFF, 2 * SLAB, 1024, kSwizzle128);   // tokens along M: U on U_lo
@@ -218,6 +255,15 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             }
             __syncwarp();
         }
+        wait(b_d, ph, abort_flag, status, ERR_LOAD);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            float u[8], v[8];
+            load8(piece(p), u);
+            load8(piece(p) + L::SB, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) inner = fmaf(sv[p][e], u[e] + v[e], inner);
+        }
         if (vt + 1 < ntile) {       // one set of tiles: the next load waits for these products
             wait(m_3, ph, abort_flag, status, ERR_MMA);
             __syncthreads();
@@ -230,7 +276,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     const bool low = row < 64;
     const uint32_t lb = (uint32_t)(quarter * 32) << 16;
     tc_fence_after();
-    wait(b_qk, 0, abort_flag, status, ERR_LOAD);
+    wait(b_qk, it & 1, abort_flag, status, ERR_LOAD);
     {
         const int c0 = hf * 32;
         uint32_t r[32];
@@ -305,16 +351,22 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
         }
         __syncwarp();
     }
-    wait(m_3, (ntile - 1) & 1, abort_flag, status, ERR_MMA);
-    wait(m_h, 0, abort_flag, status, ERR_MMA);
+    wait(m_3, (cnt - 1) & 1, abort_flag, status, ERR_MMA);
+    wait(m_h, it & 1, abort_flag, status, ERR_MMA);
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && more) {
+        // U and dS are used (and everyone has read dS): the next chunk's U and S take their place
+        load_u(at + gridDim.x, 0);
+        load_s(at + gridDim.x, 0);
+    }
     {
         // one row and half of the keys a thread
         const float e = gt[C + i], l = gt[2 * C + i];
         const float f2s = low ? a.scale * e : -e;
         float sum = 0.f, st = 0.f;
-        float* ex = reinterpret_cast<float*>(sm + L::E_OFF) + i * L::LDE;
+        float* ex = reinterpret_cast<float*>(sm + L::E_OFF) + i * DK;   // groups of four in another order by row
+        auto slot = [&](int k) { return ((k >> 2) ^ (i & 7)) * 4; };
         const bool in = t0 + i < a.T;
         const size_t orow = ((size_t)bh * a.T + t0 + i) * DK;
         auto store = [&](void* out, float* part, int k, const float (&x)[16]) {
@@ -363,7 +415,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                 store(a.dq, a.part_q, k, x);
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4*>(ex + k + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4*>(ex + slot(k + j)) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
             }
         }
         rs[((low ? 0 : 1) + 2 * hf) * C + i] = sum;
@@ -378,7 +430,11 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                 const int k = hf * (DK / 2) + kc;
                 float x[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = col[kc + j] + ex[k + j];
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(ex + slot(k + j));
+                    x[j] = col[kc + j] + f.x; x[j + 1] = col[kc + j + 1] + f.y;
+                    x[j + 2] = col[kc + j + 2] + f.z; x[j + 3] = col[kc + j + 3] + f.w;
+                }
                 store(a.dk_out, a.part_k, k, x);
             }
         }
@@ -409,6 +465,13 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             if (t0 + p + 1 < a.T) out[1] = y - x0 + s;
         }
     }
+    __syncthreads();        // the exchange is read
+    zero_slabs();
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();        // everything of this chunk is read: the next one's loads may land
+    tc_fence_after();
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -430,7 +493,8 @@ cudaError_t launch_dk(const DeltaGrads& a, const GMaps& m, int* status, cudaStre
     using L = GL<DK>;
     cudaError_t e = cudaFuncSetAttribute(gla_delta_grads_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
-    gla_delta_grads_kernel<DK><<<(unsigned)((long long)a.B * a.H * a.nch), NT, L::SMEM, s>>>(a, m, status);
+    const long long n = (long long)a.B * a.H * a.nch;
+    gla_delta_grads_kernel<DK><<<(unsigned)(n < a.sms ? n : a.sms), NT, L::SMEM, s>>>(a, m, status);
     return cudaGetLastError();
 }
 

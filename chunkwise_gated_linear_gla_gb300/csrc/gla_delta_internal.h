@@ -105,7 +105,7 @@ struct DeltaGrads {
     const void* d_hi; const void* d_lo; const void* x_hi; const void* x_lo;
     const float* log_g; const float* gates;
     void* dq; void* dk_out; float* part_q; float* part_k; float* dlog_g; void* dbeta;
-    int B, H, Hk, T, dk, dv, nch;
+    int B, H, Hk, T, dk, dv, nch, sms;
     float scale;
 };
 cudaError_t launch_delta_grads(const DeltaGrads& a, int* status, cudaStream_t s);
