@@ -125,24 +125,6 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
                 __syncwarp();
             }
             for (int m = max(0, issued - NST); m < issued; ++m) wait(&full[m % NST], (m / NST) & 1, abort_flag, status, ERR_TMA);
-        } else if (warp == 2) {
-            // L2 prefetch, two chunks ahead of the loads
-            for (int m = 0; m + NST < n; ++m) {
-                if (__any_sync(~0u, *abort_flag)) break;
-                if (m >= NST) wait(&empty[m % NST], ((m / NST) - 1) & 1, abort_flag, status, ERR_TMA);
-                __syncwarp();
-                const int c1 = chunk(m + NST), t1 = c1 * C, a1 = bh * n + c1;
-                if (elect_one()) {
-                    prefetch_l2_tile_4d(&mp.v, 0, t1, dv0 / 64, bh);
-                    if (blockIdx.x == 0) {
-                        prefetch_l2_tile_3d(&mp.t, 0, 0, a1);
-                        prefetch_l2_tile_4d(&mp.k, 0, t1, 0, bk);
-                        if (REV) prefetch_l2_tile_4d(&mp.q, 0, t1, 0, bk);
-                        if (REV) prefetch_l2_tile_3d(&mp.p, 0, 0, a1);
-                    }
-                }
-                __syncwarp();
-            }
         } else if (warp == 1) {
             const uint32_t id64 = idesc_bf16(128, 64, false, false), id64n = idesc_bf16(128, 64, false, true);
             const uint32_t idS = idesc_bf16(128, DK, false, true);

@@ -39,7 +39,6 @@ constexpr int NT = 768;
 constexpr int NKQ = 3;            // K and Q stages: chunk m's, the next one's (read by the prep), one in flight
 constexpr int NV = 2;             // V stages, T and P buffers
 constexpr int NG = 4;             // gate slots (the drain is the last reader)
-constexpr int PF = 4;             // chunks between a tile's prefetch into L2 and its load
 constexpr int DVT = 128;          // dv columns per CTA
 constexpr int LDD = 20;           // row stride of the fp32 diagonal blocks
 constexpr float kRange = 60.f;    // |G - G_mid| up to which the two-factor form of D is used
@@ -257,18 +256,6 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                     for (int i = 0; i < DK / 64; ++i) {
                         tma_load_3d(sb + 2 * i * SLAB, &mp.k, &kq_full[st], 64 * i, t0, bk);
                         tma_load_3d(sb + (2 * i + 1) * SLAB, &mp.q, &kq_full[st], 64 * i, t0, bk);
-                    }
-                    if (m + PF < n) {
-                        // on their way into L2, PF chunks ahead
-                        const int t1 = t0 + PF * C;
-                        if (blockIdx.x == 0) {
-#pragma unroll
-                            for (int i = 0; i < DK / 64; ++i) {
-                                prefetch_l2_tile_3d(&mp.k, 64 * i, t1, bk);
-                                prefetch_l2_tile_3d(&mp.q, 64 * i, t1, bk);
-                            }
-                        }
-                        if (!ident) prefetch_l2_tile_4d(&mp.v, 0, t1, dv0 / 64, bh);
                     }
                 }
                 __syncwarp();
@@ -830,40 +817,70 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
 }
 
 // The states entering the segments: S_in[0] = S0, S_in[s + 1] = M_s S_in[s] + S*_s, with each segment's
-// (S* [dk][dv], M [dk][dk]) side by side. A block owns 32 columns of one head; 1.5 us a segment.
+// (S* [dk][dv], M [dk][dk]) side by side. A block owns 32 columns of one head, a thread 4 x 4 (dk = 128)
+// or 2 x 4 values; the next segment's M is on its way to shared memory during a product.
 template <int DK>
 __global__ void __launch_bounds__(256) gla_delta_scan_kernel(const float* __restrict__ S0, const float* __restrict__ pair,
                                                              float* S_in, int dv, int nseg)
 {
-    __shared__ float s[2][DK][32];
-    const int bh = blockIdx.y, c = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
-    const bool in = col < dv;
+    constexpr int R = DK / 32;                   // rows a thread
+    extern __shared__ __align__(16) float scan_smem[];
+    float* M = scan_smem;                        // [2][DK][DK]
+    float* S = scan_smem + 2 * DK * DK;          // [2][DK][32]
+    const int bh = blockIdx.y, tid = threadIdx.x, r0 = tid / 8 * R, c = tid % 8 * 4, col = blockIdx.x * 32 + c;
+    const bool in = col < dv;                    // dv is a multiple of 16
     const size_t st = (size_t)DK * dv, step = st + DK * DK;
+    const float* pp = pair + (size_t)bh * (nseg - 1) * step;
     float* out = S_in + (size_t)bh * nseg * st + col;
-    for (int r = w; r < DK; r += 8) {
-        const float x = S0 && in ? S0[bh * st + (size_t)r * dv + col] : 0.f;
-        s[0][r][c] = x;
-        if (in) out[(size_t)r * dv] = x;
+    auto fetch = [&](int g) {
+        const float* m = pp + g * step + st;
+        const uint32_t d = smem_u32(M + (g & 1) * DK * DK);
+        for (int i = tid; i < DK * DK / 4; i += 256)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i * 16), "l"(m + i * 4) : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(0);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const float4 x = S0 && in ? *reinterpret_cast<const float4*>(S0 + bh * st + (size_t)(r0 + i) * dv + col) : zero;
+        *reinterpret_cast<float4*>(S + (r0 + i) * 32 + c) = x;
+        if (in) *reinterpret_cast<float4*>(out + (size_t)(r0 + i) * dv) = x;
     }
     for (int g = 0; g + 1 < nseg; ++g) {
+        float2 y[R][2];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const float4 x = in ? *reinterpret_cast<const float4*>(pp + g * step + (size_t)(r0 + i) * dv + col) : zero;
+            y[i][0] = make_float2(x.x, x.y);
+            y[i][1] = make_float2(x.z, x.w);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        const float* p = pair + ((size_t)bh * (nseg - 1) + g) * step;
-        const float* M = p + st;
-        float y[DK / 8];
-#pragma unroll
-        for (int i = 0; i < DK / 8; ++i) y[i] = in ? p[(size_t)(w + 8 * i) * dv + col] : 0.f;
+        if (g + 2 < nseg) fetch(g + 1);
+        const float* m = M + (g & 1) * DK * DK + r0 * DK;
+        const float* s = S + (g & 1) * DK * 32 + c;
+#pragma unroll 4
         for (int j = 0; j < DK; j += 4) {
-            const float x0 = s[g & 1][j][c], x1 = s[g & 1][j + 1][c], x2 = s[g & 1][j + 2][c], x3 = s[g & 1][j + 3][c];
+            float4 f[R];
 #pragma unroll
-            for (int i = 0; i < DK / 8; ++i) {
-                const float4 f = *reinterpret_cast<const float4*>(M + (size_t)(w + 8 * i) * DK + j);
-                y[i] = fmaf(f.x, x0, fmaf(f.y, x1, fmaf(f.z, x2, fmaf(f.w, x3, y[i]))));
+            for (int i = 0; i < R; ++i) f[i] = *reinterpret_cast<const float4*>(m + i * DK + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 x = *reinterpret_cast<const float4*>(s + (j + e) * 32);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float w = e == 0 ? f[i].x : e == 1 ? f[i].y : e == 2 ? f[i].z : f[i].w;
+                    y[i][0] = fma2(make_float2(w, w), make_float2(x.x, x.y), y[i][0]);
+                    y[i][1] = fma2(make_float2(w, w), make_float2(x.z, x.w), y[i][1]);
+                }
             }
         }
 #pragma unroll
-        for (int i = 0; i < DK / 8; ++i) {
-            s[(g + 1) & 1][w + 8 * i][c] = y[i];
-            if (in) out[(g + 1) * st + (size_t)(w + 8 * i) * dv] = y[i];
+        for (int i = 0; i < R; ++i) {
+            const float4 x = make_float4(y[i][0].x, y[i][0].y, y[i][1].x, y[i][1].y);
+            *reinterpret_cast<float4*>(S + ((g + 1) & 1) * DK * 32 + (r0 + i) * 32 + c) = x;
+            if (in) *reinterpret_cast<float4*>(out + (g + 1) * st + (size_t)(r0 + i) * dv) = x;
         }
     }
 }
@@ -895,7 +912,10 @@ cudaError_t launch_dk(const DeltaChunks& p, const FusedMaps& m, int* status, cud
         a.S_out = p.pair; a.out_seg = st + (long long)p.dk * p.dk; a.out_bh = a.out_seg * (p.nseg - 1);
         cudaError_t e = launch_pass<DK, false>(a, m, dim3(tiles + 1, BH, p.nseg - 1), s);
         if (e != cudaSuccess) return e;
-        gla_delta_scan_kernel<DK><<<dim3((p.dv + 31) / 32, BH), 256, 0, s>>>(p.S0, p.pair, p.seg_in, p.dv, p.nseg);
+        constexpr int smem = (2 * DK * DK + 2 * DK * 32) * 4;
+        e = cudaFuncSetAttribute(gla_delta_scan_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        gla_delta_scan_kernel<DK><<<dim3((p.dv + 31) / 32, BH), 256, smem, s>>>(p.S0, p.pair, p.seg_in, p.dv, p.nseg);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         a.S_in = p.seg_in; a.in_bh = st * p.nseg; a.in_seg = st;
