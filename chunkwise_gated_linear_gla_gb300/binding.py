@@ -608,19 +608,24 @@ def _delta_shapes(q, k, v, log_g, beta, S0):
     import torch
     if q.dim() != 4 or v.dim() != 4:
         _refuse("q and v have four dimensions: [B,Hk,T,dk] and [B,H,T,dv]")
-    B, Hk, T, dk = q.shape
-    H, dv = v.shape[1], v.shape[3]
-    code, dt, dev = _dtype_code(q, "q"), q.dtype, q.device
+    shape, dt, dev, f32 = q.shape, q.dtype, q.device, torch.float32
+    B, Hk, T, dk = shape
+    _, H, _, dv = v.shape
+    code = _dtype_code(q, "q")
     if Hk == 0 or H % Hk:
         _refuse(f"{H} heads of v do not divide over {Hk} of q and k")
-    _dense(q, (B, Hk, T, dk), dt, dev, "q")
-    _dense(k, (B, Hk, T, dk), dt, dev, "k")
-    _dense(v, (B, H, T, dv), dt, dev, "v")
-    _dense(beta, (B, H, T), dt, dev, "beta")
+    # one look at everything; what is wrong is told below
+    if not (k.shape == shape and v.shape == (B, H, T, dv) and beta.shape == (B, H, T) and k.dtype is dt and
+            v.dtype is dt and beta.dtype is dt and k.device == dev and v.device == dev and beta.device == dev and
+            q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and beta.is_contiguous()):
+        _dense(q, (B, Hk, T, dk), dt, dev, "q")
+        _dense(k, (B, Hk, T, dk), dt, dev, "k")
+        _dense(v, (B, H, T, dv), dt, dev, "v")
+        _dense(beta, (B, H, T), dt, dev, "beta")
     if log_g is not None:
-        _dense(log_g, (B, H, T), torch.float32, dev, "log_g")
+        _dense(log_g, (B, H, T), f32, dev, "log_g")
     if S0 is not None:
-        _dense(S0, (B, H, dk, dv), torch.float32, dev, "S0")
+        _dense(S0, (B, H, dk, dv), f32, dev, "S0")
     return B, H, Hk, T, dk, dv, code, dt, dev
 
 
@@ -644,9 +649,9 @@ def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, pa
         _refuse("an empty batch")
     lib = _lib or load()
     if O is None:
-        O = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+        O = torch.empty_like(v)
     if ST is None and want_state:
-        ST = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        ST = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if S0 is None else torch.empty_like(S0)
     p = gla_delta_params(_ptr(q), _ptr(k), _ptr(v), _ptr(log_g), _ptr(beta), _ptr(S0), _ptr(O), _ptr(ST),
                          B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path, None, 0, force_segments)
     n = 0 if T < 128 else _here_size(lib.gla_delta_fwd_workspace_size, p, dev)   # (two chunks at least: none below)

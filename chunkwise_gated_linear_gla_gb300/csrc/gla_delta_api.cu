@@ -70,14 +70,15 @@ gla_status plan_fwd(const gla_delta_params* p, DeltaPlan& pl)
     const bool ok = chunk_shape_ok(p->B, p->H, p->T, p->dk, p->dv, p->dtype);
     if (p->path == GLA_PATH_TENSOR && !ok) return GLA_ERR_UNSUPPORTED;
     if (p->T == 0 || !ok || p->path == GLA_PATH_SIMT) return GLA_OK;
-    if (p->path == GLA_PATH_AUTO && p->T < kDeltaChunkMinT) return GLA_OK;
+    const long long units = (long long)p->B * p->H * ((p->dv + kDvTile - 1) / kDvTile);
+    if (p->path == GLA_PATH_AUTO && p->T < (units < kDeltaFewTiles ? kDeltaChunkMinTFew : kDeltaChunkMinT)) return GLA_OK;
     pl.path = GLA_PATH_TENSOR;
     pl.nch = (p->T + kChunk - 1) / kChunk;
     int sms = 0;
     if (device_ready(&sms) != GLA_OK) sms = 152;
     const int BH = p->B * p->H;
     int n = p->force_segments > 0 ? p->force_segments
-                                  : choose_segments(BH * ((p->dv + kDvTile - 1) / kDvTile), BH, pl.nch, sms);
+                                  : choose_segments((int)units, BH, pl.nch, sms);
     if (n > pl.nch) n = pl.nch;
     if (n > 65535) n = 65535;
     pl.cps = (pl.nch + n - 1) / n;
