@@ -5,7 +5,9 @@
 //
 //     dw = sum over rows of z (.) x^,    dx = (z (.) w - x^ (sum z (.) w (.) x^) / N) / n.
 //
-// Bound by HBM: every row is read once and written once (backward: x and dy read, dx written).
+// Bound by HBM: every row is read once and written once (backward: x and dy read, dx written); the
+// rows of 8 x 2048 tokens, 16 + 16 heads of 128 bf16 values take 45 us forward, 5.9 TB/s, 0.88 of the
+// measured copy rate, with four blocks of 64 registers a thread per SM (three of 80: 54 us).
 // A row is LPR lanes of eight values (16 bytes in bf16); a thread keeps its row of the batch and
 // takes that token's heads one after the other, so a token's angles are formed once per block
 // (in shared memory) and four heads' loads are in flight at a time. Reads go through strides (a fused projection's
@@ -30,8 +32,8 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int VEC = 8;        // values per lane
-constexpr int UNR = 4;        // heads in flight per thread (backward: 2, of two rows each)
-constexpr long long kBlocksPerSm = 16;
+constexpr int UNR = 4;        // heads in flight per thread; the backward takes one at a time
+constexpr long long kBlocksPerSm = 4;
 
 struct QkArgs {
     const void* x[2]; void* y[2];                 // q, k (strided) and their results (dense)
@@ -129,9 +131,9 @@ __device__ __forceinline__ void rotate(float (&x)[VEC], const float (&cs)[VEC], 
 
 // One block: NT / LPR tokens by hsplit heads. BWD: dy, x -> dx and the weights' partials.
 template <typename E, int LPR, bool BWD>
-__global__ void __launch_bounds__(NT, BWD ? 2 : 3) gla_qk_norm_rope_kernel(QkArgs a)
+__global__ void __launch_bounds__(NT, BWD ? 3 : 4) gla_qk_norm_rope_kernel(QkArgs a)
 {
-    constexpr int RPB = NT / LPR, U = BWD ? 2 : UNR;
+    constexpr int RPB = NT / LPR, U = BWD ? 1 : UNR;
     __shared__ unsigned long long turns[LPR * VEC / 2];
     // cosines and sines of the block's tokens; the weights' sums take their place at the end
     __shared__ __align__(16) float trig[2][RPB][LPR * VEC / 2];
@@ -295,16 +297,16 @@ dim3 grid_of(const QkArgs& a, int lpr, int sms, bool bwd, int* hsplit)
 {
     const long long rows = NT / lpr, tg = ((long long)a.B * a.T + rows - 1) / rows;
     const int nh = a.heads[0] + a.heads[1];
-    // The heads are spread over blocks (each forms the token's angles again) until there are
-    // kBlocksPerSm blocks per SM, so that the last wave's idle SMs cost little: forward only, where
-    // blocks leave nothing behind.
+    // The heads are spread over blocks (each forms the token's angles again) until every SM has its
+    // four: more blocks pay the set-up more often (the layer's rows, 8 x 2048 tokens of 32 heads of 128
+    // values: 45 us so, 60 with four times as many blocks).
     int split = 1;
-    while (split < nh && tg * split < (bwd ? 4LL : kBlocksPerSm) * sms) split *= 2;
+    while (split < nh && tg * split < kBlocksPerSm * sms) split *= 2;
     if (split > nh) split = nh;
     *hsplit = (nh + split - 1) / split;
     const int gy = (nh + *hsplit - 1) / *hsplit;
     long long gx = tg;
-    const long long most = bwd ? 4LL * sms : 1LL << 30;   // backward: few blocks, few partials
+    const long long most = bwd ? kBlocksPerSm * sms : 1LL << 30;   // backward: few blocks, few partials
     if (gx > most) gx = most;
     return dim3((unsigned)gx, gy);
 }
