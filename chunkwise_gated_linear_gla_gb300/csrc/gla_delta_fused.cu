@@ -27,6 +27,7 @@
 // Warps: 0 TMA, 1 products, 3 gates, 4-11 chain, 12-15 drain of O, 16-23 prep. Reads K, Q, V once
 // and writes O once; bound by the chain's latency, with the tensor pipe busy 2800 cycles a chunk.
 #include "gla_delta_dev.cuh"
+#include "gla_delta_tri.cuh"
 #include "gla_delta_internal.h"
 
 namespace gla {
@@ -40,12 +41,8 @@ constexpr int NKQ = 3;            // K and Q stages: chunk m's, the next one's (
 constexpr int NV = 2;             // V stages, T and P buffers
 constexpr int NG = 4;             // gate slots (the drain is the last reader)
 constexpr int DVT = 128;          // dv columns per CTA
-constexpr int LDD = 20;           // row stride of the fp32 diagonal blocks
-constexpr float kRange = 60.f;    // |G - G_mid| up to which the two-factor form of D is used
 
 enum { ERR_TMA = 0x641, ERR_MMA = 0x642, ERR_EPI = 0x643, ERR_DRAIN = 0x644, ERR_PREP = 0x645 };
-
-__device__ __forceinline__ float2 f2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
 
 template <int DK>
 struct FL {
@@ -82,105 +79,6 @@ struct FusedArgs {
     int* status;
 };
 struct FusedMaps { CUtensorMap k, q, v, o; };
-
-// ---- mma.sync on 16-row pieces of a swizzled 64 x 64 bf16 matrix (128-byte rows)
-__device__ __forceinline__ uint32_t sw(uint32_t base, int row, int col8) { return base + row * 128 + ((col8 ^ (row & 7)) << 4); }
-__device__ __forceinline__ void ldm_a(uint32_t base, int r0, int k0, uint32_t (&a)[4])
-{
-    const int lane = threadIdx.x & 31;
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(sw(base, r0 + (lane & 15), k0 / 8 + (lane >> 4))) : "memory");
-}
-__device__ __forceinline__ void ldm_b(uint32_t base, int k0, int n0, uint32_t (&b)[2])
-{
-    const int lane = threadIdx.x & 31;
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
-                 : "=r"(b[0]), "=r"(b[1]) : "r"(sw(base, k0 + (lane & 15), n0 / 8)) : "memory");
-}
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-// c (16 x 8) += Y Z over K values: Y's rows from (yr, yc) of a matrix whose low parts lie ylo bytes
-// behind, or in the rows' other halves (ylo = 64); Z's from (zr, zc), low parts SLAB behind.
-template <int K>
-__device__ __forceinline__ void block_product(uint32_t y, int yr, int yc, uint32_t ylo, uint32_t z, int zr, int zc, float (&c)[4])
-{
-#pragma unroll
-    for (int k = 0; k < K; k += 16) {
-        uint32_t ah[4], al[4], bh[2], bl[2];
-        ldm_a(y, yr, yc + k, ah);
-        if (ylo == 64) ldm_a(y, yr, yc + k + 32, al);
-        else ldm_a(y + ylo, yr, yc + k, al);
-        ldm_b(z, zr + k, zc, bh);
-        ldm_b(z + SLAB, zr + k, zc, bl);
-        mma16(c, ah, bh);
-        mma16(c, al, bh);
-        mma16(c, ah, bl);
-    }
-}
-// X (16 x 8 at column n0 of the block) = -(Y C) Z for K-wide pieces: Y at (yr, yc), C at (yc, zc) and Z at
-// (zc, zc) of the matrix whose parts start at hi and hi + SLAB. Columns n0 .. n0 + 7 of the product.
-template <int K>
-__device__ __forceinline__ void block_rule(uint32_t hi, int yr, int yc, int zc, int n0, float (&x)[4])
-{
-    float w[K / 8][4];
-#pragma unroll
-    for (int i = 0; i < K / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[i][e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; k += 16) {
-        uint32_t ah[4], al[4];
-        ldm_a(hi, yr, yc + k, ah);
-        ldm_a(hi + SLAB, yr, yc + k, al);
-#pragma unroll
-        for (int i = 0; i < K / 8; ++i) {
-            uint32_t bh[2], bl[2];
-            ldm_b(hi, yc + k, zc + 8 * i, bh);
-            ldm_b(hi + SLAB, yc + k, zc + 8 * i, bl);
-            mma16(w[i], ah, bh);
-            mma16(w[i], al, bh);
-            mma16(w[i], ah, bl);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; k += 16) {
-        uint32_t ah[4], al[4], bh[2], bl[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            split2(-w[k / 8 + e][0], -w[k / 8 + e][1], ah[2 * e], al[2 * e]);
-            split2(-w[k / 8 + e][2], -w[k / 8 + e][3], ah[2 * e + 1], al[2 * e + 1]);
-        }
-        ldm_b(hi, zc + k, zc + n0, bh);
-        ldm_b(hi + SLAB, zc + k, zc + n0, bl);
-        mma16(x, ah, bh);
-        mma16(x, al, bh);
-        mma16(x, ah, bl);
-    }
-}
-// The 16 x 8 fragment times f to rows r0.., columns c0.. of both parts (the low one as above).
-__device__ __forceinline__ void put_fragment(uint32_t hi, int r0, int c0, uint32_t lo, const float (&x)[4], float f)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        uint32_t h, l;
-        split2(f * x[2 * e], f * x[2 * e + 1], h, l);
-        const uint32_t a = sw(hi, r0 + g + 8 * e, c0 / 8) + t * 4;
-        const uint32_t b = lo == 64 ? sw(hi, r0 + g + 8 * e, c0 / 8 + 4) + t * 4 : a + lo;
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(h) : "memory");
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(b), "r"(l) : "memory");
-    }
-}
-__device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
 
 // OUT: O is formed (and its loads, products and drain run). Without it the state alone, from zero, and
 // in the tiles after dv's the state that starts from the identity without V: the segment's transition.
@@ -292,35 +190,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 // next chunk's increment is formed
                 if (m >= NG - 1) wait(&d_full[1], (m - NG + 1) & 1, abort_flag, status, ERR_PREP);
                 __syncwarp();
-                // running sum of the gate over the chunk
-                const bool bad = __any_sync(~0u, x0 != x0 || x1 != x1);   // a NaN gate reaches the state through exp(G)
-                // below -1e5 exp() is zero whatever comes later
-                x0 = fminf(fmaxf(x0, -1e5f), 1e5f);
-                x1 = fminf(fmaxf(x1, -1e5f), 1e5f);
-                Two s = two_add(Two{x0, 0.f}, Two{x1, 0.f});
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const Two y = {__shfl_up_sync(~0u, s.h, o), __shfl_up_sync(~0u, s.l, o)};
-                    if (lane >= o) s = two_add(s, y);
-                }
-                const Two g1 = s, g0 = two_add(s, Two{-x1, 0.f});
-                const Two mid = {__shfl_sync(~0u, g1.h, 15), __shfl_sync(~0u, g1.l, 15)};   // G at token 31
-                const Two end = {__shfl_sync(~0u, g1.h, 31), __shfl_sync(~0u, g1.l, 31)};
-                auto minus = [](Two x, Two y) { return (x.h - y.h) + (x.l - y.l); };
-                const float d0 = minus(g0, mid), d1 = minus(g1, mid);
-                const bool near = __all_sync(~0u, fmaxf(fabsf(d0), fabsf(d1)) <= kRange);
-                const float nan = __int_as_float(0x7fc00000);
-                const float e0 = bad ? nan : expf(g0.h + g0.l), e1 = bad ? nan : expf(g1.h + g1.l);
-                float2* o = reinterpret_cast<float2*>(sm + L::G_OFF + (m % NG) * L::GB) + lane;
-                o[0] = make_float2(b0, b1);
-                o[C / 2] = make_float2(e0, e1);
-                o[C] = make_float2(expf(minus(end, g0)), expf(minus(end, g1)));
-                o[3 * C / 2] = make_float2(-e0, -e1);
-                // the factors of D (zeros where the gate is too steep for them) and G
-                o[2 * C] = near ? make_float2(expf(d0), expf(d1)) : make_float2(0.f, 0.f);
-                o[5 * C / 2] = near ? make_float2(expf(-d0), expf(-d1)) : make_float2(0.f, 0.f);
-                o[3 * C] = make_float2(g0.h, g1.h);
-                o[7 * C / 2] = make_float2(g0.l, g1.l);
+                chunk_gates(x0, x1, b0, b1, sm + L::G_OFF + (m % NG) * L::GB);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&gt_ready[m % NG]);
                 if (m + 1 < n) fetch(m + 1);
@@ -644,165 +514,21 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
     } else {
         // ---------------------------------------------------------- prep, one chunk ahead
         regs_dec<64>();
-        const int pw = warp - 16, quarter = warp & 3, c0 = (pw >> 2) * 32;
-        const int i = (quarter & 1) * 32 + lane;      // row of the chunk
-        const bool isP = quarter >= 2;
+        const int pw = warp - 16;
         float* diag = reinterpret_cast<float*>(sm + L::D_OFF);
-        // Of the warps' 32 x 32 pieces the one above the diagonal is zero, once and for all, the one below
-        // needs no mask.
-        const bool above = !(quarter & 1) && c0 > 0, below = (quarter & 1) && c0 == 0;
-        if (above)
-            for (int x = 0; x < NV * 2 * 4; ++x)
-                sts4(sw(s0 + L::TP_OFF + (x >> 3) * 4 * SLAB + (isP ? 2 * SLAB : 0) + ((x >> 2) & 1) * SLAB, i, 4 + (x & 3)), 0u, 0u, 0u, 0u);
+        for (int x = 0; x < NV; ++x) chunk_zeros(s0 + L::TP_OFF + x * 4 * SLAB, pw);
         for (int m = 0; m < n; ++m) {
             const float* gt = reinterpret_cast<const float*>(sm + L::G_OFF + (m % NG) * L::GB);
-            const uint32_t tb = s0 + L::TP_OFF + (m % NV) * 4 * SLAB, pb = tb + 2 * SLAB;
+            const uint32_t tb = s0 + L::TP_OFF + (m % NV) * 4 * SLAB;
             wait(&gt_ready[m % NG], (m / NG) & 1, abort_flag, status, ERR_PREP);
             wait(g_full, m & 1, abort_flag, status, ERR_PREP);
             tc_fence_after();
-            if (!above) {
-                // tensor-memory lanes 0-63: rows of L; 64-127: rows of P
-                const bool near = gt[4 * C] != 0.f;
-                const float f = isP ? a.scale : 1.f;
-                const int last = below ? C : isP ? i : i - 1;
-                const float fi = f * gt[4 * C + i];
-#pragma unroll 1
-                for (int c = c0; c < c0 + 32; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(tm + ((uint32_t)(quarter * 32) << 16) + L::tG + c, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {          // eight columns at a time
-                        const int cq = c + 8 * q;
-                        float2 x[4];
-                        if (near) {
-                            const float4 u = *reinterpret_cast<const float4*>(gt + 5 * C + cq);
-                            const float4 v = *reinterpret_cast<const float4*>(gt + 5 * C + cq + 4);
-                            const float2 ff = make_float2(fi, fi);
-                            x[0] = mul2(f2(r[8 * q], r[8 * q + 1]), mul2(ff, make_float2(u.x, u.y)));
-                            x[1] = mul2(f2(r[8 * q + 2], r[8 * q + 3]), mul2(ff, make_float2(u.z, u.w)));
-                            x[2] = mul2(f2(r[8 * q + 4], r[8 * q + 5]), mul2(ff, make_float2(v.x, v.y)));
-                            x[3] = mul2(f2(r[8 * q + 6], r[8 * q + 7]), mul2(ff, make_float2(v.z, v.w)));
-                        } else {
-                            const float gh = gt[6 * C + i], gl = gt[7 * C + i];
-                            auto D = [&](int j) { return f * expf((gh - gt[6 * C + cq + j]) + (gl - gt[7 * C + cq + j])); };
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                x[j] = mul2(f2(r[8 * q + 2 * j], r[8 * q + 2 * j + 1]), make_float2(D(2 * j), D(2 * j + 1)));
-                        }
-                        if (!below) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                x[j].x = cq + 2 * j <= last ? x[j].x : 0.f;
-                                x[j].y = cq + 2 * j + 1 <= last ? x[j].y : 0.f;
-                            }
-                        }
-                        if (!isP && !below && (cq >> 4) == (i >> 4)) {
-                            // the row's diagonal block: to fp32, times beta in its 8-row halves (which are
-                            // solved), plain in the quarter below the diagonal (which enters the block rule)
-                            const float be = (cq >> 3) == (i >> 3) ? gt[i] : 1.f;
-                            float* dd = diag + (i >> 4) * 16 * LDD + (i & 15) * LDD + (cq & 15);
-                            *reinterpret_cast<float4*>(dd) = make_float4(be * x[0].x, be * x[0].y, be * x[1].x, be * x[1].y);
-                            *reinterpret_cast<float4*>(dd + 4) = make_float4(be * x[2].x, be * x[2].y, be * x[3].x, be * x[3].y);
-                        } else {
-                            uint32_t h8[4], l8[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) split2(x[e], h8[e], l8[e]);
-                            const uint32_t o = sw(isP ? pb : tb, i, cq / 8);
-                            sts4(o, h8[0], h8[1], h8[2], h8[3]);
-                            sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
-                        }
-                    }
-                }
-            }
+            chunk_scores(tm + L::tG, gt, a.scale, tb, diag, pw);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(g_read);
             named_bar_sync(2, 256);
-            if (pw < 4) {
-                // The 16-row diagonal block `pw`, in place in fp32: its two 8-row halves by forward
-                // substitution, a lane per column, then the block rule, two outputs a lane.
-                const int cc = lane & 7, rr = lane >> 3, hb = rr & 1;
-                float* B = diag + pw * 16 * LDD;
-                float* A = B + hb * 8 * (LDD + 1);
-                float x[8];
-#pragma unroll
-                for (int ii = 0; ii < 8; ++ii) {
-                    float u = ii == cc ? 1.f : 0.f, v = 0.f;
-                    if (ii > 0) {
-                        const float4 q = *reinterpret_cast<const float4*>(A + ii * LDD);
-                        u = fmaf(-q.x, x[0], u);
-                        if (ii > 1) v = fmaf(-q.y, x[1], v);
-                        if (ii > 2) u = fmaf(-q.z, x[2], u);
-                        if (ii > 3) v = fmaf(-q.w, x[3], v);
-                    }
-                    if (ii > 4) {
-                        const float4 q = *reinterpret_cast<const float4*>(A + ii * LDD + 4);
-                        u = fmaf(-q.x, x[4], u);
-                        if (ii > 5) v = fmaf(-q.y, x[5], v);
-                        if (ii > 6) u = fmaf(-q.z, x[6], u);
-                    }
-                    x[ii] = u + v;
-                }
-                const float be = gt[16 * pw + 8 * hb + cc];
-                __syncwarp();                        // the half's rows are read
-                if (lane < 16) {
-#pragma unroll
-                    for (int ii = 0; ii < 8; ++ii) A[ii * LDD + cc] = be * x[ii];
-                }
-                __syncwarp();
-                float w[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {        // rows rr and rr + 4 of C Z
-                    const float z = B[k * LDD + cc];
-                    w[0] = fmaf(B[(8 + rr) * LDD + k], z, w[0]);
-                    w[1] = fmaf(B[(12 + rr) * LDD + k], z, w[1]);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {        // and of -Y (C Z)
-                    const float z = __shfl_sync(~0u, w[k >> 2], (k & 3) * 8 + cc);
-                    y[0] = fmaf(-B[(8 + rr) * LDD + 8 + k], z, y[0]);
-                    y[1] = fmaf(-B[(12 + rr) * LDD + 8 + k], z, y[1]);
-                }
-                __syncwarp();                        // C is read
-                B[(8 + rr) * LDD + cc] = y[0];
-                B[(12 + rr) * LDD + cc] = y[1];
-                __syncwarp();
-                const int row = lane >> 1, col = (lane & 1) * 8;
-                uint32_t h8[4], l8[4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float4 q = *reinterpret_cast<const float4*>(B + row * LDD + col + 4 * e);
-                    split2(q.x, q.y, h8[2 * e], l8[2 * e]);
-                    split2(q.z, q.w, h8[2 * e + 1], l8[2 * e + 1]);
-                }
-                const uint32_t o = sw(tb, 16 * pw + row, 2 * pw + (lane & 1));
-                sts4(o, h8[0], h8[1], h8[2], h8[3]);
-                sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
-            }
-            named_bar_sync(2, 256);
-            {
-                // 16 -> 32, eight columns a warp for each of the two pairs
-                float x[4];
-                const int o = 32 * (pw >> 1), n0 = (pw & 1) * 8;
-                if (pw < 4) block_rule<16>(tb, o + 16, o + 16, o, n0, x);
-                named_bar_sync(2, 256);
-                if (pw < 4) put_fragment(tb, o + 16, o + n0, SLAB, x, 1.f);
-            }
-            named_bar_sync(2, 256);
-            {
-                // 32 -> 64: 16 rows by eight columns a warp, Y C by way of shared memory
-                const int r0 = (pw >> 2) * 16, n0 = (pw & 3) * 8;
-                const uint32_t wb = s0 + L::W_OFF;
-                float x[4] = {0.f, 0.f, 0.f, 0.f};
-                block_product<32>(tb, 32 + r0, 32, SLAB, tb, 32, n0, x);
-                put_fragment(wb, r0, n0, 64, x, -1.f);
-                named_bar_sync(2, 256);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = 0.f;
-                block_product<32>(wb, r0, 0, 64, tb, 0, n0, x);
-                put_fragment(tb, 32 + r0, n0, SLAB, x, 1.f);
-            }
+            chunk_inverse(tb, s0 + L::W_OFF, gt, diag, pw);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&t_ready[m & 1]);
