@@ -121,7 +121,9 @@ def gla_attention(q, k, v, log_g=None, S0=None, gate=None):
 
 def delta_attention(q, k, v, log_g, beta, S0=None, scale=None, path=_b.GLA_PATH_AUTO):
     """(O, S_T) of the gated delta rule (binding.delta_forward), differentiable once in q, k, v, log_g, beta
-    and S0. The inputs must be contiguous device tensors."""
+    and S0. The inputs must be contiguous device tensors. A step captured into a CUDA graph starts from
+    leaves of which no eager graph is alive (fresh detached ones, say): autograd would wait on the stream
+    of that graph, which a capture cannot."""
     import torch
     if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in (q, k, v, log_g, beta, S0)):
         return _b.delta_forward(q, k, v, log_g, beta, S0, scale=scale, path=path)

@@ -654,7 +654,7 @@ def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, pa
         ST = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if S0 is None else torch.empty_like(S0)
     p = gla_delta_params(_ptr(q), _ptr(k), _ptr(v), _ptr(log_g), _ptr(beta), _ptr(S0), _ptr(O), _ptr(ST),
                          B, H, Hk, T, dk, dv, dk ** -0.5 if scale is None else scale, code, path, None, 0, force_segments)
-    n = 0 if T < 128 else _here_size(lib.gla_delta_fwd_workspace_size, p, dev)   # (two chunks at least: none below)
+    n = 0 if T <= 64 else _here_size(lib.gla_delta_fwd_workspace_size, p, dev)   # (one chunk needs none)
     ws = None
     if n:
         ws = torch.empty(n, dtype=torch.uint8, device=dev)

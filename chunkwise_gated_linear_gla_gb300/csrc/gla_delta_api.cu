@@ -38,7 +38,7 @@ gla_status check_sizes(int B, int H, int Hk, int T, int dk, int dv, float scale,
 bool chunk_shape_ok(int B, int H, int T, int dk, int dv, int dtype)
 {
     const long long nch = ((long long)T + kChunk - 1) / kChunk;
-    return dtype == GLA_BF16 && (dk == 64 || dk == 128) && dv % 64 == 0 && (long long)B * H <= 65535 &&
+    return dtype == GLA_BF16 && T <= kDeltaChunkMaxT && (dk == 64 || dk == 128) && dv % 64 == 0 && (long long)B * H <= 65535 &&
            (long long)B * H * nch < (1LL << 31) && (long long)B * H * T < (1LL << 40);
 }
 

@@ -14,6 +14,9 @@ constexpr int kDeltaMaxDk = 256;    // widest keys of the recurrent form (its st
 // AUTO: the shortest call that the chunk form takes. With 128 heads (dk = dv = 128) 9 tokens are 14 us
 // against 18 in the recurrent form; with 4 to 16 heads both are launch latency up to 24 tokens (13 us).
 constexpr int kDeltaChunkMinT = 9, kDeltaChunkMinTFew = 24, kDeltaFewTiles = 64;
+// The longest: a CTA that walks 2^25 tokens (half a million chunks at 3.3 us) is done within the four
+// seconds after which its waits give up.
+constexpr int kDeltaChunkMaxT = 1 << 25;
 constexpr int kDeltaKeep = 16;      // recurrent backward: tokens between two kept states
 
 // The recurrent form (gla_delta_step.cu): the recurrence token by token, the state tile in

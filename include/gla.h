@@ -389,7 +389,7 @@ const char* gla_bwd_stage_name(const gla_bwd_params* p, int stage);
 /*
  * gla_delta_fwd — the gated delta rule. Where the pass above only adds k_t^T v_t to the
  * decayed state, the delta rule first takes out what the state already answers for k_t
- * (the recurrence of gated delta networks, whose chunk kernels the FlashQLA talk describes):
+ * (the recurrence of gated delta networks):
  *
  *     S~_t = alpha_t S_{t-1},   u_t = beta_t (v_t - k_t S~_t),
  *     S_t  = S~_t + k_t^T u_t,  o_t = scale q_t S_t,
@@ -403,7 +403,7 @@ const char* gla_bwd_stage_name(const gla_bwd_params* p, int stage);
  *                    single tokens (decoding; bound by the state's bytes), a few tokens,
  *                    fp32 inputs and other shapes; dk <= 256.
  *   GLA_PATH_TENSOR  the chunk form on the tensor cores (bf16, dk 64 or 128, dv a multiple of
- *                    64, B H <= 65535; else GLA_ERR_UNSUPPORTED): 64-token chunks, the
+ *                    64, B H <= 65535, T <= 2^25; else GLA_ERR_UNSUPPORTED): 64-token chunks, the
  *                    corrections u of a chunk through the inverse of a unit triangular matrix.
  *                    What feeds the state is kept to 17 bits (pairs of bf16) and summed in
  *                    fp32: S_T is good to about 3e-6, O to its bf16 rounding. With few heads the

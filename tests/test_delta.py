@@ -105,7 +105,7 @@ def _params(**kw):
     (dict(q=0), 1), (dict(beta=0), 1), (dict(O=0), 1), (dict(q=(1 << 12) + 8), 1), (dict(ST=(7 << 12) + 4), 1),
     (dict(O=3 << 12), 1), (dict(ST=1 << 12), 1), (dict(S0=(7 << 12) + 64), 1),
     (dict(path=gla.GLA_PATH_TENSOR, dk=128, dv=80), 2), (dict(path=gla.GLA_PATH_TENSOR, dtype=gla.GLA_FP32), 2),
-    (dict(path=gla.GLA_PATH_TENSOR, dk=256), 2),
+    (dict(path=gla.GLA_PATH_TENSOR, dk=256), 2), (dict(path=gla.GLA_PATH_TENSOR, T=(1 << 25) + 1), 2),
 ])
 def test_forward_refuses_before_launch(kw, want):
     assert bnd.gla_delta_fwd(_params(**kw), 0, check=False) == want
@@ -203,6 +203,16 @@ def test_cut_sequences(dk, dv, T, gate, segments):
     assert gla.gla_device_status() == 0
     assert_close(to_np(got_O), to_np(O), torch.bfloat16, "O")
     close(got_S, S, 6 * PARTS, "S_T")        # the transition's two-part operands too
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 64, 65, 100, 127, 128])
+def test_more_segments_than_chunks(T):
+    x = ref.make(1, 2, 2, T, 64, 64, torch.bfloat16, seed=T)[0]
+    O, S = ref.delta(*ref.f64(x), 64 ** -0.5)
+    got_O, got_S = gla.delta_forward(*ref.cuda(x), path=gla.GLA_PATH_TENSOR, force_segments=3)
+    assert_close(to_np(got_O), to_np(O), torch.bfloat16, "O")
+    close(got_S, S, 6 * PARTS, "S_T")
 
 
 @pytest.mark.gpu
@@ -357,6 +367,59 @@ def test_autograd_and_unused_outputs():
         assert torch.equal(a, b)
     (O.float().square().sum()).backward()
     assert all(t.grad is not None for t in leaves)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 100])
+def test_training_step_replays_from_a_cuda_graph(T):
+    """The norms and the delta rule with their gradients through autograd, captured and replayed on new inputs."""
+    def inputs(seed):
+        x, g = ref.make(1, 4, 2, T, 64, 64, torch.bfloat16, seed=seed)
+        return [*(t.cuda() for t in x), torch.randn(x[2].shape, generator=g).bfloat16().cuda()]
+
+    def step(q, k, v, log_g, beta, S0, dO):
+        leaves = [t.detach().requires_grad_(True) for t in (q, k, v, log_g, beta, S0)]
+        O, ST = gla.delta_attention(*gla.qk_norm_rope(*leaves[:2]), *leaves[2:])
+        return [O.detach(), ST.detach(), *torch.autograd.grad((O, ST), leaves, (dO, torch.ones_like(ST)))]
+
+    buf = inputs(1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(*buf)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = step(*buf)
+    for seed in (2, 3):
+        new = inputs(seed)
+        for b, t in zip(buf, new):
+            b.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, step(*new)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_calls_in_flight_on_two_streams():
+    """Two passes and their gradients at once: neither sees the other's workspace or status."""
+    sets = [ref.cuda(ref.make(1, 4, 2, T, 128, 128, torch.bfloat16, seed=T)[0]) for T in (300, 2000)]
+    dO = [torch.ones_like(x[2]) for x in sets]
+    want = [[*gla.delta_forward(*x), *gla.delta_backward(*x, d)] for x, d in zip(sets, dO)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append([*gla.delta_forward(*sets[i]), *gla.delta_backward(*sets[i], dO[i])])
+    torch.cuda.synchronize()
+    assert gla.gla_device_status() == 0
+    for i in range(2):
+        for g in got[i]:
+            for a, b in zip(g, want[i]):
+                assert torch.equal(a, b)
 
 
 @pytest.mark.gpu
