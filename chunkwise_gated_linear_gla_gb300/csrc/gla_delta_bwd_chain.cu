@@ -1,5 +1,5 @@
 // gla_delta_sweep: the two serial passes of the delta rule's backward, built like the forward
-// chain (gla_delta_chain.cu): dv along the tensor-memory lanes, the state in fp32 registers,
+// chain (gla_delta_fused.cu): dv along the tensor-memory lanes, the state in fp32 registers,
 // every operand that feeds it in two bf16 parts. With e = exp(G), l = exp(G_end - G):
 //
 //   forward:  U = T (V - e K S),              S  <- exp(G_end) S + K^T (l U)

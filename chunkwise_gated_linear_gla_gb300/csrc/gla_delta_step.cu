@@ -11,6 +11,8 @@
 // Bound by the state's bytes at small T: 4 dk dv read and written once per call. CT = 128
 // columns by 256 threads keeps 16 16-byte loads per thread in flight at dk = 128; when the
 // tiles are fewer than the SMs they narrow to 32 columns so that more SMs pull (the launcher).
+// dk = dv = 128: the next token of 2048 heads 51 us, 5.3 TB/s; of 16 heads 4.5 us, launch latency;
+// five tokens of 512 heads 23.4 us, two of them a token's barriers (tiles of 64 columns: 26.7 us).
 #include <cuda_bf16.h>
 
 #include "gla_delta_dev.cuh"
@@ -218,21 +220,24 @@ __device__ __forceinline__ void cp16(void* dst, const void* src)
 }
 
 // The same recurrence for several tokens: nothing but the block's token loads is shared between
-// warps, so no barrier stands between two tokens. A warp owns four columns; lane (r, c) holds rows
-// r RPT .. of one of them, and a token's two sums cross eight lanes in four shuffle steps (about
-// 250 cycles a token at dk = 64, 1000 in the kernel above, whose warps meet at every token). Its
-// state accesses are 16 bytes a row and warp, the reason why single tokens take the other kernel.
+// warps, so no barrier stands between two tokens. A warp owns LC columns; lane (r, c) holds rows
+// r RPT .. of one of them. A token's way from one state to the next is k S over 32 / LC lanes, two
+// shuffles deep (three at dk = 256, where a lane cannot hold 64 rows of everything); o = scale q S of
+// the token before, from the same state, is reduced beside it, and the next token's row is on its way
+// from shared memory meanwhile. Bound by that latency: 256 tokens of two heads, fp32, dk = dv = 64,
+// 41 us (59 with q . k formed ahead, three shuffles and nothing loaded early). Its state accesses
+// are 32 bytes a row and warp, the reason why single tokens take the other kernel.
 template <typename E, int DK>
-__global__ void __launch_bounds__(256) gla_delta_tokens_kernel(DeltaStep a)
+__global__ void __launch_bounds__(DK <= 128 ? 128 : 256) gla_delta_tokens_kernel(DeltaStep a)
 {
-    constexpr int NT = 256, NW = 8, CT = 32, RPT = DK / 8, V = 16 / sizeof(E);
+    constexpr int CT = 32, LC = DK <= 128 ? 8 : 4, NT = CT / LC * 32, RPT = DK * LC / 32, V = 16 / sizeof(E);
     __shared__ __align__(16) E sq[2][TB][DK], sk[2][TB][DK], sv[2][TB][CT];
-    __shared__ float sal[2][TB], sbe[2][TB], sqk[2][TB];
+    __shared__ float sal[2][TB], sbe[2][TB];
 
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, c = lane & 3, r = lane >> 2;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, c = lane % LC, r = lane / LC;
     const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H;
     const int bk = b * a.Hk + h / (a.H / a.Hk);
-    const int c0 = blockIdx.y * CT, col = c0 + 4 * warp + c;
+    const int c0 = blockIdx.y * CT, lc = LC * warp + c, col = c0 + lc;
     const bool in = col < a.dv;
     const int row0 = r * RPT;
 
@@ -280,17 +285,23 @@ __global__ void __launch_bounds__(256) gla_delta_tokens_kernel(DeltaStep a)
         S[i].y = ok ? a.S0[sbase + (size_t)(x + 1) * a.dv] : 0.f;
     }
 
+    // this lane's rows of x S
+    auto sum = [&](const float (&x)[RPT]) {
+        float2 z[2] = {};
+#pragma unroll
+        for (int i = 0; i < RPT / 2; ++i) z[i & 1] = fma2(make_float2(x[2 * i], x[2 * i + 1]), S[i], z[i & 1]);
+        return (z[0].x + z[0].y) + (z[1].x + z[1].y);
+    };
+    auto put = [&](int t, float y) {
+        if (!go || r != 0 || !in) return;
+        if constexpr (sizeof(E) == 2) go[(size_t)t * a.dv + col] = __float2bfloat16_rn(a.scale * y);
+        else go[(size_t)t * a.dv + col] = a.scale * y;
+    };
+    float q[RPT] = {};                   // of the token before
     for (int t0 = 0, f = 0; t0 < a.T; t0 += TB, f ^= 1) {
         const int n = min(TB, a.T - t0);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        for (int t = warp; t < n; t += NW) {
-            float s = 0.f;
-            for (int x = lane; x < DK; x += 32) s = fmaf(to_f(sq[f][t][x]), to_f(sk[f][t][x]), s);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-            if (lane == 0) sqk[f][t] = s;
-        }
         if (t0 + TB < a.T) fetch(t0 + TB, f ^ 1);
         if (a.keep && in) {
             float* kp = a.keep + ((size_t)bh * nkeep + t0 / kDeltaKeep) * a.dk * a.dv + col;
@@ -301,37 +312,44 @@ __global__ void __launch_bounds__(256) gla_delta_tokens_kernel(DeltaStep a)
                     kp[(size_t)(row0 + 2 * i + 1) * a.dv] = S[i].y;
                 }
         }
-        __syncthreads();                 // q . k of every token
+        // u = beta v - (beta alpha) k S: nothing but one fma waits for the sum
+        float k[RPT], al, uv, ua;
+        auto gate = [&](int t) {
+            al = sal[f][t];
+            uv = in ? sbe[f][t] * to_f(sv[f][t][lc]) : 0.f;
+            ua = -sbe[f][t] * al;
+        };
+        gate(0);
+        read_row<RPT>(&sk[f][0][row0], k);
+#pragma unroll 2
         for (int t = 0; t < n; ++t) {
-            float k[RPT], q[RPT];
-            read_row<RPT>(&sk[f][t][row0], k);
+            float x = sum(k), y = sum(q);
+            // what the next token takes (the row's last: itself again)
+            const int nx = min(t + 1, n - 1);
+            float kn[RPT];
+            read_row<RPT>(&sk[f][nx][row0], kn);
             read_row<RPT>(&sq[f][t][row0], q);
-            const float al = sal[f][t], be = sbe[f][t], qk = sqk[f][t], v = to_f(sv[f][t][4 * warp + c]);
-            float2 ks[2] = {}, qs[2] = {};
 #pragma unroll
-            for (int i = 0; i < RPT / 2; ++i) {
-                ks[i & 1] = fma2(make_float2(k[2 * i], k[2 * i + 1]), S[i], ks[i & 1]);
-                qs[i & 1] = fma2(make_float2(q[2 * i], q[2 * i + 1]), S[i], qs[i & 1]);
+            for (int o = LC; o < 32; o <<= 1) {
+                const float x1 = __shfl_xor_sync(~0u, x, o), y1 = __shfl_xor_sync(~0u, y, o);
+                x += x1;
+                y += y1;
             }
-            float x = (ks[0].x + ks[0].y) + (ks[1].x + ks[1].y), y = (qs[0].x + qs[0].y) + (qs[1].x + qs[1].y);
-            // eight row groups (lanes 4 apart): one half of the lanes sums k S, the other q S
-            const bool up = lane & 16;
-            const float sent = __shfl_xor_sync(~0u, up ? x : y, 16);
-            float m = (up ? y : x) + sent;
-            m += __shfl_xor_sync(~0u, m, 8);
-            m += __shfl_xor_sync(~0u, m, 4);
-            const float kS = __shfl_sync(~0u, m, c), qS = __shfl_sync(~0u, m, 16 + c);
-            const float u = in ? be * (v - al * kS) : 0.f;
+            const float u = fmaf(ua, x, uv);
 #pragma unroll
             for (int i = 0; i < RPT / 2; ++i)
-                S[i] = fma2(make_float2(k[2 * i], k[2 * i + 1]), make_float2(u, u),
-                            mul2(make_float2(al, al), S[i]));
-            if (go && r == 0 && in) {
-                const float o = a.scale * fmaf(qk, u, al * qS);
-                if constexpr (sizeof(E) == 2) go[(size_t)(t0 + t) * a.dv + col] = __float2bfloat16_rn(o);
-                else go[(size_t)(t0 + t) * a.dv + col] = o;
-            }
+                S[i] = fma2(make_float2(k[2 * i], k[2 * i + 1]), make_float2(u, u), mul2(make_float2(al, al), S[i]));
+            gate(nx);
+            if (t0 + t > 0) put(t0 + t - 1, y);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) k[i] = kn[i];
         }
+    }
+    {
+        float y = sum(q);
+#pragma unroll
+        for (int o = LC; o < 32; o <<= 1) y += __shfl_xor_sync(~0u, y, o);
+        put(a.T - 1, y);
     }
     if (a.ST && in) {
 #pragma unroll
@@ -345,18 +363,19 @@ __global__ void __launch_bounds__(256) gla_delta_tokens_kernel(DeltaStep a)
 
 template <typename E, int DK>
 cudaError_t launch_dk(const DeltaStep& a, cudaStream_t s) {
-    // Beyond a few tokens the barriers between them cost more than the narrow state accesses (20
-    // tokens of 128 heads, dk = dv = 128: 29 us against 46; 3 tokens of 256 heads: 21 against 17).
-    if (a.T > 8) {
-        gla_delta_tokens_kernel<E, DK><<<dim3((unsigned)(a.B * a.H), (a.dv + 31) / 32), 256, 0, s>>>(a);
-        return cudaGetLastError();
-    }
     // A thread holds at least four rows and at most 32 of them of four columns.
     constexpr int WIDE = DK <= 128 ? 128 : 64, NARROW = DK == 64 ? 64 : 32;
     const unsigned BH = (unsigned)(a.B * a.H);
+    const long long wide = (long long)BH * ((a.dv + WIDE - 1) / WIDE);
+    // Beyond a few tokens the barriers between them cost more than the tokens kernel's narrower state
+    // accesses: with fewer wide tiles than SMs from three tokens on (dk = dv = 128, 16 heads, 5 tokens:
+    // 8.9 us against 10.9), else from nine (512 heads, 8 tokens: 39.6 against 35.5, 12: 47.8 against 53.9).
+    if (a.T > (wide < a.sms && DK <= 128 ? 2 : 8)) {
+        gla_delta_tokens_kernel<E, DK><<<dim3((unsigned)(a.B * a.H), (a.dv + 31) / 32), DK <= 128 ? 128 : 256, 0, s>>>(a);
+        return cudaGetLastError();
+    }
     // Wide tiles move the most bytes per thread; with fewer of them than SMs, narrow ones put
     // more SMs on the same state.
-    const long long wide = (long long)BH * ((a.dv + WIDE - 1) / WIDE);
     if (wide < a.sms || a.dv <= NARROW)
         gla_delta_step_kernel<E, DK, NARROW><<<dim3(BH, (a.dv + NARROW - 1) / NARROW), NT, 0, s>>>(a);
     else
