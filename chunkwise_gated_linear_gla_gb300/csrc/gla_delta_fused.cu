@@ -543,70 +543,96 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
 }
 
 // The states entering the segments: S_in[0] = S0, S_in[s + 1] = M_s S_in[s] + S*_s, with each segment's
-// (S* [dk][dv], M [dk][dk]) side by side. A block owns 32 columns of one head, a thread 4 x 4 (dk = 128)
-// or 2 x 4 values; the next segment's M is on its way to shared memory during a product.
+// (S* [dk][dv], M [dk][dk]) side by side, in fp32 (what this rounds stays in the state over all segments).
+// A block owns 16 columns of one head. Each of its four groups of 64 threads sums over a quarter of the
+// keys, DK / 16 rows by four columns a thread (16-byte loads from shared memory are what bounds it: twice
+// as many with smaller tiles and no groups, 4.3 us a segment against 3.2); neighbouring lanes take
+// neighbouring rows of M, which are padded by 16 bytes: no bank conflicts. The next segment's M and S* are on
+// their way during a product.
+template <int DK>
+struct SL {
+    static constexpr int COLS = 16, LDM = DK + 4;
+    static constexpr int M_FLOATS = DK * LDM, S_FLOATS = DK * COLS;
+    static constexpr int SMEM = (2 * M_FLOATS + 5 * S_FLOATS) * 4;
+};
 template <int DK>
 __global__ void __launch_bounds__(256) gla_delta_scan_kernel(const float* __restrict__ S0, const float* __restrict__ pair,
                                                              float* S_in, int dv, int nseg)
 {
-    constexpr int R = DK / 32;                   // rows a thread
+    using L = SL<DK>;
+    constexpr int R = DK / 16, F = DK / 64;      // rows of a thread's tile; float4s of the block's columns a thread
     extern __shared__ __align__(16) float scan_smem[];
-    float* M = scan_smem;                        // [2][DK][DK]
-    float* S = scan_smem + 2 * DK * DK;          // [2][DK][32]
-    const int bh = blockIdx.y, tid = threadIdx.x, r0 = tid / 8 * R, c = tid % 8 * 4, col = blockIdx.x * 32 + c;
+    float* M = scan_smem;                        // [2][DK][LDM]
+    float* S = scan_smem + 2 * L::M_FLOATS;      // [DK][COLS]
+    float* part = S + L::S_FLOATS;               // [4][DK][COLS]
+    const int bh = blockIdx.y, tid = threadIdx.x, kg = tid / 64, rg = tid % 64 / 4;
+    const int r0 = tid / 4, c = tid % 4 * 4, col = blockIdx.x * L::COLS + c;
     const bool in = col < dv;                    // dv is a multiple of 16
     const size_t st = (size_t)DK * dv, step = st + DK * DK;
     const float* pp = pair + (size_t)bh * (nseg - 1) * step;
     float* out = S_in + (size_t)bh * nseg * st + col;
     auto fetch = [&](int g) {
         const float* m = pp + g * step + st;
-        const uint32_t d = smem_u32(M + (g & 1) * DK * DK);
+        const uint32_t d = smem_u32(M + (g & 1) * L::M_FLOATS);
         for (int i = tid; i < DK * DK / 4; i += 256)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i * 16), "l"(m + i * 4) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         ::"r"(d + (i / (DK / 4) * L::LDM + i % (DK / 4) * 4) * 4), "l"(m + i * 4) : "memory");
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     fetch(0);
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a thread's rows r0 + 64 i of the state, and of the next S*
+    float4 x[F], own[F];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const float4 x = S0 && in ? *reinterpret_cast<const float4*>(S0 + bh * st + (size_t)(r0 + i) * dv + col) : zero;
-        *reinterpret_cast<float4*>(S + (r0 + i) * 32 + c) = x;
-        if (in) *reinterpret_cast<float4*>(out + (size_t)(r0 + i) * dv) = x;
+    for (int i = 0; i < F; ++i) {
+        const int r = r0 + 64 * i;
+        x[i] = S0 && in ? *reinterpret_cast<const float4*>(S0 + bh * st + (size_t)r * dv + col) : zero;
+        own[i] = in ? *reinterpret_cast<const float4*>(pp + (size_t)r * dv + col) : zero;
     }
-    for (int g = 0; g + 1 < nseg; ++g) {
-        float2 y[R][2];
+    for (int g = 0;; ++g) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float4 x = in ? *reinterpret_cast<const float4*>(pp + g * step + (size_t)(r0 + i) * dv + col) : zero;
-            y[i][0] = make_float2(x.x, x.y);
-            y[i][1] = make_float2(x.z, x.w);
+        for (int i = 0; i < F; ++i) {
+            const int r = r0 + 64 * i;
+            *reinterpret_cast<float4*>(S + r * L::COLS + c) = x[i];
+            if (in) *reinterpret_cast<float4*>(out + g * st + (size_t)r * dv) = x[i];
         }
+        if (g + 1 == nseg) break;
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
         if (g + 2 < nseg) fetch(g + 1);
-        const float* m = M + (g & 1) * DK * DK + r0 * DK;
-        const float* s = S + (g & 1) * DK * 32 + c;
-#pragma unroll 4
-        for (int j = 0; j < DK; j += 4) {
-            float4 f[R];
+        float2 y[R][2] = {};
+        const float* m = M + (g & 1) * L::M_FLOATS + rg * L::LDM + kg * (DK / 4);
+        const float* s = S + kg * (DK / 4) * L::COLS + c;
+#pragma unroll 2
+        for (int j = 0; j < DK / 4; j += 4) {
+            float4 f[R], v[4];
 #pragma unroll
-            for (int i = 0; i < R; ++i) f[i] = *reinterpret_cast<const float4*>(m + i * DK + j);
+            for (int i = 0; i < R; ++i) f[i] = *reinterpret_cast<const float4*>(m + 16 * i * L::LDM + j);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 x = *reinterpret_cast<const float4*>(s + (j + e) * 32);
+            for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float4*>(s + (j + e) * L::COLS);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     const float w = e == 0 ? f[i].x : e == 1 ? f[i].y : e == 2 ? f[i].z : f[i].w;
-                    y[i][0] = fma2(make_float2(w, w), make_float2(x.x, x.y), y[i][0]);
-                    y[i][1] = fma2(make_float2(w, w), make_float2(x.z, x.w), y[i][1]);
+                    y[i][0] = fma2(make_float2(w, w), make_float2(v[e].x, v[e].y), y[i][0]);
+                    y[i][1] = fma2(make_float2(w, w), make_float2(v[e].z, v[e].w), y[i][1]);
                 }
-            }
         }
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float4 x = make_float4(y[i][0].x, y[i][0].y, y[i][1].x, y[i][1].y);
-            *reinterpret_cast<float4*>(S + ((g + 1) & 1) * DK * 32 + (r0 + i) * 32 + c) = x;
-            if (in) *reinterpret_cast<float4*>(out + (g + 1) * st + (size_t)(r0 + i) * dv) = x;
+        for (int i = 0; i < R; ++i)
+            *reinterpret_cast<float4*>(part + (kg * DK + rg + 16 * i) * L::COLS + c) = make_float4(y[i][0].x, y[i][0].y, y[i][1].x, y[i][1].y);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            const int r = r0 + 64 * i;
+            x[i] = own[i];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 p = *reinterpret_cast<const float4*>(part + (k * DK + r) * L::COLS + c);
+                x[i].x += p.x; x[i].y += p.y; x[i].z += p.z; x[i].w += p.w;
+            }
+            if (g + 2 < nseg && in) own[i] = *reinterpret_cast<const float4*>(pp + (g + 1) * step + (size_t)r * dv + col);
         }
     }
 }
@@ -638,10 +664,10 @@ cudaError_t launch_dk(const DeltaChunks& p, const FusedMaps& m, int* status, cud
         a.S_out = p.pair; a.out_seg = st + (long long)p.dk * p.dk; a.out_bh = a.out_seg * (p.nseg - 1);
         cudaError_t e = launch_pass<DK, false>(a, m, dim3(tiles + 1, BH, p.nseg - 1), s);
         if (e != cudaSuccess) return e;
-        constexpr int smem = (2 * DK * DK + 2 * DK * 32) * 4;
+        constexpr int smem = SL<DK>::SMEM, cols = SL<DK>::COLS;
         e = cudaFuncSetAttribute(gla_delta_scan_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        gla_delta_scan_kernel<DK><<<dim3((p.dv + 31) / 32, BH), 256, smem, s>>>(p.S0, p.pair, p.seg_in, p.dv, p.nseg);
+        gla_delta_scan_kernel<DK><<<dim3((p.dv + cols - 1) / cols, BH), 256, smem, s>>>(p.S0, p.pair, p.seg_in, p.dv, p.nseg);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         a.S_in = p.seg_in; a.in_bh = st * p.nseg; a.in_seg = st;
