@@ -226,7 +226,7 @@ __device__ __forceinline__ void cp16(void* dst, const void* src)
 // shuffles deep (three at dk = 256, where a lane cannot hold 64 rows of everything); o = scale q S of
 // the token before, from the same state, is reduced beside it, and the next token's row is on its way
 // from shared memory meanwhile. Bound by that latency: 256 tokens of two heads, fp32, dk = dv = 64,
-// 41 us (59 with q . k formed ahead, three shuffles and nothing loaded early). Its state accesses
+// 37 us (59 with q . k formed ahead, three shuffles and nothing loaded early). Its state accesses
 // are 32 bytes a row and warp, the reason why single tokens take the other kernel.
 template <typename E, int DK>
 __global__ void __launch_bounds__(DK <= 128 ? 128 : 256) gla_delta_tokens_kernel(DeltaStep a)
@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(DK <= 128 ? 128 : 256) gla_delta_tokens_kernel
     const int nkeep = (a.T + kDeltaKeep - 1) / kDeltaKeep;
 
     // tokens t0 .. of the sequence on their way to buffer f
+    float next_g = 0.f, next_b = 0.f;
     auto fetch = [&](int t0, int f) {
         const int n = min(TB, a.T - t0);
         for (int i = tid; i < n * (DK / V); i += NT) {
@@ -264,8 +265,16 @@ __global__ void __launch_bounds__(DK <= 128 ? 128 : 256) gla_delta_tokens_kernel
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (tid < n) {
-            sal[f][tid] = a.log_g ? expf(a.log_g[(size_t)bh * a.T + t0 + tid]) : 1.f;
-            sbe[f][tid] = to_f(static_cast<const E*>(a.beta)[(size_t)bh * a.T + t0 + tid]);
+            next_g = a.log_g ? a.log_g[(size_t)bh * a.T + t0 + tid] : 0.f;
+            next_b = to_f(static_cast<const E*>(a.beta)[(size_t)bh * a.T + t0 + tid]);
+        }
+    };
+    // the first warp's gates, once its block of tokens is done: waiting for them before it, that warp
+    // came to every barrier a memory latency late
+    auto put_gates = [&](int f) {
+        if (tid < TB) {
+            sal[f][tid] = expf(next_g);
+            sbe[f][tid] = next_b;
         }
     };
     if (a.dk < DK)   // keys past dk are zero in both buffers, for good
@@ -275,6 +284,7 @@ __global__ void __launch_bounds__(DK <= 128 ? 128 : 256) gla_delta_tokens_kernel
             (&sk[0][0][0])[t * DK + x] = E(0.f);
         }
     fetch(0, 0);
+    put_gates(0);
 
     float2 S[RPT / 2];
     const size_t sbase = (size_t)bh * a.dk * a.dv + col;
@@ -293,10 +303,14 @@ __global__ void __launch_bounds__(DK <= 128 ? 128 : 256) gla_delta_tokens_kernel
         for (int i = 0; i < RPT / 2; ++i) z[i & 1] = fma2(make_float2(x[2 * i], x[2 * i + 1]), S[i], z[i & 1]);
         return (z[0].x + z[0].y) + (z[1].x + z[1].y);
     };
-    auto put = [&](int t, float y) {
-        if (!go || r != 0 || !in) return;
-        if constexpr (sizeof(E) == 2) go[(size_t)t * a.dv + col] = __float2bfloat16_rn(a.scale * y);
-        else go[(size_t)t * a.dv + col] = a.scale * y;
+    const bool writes = go && r == 0 && in;
+    size_t at = col;                     // of the next row of O to be written
+    auto put = [&](float y) {
+        if (writes) {
+            if constexpr (sizeof(E) == 2) go[at] = __float2bfloat16_rn(a.scale * y);
+            else go[at] = a.scale * y;
+        }
+        at += a.dv;
     };
     float q[RPT] = {};                   // of the token before
     for (int t0 = 0, f = 0; t0 < a.T; t0 += TB, f ^= 1) {
@@ -322,7 +336,7 @@ __global__ void __launch_bounds__(DK <= 128 ? 128 : 256) gla_delta_tokens_kernel
         };
         gate(0);
         read_row<RPT>(&sk[f][0][row0], k);
-#pragma unroll 2
+#pragma unroll 4
         for (int t = 0; t < n; ++t) {
             float x = sum(k), y = sum(q);
             // what the next token takes (the row's last: itself again)
@@ -341,16 +355,17 @@ __global__ void __launch_bounds__(DK <= 128 ? 128 : 256) gla_delta_tokens_kernel
             for (int i = 0; i < RPT / 2; ++i)
                 S[i] = fma2(make_float2(k[2 * i], k[2 * i + 1]), make_float2(u, u), mul2(make_float2(al, al), S[i]));
             gate(nx);
-            if (t0 + t > 0) put(t0 + t - 1, y);
+            if (t0 + t > 0) put(y);
 #pragma unroll
             for (int i = 0; i < RPT; ++i) k[i] = kn[i];
         }
+        put_gates(f ^ 1);
     }
     {
         float y = sum(q);
 #pragma unroll
         for (int o = LC; o < 32; o <<= 1) y += __shfl_xor_sync(~0u, y, o);
-        put(a.T - 1, y);
+        put(y);
     }
     if (a.ST && in) {
 #pragma unroll
