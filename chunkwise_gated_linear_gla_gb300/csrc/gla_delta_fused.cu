@@ -526,7 +526,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
             wait(&gt_ready[m % NG], (m / NG) & 1, abort_flag, status, ERR_PREP);
             wait(g_full, m & 1, abort_flag, status, ERR_PREP);
             tc_fence_after();
-            chunk_scores(tm + L::tG, gt, a.scale, tb, diag, pw);
+            if (OUT || !(pw & 2)) chunk_scores(tm + L::tG, gt, a.scale, tb, diag, pw);   // (P's warps: only for O)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(g_read);
