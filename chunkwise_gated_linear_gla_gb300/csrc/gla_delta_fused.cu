@@ -112,8 +112,11 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
     uint64_t* fin = s_ready + 16;
     uint64_t* o_empty = s_ready + 17;       // O read out (4 warps)
     uint64_t* gt_ready = s_ready + 18;      // [NG] a chunk's gates written
-    uint32_t* holder = reinterpret_cast<uint32_t*>(s_ready + 18 + NG);
-    const Abort abort_flag(s_ready + 19 + NG);
+    uint64_t* l_ready = gt_ready + NG;      // without O: L written (2 warps)
+    uint64_t* d_free = l_ready + 1;         // and its diagonal blocks done with
+    uint32_t* holder = reinterpret_cast<uint32_t*>(l_ready + 2);
+    const Abort abort_flag(l_ready + 3);
+    const uint32_t tG = OUT ? L::tG : L::tOp;
 
     const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32, wg = warp / 4;
     const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
@@ -125,7 +128,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * NKQ + 2 * NV; ++i) mbar_init(&bar[i], 1);
-        for (int i = 0; i < 18 + NG; ++i) mbar_init(&s_ready[i], i < 10 ? 8 : i == 17 ? 4 : 1);
+        for (int i = 0; i < 20 + NG; ++i) mbar_init(&s_ready[i], i == 7 && !OUT ? 2 : i < 10 ? 8 : i == 17 ? 4 : i == 18 + NG ? 2 : 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -151,12 +154,12 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 __syncwarp();
                 if (elect_one()) {
                     // K's and Q's slab of the same 64 keys side by side: 128 rows of one operand
-                    mbar_arrive_expect_tx(&kq_full[st], 2 * L::KB);
+                    mbar_arrive_expect_tx(&kq_full[st], (OUT ? 2 : 1) * L::KB);
                     uint8_t* sb = sm + L::KQ_OFF + st * 2 * L::KB;
 #pragma unroll
                     for (int i = 0; i < DK / 64; ++i) {
                         tma_load_3d(sb + 2 * i * SLAB, &mp.k, &kq_full[st], 64 * i, t0, bk);
-                        tma_load_3d(sb + (2 * i + 1) * SLAB, &mp.q, &kq_full[st], 64 * i, t0, bk);
+                        if (OUT) tma_load_3d(sb + (2 * i + 1) * SLAB, &mp.q, &kq_full[st], 64 * i, t0, bk);
                     }
                 }
                 __syncwarp();
@@ -205,7 +208,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
             // cycles of moves, twice its time on the tensor cores).
             const uint32_t id64 = idesc_bf16(128, 64, false, false), idS = idesc_bf16(128, DK, false, true);
             const uint32_t idV = idesc_bf16(128, 64, true, false), idH = idesc_bf16(128, 64, false, true);
-            // chunk m's K on Q (128 rows) against K
+            // chunk m's K on Q (128 rows; without O nothing reads Q's) against K
             auto gram = [&](int m) {
                 const int st = m % NKQ;
                 wait(&kq_full[st], (m / NKQ) & 1, abort_flag, status, ERR_MMA);
@@ -215,13 +218,19 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
 #pragma unroll
                     for (int kk = 0; kk < DK / 16; ++kk) {
                         const uint64_t d = d0 + (((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4);
-                        mma_ss(tm + L::tG, d, d, id64, kk > 0);
+                        mma_ss(tm + tG, d, d, id64, kk > 0);
                     }
                     mma_commit(g_full);
                 }
                 __syncwarp();
             };
             if (n > 0) gram(0);
+            if (!OUT && n > 1) {
+                wait(g_read, 0, abort_flag, status, ERR_MMA);
+                __syncwarp();
+                tc_fence_after();
+                gram(1);
+            }
             for (int m = 0; m < n; ++m) {
                 if (__any_sync(~0u, *abort_flag)) break;
                 const int st = m % NKQ, vt = m % NV;
@@ -236,7 +245,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 for (int part = 0; part < 2; ++part) {
                     wait(&s_ready[part], ph, abort_flag, status, ERR_MMA);
                     // (the first product's buffer: chunk 0's product has been read by then)
-                    if (part == 0 && m == 0) wait(g_read, 0, abort_flag, status, ERR_MMA);
+                    if (OUT && part == 0 && m == 0) wait(g_read, 0, abort_flag, status, ERR_MMA);
                     __syncwarp();
                     tc_fence_after();
                     if (elect_one()) {
@@ -251,7 +260,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                     __syncwarp();
                 }
                 // the next chunk's K on Q against K, then V^T T^T, in the gap of R's register step
-                if (m + 1 < n) gram(m + 1);
+                if (OUT && m + 1 < n) gram(m + 1);
                 wait(&t_ready[m & 1], (m >> 1) & 1, abort_flag, status, ERR_MMA);
                 if (!ident) {
                     wait(&v_full[vt], (m / NV) & 1, abort_flag, status, ERR_MMA);
@@ -300,7 +309,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                     }
                     __syncwarp();
                 }
-                if (m + 1 < n) wait(g_read, (m + 1) & 1, abort_flag, status, ERR_MMA);
+                if (OUT && m + 1 < n) wait(g_read, (m + 1) & 1, abort_flag, status, ERR_MMA);
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
                     wait(&u_ready[part], ph, abort_flag, status, ERR_MMA);
@@ -325,6 +334,13 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                         if (part && !OUT) mma_commit(&kq_empty[st]);
                     }
                     __syncwarp();
+                }
+                if (!OUT && m + 2 < n) {
+                    // the scores are two chunks ahead; once their product is formed T's slot has been read
+                    wait(g_read, (m + 1) & 1, abort_flag, status, ERR_MMA);
+                    __syncwarp();
+                    tc_fence_after();
+                    gram(m + 2);
                 }
                 if (OUT) {
                     wait(p_ready, ph, abort_flag, status, ERR_MMA);
@@ -353,7 +369,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
     } else if (wg < 3) {
         // ---------------------------------------------------------- the chain's register steps
         // Group g owns, of part p, the keys p DK/2 + g DK/4 .. and the tokens 32 p + 16 g ..
-        regs_inc<128>();
+        regs_inc<OUT ? 128 : 120>();
         constexpr int KP = DK / 4;                    // keys of one part
         const int grp = wg - 1, d = (warp & 3) * 32 + lane;
         const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
@@ -472,8 +488,29 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 }
         }
     } else if (wg == 3) {
-        // ---------------------------------------------------------- drain of O
-        regs_dec<48>();
+        // ---------------------------------------------------------- drain of O; without O, the scores
+        regs_dec<OUT ? 48 : 64>();
+        if (!OUT && (warp & 3) < 2) {
+            // tensor-memory lanes 0-63: the rows of L
+            for (int m = 0; m < n; ++m) {
+                const float* gt = reinterpret_cast<const float*>(sm + L::G_OFF + (m % NG) * L::GB);
+                float* diag = reinterpret_cast<float*>(sm + L::D_OFF);
+                wait(&gt_ready[m % NG], (m / NG) & 1, abort_flag, status, ERR_PREP);
+                wait(g_full, m & 1, abort_flag, status, ERR_PREP);
+                if (m > 0) wait(d_free, (m - 1) & 1, abort_flag, status, ERR_PREP);
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x)
+                    chunk_scores(tm + tG, gt, a.scale, s0 + L::TP_OFF + (m % NV) * 4 * SLAB, diag, (warp & 3) + 4 * x);
+                tc_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(g_read);
+                    mbar_arrive(l_ready);
+                }
+            }
+        }
         if (OUT) {
             const int d = (warp & 3) * 32 + lane;
             const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
@@ -523,15 +560,22 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
         for (int m = 0; m < n; ++m) {
             const float* gt = reinterpret_cast<const float*>(sm + L::G_OFF + (m % NG) * L::GB);
             const uint32_t tb = s0 + L::TP_OFF + (m % NV) * 4 * SLAB;
-            wait(&gt_ready[m % NG], (m / NG) & 1, abort_flag, status, ERR_PREP);
-            wait(g_full, m & 1, abort_flag, status, ERR_PREP);
-            tc_fence_after();
-            if (OUT || !(pw & 2)) chunk_scores(tm + L::tG, gt, a.scale, tb, diag, pw);   // (P's warps: only for O)
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(g_read);
-            named_bar_sync(2, 256);
-            chunk_inverse(tb, s0 + L::W_OFF, gt, diag, pw);
+            if (OUT) {
+                wait(&gt_ready[m % NG], (m / NG) & 1, abort_flag, status, ERR_PREP);
+                wait(g_full, m & 1, abort_flag, status, ERR_PREP);
+                tc_fence_after();
+                chunk_scores(tm + tG, gt, a.scale, tb, diag, pw);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(g_read);
+                named_bar_sync(2, 256);
+            } else {
+                wait(l_ready, m & 1, abort_flag, status, ERR_PREP);
+                __syncwarp();
+            }
+            chunk_inverse(tb, s0 + L::W_OFF, gt, diag, pw, [&] {
+                if (!OUT && threadIdx.x == 512) mbar_arrive(d_free);
+            });
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&t_ready[m & 1]);

@@ -116,7 +116,7 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
         tc_fence_after();
         tmem_dealloc(tD, 64);
     }
-    chunk_inverse(s0, s0 + L::W_OFF, gt, diag, warp);
+    chunk_inverse(s0, s0 + L::W_OFF, gt, diag, warp, [] {});
     fence_proxy_async_smem();
     __syncthreads();
     if (warp == 1) {

@@ -228,8 +228,10 @@ __device__ __forceinline__ void chunk_scores(uint32_t tG, const float* gt, float
     }
 }
 
-// T in place of L, from the diagonal blocks up. All 256 threads; ends without a barrier.
-__device__ __forceinline__ void chunk_inverse(uint32_t tb, uint32_t wb, const float* gt, float* diag, int pw)
+// T in place of L, from the diagonal blocks up. All 256 threads; ends without a barrier. `read` is called
+// once the fp32 diagonal blocks are done with.
+template <typename F>
+__device__ __forceinline__ void chunk_inverse(uint32_t tb, uint32_t wb, const float* gt, float* diag, int pw, F read)
 {
     const int lane = threadIdx.x & 31;
     if (pw < 4) {
@@ -294,6 +296,7 @@ __device__ __forceinline__ void chunk_inverse(uint32_t tb, uint32_t wb, const fl
         sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
     }
     sm100::named_bar_sync(2, 256);
+    read();
     {
         // 16 -> 32, eight columns a warp for each of the two pairs
         float x[4];
