@@ -53,9 +53,9 @@ struct DeltaPlan {
 // Segments of the sequence. The pass is serial over the chunks of a head's 128 dv columns, so few
 // heads leave SMs idle. Cut into n segments the pass takes two walks of nch / n chunks (the first, of
 // all segments but the last, has one more tile per head for the transitions), a scan of 1.1 chunks' time
-// per segment (3.2 us against 2.9) and about four for the launches; n is the best of those that one wave
-// of the first walk holds (16384 tokens, dk = dv = 128, one head: uncut 756 us, 5 segments 335, 21 166,
-// 40 183, 64 245; 16 heads: uncut 745, 5 342, 6, whose walk takes two waves, 410).
+// per segment (3.2 us against 2.3 and 2.9) and about four for the launches; n is the best of those that one
+// wave of the first walk holds (16384 tokens, dk = dv = 128, one head: uncut 757 us, 5 segments 314, 20 161,
+// 40 179; 16 heads: uncut 747, 5 317, 6, whose walk takes two waves, 374).
 int choose_segments(int units, int trans, int nch, int sms)
 {
     const int most = std::min(1 + sms / (units + trans), nch / 4);

@@ -83,8 +83,11 @@ struct FusedArgs {
 };
 struct FusedMaps { CUtensorMap k, q, v, o; };
 
-// OUT: O is formed (and its loads, products and drain run). Without it the state alone, from zero, and
-// in the tiles after dv's the state that starts from the identity without V: the segment's transition.
+// OUT: O is formed (and its products and drain run). Without it the state alone, from zero, and in the
+// tiles after dv's the state that starts from the identity without V: the segment's transition. Its scores are L
+// alone and are formed on the drain's warps, two chunks ahead, in P U's place, while the prep's warps form T
+// one chunk ahead: 2.3 us a chunk against 2.7 with both on the prep's warps (with O there is no such place:
+// the product lies over the increment's second half for as long as that is free).
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(NT, 1)
 gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
@@ -112,7 +115,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
     uint64_t* fin = s_ready + 16;
     uint64_t* o_empty = s_ready + 17;       // O read out (4 warps)
     uint64_t* gt_ready = s_ready + 18;      // [NG] a chunk's gates written
-    uint64_t* l_ready = gt_ready + NG;      // without O: L written (2 warps)
+    uint64_t* l_ready = gt_ready + NG;      // without O: L written (4 warps)
     uint64_t* d_free = l_ready + 1;         // and its diagonal blocks done with
     uint32_t* holder = reinterpret_cast<uint32_t*>(l_ready + 2);
     const Abort abort_flag(l_ready + 3);
@@ -128,7 +131,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * NKQ + 2 * NV; ++i) mbar_init(&bar[i], 1);
-        for (int i = 0; i < 20 + NG; ++i) mbar_init(&s_ready[i], i == 7 && !OUT ? 2 : i < 10 ? 8 : i == 17 ? 4 : i == 18 + NG ? 2 : 1);
+        for (int i = 0; i < 20 + NG; ++i) mbar_init(&s_ready[i], i == 7 && !OUT ? 4 : i < 10 ? 8 : i == 17 || i == 18 + NG ? 4 : 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -153,13 +156,14 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 if (m >= NKQ) wait(&kq_empty[st], ((m / NKQ) - 1) & 1, abort_flag, status, ERR_TMA);
                 __syncwarp();
                 if (elect_one()) {
-                    // K's and Q's slab of the same 64 keys side by side: 128 rows of one operand
-                    mbar_arrive_expect_tx(&kq_full[st], (OUT ? 2 : 1) * L::KB);
+                    // K's and Q's slab of the same 64 keys side by side: 128 rows of one operand (without O
+                    // K's twice, so that two warps read the product's longer rows)
+                    mbar_arrive_expect_tx(&kq_full[st], 2 * L::KB);
                     uint8_t* sb = sm + L::KQ_OFF + st * 2 * L::KB;
 #pragma unroll
                     for (int i = 0; i < DK / 64; ++i) {
                         tma_load_3d(sb + 2 * i * SLAB, &mp.k, &kq_full[st], 64 * i, t0, bk);
-                        if (OUT) tma_load_3d(sb + (2 * i + 1) * SLAB, &mp.q, &kq_full[st], 64 * i, t0, bk);
+                        tma_load_3d(sb + (2 * i + 1) * SLAB, OUT ? &mp.q : &mp.k, &kq_full[st], 64 * i, t0, bk);
                     }
                 }
                 __syncwarp();
@@ -208,7 +212,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
             // cycles of moves, twice its time on the tensor cores).
             const uint32_t id64 = idesc_bf16(128, 64, false, false), idS = idesc_bf16(128, DK, false, true);
             const uint32_t idV = idesc_bf16(128, 64, true, false), idH = idesc_bf16(128, 64, false, true);
-            // chunk m's K on Q (128 rows; without O nothing reads Q's) against K
+            // chunk m's K on Q (128 rows) against K
             auto gram = [&](int m) {
                 const int st = m % NKQ;
                 wait(&kq_full[st], (m / NKQ) & 1, abort_flag, status, ERR_MMA);
@@ -490,8 +494,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
     } else if (wg == 3) {
         // ---------------------------------------------------------- drain of O; without O, the scores
         regs_dec<OUT ? 48 : 64>();
-        if (!OUT && (warp & 3) < 2) {
-            // tensor-memory lanes 0-63: the rows of L
+        if (!OUT) {
             for (int m = 0; m < n; ++m) {
                 const float* gt = reinterpret_cast<const float*>(sm + L::G_OFF + (m % NG) * L::GB);
                 float* diag = reinterpret_cast<float*>(sm + L::D_OFF);
@@ -499,9 +502,8 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 wait(g_full, m & 1, abort_flag, status, ERR_PREP);
                 if (m > 0) wait(d_free, (m - 1) & 1, abort_flag, status, ERR_PREP);
                 tc_fence_after();
-#pragma unroll 1
-                for (int x = 0; x < 2; ++x)
-                    chunk_scores(tm + tG, gt, a.scale, s0 + L::TP_OFF + (m % NV) * 4 * SLAB, diag, (warp & 3) + 4 * x);
+                // lanes 0-63: L's columns 0-31, 64-127: columns 32-63
+                chunk_scores<true>(tm + tG, gt, 1.f, s0 + L::TP_OFF + (m % NV) * 4 * SLAB, diag, (warp & 3) + (warp & 2) * 2);
                 tc_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -564,7 +566,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 wait(&gt_ready[m % NG], (m / NG) & 1, abort_flag, status, ERR_PREP);
                 wait(g_full, m & 1, abort_flag, status, ERR_PREP);
                 tc_fence_after();
-                chunk_scores(tm + tG, gt, a.scale, tb, diag, pw);
+                chunk_scores<false>(tm + tG, gt, a.scale, tb, diag, pw);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(g_read);

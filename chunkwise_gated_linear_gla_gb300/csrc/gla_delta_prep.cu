@@ -109,7 +109,7 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
     __syncthreads();     // the tiles are read: T and P may take their place
     tc_fence_after();
     chunk_zeros(s0, warp);
-    chunk_scores(tD, gt, a.scale, s0, diag, warp);
+    chunk_scores<false>(tD, gt, a.scale, s0, diag, warp);
     tc_fence_before();
     __syncthreads();
     if (warp == 4) {

@@ -162,17 +162,18 @@ __device__ __forceinline__ void chunk_zeros(uint32_t tb, int pw)
         sts4(sw(tb + (quarter >= 2 ? 2 * SLAB : 0) + (x >> 2) * SLAB, i, 4 + (x & 3)), 0u, 0u, 0u, 0u);
 }
 
-// K on Q against K (128 tensor-memory lanes from tG) to L's pieces below the 16-row diagonal blocks and to
-// P, both masked and decayed; L's diagonal blocks to fp32.
+// K on Q (KK: on K again) against K, 128 tensor-memory lanes from tG, to L's pieces below the 16-row diagonal
+// blocks and to P, both masked and decayed; L's diagonal blocks to fp32. A warp takes 32 rows, its quarter
+// of the lanes, by 32 columns.
+template <bool KK>
 __device__ __forceinline__ void chunk_scores(uint32_t tG, const float* gt, float scale, uint32_t tb, float* diag, int pw)
 {
     const int lane = threadIdx.x & 31, quarter = pw & 3, c0 = (pw >> 2) * 32;
+    const bool isP = !KK && quarter >= 2;
     const int i = (quarter & 1) * 32 + lane;      // row of the chunk
-    const bool isP = quarter >= 2;
     // of the warps' 32 x 32 pieces the one above the diagonal is zero, the one below needs no mask
     const bool above = !(quarter & 1) && c0 > 0, below = (quarter & 1) && c0 == 0;
     if (!above) {
-        // tensor-memory lanes 0-63: rows of L; 64-127: rows of P
         const bool near = gt[4 * C] != 0.f;
         const float f = isP ? scale : 1.f;
         const int last = below ? C : isP ? i : i - 1;
