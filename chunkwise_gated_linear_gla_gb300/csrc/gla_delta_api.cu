@@ -45,24 +45,34 @@ bool chunk_shape_ok(int B, int H, int T, int dk, int dv, int dtype)
 
 struct DeltaPlan {
     int path = GLA_PATH_SIMT;
-    int nch = 0, cps = 0, nseg = 1;
+    int nch = 0, cps = 0, nseg = 1, per = 1;
     size_t off_pair = 0, off_in = 0;
     size_t ws = 0;
 };
 
 // Segments of the sequence. The pass is serial over the chunks of a head's 128 dv columns, so few
 // heads leave SMs idle. Cut into n segments the pass takes two walks of nch / n chunks (the first, of
-// all segments but the last, has one more tile per head for the transitions), a scan of 1.1 chunks' time
-// per segment (3.2 us against 2.3 and 2.9) and about four for the launches; n is the best of those that one
-// wave of the first walk holds (16384 tokens, dk = dv = 128, one head: uncut 757 us, 5 segments 314, 20 161,
-// 40 179; 16 heads: uncut 747, 5 317, 6, whose walk takes two waves, 374).
-int choose_segments(int units, int trans, int nch, int sms)
+// all segments but the last, has one more tile per head for the transitions; 2.4 and 3.3 us a chunk with all
+// SMs busy) and a scan of 3.5 us per segment and wave of its blocks (16 columns each). Where one wave does not
+// hold the first walk's segments, its CTAs take two each, one after the other, if it holds them so.
+int segments_per_cta(int n, int units, int trans, int sms)
 {
-    const int most = std::min(1 + sms / (units + trans), nch / 4);
+    const long long u = (long long)units + trans;
+    return (n - 1) * u > sms && n / 2 * u <= sms ? 2 : 1;
+}
+// The best n of those that take one wave each time, by these rates and 12 us of launches (16384 tokens,
+// dk = dv = 128, one head: uncut 757 us, 5 segments 316, 20 162, 40 184; 16 heads: uncut 750, 5 segments
+// 322, 9, two to a CTA, 289, 12 in several waves 365).
+int choose_segments(int units, int trans, int dv, int nch, int sms)
+{
+    const int most = std::min(sms / units, nch / 4);
+    const long long waves = ((long long)trans * (dv / 16) + sms - 1) / sms;
     int best = 1;
-    long long least = 10LL * nch - 40;
+    long long least = 29LL * nch - 120;
     for (int n = 3; n <= most; ++n) {
-        const long long cost = 20LL * ((nch + n - 1) / n) + 11 * n;
+        const int per = segments_per_cta(n, units, trans, sms);
+        if ((long long)(per == 2 ? n / 2 : n - 1) * (units + trans) > sms) continue;
+        const long long cost = (24LL * per + 33) * ((nch + n - 1) / n) + 35 * waves * n;
         if (cost < least) { least = cost; best = n; }
     }
     return best;
@@ -85,11 +95,12 @@ gla_status plan_fwd(const gla_delta_params* p, DeltaPlan& pl)
     if (device_ready(&sms) != GLA_OK) sms = 152;
     const int BH = p->B * p->H;
     int n = p->force_segments > 0 ? p->force_segments
-                                  : choose_segments((int)units, BH, pl.nch, sms);
+                                  : choose_segments((int)units, BH, p->dv, pl.nch, sms);
     if (n > pl.nch) n = pl.nch;
     if (n > 65535) n = 65535;
     pl.cps = (pl.nch + n - 1) / n;
     pl.nseg = (pl.nch + pl.cps - 1) / pl.cps;
+    pl.per = segments_per_cta(pl.nseg, (int)units, BH, sms);
     if (pl.nseg > 1) {
         const size_t st4 = (size_t)p->dk * p->dv * 4, m4 = (size_t)p->dk * p->dk * 4;
         size_t off = 0;
@@ -300,7 +311,7 @@ gla_status gla_delta_fwd(const gla_delta_params* p, cudaStream_t stream)
         a.pair = pl.ws ? reinterpret_cast<float*>(ws + pl.off_pair) : nullptr;
         a.seg_in = pl.ws ? reinterpret_cast<float*>(ws + pl.off_in) : nullptr;
         a.B = p->B; a.H = p->H; a.Hk = p->Hk; a.T = p->T; a.dk = p->dk; a.dv = p->dv;
-        a.nch = pl.nch; a.cps = pl.cps; a.nseg = pl.nseg; a.scale = p->scale;
+        a.nch = pl.nch; a.cps = pl.cps; a.nseg = pl.nseg; a.per = pl.per; a.scale = p->scale;
         e = launch_delta_chunks(a, status, stream);
     } else {
         e = launch_delta_step(step_args(p, sms), stream);

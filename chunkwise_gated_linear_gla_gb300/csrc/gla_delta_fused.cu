@@ -77,7 +77,7 @@ struct FusedArgs {
     const float* log_g; const __nv_bfloat16* beta;
     const float* S_in; float* S_out;      // + bh * s_bh + segment * s_seg
     long long in_bh, in_seg, out_bh, out_seg;
-    int H, Hk, T, dv, nch, cps, nseg, tiles;
+    int H, Hk, T, dv, nch, cps, nseg, per, tiles;   // without O cps are the chunks of `per` segments
     float scale;
     int* status;
 };
@@ -411,6 +411,21 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
             }
             signal(&s_ready[p]);
         };
+        // to pair j (without O: a transition lies after the states)
+        auto put_out = [&](int j) {
+            if (!a.S_out || !in) return;
+            float* S = a.S_out + bh * a.out_bh + j * a.out_seg + (ident ? (size_t)DK * a.dv : 0);
+            int w = dvs;
+            asm volatile("" : "+r"(w));              // (64 addresses, not to be kept over the chunks)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int i = 0; i < KP / 2; ++i) {
+                    float* o = S + sbase + (size_t)(key(p) + 2 * i) * w;
+                    o[0] = s[p][i].x;
+                    o[w] = s[p][i].y;
+                }
+        };
         if (n > 0) {
             put_state(0);
             put_state(1);
@@ -478,19 +493,12 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                     s[p][i] = fma2(make_float2(gend, gend), s[p][i], f2(x[2 * i], x[2 * i + 1]));
                 if (m + 1 < n) put_state(p);
             }
+            // the first of two segments
+            if (!OUT && a.per == 2 && m + 1 == a.cps / 2 && m + 1 < n) put_out(2 * seg);
         }
-        // the state after the last segment; without O every segment's, a transition after the states
-        if (a.S_out && in && (!OUT || seg == a.nseg - 1)) {
-            float* S = a.S_out + bh * a.out_bh + seg * a.out_seg + (ident ? (size_t)DK * a.dv : 0);
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int i = 0; i < KP / 2; ++i) {
-                    float* o = S + sbase + (size_t)(key(p) + 2 * i) * dvs;
-                    o[0] = s[p][i].x;
-                    o[dvs] = s[p][i].y;
-                }
-        }
+        // the state after the last segment; without O every segment's
+        if (!OUT) put_out(seg * a.per + (a.per == 2 && n > a.cps / 2));
+        else if (seg == a.nseg - 1) put_out(0);
     } else if (wg == 3) {
         // ---------------------------------------------------------- drain of O; without O, the scores
         regs_dec<OUT ? 48 : 64>();
@@ -593,7 +601,8 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
 
 // The states entering the segments: S_in[0] = S0, S_in[s + 1] = M_s S_in[s] + S*_s, with each segment's
 // (S* [dk][dv], M [dk][dk]) side by side, in fp32 (what this rounds stays in the state over all segments).
-// A block owns 16 columns of one head. Each of its four groups of 64 threads sums over a quarter of the
+// With two segments a CTA the second's pair is of both: S_in[2 s + 2] = M S_in[2 s] + S*, as S_in[2 s + 1] is of the
+// first's. A block owns 16 columns of one head. Each of its four groups of 64 threads sums over a quarter of the
 // keys, DK / 16 rows by four columns a thread (16-byte loads from shared memory are what bounds it: twice
 // as many with smaller tiles and no groups, 4.3 us a segment against 3.2); neighbouring lanes take
 // neighbouring rows of M, which are padded by 16 bytes: no bank conflicts. The next segment's M and S* are on
@@ -606,7 +615,7 @@ struct SL {
 };
 template <int DK>
 __global__ void __launch_bounds__(256) gla_delta_scan_kernel(const float* __restrict__ S0, const float* __restrict__ pair,
-                                                             float* S_in, int dv, int nseg)
+                                                             float* S_in, int dv, int nseg, int per)
 {
     using L = SL<DK>;
     constexpr int R = DK / 16, F = DK / 64;      // rows of a thread's tile; float4s of the block's columns a thread
@@ -642,7 +651,7 @@ __global__ void __launch_bounds__(256) gla_delta_scan_kernel(const float* __rest
 #pragma unroll
         for (int i = 0; i < F; ++i) {
             const int r = r0 + 64 * i;
-            *reinterpret_cast<float4*>(S + r * L::COLS + c) = x[i];
+            if (per == 1 || !(g & 1)) *reinterpret_cast<float4*>(S + r * L::COLS + c) = x[i];
             if (in) *reinterpret_cast<float4*>(out + g * st + (size_t)r * dv) = x[i];
         }
         if (g + 1 == nseg) break;
@@ -703,7 +712,7 @@ cudaError_t launch_dk(const DeltaChunks& p, const FusedMaps& m, int* status, cud
     const long long st = (long long)p.dk * p.dv;
     FusedArgs a;
     a.log_g = p.log_g; a.beta = static_cast<const __nv_bfloat16*>(p.beta);
-    a.H = p.H; a.Hk = p.Hk; a.T = p.T; a.dv = p.dv; a.nch = p.nch; a.cps = p.cps; a.nseg = p.nseg;
+    a.H = p.H; a.Hk = p.Hk; a.T = p.T; a.dv = p.dv; a.nch = p.nch; a.cps = p.cps; a.nseg = p.nseg; a.per = 1;
     a.tiles = (p.dv + DVT - 1) / DVT;
     a.scale = p.scale; a.status = status;
     const unsigned tiles = (unsigned)a.tiles;
@@ -711,14 +720,16 @@ cudaError_t launch_dk(const DeltaChunks& p, const FusedMaps& m, int* status, cud
         // every segment but the last: its state from zero and its transition
         a.S_in = nullptr; a.in_bh = a.in_seg = 0;
         a.S_out = p.pair; a.out_seg = st + (long long)p.dk * p.dk; a.out_bh = a.out_seg * (p.nseg - 1);
-        cudaError_t e = launch_pass<DK, false>(a, m, dim3(tiles + 1, BH, p.nseg - 1), s);
+        a.per = p.per; a.cps = p.cps * p.per; a.nch = (p.nseg - 1) * p.cps;
+        cudaError_t e = launch_pass<DK, false>(a, m, dim3(tiles + 1, BH, p.per == 2 ? p.nseg / 2 : p.nseg - 1), s);
         if (e != cudaSuccess) return e;
         constexpr int smem = SL<DK>::SMEM, cols = SL<DK>::COLS;
         e = cudaFuncSetAttribute(gla_delta_scan_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        gla_delta_scan_kernel<DK><<<dim3((p.dv + cols - 1) / cols, BH), 256, smem, s>>>(p.S0, p.pair, p.seg_in, p.dv, p.nseg);
+        gla_delta_scan_kernel<DK><<<dim3((p.dv + cols - 1) / cols, BH), 256, smem, s>>>(p.S0, p.pair, p.seg_in, p.dv, p.nseg, p.per);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
+        a.cps = p.cps; a.nch = p.nch;
         a.S_in = p.seg_in; a.in_bh = st * p.nseg; a.in_seg = st;
     } else {
         a.S_in = p.S0; a.in_bh = st; a.in_seg = 0;

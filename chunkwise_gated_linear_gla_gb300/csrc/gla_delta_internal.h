@@ -80,7 +80,7 @@ cudaError_t launch_delta_prep(const DeltaPrep& a, int* status, cudaStream_t s);
 struct DeltaChunks {
     const void* q; const void* k; const void* v; const float* log_g; const void* beta;
     const float* S0; void* O; float* ST; float* pair; float* seg_in;
-    int B, H, Hk, T, dk, dv, nch, cps, nseg;
+    int B, H, Hk, T, dk, dv, nch, cps, nseg, per;   // per: segments that one CTA of the first walk takes
     float scale;
 };
 cudaError_t launch_delta_chunks(const DeltaChunks& a, int* status, cudaStream_t s);

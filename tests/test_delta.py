@@ -206,6 +206,20 @@ def test_cut_sequences(dk, dv, T, gate, segments):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,segments", [(40, 3), (24, 5), (24, 6), (24, 7), (20, 4), (16, 8), (16, 9)])
+@pytest.mark.parametrize("T", [320, 900])
+def test_cut_sequences_of_more_heads(H, segments, T):
+    """Two segments to a CTA of the first walk where one wave would not hold them singly; odd and even numbers."""
+    x = ref.make(1, H, H // 2, T, 64, 64, torch.bfloat16, seed=T + segments)[0]
+    O, S = ref.delta(*ref.f64(x), 64 ** -0.5)
+    got_O, got_S = gla.delta_forward(*ref.cuda(x), path=gla.GLA_PATH_TENSOR, force_segments=segments)
+    torch.cuda.synchronize()
+    assert gla.gla_device_status() == 0
+    assert_close(to_np(got_O), to_np(O), torch.bfloat16, "O")
+    close(got_S, S, 6 * PARTS, "S_T")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 64, 65, 100, 127, 128])
 def test_more_segments_than_chunks(T):
     x = ref.make(1, 2, 2, T, 64, 64, torch.bfloat16, seed=T)[0]
