@@ -715,10 +715,13 @@ def gla_qk_norm_rope_bwd_workspace_size(p: gla_qk_norm_params) -> int:
     return load().gla_qk_norm_rope_bwd_workspace_size(ctypes.byref(p))
 
 
-def _strides(t):
+_Steps = ctypes.c_longlong * 3
+_NO_STEPS = _Steps()
+
+
+def _steps(s, B, H, T):
     """(batch, head, token) strides; those of dimensions of one are never stepped and count as 0."""
-    (a, b, c, _), (x, y, z, _) = t.shape, t.stride()
-    return x if a > 1 else 0, y if b > 1 else 0, z if c > 1 else 0
+    return _Steps(s[0] if B > 1 else 0, s[1] if H > 1 else 0, s[2] if T > 1 else 0)
 
 
 def _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved):
@@ -728,20 +731,22 @@ def _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleave
     if q.dim() != 4:
         _refuse("q has four dimensions: [B,H,T,d]")
     B, H, T, d = q.shape
-    code, dev = _dtype_code(q, "q"), q.device
-    Hk = 0
+    dt, dev, f32 = q.dtype, q.device, torch.float32
+    code = _dtype_code(q, "q")
+    qs, ks, Hk, pk = q.stride(), None, 0, None
     if k is not None:
         if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, T, d):
             _refuse(f"k has shape {tuple(k.shape)}, not [{B},Hk,{T},{d}]")
-        if k.dtype != q.dtype or k.device != dev:
+        if k.dtype != dt or k.device != dev:
             _refuse("k has another type or device than q")
-        Hk = k.shape[1]
-    for t, what in ((q, "q"), (k, "k")):
-        if t is not None and t.stride(3) != 1 and d > 1:
+        ks, Hk, pk = k.stride(), k.shape[1], _ptr(k)
+    for s, what in ((qs, "q"), (ks, "k")):
+        if s is not None and s[3] != 1 and d > 1:
             _refuse(f"the last dimension of {what} is not contiguous")
+    # one look at each; what is wrong is told below
     for w, what in ((w_q, "w_q"), (w_k, "w_k")):
-        if w is not None:
-            _dense(w, (d,), torch.float32, dev, what)
+        if w is not None and not (w.shape == (d,) and w.dtype is f32 and w.device == dev and w.is_contiguous()):
+            _dense(w, (d,), f32, dev, what)
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
@@ -749,8 +754,8 @@ def _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleave
     if positions is not None:
         _dense(positions, (B, T), torch.int64, dev, "positions")
     _on_gpu(q, "q")
-    return gla_qk_norm_params(_ptr(q), _ptr(k), _strides(q), (0, 0, 0) if k is None else _strides(k), _ptr(w_q),
-                              _ptr(w_k), _ptr(inv_freq), _ptr(positions), start, B, H, Hk, T, d, rot,
+    return gla_qk_norm_params(_ptr(q), pk, _steps(qs, B, H, T), _NO_STEPS if ks is None else _steps(ks, B, Hk, T),
+                              _ptr(w_q), _ptr(w_k), _ptr(inv_freq), _ptr(positions), start, B, H, Hk, T, d, rot,
                               1 if interleaved else 0, _NORMS[norm], eps, code)
 
 
@@ -763,8 +768,8 @@ def qk_norm_rope_forward(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv
     import torch
     p = _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved)
     lib, dev = _lib or load(), q.device
-    qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    ko = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=dev)
+    qo = q.new_empty(q.shape)
+    ko = None if k is None else k.new_empty(k.shape)
     po, pk = _ptr(qo), _ptr(ko)
     _launch(lambda r, s: lib.gla_qk_norm_rope(r, po, pk, s), "gla_qk_norm_rope", p, dev, stream, qo, ko)
     return qo, ko
@@ -773,11 +778,10 @@ def qk_norm_rope_forward(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv
 def _rows_like(t):
     """An uninitialised tensor for t's gradient: token-major as a projection's slices are, when t is
     such a view, else dense."""
-    import torch
     if t.is_contiguous() or t.stride(1) >= t.stride(2):
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        return t.new_empty(t.shape)
     B, H, T, d = t.shape
-    return torch.empty((B, T, H, d), dtype=t.dtype, device=t.device).transpose(1, 2)
+    return t.new_empty((B, T, H, d)).transpose(1, 2)
 
 
 def _here_size(f, p, device):
@@ -802,8 +806,10 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, norm="l2", w_q=None, w_k=None, e
     gq, gk = _rows_like(q), None if k is None else _rows_like(k)
     gwq = None if w_q is None else torch.empty_like(w_q)
     gwk = None if w_k is None or k is None else torch.empty_like(w_k)
-    g = gla_qk_norm_grads(_ptr(dq_out), None if k is None else _ptr(dk_out), _ptr(gq), _ptr(gk), _strides(gq),
-                          (0, 0, 0) if k is None else _strides(gk), _ptr(gwq), _ptr(gwk))
+    B, H, T, _ = q.shape
+    g = gla_qk_norm_grads(_ptr(dq_out), None if k is None else _ptr(dk_out), _ptr(gq), _ptr(gk),
+                          _steps(gq.stride(), B, H, T),
+                          _NO_STEPS if k is None else _steps(gk.stride(), B, k.shape[1], T), _ptr(gwq), _ptr(gwk))
     n, ws = 0, None
     if gwq is not None or gwk is not None:
         n = _here_size(lib.gla_qk_norm_rope_bwd_workspace_size, p, dev)
