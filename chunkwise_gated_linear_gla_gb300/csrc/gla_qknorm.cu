@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(NT, BWD ? 3 : 4) gla_qk_norm_rope_kernel(QkArg
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) s = fmaf(x[j], x[j], s);
                     inv = rsqrtf(fmaf(row_sum<LPR>(s), invn, a.eps));
+                    if (BWD && !on) inv = 0.f;      // rows past the last token hold zeros: with eps = 0, 1 / 0
                 }
                 if constexpr (!BWD) {
 #pragma unroll
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(NT, BWD ? 3 : 4) gla_qk_norm_rope_kernel(QkArg
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
                         x[j] *= inv;                                    // x^
-                        dw[z][j] = fmaf(g[j], x[j], dw[z][j]);          // (rows past the last token hold zeros)
+                        dw[z][j] = fmaf(g[j], x[j], dw[z][j]);          // (rows past the last token: x^ = 0)
                         g[j] *= w[j];
                         s = fmaf(g[j], x[j], s);
                     }

@@ -163,6 +163,31 @@ def test_replays_from_a_cuda_graph_with_new_positions():
         assert torch.equal(a, b)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("norm", ["l2", "rms"])
+@pytest.mark.parametrize("d,T", [(64, 7), (128, 17), (256, 3)])
+def test_gradients_without_eps(d, T, norm, dtype):
+    """eps = 0 and tokens that do not fill the last block: its idle rows hold zeros, of which no inverse norm exists."""
+    proj, q, k, w, f, pos, g = case(1, 3, 1, T, d, 32, dtype, d + T, False, True)
+    kw = dict(norm=norm, w_q=w[0].cuda(), w_k=w[1].cuda(), eps=0.0, inv_freq=f.cuda())
+    oq, ok = gla.qk_norm_rope_forward(q.cuda(), k.cuda(), **kw)
+    xs = [t.double().requires_grad_(True) for t in (q, k, *w)]
+    at = torch.arange(T).expand(1, T)
+    want = [ref.norm_rope(xs[i], norm, xs[2 + i], 0.0, f, at, False) for i in (0, 1)]
+    rows_close(oq, want[0], dtype, "q")
+    rows_close(ok, want[1], dtype, "k")
+    dq, dk = torch.randn(oq.shape, generator=g).to(dtype), torch.randn(ok.shape, generator=g).to(dtype)
+    ref_g = torch.autograd.grad((want[0] * dq.double()).sum() + (want[1] * dk.double()).sum(), xs)
+    got = gla.qk_norm_rope_backward(q.cuda(), k.cuda(), dq.cuda(), dk.cuda(), **kw)
+    rows_close(got[0], ref_g[0], dtype, "dq")
+    rows_close(got[1], ref_g[1], dtype, "dk")
+    for a, b, n in ((got[2], ref_g[2], "dw_q"), (got[3], ref_g[3], "dw_k")):
+        assert torch.isfinite(a).all(), n
+        e = (a.double().cpu() - b).norm() / b.norm()
+        assert e <= 1e-5, f"{n}: {e:.1e}"
+
+
 # ---------------------------------------------------------------- refusals, no GPU needed
 
 def _params(**kw):
