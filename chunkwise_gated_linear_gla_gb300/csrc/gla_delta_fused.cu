@@ -117,8 +117,10 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
     uint64_t* gt_ready = s_ready + 18;      // [NG] a chunk's gates written
     uint64_t* l_ready = gt_ready + NG;      // without O: L written (4 warps)
     uint64_t* d_free = l_ready + 1;         // and its diagonal blocks done with
-    uint32_t* holder = reinterpret_cast<uint32_t*>(l_ready + 2);
-    const Abort abort_flag(l_ready + 3);
+    uint64_t* gt_free = l_ready + 2;        // [NG] a chunk's gates read by everyone (4 warps; without O one)
+    uint32_t* holder = reinterpret_cast<uint32_t*>(gt_free + NG);
+    const Abort abort_flag(gt_free + NG + 1);
+    static_assert((2 * NKQ + 2 * NV + 18 + 2 * NG + 4) * 8 <= 320, "barriers");
     const uint32_t tG = OUT ? L::tG : L::tOp;
 
     const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32, wg = warp / 4;
@@ -131,7 +133,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * NKQ + 2 * NV; ++i) mbar_init(&bar[i], 1);
-        for (int i = 0; i < 20 + NG; ++i) mbar_init(&s_ready[i], i == 7 && !OUT ? 4 : i < 10 ? 8 : i == 17 || i == 18 + NG ? 4 : 1);
+        for (int i = 0; i < 20 + 2 * NG; ++i) mbar_init(&s_ready[i], i == 7 && !OUT ? 4 : i < 10 ? 8 : i == 17 || i == 18 + NG || (OUT && i >= 20 + NG) ? 4 : 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -182,7 +184,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
             for (int m = max(0, kq - NKQ); m < kq; ++m) wait(&kq_full[m % NKQ], (m / NKQ) & 1, abort_flag, status, ERR_TMA);
             for (int m = max(0, v - NV); m < v; ++m) wait(&v_full[m % NV], (m / NV) & 1, abort_flag, status, ERR_TMA);
         } else if (warp == 3) {
-            // ------------------------------------------------------ gates, up to NG - 1 chunks ahead
+            // ------------------------------------------------------ gates, up to NG chunks ahead
             const float* lg = a.log_g ? a.log_g + (size_t)bh * a.T : nullptr;
             const __nv_bfloat16* bp = a.beta + (size_t)bh * a.T;
             float x0, x1, b0, b1;                           // two tokens of the next chunk
@@ -196,9 +198,10 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
             };
             if (n > 0) fetch(0);
             for (int m = 0; m < n; ++m) {
-                // the slot's last readers, chunk m - NG's register steps and drain, are done when the
-                // next chunk's increment is formed
-                if (m >= NG - 1) wait(&d_full[1], (m - NG + 1) & 1, abort_flag, status, ERR_PREP);
+                // A slot's barrier cannot get ahead of this wait: its next phase is chunk m's own. (One that also
+                // counts the chunks between could: two of them done and a wait by parity sees the third's, which
+                // cannot complete without chunk m's gates.)
+                if (m >= NG) wait(&gt_free[m % NG], ((m / NG) - 1) & 1, abort_flag, status, ERR_PREP);
                 __syncwarp();
                 chunk_gates(x0, x1, b0, b1, sm + L::G_OFF + (m % NG) * L::GB);
                 __syncwarp();
@@ -335,7 +338,10 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                             if (part) mma_commit(&d_full[nh]);
                         }
                         if (part && NH == 1) mma_commit(&d_full[1]);
-                        if (part && !OUT) mma_commit(&kq_empty[st]);
+                        if (part && !OUT) {
+                            mma_commit(&kq_empty[st]);
+                            mbar_arrive(&gt_free[m % NG]);    // without O the chain is the last reader
+                        }
                     }
                     __syncwarp();
                 }
@@ -551,7 +557,10 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 tc_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(o_empty);
+                if (lane == 0) {
+                    mbar_arrive(o_empty);
+                    mbar_arrive(&gt_free[m % NG]);    // (the last reader of a chunk's gates)
+                }
                 named_bar_sync(1, 128);
                 if (lead) {
                     tma_store_3d(&mp.o, sm + L::O_OFF, dv0, (first + m) * C, bh);
