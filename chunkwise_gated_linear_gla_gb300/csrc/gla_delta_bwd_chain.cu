@@ -108,13 +108,14 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
         regs_dec<56>();
         if (warp == 0) {
             int issued = 0;
-            for (int m = 0; m < n; ++m, ++issued) {
+            bool ok = true;                 // this lane's waits so far have come to their ends
+            for (int m = 0; m < n; ++m) {
                 if (__any_sync(~0u, *abort_flag)) break;
                 const int st = m % NST, c = chunk(m), t0 = c * C, at = bh * n + c;
-                if (m >= NST) wait(&empty[st], ((m / NST) - 1) & 1, abort_flag, status, ERR_TMA);
+                if (m >= NST) ok &= wait(&empty[st], ((m / NST) - 1) & 1, abort_flag, status, ERR_TMA);
                 __syncwarp();
                 uint8_t* sb = sm + st * L::STAGE;
-                if (elect_one()) {
+                if (elect_one() && ok) {
                     mbar_arrive_expect_tx(&full[st], L::BYTES);
                     tma_load_4d(sb + L::V_OFF, &mp.v, &full[st], 0, t0, dv0 / 64, bh);   // (slabs past dv: zeros)
                     tma_load_3d(sb + L::T_OFF, &mp.t, &full[st], 0, 0, at);
@@ -124,8 +125,12 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
                     if (REV) tma_load_4d(sb + L::Q_OFF, &mp.q, &full[st], 0, t0, 0, bk);
                 }
                 __syncwarp();
+                issued += ok;
             }
-            for (int m = max(0, issued - NST); m < issued; ++m) wait(&full[m % NST], (m / NST) & 1, abort_flag, status, ERR_TMA);
+            // no copy may land after the CTA has ended
+            if (elect_one())
+                for (int m = max(0, issued - NST); m < issued; ++m) mbar_wait(&full[m % NST], (m / NST) & 1, kTimeoutNs);
+            __syncwarp();
         } else if (warp == 1) {
             const uint32_t id64 = idesc_bf16(128, 64, false, false), id64n = idesc_bf16(128, 64, false, true);
             const uint32_t idS = idesc_bf16(128, DK, false, true);
@@ -232,6 +237,7 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
             const int st = m % NST;
             const uint32_t ph = m & 1;
             const uint32_t gt = s0 + st * L::STAGE + L::G_OFF;
+            if (__any_sync(~0u, *abort_flag)) break;
             if (m > 0) wait(sp_free, (m - 1) & 1, abort_flag, status, ERR_EPI);
             tc_fence_after();
 #pragma unroll
@@ -318,11 +324,12 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
         const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
         const bool lead = threadIdx.x == NT - 128;
         const uint32_t ob = s0 + L::O_OFF;
-        // the buffer's last stores must have read it
+        // the buffer's last stores must have read it; false, to all four warps, when they have to quit
         auto buffer_free = [&]() {
             if (lead) bulk_wait_read0();
-            named_bar_sync(1, 128);
+            return !named_bar_any(1, 128, *abort_flag);
         };
+        bool on = true;
         auto buffer_full = [&]() {
             fence_proxy_async_smem();
             named_bar_sync(1, 128);
@@ -374,7 +381,8 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
             tc_fence_after();
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-                buffer_free();
+                on = on && buffer_free();
+                if (!on) break;
 #pragma unroll
                 for (int x = 0; x < DK / 2; x += 16) {
                     uint32_t r[16];
@@ -395,10 +403,12 @@ gla_delta_sweep_kernel(DeltaSweep a, const __grid_constant__ Maps mp, int* statu
                     bulk_commit();
                 }
             }
+            if (!on) break;
             // U: [dv][64 tokens]; dV: [64 tokens][dv]
             wait(u_full, ph, abort_flag, status, ERR_DRAIN);
             tc_fence_after();
-            buffer_free();
+            on = buffer_free();
+            if (!on) break;
 #pragma unroll
             for (int x = 0; x < C; x += 32) {
                 uint32_t r[32], hi[16], lo[16];

@@ -12,7 +12,7 @@ namespace delta {
 
 constexpr int C = kChunk;
 constexpr int SLAB = C * 128;                     // 64 rows of 128 bytes: one swizzled TMA box
-constexpr uint64_t kTimeoutNs = 2000000000ull;    // per wait
+constexpr uint64_t kTimeoutNs = 2000000000ull;    // of the waits, after a role's loop, for what is in flight
 
 // A CTA's abort flag and the time at which its waits give up: between 4.3 and 8.6 seconds after its
 // start (the upper word of the nanosecond clock, two steps on).
@@ -26,11 +26,18 @@ struct Abort {
     __device__ __forceinline__ volatile int& operator*() const { return *flag; }
 };
 
-// Bounded wait. When it runs out the caller goes on without waiting: every role keeps its sequence of
-// arrivals, and all of a CTA's roles give up at the same time, so the CTA ends; the status word
-// reports it. The loop is short on purpose: it is copied to every wait, and code that pushes the
-// roles' steps out of the instruction caches costs them dearly.
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, const Abort& abort_flag, int* status, int code)
+// Bounded wait; false when it runs out. All of a CTA's roles give up at the same time; the status word
+// reports it. From then on
+//   - a thread that issues copies issues none any more (its own waits tell it; of the products, which stay in
+//     the CTA's own memories, the rest of a chunk's may follow: asking at each costs the passes 3%),
+//   - roles leave their loops at the next look at the flag: a warp on its own by a vote, warps that share
+//     a named barrier by that barrier's word (the same for all of them); until then they go on without
+//     waiting, on what their buffers hold,
+//   - who issued copies or products waits for them, with a limit of its own, before the CTA frees its
+//     tensor memory and ends.
+// The loop is short on purpose: it is copied to every wait, and code that pushes the roles' steps out of
+// the instruction caches costs them dearly.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Abort& abort_flag, int* status, int code)
 {
 #pragma unroll 1
     while (!sm100::mbar_try_wait(bar, parity)) {
@@ -39,9 +46,20 @@ __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, const Abort
         if ((int)(now - abort_flag.deadline) >= 0) {
             *abort_flag = 1;
             atomicExch(status, code);
-            return;
+            return false;
         }
     }
+    return true;
+}
+
+// bar.sync of `n` threads that tells all of them the same: whether any of them said yes.
+__device__ __forceinline__ bool named_bar_any(int id, int n, bool x)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(id), "r"(n), "r"((uint32_t)x) : "memory");
+    return r != 0;
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }

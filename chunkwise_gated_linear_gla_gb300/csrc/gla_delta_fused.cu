@@ -152,12 +152,13 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
         if (warp == 0) {
             // ------------------------------------------------------ TMA producer
             int kq = 0, v = 0;
+            bool ok = true;                 // this lane's waits so far have come to their ends
             for (int m = 0; m < n; ++m) {
                 if (__any_sync(~0u, *abort_flag)) break;
                 const int t0 = (first + m) * C, st = m % NKQ;
-                if (m >= NKQ) wait(&kq_empty[st], ((m / NKQ) - 1) & 1, abort_flag, status, ERR_TMA);
+                if (m >= NKQ) ok &= wait(&kq_empty[st], ((m / NKQ) - 1) & 1, abort_flag, status, ERR_TMA);
                 __syncwarp();
-                if (elect_one()) {
+                if (elect_one() && ok) {
                     // K's and Q's slab of the same 64 keys side by side: 128 rows of one operand (without O
                     // K's twice, so that two warps read the product's longer rows)
                     mbar_arrive_expect_tx(&kq_full[st], 2 * L::KB);
@@ -169,20 +170,24 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                     }
                 }
                 __syncwarp();
-                ++kq;
+                kq += ok;
                 if (ident) continue;
-                if (m >= NV) wait(&v_empty[m % NV], ((m / NV) - 1) & 1, abort_flag, status, ERR_TMA);
+                if (m >= NV) ok &= wait(&v_empty[m % NV], ((m / NV) - 1) & 1, abort_flag, status, ERR_TMA);
                 __syncwarp();
-                if (elect_one()) {
+                if (elect_one() && ok) {
                     mbar_arrive_expect_tx(&v_full[m % NV], 2 * SLAB);
                     // (slabs past dv: zeros)
                     tma_load_4d(sm + L::V_OFF + (m % NV) * 2 * SLAB, &mp.v, &v_full[m % NV], 0, t0, dv0 / 64, bh);
                 }
                 __syncwarp();
-                ++v;
+                v += ok;
             }
-            for (int m = max(0, kq - NKQ); m < kq; ++m) wait(&kq_full[m % NKQ], (m / NKQ) & 1, abort_flag, status, ERR_TMA);
-            for (int m = max(0, v - NV); m < v; ++m) wait(&v_full[m % NV], (m / NV) & 1, abort_flag, status, ERR_TMA);
+            // no copy may land after the CTA has ended
+            if (elect_one()) {
+                for (int m = max(0, kq - NKQ); m < kq; ++m) mbar_wait(&kq_full[m % NKQ], (m / NKQ) & 1, kTimeoutNs);
+                for (int m = max(0, v - NV); m < v; ++m) mbar_wait(&v_full[m % NV], (m / NV) & 1, kTimeoutNs);
+            }
+            __syncwarp();
         } else if (warp == 3) {
             // ------------------------------------------------------ gates, up to NG chunks ahead
             const float* lg = a.log_g ? a.log_g + (size_t)bh * a.T : nullptr;
@@ -201,8 +206,8 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 // A slot's barrier cannot get ahead of this wait: its next phase is chunk m's own. (One that also
                 // counts the chunks between could: two of them done and a wait by parity sees the third's, which
                 // cannot complete without chunk m's gates.)
-                if (m >= NG) wait(&gt_free[m % NG], ((m / NG) - 1) & 1, abort_flag, status, ERR_PREP);
-                __syncwarp();
+                const bool ok = m < NG || wait(&gt_free[m % NG], ((m / NG) - 1) & 1, abort_flag, status, ERR_PREP);
+                if (!__all_sync(~0u, ok)) break;
                 chunk_gates(x0, x1, b0, b1, sm + L::G_OFF + (m % NG) * L::GB);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&gt_ready[m % NG]);
@@ -437,6 +442,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
             put_state(1);
         }
         for (int m = 0; m < n; ++m) {
+            if (__any_sync(~0u, *abort_flag)) break;
             const uint32_t ph = m & 1;
             const uint32_t gt = s0 + L::G_OFF + (m % NG) * L::GB;
             wait(&t_ready[m & 1], (m >> 1) & 1, abort_flag, status, ERR_EPI);
@@ -510,6 +516,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
         regs_dec<OUT ? 48 : 64>();
         if (!OUT) {
             for (int m = 0; m < n; ++m) {
+                if (__any_sync(~0u, *abort_flag)) break;
                 const float* gt = reinterpret_cast<const float*>(sm + L::G_OFF + (m % NG) * L::GB);
                 float* diag = reinterpret_cast<float*>(sm + L::D_OFF);
                 wait(&gt_ready[m % NG], (m / NG) & 1, abort_flag, status, ERR_PREP);
@@ -538,7 +545,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 tc_fence_after();
                 // the tile's last store must have read it
                 if (lead) bulk_wait_read0();
-                named_bar_sync(1, 128);
+                if (named_bar_any(1, 128, *abort_flag)) break;
 #pragma unroll 1
                 for (int c = 0; c < 64; c += 16) {
                     uint32_t x[16], y[16];
@@ -592,9 +599,10 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                 wait(l_ready, m & 1, abort_flag, status, ERR_PREP);
                 __syncwarp();
             }
-            chunk_inverse(tb, s0 + L::W_OFF, gt, diag, pw, [&] {
-                if (!OUT && threadIdx.x == 512) mbar_arrive(d_free);
-            });
+            if (!chunk_inverse(tb, s0 + L::W_OFF, gt, diag, pw, *abort_flag, [&] {
+                    if (!OUT && threadIdx.x == 512) mbar_arrive(d_free);
+                }))
+                break;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&t_ready[m & 1]);

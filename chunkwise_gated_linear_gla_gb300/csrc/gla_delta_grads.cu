@@ -80,8 +80,9 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     uint64_t* m_1 = bar + 6;     // products with U^T and S^T done
     uint64_t* m_3 = bar + 7;     // products with dS^T done
     uint64_t* m_h = bar + 8;     // products of W and M done
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 9);
-    const Abort abort_flag(bar + 10);
+    uint64_t* fin = bar + 9;     // every product done
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 10);
+    const Abort abort_flag(bar + 11);
     float* gt = reinterpret_cast<float*>(sm + L::G_OFF);
     float* rs = reinterpret_cast<float*>(sm + L::R_OFF);        // [4][64] row sums
     float* ss = rs + 4 * C;                                     // [4][64] k . (l U dS^T)
@@ -92,7 +93,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     const int total = a.B * a.H * a.nch;
 
     if (tid == 0) {
-        for (int i = 0; i < 9; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < 10; ++i) mbar_init(&bar[i], 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -112,11 +113,20 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     const uint32_t tm = *holder;
 
     int it = 0, cnt = 0;                // chunks done, and tiles of dv: the barriers' phases
+    // this thread's waits so far have come to their ends (else it issues nothing any more); in the thread that
+    // loads, the barriers that it has armed and the parities of their next phases
+    bool ok = true;
+    uint32_t armed = 0, next = 0;
+    auto arm = [&](uint64_t* x, uint32_t bytes) {
+        armed |= 1u << (x - bar);
+        next ^= 1u << (x - bar);
+        mbar_arrive_expect_tx(x, bytes);
+    };
     for (int at = blockIdx.x; at < total; at += gridDim.x, ++it) {
     const int c = at % a.nch, bh = at / a.nch, t0 = c * C;
     const int b = bh / a.H, h = bh % a.H, bk = b * a.Hk + h / (a.H / a.Hk);
     auto load_s = [&](int chunk, int dv0) {
-        mbar_arrive_expect_tx(b_s, 2 * L::SB);
+        arm(b_s, 2 * L::SB);
 #pragma unroll
         for (int i = 0; i < L::NS; ++i) {
             tma_load_3d(sm + L::S_OFF + i * 2 * SLAB, &mp.sh, b_s, 64 * i, dv0, chunk);
@@ -125,7 +135,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     };
     // (tiles of dv that end inside the pair of slabs are filled with zeros)
     auto load_xa = [&](int chunk, int dv0) {
-        mbar_arrive_expect_tx(b_xa, 4 * SLAB);
+        arm(b_xa, 4 * SLAB);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             tma_load_3d(sm + L::XA_OFF + 2 * i * SLAB, &mp.dO, b_xa, dv0 + 64 * i, chunk % a.nch * C, chunk / a.nch);
@@ -133,7 +143,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
         }
     };
     auto load_u = [&](int chunk, int dv0) {
-        mbar_arrive_expect_tx(b_u, 4 * SLAB);
+        arm(b_u, 4 * SLAB);
         tma_load_3d(sm + L::U_OFF, &mp.uh, b_u, 0, dv0, chunk);
         tma_load_3d(sm + L::U_OFF + 2 * SLAB, &mp.ul, b_u, 0, dv0, chunk);
     };
@@ -143,9 +153,9 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
         const int dv0 = vt * 128;
         const uint32_t ph = cnt & 1;
         if (warp == 0) {
-            if (lane == 0) {
+            if (lane == 0 && ok) {
                 if (vt == 0) {
-                    mbar_arrive_expect_tx(b_qk, 2 * L::NS * SLAB + 8 * C * 4);
+                    arm(b_qk, 2 * L::NS * SLAB + 8 * C * 4);
 #pragma unroll
                     for (int i = 0; i < L::NS; ++i) {
                         tma_load_3d(sm + L::QK_OFF + 2 * i * SLAB, &mp.q, b_qk, 64 * i, t0, bk);
@@ -153,7 +163,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                     }
                     bulk_load(gt, a.gates + (size_t)at * 8 * C, 8 * C * 4, b_qk);
                 }
-                mbar_arrive_expect_tx(b_xb, 2 * SLAB);
+                arm(b_xb, 2 * SLAB);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     tma_load_3d(sm + L::XB_OFF + (2 * i + 1) * SLAB, &mp.xl, b_xb, dv0 + 64 * i, t0, bh);
@@ -168,10 +178,10 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             const uint64_t dU = sdesc(s0 + L::U_OFF, 2 * SLAB, 1024, kSwizzle128);
             const uint64_t dS = sdesc(s0 + L::S_OFF, 2 * SLAB, 1024, kSwizzle128);
             const uint32_t id1 = idesc_bf16(128, 64, false, true), id2 = idesc_bf16(128, DK, false, true);
-            wait(b_xa, ph, abort_flag, status, ERR_LOAD);
-            wait(b_u, ph, abort_flag, status, ERR_LOAD);
+            ok &= wait(b_xa, ph, abort_flag, status, ERR_LOAD);
+            ok &= wait(b_u, ph, abort_flag, status, ERR_LOAD);
             __syncwarp();
-            if (elect_one()) {
+            if (elect_one() && ok) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
                     const uint64_t o = ((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4, r = (kk * 2048) >> 4;
@@ -179,9 +189,9 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                     mma_ss(tm + L::t1, dXa + o, dU + (2 * SLAB >> 4) + r, id1, 1);
                 }
             }
-            wait(b_s, ph, abort_flag, status, ERR_LOAD);
+            ok &= wait(b_s, ph, abort_flag, status, ERR_LOAD);
             __syncwarp();
-            if (elect_one()) {
+            if (elect_one() && ok) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
                     const uint64_t o = ((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4, r = (kk * 2048) >> 4;
@@ -189,9 +199,9 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                     mma_ss(tm + L::t2, dXa + o, dS + (L::SB >> 4) + r, id2, 1);
                 }
             }
-            wait(b_xb, ph, abort_flag, status, ERR_LOAD);
+            ok &= wait(b_xb, ph, abort_flag, status, ERR_LOAD);
             __syncwarp();
-            if (elect_one()) {
+            if (elect_one() && ok) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
                     const uint64_t o = ((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4, r = (kk * 2048) >> 4;
@@ -218,7 +228,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             return s0 + L::S_OFF + (k >> 3) * 2 * SLAB + r * 128 + (((k & 7) ^ (r & 7)) << 4);
         };
         float sv[NP][8];
-        wait(b_s, ph, abort_flag, status, ERR_LOAD);
+        ok &= wait(b_s, ph, abort_flag, status, ERR_LOAD);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             float v[8];
@@ -227,11 +237,11 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
 #pragma unroll
             for (int e = 0; e < 8; ++e) sv[p][e] += v[e];
         }
-        wait(m_1, ph, abort_flag, status, ERR_MMA);
+        ok &= wait(m_1, ph, abort_flag, status, ERR_MMA);
         __syncthreads();            // S is read by everyone: dS may take its place
         if (warp == 0) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(b_d, 2 * L::SB);
+            if (lane == 0 && ok) {
+                arm(b_d, 2 * L::SB);
 #pragma unroll
                 for (int i = 0; i < L::NS; ++i) {
                     tma_load_3d(sm + L::S_OFF + i * 2 * SLAB, &mp.dh, b_d, 64 * i, dv0, at);
@@ -243,9 +253,9 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             const uint64_t dU = sdesc(s0 + L::U_OFF, 2 * SLAB, 1024, kSwizzle128);   // tokens along M: U on U_lo
             const uint64_t dS = sdesc(s0 + L::S_OFF, 2 * SLAB, 1024, kSwizzle128);
             const uint32_t id3 = idesc_bf16(128, DK, true, true);
-            wait(b_d, ph, abort_flag, status, ERR_LOAD);
+            ok &= wait(b_d, ph, abort_flag, status, ERR_LOAD);
             __syncwarp();
-            if (elect_one()) {
+            if (elect_one() && ok) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
                     const uint64_t r = (kk * 2048) >> 4;
@@ -256,7 +266,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             }
             __syncwarp();
         }
-        wait(b_d, ph, abort_flag, status, ERR_LOAD);
+        ok &= wait(b_d, ph, abort_flag, status, ERR_LOAD);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             float u[8], v[8];
@@ -266,7 +276,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             for (int e = 0; e < 8; ++e) inner = fmaf(sv[p][e], u[e] + v[e], inner);
         }
         if (vt + 1 < ntile) {       // one set of tiles: the next load waits for these products
-            wait(m_3, ph, abort_flag, status, ERR_MMA);
+            ok &= wait(m_3, ph, abort_flag, status, ERR_MMA);
             __syncthreads();
         }
     }
@@ -277,7 +287,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     const bool low = row < 64;
     const uint32_t lb = (uint32_t)(quarter * 32) << 16;
     tc_fence_after();
-    wait(b_qk, it & 1, abort_flag, status, ERR_LOAD);
+    ok &= wait(b_qk, it & 1, abort_flag, status, ERR_LOAD);
     {
         const int c0 = hf * 32;
         uint32_t r[32];
@@ -336,7 +346,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
         const uint64_t dQ = sdesc(s0 + L::QK_OFF, 2 * SLAB, 1024, kSwizzle128);      // 128 rows [Q; K], keys along N
         const uint64_t dK = sdesc(s0 + L::QK_OFF + SLAB, 2 * SLAB, 1024, kSwizzle128);
         const uint32_t idH = idesc_bf16(128, DK, false, true), idT = idesc_bf16(128, DK, true, true);
-        if (elect_one()) {
+        if (elect_one() && ok) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
                 const uint64_t o = (kk * 32) >> 4, r = (kk * 2048) >> 4;
@@ -352,11 +362,11 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
         }
         __syncwarp();
     }
-    wait(m_3, (cnt - 1) & 1, abort_flag, status, ERR_MMA);
-    wait(m_h, it & 1, abort_flag, status, ERR_MMA);
+    ok &= wait(m_3, (cnt - 1) & 1, abort_flag, status, ERR_MMA);
+    ok &= wait(m_h, it & 1, abort_flag, status, ERR_MMA);
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && more) {
+    if (tid == 0 && more && ok) {
         // U and dS are used (and everyone has read dS): the next chunk's U and S take their place
         load_u(at + gridDim.x, 0);
         load_s(at + gridDim.x, 0);
@@ -470,8 +480,20 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     zero_slabs();
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();        // everything of this chunk is read: the next one's loads may land
+    // everything of this chunk is read: the next one's loads may land
+    const bool quit = __syncthreads_or(!ok);
     tc_fence_after();
+    if (quit) break;
+    }
+    // nothing may be in flight when the CTA ends (it is not, unless a wait has run out)
+    if (warp == 0) {
+        if (lane == 0)
+            for (int i = 0; i < 6; ++i)
+                if (armed >> i & 1) mbar_wait(&bar[i], (next >> i & 1) ^ 1, kTimeoutNs);
+        __syncwarp();
+        if (elect_one()) mma_commit(fin);
+        __syncwarp();
+        mbar_wait(fin, 0, kTimeoutNs);
     }
     tc_fence_before();
     __syncthreads();

@@ -88,25 +88,37 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tD = *holder;
+    bool ok = true, issued = false;     // this thread's waits have come to their ends; it has products in flight
     if (tid < 8 * C / 4)
         reinterpret_cast<float4*>(a.gates + (size_t)at * 8 * C)[tid] = reinterpret_cast<const float4*>(gt)[tid];
     if (warp == 1) {
-        wait(&bar[0], 0, abort_flag, status, ERR_LOAD);
+        ok = wait(&bar[0], 0, abort_flag, status, ERR_LOAD);
         __syncwarp();
         const uint32_t id = idesc_bf16(128, 64, false, false);
         const uint64_t d0 = sdesc(s0, 16, 1024, kSwizzle128);   // K on Q: 128 rows; K alone: 64
-        if (elect_one()) {
+        if (elect_one() && ok) {
 #pragma unroll
             for (int kk = 0; kk < DK / 16; ++kk) {
                 const uint64_t d = d0 + (((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4);
                 mma_ss(tD, d, d, id, kk > 0);
             }
             mma_commit(&bar[1]);
+            issued = true;
         }
         __syncwarp();
     }
-    wait(&bar[1], 0, abort_flag, status, ERR_MMA);
-    __syncthreads();     // the tiles are read: T and P may take their place
+    ok &= wait(&bar[1], 0, abort_flag, status, ERR_MMA);
+    if (__syncthreads_or(!ok)) {
+        // given up: what is in flight is waited for before the memory that it uses is left
+        if (warp == 1) {
+            mbar_wait(&bar[0], 0, kTimeoutNs);
+            if (issued) mbar_wait(&bar[1], 0, kTimeoutNs);
+            __syncwarp();
+            tmem_dealloc(tD, 64);
+        }
+        return;
+    }
+    // the tiles are read: T and P may take their place
     tc_fence_after();
     chunk_zeros(s0, warp);
     chunk_scores<false>(tD, gt, a.scale, s0, diag, warp);
@@ -116,7 +128,7 @@ gla_delta_prep_kernel(DeltaPrep a, const __grid_constant__ CUtensorMap tmK, cons
         tc_fence_after();
         tmem_dealloc(tD, 64);
     }
-    chunk_inverse(s0, s0 + L::W_OFF, gt, diag, warp, [] {});
+    chunk_inverse(s0, s0 + L::W_OFF, gt, diag, warp, false, [] {});
     fence_proxy_async_smem();
     __syncthreads();
     if (warp == 1) {

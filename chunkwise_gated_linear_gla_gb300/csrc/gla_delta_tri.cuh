@@ -230,9 +230,9 @@ __device__ __forceinline__ void chunk_scores(uint32_t tG, const float* gt, float
 }
 
 // T in place of L, from the diagonal blocks up. All 256 threads; ends without a barrier. `read` is called
-// once the fp32 diagonal blocks are done with.
+// once the fp32 diagonal blocks are done with. False, to all of them, and nothing more done if one has to quit.
 template <typename F>
-__device__ __forceinline__ void chunk_inverse(uint32_t tb, uint32_t wb, const float* gt, float* diag, int pw, F read)
+__device__ __forceinline__ bool chunk_inverse(uint32_t tb, uint32_t wb, const float* gt, float* diag, int pw, bool quit, F read)
 {
     const int lane = threadIdx.x & 31;
     if (pw < 4) {
@@ -296,7 +296,7 @@ __device__ __forceinline__ void chunk_inverse(uint32_t tb, uint32_t wb, const fl
         sts4(o, h8[0], h8[1], h8[2], h8[3]);
         sts4(o + SLAB, l8[0], l8[1], l8[2], l8[3]);
     }
-    sm100::named_bar_sync(2, 256);
+    if (named_bar_any(2, 256, quit)) return false;
     read();
     {
         // 16 -> 32, eight columns a warp for each of the two pairs
@@ -319,6 +319,7 @@ __device__ __forceinline__ void chunk_inverse(uint32_t tb, uint32_t wb, const fl
         block_product<32>(wb, r0, 0, 64, tb, 0, n0, x);
         put_fragment(tb, 32 + r0, n0, SLAB, x, 1.f);
     }
+    return true;
 }
 
 }  // namespace delta

@@ -4,6 +4,9 @@ kernel: it passes while the barrier's current phase has the other parity, so a b
 waiting warp holds it up. The model counts a stall (no role can go on), a gate slot read with another chunk's gates, and a
 slot overwritten before its readers are done.
 
+Waits have a limit. The second part of the model holds a copy or the products up until every wait has run out: then the
+roles leave their loops, no copy is issued any more, and the CTA does not end before what was issued has arrived.
+
 Sizes as in the kernel: 3 stages of K and Q, 2 of V, 4 gate slots; 8 chain, 4 drain and 8 prep warps."""
 import random
 
@@ -32,8 +35,10 @@ class Bar:
 class Sim:
     """Roles are generators of operations; each step lets one of those that can go on do its next."""
 
-    def __init__(self, n, out, rng, rule="slot"):
+    def __init__(self, n, out, rng, rule="slot", hold=None):
         self.n, self.out, self.rng, self.rule = n, out, rng, rule
+        # what does not arrive any more from some step on ("loads" or "tensor"); whether the limit is over; the flag
+        self.hold, self.late, self.flag = hold, False, False
         b = self.bars = {}
         for name, k, count in (("kq_full", NKQ, 1), ("kq_empty", NKQ, 1), ("v_full", NV, 1), ("v_empty", NV, 1),
                                ("s_ready", 2, 8), ("r_ready", 2, 8), ("u_ready", 2, 8), ("p_ready", 1, 8),
@@ -53,19 +58,25 @@ class Sim:
 
     # ------------------------------------------------------------ what a role may do
     def can(self, op, next_op):
-        if op[0] == "wait":
-            return self.bars[op[1], op[2]].passed(op[3])
+        if op[0] in ("wait", "drain"):
+            return self.bars[op[1], op[2]].passed(op[3]) or (op[0] == "wait" and self.late)
         if op[0] == "sync":
-            return sum(o == op for o in next_op.values()) == op[2]
+            return sum(o is not None and o[:3] == op[:3] for o in next_op.values()) == op[2]
         return True
 
     def do(self, op):
+        if op[0] in ("wait", "drain"):
+            ok = self.bars[op[1], op[2]].passed(op[3])
+            self.flag |= not ok
+            return ok
         if op[0] == "arrive":
             self.bars[op[1], op[2]].arrive()
         elif op[0] == "commit":            # arrives once every product before it is done
             self.tensor.append(op[1:])
         elif op[0] == "load":
             self.loads.append(op[1:])
+        elif self.late:
+            pass                           # (gates are of any chunk by then)
         elif op[0] == "write":
             assert self.readers[op[1]] == 0, "gates of chunk %s overwritten before they are read" % self.slot[op[1]]
             # chain, prep, drain (or the four warps of the scores)
@@ -76,20 +87,27 @@ class Sim:
 
     def run(self, most=200000):
         rng = self.rng
-        next_op = {}
         weight = {r: rng.choice([1, 1, 1, 0.02]) for r in self.roles}
         weight["gates"] = rng.choice([1, 0.01, 0.001])
-        for r, g in list(self.roles.items()):
-            next_op[r] = next(g, None)
-        for _ in range(most):
+        next_op = {r: next(g, None) for r, g in self.roles.items()}
+        held, hold_at = None, rng.randrange(3000) if self.hold else None
+        for step in range(most):
+            if step == hold_at:
+                held = self.hold
             at = [r for r, op in next_op.items() if op is not None and self.can(op, next_op)]
-            idle = len(self.tensor) + len(self.loads)
-            if not at and not idle:
+            queues = [q for q in ("tensor", "loads") if q != held and getattr(self, q)]
+            if not at and not queues:
                 if all(op is None for op in next_op.values()):
+                    assert not self.tensor and not self.loads, "the CTA ends with something in flight"
                     return
+                if held and not self.late:
+                    self.late = True       # every role waits: the limit passes
+                    continue
+                if held:
+                    held = None            # what was held up arrives after all
+                    continue
                 raise Stall({r: op for r, op in next_op.items() if op is not None})
-            pick = rng.choices(at + ["tensor", "loads"], [weight[r] for r in at] +
-                               [bool(self.tensor) * 1.0, bool(self.loads) * rng.choice([1, 0.1])])[0]
+            pick = rng.choices(at + queues, [weight[r] for r in at] + [rng.choice([1, 0.1]) for _ in queues])[0]
             if pick == "tensor":
                 self.bars[self.tensor.pop(0)].arrive()      # in order
             elif pick == "loads":
@@ -97,89 +115,114 @@ class Sim:
             else:
                 op = next_op[pick]
                 if op[0] == "sync":
-                    # all of the group are at the barrier: they go on together
-                    for r in [r for r, o in next_op.items() if o == op]:
-                        next_op[r] = next(self.roles[r], None)
+                    # all of the group are at the barrier: they go on together, with the same word
+                    group = [r for r, o in next_op.items() if o is not None and o[:3] == op[:3]]
+                    word = any(len(next_op[r]) > 3 and next_op[r][3] for r in group)
+                    for r in group:
+                        next_op[r] = self.step(r, word)
                     continue
-                self.do(op)
-                next_op[pick] = next(self.roles[pick], None)
+                next_op[pick] = self.step(pick, self.do(op))
         raise Stall("no end")
+
+    def step(self, role, answer):
+        try:
+            return self.roles[role].send(answer)
+        except StopIteration:
+            return None
+
+    def chunks(self, look=True):
+        """A role's loop over the chunks; it leaves at its look at the flag."""
+        for m in range(self.n):
+            if look and self.flag:
+                return
+            yield m
 
     # ------------------------------------------------------------ the roles
     def tma(self):
-        for m in range(self.n):
+        kq = v = 0
+        ok = True
+        for m in self.chunks():
             if m >= NKQ:
-                yield "wait", "kq_empty", m % NKQ, (m // NKQ - 1) & 1
-            yield "load", "kq_full", m % NKQ
+                ok &= yield "wait", "kq_empty", m % NKQ, (m // NKQ - 1) & 1
+            if ok:
+                yield "load", "kq_full", m % NKQ
+                kq += 1
             if m >= NV:
-                yield "wait", "v_empty", m % NV, (m // NV - 1) & 1
-            yield "load", "v_full", m % NV
-        for m in range(max(0, self.n - NKQ), self.n):
-            yield "wait", "kq_full", m % NKQ, (m // NKQ) & 1
-        for m in range(max(0, self.n - NV), self.n):
-            yield "wait", "v_full", m % NV, (m // NV) & 1
+                ok &= yield "wait", "v_empty", m % NV, (m // NV - 1) & 1
+            if ok:
+                yield "load", "v_full", m % NV
+                v += 1
+        for m in range(max(0, kq - NKQ), kq):
+            yield "drain", "kq_full", m % NKQ, (m // NKQ) & 1
+        for m in range(max(0, v - NV), v):
+            yield "drain", "v_full", m % NV, (m // NV) & 1
 
     def gates(self):
-        for m in range(self.n):
+        for m in self.chunks(look=False):
+            ok = True
             if self.rule == "slot":
                 if m >= NG:
-                    yield "wait", "gt_free", m % NG, (m // NG - 1) & 1
+                    ok = yield "wait", "gt_free", m % NG, (m // NG - 1) & 1
             elif m >= NG - 1:              # by the parity of the increment of three chunks before
-                yield "wait", "d_full", 1, (m - NG + 1) & 1
+                ok = yield "wait", "d_full", 1, (m - NG + 1) & 1
+            if not ok:
+                return
             yield "write", m % NG, m
             yield "arrive", "gt_ready", m % NG
 
     def products(self):
         n, out = self.n, self.out
 
+        def commit(*bars):
+            for x in bars:
+                yield "commit", *x
+
         def gram(m):
             yield "wait", "kq_full", m % NKQ, (m // NKQ) & 1
-            yield "commit", "g_full", 0
+            yield from commit(("g_full", 0))
 
         yield from gram(0)
         if not out and n > 1:
             yield "wait", "g_read", 0, 0
             yield from gram(1)
-        for m in range(n):
+        for m in self.chunks():
             ph = m & 1
             for part in range(2):
                 yield "wait", "s_ready", part, ph
                 if out and part == 0 and m == 0:
                     yield "wait", "g_read", 0, 0
-            yield "commit", "ks_full", 0
+            yield from commit(("ks_full", 0))
             if out and m + 1 < n:
                 yield from gram(m + 1)
             yield "wait", "t_ready", m & 1, (m >> 1) & 1
             yield "wait", "v_full", m % NV, (m // NV) & 1
-            yield "commit", "v_empty", m % NV
+            yield from commit(("v_empty", m % NV))
             for part in range(2):
                 yield "wait", "r_ready", part, ph
-            yield "commit", "u_full", 0
+            yield from commit(("u_full", 0))
             if out and m > 0:
                 yield "wait", "o_empty", 0, (m - 1) & 1
             if out and m + 1 < n:
                 yield "wait", "g_read", 0, (m + 1) & 1
             for part in range(2):
                 yield "wait", "u_ready", part, ph
-            yield "commit", "d_full", 0
-            yield "commit", "d_full", 1
+            yield from commit(("d_full", 0), ("d_full", 1))
             if not out:
-                yield "commit", "kq_empty", m % NKQ
+                yield from commit(("kq_empty", m % NKQ))
                 yield "arrive", "gt_free", m % NG
                 if m + 2 < n:
                     yield "wait", "g_read", 0, (m + 1) & 1
                     yield from gram(m + 2)
             else:
                 yield "wait", "p_ready", 0, ph
-                yield "commit", "o_full", 0
-                yield "commit", "kq_empty", m % NKQ
+                yield from commit(("o_full", 0), ("kq_empty", m % NKQ))
         yield "commit", "fin", 0
-        yield "wait", "fin", 0, 0
+        yield "drain", "fin", 0, 0
 
     def chain(self):
         for p in range(2):
             yield "arrive", "s_ready", p
-        for m in range(self.n):
+        for m in self.chunks():
             ph = m & 1
             yield "wait", "t_ready", m & 1, (m >> 1) & 1
             yield "read", m % NG, m
@@ -199,16 +242,17 @@ class Sim:
                     yield "arrive", "s_ready", p
 
     def drain(self):
-        for m in range(self.n):
+        for m in self.chunks(look=False):
             yield "wait", "o_full", 0, m & 1
-            yield "sync", "drain", 4
+            if (yield "sync", "drain", 4, self.flag):
+                return
             yield "read", m % NG, m, "last"
             yield "arrive", "o_empty", 0
             yield "arrive", "gt_free", m % NG
-            yield "sync", "drain", 4
+            yield "sync", "drained", 4
 
     def scores(self):
-        for m in range(self.n):
+        for m in self.chunks():
             yield "wait", "gt_ready", m % NG, (m // NG) & 1
             yield "wait", "g_full", 0, m & 1
             if m > 0:
@@ -218,7 +262,7 @@ class Sim:
             yield "arrive", "l_ready", 0
 
     def prep(self, w):
-        for m in range(self.n):
+        for m in self.chunks(look=False):
             if self.out:
                 yield "wait", "gt_ready", m % NG, (m // NG) & 1
                 yield "wait", "g_full", 0, m & 1
@@ -228,7 +272,8 @@ class Sim:
             else:
                 yield "wait", "l_ready", 0, m & 1
             yield "read", m % NG, m, "last"
-            yield "sync", "inverse", 8
+            if (yield "sync", "inverse", 8, self.flag):
+                return
             if not self.out and w == 0:
                 yield "arrive", "d_free", 0
             for k in range(3):
@@ -239,7 +284,7 @@ class Sim:
 @pytest.mark.parametrize("out", [True, False])
 @pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 6, 13])
 def test_no_order_stalls(n, out):
-    for seed in range(25):
+    for seed in range(15):
         Sim(n, out, random.Random(1000 * n + seed)).run()
 
 
@@ -252,3 +297,29 @@ def test_a_wait_on_a_barrier_that_gets_ahead_stalls():
         except Stall:
             stalled += 1
     assert stalled > 0
+
+
+@pytest.mark.parametrize("out", [True, False])
+@pytest.mark.parametrize("hold", ["loads", "tensor"])
+def test_giving_up_leaves_nothing_in_flight(hold, out):
+    gave_up = 0
+    for seed in range(40):
+        sim = Sim(13, out, random.Random(seed), hold=hold)
+        sim.run()
+        gave_up += sim.late
+    assert gave_up > 13
+
+
+def test_a_drain_under_the_passed_limit_ends_too_early():
+    """What the drains' own limits replaced: waits that the passed deadline ends at once."""
+    class Former(Sim):
+        def can(self, op, next_op):
+            return super().can(("wait", *op[1:]) if op[0] == "drain" else op, next_op)
+
+    early = 0
+    for seed in range(30):
+        try:
+            Former(13, True, random.Random(seed), hold="loads").run()
+        except AssertionError as e:
+            early += "in flight" in str(e)
+    assert early > 0
