@@ -30,7 +30,7 @@ gla_status check_sizes(int B, int H, int Hk, int T, int dk, int dv, float scale,
     if (path != GLA_PATH_AUTO && path != GLA_PATH_TENSOR && path != GLA_PATH_SIMT) return GLA_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return GLA_ERR_INVALID_ARG;
     if ((long long)B * H > (1LL << 30)) return GLA_ERR_INVALID_ARG;
-    if (dk > kDeltaMaxDk || dv > (1 << 20)) return GLA_ERR_UNSUPPORTED;
+    if (dk > kDeltaMaxDk || dv > (1 << 20) || T > kDeltaMaxT) return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
 }
 

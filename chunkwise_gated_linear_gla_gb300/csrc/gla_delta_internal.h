@@ -17,6 +17,9 @@ constexpr int kDeltaChunkMinT = 9, kDeltaChunkMinTFew = 24, kDeltaFewTiles = 64;
 // The longest: a CTA that walks 2^25 tokens (half a million chunks at 3.3 us) is done within the four
 // seconds after which its waits give up.
 constexpr int kDeltaChunkMaxT = 1 << 25;
+// The longest sequence of the recurrent form: it counts tokens in steps of 16, and the step past the last
+// token stays an int.
+constexpr int kDeltaMaxT = 0x7fffffff - 15;
 constexpr int kDeltaKeep = 16;      // recurrent backward: tokens between two kept states
 
 // The recurrent form (gla_delta_step.cu): the recurrence token by token, the state tile in

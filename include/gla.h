@@ -403,7 +403,7 @@ const char* gla_bwd_stage_name(const gla_bwd_params* p, int stage);
  * padded row is passed over.
  *   GLA_PATH_SIMT    the recurrent form on CUDA cores, token by token, the state in registers:
  *                    single tokens (decoding; bound by the state's bytes), a few tokens,
- *                    fp32 inputs and other shapes; dk <= 256.
+ *                    fp32 inputs and other shapes; dk <= 256, dv <= 2^20, T <= 2^31 - 16.
  *   GLA_PATH_TENSOR  the chunk form on the tensor cores (bf16, dk 64 or 128, dv a multiple of
  *                    64, B H <= 65535, T <= 2^25; else GLA_ERR_UNSUPPORTED): 64-token chunks, the
  *                    corrections u of a chunk through the inverse of a unit triangular matrix.

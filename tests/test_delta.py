@@ -111,6 +111,17 @@ def test_forward_refuses_before_launch(kw, want):
     assert bnd.gla_delta_fwd(_params(**kw), 0, check=False) == want
 
 
+@pytest.mark.parametrize("T,want", [(2 ** 31 - 1, 2), (2 ** 31 - 15, 2), (2 ** 31 - 16, 1)])
+def test_the_longest_sequences(T, want):
+    """The step of 16 past the last token is an int up to 2^31 - 16 (nothing runs: q is missing, which is looked at next)."""
+    assert bnd.gla_delta_fwd(_params(T=T, q=0), 0, check=False) == want
+    p = bnd.gla_delta_bwd_params()
+    for n, v in dict(B=1, H=1, Hk=1, T=T, dk=16, dv=16, scale=1.0, dtype=gla.GLA_BF16).items():
+        setattr(p, n, v)
+    assert bnd.gla_delta_bwd(p, 0, check=False) == want
+    assert (bnd.gla_delta_bwd_workspace_size(p) > 0) == (want == 1)
+
+
 def test_null_params_are_refused():
     lib = bnd.load()
     assert lib.gla_delta_fwd(None, None) == 1 and lib.gla_delta_bwd(None, None) == 1
