@@ -105,6 +105,20 @@ def _qk_function():
     return QkNormRopeFunction
 
 
+def _plain(*tensors):
+    """Whether no derivative of any kind is asked of these inputs (some may be None). A dual tensor of forward
+    mode need not require grad, and no_grad() does not switch forward mode off: with a dual level open the
+    autograd function is called, which refuses what it has no derivative for."""
+    import torch
+    if torch.autograd.forward_ad._current_level >= 0:
+        return False
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return False
+    return True
+
+
 _FN = None
 _DELTA = None
 _QK = None
@@ -121,13 +135,10 @@ def gla_attention(q, k, v, log_g=None, S0=None, gate=None):
 
 def delta_attention(q, k, v, log_g, beta, S0=None, scale=None, path=_b.GLA_PATH_AUTO):
     """(O, S_T) of the gated delta rule (binding.delta_forward), differentiable once in q, k, v, log_g, beta
-    and S0. The inputs must be contiguous device tensors. A step captured into a CUDA graph starts from
+    and S0, in reverse mode (forward mode is refused). The inputs must be contiguous device tensors. A step captured into a CUDA graph starts from
     leaves of which no eager graph is alive (fresh detached ones, say): autograd would wait on the stream
     of that graph, which a capture cannot."""
-    import torch
-    if not torch.is_grad_enabled() or not (
-            q.requires_grad or k.requires_grad or v.requires_grad or beta.requires_grad or
-            (log_g is not None and log_g.requires_grad) or (S0 is not None and S0.requires_grad)):
+    if _plain(q, k, v, log_g, beta, S0):
         return _b.delta_forward(q, k, v, log_g, beta, S0, scale=scale, path=path)
     global _DELTA
     if _DELTA is None:
@@ -137,11 +148,8 @@ def delta_attention(q, k, v, log_g, beta, S0=None, scale=None, path=_b.GLA_PATH_
 
 def qk_norm_rope(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv_freq=None, positions=None, start=0,
                  interleaved=False):
-    """binding.qk_norm_rope_forward, differentiable once in q, k and the weights."""
-    import torch
-    if not torch.is_grad_enabled() or not (
-            q.requires_grad or (k is not None and k.requires_grad) or (w_q is not None and w_q.requires_grad) or
-            (w_k is not None and w_k.requires_grad)):
+    """binding.qk_norm_rope_forward, differentiable once in q, k and the weights, in reverse mode."""
+    if _plain(q, k, w_q, w_k):
         return _b.qk_norm_rope_forward(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved)
     global _QK
     if _QK is None:
