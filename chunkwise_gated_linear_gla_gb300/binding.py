@@ -604,6 +604,22 @@ def _used_on(stream, device, *tensors):
                 t.record_stream(s)
 
 
+def _given(t, what):
+    """An output tensor of the caller's: as with torch's own `out=`, it takes no part in autograd."""
+    import torch
+    if t.requires_grad and torch.is_grad_enabled():
+        _refuse(f"{what} requires grad and is written in place")
+
+
+def _written(*tensors):
+    """Counts tensors of the caller's as written, so that a graph which saved one of them says so. (Inference
+    tensors have no versions.)"""
+    import torch
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _delta_shapes(q, k, v, log_g, beta, S0):
     import torch
     if q.dim() != 4 or v.dim() != 4:
@@ -635,15 +651,18 @@ def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, pa
 
     q, k [B,Hk,T,dk], v [B,H,T,dv], beta [B,H,T] (bf16 or fp32, one type); log_g fp32 [B,H,T] or
     None; S0 fp32 [B,H,dk,dv] or None; scale defaults to dk^-0.5. Returns (O, S_T). A decoding
-    loop passes ST=S0 to carry the state in place. With `stream` the outputs may be used there,
+    loop passes ST=S0 to carry the state in place; O and ST count as modified in place. With `stream` the outputs may be used there,
     and on other streams after it.
     """
     import torch
     B, H, Hk, T, dk, dv, code, dt, dev = _delta_shapes(q, k, v, log_g, beta, S0)
     if O is not None:
         _dense(O, (B, H, T, dv), dt, dev, "O")
+        _given(O, "O")
     if ST is not None:
         _dense(ST, (B, H, dk, dv), torch.float32, dev, "ST")
+        _given(ST, "ST")
+    given = O, ST
     _on_gpu(q, "q")
     if B == 0:
         _refuse("an empty batch")
@@ -660,6 +679,7 @@ def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, pa
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
         p.workspace, p.workspace_bytes = ws.data_ptr(), n
     _launch(lib.gla_delta_fwd, "gla_delta_fwd", p, dev, stream, O, ST, ws)
+    _written(*given)
     return O, ST
 
 

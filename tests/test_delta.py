@@ -427,6 +427,36 @@ def test_training_step_replays_from_a_cuda_graph(T):
 
 
 @pytest.mark.gpu
+def test_outputs_that_are_given_count_as_written():
+    """A state carried in place is seen by a graph that saved it, as with any torch operation."""
+    x, _ = ref.make(1, 2, 1, 3, 64, 64, torch.bfloat16, seed=15)
+    q, k, v, lg, be, S0 = ref.cuda(x)
+    O, ST = torch.empty_like(v), S0.clone()
+    seen = O._version, ST._version
+    gla.delta_forward(q, k, v, lg, be, S0, O=O, ST=ST)
+    assert (O._version, ST._version) == (seen[0] + 1, seen[1] + 1)
+    leaf = v.clone().requires_grad_(True)
+    out, _ = gla.delta_attention(q, k, leaf, lg, be, S0)
+    gla.delta_forward(q, k, v, lg, be, S0, ST=S0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    with torch.inference_mode():                       # tensors without versions
+        S = S0.clone()
+        want = gla.delta_forward(q, k, v, lg, be, S)
+        got = gla.delta_forward(q, k, v, lg, be, S, O=torch.empty_like(v), ST=S)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_given_outputs_that_require_gradients_are_refused():
+    x, _ = ref.make(1, 2, 1, 3, 64, 64, torch.bfloat16, seed=15)
+    for kw in (dict(ST=x[5].clone().requires_grad_(True)), dict(O=x[2].clone().requires_grad_(True))):
+        with pytest.raises(gla.GlaError, match="requires grad"):
+            gla.delta_forward(*x, **kw)
+        with torch.no_grad(), pytest.raises(gla.GlaError, match="not on a GPU"):
+            gla.delta_forward(*x, **kw)
+
+
+@pytest.mark.gpu
 def test_calls_in_flight_on_two_streams():
     """Two passes and their gradients at once: neither sees the other's workspace or status."""
     sets = [ref.cuda(ref.make(1, 4, 2, T, 128, 128, torch.bfloat16, seed=T)[0]) for T in (300, 2000)]
