@@ -48,6 +48,13 @@ def _function():
     return GLAFunction
 
 
+def _placed(g):
+    """A gradient as the library takes it: dense and from a 16-byte boundary. What autograd hands over may be a slice of
+    another tensor that starts at any element."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 def _delta_function():
     import torch
 
@@ -66,8 +73,8 @@ def _delta_function():
             q, k, v, log_g, beta, S0 = ctx.saved_tensors
             if dO is None and dST is None:
                 return (None,) * 8
-            dO = torch.zeros_like(v) if dO is None else dO.contiguous()
-            dST = None if dST is None else dST.contiguous()
+            dO = torch.zeros_like(v) if dO is None else _placed(dO)
+            dST = None if dST is None else _placed(dST)
             want = ctx.needs_input_grad
             g = _b.delta_backward(q, k, v, log_g, beta, S0, dO, dST, scale=ctx.scale,
                                   want_dS0=S0 is not None and want[5], path=ctx.path)
@@ -97,7 +104,7 @@ def _qk_function():
             norm, eps, start, interleaved = ctx.how
             want = ctx.needs_input_grad
             dense = lambda g, x: (torch.zeros(x.shape, dtype=x.dtype, device=x.device) if g is None
-                                  else g.contiguous())
+                                  else _placed(g))
             g = _b.qk_norm_rope_backward(q, k, dense(dqo, q), None if k is None else dense(dko, k), norm, w_q, w_k,
                                          eps, inv_freq, positions, start, interleaved)
             return (*(x if w else None for x, w in zip(g, want)), None, None, None, None, None, None)

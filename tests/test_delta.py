@@ -457,6 +457,27 @@ def test_given_outputs_that_require_gradients_are_refused():
 
 
 @pytest.mark.gpu
+def test_gradients_that_arrive_anywhere():
+    """What autograd hands to the backward may be a slice that starts at any element (here of a concatenation's)."""
+    x, g = ref.make(1, 2, 1, 5, 64, 64, torch.bfloat16, seed=16)
+    leaves = [t.cuda().requires_grad_(True) for t in x]
+    O, ST = gla.delta_attention(*leaves)
+    dO, dST = torch.randn(O.shape, generator=g).bfloat16().cuda(), torch.randn(ST.shape, generator=g).cuda()
+    one = lambda t: torch.ones(1, dtype=t.dtype, device="cuda")  # noqa: E731
+    after = [torch.cat([one(t), t.flatten()]) for t in (O, ST)]
+    got = torch.autograd.grad(after, leaves, [torch.cat([one(t), t.flatten()]) for t in (dO, dST)])
+    for a, b in zip(got, gla.delta_backward(*[t.detach() for t in leaves], dO, dST)):
+        assert torch.equal(a, b)
+    q, k = (torch.randn(1, h, 5, 64, generator=g).bfloat16().cuda().requires_grad_(True) for h in (2, 1))
+    qo, ko = gla.qk_norm_rope(q, k)
+    dq, dk = torch.randn(q.shape, generator=g).bfloat16().cuda(), torch.randn(k.shape, generator=g).bfloat16().cuda()
+    after = [torch.cat([one(t), t.flatten()]) for t in (qo, ko)]
+    got = torch.autograd.grad(after, (q, k), [torch.cat([one(t), t.flatten()]) for t in (dq, dk)])
+    for a, b in zip(got, gla.qk_norm_rope_backward(q.detach(), k.detach(), dq, dk)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_calls_in_flight_on_two_streams():
     """Two passes and their gradients at once: neither sees the other's workspace or status."""
     sets = [ref.cuda(ref.make(1, 4, 2, T, 128, 128, torch.bfloat16, seed=T)[0]) for T in (300, 2000)]
