@@ -3,6 +3,7 @@
 // pass runs in the kernels.
 #include <cstdint>
 #include <cstring>
+#include <cuda.h>
 #include <mutex>
 
 #include "gla_internal.h"
@@ -23,17 +24,29 @@ struct DevCache {
 std::mutex g_mu;
 DevCache g_dev[64];
 
+// Whether the calling thread has a context current (its own, made through the driver, or the device's).
+bool has_context()
+{
+    typedef CUresult (*Fn)(CUcontext*);
+    static const Fn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<Fn>(p);
+    }();
+    CUcontext c = nullptr;
+    return fn && fn(&c) == CUDA_SUCCESS && c;
+}
+
 DevCache* dev_cache()
 {
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64) return nullptr;
     // A thread that has made no CUDA call yet (an autograd worker whose allocations came from a
-    // cache) has no context current, and encoding a tensor map needs one.
-    static thread_local int bound = -1;
-    if (bound != d) {
-        if (cudaSetDevice(d) != cudaSuccess) return nullptr;
-        bound = d;
-    }
+    // cache) has no context current, and encoding a tensor map needs one. A thread that has one keeps it.
+    if (!has_context() && cudaSetDevice(d) != cudaSuccess) return nullptr;
     std::lock_guard<std::mutex> lk(g_mu);
     DevCache& c = g_dev[d];
     if (!c.init) {

@@ -478,6 +478,49 @@ def test_gradients_that_arrive_anywhere():
 
 
 @pytest.mark.gpu
+def test_a_thread_keeps_its_own_driver_context():
+    """A thread that works in a context of its own (made through the driver) finds it current after a call. The call
+    launches nothing: no token, no state asked for."""
+    import threading
+    drv = ctypes.CDLL("libcuda.so.1")
+    said = []
+
+    def work():
+        ctx, now = ctypes.c_void_p(), ctypes.c_void_p()
+        said.append(drv.cuCtxCreate_v2(ctypes.byref(ctx), 0, 0))
+        p = _params(T=0, ST=0)
+        said.append(bnd.load().gla_delta_fwd(ctypes.byref(p), None))
+        drv.cuCtxGetCurrent(ctypes.byref(now))
+        said.append(now.value == ctx.value)
+        drv.cuCtxDestroy_v2(ctx)
+
+    torch.cuda.synchronize()
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    assert said == [0, 0, True]
+
+
+@pytest.mark.gpu
+def test_a_thread_without_a_context_gets_one():
+    """The first thing that a new thread does is a call in the chunk form (an autograd worker's case)."""
+    import threading
+    x, _ = ref.make(1, 2, 1, 70, 64, 64, torch.bfloat16, seed=17)
+    c = ref.cuda(x)
+    O, ST = gla.delta_forward(*c)
+    torch.cuda.synchronize()
+    got = torch.empty_like(O)
+    p = bnd.gla_delta_params(*(t.data_ptr() for t in c), got.data_ptr(), None, 1, 2, 1, 70, 64, 64, 0.125, gla.GLA_BF16,
+                             gla.GLA_PATH_TENSOR, None, 0, 1)
+    said = []
+    t = threading.Thread(target=lambda: said.append(bnd.load().gla_delta_fwd(ctypes.byref(p), None)))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert said == [0] and torch.equal(got, O)
+
+
+@pytest.mark.gpu
 def test_calls_in_flight_on_two_streams():
     """Two passes and their gradients at once: neither sees the other's workspace or status."""
     sets = [ref.cuda(ref.make(1, 4, 2, T, 128, 128, torch.bfloat16, seed=T)[0]) for T in (300, 2000)]
