@@ -14,9 +14,11 @@
 // [B,T,heads,d] slice), writes are dense [B,H,T,d].
 //
 // Angles: the caller's frequencies are radians per position in fp64. Each becomes a fraction of
-// a turn in 2^-64 units, so position * frequency modulo one turn is one wrapping 64-bit product,
-// exact at any position (fp32 products lose the angle beyond a few thousand positions, and fp64
+// a turn in 2^-64 units, so position * frequency modulo one turn is one wrapping 64-bit product
+// without rounding (fp32 products lose the angle beyond a few thousand positions, and fp64
 // ones cost the few fp64 units this chip has); the remaining fraction goes to sincospi in fp32.
+// What the fraction itself was rounded by, 2^-52 of it and half a unit, grows with the position: at
+// most |pos f| 2^-52 + |pos| 2^-62 radians, below the fp32 rounding up to pos f = 2^28.
 //
 // The weights' gradients are summed in fp32: over a thread's rows, over the block in shared
 // memory, over the blocks by a second kernel, each in a fixed order.

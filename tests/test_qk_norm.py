@@ -5,6 +5,9 @@ pair of a rotation adds fp32 errors of both, so 2^-8 of |y| plus 2^-20 of the ro
 row's sum of 256 squares, a square root, a division, a product, the angle to 2^-24 turns and a
 rotation: below 16 roundings of 2^-24 relative to the row's norm, 1e-6. Weight gradients sum rows in
 fp32: 1e-5 of their norm."""
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -104,6 +107,36 @@ def test_far_positions_keep_their_angle():
             turn = Fraction(float(f[i]) * 0.15915494309189533577) * p
             th = float(turn - math.floor(turn)) * 2 * math.pi
             assert abs(float(y[0, 0, t, i]) - math.cos(th)) < 1e-6 and abs(float(y[0, 0, t, i + 16]) - math.sin(th)) < 1e-6
+
+
+# 2 pi to 60 digits
+TWO_PI = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_true_angles_of_far_positions(interleaved):
+    """Positions on both sides of zero against pos * f reduced by 2 pi in exact fractions. f / (2 pi) is rounded twice in
+    fp64 (the constant and the product, 2^-53 each) and once to units of 2^-64 turns (half of one, 2^-62.3 radians): the
+    angle is off by |pos| times that. The rest is fp32: the turn's upper 32 bits rounded to 24 (2^-25 of half a turn,
+    9.4e-8) and the two functions' 2 ulp (1.2e-7)."""
+    d = 32
+    f = torch.tensor([1.0, 0.3, 0.01, 1e-4, 7e-9, 2.5, 0.7390851332151607, 1e-2 / 3] * 2, dtype=torch.float64)
+    pos = torch.tensor([[0, 1, -1, 12345, 2 ** 20 + 1, -(2 ** 31) - 7, 2 ** 40 + 3, -(2 ** 40) - 3, 2 ** 46 + 1]])
+    n = pos.shape[1]
+    x = torch.zeros(1, 1, n, d)
+    x[..., 0::2 if interleaved else 1] = 1
+    if not interleaved:
+        x[..., d // 2:] = 0              # pairs (1, 0): the result is (cos, sin)
+    y = gla.qk_norm_rope_forward(x.cuda(), None, norm=None, inv_freq=f.cuda(), positions=pos.cuda(),
+                                 interleaved=interleaved)[0].cpu()[0, 0].double()
+    c, s = (y[:, 0::2], y[:, 1::2]) if interleaved else (y[:, :d // 2], y[:, d // 2:])
+    for t, p in enumerate(pos[0].tolist()):
+        for i in range(d // 2):
+            tol = 4e-7 + abs(p * float(f[i])) * 2.0 ** -52 + abs(p) * 2.0 ** -62
+            turn = p * Fraction(float(f[i])) / TWO_PI
+            th = float(turn - math.floor(turn)) * 2 * math.pi
+            assert abs(float(c[t, i]) - math.cos(th)) <= tol and abs(float(s[t, i]) - math.sin(th)) <= tol, (p, float(f[i]))
 
 
 @pytest.mark.gpu
