@@ -377,6 +377,54 @@ def test_backward_against_differences_of_the_forward():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,H,Hk,T,dk,dv,gate,keys", [
+    (1, 1, 1, 6000, 128, 128, "sigmoid", "unit"), (1, 2, 1, 4100, 64, 128, "none", "unit"),
+    (2, 2, 2, 2999, 128, 64, "none", "same"), (1, 4, 2, 5000, 64, 64, "resets", "unit")])
+def test_long_prompts_are_cut_by_the_planner(B, H, Hk, T, dk, dv, gate, keys):
+    """AUTO's own split of a long prompt of few heads (its workspace shows that there is one) against fp64. Every increment
+    of the state is good to four two-part operands' 2^-17 and so are the joins; the errors do not grow along the sequence,
+    as no step of unit keys grows the state."""
+    x = ref.make(B, H, Hk, T, dk, dv, torch.bfloat16, seed=T, gate=gate, keys=keys)[0]
+    p = _params(B=B, H=H, Hk=Hk, T=T, dk=dk, dv=dv)
+    state = B * H * dk * dv * 4
+    assert bnd.gla_delta_fwd_workspace_size(p) >= 2 * 3 * state     # three segments or more
+    O, S = ref.delta(*ref.f64(x), dk ** -0.5)
+    got_O, got_S = gla.delta_forward(*ref.cuda(x))
+    torch.cuda.synchronize()
+    assert gla.gla_device_status() == 0
+    assert_close(to_np(got_O), to_np(O), torch.bfloat16, "O")
+    close(got_S, S, 6 * PARTS, "S_T")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,dk,dv,gate", [(1300, 128, 128, "sigmoid"), (1100, 64, 192, "none"), (900, 128, 64, "resets")])
+def test_chunk_backward_of_many_chunks(T, dk, dv, gate):
+    x, g = ref.make(1, 2, 1, T, dk, dv, torch.bfloat16, seed=T, gate=gate)
+    dO = torch.randn(x[2].shape, generator=g).bfloat16()
+    check_backward(x, dO, torch.randn((1, 2, dk, dv), generator=g), path=gla.GLA_PATH_TENSOR)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("i", range(6))
+def test_backward_against_differences_along_the_gradient(i):
+    """fp32, recurrent form, one input at a time, moved along its own gradient, so that the derivative is |grad| |d| and a
+    wrong part of it shows in full. Central differences of <dO, O> with a step of 2^-6 of the input's norm: in fp64 the
+    reference's own are off by 7.7e-5 of the derivative for k, 2.6e-5 for log_g, below 1e-8 for the others (O is linear
+    or nearly so in them). O's rounding in fp32, 16 x 2^-24 of each value, over the step: at most 6e-5 (log_g). Together
+    below 2^-12."""
+    x, g = ref.make(1, 2, 1, 20, 64, 64, torch.float32, seed=12)
+    dO = torch.randn(x[2].shape, generator=g)
+    grad = gla.delta_backward(*ref.cuda(x), dO.cuda())[i].double().cpu()
+    f = lambda y: (gla.delta_forward(*ref.cuda(y))[0].double().cpu() * dO.double()).sum()  # noqa: E731
+    d = (grad / grad.norm() * x[i].norm()).float()
+    up, down = list(x), list(x)
+    up[i], down[i] = x[i] + d / 64, x[i] - d / 64
+    got = (f(up) - f(down)) * 32
+    want = (grad * d.double()).sum()
+    assert abs(got - want) <= 2.0 ** -12 * abs(want), (got, want)
+
+
+@pytest.mark.gpu
 def test_autograd_and_unused_outputs():
     x, g = ref.make(1, 2, 1, 70, 64, 64, torch.bfloat16, seed=13)
     leaves = [t.cuda().requires_grad_(True) for t in x]
