@@ -651,7 +651,8 @@ def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, pa
 
     q, k [B,Hk,T,dk], v [B,H,T,dv], beta [B,H,T] (bf16 or fp32, one type); log_g fp32 [B,H,T] or
     None; S0 fp32 [B,H,dk,dv] or None; scale defaults to dk^-0.5. Returns (O, S_T). A decoding
-    loop passes ST=S0 to carry the state in place; O and ST count as modified in place. With `stream` the outputs may be used there,
+    loop passes ST=S0 to carry the state in place; O and ST count as modified in place. Values are finite
+    (log_g may be -inf), those of padded rows too. With `stream` the outputs may be used there,
     and on other streams after it.
     """
     import torch

@@ -400,7 +400,11 @@ const char* gla_bwd_stage_name(const gla_bwd_params* p, int stage);
  * beta_t in [0, 1]. Keys are meant to have unit 2-norm (gla_qk_norm_rope makes such rows):
  * then no step grows the state. H / Hk value heads share one head of q and k (head h reads
  * h / (H / Hk)). A token with beta = 0 and log_g = 0 leaves the state as it is: that is how a
- * padded row is passed over.
+ * padded row is passed over; its q, k and v must be finite all the same (0 x NaN is NaN).
+ * Inputs are finite but for log_g = -inf. A NaN or an infinity reaches the tokens after it in
+ * every form, and in the chunk form the tokens before it in its chunk of 64 as well: the products
+ * there multiply zeros with later tokens' values. Heads that do not read it are not touched, and one
+ * in v stays in its column of dv.
  *   GLA_PATH_SIMT    the recurrent form on CUDA cores, token by token, the state in registers:
  *                    single tokens (decoding; bound by the state's bytes), a few tokens,
  *                    fp32 inputs and other shapes; dk <= 256, dv <= 2^20, T <= 2^31 - 16.

@@ -285,6 +285,30 @@ def test_passed_over_tokens_leave_the_state():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("path", [gla.GLA_PATH_TENSOR, gla.GLA_PATH_SIMT])
+def test_how_far_a_bad_value_reaches(path, bad):
+    x, _ = ref.make(1, 2, 2, 150, 128, 128, torch.bfloat16, seed=18)
+    O, S = gla.delta_forward(*ref.cuda(x), path=path)
+    first = 64 if path == gla.GLA_PATH_TENSOR else 70      # the first token that it may reach
+    y = [t.clone() for t in x]
+    y[2][0, 1, 70, 3] = bad
+    got_O, got_S = gla.delta_forward(*ref.cuda(y), path=path)
+    assert torch.equal(got_O[:, 0], O[:, 0]) and torch.equal(got_S[:, 0], S[:, 0])
+    rest = [c for c in range(128) if c != 3]
+    assert torch.equal(got_O[0, 1][:, rest], O[0, 1][:, rest]) and torch.equal(got_S[0, 1][:, rest], S[0, 1][:, rest])
+    assert torch.equal(got_O[0, 1, :first], O[0, 1, :first])
+    assert not torch.isfinite(got_O[0, 1, 70:, 3]).any() and not torch.isfinite(got_S[0, 1, :, 3]).any()
+    y = [t.clone() for t in x]
+    y[1][0, 1, 70, 5] = bad
+    got_O, got_S = gla.delta_forward(*ref.cuda(y), path=path)
+    assert torch.equal(got_O[:, 0], O[:, 0]) and torch.equal(got_O[0, 1, :first], O[0, 1, :first])
+    assert not torch.isfinite(got_S[0, 1]).any()
+    torch.cuda.synchronize()
+    assert gla.gla_device_status() == 0
+
+
+@pytest.mark.gpu
 def test_streams_and_bitwise_repeats():
     x, g = ref.make(2, 4, 2, 130, 128, 128, torch.bfloat16, seed=6)
     dO = torch.randn(x[2].shape, generator=g).bfloat16().cuda()
