@@ -61,8 +61,10 @@ int segments_per_cta(int n, int units, int trans, int sms)
     return (n - 1) * u > sms && n / 2 * u <= sms ? 2 : 1;
 }
 // The best n of those that take one wave each time, by these rates and 12 us of launches (16384 tokens,
-// dk = dv = 128, one head: uncut 757 us, 5 segments 316, 20 162, 40 184; 16 heads: uncut 750, 5 segments
-// 322, 9, two to a CTA, 289, 12 in several waves 365).
+// dk = dv = 128, caches flushed, one head: uncut 736 us, 5 segments 296, 20 140, 40 158; 16 heads: uncut 728,
+// 5 segments 300, 9, two to a CTA, 267, 12 in several waves 347). With 64-wide keys both are cheaper and n is
+// taken by the same rates: one head 97 us at the rule's 20 against 87 at 32 and 105 at 64; 16 heads 212 at its 9, the
+// best of 1 to 32.
 int choose_segments(int units, int trans, int dv, int nch, int sms)
 {
     const int most = std::min(sms / units, nch / 4);

@@ -12,8 +12,8 @@
 //
 // Four warps off the chain take the results out: they read the parts (and U or dV, still fp32 in
 // tensor memory) into one 32 KB buffer and store it by TMA, hi, then lo, then U or dV; in
-// reverse they also form the parts of scale e dO. 8 x 2048 tokens, 16 heads, dk = dv = 128: 105 us forward
-// (145 KB a chunk read and written, 5.7 TB/s), 118 us in reverse (177 KB, 6.1 TB/s): bound by those bytes.
+// reverse they also form the parts of scale e dO. 8 x 2048 tokens, 16 heads, dk = dv = 128: 107 us forward
+// (145 KB a chunk read and written, 5.5 TB/s), 120 us in reverse (177 KB, 6.0 TB/s): bound by those bytes.
 #include "gla_delta_dev.cuh"
 #include "gla_delta_internal.h"
 

@@ -13,7 +13,8 @@
 // fp32 registers. Every step comes in two halves (of the keys, or of the tokens), so that the
 // products of one run beside the register step of the other. Every operand that is not an input (S,
 // R, U, T, P) goes into the products in two bf16 parts, hi + lo, good to 2^-17; K, V and Q are exact:
-// two products for K S, K^T U, Q S and T V, three for T R and P U. So the fp32 state is good to 3e-6
+// two products for K S, K^T U, Q S and T V, three for T R and P U. So the fp32 state is good to 3e-6 (4e-6
+// without a gate; nearly all of it l U's rounding: with three parts of that 8e-7, the layer below 111 us)
 // and O to its last rounding (with one part of P and U it was not: where keys repeat, P U is a sum of
 // cancelling terms, 7.5e-3 off when all keys are the same).
 //
@@ -25,9 +26,9 @@
 // of two factors around the chunk's middle while both stay within e^60, else one exponential per pair.
 //
 // Warps: 0 TMA, 1 products, 3 gates, 4-11 chain, 12-15 drain of O, 16-23 prep. Reads K, Q, V once
-// and writes O once. 8 x 2048 tokens, 16 heads, dk = dv = 128: 101 us, 2.8 TB/s, 6050 cycles a chunk, of
-// which the chain and the prep each need about as many: with the tensor pipe busy 52% and the issue slots
-// 51% of the time, neither shortens the other by more warps (16 for the chain: 107 us; scores and inverse
+// and writes O once. 8 x 2048 tokens, 16 heads, dk = dv = 128: 103 us, 2.8 TB/s, 6100 cycles a chunk, of
+// which the chain and the prep each need about as many: with the tensor pipe busy 51% and the issue slots
+// 49% of the time, neither shortens the other by more warps (16 for the chain: 107 us; scores and inverse
 // on eight warps each, a chunk apart: 110 us).
 #include "gla_delta_dev.cuh"
 #include "gla_delta_tri.cuh"
@@ -86,7 +87,7 @@ struct FusedMaps { CUtensorMap k, q, v, o; };
 // OUT: O is formed (and its products and drain run). Without it the state alone, from zero, and in the
 // tiles after dv's the state that starts from the identity without V: the segment's transition. Its scores are L
 // alone and are formed on the drain's warps, two chunks ahead, in P U's place, while the prep's warps form T
-// one chunk ahead: 2.3 us a chunk against 2.7 with both on the prep's warps (with O there is no such place:
+// one chunk ahead: 2.5 us a chunk against 2.7 with both on the prep's warps (with O there is no such place:
 // the product lies over the increment's second half for as long as that is free).
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(NT, 1)

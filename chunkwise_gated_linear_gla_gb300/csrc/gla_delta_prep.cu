@@ -11,7 +11,7 @@
 //
 // One CTA of eight warps per chunk and head, several per SM (76 KB less the tiles that T and P
 // replace: 44 KB at dk = 128), so that one's solving hides behind the others' loads. Bound by its 66 KB
-// of traffic a chunk and by the latency of the solve about equally: 4096 chunks in 48 us, 5.6 TB/s.
+// of traffic a chunk and by the latency of the solve about equally: 4096 chunks in 49 us, 5.5 TB/s.
 #include "gla_delta_dev.cuh"
 #include "gla_delta_tri.cuh"
 #include "gla_delta_internal.h"

@@ -11,8 +11,9 @@
 // Bound by the state's bytes at small T: 4 dk dv read and written once per call. CT = 128
 // columns by 256 threads keeps 16 16-byte loads per thread in flight at dk = 128; when the
 // tiles are fewer than the SMs they narrow to 32 columns so that more SMs pull (the launcher).
-// dk = dv = 128: the next token of 2048 heads 51 us, 5.3 TB/s; of 16 heads 4.5 us, launch latency;
-// five tokens of 512 heads 23.4 us, two of them a token's barriers (tiles of 64 columns: 26.7 us).
+// dk = dv = 128, caches cold: the next token of 2048 heads 52 us, 5.2 TB/s; of 16 heads 6.2 us, launch latency;
+// five tokens of 512 heads 25 us, two of them a token's barriers (calls back to back 24.1, with tiles of 64
+// columns 26.7).
 #include <cuda_bf16.h>
 
 #include "gla_delta_dev.cuh"

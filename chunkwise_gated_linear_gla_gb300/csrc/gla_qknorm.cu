@@ -6,8 +6,8 @@
 //     dw = sum over rows of z (.) x^,    dx = (z (.) w - x^ (sum z (.) w (.) x^) / N) / n.
 //
 // Bound by HBM: every row is read once and written once (backward: x and dy read, dx written); the
-// rows of 8 x 2048 tokens, 16 + 16 heads of 128 bf16 values take 45 us forward, 5.9 TB/s, 0.88 of the
-// measured copy rate, with four blocks of 64 registers a thread per SM (three of 80: 54 us).
+// rows of 8 x 2048 tokens, 16 + 16 heads of 128 bf16 values take 47 us forward, 5.7 TB/s, 0.84 of the
+// measured copy rate, caches cold, with four blocks of 64 registers a thread per SM (three of 80: 54 us).
 // A row is LPR lanes of eight values (16 bytes in bf16); a thread keeps its row of the batch and
 // takes that token's heads one after the other, so a token's angles are formed once per block
 // (in shared memory) and four heads' loads are in flight at a time. Reads go through strides (a fused projection's
@@ -302,7 +302,7 @@ dim3 grid_of(const QkArgs& a, int lpr, int sms, bool bwd, int* hsplit)
     const int nh = a.heads[0] + a.heads[1];
     // The heads are spread over blocks (each forms the token's angles again) until every SM has its
     // four: more blocks pay the set-up more often (the layer's rows, 8 x 2048 tokens of 32 heads of 128
-    // values: 45 us so, 60 with four times as many blocks).
+    // values: 47 us so, 60 with four times as many blocks).
     int split = 1;
     while (split < nh && tg * split < kBlocksPerSm * sms) split *= 2;
     if (split > nh) split = nh;

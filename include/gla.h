@@ -412,7 +412,7 @@ const char* gla_bwd_stage_name(const gla_bwd_params* p, int stage);
  *                    64, B H <= 65535, T <= 2^25; else GLA_ERR_UNSUPPORTED): 64-token chunks, the
  *                    corrections u of a chunk through the inverse of a unit triangular matrix.
  *                    What feeds the state is kept to 17 bits (pairs of bf16) and summed in
- *                    fp32: S_T is good to about 3e-6, O to its bf16 rounding. With few heads the
+ *                    fp32: S_T is good to about 3e-6 (4e-6 without a gate), O to its bf16 rounding. With few heads the
  *                    sequence is cut into segments: their states from zero and their dk x dk
  *                    transitions first, then the states entering them, then the pass over all.
  *   GLA_PATH_AUTO    the form that is faster for the sizes.
