@@ -87,7 +87,7 @@ struct FusedMaps { CUtensorMap k, q, v, o; };
 // OUT: O is formed (and its products and drain run). Without it the state alone, from zero, and in the
 // tiles after dv's the state that starts from the identity without V: the segment's transition. Its scores are L
 // alone and are formed on the drain's warps, two chunks ahead, in P U's place, while the prep's warps form T
-// one chunk ahead: 2.5 us a chunk against 2.7 with both on the prep's warps (with O there is no such place:
+// one chunk ahead: 2.4 us a chunk against 2.7 with both on the prep's warps (with O there is no such place:
 // the product lies over the increment's second half for as long as that is free).
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(NT, 1)
@@ -118,7 +118,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
     uint64_t* gt_ready = s_ready + 18;      // [NG] a chunk's gates written
     uint64_t* l_ready = gt_ready + NG;      // without O: L written (4 warps)
     uint64_t* d_free = l_ready + 1;         // and its diagonal blocks done with
-    uint64_t* gt_free = l_ready + 2;        // [NG] a chunk's gates read by everyone (4 warps; without O one)
+    uint64_t* gt_free = l_ready + 2;        // [NG] a chunk's gates read by everyone (4 warps; without O 8)
     uint32_t* holder = reinterpret_cast<uint32_t*>(gt_free + NG);
     const Abort abort_flag(gt_free + NG + 1);
     static_assert((2 * NKQ + 2 * NV + 18 + 2 * NG + 4) * 8 <= 320, "barriers");
@@ -134,7 +134,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * NKQ + 2 * NV; ++i) mbar_init(&bar[i], 1);
-        for (int i = 0; i < 20 + 2 * NG; ++i) mbar_init(&s_ready[i], i == 7 && !OUT ? 4 : i < 10 ? 8 : i == 17 || i == 18 + NG || (OUT && i >= 20 + NG) ? 4 : 1);
+        for (int i = 0; i < 20 + 2 * NG; ++i) mbar_init(&s_ready[i], i == 7 && !OUT ? 4 : i < 10 ? 8 : i == 17 || i == 18 + NG || (OUT && i >= 20 + NG) ? 4 : i >= 20 + NG ? 8 : 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -344,10 +344,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
                             if (part) mma_commit(&d_full[nh]);
                         }
                         if (part && NH == 1) mma_commit(&d_full[1]);
-                        if (part && !OUT) {
-                            mma_commit(&kq_empty[st]);
-                            mbar_arrive(&gt_free[m % NG]);    // without O the chain is the last reader
-                        }
+                        if (part && !OUT) mma_commit(&kq_empty[st]);
                     }
                     __syncwarp();
                 }
@@ -479,6 +476,7 @@ gla_delta_fused_kernel(FusedArgs a, const __grid_constant__ FusedMaps mp)
             signal(&u_ready[0]);
             put_tokens(1, x1, 2);
             signal(&u_ready[1]);
+            if (!OUT && lane == 0) mbar_arrive(&gt_free[m % NG]);    // (without O the chain is the last reader)
             if (OUT) {
                 // U's own parts, off the chain: the increment's products run meanwhile
 #pragma unroll

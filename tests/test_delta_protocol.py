@@ -44,7 +44,7 @@ class Sim:
                                ("s_ready", 2, 8), ("r_ready", 2, 8), ("u_ready", 2, 8), ("p_ready", 1, 8),
                                ("g_read", 1, 8 if out else 4), ("t_ready", 2, 8), ("ks_full", 1, 1), ("u_full", 1, 1),
                                ("d_full", 2, 1), ("o_full", 1, 1), ("g_full", 1, 1), ("fin", 1, 1), ("o_empty", 1, 4),
-                               ("gt_ready", NG, 1), ("l_ready", 1, 4), ("d_free", 1, 1), ("gt_free", NG, 4 if out else 1)):
+                               ("gt_ready", NG, 1), ("l_ready", 1, 4), ("d_free", 1, 1), ("gt_free", NG, 4 if out else 8)):
             for i in range(k):
                 b[name, i] = Bar(count)
         self.slot, self.readers = [None] * NG, [0] * NG
@@ -209,7 +209,6 @@ class Sim:
             yield from commit(("d_full", 0), ("d_full", 1))
             if not out:
                 yield from commit(("kq_empty", m % NKQ))
-                yield "arrive", "gt_free", m % NG
                 if m + 2 < n:
                     yield "wait", "g_read", 0, (m + 1) & 1
                     yield from gram(m + 2)
@@ -234,6 +233,8 @@ class Sim:
             yield "read", m % NG, m, "last"
             for p in range(2):
                 yield "arrive", "u_ready", p
+            if not self.out:
+                yield "arrive", "gt_free", m % NG
             if self.out:
                 yield "arrive", "p_ready", 0
             for p in range(2):
