@@ -652,7 +652,8 @@ def delta_forward(q, k, v, log_g, beta, S0=None, scale=None, want_state=True, pa
     q, k [B,Hk,T,dk], v [B,H,T,dv], beta [B,H,T] (bf16 or fp32, one type); log_g fp32 [B,H,T] or
     None; S0 fp32 [B,H,dk,dv] or None; scale defaults to dk^-0.5. Returns (O, S_T). A decoding
     loop passes ST=S0 to carry the state in place; O and ST count as modified in place. Values are finite
-    (log_g may be -inf), those of padded rows too. With `stream` the outputs may be used there,
+    (log_g may be -inf), those of padded rows too. Tensors are contiguous and start on 16 bytes (log_g and beta on
+    their values' size). With `stream` the outputs may be used there,
     and on other streams after it.
     """
     import torch
@@ -783,8 +784,8 @@ def _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleave
 def qk_norm_rope_forward(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv_freq=None, positions=None, start=0,
                          interleaved=False, stream=None):
     """Norm, weight and position rotation of every row of q [B,H,T,d] and k [B,Hk,T,d] (or None) in
-    one pass (gla_qk_norm_rope). Inputs may be strided views, the last dimension contiguous;
-    returns dense (q', k'). inv_freq: fp64 [rot/2], radians per position (None: no rotation);
+    one pass (gla_qk_norm_rope). Inputs may be strided views, the last dimension contiguous and every row, and the
+    weights, from a 16-byte boundary; returns dense (q', k'). inv_freq: fp64 [rot/2], radians per position (None: no rotation);
     positions: int64 [B,T], else start + t."""
     import torch
     p = _qk_params(q, k, norm, w_q, w_k, eps, inv_freq, positions, start, interleaved)
