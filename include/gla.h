@@ -481,12 +481,13 @@ size_t gla_delta_bwd_workspace_size(const gla_delta_bwd_params* p);
  *     n(x) = sqrt(sum x^2 + eps)  (GLA_NORM_L2: unit rows, what the delta rule wants)
  *          = sqrt(mean x^2 + eps) (GLA_NORM_RMS)   or 1 (GLA_NORM_NONE)
  *     y = R(pos) (w (.) x / n(x)),
- * w per value, from a 16-byte boundary (NULL: 1). R turns the pairs of the first `rot` values (a multiple of 16, 0: no
- * rotation) by pos * inv_freq[i] radians: pair i is (2i, 2i+1) when `interleaved`, else
- * (i, i + rot/2). The angle is taken modulo a turn in 64-bit integers, with inv_freq / (2 pi)
- * rounded to fp64 once: off by at most |pos * inv_freq| 2^-52 + |pos| 2^-62 radians beside its
- * fp32 rounding (2e-10 at a million positions of one radian, 2e-4 at 2^40). Position of token t of row b: positions[b,t], or start + t when positions is NULL;
- * any 64-bit value. Inputs are read through strides in elements (batch, head, token; the last
+ * w per value, from a 16-byte boundary (NULL: 1). R turns the pairs of the first `rot` values (a
+ * multiple of 16, 0: no rotation) by pos * inv_freq[i] radians: pair i is (2i, 2i+1) when
+ * `interleaved`, else (i, i + rot/2). The angle is taken modulo a turn in 64-bit integers, with
+ * inv_freq / (2 pi) rounded to fp64 once: off by at most |pos * inv_freq| 2^-52 + |pos| 2^-62
+ * radians beside its fp32 rounding (2e-10 at a million positions of one radian, 2e-4 at 2^40).
+ * Position of token t of row b: positions[b,t], or start + t when positions is NULL; any 64-bit
+ * value. Inputs are read through strides in elements (batch, head, token; the last
  * dimension contiguous), every row starting on 16 bytes; strides may be zero or negative.
  * d is a multiple of 16 up to 256. Hk = 0 with k = NULL takes q alone.
  */
