@@ -6,19 +6,23 @@
 //   dQ  = scale e (dO S^T) + W K,
 //   dK  = [M K - e (dV S^T)]  +  [M^T K + W^T Q + l (U dS^T)]      (row role + column role),
 //   dbeta_i = (dV_i . u_i) / beta_i^2,
-//   dlog_g_t = sum over i >= t of (q_i . dQ_i + k_i . dK_row_i - k_i . dK_col_i) + <dS, S'>,
-//   <dS, S'> = exp(G_end) <dS, S> + sum_i k_i . (l U dS^T)_i   (S' the state leaving the chunk).
+//   dlog_g_t = sum over i >= t of (q_i . scale e (dO S^T)_i - k_i . e (dV S^T)_i)    (the state entering, read at i)
+//            + sum over j < t of k_j . l (U dS^T)_j                                    (token j in the state leaving)
+//            + exp(G_end) <dS, S> + sum over i >= t > j of Z_ij,   Z_ij = W_ij (q_i . k_j) + M_ij (k_i . k_j).
 //
-// The gate's gradient is a sum of nearly cancelling terms, so every operand that is not an input
-// comes in two bf16 parts and products keep hi hi + hi lo + lo hi. To use 128 tensor-memory lanes
+// dlog_g_t is the sum over all that decays across token t, pair by pair, and is formed as that: as the running sum of
+// q . dQ + k . dK_row - k . dK_col, which is the same, it cancels what both of a pair's tokens lie behind t, and of a steep
+// gate's gradient few digits were left (2e-4 off at decays around e^-6, none right at e^-14). Its terms have both signs, so every operand
+// that is not an input comes in two bf16 parts and products keep hi hi + hi lo + lo hi. To use 128 tensor-memory lanes
 // the operands are stacked: [dO; dV] on the left of U^T and of S^T, [U; U_lo] on the left of
 // dS^T (both halves of the result belong to one row and are added at the end), [W; M] on the left
 // of K, and transposed, hi over lo, on the left of [Q; K].
 //
 // One persistent CTA per SM (the operands and accumulators fill its shared and tensor memory) walks
 // the chunks; the next chunk's dO, dV, U and S are loaded as soon as this one's are used. Bound by its
-// loads, 240 KB per chunk at dk = dv = 128, and the latency of its own steps, about equally: 231 us for
-// 8 x 2048 tokens of 16 heads, 4.9 TB/s (345 with a CTA per chunk and nothing loaded ahead).
+// loads, 240 KB per chunk at dk = dv = 128, and the latency of its own steps, about equally: 245 us for
+// 8 x 2048 tokens of 16 heads, 4.6 TB/s (of which the pairs' sums 13; with a CTA per chunk and nothing loaded ahead
+// it was 345 to 231).
 #include "gla_delta_dev.cuh"
 #include "gla_delta_internal.h"
 
@@ -43,12 +47,13 @@ struct GL {
     static constexpr int SB = NS * 2 * SLAB;                  // one part
     static constexpr int G_OFF = S_OFF + 2 * SB;              // gates, 8 x 64 floats
     static constexpr int R_OFF = G_OFF + 8 * C * 4;           // row sums 4 x 64, state sums 4 x 64, 8 partials
-    static constexpr int BAR_OFF = R_OFF + 8 * C * 4 + 64;
+    static constexpr int F_OFF = R_OFF + 8 * C * 4 + 64;      // the pairs' part of dlog_g: 8 warps and two suffix sums x 32
+    static constexpr int BAR_OFF = F_OFF + 10 * 32 * 4;
     static constexpr int SMEM = BAR_OFF + 128 + 1024;
     static constexpr int W_OFF = XB_OFF;                      // [W; M] in two parts, once dV_lo is used
     static constexpr int E_OFF = XB_OFF;                      // then dK's partial rows (fp32), when W is used
     static_assert(64 * DK * 4 <= 4 * SLAB, "exchange buffer");
-    static constexpr int t1 = 0, t2 = 128, t3 = 256, tH = 384, tH2 = 0;
+    static constexpr int t1 = 0, tG = 64, t2 = 128, t3 = 256, tH = 384, tH2 = 0;   // tG: [Q; K] K^T, until tH2 is formed
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -80,20 +85,22 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     uint64_t* m_1 = bar + 6;     // products with U^T and S^T done
     uint64_t* m_3 = bar + 7;     // products with dS^T done
     uint64_t* m_h = bar + 8;     // products of W and M done
-    uint64_t* fin = bar + 9;     // every product done
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 10);
-    const Abort abort_flag(bar + 11);
+    uint64_t* m_g = bar + 9;     // the scores done
+    uint64_t* fin = bar + 10;    // every product done
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 11);
+    const Abort abort_flag(bar + 12);
     float* gt = reinterpret_cast<float*>(sm + L::G_OFF);
     float* rs = reinterpret_cast<float*>(sm + L::R_OFF);        // [4][64] row sums
     float* ss = rs + 4 * C;                                     // [4][64] k . (l U dS^T)
     float* ip = ss + 4 * C;                                     // [8] warps' parts of <dS, S>
+    float* fz = reinterpret_cast<float*>(sm + L::F_OFF);        // [8][32] and [2][32]
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid % 32;
     const int ntile = (a.dv + 127) / 128;
     const int total = a.B * a.H * a.nch;
 
     if (tid == 0) {
-        for (int i = 0; i < 10; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < 11; ++i) mbar_init(&bar[i], 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -250,6 +257,22 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
                 if (more && vt == ntile - 1) load_xa(at + gridDim.x, 0);   // (the next chunk's)
             }
             __syncwarp();
+            if (vt == ntile - 1 && a.dlog_g) {
+                // the scores, for the gate, while dS is on its way
+                ok &= wait(b_qk, it & 1, abort_flag, status, ERR_LOAD);
+                __syncwarp();
+                const uint32_t idG = idesc_bf16(128, 64, false, false);
+                const uint64_t dG = sdesc(s0 + L::QK_OFF, 16, 1024, kSwizzle128), dG2 = sdesc(s0 + L::QK_OFF + SLAB, 16, 1024, kSwizzle128);
+                if (elect_one() && ok) {
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk) {
+                        const uint64_t o = ((kk >> 2) * 2 * SLAB + (kk & 3) * 32) >> 4;
+                        mma_ss(tm + L::tG, dG + o, dG2 + o, idG, kk > 0);
+                    }
+                    mma_commit(m_g);
+                }
+                __syncwarp();
+            }
             const uint64_t dU = sdesc(s0 + L::U_OFF, 2 * SLAB, 1024, kSwizzle128);   // tokens along M: U on U_lo
             const uint64_t dS = sdesc(s0 + L::S_OFF, 2 * SLAB, 1024, kSwizzle128);
             const uint32_t id3 = idesc_bf16(128, DK, true, true);
@@ -288,15 +311,16 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
     const uint32_t lb = (uint32_t)(quarter * 32) << 16;
     tc_fence_after();
     ok &= wait(b_qk, it & 1, abort_flag, status, ERR_LOAD);
+    const int c0 = hf * 32;
+    float x[32];                  // this row's W or M, and its scores
+    uint32_t kqk[32];
     {
-        const int c0 = hf * 32;
         uint32_t r[32];
         tmem_ld32(tm + lb + L::t1 + c0, r);
         tmem_wait_ld();
         const bool near = gt[4 * C] != 0.f;
         const float f = low ? a.scale : -1.f;
         const int last = low ? i : i - 1;
-        float x[32];
         if (!low && i >= c0 && i < c0 + 32) {
             float d = 0.f;
 #pragma unroll
@@ -321,6 +345,15 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             for (int j = 0; j < 32; ++j)
                 x[j] = f * __uint_as_float(r[j]) * expf((gh - gt[6 * C + c0 + j]) + (gl - gt[7 * C + c0 + j]));
         }
+        // (nothing above the diagonal; there x may be anything)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = c0 + j <= last ? x[j] : 0.f;
+        if (a.dlog_g) {                 // (the products of W and M lie over the scores)
+            ok &= wait(m_g, it & 1, abort_flag, status, ERR_MMA);
+            tc_fence_after();
+            tmem_ld32(tm + lb + L::tG + c0, kqk);
+            tmem_wait_ld();
+        }
         // rows of 64 values, hi then lo; the products with dO and dV, whose place this is, are done
         const uint32_t wo = s0 + L::W_OFF + row * 128;
 #pragma unroll
@@ -329,7 +362,7 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int j = 8 * p + 2 * e;
-                split2(c0 + j <= last ? x[j] : 0.f, c0 + j + 1 <= last ? x[j + 1] : 0.f, hi[e], lo[e]);
+                split2(x[j], x[j + 1], hi[e], lo[e]);
             }
             const uint32_t o = wo + (((hf * 4 + p) ^ (row & 7)) << 4);
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(o), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]));
@@ -361,6 +394,39 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             mma_commit(m_h);
         }
         __syncwarp();
+    }
+    if (a.dlog_g) {
+        // While those products run: the pairs across token t = c0 + j, of this row for j' in c0 .. t - 1, if the row is not
+        // before t; then over the warp's rows, which leaves token c0 + lane with a lane (halves of the 32 values are
+        // exchanged for halves of the lanes, five times).
+        float z[32], run = 0.f;
+        z[0] = 0.f;
+        if (hf == 0 || (quarter & 1)) {         // (the first rows have no pairs in the second half)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                z[j] = i >= c0 + j ? run : 0.f;
+                run = fmaf(x[j], __uint_as_float(kqk[j]), run);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const bool up = lane & o;
+#pragma unroll
+                for (int j = 0; j < o; ++j) {
+                    const float other = __shfl_xor_sync(~0u, up ? z[j] : z[j + o], o);
+                    z[j] = (up ? z[j + o] : z[j]) + other;
+                }
+            }
+        }
+        fz[warp * 32 + lane] = z[0];
+        // a row of the second half has all of the first half's columns before every t of its own half
+        if (hf == 0 && (quarter & 1)) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float later = __shfl_down_sync(~0u, run, o);
+                if (lane + o < 32) run += later;
+            }
+            fz[(8 + (quarter >> 1)) * 32 + lane] = run;
+        }
     }
     ok &= wait(m_3, (cnt - 1) & 1, abort_flag, status, ERR_MMA);
     ok &= wait(m_h, it & 1, abort_flag, status, ERR_MMA);
@@ -413,11 +479,11 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             float x[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
+                const float read = f2s * __uint_as_float(g2[j]);
                 const float own = fmaf(f2s, __uint_as_float(g2[j]), __uint_as_float(g4[j]));
                 const float state = l * __uint_as_float(g3[j]);
                 const float cr = state + __uint_as_float(g5[j]);
-                sum = fmaf(low ? q[j] : kr[j], own, sum);
-                sum = fmaf(-kr[j], cr, sum);
+                sum = fmaf(low ? q[j] : kr[j], read, sum);
                 st = fmaf(kr[j], state, st);
                 col[kc + j] = cr;
                 x[j] = low ? own : own + cr;
@@ -450,30 +516,44 @@ gla_delta_grads_kernel(DeltaGrads a, const __grid_constant__ GMaps mp, int* stat
             }
         }
         if (warp == 4 && a.dlog_g) {
-            // per token, then the sum over the later ones, two tokens a lane
-            float x0 = 0.f, x1 = 0.f, s = 0.f;
-            const int p = 2 * lane;
+            // two tokens a lane: what reads the state behind them, what they find written, the pairs across, the state
+            // through the chunk
+            const int p = 2 * lane, half = p >> 5;
+            float r0 = 0.f, r1 = 0.f, w0 = 0.f, w1 = 0.f, f0 = 0.f, f1 = 0.f;
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-                x0 += rs[z * C + p];
-                x1 += rs[z * C + p + 1];
-                s += ss[z * C + p] + ss[z * C + p + 1];
+                r0 += rs[z * C + p];
+                r1 += rs[z * C + p + 1];
+                w0 += ss[z * C + p];
+                w1 += ss[z * C + p + 1];
+                f0 += fz[(half * 4 + z) * 32 + (p & 31)];
+                f1 += fz[(half * 4 + z) * 32 + (p & 31) + 1];
             }
+            if (half) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+                for (int z = 8; z < 10; ++z) {
+                    f0 += fz[z * 32 + (p & 31)];
+                    f1 += fz[z * 32 + (p & 31) + 1];
+                }
+            }
             float in8 = 0.f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) in8 += ip[w];
-            s = fmaf(gt[2 * C - 1], in8, s);            // <dS, S'>
-            float y = x0 + x1;
+            const float s = gt[2 * C - 1] * in8;
+            float y = r0 + r1, x = w0 + w1;          // over the later lanes, over the earlier ones
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float z = __shfl_down_sync(~0u, y, o);
-                if (lane + o < 32) y += z;
+                const float u = __shfl_down_sync(~0u, y, o), v = __shfl_up_sync(~0u, x, o);
+                if (lane + o < 32) y += u;
+                if (lane >= o) x += v;
             }
+            y = __shfl_down_sync(~0u, y, 1);
+            x = __shfl_up_sync(~0u, x, 1);
+            if (lane == 31) y = 0.f;
+            if (lane == 0) x = 0.f;
             float* out = a.dlog_g + (size_t)bh * a.T + t0 + p;
-            if (t0 + p < a.T) out[0] = y + s;
-            if (t0 + p + 1 < a.T) out[1] = y - x0 + s;
+            if (t0 + p < a.T) out[0] = ((y + r1) + r0) + x + f0 + s;
+            if (t0 + p + 1 < a.T) out[1] = (y + r1) + (x + w0) + f1 + s;
         }
     }
     __syncthreads();        // the exchange is read

@@ -429,6 +429,24 @@ def test_chunk_backward_of_many_chunks(T, dk, dv, gate):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("path", [gla.GLA_PATH_TENSOR, gla.GLA_PATH_SIMT])
+@pytest.mark.parametrize("T,dk,dv", [(6, 128, 192), (84, 128, 192), (200, 64, 64), (70, 64, 320)])
+@pytest.mark.parametrize("decay", [2.0, 6.0, 14.0])
+def test_gradients_of_a_steep_gate(decay, T, dk, dv, path):
+    """Every token decays by about exp(-decay): what is left to differentiate is as small as that, and has all its digits
+    (the same bound relative to its own size as for any gate)."""
+    x, g = ref.make(1, 3, 3, T, dk, dv, torch.bfloat16, seed=T)
+    x[3] = -decay * (1 + torch.rand(x[3].shape, generator=g) / 4)
+    dO = torch.randn(x[2].shape, generator=g).bfloat16()
+    want = reference_grads(x, dO, None, dk ** -0.5)
+    got = gla.delta_backward(*ref.cuda(x), dO.cuda(), path=path)
+    for n in (3, 5):
+        close(got[n], want[n], (8 if n == 3 else 4) * PARTS, NAMES[n])
+    for n in (0, 1, 2, 4):
+        assert_close(to_np(got[n]), to_np(want[n]), torch.bfloat16, NAMES[n])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("i", range(6))
 def test_backward_against_differences_along_the_gradient(i):
     """fp32, recurrent form, one input at a time, moved along its own gradient, so that the derivative is |grad| |d| and a
