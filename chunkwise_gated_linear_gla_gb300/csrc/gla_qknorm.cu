@@ -481,7 +481,8 @@ gla_status gla_qk_norm_rope_bwd(const gla_qk_norm_params* p, const gla_qk_norm_g
             if (!(i == 0 && j == 1) && overlap(out[i], out[j])) return GLA_ERR_INVALID_ARG;
     }
     if (p->T > 0 && g->grad_q == g->grad_k) return GLA_ERR_INVALID_ARG;
-    if (p->T > 0 && (!apart(g->q_stride, p->B, p->H, p->T, p->d) || !apart(g->k_stride, p->B, p->Hk, p->T, p->d)))
+    if (p->T > 0 && (!apart(g->q_stride, p->B, p->H, p->T, p->d) ||
+                     (p->Hk > 0 && !apart(g->k_stride, p->B, p->Hk, p->T, p->d))))
         return GLA_ERR_INVALID_ARG;
     int sms = 0, blocks = 0;
     st = device_ready(&sms);

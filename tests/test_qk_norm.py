@@ -152,6 +152,24 @@ def test_one_tensor_alone_dense_and_broadcast():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("weights", [True, False])
+@pytest.mark.parametrize("B,T", [(1, 1), (2, 1), (1, 5), (3, 40)])
+def test_gradients_of_one_tensor_alone(B, T, weights):
+    """Without k: q's gradient as beside one, bit for bit, and the weight's to its sums' order."""
+    proj, q, k, w, f, pos, g = case(B, 3, 2, T, 64, 32, torch.bfloat16, 3 * B + T, False, True)
+    q, k, dq, dk = (t.bfloat16().cuda() for t in (q, k, torch.randn(q.shape, generator=g), torch.randn(k.shape, generator=g)))
+    wq = w[0].cuda() if weights else None
+    leaves = [t.requires_grad_(True) for t in ([q, wq] if weights else [q])]
+    y, none = gla.qk_norm_rope(q, None, w_q=wq, inv_freq=f.cuda())
+    assert none is None
+    got = torch.autograd.grad(y, leaves, dq)
+    want = gla.qk_norm_rope_backward(q.detach(), k, dq, dk, w_q=None if wq is None else wq.detach(), inv_freq=f.cuda())
+    assert torch.equal(got[0], want[0])
+    if weights:
+        assert torch.allclose(got[1], want[2], rtol=0, atol=1e-5 * float(want[2].norm()))
+
+
+@pytest.mark.gpu
 def test_autograd_through_both_operators():
     """A layer's run: projection -> norms and rotation -> gated delta rule -> loss, against fp64."""
     B, H, Hk, T, d = 1, 4, 2, 100, 64
