@@ -430,6 +430,27 @@ def test_chunk_backward_of_many_chunks(T, dk, dv, gate):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("path", [gla.GLA_PATH_TENSOR, gla.GLA_PATH_SIMT])
+def test_gradients_that_are_not_wanted(path):
+    """grad_log_g, grad_beta and grad_S0 absent: the others are the same, bit for bit; a short workspace is refused."""
+    x, _ = ref.make(1, 4, 2, 70, 64, 64, torch.bfloat16, seed=3)
+    c = ref.cuda(x)
+    dO = torch.ones_like(c[2])
+    want = gla.delta_backward(*c, dO, path=path)
+    out = [torch.empty_like(t) for t in c[:3]]
+    p = bnd.gla_delta_bwd_params(*(t.data_ptr() for t in c), dO.data_ptr(), None, *(t.data_ptr() for t in out),
+                                 None, None, None, 1, 4, 2, 70, 64, 64, 0.125, gla.GLA_BF16, path)
+    ws = torch.empty(bnd.gla_delta_bwd_workspace_size(p), dtype=torch.uint8, device="cuda")
+    p.workspace, p.workspace_bytes = ws.data_ptr(), ws.numel()
+    bnd.gla_delta_bwd(p)
+    torch.cuda.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+    p.workspace_bytes -= 1
+    assert bnd.gla_delta_bwd(p, check=False) == 4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("path", [gla.GLA_PATH_TENSOR, gla.GLA_PATH_SIMT])
 @pytest.mark.parametrize("T,dk,dv", [(6, 128, 192), (84, 128, 192), (200, 64, 64), (70, 64, 320)])
 @pytest.mark.parametrize("decay", [2.0, 6.0, 14.0])
 def test_gradients_of_a_steep_gate(decay, T, dk, dv, path):
