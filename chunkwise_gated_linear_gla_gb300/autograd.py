@@ -12,7 +12,12 @@ forward pass but its inputs: the backward recomputes the chunk states (gla_bwd's
     q, k = qk_norm_rope(q, k, norm="l2", inv_freq=f)      # norms of q and k, position rotation
 
 delta_attention's backward runs gla_delta_bwd and qk_norm_rope's gla_qk_norm_rope_bwd; both
-keep their inputs only.
+keep their inputs only. So do, each with the _bwd call of its kernel,
+
+    y, ST = causal_conv(x, w, bias, S0)                   # the short causal convolution
+    y, ST = selective_scan(x, dt, A, B, C, D, z, dt_bias, S0)
+    y = norm_gate(x, gate, w)                             # the heads' norm with its gate
+    h, y = residual_norm(x, residual, w, scale)           # the residual with its norm
 """
 from __future__ import annotations
 
@@ -112,6 +117,107 @@ def _qk_function():
     return QkNormRopeFunction
 
 
+def _conv_function():
+    import torch
+
+    class CausalConvFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, bias, S0, activation, want_state):
+            y, ST = _b.causal_conv_forward(x, w, bias, S0, activation, want_state)
+            ctx.activation = activation
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(x, w, bias, S0)
+            return y, ST
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dy, dST):
+            x, w, bias, S0 = ctx.saved_tensors
+            if dy is None and dST is None:
+                return (None,) * 6
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _placed(dy)
+            want = ctx.needs_input_grad
+            g = _b.causal_conv_backward(x, w, bias, S0, dy, None if dST is None else _placed(dST), ctx.activation,
+                                        want_dw=want[1] or want[2], want_dS0=want[3])
+            return (*(x if w else None for x, w in zip(g, want)), None, None)
+
+    return CausalConvFunction
+
+
+def _scan_function():
+    import torch
+
+    class SelectiveScanFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, dt, A, B, C, D, z, dt_bias, S0, softplus, want_state):
+            y, ST = _b.selective_scan_forward(x, dt, A, B, C, D, z, dt_bias, S0, softplus, want_state)
+            ctx.softplus = softplus
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, S0)
+            return y, ST
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dy, dST):
+            t = ctx.saved_tensors
+            if dy is None and dST is None:
+                return (None,) * 11
+            x = t[0]
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _placed(dy)
+            want = ctx.needs_input_grad
+            g = _b.selective_scan_backward(*t, dy, None if dST is None else _placed(dST), ctx.softplus, want_dS0=want[8])
+            return (*(x if w else None for x, w in zip(g, want)), None, None)
+
+    return SelectiveScanFunction
+
+
+def _gate_function():
+    import torch
+
+    class NormGateFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, gate, w, norm, eps, activation, gate_first):
+            ctx.how = norm, eps, activation, gate_first
+            ctx.save_for_backward(x, gate, w)
+            return _b.norm_gate_forward(x, gate, w, norm, eps, activation, gate_first)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dy):
+            x, gate, w = ctx.saved_tensors
+            g = _b.norm_gate_backward(x, gate, w, _placed(dy), *ctx.how)
+            return (*(x if w else None for x, w in zip(g, ctx.needs_input_grad)), None, None, None, None)
+
+    return NormGateFunction
+
+
+def _residual_function():
+    import torch
+
+    class ResidualNormFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, residual, w, scale, post_norm, eps):
+            ctx.number = None if isinstance(scale, torch.Tensor) else scale
+            ctx.how = post_norm, eps
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(x, residual, w, scale if ctx.number is None else None)
+            return _b.residual_norm_forward(x, residual, w, scale, post_norm, eps)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dh, dy):
+            x, residual, w, scale = ctx.saved_tensors
+            if dh is None and dy is None:
+                return (None,) * 6
+            placed = lambda g: None if g is None else _placed(g)  # noqa: E731
+            want = ctx.needs_input_grad
+            g = _b.residual_norm_backward(x, residual, w, scale if ctx.number is None else ctx.number, placed(dh),
+                                          placed(dy), *ctx.how, want_dx=want[0], want_dres=want[1])
+            return (*(x if w else None for x, w in zip(g, want)), None, None)
+
+    return ResidualNormFunction
+
+
 def _plain(*tensors):
     """Whether no derivative of any kind is asked of these inputs (some may be None). A dual tensor of forward
     mode need not require grad, and no_grad() does not switch forward mode off: with a dual level open the
@@ -129,6 +235,10 @@ def _plain(*tensors):
 _FN = None
 _DELTA = None
 _QK = None
+_CONV = None
+_SCAN = None
+_GATE = None
+_RESIDUAL = None
 
 
 def gla_attention(q, k, v, log_g=None, S0=None, gate=None):
@@ -162,3 +272,46 @@ def qk_norm_rope(q, k=None, norm="l2", w_q=None, w_k=None, eps=1e-6, inv_freq=No
     if _QK is None:
         _QK = _qk_function()
     return _QK.apply(q, k, w_q, w_k, inv_freq, positions, norm, eps, start, interleaved)
+
+
+def causal_conv(x, w, bias=None, S0=None, activation="silu", want_state=True):
+    """(y, ST) of the short causal convolution (binding.causal_conv_forward), differentiable once in x, w, bias and S0, in
+    reverse mode."""
+    if _plain(x, w, bias, S0):
+        return _b.causal_conv_forward(x, w, bias, S0, activation, want_state)
+    global _CONV
+    if _CONV is None:
+        _CONV = _conv_function()
+    return _CONV.apply(x, w, bias, S0, activation, want_state)
+
+
+def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, softplus=True, want_state=True):
+    """(y, ST) of the selective scan (binding.selective_scan_forward), differentiable once in every tensor, in reverse
+    mode. What delta_attention says of captured steps holds here too, and for the other functions of this module."""
+    if _plain(x, dt, A, B, C, D, z, dt_bias, S0):
+        return _b.selective_scan_forward(x, dt, A, B, C, D, z, dt_bias, S0, softplus, want_state)
+    global _SCAN
+    if _SCAN is None:
+        _SCAN = _scan_function()
+    return _SCAN.apply(x, dt, A, B, C, D, z, dt_bias, S0, softplus, want_state)
+
+
+def norm_gate(x, gate=None, w=None, norm="rms", eps=1e-6, activation="silu", gate_first=False):
+    """binding.norm_gate_forward, differentiable once in x, gate and w, in reverse mode."""
+    if _plain(x, gate, w):
+        return _b.norm_gate_forward(x, gate, w, norm, eps, activation, gate_first)
+    global _GATE
+    if _GATE is None:
+        _GATE = _gate_function()
+    return _GATE.apply(x, gate, w, norm, eps, activation, gate_first)
+
+
+def residual_norm(x, residual=None, w=None, scale=None, post_norm=False, eps=1e-6):
+    """(h, y) of binding.residual_norm_forward, differentiable once in x, residual, w and a scale that is a tensor, in
+    reverse mode."""
+    if _plain(x, residual, w, None if isinstance(scale, (int, float)) else scale):
+        return _b.residual_norm_forward(x, residual, w, scale, post_norm, eps)
+    global _RESIDUAL
+    if _RESIDUAL is None:
+        _RESIDUAL = _residual_function()
+    return _RESIDUAL.apply(x, residual, w, scale, post_norm, eps)

@@ -17,6 +17,7 @@ GLA_OK, GLA_ERR_INVALID_ARG, GLA_ERR_UNSUPPORTED, GLA_ERR_CUDA, GLA_ERR_WORKSPAC
 GLA_BF16, GLA_FP32 = 0, 1
 GLA_GATE_NONE, GLA_GATE_HEAD_SCALAR, GLA_GATE_PER_KEY, GLA_GATE_TOKEN_SCALAR, GLA_GATE_BILINEAR = 0, 1, 2, 3, 4
 GLA_NORM_NONE, GLA_NORM_L2, GLA_NORM_RMS = 0, 1, 2
+GLA_ACT_NONE, GLA_ACT_SILU, GLA_ACT_SIGMOID = 0, 1, 2
 GLA_PATH_AUTO, GLA_PATH_TENSOR, GLA_PATH_SIMT, GLA_PATH_STAGED, GLA_PATH_FUSED, GLA_PATH_SPLIT = 0, 1, 2, 3, 4, 5
 
 # Every symbol include/gla.h declares.
@@ -27,7 +28,11 @@ EXPORTED = ("gla_fwd", "gla_fwd_ex", "gla_fwd_workspace_size", "gla_fwd_num_stag
             "gla_segment_pair_workspace_size", "gla_segment_pair",
             "gla_pair_scan", "gla_pair_combine", "gla_selftest_bounded_wait",
             "gla_delta_fwd", "gla_delta_fwd_workspace_size", "gla_delta_bwd", "gla_delta_bwd_workspace_size",
-            "gla_qk_norm_rope", "gla_qk_norm_rope_bwd", "gla_qk_norm_rope_bwd_workspace_size")
+            "gla_qk_norm_rope", "gla_qk_norm_rope_bwd", "gla_qk_norm_rope_bwd_workspace_size",
+            "gla_conv_fwd", "gla_conv_bwd", "gla_conv_bwd_workspace_size",
+            "gla_ssm_fwd", "gla_ssm_fwd_workspace_size", "gla_ssm_bwd", "gla_ssm_bwd_workspace_size",
+            "gla_norm_gate", "gla_norm_gate_bwd", "gla_norm_gate_bwd_workspace_size",
+            "gla_residual_norm", "gla_residual_norm_bwd", "gla_residual_norm_bwd_workspace_size")
 
 
 class GlaError(RuntimeError):
@@ -113,6 +118,71 @@ class gla_qk_norm_grads(ctypes.Structure):
     ]
 
 
+class gla_conv_params(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("x_stride", ctypes.c_longlong * 3),
+        ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("S0", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int), ("d", ctypes.c_int), ("W", ctypes.c_int),
+        ("activation", ctypes.c_int), ("dtype", ctypes.c_int),
+    ]
+
+
+class gla_conv_grads(ctypes.Structure):
+    _fields_ = [
+        ("grad_y", ctypes.c_void_p), ("grad_ST", ctypes.c_void_p),
+        ("grad_x", ctypes.c_void_p), ("x_stride", ctypes.c_longlong * 3),
+        ("grad_w", ctypes.c_void_p), ("grad_bias", ctypes.c_void_p), ("grad_S0", ctypes.c_void_p),
+    ]
+
+
+class gla_ssm_params(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("dt", ctypes.c_void_p), ("z", ctypes.c_void_p),
+        ("Bm", ctypes.c_void_p), ("Cm", ctypes.c_void_p),
+        ("x_stride", ctypes.c_longlong * 2), ("dt_stride", ctypes.c_longlong * 2), ("z_stride", ctypes.c_longlong * 2),
+        ("B_stride", ctypes.c_longlong * 2), ("C_stride", ctypes.c_longlong * 2),
+        ("A", ctypes.c_void_p), ("D_skip", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("S0", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("G", ctypes.c_int), ("N", ctypes.c_int),
+        ("softplus", ctypes.c_int), ("dtype", ctypes.c_int), ("force_segments", ctypes.c_int),
+    ]
+
+
+class gla_ssm_grads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "grad_y", "grad_ST", "grad_x", "grad_dt", "grad_z", "grad_B", "grad_C", "grad_A", "grad_D", "grad_dt_bias",
+        "grad_S0")]
+
+
+class gla_norm_gate_params(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+        ("x_stride", ctypes.c_longlong * 3), ("gate_stride", ctypes.c_longlong * 3), ("w", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int), ("d", ctypes.c_int),
+        ("norm", ctypes.c_int), ("activation", ctypes.c_int), ("gate_first", ctypes.c_int),
+        ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+    ]
+
+
+class gla_norm_gate_grads(ctypes.Structure):
+    _fields_ = [
+        ("grad_y", ctypes.c_void_p), ("grad_x", ctypes.c_void_p), ("grad_gate", ctypes.c_void_p),
+        ("x_stride", ctypes.c_longlong * 3), ("gate_stride", ctypes.c_longlong * 3), ("grad_w", ctypes.c_void_p),
+    ]
+
+
+class gla_residual_params(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("w", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+        ("alpha", ctypes.c_float), ("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("post_norm", ctypes.c_int),
+        ("eps", ctypes.c_float), ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
+    ]
+
+
+class gla_residual_grads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "grad_h", "grad_y", "grad_x", "grad_residual", "grad_w", "grad_scale")]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -182,12 +252,24 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.gla_pair_combine.argtypes = [vp, vp, vp, vp, i, i, i, i, vp]
         D, DB = ctypes.POINTER(gla_delta_params), ctypes.POINTER(gla_delta_bwd_params)
         N, NG = ctypes.POINTER(gla_qk_norm_params), ctypes.POINTER(gla_qk_norm_grads)
+        C, CG = ctypes.POINTER(gla_conv_params), ctypes.POINTER(gla_conv_grads)
+        S, SG = ctypes.POINTER(gla_ssm_params), ctypes.POINTER(gla_ssm_grads)
+        NR, NRG = ctypes.POINTER(gla_norm_gate_params), ctypes.POINTER(gla_norm_gate_grads)
+        R, RG = ctypes.POINTER(gla_residual_params), ctypes.POINTER(gla_residual_grads)
         for name, restype, argtypes in (
                 ("gla_delta_fwd", st, [D, vp]), ("gla_delta_fwd_workspace_size", ctypes.c_size_t, [D]),
                 ("gla_delta_bwd", st, [DB, vp]), ("gla_delta_bwd_workspace_size", ctypes.c_size_t, [DB]),
                 ("gla_qk_norm_rope", st, [N, vp, vp, vp]),
                 ("gla_qk_norm_rope_bwd", st, [N, NG, vp, ctypes.c_size_t, vp]),
-                ("gla_qk_norm_rope_bwd_workspace_size", ctypes.c_size_t, [N])):
+                ("gla_qk_norm_rope_bwd_workspace_size", ctypes.c_size_t, [N]),
+                ("gla_conv_fwd", st, [C, vp, vp, vp]), ("gla_conv_bwd", st, [C, CG, vp, ctypes.c_size_t, vp]),
+                ("gla_conv_bwd_workspace_size", ctypes.c_size_t, [C]),
+                ("gla_ssm_fwd", st, [S, vp, vp, vp, ctypes.c_size_t, vp]), ("gla_ssm_fwd_workspace_size", ctypes.c_size_t, [S]),
+                ("gla_ssm_bwd", st, [S, SG, vp, ctypes.c_size_t, vp]), ("gla_ssm_bwd_workspace_size", ctypes.c_size_t, [S]),
+                ("gla_norm_gate", st, [NR, vp, vp]), ("gla_norm_gate_bwd", st, [NR, NRG, vp, ctypes.c_size_t, vp]),
+                ("gla_norm_gate_bwd_workspace_size", ctypes.c_size_t, [NR]),
+                ("gla_residual_norm", st, [R, vp, vp, vp]), ("gla_residual_norm_bwd", st, [R, RG, vp, ctypes.c_size_t, vp]),
+                ("gla_residual_norm_bwd_workspace_size", ctypes.c_size_t, [R])):
             f = getattr(lib, name)
             f.restype, f.argtypes = restype, argtypes
         _lib = lib
@@ -841,3 +923,415 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, norm="l2", w_q=None, w_k=None, e
     _launch(lambda r, s: lib.gla_qk_norm_rope_bwd(r, ctypes.byref(g), pw, n, s), "gla_qk_norm_rope_bwd", p, dev, stream,
             gq, gk, gwq, gwk, ws)
     return gq, gk, gwq, gwk
+
+
+# ---------------------------------------------------------------- what stands around the recurrences
+
+_ACTS = {None: GLA_ACT_NONE, "silu": GLA_ACT_SILU, "sigmoid": GLA_ACT_SIGMOID}
+
+
+def _ws_bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def gla_conv_fwd(p: gla_conv_params, y, ST=None, stream=None, check=True) -> int:
+    s = load().gla_conv_fwd(ctypes.byref(p), _ptr(y), _ptr(ST), _stream(stream))
+    if check:
+        _check(s, "gla_conv_fwd")
+    return s
+
+
+def gla_conv_bwd(p: gla_conv_params, g: gla_conv_grads, workspace=None, stream=None, check=True) -> int:
+    s = load().gla_conv_bwd(ctypes.byref(p), ctypes.byref(g), _ptr(workspace), _ws_bytes(workspace), _stream(stream))
+    if check:
+        _check(s, "gla_conv_bwd")
+    return s
+
+
+def gla_conv_bwd_workspace_size(p: gla_conv_params) -> int:
+    return load().gla_conv_bwd_workspace_size(ctypes.byref(p))
+
+
+def gla_ssm_fwd(p: gla_ssm_params, y, ST=None, workspace=None, stream=None, check=True) -> int:
+    s = load().gla_ssm_fwd(ctypes.byref(p), _ptr(y), _ptr(ST), _ptr(workspace), _ws_bytes(workspace), _stream(stream))
+    if check:
+        _check(s, "gla_ssm_fwd")
+    return s
+
+
+def gla_ssm_fwd_workspace_size(p: gla_ssm_params) -> int:
+    return load().gla_ssm_fwd_workspace_size(ctypes.byref(p))
+
+
+def gla_ssm_bwd(p: gla_ssm_params, g: gla_ssm_grads, workspace=None, stream=None, check=True) -> int:
+    s = load().gla_ssm_bwd(ctypes.byref(p), ctypes.byref(g), _ptr(workspace), _ws_bytes(workspace), _stream(stream))
+    if check:
+        _check(s, "gla_ssm_bwd")
+    return s
+
+
+def gla_ssm_bwd_workspace_size(p: gla_ssm_params) -> int:
+    return load().gla_ssm_bwd_workspace_size(ctypes.byref(p))
+
+
+def gla_norm_gate(p: gla_norm_gate_params, y, stream=None, check=True) -> int:
+    s = load().gla_norm_gate(ctypes.byref(p), _ptr(y), _stream(stream))
+    if check:
+        _check(s, "gla_norm_gate")
+    return s
+
+
+def gla_norm_gate_bwd(p: gla_norm_gate_params, g: gla_norm_gate_grads, workspace=None, stream=None, check=True) -> int:
+    s = load().gla_norm_gate_bwd(ctypes.byref(p), ctypes.byref(g), _ptr(workspace), _ws_bytes(workspace), _stream(stream))
+    if check:
+        _check(s, "gla_norm_gate_bwd")
+    return s
+
+
+def gla_norm_gate_bwd_workspace_size(p: gla_norm_gate_params) -> int:
+    return load().gla_norm_gate_bwd_workspace_size(ctypes.byref(p))
+
+
+def gla_residual_norm(p: gla_residual_params, h, y, stream=None, check=True) -> int:
+    s = load().gla_residual_norm(ctypes.byref(p), _ptr(h), _ptr(y), _stream(stream))
+    if check:
+        _check(s, "gla_residual_norm")
+    return s
+
+
+def gla_residual_norm_bwd(p: gla_residual_params, g: gla_residual_grads, workspace=None, stream=None, check=True) -> int:
+    s = load().gla_residual_norm_bwd(ctypes.byref(p), ctypes.byref(g), _ptr(workspace), _ws_bytes(workspace), _stream(stream))
+    if check:
+        _check(s, "gla_residual_norm_bwd")
+    return s
+
+
+def gla_residual_norm_bwd_workspace_size(p: gla_residual_params) -> int:
+    return load().gla_residual_norm_bwd_workspace_size(ctypes.byref(p))
+
+
+def _rows(t, shape, dtype, device, what):
+    """A tensor of this shape, type and device whose last dimension is contiguous."""
+    if t.shape != shape:
+        _refuse(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype != dtype or t.device != device:
+        _refuse(f"{what} is {t.dtype} on {t.device}, not {dtype} on {device}")
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        _refuse(f"the last dimension of {what} is not contiguous")
+
+
+def _workspace(nbytes, device):
+    """(tensor or None, its pointer): torch hands out blocks of 512 bytes."""
+    import torch
+    if not nbytes:
+        return None, None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr()
+
+
+def _conv_params(x, w, bias, S0, activation):
+    import torch
+    if activation not in (None, "silu"):
+        _refuse(f"activation is None or 'silu', not {activation!r}")
+    if x.dim() == 3:
+        (B, T, d), H = x.shape, 1
+        s = x.stride()
+        steps = _steps((s[0], 0, s[1]), B, 1, T)
+    elif x.dim() == 4:
+        B, H, T, d = x.shape
+        steps = _steps(x.stride(), B, H, T)
+    else:
+        _refuse("x has three or four dimensions: [B,T,D] or [B,H,T,d]")
+    dt, dev, D = x.dtype, x.device, H * d
+    code = _dtype_code(x, "x")
+    _rows(x, x.shape, dt, dev, "x")
+    if w.dim() != 2:
+        _refuse("w has two dimensions: [H d, W]")
+    W = w.shape[1]
+    _dense(w, (D, W), torch.float32, dev, "w")
+    if bias is not None:
+        _dense(bias, (D,), torch.float32, dev, "bias")
+    if S0 is not None:
+        _dense(S0, (B, W - 1, D), dt, dev, "S0")
+    _on_gpu(x, "x")
+    if B == 0:
+        _refuse("an empty batch")
+    return gla_conv_params(_ptr(x), steps, _ptr(w), _ptr(bias), _ptr(S0), B, H, T, d, W, _ACTS[activation], code), D
+
+
+def causal_conv_forward(x, w, bias=None, S0=None, activation="silu", want_state=True, stream=None, y=None, ST=None):
+    """The short causal convolution of every channel (gla_conv_fwd), outputs from torch.
+
+    x [B,T,D] or, head by head, [B,H,T,d] (bf16 or fp32; strided views, the last dimension contiguous and every row from a
+    16-byte boundary); w fp32 [D,W] with D = H d and W 2 to 4, bias fp32 [D] or None; S0 [B,W-1,D] in x's type, the W - 1
+    rows before the first token, oldest first, or None (zeros); activation "silu" or None. Returns (y, ST): y dense in
+    x's shape, ST the last W - 1 rows of (S0, x) (None unless wanted). A decoding loop passes ST=S0 to carry the state
+    in place; y and ST count as modified in place. A batch of unequal prompts is padded in front, with zeros.
+    """
+    p, D = _conv_params(x, w, bias, S0, activation)
+    dev, shape = x.device, (p.B, p.W - 1, D)
+    if y is not None:
+        _dense(y, x.shape, x.dtype, dev, "y")
+        _given(y, "y")
+    if ST is not None:
+        _dense(ST, shape, x.dtype, dev, "ST")
+        _given(ST, "ST")
+    given = y, ST
+    lib = _lib or load()
+    if y is None:
+        y = x.new_empty(x.shape)
+    if ST is None and want_state:
+        ST = x.new_empty(shape)
+    py, ps = _ptr(y), _ptr(ST)
+    _launch(lambda r, s: lib.gla_conv_fwd(r, py, ps, s), "gla_conv_fwd", p, dev, stream, y, ST)
+    _written(*given)
+    return y, ST
+
+
+def causal_conv_backward(x, w, bias, S0, dy, dST=None, activation="silu", want_dw=True, want_dS0=True, stream=None):
+    """Gradients of causal_conv_forward: (dx, dw, dbias, dS0); dx (token-major where x is a token-major view) and dS0 in
+    x's type, dw and dbias fp32; dw and dbias None unless wanted, dbias without a bias, dS0 unless wanted (it is defined
+    without S0 too, zeros)."""
+    import torch
+    p, D = _conv_params(x, w, bias, S0, activation)
+    dev = x.device
+    _dense(dy, x.shape, x.dtype, dev, "dy")
+    if dST is not None:
+        _dense(dST, (p.B, p.W - 1, D), x.dtype, dev, "dST")
+    lib = _lib or load()
+    gx = x.new_empty(x.shape) if x.dim() == 3 else _rows_like(x)
+    gw = torch.empty_like(w) if want_dw else None
+    gb = torch.empty_like(bias) if want_dw and bias is not None else None
+    gs = x.new_empty((p.B, p.W - 1, D)) if want_dS0 else None
+    s = gx.stride()
+    steps = _steps((s[0], 0, s[1]), p.B, 1, p.T) if x.dim() == 3 else _steps(s, p.B, p.H, p.T)
+    g = gla_conv_grads(_ptr(dy), _ptr(dST), _ptr(gx), steps, _ptr(gw), _ptr(gb), _ptr(gs))
+    n = _here_size(lib.gla_conv_bwd_workspace_size, p, dev) if want_dw else 0
+    ws, pw = _workspace(n, dev)
+    _launch(lambda r, s: lib.gla_conv_bwd(r, ctypes.byref(g), pw, n, s), "gla_conv_bwd", p, dev, stream, gx, gw, gb, gs, ws)
+    return gx, gw, gb, gs
+
+
+_Steps2 = ctypes.c_longlong * 2
+
+
+def _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments=0):
+    import torch
+    if x.dim() != 3 or B.dim() != 4 or A.dim() != 2:
+        _refuse("x has three dimensions [B,T,D], B and C four [B,T,G,N], A two [D,N]")
+    nb, T, nd = x.shape
+    G, N = B.shape[2:]
+    t, dev, f32 = x.dtype, x.device, torch.float32
+    code = _dtype_code(x, "x")
+    if G == 0 or nd % G:
+        _refuse(f"{nd} channels do not divide over {G} groups of B and C")
+    _rows(x, (nb, T, nd), t, dev, "x")
+    _rows(dt, (nb, T, nd), t, dev, "dt")
+    if z is not None:
+        _rows(z, (nb, T, nd), t, dev, "z")
+    for m, what in ((B, "B"), (C, "C")):
+        _rows(m, (nb, T, G, N), t, dev, what)
+        if G > 1 and m.stride(2) != N:
+            _refuse(f"the groups of {what} do not lie side by side")
+    _dense(A, (nd, N), f32, dev, "A")
+    if D is not None:
+        _dense(D, (nd,), f32, dev, "D")
+    if dt_bias is not None:
+        _dense(dt_bias, (nd,), f32, dev, "dt_bias")
+    if S0 is not None:
+        _dense(S0, (nb, nd, N), f32, dev, "S0")
+    _on_gpu(x, "x")
+    if nb == 0:
+        _refuse("an empty batch")
+    steps = lambda m: _Steps2(0, 0) if m is None else _Steps2(m.stride(0) if nb > 1 else 0, m.stride(1) if T > 1 else 0)  # noqa: E731
+    return gla_ssm_params(_ptr(x), _ptr(dt), _ptr(z), _ptr(B), _ptr(C), steps(x), steps(dt), steps(z), steps(B), steps(C),
+                          _ptr(A), _ptr(D), _ptr(dt_bias), _ptr(S0), nb, T, nd, G, N, 1 if softplus else 0, code,
+                          force_segments)
+
+
+def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, softplus=True, want_state=True,
+                           stream=None, y=None, ST=None, force_segments=0):
+    """The selective scan (gla_ssm_fwd), outputs and workspace from torch.
+
+    x, dt, z [B,T,D], B and C [B,T,G,N] (bf16 or fp32, one type; strided views, a token's row contiguous and from a 16-byte
+    boundary); A fp32 [D,N], D and dt_bias fp32 [D] or None, S0 fp32 [B,D,N] or None (zero). N is 8, 16, 32 or 64, D / G a
+    multiple of 8. With softplus the steps are softplus(dt + dt_bias), else dt + dt_bias. Returns (y, ST): y dense
+    [B,T,D], ST fp32 [B,D,N] (None unless wanted). A decoding loop passes ST=S0 to carry the state in place; y and ST count
+    as modified in place. A token is passed over where its dt is -inf (with softplus; its other values finite).
+    """
+    import torch
+    p = _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments)
+    dev, states = x.device, (p.B, p.D, p.N)
+    if y is not None:
+        _dense(y, x.shape, x.dtype, dev, "y")
+        _given(y, "y")
+    if ST is not None:
+        _dense(ST, states, torch.float32, dev, "ST")
+        _given(ST, "ST")
+    given = y, ST
+    lib = _lib or load()
+    if y is None:
+        y = x.new_empty(x.shape)
+    if ST is None and want_state:
+        ST = torch.empty(states, dtype=torch.float32, device=dev)
+    n = 0 if p.T <= 8 and not force_segments else _here_size(lib.gla_ssm_fwd_workspace_size, p, dev)
+    ws, pw = _workspace(n, dev)
+    py, ps = _ptr(y), _ptr(ST)
+    _launch(lambda r, s: lib.gla_ssm_fwd(r, py, ps, pw, n, s), "gla_ssm_fwd", p, dev, stream, y, ST, ws)
+    _written(*given)
+    return y, ST
+
+
+def selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, S0, dy, dST=None, softplus=True, want_dS0=True, stream=None,
+                            force_segments=0):
+    """Gradients of selective_scan_forward: (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dS0), dense; dx, ddt, dB, dC and dz in the
+    inputs' type, the others fp32; None without the input, dS0 unless wanted (it is defined without S0 too, zero)."""
+    import torch
+    p = _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments)
+    dev, states = x.device, (p.B, p.D, p.N)
+    _dense(dy, x.shape, x.dtype, dev, "dy")
+    if dST is not None:
+        _dense(dST, states, torch.float32, dev, "dST")
+    lib = _lib or load()
+    like = lambda m: None if m is None else m.new_empty(m.shape)  # noqa: E731
+    gx, gdt, gA, gB, gC, gD, gz, gb = (like(m) for m in (x, dt, A, B, C, D, z, dt_bias))
+    gS = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
+    g = gla_ssm_grads(_ptr(dy), _ptr(dST), _ptr(gx), _ptr(gdt), _ptr(gz), _ptr(gB), _ptr(gC), _ptr(gA), _ptr(gD),
+                      _ptr(gb), _ptr(gS))
+    n = _here_size(lib.gla_ssm_bwd_workspace_size, p, dev)
+    ws, pw = _workspace(n, dev)
+    _launch(lambda r, s: lib.gla_ssm_bwd(r, ctypes.byref(g), pw, n, s), "gla_ssm_bwd", p, dev, stream,
+            gx, gdt, gA, gB, gC, gD, gz, gb, gS, ws)
+    return gx, gdt, gA, gB, gC, gD, gz, gb, gS
+
+
+def _gate_params(x, gate, w, norm, eps, activation, gate_first):
+    import torch
+    if norm not in _NORMS:
+        _refuse(f"norm is None, 'l2' or 'rms', not {norm!r}")
+    if activation not in ("silu", "sigmoid"):
+        _refuse(f"activation is 'silu' or 'sigmoid', not {activation!r}")
+    if x.dim() != 4:
+        _refuse("x has four dimensions: [B,H,T,d]")
+    B, H, T, d = x.shape
+    dev = x.device
+    code = _dtype_code(x, "x")
+    _rows(x, x.shape, x.dtype, dev, "x")
+    if gate is not None:
+        _rows(gate, x.shape, x.dtype, dev, "gate")
+    if w is not None:
+        _dense(w, (d,), torch.float32, dev, "w")
+    _on_gpu(x, "x")
+    return gla_norm_gate_params(_ptr(x), _ptr(gate), _steps(x.stride(), B, H, T),
+                                _NO_STEPS if gate is None else _steps(gate.stride(), B, H, T), _ptr(w), B, H, T, d,
+                                _NORMS[norm], _ACTS[activation], 1 if gate_first else 0, eps, code)
+
+
+def norm_gate_forward(x, gate=None, w=None, norm="rms", eps=1e-6, activation="silu", gate_first=False, stream=None):
+    """Norm, weight and gate of every row of x [B,H,T,d] (a recurrence's output) into the output projection's layout
+    (gla_norm_gate): y = w x / n(x) act(gate), or with gate_first w u / n(u) of u = x act(gate); returns dense [B,T,H,d].
+
+    x and gate (or None: no gate) may be strided views of [B,H,T,d] (bf16 or fp32, one type), the last dimension
+    contiguous and every row from a 16-byte boundary; w fp32 [d] or None; norm "rms", "l2" or None; activation "silu" or
+    "sigmoid"; d a multiple of 16 up to 1024."""
+    p = _gate_params(x, gate, w, norm, eps, activation, gate_first)
+    lib, dev = _lib or load(), x.device
+    B, H, T, d = x.shape
+    y = x.new_empty((B, T, H, d))
+    py = _ptr(y)
+    _launch(lambda r, s: lib.gla_norm_gate(r, py, s), "gla_norm_gate", p, dev, stream, y)
+    return y
+
+
+def norm_gate_backward(x, gate, w, dy, norm="rms", eps=1e-6, activation="silu", gate_first=False, stream=None):
+    """Gradients of norm_gate_forward: (dx, dgate, dw); dx and dgate in the inputs' type (token-major where the input is a
+    token-major view), dw fp32; None where there is no input."""
+    import torch
+    p = _gate_params(x, gate, w, norm, eps, activation, gate_first)
+    B, H, T, d = x.shape
+    _dense(dy, (B, T, H, d), x.dtype, x.device, "dy")
+    lib, dev = _lib or load(), x.device
+    gx, gg = _rows_like(x), None if gate is None else _rows_like(gate)
+    gw = None if w is None else torch.empty_like(w)
+    g = gla_norm_gate_grads(_ptr(dy), _ptr(gx), _ptr(gg), _steps(gx.stride(), B, H, T),
+                            _NO_STEPS if gg is None else _steps(gg.stride(), B, H, T), _ptr(gw))
+    n = 0 if gw is None else _here_size(lib.gla_norm_gate_bwd_workspace_size, p, dev)
+    ws, pw = _workspace(n, dev)
+    _launch(lambda r, s: lib.gla_norm_gate_bwd(r, ctypes.byref(g), pw, n, s), "gla_norm_gate_bwd", p, dev, stream,
+            gx, gg, gw, ws)
+    return gx, gg, gw
+
+
+def _residual_params(x, residual, w, scale, post_norm, eps):
+    import torch
+    if x.dim() < 1:
+        _refuse("x has rows: [..., D]")
+    D, dev, f32 = x.shape[-1], x.device, torch.float32
+    code, rcode = _dtype_code(x, "x"), _dtype_code(x, "x")
+    _dense(x, x.shape, x.dtype, dev, "x")
+    if residual is not None:
+        rcode = _dtype_code(residual, "residual")
+        if code == GLA_FP32 and rcode != GLA_FP32:
+            _refuse("an fp32 x goes into an fp32 residual")
+        _dense(residual, x.shape, residual.dtype, dev, "residual")
+    alpha, vec = 1.0, None
+    if isinstance(scale, torch.Tensor):
+        vec = scale
+        _dense(vec, (D,), f32, dev, "scale")
+    elif scale is not None:
+        alpha = float(scale)
+    if w is not None:
+        _dense(w, (D,), f32, dev, "w")
+    _on_gpu(x, "x")
+    rows = x.numel() // D if D else 0
+    return gla_residual_params(_ptr(x), _ptr(residual), _ptr(w), _ptr(vec), alpha, rows, D, 1 if post_norm else 0, eps,
+                               code, rcode)
+
+
+def residual_norm_forward(x, residual=None, w=None, scale=None, post_norm=False, eps=1e-6, stream=None, h=None):
+    """A block's output x into the residual, and the next block's normed input out of it, in one pass
+    (gla_residual_norm): h = residual + scale u, u = x or (post_norm) x / rms(x), y = w h / rms(h). Returns (h, y).
+
+    x [..., D] (bf16 or fp32), residual of x's shape in x's type or fp32 (None: 0), both contiguous; w fp32 [D] or None;
+    scale a number, fp32 [D] or None; D a multiple of 16 up to 16384, tensors from a 16-byte boundary. h has the residual's
+    type and may be the residual itself (h=residual: in place); it counts as modified in place. The norm reads h before its rounding."""
+    p = _residual_params(x, residual, w, scale, post_norm, eps)
+    lib, dev = _lib or load(), x.device
+    like = x if residual is None else residual
+    if h is not None:
+        _dense(h, x.shape, like.dtype, dev, "h")
+        _given(h, "h")
+    given = h
+    if h is None:
+        h = like.new_empty(like.shape)
+    y = x.new_empty(x.shape)
+    ph, py = _ptr(h), _ptr(y)
+    _launch(lambda r, s: lib.gla_residual_norm(r, ph, py, s), "gla_residual_norm", p, dev, stream, h, y)
+    _written(given)
+    return h, y
+
+
+def residual_norm_backward(x, residual, w, scale, dh, dy, post_norm=False, eps=1e-6, want_dx=True, want_dres=True,
+                           stream=None):
+    """Gradients of residual_norm_forward from those of h and y (either may be None: zero): (dx, dresidual, dw, dscale), the
+    vectors' fp32; None where there is no input or it is not wanted, dscale for a number too. Where dx and dresidual are
+    equal (no scale, no post_norm, one type) they are one tensor."""
+    import torch
+    p = _residual_params(x, residual, w, scale, post_norm, eps)
+    like = x if residual is None else residual
+    if dh is not None:
+        _dense(dh, x.shape, like.dtype, x.device, "dh")
+    if dy is not None:
+        _dense(dy, x.shape, x.dtype, x.device, "dy")
+    lib, dev = _lib or load(), x.device
+    same = want_dx and want_dres and residual is not None and scale is None and not post_norm and residual.dtype == x.dtype
+    gr = residual.new_empty(residual.shape) if want_dres and residual is not None else None
+    gx = gr if same else x.new_empty(x.shape) if want_dx else None
+    gw = None if w is None else torch.empty_like(w)
+    gs = torch.empty_like(scale) if isinstance(scale, torch.Tensor) else None
+    g = gla_residual_grads(_ptr(dh), _ptr(dy), None if same else _ptr(gx), _ptr(gr), _ptr(gw), _ptr(gs))
+    n = 0 if gw is None and gs is None else _here_size(lib.gla_residual_norm_bwd_workspace_size, p, dev)
+    ws, pw = _workspace(n, dev)
+    _launch(lambda r, s: lib.gla_residual_norm_bwd(r, ctypes.byref(g), pw, n, s), "gla_residual_norm_bwd", p, dev, stream,
+            gx, gr, gw, gs, ws)
+    return gx, gr, gw, gs

@@ -90,6 +90,12 @@ gla_status plan_workspace(const gla_fwd_params* p, size_t* bytes);
 // Whether the current device runs this build (GLA_OK), and its multiprocessors.
 gla_status device_ready(int* sms);
 
+// Sums over the rows of part [rows][cols], in a fixed order, to up to three outputs that take its columns in turn
+// (null: not wanted) (gla_column_sum.cu). cols is what `n` adds up to.
+struct ColumnOut { float* to; long long n; };
+struct ColumnOuts { ColumnOut o[3]; };
+cudaError_t launch_column_sum(const float* part, long long rows, long long cols, const ColumnOuts& out, cudaStream_t s);
+
 // Device status word (per device), written by kernels whose bounded waits run out.
 int* device_status_ptr();   // nullptr on failure
 

@@ -22,18 +22,17 @@
 //
 // The weights' gradients are summed in fp32: over a thread's rows, over the block in shared
 // memory, over the blocks by a second kernel, each in a fixed order.
-#include <cuda_bf16.h>
 #include <cmath>
 #include <cstring>
-#include <utility>
 
 #include "gla_internal.h"
+#include "gla_rows.cuh"
+#include "gla_span.h"
 
 namespace gla {
 namespace {
 
 constexpr int NT = 256;
-constexpr int VEC = 8;        // values per lane
 constexpr int UNR = 4;        // heads in flight per thread; the backward takes one at a time
 constexpr long long kBlocksPerSm = 4;
 
@@ -49,43 +48,6 @@ struct QkArgs {
     int hsplit;                                   // heads (q's and k's in a row) per block
 };
 
-// Eight values as loaded, and as fp32: a row waits in its own type (half the registers in bf16).
-template <typename E> struct Raw;
-template <> struct Raw<__nv_bfloat16> { typedef uint4 type; };
-template <> struct Raw<float> { struct type { float4 a, b; }; };
-__device__ __forceinline__ uint4 fetch(const __nv_bfloat16* p) {
-    return p ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
-}
-__device__ __forceinline__ Raw<float>::type fetch(const float* p) {
-    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-    return p ? Raw<float>::type{__ldcs(reinterpret_cast<const float4*>(p)), __ldcs(reinterpret_cast<const float4*>(p) + 1)}
-             : Raw<float>::type{z, z};
-}
-__device__ __forceinline__ void unpack(const uint4& w, float (&x)[VEC]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(u[j] << 16);
-        x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void unpack(const Raw<float>::type& w, float (&x)[VEC]) {
-    x[0] = w.a.x; x[1] = w.a.y; x[2] = w.a.z; x[3] = w.a.w; x[4] = w.b.x; x[5] = w.b.y; x[6] = w.b.z; x[7] = w.b.w;
-}
-__device__ __forceinline__ void save8(__nv_bfloat16* p, const float (&x)[VEC]) {
-    uint32_t u[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-        u[j] = *reinterpret_cast<const uint32_t*>(&t);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-}
-__device__ __forceinline__ void save8(float* p, const float (&x)[VEC]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *(reinterpret_cast<float4*>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
-}
-
 // f radians per position as a fraction of a turn in units of 2^-64 (modulo one turn).
 __device__ __forceinline__ unsigned long long turn_units(double f)
 {
@@ -99,13 +61,6 @@ __device__ __forceinline__ unsigned long long turn_units(double f)
     if (sh >= 0) u = sh < 64 ? m << sh : 0ull;
     else u = sh > -54 ? (m + (1ull << (-sh - 1))) >> -sh : 0ull;
     return (bits >> 63) ? 0ull - u : u;
-}
-
-template <int LPR>
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    return x;
 }
 
 // The rotation of this lane's eight values. Neighbouring pairs lie in the lane; halves pair value
@@ -325,8 +280,6 @@ cudaError_t launch(QkArgs a, int sms, cudaStream_t s)
     return cudaGetLastError();
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // Sizes, modes and presence shared by both directions.
 gla_status check(const gla_qk_norm_params* p)
 {
@@ -346,42 +299,6 @@ gla_status check(const gla_qk_norm_params* p)
     if (!aligned(p->inv_freq, 8) || !aligned(p->positions, 8)) return GLA_ERR_INVALID_ARG;
     if (p->d > 256) return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
-}
-
-// The bytes a strided [B,H,T,d] tensor spans (strides may be zero or negative).
-struct Span { uintptr_t lo, hi; };
-Span span(const void* p, const long long* st, int B, int H, int T, int d, size_t e)
-{
-    if (!p || B <= 0 || H <= 0 || T <= 0) return Span{0, 0};
-    long long lo = 0, hi = d;
-    const long long n[3] = {B - 1LL, H - 1LL, T - 1LL};
-    for (int i = 0; i < 3; ++i) (st[i] < 0 ? lo : hi) += st[i] * n[i];
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Span{a + (uintptr_t)(lo * (long long)e), a + (uintptr_t)(hi * (long long)e)};
-}
-Span flat(const void* p, size_t bytes)
-{
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return p ? Span{a, a + bytes} : Span{0, 0};
-}
-bool overlap(Span a, Span b) { return a.lo != a.hi && b.lo != b.hi && a.lo < b.hi && b.lo < a.hi; }
-
-// Whether the rows of a strided output are apart: dimension by dimension, from the smallest
-// stride, each steps past everything that the ones before it cover.
-bool apart(const long long* st, int B, int H, int T, int d)
-{
-    long long n[3] = {B, H, T}, s[3];
-    for (int i = 0; i < 3; ++i) s[i] = st[i] < 0 ? -st[i] : st[i];
-    for (int i = 0; i < 2; ++i)
-        for (int j = i + 1; j < 3; ++j)
-            if (s[j] < s[i]) { std::swap(s[i], s[j]); std::swap(n[i], n[j]); }
-    long long cover = d;
-    for (int i = 0; i < 3; ++i) {
-        if (n[i] <= 1) continue;
-        if (s[i] < cover) return false;
-        cover += s[i] * (n[i] - 1);
-    }
-    return true;
 }
 
 QkArgs common(const gla_qk_norm_params* p)

@@ -1,0 +1,343 @@
+// gla_residual_norm: what lies between two blocks of a layer stack, in one pass over the rows: the block's output x
+// goes into the residual r, scaled and, if wanted, normed first, and the next block's normed input comes out,
+//
+//     u = x or x / n(x),   h = r + alpha scale (.) u,   y = w (.) h / n(h),   n(x) = sqrt(mean x^2 + eps).
+//
+// Backward, h^ = h / n(h), u^ = x / n(x), means over the row:
+//
+//     dr = dh + (dy (.) w - h^ mean(dy (.) w (.) h^)) / n(h),   dw = sum dy (.) h^,
+//     du = alpha scale (.) dr,  dscale = alpha sum dr (.) u,    dx = du or (du - u^ mean(du (.) u^)) / n(x).
+//
+// The norm reads h as summed in fp32, before its rounding to the residual's type, and the backward forms it again
+// from r and x, so that no gradient carries that rounding.
+//
+// Bound by HBM: x and r read, h and y written once (backward: x, r, dh, dy read, dx and dr written). Rows of up to 512
+// values are a warp's, with shuffles for the sums; wider rows a block's, K pieces of eight values per thread. The
+// vectors' gradients are summed in fp32 over a thread's rows, then over the blocks, each in a fixed order.
+#include <cmath>
+#include <cstring>
+
+#include "gla_internal.h"
+#include "gla_rows.cuh"
+#include "gla_span.h"
+
+namespace gla {
+namespace {
+
+constexpr int kWarpD = 512;          // the widest row that one warp takes
+constexpr int kWarps = 8;            // warps (rows) per block of that form
+constexpr int kMaxD = 16384;
+
+struct ResArgs {
+    const void* x; const void* r; const float* w; const float* scale;
+    void* h; void* y;
+    const void* dh; const void* dy; void* dx; void* dr; float* part;
+    long long rows;
+    int D, post;
+    float alpha, eps;
+};
+
+// The sum of up to two values over the row's threads, in every one of them.
+template <int NTR>
+__device__ __forceinline__ void sum_row(float& a, float& b, float (*red)[2][NTR / 32 + 1], int& turn)
+{
+    a = row_sum<32>(a);
+    b = row_sum<32>(b);
+    if constexpr (NTR > 32) {
+        // two buffers in turn: a warp may be one sum ahead of another, not two
+        if (threadIdx.x % 32 == 0) {
+            red[turn][0][threadIdx.x / 32] = a;
+            red[turn][1][threadIdx.x / 32] = b;
+        }
+        __syncthreads();
+        a = b = 0.f;
+#pragma unroll
+        for (int i = 0; i < NTR / 32; ++i) {
+            a += red[turn][0][i];
+            b += red[turn][1][i];
+        }
+        turn ^= 1;
+    }
+}
+
+template <typename E, typename R, int NTR, int K, bool BWD>
+__global__ void __launch_bounds__(NTR == 32 ? 32 * kWarps : NTR) gla_residual_norm_kernel(ResArgs a)
+{
+    __shared__ float red[2][2][NTR / 32 + 1];
+    int turn = 0;
+    constexpr int RPB = NTR == 32 ? kWarps : 1;
+    const int l = threadIdx.x % NTR;
+    const float invn = 1.f / (float)a.D;
+    bool in[K];
+    float dw[BWD ? K : 1][VEC], ds[BWD ? K : 1][VEC];
+#pragma unroll
+    for (int k = 0; k < K; ++k) in[k] = (k * NTR + l) * VEC < a.D;
+    if constexpr (BWD)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) dw[k][j] = ds[k][j] = 0.f;
+
+    for (long long row = (long long)blockIdx.x * RPB + (NTR == 32 ? threadIdx.x / 32 : 0); row < a.rows; row += (long long)gridDim.x * RPB) {
+        const long long at = row * a.D + l * VEC;
+        typename Raw<E>::type xr[K], yr[K];
+        typename Raw<R>::type rr[K], hr[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const long long o = at + k * NTR * VEC;
+            xr[k] = fetch(in[k] ? static_cast<const E*>(a.x) + o : nullptr);
+            rr[k] = fetch(in[k] && a.r ? static_cast<const R*>(a.r) + o : nullptr);
+            if constexpr (BWD) {
+                yr[k] = fetch(in[k] && a.dy ? static_cast<const E*>(a.dy) + o : nullptr);
+                hr[k] = fetch(in[k] && a.dh ? static_cast<const R*>(a.dh) + o : nullptr);
+            }
+        }
+        float x[K][VEC], h[K][VEC], invx = 1.f, s = 0.f, none = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            unpack(xr[k], x[k]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s = fmaf(x[k][j], x[k][j], s);
+        }
+        if (a.post) {
+            sum_row<NTR>(s, none, red, turn);
+            invx = rsqrtf(fmaf(s, invn, a.eps));
+        }
+        auto vec = [&](const float* p, int k, float (&f)[VEC]) {
+            const int c = (k * NTR + l) * VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; j += 4) {
+                const float4 q = p && in[k] ? __ldg(reinterpret_cast<const float4*>(p + c + j)) : make_float4(1.f, 1.f, 1.f, 1.f);
+                f[j] = q.x; f[j + 1] = q.y; f[j + 2] = q.z; f[j + 3] = q.w;
+            }
+        };
+        float m = 0.f;
+        s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float sc[VEC], wv[VEC], g[VEC];
+            unpack(rr[k], h[k]);
+            vec(a.scale, k, sc);
+            if constexpr (BWD) {
+                vec(a.w, k, wv);
+                unpack(yr[k], g);
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                h[k][j] = fmaf(x[k][j] * invx, a.alpha * sc[j], h[k][j]);
+                s = fmaf(h[k][j], h[k][j], s);
+                if constexpr (BWD) m = fmaf(g[j] * wv[j], h[k][j], m);
+            }
+        }
+        sum_row<NTR>(s, m, red, turn);
+        const float inv = rsqrtf(fmaf(s, invn, a.eps));
+        if constexpr (!BWD) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!in[k]) continue;
+                const long long o = at + k * NTR * VEC;
+                if (a.h) save8(static_cast<R*>(a.h) + o, h[k]);
+                float wv[VEC];
+                vec(a.w, k, wv);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) h[k][j] *= inv * wv[j];
+                save8(static_cast<E*>(a.y) + o, h[k]);
+            }
+        } else {
+            m *= inv * invn;                     // mean(dy w h^)
+            float q = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float sc[VEC], wv[VEC], g[VEC], d[VEC];
+                unpack(yr[k], g);
+                unpack(hr[k], d);
+                vec(a.w, k, wv);
+                vec(a.scale, k, sc);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float hh = h[k][j] * inv;
+                    dw[k][j] = fmaf(g[j], hh, dw[k][j]);
+                    h[k][j] = fmaf(inv, fmaf(-hh, m, g[j] * wv[j]), d[j]);        // dr
+                    x[k][j] *= invx;                                             // u
+                    ds[k][j] = fmaf(h[k][j], x[k][j], ds[k][j]);
+                    q = fmaf(h[k][j] * sc[j], x[k][j], q);
+                }
+                if (in[k] && a.dr) save8(static_cast<R*>(a.dr) + at + k * NTR * VEC, h[k]);
+            }
+            if (a.post) {
+                sum_row<NTR>(q, none, red, turn);
+                q *= invn;
+            } else {
+                q = 0.f;
+            }
+            if (a.dx) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    if (!in[k]) continue;
+                    float sc[VEC];
+                    vec(a.scale, k, sc);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) x[k][j] = a.alpha * invx * fmaf(-x[k][j], q, h[k][j] * sc[j]);
+                    save8(static_cast<E*>(a.dx) + at + k * NTR * VEC, x[k]);
+                }
+            }
+        }
+    }
+    if constexpr (BWD) {
+        if (!a.part) return;
+        if constexpr (NTR > 32) {
+            float* p = a.part + (size_t)blockIdx.x * 2 * a.D;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!in[k]) continue;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) ds[k][j] *= a.alpha;
+                save8(p + (k * NTR + l) * VEC, dw[k]);
+                save8(p + a.D + (k * NTR + l) * VEC, ds[k]);
+            }
+        } else {
+            __shared__ float sums[kWarps][K * 32 * VEC];
+            for (int z = 0; z < 2; ++z) {
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) sums[threadIdx.x / 32][(k * 32 + l) * VEC + j] = z ? a.alpha * ds[k][j] : dw[k][j];
+                __syncthreads();
+                for (int i = threadIdx.x; i < a.D; i += 32 * kWarps) {
+                    float t = 0.f;
+                    for (int k = 0; k < kWarps; ++k) t += sums[k][i];
+                    a.part[((size_t)blockIdx.x * 2 + z) * a.D + i] = t;
+                }
+            }
+        }
+    }
+}
+
+long long blocks_of(long long rows, int D, int sms, bool bwd)
+{
+    const long long n = D <= kWarpD ? (rows + kWarps - 1) / kWarps : rows;
+    // backward: as many blocks as are resident, a partial row of both sums each
+    const long long per = D <= kWarpD ? 2 : D <= 1024 ? 12 : D <= 2048 ? 6 : D <= 4096 ? 3 : 1;
+    const long long most = bwd ? per * sms : 0x7fffffff;
+    return n < most ? n : most;
+}
+
+template <typename E, typename R, bool BWD>
+cudaError_t launch(const ResArgs& a, int sms, cudaStream_t s)
+{
+    const unsigned g = (unsigned)blocks_of(a.rows, a.D, sms, BWD);
+    if (a.D <= 256) gla_residual_norm_kernel<E, R, 32, 1, BWD><<<g, 32 * kWarps, 0, s>>>(a);
+    else if (a.D <= 512) gla_residual_norm_kernel<E, R, 32, 2, BWD><<<g, 32 * kWarps, 0, s>>>(a);
+    else if (a.D <= 1024) gla_residual_norm_kernel<E, R, 128, 1, BWD><<<g, 128, 0, s>>>(a);
+    else if (a.D <= 2048) gla_residual_norm_kernel<E, R, 256, 1, BWD><<<g, 256, 0, s>>>(a);
+    else if (a.D <= 4096) gla_residual_norm_kernel<E, R, 512, 1, BWD><<<g, 512, 0, s>>>(a);
+    else if (a.D <= 8192) gla_residual_norm_kernel<E, R, 512, 2, BWD><<<g, 512, 0, s>>>(a);
+    else gla_residual_norm_kernel<E, R, 512, 4, BWD><<<g, 512, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <bool BWD>
+cudaError_t launch(const gla_residual_params* p, const ResArgs& a, int sms, cudaStream_t s)
+{
+    if (p->dtype == GLA_FP32) return launch<float, float, BWD>(a, sms, s);
+    return p->residual_dtype == GLA_FP32 ? launch<__nv_bfloat16, float, BWD>(a, sms, s)
+                                         : launch<__nv_bfloat16, __nv_bfloat16, BWD>(a, sms, s);
+}
+
+gla_status check(const gla_residual_params* p)
+{
+    if (!p || p->rows < 0 || p->D <= 0 || p->D % 16 != 0) return GLA_ERR_INVALID_ARG;
+    if (p->dtype != GLA_BF16 && p->dtype != GLA_FP32) return GLA_ERR_INVALID_ARG;
+    if (p->residual_dtype != GLA_FP32 && p->residual_dtype != p->dtype) return GLA_ERR_INVALID_ARG;
+    if (!(p->eps >= 0.f) || !std::isfinite(p->eps) || !std::isfinite(p->alpha)) return GLA_ERR_INVALID_ARG;
+    if (p->rows > 0 && !p->x) return GLA_ERR_INVALID_ARG;
+    for (const void* x : {p->x, p->residual, (const void*)p->w, (const void*)p->scale})
+        if (!aligned(x, 16)) return GLA_ERR_INVALID_ARG;
+    if (p->D > kMaxD || p->rows > (1LL << 40) / p->D) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+ResArgs common(const gla_residual_params* p)
+{
+    ResArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = p->x; a.r = p->residual; a.w = p->w; a.scale = p->scale;
+    a.rows = p->rows; a.D = p->D; a.post = p->post_norm != 0; a.alpha = p->alpha; a.eps = p->eps;
+    return a;
+}
+
+}  // namespace
+}  // namespace gla
+
+using namespace gla;
+
+extern "C" {
+
+gla_status gla_residual_norm(const gla_residual_params* p, void* h, void* y, cudaStream_t stream)
+{
+    gla_status st = check(p);
+    if (st != GLA_OK) return st;
+    if ((p->rows > 0 && !y) || !aligned(h, 16) || !aligned(y, 16)) return GLA_ERR_INVALID_ARG;
+    const size_t e = p->dtype == GLA_BF16 ? 2 : 4, er = p->residual_dtype == GLA_BF16 ? 2 : 4, n = (size_t)p->rows * p->D;
+    const Span r = flat(p->residual, n * er), in[] = {flat(p->x, n * e), flat(p->w, p->D * 4), flat(p->scale, p->D * 4)};
+    const Span ho = flat(h, n * er), yo = flat(y, n * e);
+    for (const Span& s : in)
+        if (overlap(ho, s) || overlap(yo, s)) return GLA_ERR_INVALID_ARG;
+    if ((overlap(ho, r) && h != p->residual) || overlap(yo, r) || overlap(ho, yo)) return GLA_ERR_INVALID_ARG;
+    int sms = 0;
+    st = device_ready(&sms);
+    if (st != GLA_OK || p->rows == 0) return st;
+    ResArgs a = common(p);
+    a.h = h; a.y = y;
+    return launch<false>(p, a, sms, stream) == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+}
+
+size_t gla_residual_norm_bwd_workspace_size(const gla_residual_params* p)
+{
+    int sms = 0;
+    if (check(p) != GLA_OK || p->rows == 0 || (!p->w && !p->scale)) return 0;
+    if (device_ready(&sms) != GLA_OK) sms = 152;
+    return (size_t)blocks_of(p->rows, p->D, sms, true) * 2 * p->D * 4;
+}
+
+gla_status gla_residual_norm_bwd(const gla_residual_params* p, const gla_residual_grads* g, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream)
+{
+    gla_status st = check(p);
+    if (st != GLA_OK) return st;
+    if (!g || (g->grad_w && !p->w) || (g->grad_scale && !p->scale) || (g->grad_residual && !p->residual)) return GLA_ERR_INVALID_ARG;
+    for (const void* x : {g->grad_h, g->grad_y, (const void*)g->grad_x, (const void*)g->grad_residual})
+        if (!aligned(x, 16)) return GLA_ERR_INVALID_ARG;
+    if (!aligned(g->grad_w, 4) || !aligned(g->grad_scale, 4) || !aligned(workspace, 256)) return GLA_ERR_INVALID_ARG;
+    const size_t e = p->dtype == GLA_BF16 ? 2 : 4, er = p->residual_dtype == GLA_BF16 ? 2 : 4, n = (size_t)p->rows * p->D;
+    const Span in[] = {flat(p->x, n * e), flat(p->residual, n * er), flat(p->w, p->D * 4), flat(p->scale, p->D * 4),
+                       flat(g->grad_h, n * er), flat(g->grad_y, n * e)};
+    const Span out[] = {flat(g->grad_x, n * e), flat(g->grad_residual, n * er), flat(g->grad_w, p->D * 4), flat(g->grad_scale, p->D * 4)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Span& s : in)
+            if (overlap(out[i], s)) return GLA_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(out[i], out[j])) return GLA_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    st = device_ready(&sms);
+    if (st != GLA_OK) return st;
+    cudaError_t r = cudaSuccess;
+    if (p->rows == 0) {
+        if (g->grad_w) r = cudaMemsetAsync(g->grad_w, 0, p->D * 4, stream);
+        if (r == cudaSuccess && g->grad_scale) r = cudaMemsetAsync(g->grad_scale, 0, p->D * 4, stream);
+        return r == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+    }
+    const bool sums = g->grad_w || g->grad_scale;
+    const long long blocks = blocks_of(p->rows, p->D, sms, true);
+    if (sums && (!workspace || workspace_bytes < (size_t)blocks * 2 * p->D * 4)) return GLA_ERR_WORKSPACE;
+    ResArgs a = common(p);
+    a.dh = g->grad_h; a.dy = g->grad_y; a.dx = g->grad_x; a.dr = g->grad_residual;
+    a.part = sums ? static_cast<float*>(workspace) : nullptr;
+    r = launch<true>(p, a, sms, stream);
+    if (r == cudaSuccess && sums)
+        r = launch_column_sum(a.part, blocks, 2LL * p->D, ColumnOuts{{{g->grad_w, p->D}, {g->grad_scale, p->D}}}, stream);
+    return r == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+}
+
+}  // extern "C"

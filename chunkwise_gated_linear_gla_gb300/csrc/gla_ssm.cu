@@ -1,0 +1,368 @@
+// The selective scan: N states for each of the D channels, with a decay per channel, state and token,
+//
+//     delta_t = softplus(dt_t + dt_bias),   h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,
+//     y_t = (C_t . h_t + D x_t) silu(z_t).
+//
+// No product of matrices is in it: per token, channel and state one exponential, two products and two fused
+// multiply-adds, all fp32, the states in registers from the first token to the last. Bound by issue: at eight
+// rows of 2048 tokens of 4096 channels of 16 states 1.07e9 exponentials and 4.3e9 multiply-adds, against 0.54 GB.
+//
+// gla_ssm_walk: a thread holds two channels by eight states and walks the tokens; B and C are read once for
+// both channels, products are packed pairs of states. The block goes in tiles of 16 tokens: raw rows
+// arrive by asynchronous copies one tile ahead, delta and delta x are formed once per channel and token into shared
+// memory, the walk leaves C . h there, and y is formed from it eight channels at a time.
+//
+// Few channels: the sequence is cut into segments. A first walk leaves each segment's state from zero and its sum of delta
+// (the decay across the segment is exp(A sum)), gla_ssm_scan the states entering them, a second walk y.
+//
+// gla_ssm_step: single and few tokens, bound by the states' bytes: a thread holds four states of a channel.
+#include "gla_rows.cuh"
+#include "gla_ssm.cuh"
+
+namespace gla {
+namespace {
+
+// ------------------------------------------------------------------ few tokens
+
+template <typename E> __device__ __forceinline__ float one(const E* p) { return (float)*p; }
+__device__ __forceinline__ void four(const __nv_bfloat16* p, float (&v)[4])
+{
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
+}
+__device__ __forceinline__ void four(const float* p, float (&v)[4])
+{
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+}
+
+constexpr int kStepNT = 128;
+
+template <typename E, int N>
+__global__ void __launch_bounds__(kStepNT) gla_ssm_step_kernel(SsmArgs a)
+{
+    constexpr int LPC = N / 4, CPB = kStepNT / LPC;
+    const int ctiles = (a.D + CPB - 1) / CPB;
+    const long long b = blockIdx.x / ctiles;
+    const int c = (int)(blockIdx.x % ctiles) * CPB + threadIdx.x / LPC, l = threadIdx.x % LPC, n = l * 4;
+    const bool on = c < a.D;
+    const int cc = on ? c : a.D - 1, g = cc / (a.D / a.G);
+    const size_t so = ((size_t)b * a.D + cc) * N + n;
+    float h[4] = {0.f, 0.f, 0.f, 0.f}, A[4];
+    if (a.S0) four(a.S0 + so, h);
+    four(a.A + (size_t)cc * N + n, A);
+    const float bias = a.bias ? a.bias[cc] : 0.f, Dk = a.Dk ? a.Dk[cc] : 0.f;
+    const E* xp = static_cast<const E*>(a.x) + b * a.sx[0] + cc;
+    const E* dp = static_cast<const E*>(a.dt) + b * a.sdt[0] + cc;
+    const E* zp = a.z ? static_cast<const E*>(a.z) + b * a.sz[0] + cc : nullptr;
+    const E* Bp = static_cast<const E*>(a.Bm) + b * a.sB[0] + g * N + n;
+    const E* Cp = static_cast<const E*>(a.Cm) + b * a.sC[0] + g * N + n;
+    E* yp = static_cast<E*>(a.y) + (size_t)b * a.T * a.D + cc;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) A[j] *= kLog2e;
+    for (int t = 0; t < a.T; ++t) {
+        const float x = one(xp + t * a.sx[1]);
+        float d = one(dp + t * a.sdt[1]) + bias, Bv[4], Cv[4];
+        four(Bp + t * a.sB[1], Bv);
+        four(Cp + t * a.sC[1], Cv);
+        const float z = zp ? one(zp + t * a.sz[1]) : 0.f;
+        if (a.softplus) d = softplus(d);
+        const float dx = d * x;
+        float y = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            h[j] = fmaf(ex2(d * A[j]), h[j], dx * Bv[j]);
+            y = fmaf(h[j], Cv[j], y);
+        }
+        y = row_sum<LPC>(y);
+        y = fmaf(Dk, x, y);
+        if (zp) y *= z * sigmoid(z);
+        if (on && l == 0) yp[(size_t)t * a.D] = (E)y;
+    }
+    if (on && a.ST) *reinterpret_cast<float4*>(a.ST + so) = make_float4(h[0], h[1], h[2], h[3]);
+}
+
+// ------------------------------------------------------------------ the walk
+
+constexpr int kS = 8, kC = 2;      // states and channels of a thread
+constexpr int kWalkWarps = 4;
+
+template <int N> constexpr int kWalkChannels = kWalkWarps * 32 * kS * kC / N;
+
+template <typename E, int N, int MODE>
+struct WalkShared {
+    static constexpr int CB = kWalkChannels<N>;
+    E raw[2][3][kSsmTile][CB];        // x, dt, z (REV: dy, dt, z)
+    E bc[2][2][kSsmTile][N];          // B, C
+    float2 work[kSsmTile][CB];        // delta, delta x (REV: dy silu(z))
+    float yw[MODE == kSsmOut ? kSsmTile : 1][CB];
+};
+
+template <typename E, int N, int MODE>
+__global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a)
+{
+    constexpr int NT = kWalkWarps * 32, CB = kWalkChannels<N>, Q = N / kS, TT = kSsmTile;
+    constexpr bool REV = MODE == kSsmRev;
+    extern __shared__ __align__(16) char smem_raw[];
+    auto& sm = *reinterpret_cast<WalkShared<E, N, MODE>*>(smem_raw);
+    const int Dg = a.D / a.G, ct = blockIdx.x % a.ctiles;
+    const long long bg = blockIdx.x / a.ctiles;
+    const int b = (int)(bg / a.G), g = (int)(bg % a.G);
+    const int c0 = g * Dg + ct * CB, c1 = g * Dg + Dg;           // this block's channels end at c1
+    const int seg = blockIdx.y + (REV ? 1 : 0), s0 = seg * a.seg, s1 = min(a.T, s0 + a.seg);
+    const int tiles = (s1 - s0 + TT - 1) / TT;
+
+    const E* src[3] = {REV ? static_cast<const E*>(a.dy) + (size_t)b * a.T * a.D : static_cast<const E*>(a.x) + b * a.sx[0],
+                       static_cast<const E*>(a.dt) + b * a.sdt[0], a.z ? static_cast<const E*>(a.z) + b * a.sz[0] : nullptr};
+    const long long st[3] = {REV ? (long long)a.D : a.sx[1], a.sdt[1], a.sz[1]};
+    const E* Bp = static_cast<const E*>(a.Bm) + b * a.sB[0] + g * N;
+    const E* Cp = static_cast<const E*>(a.Cm) + b * a.sC[0] + g * N;
+    auto load = [&](int tile) {
+        const int stage = tile & 1, t0 = s0 + (REV ? tiles - 1 - tile : tile) * TT;
+        copy_rows<E, CB, NT>(&sm.raw[stage][0][0][0], src[0], st[0], t0, s1, c0, c1);
+        copy_rows<E, CB, NT>(&sm.raw[stage][1][0][0], src[1], st[1], t0, s1, c0, c1);
+        if ((MODE == kSsmOut || REV) && a.z) copy_rows<E, CB, NT>(&sm.raw[stage][2][0][0], src[2], st[2], t0, s1, c0, c1);
+        if (!REV) copy_states<E, N, NT>(&sm.bc[stage][0][0][0], Bp, a.sB[1], t0, s1);
+        if (MODE == kSsmOut || REV) copy_states<E, N, NT>(&sm.bc[stage][1][0][0], Cp, a.sC[1], t0, s1);
+        copies_end();
+    };
+    load(0);
+
+    // this thread's two channels (cl, cl + 1) and eight states
+    const int sg = threadIdx.x % Q, cl = threadIdx.x / Q * kC;
+    const bool on = c0 + cl < c1;
+    f2 h[kC][kS / 2], A[kC][kS / 2];
+    const size_t per = (size_t)a.D * N, so = (size_t)(on ? c0 + cl : c0) * N + sg * kS;
+    const float* from = nullptr;          // this batch row's states, [D][N]
+    if (REV) {
+        if (seg == a.nseg - 1 && a.dST) from = a.dST + b * per;
+    } else if (MODE != kSsmState || seg == 0) {
+        if (seg > 0) from = a.segS + ((size_t)b * (a.nseg - 1) + seg - 1) * per;
+        else if (a.S0) from = a.S0 + b * per;
+    }
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        states<kS>(a.A + (size_t)(on ? c0 + cl + i : c0) * N + sg * kS, A[i]);
+#pragma unroll
+        for (int j = 0; j < kS / 2; ++j) {
+            A[i][j] = mul2(A[i][j], pk(kLog2e, kLog2e));
+            h[i][j] = pk(0.f, 0.f);
+        }
+        if (from) states<kS>(from + so + i * N, h[i]);
+    }
+    // the vectors of eight channels that this thread prepares and finishes: always the same channels
+    constexpr int COLS = CB / VEC, VPT = TT * COLS;
+    const int vc = threadIdx.x % COLS * VEC;
+    float bias[VEC], Dk[VEC], sumd[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        const bool in = c0 + vc < c1;
+        bias[j] = a.bias && in ? a.bias[c0 + vc + j] : 0.f;
+        Dk[j] = MODE == kSsmOut && a.Dk && in ? a.Dk[c0 + vc + j] : 0.f;
+        sumd[j] = 0.f;
+    }
+
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int stage = tile & 1, t0 = s0 + (REV ? tiles - 1 - tile : tile) * TT;
+        copies_wait<0>();
+        __syncthreads();
+        if (tile + 1 < tiles) load(tile + 1);
+        for (int i = threadIdx.x; i < VPT; i += NT) {
+            const int tok = i / COLS;
+            float x[VEC], d[VEC];
+            const E* rows = &sm.raw[stage][0][tok][vc];
+            unpack(*reinterpret_cast<const typename Raw<E>::type*>(rows), x);
+            unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][1][tok][vc]), d);
+            const bool ok = t0 + tok < s1;
+            float z[VEC];
+            if (REV && a.z) unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][2][tok][vc]), z);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                d[j] += bias[j];
+                if (a.softplus) d[j] = softplus(d[j]);
+                if (!ok) d[j] = 0.f;
+                if (MODE == kSsmState) sumd[j] += d[j];
+                if (REV) {
+                    if (a.z) x[j] *= z[j] * sigmoid(z[j]);
+                } else {
+                    x[j] *= d[j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; j += 2)
+                *reinterpret_cast<float4*>(&sm.work[tok][vc + j]) = make_float4(d[j], x[j], d[j + 1], x[j + 1]);
+        }
+        __syncthreads();
+        if (MODE == kSsmKeep && on) {
+            float* k = a.keep + ((size_t)b * ((a.T + TT - 1) / TT) + t0 / TT) * per + so;
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+#pragma unroll
+                for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(k + i * N + 2 * j) = make_ulonglong2(h[i][j], h[i][j + 1]);
+        }
+#pragma unroll 4
+        for (int n = 0; n < TT; ++n) {
+            const int tok = REV ? TT - 1 - n : n;
+            const float4 w = *reinterpret_cast<const float4*>(&sm.work[tok][cl]);
+            const float dl[kC] = {w.x, w.z}, dx[kC] = {w.y, w.w};
+            f2 Bv[kS / 2], Cv[kS / 2];
+            states<kS>(&sm.bc[stage][REV ? 1 : 0][tok][sg * kS], Bv);
+            if (MODE == kSsmOut) states<kS>(&sm.bc[stage][1][tok][sg * kS], Cv);
+            float y[kC];
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                const f2 d2 = pk(dl[i], dl[i]), x2 = pk(dx[i], dx[i]);
+                f2 s = pk(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < kS / 2; ++j) {
+                    const f2 e = ex2_2(mul2(d2, A[i][j]));
+                    if (REV) h[i][j] = mul2(e, fma2(x2, Bv[j], h[i][j]));
+                    else h[i][j] = fma2(e, h[i][j], mul2(x2, Bv[j]));
+                    if (MODE == kSsmOut) s = fma2(h[i][j], Cv[j], s);
+                }
+                float p, q;
+                up(s, p, q);
+                y[i] = p + q;
+            }
+            if (MODE == kSsmOut) {
+                // over the channel's Q threads: a pair keeps one channel each, the rest agree
+                if constexpr (Q == 1) {
+                    *reinterpret_cast<float2*>(&sm.yw[tok][cl]) = make_float2(y[0], y[1]);
+                } else {
+                    const bool odd = sg & 1;
+                    float v = (odd ? y[1] : y[0]) + __shfl_xor_sync(~0u, odd ? y[0] : y[1], 1);
+#pragma unroll
+                    for (int o = 2; o < Q; o *= 2) v += __shfl_xor_sync(~0u, v, o);
+                    if (sg < 2) sm.yw[tok][cl + sg] = v;
+                }
+            }
+        }
+        if (MODE != kSsmOut) continue;
+        __syncthreads();
+        for (int i = threadIdx.x; i < VPT; i += NT) {
+            const int tok = i / COLS;
+            if (t0 + tok >= s1 || c0 + vc >= c1) continue;
+            float x[VEC], z[VEC], y[VEC];
+            unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][0][tok][vc]), x);
+            if (a.z) unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][2][tok][vc]), z);
+#pragma unroll
+            for (int j = 0; j < VEC; j += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(&sm.yw[tok][vc + j]);
+                y[j] = q.x; y[j + 1] = q.y; y[j + 2] = q.z; y[j + 3] = q.w;
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                y[j] = fmaf(Dk[j], x[j], y[j]);
+                if (a.z) y[j] *= z[j] * sigmoid(z[j]);
+            }
+            save8(static_cast<E*>(a.y) + ((size_t)b * a.T + t0 + tok) * a.D + c0 + vc, y);
+        }
+    }
+
+    float* to = nullptr;
+    if (MODE == kSsmOut && seg == a.nseg - 1 && a.ST) to = a.ST + b * per;
+    if (MODE == kSsmState) to = a.segS + ((size_t)b * (a.nseg - 1) + seg) * per;
+    if (REV) to = a.segG + ((size_t)b * (a.nseg - 1) + seg - 1) * per;
+    if (to && on) {
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+#pragma unroll
+            for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(to + so + i * N + 2 * j) = make_ulonglong2(h[i][j], h[i][j + 1]);
+    }
+    if (MODE == kSsmState) {
+        // the sums of delta over the threads that prepared the same channels, in order
+        __syncthreads();
+        float* sd = reinterpret_cast<float*>(&sm.work[0][0]);
+        constexpr int ROWS = (NT < VPT ? NT : VPT) / COLS;
+        if (threadIdx.x < ROWS * COLS)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sd[threadIdx.x / COLS * CB + vc + j] = sumd[j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < CB; c += NT) {
+            float s = 0.f;
+            for (int r = 0; r < ROWS; ++r) s += sd[r * CB + c];
+            if (c0 + c < c1) a.sumd[((size_t)b * (a.nseg - 1) + seg) * a.D + c0 + c] = s;
+        }
+    }
+}
+
+// The states entering segments 1 .., in place of the segments' own: the first's own starts from S0, X_{s+1} = exp(A sum_s) X_s
+// + own_s. rev: the gradients of the states after segments .. nseg - 2, in place of what each next segment leaves of its
+// own (the last one's starts from dST).
+__global__ void gla_ssm_scan_kernel(SsmArgs a, int rev)
+{
+    const long long per = (long long)a.D * a.N, all = (long long)a.B * per;
+    const int m = a.nseg - 1;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (long long)gridDim.x * blockDim.x) {
+        const long long b = i / per, o = i - b * per;
+        const float A = a.A[o] * kLog2e;
+        const float* sd = a.sumd + b * m * a.D + o / a.N;
+        float* s = (rev ? a.segG : a.segS) + b * m * per + o;
+        float X = s[rev ? (m - 1) * per : 0];
+        for (int k = 1; k < m; ++k) {
+            const int n = rev ? m - 1 - k : k, d = rev ? n + 1 : n;
+            X = fmaf(ex2(A * sd[(long long)d * a.D]), X, s[n * per]);
+            s[n * per] = X;
+        }
+    }
+}
+
+template <typename E, int N, int MODE>
+cudaError_t walk(const SsmArgs& a0, cudaStream_t s)
+{
+    SsmArgs a = a0;
+    constexpr int CB = kWalkChannels<N>;
+    a.ctiles = (a.D / a.G + CB - 1) / CB;
+    const int n = (int)sizeof(WalkShared<E, N, MODE>);
+    const cudaError_t r = cudaFuncSetAttribute(gla_ssm_walk_kernel<E, N, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+    if (r != cudaSuccess) return r;
+    const dim3 g((unsigned)((long long)a.B * a.G * a.ctiles), MODE == kSsmState || MODE == kSsmRev ? a.nseg - 1 : a.nseg);
+    gla_ssm_walk_kernel<E, N, MODE><<<g, kWalkWarps * 32, n, s>>>(a);
+    return cudaGetLastError();
+}
+template <typename E, int N>
+cudaError_t walk(const SsmArgs& a, int mode, cudaStream_t s)
+{
+    return mode == kSsmOut ? walk<E, N, kSsmOut>(a, s) : mode == kSsmState ? walk<E, N, kSsmState>(a, s)
+           : mode == kSsmKeep ? walk<E, N, kSsmKeep>(a, s) : walk<E, N, kSsmRev>(a, s);
+}
+template <typename E>
+cudaError_t walk(const SsmArgs& a, int mode, cudaStream_t s)
+{
+    return a.N == 8 ? walk<E, 8>(a, mode, s) : a.N == 16 ? walk<E, 16>(a, mode, s)
+           : a.N == 32 ? walk<E, 32>(a, mode, s) : walk<E, 64>(a, mode, s);
+}
+
+template <typename E>
+cudaError_t step(const SsmArgs& a, cudaStream_t s)
+{
+    const int cpb = kStepNT / (a.N / 4);
+    const unsigned g = (unsigned)((long long)a.B * ((a.D + cpb - 1) / cpb));
+    if (a.N == 8) gla_ssm_step_kernel<E, 8><<<g, kStepNT, 0, s>>>(a);
+    else if (a.N == 16) gla_ssm_step_kernel<E, 16><<<g, kStepNT, 0, s>>>(a);
+    else if (a.N == 32) gla_ssm_step_kernel<E, 32><<<g, kStepNT, 0, s>>>(a);
+    else gla_ssm_step_kernel<E, 64><<<g, kStepNT, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int ssm_walk_channels(int N) { return kWalkWarps * 32 * kS * kC / N; }
+
+cudaError_t launch_ssm_step(const SsmArgs& a, gla_dtype dtype, cudaStream_t s)
+{
+    return dtype == GLA_BF16 ? step<__nv_bfloat16>(a, s) : step<float>(a, s);
+}
+cudaError_t launch_ssm_walk(const SsmArgs& a, int mode, gla_dtype dtype, cudaStream_t s)
+{
+    return dtype == GLA_BF16 ? walk<__nv_bfloat16>(a, mode, s) : walk<float>(a, mode, s);
+}
+cudaError_t launch_ssm_scan(const SsmArgs& a, bool rev, int sms, cudaStream_t s)
+{
+    const long long n = ((long long)a.B * a.D * a.N + 255) / 256;
+    gla_ssm_scan_kernel<<<(unsigned)(n < 8LL * sms ? n : 8LL * sms), 256, 0, s>>>(a, rev);
+    return cudaGetLastError();
+}
+
+}  // namespace gla

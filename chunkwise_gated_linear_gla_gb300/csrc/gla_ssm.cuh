@@ -1,0 +1,146 @@
+// The selective scan's device helpers and launchers, shared by its forward, backward and entry points.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstddef>
+#include <cstdint>
+
+#include "gla_internal.h"
+
+namespace gla {
+
+constexpr int kSsmTile = 16;      // tokens per tile, and between two kept states of the backward
+
+// What a pass over [B,T,D] channels reads and writes. Group g of the channels, Dg = D / G wide, reads row g of B and C.
+struct SsmArgs {
+    const void* x; const void* dt; const void* z; const void* Bm; const void* Cm;
+    long long sx[2], sdt[2], sz[2], sB[2], sC[2];   // strides (b, t) in elements
+    const float* A; const float* Dk; const float* bias; const float* S0;
+    void* y; float* ST;
+    int B, T, D, G, N, softplus;
+    int nseg, seg;                // segments of the sequence, tokens in each (a multiple of kSsmTile)
+    float* segS;                  // [B][nseg - 1][D][N] states: each segment's own, then those entering 1 .. nseg - 1
+    float* sumd;                  // [B][nseg - 1][D] sums of delta
+    float* keep;                  // KEEP: [B][ceil(T / kSsmTile)][D][N] states entering every tile
+    // backward
+    const void* dy; const float* dST;
+    void* dx; void* ddt; void* dz; float* dS0;
+    float* part_bc;               // [tiles per group][B][T][G][2 N]
+    float* part_p;                // [B nseg][D N + 2 D]: dA, dD, ddt_bias
+    float* segG;                  // [B][nseg - 1][D][N] gradients of the states after segments 0 .. nseg - 2
+    int ctiles;                   // channel tiles per group
+};
+
+// What a walk over a segment does.
+enum SsmMode {
+    kSsmOut = 0,      // y and the last state
+    kSsmState = 1,    // the segment's state from zero and its sum of delta (all segments but the last)
+    kSsmKeep = 2,     // the state entering every tile
+    kSsmRev = 3,      // backwards: the gradient of the state before the segment, from zero (all but the first)
+};
+
+cudaError_t launch_ssm_step(const SsmArgs& a, gla_dtype dtype, cudaStream_t s);
+cudaError_t launch_ssm_walk(const SsmArgs& a, int mode, gla_dtype dtype, cudaStream_t s);
+// The states entering the segments from each segment's own, in place; `rev`: from the last, into segG.
+cudaError_t launch_ssm_scan(const SsmArgs& a, bool rev, int sms, cudaStream_t s);
+cudaError_t launch_ssm_bwd(const SsmArgs& a, gla_dtype dtype, cudaStream_t s);
+cudaError_t launch_ssm_bc_sum(const SsmArgs& a, void* dB, void* dC, gla_dtype dtype, int sms, cudaStream_t s);
+int ssm_walk_channels(int N);     // channels per block of the walk, and of the backward
+int ssm_bwd_channels(int N);
+
+#ifdef __CUDACC__
+
+// Pairs of fp32 values, as the packed instructions take them.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pk(float a, float b) { f2 r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b)); return r; }
+__device__ __forceinline__ void up(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) { f2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { f2 r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c)); return r; }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) { f2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+__device__ __forceinline__ float ex2(float x) { float r; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x)); return r; }
+__device__ __forceinline__ f2 ex2_2(f2 v) { float a, b; up(v, a, b); return pk(ex2(a), ex2(b)); }
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// log(1 + exp(v)): log(1 + u) = 2 atanh(s), s = u / (2 + u) <= 1/3, u = exp(-|v|); its series to s^15 is good to 2e-9, so
+// small steps keep their digits (a logarithm of the rounded 1 + u would lose them). -inf gives 0.
+__device__ __forceinline__ float softplus(float v)
+{
+    const float u = expf(-fabsf(v)), s = __fdividef(u, 2.f + u), q = s * s;
+    float p = fmaf(q, 1.f / 15, 1.f / 13);
+    p = fmaf(p, q, 1.f / 11);
+    p = fmaf(p, q, 1.f / 9);
+    p = fmaf(p, q, 1.f / 7);
+    p = fmaf(p, q, 1.f / 5);
+    p = fmaf(p, q, 1.f / 3);
+    p = fmaf(p, q, 1.f);
+    return fmaf(2.f * s, p, fmaxf(v, 0.f));
+}
+// Its slope.
+__device__ __forceinline__ float softplus_slope(float v)
+{
+    const float u = expf(-fabsf(v));
+    return __fdividef(v >= 0.f ? 1.f : u, 1.f + u);
+}
+
+// S states from p, as fp32 pairs.
+template <int S>
+__device__ __forceinline__ void states(const __nv_bfloat16* p, f2 (&r)[S / 2])
+{
+    uint32_t u[S / 2];
+    if constexpr (S == 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        u[0] = q.x; u[1] = q.y; u[2] = q.z; u[3] = q.w;
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        u[0] = q.x; u[1] = q.y;
+    }
+#pragma unroll
+    for (int i = 0; i < S / 2; ++i) r[i] = pk(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+template <int S>
+__device__ __forceinline__ void states(const float* p, f2 (&r)[S / 2])
+{
+#pragma unroll
+    for (int i = 0; i < S / 4; ++i) {
+        const ulonglong2 q = *(reinterpret_cast<const ulonglong2*>(p) + i);
+        r[2 * i] = q.x;
+        r[2 * i + 1] = q.y;
+    }
+}
+
+__device__ __forceinline__ void copy16(void* smem, const void* g, bool ok)
+{
+    const unsigned d = (unsigned)__cvta_generic_to_shared(smem);
+    const int n = ok ? 16 : 0;                     // the rest of the 16 bytes is zero
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(g), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// Rows [t0, t0 + kSsmTile) of channels [c0, c0 + CB) into smem [kSsmTile][CB]; tokens from t1 and channels from c1 on as zeros.
+template <typename E, int CB, int NT>
+__device__ __forceinline__ void copy_rows(E* smem, const E* src, long long st, int t0, int t1, int c0, int c1)
+{
+    constexpr int PER = 16 / sizeof(E), COLS = CB / PER;
+    for (int i = threadIdx.x; i < kSsmTile * COLS; i += NT) {
+        const int tok = i / COLS, c = i % COLS * PER;
+        const bool ok = t0 + tok < t1 && c0 + c < c1;
+        copy16(smem + tok * CB + c, ok ? src + (t0 + tok) * st + c0 + c : src, ok);
+    }
+}
+// A tile's rows of one group of B or C, N values a token.
+template <typename E, int N, int NT>
+__device__ __forceinline__ void copy_states(E* smem, const E* src, long long st, int t0, int t1)
+{
+    constexpr int PER = 16 / sizeof(E), COLS = N / PER;
+    for (int i = threadIdx.x; i < kSsmTile * COLS; i += NT) {
+        const int tok = i / COLS, c = i % COLS * PER;
+        const bool ok = t0 + tok < t1;
+        copy16(smem + tok * N + c, ok ? src + (t0 + tok) * st + c : src, ok);
+    }
+}
+
+#endif
+}  // namespace gla

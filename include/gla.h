@@ -534,6 +534,199 @@ gla_status gla_qk_norm_rope_bwd(const gla_qk_norm_params* p, const gla_qk_norm_g
                                 size_t workspace_bytes, cudaStream_t stream);
 size_t gla_qk_norm_rope_bwd_workspace_size(const gla_qk_norm_params* p);
 
+/*
+ * gla_conv_fwd — the short causal convolution of every channel of a layer's rows on their way to a recurrence, a filter
+ * of W taps over the tokens up to and with their own:
+ *     y_t = act(bias + sum_j w_j x_{t-W+1+j}),     act the identity or silu(a) = a / (1 + exp(-a)).
+ * x is read through strides in elements (batch, head, token; the last dimension contiguous), every row starting on 16
+ * bytes; strides may be zero or negative. Channel c of the H d is value c % d of head c / d. What lies before the first
+ * token is the carried state S0, the last W - 1 rows of the call before, oldest first (NULL: zeros), and ST gets the last
+ * W - 1 rows of (S0, x), copies of what came in; ST may equal S0. Rows of a batch of unequal prompts are padded in front,
+ * with zeros: that is what a zero state holds. W is 2, 3 or 4 (else GLA_ERR_UNSUPPORTED), d a multiple of 16, H d <= 2^24.
+ * Sums are fp32; y is rounded once. T = 0 copies S0 to ST.
+ */
+typedef enum { GLA_ACT_NONE = 0, GLA_ACT_SILU = 1, GLA_ACT_SIGMOID = 2 } gla_activation;
+
+typedef struct {
+    const void* x;              /* [B,H,T,d] through x_stride, dtype */
+    long long x_stride[3];
+    const float* w;             /* [H d, W], from a 16-byte boundary */
+    const float* bias;          /* [H d] or NULL (0) */
+    const void* S0;             /* [B,W-1,H d] dtype, or NULL */
+    int B, H, T, d, W;
+    int activation;             /* gla_activation: GLA_ACT_NONE or GLA_ACT_SILU */
+    gla_dtype dtype;
+} gla_conv_params;
+
+/* y [B,H,T,d] dense and ST [B,W-1,H d] (NULL: not written), 16-byte aligned, apart from every other input. */
+gla_status gla_conv_fwd(const gla_conv_params* p, void* y, void* ST, cudaStream_t stream);
+
+/*
+ * gla_conv_bwd — its gradients, from grad_y (dense) and grad_ST (NULL: zero): grad_x in `dtype` through strides of its
+ * own (rows apart), grad_w and grad_bias fp32 and grad_S0 in `dtype` (each NULL: not wanted; grad_bias must be NULL without
+ * the bias). The workspace holds the sums' partials: gla_conv_bwd_workspace_size() bytes, 256-byte aligned, needed if
+ * grad_w or grad_bias is wanted. Results are bitwise reproducible on one device.
+ */
+typedef struct {
+    const void* grad_y;
+    const void* grad_ST;
+    void* grad_x;
+    long long x_stride[3];
+    float* grad_w;
+    float* grad_bias;
+    void* grad_S0;
+} gla_conv_grads;
+
+gla_status gla_conv_bwd(const gla_conv_params* p, const gla_conv_grads* g, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+size_t gla_conv_bwd_workspace_size(const gla_conv_params* p);
+
+/*
+ * gla_ssm_fwd — the selective scan: where the gates above decay a whole state (or row of keys) alike, here each of the
+ * N states of each of the D channels decays by itself,
+ *     delta_t = softplus(dt_t + dt_bias)  (or dt_t + dt_bias),
+ *     h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,     y_t = (C_t . h_t + D_skip x_t) silu(z_t),
+ * A [D,N] (negative for states that decay), B and C one row of N values for each of the G groups of D / G channels.
+ * A dt of -inf (with softplus; or of 0 without it and the bias) passes a token over: the state stays as it is. Other inputs are finite.
+ * x, dt, z, B and C are read through strides in elements (batch, token; a row contiguous), every row starting on 16 bytes;
+ * strides may be zero or negative. D / G is a multiple of 8, N 8, 16, 32 or 64 (else GLA_ERR_UNSUPPORTED), D <= 2^20.
+ * States and sums are fp32, y is rounded once; ST may equal S0. Up to eight tokens are taken one by one, longer calls in
+ * tiles of 16; with few channels the sequence is cut into segments, whose states from zero come first. T = 0 copies S0 to
+ * ST. Ownership and asynchrony are as for gla_fwd_ex.
+ */
+typedef struct {
+    const void* x;              /* [B,T,D] dtype */
+    const void* dt;             /* [B,T,D] dtype */
+    const void* z;              /* [B,T,D] dtype, or NULL (no gate) */
+    const void* Bm;             /* [B,T,G,N] dtype */
+    const void* Cm;             /* [B,T,G,N] dtype */
+    long long x_stride[2], dt_stride[2], z_stride[2], B_stride[2], C_stride[2];
+    const float* A;             /* [D,N] */
+    const float* D_skip;        /* [D] or NULL (0) */
+    const float* dt_bias;       /* [D] or NULL (0) */
+    const float* S0;            /* [B,D,N] or NULL (zero) */
+    int B, T, D, G, N;
+    int softplus;
+    gla_dtype dtype;
+    int force_segments;         /* 0: the planner chooses the sequence split; n >= 1: n segments (as many as there are tiles at most) */
+} gla_ssm_params;
+
+/* y [B,T,D] dense, ST [B,D,N] or NULL (not written). The workspace is for the sequence split: gla_ssm_fwd_workspace_size()
+ * bytes, 256-byte aligned. */
+gla_status gla_ssm_fwd(const gla_ssm_params* p, void* y, float* ST, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+size_t gla_ssm_fwd_workspace_size(const gla_ssm_params* p);
+
+/*
+ * gla_ssm_bwd — its gradients, from grad_y (dense) and grad_ST (NULL: zero): grad_x, grad_dt, grad_z ([B,T,D] dense) and
+ * grad_B, grad_C ([B,T,G,N] dense, summed over the group's channels) in `dtype`, each rounded once from fp32; grad_A,
+ * grad_D, grad_dt_bias and grad_S0 fp32 (the last three NULL: not wanted; grad_z, grad_D and grad_dt_bias must be NULL without
+ * their input). Nothing of the forward call is needed but its inputs. The workspace holds the state at every 16th token
+ * (B T D N / 4 bytes) and partial sums of grad_B and grad_C (8 B T G N bytes for every 1024 / N channels of a group).
+ * Results are bitwise reproducible.
+ */
+typedef struct {
+    const void* grad_y;
+    const float* grad_ST;
+    void* grad_x;
+    void* grad_dt;
+    void* grad_z;
+    void* grad_B;
+    void* grad_C;
+    float* grad_A;
+    float* grad_D;
+    float* grad_dt_bias;
+    float* grad_S0;
+} gla_ssm_grads;
+
+gla_status gla_ssm_bwd(const gla_ssm_params* p, const gla_ssm_grads* g, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+size_t gla_ssm_bwd_workspace_size(const gla_ssm_params* p);
+
+/*
+ * gla_norm_gate — the rows of every head's output on their way to the output projection: norm, weight and gate in one pass,
+ * from [B,H,T,d] to the projection's layout [B,T,H,d],
+ *     y = w (.) x / n(x) (.) act(gate),     or with gate_first   u = x (.) act(gate),  y = w (.) u / n(u),
+ * n(x) as for gla_qk_norm_rope (GLA_NORM_NONE: 1), act silu or the sigmoid, gate NULL: act = 1. x and gate are read
+ * through strides in elements (batch, head, token; the last dimension contiguous), every row starting on 16 bytes; strides
+ * may be zero or negative. d is a multiple of 16 up to 1024. Sums are fp32, y is rounded once.
+ */
+typedef struct {
+    const void* x;              /* [B,H,T,d] through x_stride, dtype */
+    const void* gate;           /* [B,H,T,d] through gate_stride, dtype, or NULL */
+    long long x_stride[3], gate_stride[3];
+    const float* w;             /* [d] or NULL (1) */
+    int B, H, T, d;
+    int norm;                   /* gla_norm */
+    int activation;             /* gla_activation: GLA_ACT_SILU or GLA_ACT_SIGMOID */
+    int gate_first;
+    float eps;                  /* >= 0 */
+    gla_dtype dtype;
+} gla_norm_gate_params;
+
+/* y [B,T,H,d] dense, 16-byte aligned, apart from every input. */
+gla_status gla_norm_gate(const gla_norm_gate_params* p, void* y, cudaStream_t stream);
+
+/*
+ * gla_norm_gate_bwd — its gradients, from grad_y (dense [B,T,H,d]): grad_x and grad_gate in `dtype` through strides of
+ * their own (they may be slices of one tensor, each row apart from every other), grad_w fp32 [d] (NULL: not wanted; must be
+ * NULL without the weight). The workspace holds the weight's partial sums, needed if grad_w is wanted:
+ * gla_norm_gate_bwd_workspace_size() bytes, 256-byte aligned. Results are bitwise reproducible on one device.
+ */
+typedef struct {
+    const void* grad_y;
+    void* grad_x;
+    void* grad_gate;
+    long long x_stride[3], gate_stride[3];
+    float* grad_w;
+} gla_norm_gate_grads;
+
+gla_status gla_norm_gate_bwd(const gla_norm_gate_params* p, const gla_norm_gate_grads* g, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+size_t gla_norm_gate_bwd_workspace_size(const gla_norm_gate_params* p);
+
+/*
+ * gla_residual_norm — what lies between two blocks: the block's output x goes into the residual, scaled and, with post_norm,
+ * normed first, and the next block's normed input comes out of it,
+ *     u = x or x / n(x),   h = residual + alpha scale (.) u,   y = w (.) h / n(h),   n(x) = sqrt(mean x^2 + eps).
+ * The norm reads h as summed in fp32. The residual and h have one type, `dtype` or fp32; h may equal residual (NULL: not
+ * written). Rows are dense, D a multiple of 16 up to 16384, all pointers on 16 bytes.
+ */
+typedef struct {
+    const void* x;              /* [rows,D] dtype */
+    const void* residual;       /* [rows,D] residual_dtype, or NULL (0) */
+    const float* w;             /* [D] or NULL (1) */
+    const float* scale;         /* [D] or NULL (1) */
+    float alpha;
+    long long rows;
+    int D;
+    int post_norm;
+    float eps;                  /* >= 0 */
+    gla_dtype dtype, residual_dtype;
+} gla_residual_params;
+
+/* h [rows,D] residual_dtype or NULL, y [rows,D] dtype. */
+gla_status gla_residual_norm(const gla_residual_params* p, void* h, void* y, cudaStream_t stream);
+
+/*
+ * gla_residual_norm_bwd — its gradients, from grad_h and grad_y (either NULL: zero): grad_x in `dtype`, grad_residual in
+ * residual_dtype, grad_w and grad_scale fp32 [D] (each NULL: not wanted; must be NULL without their input). h is formed
+ * again from the inputs. The workspace holds the vectors' partial sums, needed if one is wanted:
+ * gla_residual_norm_bwd_workspace_size() bytes, 256-byte aligned. Results are bitwise reproducible on one device.
+ */
+typedef struct {
+    const void* grad_h;
+    const void* grad_y;
+    void* grad_x;
+    void* grad_residual;
+    float* grad_w;
+    float* grad_scale;
+} gla_residual_grads;
+
+gla_status gla_residual_norm_bwd(const gla_residual_params* p, const gla_residual_grads* g, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+size_t gla_residual_norm_bwd_workspace_size(const gla_residual_params* p);
+
 /* Synchronises `stream`, then reads and clears the library's device status
  * word for the current device. GLA_ERR_TIMEOUT if a kernel gave up on a
  * bounded wait since the last call, GLA_ERR_CUDA if the stream reports an
