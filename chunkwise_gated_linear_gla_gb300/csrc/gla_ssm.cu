@@ -7,8 +7,7 @@
 // multiply-adds, all fp32, the states in registers from the first token to the last. Bound by issue: at eight
 // rows of 2048 tokens of 4096 channels of 16 states 1.07e9 exponentials and 4.3e9 multiply-adds, against 0.54 GB.
 //
-// gla_ssm_walk: a thread holds two channels by eight states and walks the tokens; B and C are read once for
-// both channels, products are packed pairs of states. The block goes in tiles of 16 tokens: raw rows
+// gla_ssm_walk: a thread holds eight states of a channel and walks the tokens, its products packed pairs of states. The block goes in tiles of 16 tokens: raw rows
 // arrive by asynchronous copies one tile ahead, delta and delta x are formed once per channel and token into shared
 // memory, the walk leaves C . h there, and y is formed from it eight channels at a time.
 //
@@ -77,7 +76,7 @@ __global__ void __launch_bounds__(kStepNT) gla_ssm_step_kernel(SsmArgs a)
         }
         y = row_sum<LPC>(y);
         y = fmaf(Dk, x, y);
-        if (zp) y *= z * sigmoid(z);
+        if (zp) y *= z * sig(z);
         if (on && l == 0) yp[(size_t)t * a.D] = (E)y;
     }
     if (on && a.ST) *reinterpret_cast<float4*>(a.ST + so) = make_float4(h[0], h[1], h[2], h[3]);
@@ -85,27 +84,32 @@ __global__ void __launch_bounds__(kStepNT) gla_ssm_step_kernel(SsmArgs a)
 
 // ------------------------------------------------------------------ the walk
 
-constexpr int kS = 8, kC = 2;      // states and channels of a thread
+constexpr int kS = 8, kC = 1;      // states and channels of a thread
 constexpr int kWalkWarps = 4;
 
 template <int N> constexpr int kWalkChannels = kWalkWarps * 32 * kS * kC / N;
 
 template <typename E, int N, int MODE>
 struct WalkShared {
-    static constexpr int CB = kWalkChannels<N>;
+    static constexpr int CB = kWalkChannels<N>, Q = N / kS;
+    static constexpr bool HAS_B = MODE != kSsmRev, HAS_C = MODE == kSsmOut || MODE == kSsmRev;
     E raw[2][3][kSsmTile][CB];        // x, dt, z (REV: dy, dt, z)
-    E bc[2][2][kSsmTile][N];          // B, C
+    E bc[2][HAS_B + HAS_C][kSsmTile][N];
+    float wide[HAS_B + HAS_C][kSsmTile][N];   // B, C of the tile in fp32
     float2 work[kSsmTile][CB];        // delta, delta x (REV: dy silu(z))
-    float yw[MODE == kSsmOut ? kSsmTile : 1][CB];
+    // C . h, over each of a channel's Q threads' states; the next Q's 64 bytes on, so that a warp's stores meet no bank twice
+    float yw[MODE == kSsmOut ? Q : 1][kSsmTile * CB + 16];
 };
 
 template <typename E, int N, int MODE>
 __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a)
 {
+    typedef WalkShared<E, N, MODE> Shared;
     constexpr int NT = kWalkWarps * 32, CB = kWalkChannels<N>, Q = N / kS, TT = kSsmTile;
-    constexpr bool REV = MODE == kSsmRev;
+    constexpr bool REV = MODE == kSsmRev, OUT = MODE == kSsmOut;
+    constexpr int IC = Shared::HAS_B ? 1 : 0;      // where C lies beside B
     extern __shared__ __align__(16) char smem_raw[];
-    auto& sm = *reinterpret_cast<WalkShared<E, N, MODE>*>(smem_raw);
+    auto& sm = *reinterpret_cast<Shared*>(smem_raw);
     const int Dg = a.D / a.G, ct = blockIdx.x % a.ctiles;
     const long long bg = blockIdx.x / a.ctiles;
     const int b = (int)(bg / a.G), g = (int)(bg % a.G);
@@ -122,14 +126,14 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
         const int stage = tile & 1, t0 = s0 + (REV ? tiles - 1 - tile : tile) * TT;
         copy_rows<E, CB, NT>(&sm.raw[stage][0][0][0], src[0], st[0], t0, s1, c0, c1);
         copy_rows<E, CB, NT>(&sm.raw[stage][1][0][0], src[1], st[1], t0, s1, c0, c1);
-        if ((MODE == kSsmOut || REV) && a.z) copy_rows<E, CB, NT>(&sm.raw[stage][2][0][0], src[2], st[2], t0, s1, c0, c1);
-        if (!REV) copy_states<E, N, NT>(&sm.bc[stage][0][0][0], Bp, a.sB[1], t0, s1);
-        if (MODE == kSsmOut || REV) copy_states<E, N, NT>(&sm.bc[stage][1][0][0], Cp, a.sC[1], t0, s1);
+        if ((OUT || REV) && a.z) copy_rows<E, CB, NT>(&sm.raw[stage][2][0][0], src[2], st[2], t0, s1, c0, c1);
+        if (Shared::HAS_B) copy_states<E, N, NT>(&sm.bc[stage][0][0][0], Bp, a.sB[1], t0, s1);
+        if (Shared::HAS_C) copy_states<E, N, NT>(&sm.bc[stage][IC][0][0], Cp, a.sC[1], t0, s1);
         copies_end();
     };
     load(0);
 
-    // this thread's two channels (cl, cl + 1) and eight states
+    // this thread's channels (cl ..) and eight states
     const int sg = threadIdx.x % Q, cl = threadIdx.x / Q * kC;
     const bool on = c0 + cl < c1;
     f2 h[kC][kS / 2], A[kC][kS / 2];
@@ -143,13 +147,13 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
     }
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-        states<kS>(a.A + (size_t)(on ? c0 + cl + i : c0) * N + sg * kS, A[i]);
+        states<kS>(a.A + so + (on ? i * N : 0), A[i]);
 #pragma unroll
         for (int j = 0; j < kS / 2; ++j) {
             A[i][j] = mul2(A[i][j], pk(kLog2e, kLog2e));
             h[i][j] = pk(0.f, 0.f);
         }
-        if (from) states<kS>(from + so + i * N, h[i]);
+        if (from) states<kS>(from + so + (on ? i * N : 0), h[i]);
     }
     // the vectors of eight channels that this thread prepares and finishes: always the same channels
     constexpr int COLS = CB / VEC, VPT = TT * COLS;
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
     for (int j = 0; j < VEC; ++j) {
         const bool in = c0 + vc < c1;
         bias[j] = a.bias && in ? a.bias[c0 + vc + j] : 0.f;
-        Dk[j] = MODE == kSsmOut && a.Dk && in ? a.Dk[c0 + vc + j] : 0.f;
+        Dk[j] = OUT && a.Dk && in ? a.Dk[c0 + vc + j] : 0.f;
         sumd[j] = 0.f;
     }
 
@@ -168,11 +172,15 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
         copies_wait<0>();
         __syncthreads();
         if (tile + 1 < tiles) load(tile + 1);
+        for (int i = threadIdx.x; i < (Shared::HAS_B + Shared::HAS_C) * TT * N / 4; i += NT) {
+            f2 v[2];
+            states<4>(&sm.bc[stage][0][0][0] + i * 4, v);
+            *reinterpret_cast<ulonglong2*>(&sm.wide[0][0][0] + i * 4) = make_ulonglong2(v[0], v[1]);
+        }
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
             float x[VEC], d[VEC];
-            const E* rows = &sm.raw[stage][0][tok][vc];
-            unpack(*reinterpret_cast<const typename Raw<E>::type*>(rows), x);
+            unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][0][tok][vc]), x);
             unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][1][tok][vc]), d);
             const bool ok = t0 + tok < s1;
             float z[VEC];
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
                 if (!ok) d[j] = 0.f;
                 if (MODE == kSsmState) sumd[j] += d[j];
                 if (REV) {
-                    if (a.z) x[j] *= z[j] * sigmoid(z[j]);
+                    if (a.z) x[j] *= z[j] * sig(z[j]);
                 } else {
                     x[j] *= d[j];
                 }
@@ -201,44 +209,52 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
 #pragma unroll
                 for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(k + i * N + 2 * j) = make_ulonglong2(h[i][j], h[i][j + 1]);
         }
+        // What the tile itself adds runs beside the states (hl, from zero); at its end the state that entered takes the tile's
+        // whole decay at once. So a long memory is rounded once per tile, not at every token.
+        f2 in[kC][kS / 2], hl[kC][kS / 2];
+        float sd[kC];
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            sd[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kS / 2; ++j) {
+                in[i][j] = h[i][j];
+                hl[i][j] = pk(0.f, 0.f);
+            }
+        }
 #pragma unroll 4
         for (int n = 0; n < TT; ++n) {
             const int tok = REV ? TT - 1 - n : n;
-            const float4 w = *reinterpret_cast<const float4*>(&sm.work[tok][cl]);
-            const float dl[kC] = {w.x, w.z}, dx[kC] = {w.y, w.w};
             f2 Bv[kS / 2], Cv[kS / 2];
-            states<kS>(&sm.bc[stage][REV ? 1 : 0][tok][sg * kS], Bv);
-            if (MODE == kSsmOut) states<kS>(&sm.bc[stage][1][tok][sg * kS], Cv);
-            float y[kC];
+            states<kS>(&sm.wide[0][tok][sg * kS], Bv);
+            if (OUT) states<kS>(&sm.wide[IC][tok][sg * kS], Cv);
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
-                const f2 d2 = pk(dl[i], dl[i]), x2 = pk(dx[i], dx[i]);
+                const float2 w = sm.work[tok][cl + i];
+                const f2 d2 = pk(w.x, w.x), x2 = pk(w.y, w.y);
+                sd[i] += w.x;
                 f2 s = pk(0.f, 0.f);
 #pragma unroll
                 for (int j = 0; j < kS / 2; ++j) {
                     const f2 e = ex2_2(mul2(d2, A[i][j]));
-                    if (REV) h[i][j] = mul2(e, fma2(x2, Bv[j], h[i][j]));
-                    else h[i][j] = fma2(e, h[i][j], mul2(x2, Bv[j]));
-                    if (MODE == kSsmOut) s = fma2(h[i][j], Cv[j], s);
+                    f2 u = mul2(x2, Bv[j]);
+                    if (REV) u = mul2(e, u);
+                    if (OUT) h[i][j] = fma2(e, h[i][j], u);
+                    hl[i][j] = fma2(e, hl[i][j], u);
+                    if (OUT) s = fma2(h[i][j], Cv[j], s);
                 }
-                float p, q;
-                up(s, p, q);
-                y[i] = p + q;
-            }
-            if (MODE == kSsmOut) {
-                // over the channel's Q threads: a pair keeps one channel each, the rest agree
-                if constexpr (Q == 1) {
-                    *reinterpret_cast<float2*>(&sm.yw[tok][cl]) = make_float2(y[0], y[1]);
-                } else {
-                    const bool odd = sg & 1;
-                    float v = (odd ? y[1] : y[0]) + __shfl_xor_sync(~0u, odd ? y[0] : y[1], 1);
-#pragma unroll
-                    for (int o = 2; o < Q; o *= 2) v += __shfl_xor_sync(~0u, v, o);
-                    if (sg < 2) sm.yw[tok][cl + sg] = v;
+                if (OUT) {
+                    float p, q;
+                    up(s, p, q);
+                    sm.yw[sg][tok * CB + cl + i] = p + q;
                 }
             }
         }
-        if (MODE != kSsmOut) continue;
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+#pragma unroll
+            for (int j = 0; j < kS / 2; ++j) h[i][j] = fma2(ex2_2(mul2(pk(sd[i], sd[i]), A[i][j])), in[i][j], hl[i][j]);
+        if (!OUT) continue;
         __syncthreads();
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
@@ -247,21 +263,23 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
             unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][0][tok][vc]), x);
             if (a.z) unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][2][tok][vc]), z);
 #pragma unroll
-            for (int j = 0; j < VEC; j += 4) {
-                const float4 q = *reinterpret_cast<const float4*>(&sm.yw[tok][vc + j]);
-                y[j] = q.x; y[j + 1] = q.y; y[j + 2] = q.z; y[j + 3] = q.w;
-            }
+            for (int j = 0; j < VEC; ++j) y[j] = Dk[j] * x[j];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                y[j] = fmaf(Dk[j], x[j], y[j]);
-                if (a.z) y[j] *= z[j] * sigmoid(z[j]);
-            }
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+                for (int j = 0; j < VEC; j += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(&sm.yw[q][tok * CB + vc + j]);
+                    y[j] += v.x; y[j + 1] += v.y; y[j + 2] += v.z; y[j + 3] += v.w;
+                }
+            if (a.z)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[j] *= z[j] * sig(z[j]);
             save8(static_cast<E*>(a.y) + ((size_t)b * a.T + t0 + tok) * a.D + c0 + vc, y);
         }
     }
 
     float* to = nullptr;
-    if (MODE == kSsmOut && seg == a.nseg - 1 && a.ST) to = a.ST + b * per;
+    if (OUT && seg == a.nseg - 1 && a.ST) to = a.ST + b * per;
     if (MODE == kSsmState) to = a.segS + ((size_t)b * (a.nseg - 1) + seg) * per;
     if (REV) to = a.segG + ((size_t)b * (a.nseg - 1) + seg - 1) * per;
     if (to && on) {
@@ -273,15 +291,15 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
     if (MODE == kSsmState) {
         // the sums of delta over the threads that prepared the same channels, in order
         __syncthreads();
-        float* sd = reinterpret_cast<float*>(&sm.work[0][0]);
+        float* sums = reinterpret_cast<float*>(&sm.work[0][0]);
         constexpr int ROWS = (NT < VPT ? NT : VPT) / COLS;
         if (threadIdx.x < ROWS * COLS)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sd[threadIdx.x / COLS * CB + vc + j] = sumd[j];
+            for (int j = 0; j < VEC; ++j) sums[threadIdx.x / COLS * CB + vc + j] = sumd[j];
         __syncthreads();
         for (int c = threadIdx.x; c < CB; c += NT) {
             float s = 0.f;
-            for (int r = 0; r < ROWS; ++r) s += sd[r * CB + c];
+            for (int r = 0; r < ROWS; ++r) s += sums[r * CB + c];
             if (c0 + c < c1) a.sumd[((size_t)b * (a.nseg - 1) + seg) * a.D + c0 + c] = s;
         }
     }

@@ -27,40 +27,44 @@ constexpr int TT = kSsmTile, HALF = TT / 2;
 
 template <int N> constexpr int kBwdChannels = NT * kS * kC / N;
 
+// A thread's four states of a channel are taken in the order n ^ m, m from its lane: then what the lanes exchange when they
+// sum over the warp's channels lies at the same place in all of them. B and C of a tile lie in shared memory once in each order,
+// 64 bytes further on each time, so that the orders' reads meet no bank twice.
+constexpr int kOrders = 4;
+
 template <typename E, int N>
 struct BwdShared {
-    static constexpr int CB = kBwdChannels<N>;
-    E raw[2][4][TT][CB];                  // x, dt, z, dy
+    static constexpr int CB = kBwdChannels<N>, Q = N / kS;
+    E raw[2][4][TT][CB];                      // x, dt, z, dy
     E bc[2][2][TT][N];
+    float wide[2][kOrders][TT * N + 16];      // B, C
     float delta[TT][CB], dx[TT][CB], r[TT][CB];
-    float y[TT][CB], p[TT][CB], e[TT][CB];
-    float red[kWarps][TT][2 * N];         // dB, dC over each warp's channels
+    float part[3][Q][TT * CB + 16];           // y, p, e over each thread's states
+    float red[kWarps][TT][2 * N];             // dB, dC over each warp's channels
+    float sums[2][VEC][NT];                   // dD, ddt_bias over each thread's tokens
 };
 
-// V values in each of the lanes that differ in bits FROM, 2 FROM .. of the lane, CNT lanes in all: halves are exchanged
-// until one value is left (lane bit i choosing the half) or the lanes are done; further lanes add up.
-template <int V, int FROM, int CNT>
-__device__ __forceinline__ void halve(float (&v)[V])
+// Four values in the order n ^ m (which is its own inverse).
+__device__ __forceinline__ void reorder(float (&v)[4], int m)
 {
-    if constexpr (CNT > 1) {
-        if constexpr (V > 1) {
-            const bool upper = threadIdx.x & FROM;
-            float w[V / 2];
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                const float give = upper ? v[i] : v[V / 2 + i], own = upper ? v[V / 2 + i] : v[i];
-                w[i] = own + __shfl_xor_sync(~0u, give, FROM);
-            }
-            halve<V / 2, FROM * 2, CNT / 2>(w);
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) v[i] = w[i];
-        } else {
-            v[0] += __shfl_xor_sync(~0u, v[0], FROM);
-            halve<1, FROM * 2, CNT / 2>(v);
-        }
-    }
+    const bool far = m & 2, near = m & 1;
+    const float a = far ? v[2] : v[0], b = far ? v[3] : v[1], c = far ? v[0] : v[2], d = far ? v[1] : v[3];
+    v[0] = near ? b : a; v[1] = near ? a : b; v[2] = near ? d : c; v[3] = near ? c : d;
 }
-constexpr int log2i(int n) { return n <= 1 ? 0 : 1 + log2i(n / 2); }
+__device__ __forceinline__ void load4(const float* p, int m, f2 (&r)[2])
+{
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    float v[4] = {q.x, q.y, q.z, q.w};
+    reorder(v, m);
+    r[0] = pk(v[0], v[1]); r[1] = pk(v[2], v[3]);
+}
+__device__ __forceinline__ void store4(float* p, int m, const f2 (&r)[2])
+{
+    float v[4];
+    up(r[0], v[0], v[1]); up(r[1], v[2], v[3]);
+    reorder(v, m);
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
 
 template <typename E, int N>
 __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
@@ -95,32 +99,29 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
     if (tiles > 0) load(tiles - 1);
 
     const int sg = threadIdx.x % Q, cl = threadIdx.x / Q * kC, warp = threadIdx.x / 32;
+    const int gi = threadIdx.x % 32 / Q;             // the lane's place among those with the same states
+    const int m = (gi & 1) * 2 + (GROUPS > 2 ? gi >> 1 & 1 : 0);
     const bool on = c0 + cl < c1;
     const size_t so = (size_t)(on ? c0 + cl : c0) * N + sg * kS;
     f2 A[kC][kS / 2], G[kC][kS / 2], dA[kC][kS / 2];
     const float* gfrom = seg < a.nseg - 1 ? a.segG + ((size_t)b * (a.nseg - 1) + seg) * per : a.dST ? a.dST + b * per : nullptr;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-        states<kS>(a.A + so + (on ? i * N : 0), A[i]);
+        load4(a.A + so + (on ? i * N : 0), m, A[i]);
 #pragma unroll
         for (int j = 0; j < kS / 2; ++j) {
             A[i][j] = mul2(A[i][j], pk(kLog2e, kLog2e));
             G[i][j] = dA[i][j] = pk(0.f, 0.f);
         }
-        if (gfrom && on) states<kS>(gfrom + so + i * N, G[i]);
+        if (gfrom && on) load4(gfrom + so + i * N, m, G[i]);
     }
     constexpr int COLS = CB / VEC, VPT = TT * COLS;
     const int vc = threadIdx.x % COLS * VEC;
-    float bias[VEC], Dk[VEC], dD[VEC], db[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const bool in = c0 + vc < c1;
-        bias[j] = a.bias && in ? a.bias[c0 + vc + j] : 0.f;
-        Dk[j] = a.Dk && in ? a.Dk[c0 + vc + j] : 0.f;
-        dD[j] = db[j] = 0.f;
-    }
+    for (int j = 0; j < VEC; ++j) sm.sums[0][j][threadIdx.x] = sm.sums[1][j][threadIdx.x] = 0.f;
     auto vec = [&](const E* p, float (&f)[VEC]) { unpack(*reinterpret_cast<const typename Raw<E>::type*>(p), f); };
     auto put = [&](float* p, const float (&f)[VEC]) { save8(p, f); };
+    auto shared = [&](const float* p, int j) -> float { return p && c0 + vc < c1 ? __ldg(p + c0 + vc + j) : 0.f; };
 
     for (int tile = tiles - 1; tile >= 0; --tile) {
         const int stage = tile & 1, t0 = s0 + tile * TT;
@@ -128,10 +129,21 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         f2 H[kC][kS / 2];
 #pragma unroll
         for (int i = 0; i < kC; ++i)
-            states<kS>(a.keep + ((size_t)b * alltiles + t0 / TT) * per + so + (on ? i * N : 0), H[i]);
+            load4(a.keep + ((size_t)b * alltiles + t0 / TT) * per + so + (on ? i * N : 0), m, H[i]);
         copies_wait<0>();
         __syncthreads();
         if (tile > 0) load(tile - 1);
+        for (int i = threadIdx.x; i < 2 * TT * N / 4; i += NT) {
+            const int which = i / (TT * N / 4), at = i % (TT * N / 4) * 4;
+            f2 q[2];
+            states<4>(&sm.bc[stage][which][0][0] + at, q);
+            float v[4];
+            up(q[0], v[0], v[1]); up(q[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(&sm.wide[which][0][at]) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(&sm.wide[which][1][at]) = make_float4(v[1], v[0], v[3], v[2]);
+            *reinterpret_cast<float4*>(&sm.wide[which][2][at]) = make_float4(v[2], v[3], v[0], v[1]);
+            *reinterpret_cast<float4*>(&sm.wide[which][3][at]) = make_float4(v[3], v[2], v[1], v[0]);
+        }
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
             float x[VEC], d[VEC], r[VEC];
@@ -142,12 +154,12 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                 float z[VEC];
                 vec(&sm.raw[stage][2][tok][vc], z);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) r[j] *= z[j] * sigmoid(z[j]);
+                for (int j = 0; j < VEC; ++j) r[j] *= z[j] * sig(z[j]);
             }
             const bool ok = t0 + tok < s1;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                d[j] += bias[j];
+                d[j] += shared(a.bias, j);
                 if (a.softplus) d[j] = softplus(d[j]);
                 if (!ok) d[j] = 0.f;
                 x[j] *= d[j];
@@ -158,12 +170,14 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         }
         __syncthreads();
 
-        // h and a of a half from the state entering it
+        // h and a of a token from the state before it
         f2 h[HALF][kC][kS / 2], ea[HALF][kC][kS / 2];
+        const float* Bw = &sm.wide[0][m][sg * kS];
+        const float* Cw = &sm.wide[1][m][sg * kS];
         auto ahead = [&](int tok, f2 (&hn)[kC][kS / 2], f2 (&an)[kC][kS / 2], const f2 (&hp)[kC][kS / 2]) {
             const float2 d = *reinterpret_cast<const float2*>(&sm.delta[tok][cl]), x = *reinterpret_cast<const float2*>(&sm.dx[tok][cl]);
             f2 Bv[kS / 2];
-            states<kS>(&sm.bc[stage][0][tok][sg * kS], Bv);
+            states<kS>(Bw + tok * N, Bv);
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
                 const float di = i ? d.y : d.x, xi = i ? x.y : x.x;
@@ -182,6 +196,18 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
 #pragma unroll
         for (int n = 0; n < HALF; ++n) ahead(n, M, unused, M);
 
+        // As the states in the walk, G takes the tile's decay at once: what the tile adds runs beside it (Gl, from zero).
+        f2 Gin[kC][kS / 2], Gl[kC][kS / 2];
+        float sd[kC];
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            sd[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kS / 2; ++j) {
+                Gin[i][j] = G[i][j];
+                Gl[i][j] = pk(0.f, 0.f);
+            }
+        }
 #pragma unroll 1
         for (int half = 1; half >= 0; --half) {
             f2 in[kC][kS / 2];
@@ -198,65 +224,67 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                 const float2 d = *reinterpret_cast<const float2*>(&sm.delta[tok][cl]), x = *reinterpret_cast<const float2*>(&sm.dx[tok][cl]),
                              r = *reinterpret_cast<const float2*>(&sm.r[tok][cl]);
                 f2 Bv[kS / 2], Cv[kS / 2], dB[kS / 2], dC[kS / 2];
-                states<kS>(&sm.bc[stage][0][tok][sg * kS], Bv);
-                states<kS>(&sm.bc[stage][1][tok][sg * kS], Cv);
-                float per_c[3][kC];                   // y, p, e of the two channels
+                states<kS>(Bw + tok * N, Bv);
+                states<kS>(Cw + tok * N, Cv);
+                float2 out[3];                        // y, p, e of the two channels over this thread's states
 #pragma unroll
                 for (int i = 0; i < kC; ++i) {
-                    const f2 d2 = i ? pk(d.y, d.y) : pk(d.x, d.x), x2 = i ? pk(x.y, x.y) : pk(x.x, x.x), r2 = i ? pk(r.y, r.y) : pk(r.x, r.x);
+                    const float di = i ? d.y : d.x;
+                    const f2 d2 = pk(di, di), x2 = i ? pk(x.y, x.y) : pk(x.x, x.x), r2 = i ? pk(r.y, r.y) : pk(r.x, r.x);
                     f2 ys = pk(0.f, 0.f), ps = ys, es = ys;
+                    sd[i] += di;
 #pragma unroll
                     for (int j = 0; j < kS / 2; ++j) {
                         const f2 hp = n ? h[n - 1][i][j] : in[i][j];
                         ys = fma2(h[n][i][j], Cv[j], ys);
                         dC[j] = i ? fma2(r2, h[n][i][j], dC[j]) : mul2(r2, h[n][i][j]);
-                        f2 gg = fma2(r2, Cv[j], G[i][j]);
+                        const f2 gg = fma2(r2, Cv[j], G[i][j]);
+                        Gl[i][j] = mul2(ea[n][i][j], fma2(r2, Cv[j], Gl[i][j]));
                         dB[j] = i ? fma2(x2, gg, dB[j]) : mul2(x2, gg);
                         ps = fma2(gg, Bv[j], ps);
-                        gg = mul2(ea[n][i][j], gg);           // a G: what goes on to the token before
-                        G[i][j] = gg;
-                        const f2 q = mul2(gg, hp);
+                        G[i][j] = mul2(ea[n][i][j], gg);      // what goes on to the token before
+                        const f2 q = mul2(G[i][j], hp);
                         es = fma2(q, A[i][j], es);
                         dA[i][j] = fma2(q, d2, dA[i][j]);
                     }
                     float u, v;
-                    up(ys, u, v); per_c[0][i] = u + v;
-                    up(ps, u, v); per_c[1][i] = u + v;
-                    up(es, u, v); per_c[2][i] = u + v;
+                    up(ys, u, v); (i ? out[0].y : out[0].x) = u + v;
+                    up(ps, u, v); (i ? out[1].y : out[1].x) = u + v;
+                    up(es, u, v); (i ? out[2].y : out[2].x) = u + v;
                 }
-                // over the channel's Q threads: one channel each, then alike
-                float* out[3] = {&sm.y[tok][cl], &sm.p[tok][cl], &sm.e[tok][cl]};
-                const bool odd = sg & 1;
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    float v = (odd ? per_c[k][1] : per_c[k][0]) + __shfl_xor_sync(~0u, odd ? per_c[k][0] : per_c[k][1], 1);
-#pragma unroll
-                    for (int o = 2; o < Q; o *= 2) v += __shfl_xor_sync(~0u, v, o);
-                    if (sg < 2) out[k][sg] = v;
-                }
-                // over the warp's channels: eight sums, halved over the lanes
-                float s[2 * kS];
-#pragma unroll
-                for (int j = 0; j < kS / 2; ++j) {
-                    up(dB[j], s[2 * j], s[2 * j + 1]);
-                    up(dC[j], s[kS + 2 * j], s[kS + 2 * j + 1]);
-                }
-                halve<2 * kS, Q, GROUPS>(s);
-                constexpr int STEPS = log2i(GROUPS) < 3 ? log2i(GROUPS) : 3, LEFT = 8 >> STEPS;
-                const int lane = threadIdx.x % 32, gi = lane / Q;     // bit 0 of gi chose half of eight, bit 1 of four, ..
-                int at = 0;
-#pragma unroll
-                for (int k = 0; k < STEPS; ++k) at += (gi >> k & 1) * (4 >> k);
-                if (gi < 1 << STEPS)
-#pragma unroll
-                    for (int k = 0; k < LEFT; ++k) {
-                        const int which = at + k;                    // 0..3 dB, 4..7 dC
-                        sm.red[warp][tok][(which / kS) * N + sg * kS + which % kS] = s[k];
+                for (int k = 0; k < 3; ++k) *reinterpret_cast<float2*>(&sm.part[k][sg][tok * CB + cl]) = out[k];
+
+                // dB, dC over the warp's channels: the lanes with the same states (GROUPS of them) halve what they hold, giving
+                // away the second half of it: first pairs, then values, then B or C; lanes beyond that add up
+                float vB[4], vC[4];
+                up(dB[0], vB[0], vB[1]); up(dB[1], vB[2], vB[3]);
+                up(dC[0], vC[0], vC[1]); up(dC[1], vC[2], vC[3]);
+                vB[0] += __shfl_xor_sync(~0u, vB[2], Q); vB[1] += __shfl_xor_sync(~0u, vB[3], Q);
+                vC[0] += __shfl_xor_sync(~0u, vC[2], Q); vC[1] += __shfl_xor_sync(~0u, vC[3], Q);
+                float* red = &sm.red[warp][tok][sg * kS];
+                if constexpr (GROUPS == 2) {
+                    red[m] = vB[0]; red[m ^ 1] = vB[1]; red[N + m] = vC[0]; red[N + (m ^ 1)] = vC[1];
+                } else {
+                    vB[0] += __shfl_xor_sync(~0u, vB[1], 2 * Q);
+                    vC[0] += __shfl_xor_sync(~0u, vC[1], 2 * Q);
+                    if constexpr (GROUPS == 4) {
+                        red[m] = vB[0]; red[N + m] = vC[0];
+                    } else {
+                        const bool isC = gi & 4;
+                        float v = (isC ? vC[0] : vB[0]) + __shfl_xor_sync(~0u, isC ? vB[0] : vC[0], 4 * Q);
+                        if constexpr (GROUPS == 16) v += __shfl_xor_sync(~0u, v, 8 * Q);
+                        if (GROUPS == 8 || gi < 8) red[(isC ? N : 0) + m] = v;
                     }
+                }
             }
         }
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+#pragma unroll
+            for (int j = 0; j < kS / 2; ++j) G[i][j] = fma2(ex2_2(mul2(pk(sd[i], sd[i]), A[i][j])), Gin[i][j], Gl[i][j]);
         __syncthreads();
-        // rows beyond the channels' end have r = 0, delta = 0 and delta x = 0: they add nothing
+        // (channels beyond the group's end have r = 0 and delta x = 0: they add nothing)
         for (int i = threadIdx.x; i < TT * 2 * N; i += NT) {
             const int tok = i / (2 * N), k = i % (2 * N);
             if (t0 + tok >= s1) continue;
@@ -268,68 +296,66 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
             if (t0 + tok >= s1 || c0 + vc >= c1) continue;
-            float x[VEC], dt[VEC], dy[VEC], d[VEC], r[VEC], y[VEC], p[VEC], e[VEC];
+            float x[VEC], dt[VEC], d[VEC], r[VEC], o[3][VEC];
             vec(&sm.raw[stage][0][tok][vc], x);
             vec(&sm.raw[stage][1][tok][vc], dt);
-            vec(&sm.raw[stage][3][tok][vc], dy);
-            auto get = [&](const float* q, float (&f)[VEC]) {
-                unpack(*reinterpret_cast<const Raw<float>::type*>(q), f);
-            };
+            auto get = [&](const float* q, float (&f)[VEC]) { unpack(*reinterpret_cast<const Raw<float>::type*>(q), f); };
             get(&sm.delta[tok][vc], d);
             get(&sm.r[tok][vc], r);
-            get(&sm.y[tok][vc], y);
-            get(&sm.p[tok][vc], p);
-            get(&sm.e[tok][vc], e);
-            const size_t o = ((size_t)b * a.T + t0 + tok) * a.D + c0 + vc;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                get(&sm.part[k][0][tok * CB + vc], o[k]);
+#pragma unroll
+                for (int q = 1; q < Q; ++q) {
+                    float f[VEC];
+                    get(&sm.part[k][q][tok * CB + vc], f);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) o[k][j] += f[j];
+                }
+            }
+            const size_t at = ((size_t)b * a.T + t0 + tok) * a.D + c0 + vc;
             if (zp) {
-                float z[VEC];
+                float z[VEC], dy[VEC];
                 vec(&sm.raw[stage][2][tok][vc], z);
+                vec(&sm.raw[stage][3][tok][vc], dy);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    const float s = sigmoid(z[j]);
-                    z[j] = dy[j] * fmaf(Dk[j], x[j], y[j]) * fmaf(z[j] * s, 1.f - s, s);
+                    const float s = sig(z[j]);
+                    z[j] = dy[j] * fmaf(shared(a.Dk, j), x[j], o[0][j]) * fmaf(z[j] * s, 1.f - s, s);
                 }
-                save8(static_cast<E*>(a.dz) + o, z);
+                save8(static_cast<E*>(a.dz) + at, z);
             }
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                dD[j] = fmaf(r[j], x[j], dD[j]);
-                float ddt = fmaf(x[j], p[j], e[j] * kLn2);
-                if (a.softplus) ddt *= softplus_slope(dt[j] + bias[j]);
-                db[j] += ddt;
+                sm.sums[0][j][threadIdx.x] += r[j] * x[j];
+                float ddt = fmaf(x[j], o[1][j], o[2][j] * kLn2);
+                if (a.softplus) ddt *= sig(dt[j] + shared(a.bias, j));
+                sm.sums[1][j][threadIdx.x] += ddt;
                 dt[j] = ddt;
-                x[j] = fmaf(d[j], p[j], Dk[j] * r[j]);
+                x[j] = fmaf(d[j], o[1][j], shared(a.Dk, j) * r[j]);
             }
-            save8(static_cast<E*>(a.dx) + o, x);
-            save8(static_cast<E*>(a.ddt) + o, dt);
+            save8(static_cast<E*>(a.dx) + at, x);
+            save8(static_cast<E*>(a.ddt) + at, dt);
         }
     }
 
     if (on && seg == 0 && a.dS0) {
 #pragma unroll
-        for (int i = 0; i < kC; ++i)
-            *reinterpret_cast<ulonglong2*>(a.dS0 + b * per + so + i * N) = make_ulonglong2(G[i][0], G[i][1]);
+        for (int i = 0; i < kC; ++i) store4(a.dS0 + b * per + so + i * N, m, G[i]);
     }
     float* part = a.part_p + ((size_t)b * a.nseg + seg) * (per + 2 * (size_t)a.D);
     if (on) {
 #pragma unroll
-        for (int i = 0; i < kC; ++i)
-            *reinterpret_cast<ulonglong2*>(part + so + i * N) = make_ulonglong2(dA[i][0], dA[i][1]);
+        for (int i = 0; i < kC; ++i) store4(part + so + i * N, m, dA[i]);
     }
     // dD and ddt_bias over the threads that finished the same channels, in order
-    __syncthreads();
-    constexpr int ROWS = (NT < VPT ? NT : VPT) / COLS;
-    if (threadIdx.x < ROWS * COLS) {
-        put(&sm.delta[0][0] + threadIdx.x / COLS * CB + vc, dD);
-        put(&sm.y[0][0] + threadIdx.x / COLS * CB + vc, db);
-    }
     __syncthreads();
     for (int c = threadIdx.x; c < CB; c += NT) {
         if (c0 + c >= c1) continue;
         float s = 0.f, q = 0.f;
-        for (int k = 0; k < ROWS; ++k) {
-            s += (&sm.delta[0][0])[k * CB + c];
-            q += (&sm.y[0][0])[k * CB + c];
+        for (int k = c / VEC; k < NT && k < VPT; k += COLS) {
+            s += sm.sums[0][c % VEC][k];
+            q += sm.sums[1][c % VEC][k];
         }
         part[per + c0 + c] = s;
         part[per + a.D + c0 + c] = q;
