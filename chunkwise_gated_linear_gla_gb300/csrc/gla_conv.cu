@@ -9,10 +9,11 @@
 //     dx_s = sum_j w_j da_{s+W-1-j} (+ dS_T where row s is in S_T; s < 0: dS0),   dw_j = sum da_t x_{t-W+1+j},
 //     dbias = sum da_t.
 //
-// Bound by HBM: x read and y written once (backward: x and dy read, dx written). A thread takes eight
-// channels (16 bytes in bf16; four in the backward, whose sums and windows fill the registers) and walks a run of tokens with
-// the window in registers; a run's first W - 1 rows are read again, from L2. Reads go through strides (a
-// projection's slice, head by head), writes are dense. Sums are fp32; S_T is a copy of inputs.
+// Bound by HBM: x read and y written once (backward: x and dy read, dx written). A thread takes four channels
+// (eight bytes in bf16; with eight the weights, windows and sums do not fit the registers: 69 us against XX for the layer below) and
+// walks a run of tokens with the window in registers; a run's first W - 1 rows are read again, from L2. A warp is 128 channels of a run
+// of one batch row, a block eight warps, runs of all rows in one order, so that single tokens of many rows fill it
+// too. Reads go through strides (a projection's slice, head by head), writes are dense. Sums are fp32; S_T is a copy of inputs.
 #include <cmath>
 #include <cstring>
 
@@ -26,6 +27,7 @@ namespace {
 constexpr int NT = 256;
 constexpr int LANES = 32;                // lanes across channels
 constexpr int RUNS = NT / LANES;         // runs of tokens per block
+constexpr int V = 4;                     // channels per thread
 constexpr int UNR = 4;                   // rows in flight per thread
 
 struct ConvArgs {
@@ -34,93 +36,85 @@ struct ConvArgs {
     const void* dy; const void* dST; void* dx; void* dS0; float* part;
     long long sx[3], sdx[3];             // strides (b, h, t) in elements
     int B, H, T, d, D, silu;
-    int run;                             // tokens per thread
-    int tblocks;                         // blocks along the tokens
+    int run, runs;                       // tokens of a run, runs of a batch row
+    int ctiles;                          // channel tiles
 };
 
-// V values of a row from p (zeros from nullptr), as loaded.
-template <typename E, int V> struct Row;
-template <> struct Row<__nv_bfloat16, 8> { uint4 u; };
-template <> struct Row<float, 8> { float4 a, b; };
-template <> struct Row<__nv_bfloat16, 4> { uint2 u; };
-template <> struct Row<float, 4> { float4 a; };
-__device__ __forceinline__ void get(Row<__nv_bfloat16, 8>& r, const __nv_bfloat16* p) { r.u = p ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ void get(Row<__nv_bfloat16, 4>& r, const __nv_bfloat16* p) { r.u = p ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0); }
-__device__ __forceinline__ void get(Row<float, 4>& r, const float* p) { r.a = p ? *reinterpret_cast<const float4*>(p) : make_float4(0, 0, 0, 0); }
-__device__ __forceinline__ void get(Row<float, 8>& r, const float* p) {
-    r.a = p ? *reinterpret_cast<const float4*>(p) : make_float4(0, 0, 0, 0);
-    r.b = p ? *(reinterpret_cast<const float4*>(p) + 1) : make_float4(0, 0, 0, 0);
+// Four values of a row from p (zeros from nullptr), as loaded, and as two pairs.
+template <typename E> struct Row;
+template <> struct Row<__nv_bfloat16> { uint2 u; };
+template <> struct Row<float> { float4 a; };
+__device__ __forceinline__ void get(Row<__nv_bfloat16>& r, const __nv_bfloat16* p) { r.u = p ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0); }
+__device__ __forceinline__ void get(Row<float>& r, const float* p) { r.a = p ? *reinterpret_cast<const float4*>(p) : make_float4(0, 0, 0, 0); }
+__device__ __forceinline__ void open(const Row<__nv_bfloat16>& r, f2 (&x)[2])
+{
+    x[0] = pk(__uint_as_float(r.u.x << 16), __uint_as_float(r.u.x & 0xffff0000u));
+    x[1] = pk(__uint_as_float(r.u.y << 16), __uint_as_float(r.u.y & 0xffff0000u));
 }
-__device__ __forceinline__ void two(uint32_t u, float& a, float& b) { a = __uint_as_float(u << 16); b = __uint_as_float(u & 0xffff0000u); }
-__device__ __forceinline__ void open(const Row<__nv_bfloat16, 8>& r, float (&x)[8]) {
-    two(r.u.x, x[0], x[1]); two(r.u.y, x[2], x[3]); two(r.u.z, x[4], x[5]); two(r.u.w, x[6], x[7]);
+__device__ __forceinline__ void open(const Row<float>& r, f2 (&x)[2]) { x[0] = pk(r.a.x, r.a.y); x[1] = pk(r.a.z, r.a.w); }
+__device__ __forceinline__ void put(__nv_bfloat16* p, const f2 (&x)[2])
+{
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2(x[0]), bf16x2(x[1]));
 }
-__device__ __forceinline__ void open(const Row<__nv_bfloat16, 4>& r, float (&x)[4]) { two(r.u.x, x[0], x[1]); two(r.u.y, x[2], x[3]); }
-__device__ __forceinline__ void open(const Row<float, 4>& r, float (&x)[4]) { x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w; }
-__device__ __forceinline__ void open(const Row<float, 8>& r, float (&x)[8]) {
-    x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w; x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
-}
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&t);
-}
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
-}
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[4]) { *reinterpret_cast<uint2*>(p) = make_uint2(pack(x[0], x[1]), pack(x[2], x[3])); }
-__device__ __forceinline__ void put(float* p, const float (&x)[4]) { *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]); }
-__device__ __forceinline__ void put(float* p, const float (&x)[8]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *(reinterpret_cast<float4*>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
-}
+__device__ __forceinline__ void put(float* p, const f2 (&x)[2]) { *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x[0], x[1]); }
 
-// The thread's place: channels c.. of batch row b, tokens [t0, t1).
-template <int V>
-struct Place {
-    int b, c, h, off, t0, t1;
-    bool on, first;
-    __device__ explicit Place(const ConvArgs& a)
+// The thread's channels c .., from the block's channel tile.
+struct Channels {
+    int c, h, off;
+    bool in;
+    __device__ explicit Channels(const ConvArgs& a)
     {
-        const int lane = threadIdx.x % LANES, r = threadIdx.x / LANES;
-        const unsigned q = blockIdx.x / a.tblocks;
-        b = blockIdx.y + blockIdx.z * 65535;
-        c = (q * LANES + lane) * V;
-        const long long at = ((long long)(blockIdx.x % a.tblocks) * RUNS + r) * a.run;
-        on = c < a.D && b < a.B && (at < a.T || at == 0);
-        t0 = (int)(at < a.T ? at : 0);
-        t1 = (int)(at + a.run < a.T ? at + a.run : a.T);
-        first = at == 0;
-        h = on ? c / a.d : 0;
-        off = c - h * a.d;
+        c = ((int)(blockIdx.x % a.ctiles) * LANES + threadIdx.x % LANES) * V;
+        in = c < a.D;
+        h = in ? c / a.d : 0;
+        off = in ? c - h * a.d : 0;
     }
 };
+// A warp's run: tokens [t0, t1) of batch row b, the r-th of all.
+struct Run {
+    int b, t0, t1;
+    bool on, first;
+    __device__ Run(const ConvArgs& a, long long r)
+    {
+        on = r < (long long)a.B * a.runs;
+        const long long q = on ? r : 0;
+        b = (int)(q / a.runs);
+        t0 = (int)(q - (long long)b * a.runs) * a.run;
+        first = t0 == 0;
+        t1 = a.T - t0 < a.run ? a.T : t0 + a.run;
+    }
+};
+// W weights of each of the thread's channels, and its bias.
+template <int W>
+__device__ __forceinline__ void weights(const ConvArgs& a, const Channels& ch, f2 (&w)[W][2], f2 (&bias)[2])
+{
+    float f[W * V];
+#pragma unroll
+    for (int i = 0; i < W * V; i += 4) {
+        const float4 q = ch.in ? __ldg(reinterpret_cast<const float4*>(a.w + (size_t)ch.c * W + i)) : make_float4(0, 0, 0, 0);
+        f[i] = q.x; f[i + 1] = q.y; f[i + 2] = q.z; f[i + 3] = q.w;
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][v] = pk(f[2 * v * W + j], f[(2 * v + 1) * W + j]);
+        bias[v] = a.bias && ch.in ? pk(__ldg(a.bias + ch.c + 2 * v), __ldg(a.bias + ch.c + 2 * v + 1)) : 0ull;
+    }
+}
 
 template <typename E, int W>
 __global__ void __launch_bounds__(NT, 4) gla_conv_fwd_kernel(ConvArgs a)
 {
-    constexpr int V = 8;
-    const Place<V> at(a);
-    if (!at.on) return;
-    float w[W][V], bias[V];
-    {
-        float f[W * V];
-#pragma unroll
-        for (int i = 0; i < W * V; i += 4) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(a.w + (size_t)at.c * W + i));
-            f[i] = q.x; f[i + 1] = q.y; f[i + 2] = q.z; f[i + 3] = q.w;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j][v] = f[v * W + j];
-#pragma unroll
-        for (int v = 0; v < V; ++v) bias[v] = a.bias ? __ldg(a.bias + at.c + v) : 0.f;
-    }
-    const E* xp = static_cast<const E*>(a.x) + at.b * a.sx[0] + at.h * a.sx[1] + at.off;
-    const E* s0 = a.S0 ? static_cast<const E*>(a.S0) + (size_t)at.b * (W - 1) * a.D + at.c : nullptr;
-    E* yp = static_cast<E*>(a.y) + ((size_t)(at.b * a.H + at.h) * a.T + at.t0) * a.d + at.off;
+    const Channels ch(a);
+    const Run at(a, (long long)(blockIdx.x / a.ctiles) * RUNS + threadIdx.x / LANES);
+    if (!ch.in || !at.on) return;
+    f2 w[W][2], bias[2];
+    weights<W>(a, ch, w, bias);
+    const E* xp = static_cast<const E*>(a.x) + at.b * a.sx[0] + ch.h * a.sx[1] + ch.off;
+    const E* s0 = a.S0 ? static_cast<const E*>(a.S0) + (size_t)at.b * (W - 1) * a.D + ch.c : nullptr;
+    E* yp = static_cast<E*>(a.y) + ((size_t)(at.b * (long long)a.H + ch.h) * a.T + at.t0) * a.d + ch.off;
 
-    Row<E, V> win[W - 1];        // rows t - W + 1 .. t - 1
+    Row<E> win[W - 1];        // rows t - W + 1 .. t - 1
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
         const int s = at.t0 - (W - 1) + i;
@@ -128,7 +122,7 @@ __global__ void __launch_bounds__(NT, 4) gla_conv_fwd_kernel(ConvArgs a)
     }
     if (at.first && a.ST) {
         // S_T may lie in S0's place: its rows are read above, by this thread alone
-        Row<E, V> last[W - 1];
+        Row<E> last[W - 1];
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
             const int s = a.T - (W - 1) + i;
@@ -142,183 +136,187 @@ __global__ void __launch_bounds__(NT, 4) gla_conv_fwd_kernel(ConvArgs a)
         }
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
-            float f[V];
+            f2 f[2];
             open(last[i], f);
-            put(static_cast<E*>(a.ST) + ((size_t)at.b * (W - 1) + i) * a.D + at.c, f);
+            put(static_cast<E*>(a.ST) + ((size_t)at.b * (W - 1) + i) * a.D + ch.c, f);
         }
     }
-    float x[W][V];               // x[j]: row t - W + 1 + j
+    f2 x[W][2];                  // x[j]: row t - W + 1 + j
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) open(win[i], x[i]);
+    const E* in_p = xp + at.t0 * a.sx[2];
     for (int t = at.t0; t < at.t1; t += UNR) {
-        Row<E, V> in[UNR];
+        Row<E> in[UNR];
 #pragma unroll
-        for (int u = 0; u < UNR; ++u) get(in[u], t + u < at.t1 ? xp + (t + u) * a.sx[2] : nullptr);
+        for (int u = 0; u < UNR; ++u) {
+            get(in[u], t + u < at.t1 ? in_p : nullptr);
+            in_p += a.sx[2];
+        }
 #pragma unroll
         for (int u = 0; u < UNR; ++u) {
             open(in[u], x[W - 1]);
-            float y[V];
+            f2 y[2];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
+            for (int v = 0; v < 2; ++v) {
                 y[v] = bias[v];
 #pragma unroll
-                for (int j = 0; j < W; ++j) y[v] = fmaf(w[j][v], x[j][v], y[v]);
-                if (a.silu) y[v] *= sigmoid(y[v]);
+                for (int j = 0; j < W; ++j) y[v] = fma2(w[j][v], x[j][v], y[v]);
+                if (a.silu) y[v] = mul2(y[v], sig(y[v]));
             }
             if (t + u < at.t1) put(yp, y);
             yp += a.d;
 #pragma unroll
             for (int j = 0; j + 1 < W; ++j)
 #pragma unroll
-                for (int v = 0; v < V; ++v) x[j][v] = x[j + 1][v];
+                for (int v = 0; v < 2; ++v) x[j][v] = x[j + 1][v];
         }
     }
 }
 
-// The backward walks W - 1 tokens past its run: dx of the run's rows needs their da. Weight sums are its own run's.
+// The backward walks W - 1 tokens past its run: dx of the run's rows needs their da. Weight sums are its own run's. A block
+// takes several groups of runs, so that it leaves one partial sum of them all.
 template <typename E, int W>
 __global__ void __launch_bounds__(NT, 2) gla_conv_bwd_kernel(ConvArgs a)
 {
-    constexpr int V = 4;
     __shared__ float red[RUNS][LANES * V * (W + 1)];
-    const Place<V> at(a);
-    float w[W][V], bias[V], dw[W + 1][V];
+    const Channels ch(a);
+    const int groups = gridDim.x / a.ctiles;
+    const long long all = (long long)a.B * a.runs;
+    f2 w[W][2], bias[2], dw[W + 1][2];
+    weights<W>(a, ch, w, bias);
 #pragma unroll
-    for (int j = 0; j <= W; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) dw[j][v] = 0.f;
-    if (at.on) {
-        float f[W * V];
-#pragma unroll
-        for (int i = 0; i < W * V; i += 4) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(a.w + (size_t)at.c * W + i));
-            f[i] = q.x; f[i + 1] = q.y; f[i + 2] = q.z; f[i + 3] = q.w;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j][v] = f[v * W + j];
-#pragma unroll
-        for (int v = 0; v < V; ++v) bias[v] = a.bias ? __ldg(a.bias + at.c + v) : 0.f;
-        const E* xp = static_cast<const E*>(a.x) + at.b * a.sx[0] + at.h * a.sx[1] + at.off;
-        const E* s0 = a.S0 ? static_cast<const E*>(a.S0) + (size_t)at.b * (W - 1) * a.D + at.c : nullptr;
-        const E* gp = static_cast<const E*>(a.dy) + (size_t)(at.b * a.H + at.h) * a.T * a.d + at.off;
-        const E* dst = a.dST ? static_cast<const E*>(a.dST) + (size_t)at.b * (W - 1) * a.D + at.c : nullptr;
-        E* dxp = static_cast<E*>(a.dx) + at.b * a.sdx[0] + at.h * a.sdx[1] + at.off;
-        E* ds0 = a.dS0 ? static_cast<E*>(a.dS0) + (size_t)at.b * (W - 1) * a.D + at.c : nullptr;
-        float x[W][V], da[W][V];     // x[j]: row t - W + 1 + j; da[j]: of row t - j
+    for (int j = 0; j <= W; ++j) dw[j][0] = dw[j][1] = 0ull;
+    for (long long r0 = (long long)(blockIdx.x / a.ctiles) * RUNS; r0 < all; r0 += (long long)groups * RUNS) {
+        const Run at(a, r0 + threadIdx.x / LANES);
+        if (!at.on || !ch.in) break;
+        const E* xp = static_cast<const E*>(a.x) + at.b * a.sx[0] + ch.h * a.sx[1] + ch.off;
+        const E* s0 = a.S0 ? static_cast<const E*>(a.S0) + (size_t)at.b * (W - 1) * a.D + ch.c : nullptr;
+        const E* gp = static_cast<const E*>(a.dy) + (size_t)(at.b * (long long)a.H + ch.h) * a.T * a.d + ch.off;
+        const E* dst = a.dST ? static_cast<const E*>(a.dST) + (size_t)at.b * (W - 1) * a.D + ch.c : nullptr;
+        E* dxp = static_cast<E*>(a.dx) + at.b * a.sdx[0] + ch.h * a.sdx[1] + ch.off;
+        E* ds0 = a.dS0 ? static_cast<E*>(a.dS0) + (size_t)at.b * (W - 1) * a.D + ch.c : nullptr;
+        f2 x[W][2], da[W][2];        // x[j]: row t - W + 1 + j; da[j]: of row t - j
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
             const int s = at.t0 - (W - 1) + i;
-            Row<E, V> r;
+            Row<E> r;
             get(r, s >= 0 ? xp + s * a.sx[2] : s0 ? s0 + (size_t)(s + W - 1) * a.D : nullptr);
             open(r, x[i]);
         }
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) da[j][v] = 0.f;
-        const int end = at.t1 + W - 1;
+        for (int j = 0; j < W; ++j) da[j][0] = da[j][1] = 0ull;
+        const int end = at.t1 + W - 1, given = end < a.T ? end : a.T;
+        const E* in_p = xp + at.t0 * a.sx[2];
+        gp += (size_t)at.t0 * a.d;
+        E* out = dxp + (at.t0 - (W - 1)) * a.sdx[2];       // of row t - W + 1
         for (int t = at.t0; t < end; t += UNR) {
-            Row<E, V> in[UNR], ing[UNR];
+            Row<E> in[UNR], ing[UNR];
 #pragma unroll
             for (int u = 0; u < UNR; ++u) {
-                const bool ok = t + u < a.T && t + u < end;
-                get(in[u], ok ? xp + (t + u) * a.sx[2] : nullptr);
-                get(ing[u], ok ? gp + (size_t)(t + u) * a.d : nullptr);
+                get(in[u], t + u < given ? in_p : nullptr);
+                get(ing[u], t + u < given ? gp : nullptr);
+                in_p += a.sx[2];
+                gp += a.d;
             }
 #pragma unroll
             for (int u = 0; u < UNR; ++u) {
                 const int tt = t + u;
                 open(in[u], x[W - 1]);
-                float g[V];
+                f2 g[2];
                 open(ing[u], g);             // (zero from T on)
 #pragma unroll
                 for (int j = W - 1; j > 0; --j)
 #pragma unroll
-                    for (int v = 0; v < V; ++v) da[j][v] = da[j - 1][v];
+                    for (int v = 0; v < 2; ++v) da[j][v] = da[j - 1][v];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
+                for (int v = 0; v < 2; ++v) {
                     da[0][v] = g[v];
                     if (a.silu) {
-                        float z = bias[v];
+                        f2 z = bias[v];
 #pragma unroll
-                        for (int j = 0; j < W; ++j) z = fmaf(w[j][v], x[j][v], z);
-                        const float s = sigmoid(z);
-                        da[0][v] = g[v] * fmaf(z * s, 1.f - s, s);
+                        for (int j = 0; j < W; ++j) z = fma2(w[j][v], x[j][v], z);
+                        const f2 s = sig(z);
+                        da[0][v] = mul2(g[v], fma2(mul2(z, s), fma2(s, both(-1.f), both(1.f)), s));
                     }
                 }
                 if (tt < at.t1) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
+                    for (int v = 0; v < 2; ++v) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][v] = fmaf(da[0][v], x[j][v], dw[j][v]);
-                        dw[W][v] += da[0][v];
+                        for (int j = 0; j < W; ++j) dw[j][v] = fma2(da[0][v], x[j][v], dw[j][v]);
+                        dw[W][v] = add2(dw[W][v], da[0][v]);
                     }
                 }
                 const int s = tt - (W - 1);
                 if (tt < end && (s >= at.t0 || (at.first && s < 0))) {
-                    float o[V];
+                    f2 o[2];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        o[v] = 0.f;
+                    for (int v = 0; v < 2; ++v) {
+                        o[v] = mul2(w[0][v], da[0][v]);
 #pragma unroll
-                        for (int j = 0; j < W; ++j) o[v] = fmaf(w[j][v], da[j][v], o[v]);
+                        for (int j = 1; j < W; ++j) o[v] = fma2(w[j][v], da[j][v], o[v]);
                     }
                     const int k = s - a.T + W - 1;
                     if (dst && k >= 0) {
-                        Row<E, V> r;
-                        float f[V];
+                        Row<E> r;
+                        f2 f[2];
                         get(r, dst + (size_t)k * a.D);
                         open(r, f);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) o[v] += f[v];
+                        o[0] = add2(o[0], f[0]);
+                        o[1] = add2(o[1], f[1]);
                     }
-                    if (s >= 0) put(dxp + s * a.sdx[2], o);
+                    if (s >= 0) put(out, o);
                     else if (ds0) put(ds0 + (size_t)(s + W - 1) * a.D, o);
                 }
+                out += a.sdx[2];
 #pragma unroll
                 for (int j = 0; j + 1 < W; ++j)
 #pragma unroll
-                    for (int v = 0; v < V; ++v) x[j][v] = x[j + 1][v];
+                    for (int v = 0; v < 2; ++v) x[j][v] = x[j + 1][v];
             }
         }
     }
     if (!a.part) return;
-    // over the block's runs, in order; a block leaves [D][W] of dw, then [D] of dbias
+    // over the block's warps, in order; a block leaves [D][W] of dw, then [D] of dbias
     const int lane = threadIdx.x % LANES, r = threadIdx.x / LANES;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < 2; ++v)
 #pragma unroll
-        for (int j = 0; j <= W; ++j) red[r][(v * (W + 1) + j) * LANES + lane] = dw[j][v];
+        for (int j = 0; j <= W; ++j) up(dw[j][v], red[r][(2 * v * (W + 1) + j) * LANES + lane], red[r][((2 * v + 1) * (W + 1) + j) * LANES + lane]);
     __syncthreads();
-    const int cols = (W + 1) * a.D, c0 = (blockIdx.x / a.tblocks) * LANES * V;
-    const long long blk = (long long)(blockIdx.y + blockIdx.z * 65535) * a.tblocks + blockIdx.x % a.tblocks;
+    const int c0 = (int)(blockIdx.x % a.ctiles) * LANES * V;
+    float* part = a.part + (size_t)(blockIdx.x / a.ctiles) * (W + 1) * a.D;
     for (int i = threadIdx.x; i < LANES * V * (W + 1); i += NT) {
-        const int ch = i / (W + 1), j = i % (W + 1);
-        if (c0 + ch >= a.D || blockIdx.y + blockIdx.z * 65535 >= (unsigned)a.B) continue;
+        const int c = i / (W + 1), j = i % (W + 1);
+        if (c0 + c >= a.D) continue;
         float s = 0.f;
-        for (int k = 0; k < RUNS; ++k) s += red[k][(ch % V * (W + 1) + j) * LANES + ch / V];
-        a.part[blk * cols + (j < W ? (c0 + ch) * W + j : a.D * W + c0 + ch)] = s;
+        for (int k = 0; k < RUNS; ++k) s += red[k][(c % V * (W + 1) + j) * LANES + c / V];
+        part[j < W ? (c0 + c) * W + j : a.D * W + c0 + c] = s;
     }
 }
 
-// Tokens per thread: long runs read fewer rows twice and leave fewer partials, short ones fill the chip.
-dim3 grid_of(ConvArgs& a, int V, int sms, bool bwd)
+// Tokens per run: long runs read fewer rows twice, short ones fill the chip. Backward: as many blocks as are resident.
+int grid_of(ConvArgs& a, int sms, bool bwd)
 {
-    const long long ct = (a.D + LANES * V - 1) / (LANES * V);
-    int run = bwd ? 64 : 32;
-    while (run > UNR && ct * a.B * ((a.T + (long long)run * RUNS - 1) / ((long long)run * RUNS)) < 4LL * sms) run /= 2;
+    a.ctiles = (a.D + LANES * V - 1) / (LANES * V);
+    const long long want = (bwd ? 4LL : 8LL) * sms * RUNS;      // warps
+    int run = 32;
+    while (run > UNR && (long long)a.ctiles * a.B * (((long long)a.T + run - 1) / run) < want) run /= 2;
     a.run = run;
-    const long long tb = (a.T + (long long)run * RUNS - 1) / ((long long)run * RUNS);
-    a.tblocks = (int)(tb > 1 ? tb : 1);
-    return dim3((unsigned)(ct * a.tblocks), a.B < 65535 ? a.B : 65535, (a.B + 65534) / 65535);
+    const long long runs = ((long long)a.T + run - 1) / run;
+    a.runs = (int)(runs > 1 ? runs : 1);
+    long long groups = ((long long)a.B * a.runs + RUNS - 1) / RUNS;
+    if (bwd) {
+        const long long most = 2LL * sms / a.ctiles > 1 ? 2LL * sms / a.ctiles : 1;
+        if (groups > most) groups = (groups + (groups + most - 1) / most - 1) / ((groups + most - 1) / most);
+    }
+    return (int)groups;
 }
 
 template <typename E, int W>
 cudaError_t launch(ConvArgs a, int sms, bool bwd, cudaStream_t s)
 {
-    const dim3 g = grid_of(a, bwd ? 4 : 8, sms, bwd);
+    const unsigned g = (unsigned)((long long)grid_of(a, sms, bwd) * a.ctiles);
     if (bwd) gla_conv_bwd_kernel<E, W><<<g, NT, 0, s>>>(a);
     else gla_conv_fwd_kernel<E, W><<<g, NT, 0, s>>>(a);
     return cudaGetLastError();
@@ -360,8 +358,7 @@ ConvArgs common(const gla_conv_params* p)
 size_t part_bytes(const gla_conv_params* p, int sms, long long* blocks)
 {
     ConvArgs a = common(p);
-    grid_of(a, 4, sms, true);
-    *blocks = (long long)a.tblocks * p->B;
+    *blocks = grid_of(a, sms, true);
     return (size_t)*blocks * a.D * (p->W + 1) * 4;
 }
 

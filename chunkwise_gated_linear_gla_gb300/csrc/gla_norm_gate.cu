@@ -10,8 +10,9 @@
 //     gate first: du = r(dy (.) w),  dx = du (.) act,  dg = du (.) x (.) act',  dw = sum dy (.) u^.
 //
 // Bound by HBM: x and g read, y written once (backward: x, g and dy read, dx and dg written). A row is LPR lanes of
-// K pieces of eight values, the rows in the order of y (a token's heads side by side); two rows' loads are in flight per
-// thread. The weight's gradient is summed in fp32 over a thread's rows, its block, then the blocks, each in a fixed order.
+// K pieces of eight values; a thread keeps its token and takes the token's heads one after the other, so that a row's address
+// is a sum (the division into batch row and token is done once), two heads' loads in flight. The weight's gradient is
+// summed in fp32 over a thread's rows, its block, then the blocks, each in a fixed order.
 #include <cmath>
 #include <cstring>
 
@@ -28,174 +29,181 @@ struct GateArgs {
     const void* x; const void* g; const float* w; void* y;
     const void* dy; void* dx; void* dg; float* part;
     long long sx[3], sg[3], sdx[3], sdg[3];   // strides (b, h, t) in elements
-    long long rows;
+    long long tokens;
     int H, T, d, norm, act, first;
+    int hsplit;                               // heads per block
     float eps;
 };
 
-__device__ __forceinline__ float act_of(float g, int silu, float& slope)
+// act(g) and its slope.
+__device__ __forceinline__ f2 act_of(f2 g, int silu, f2& slope)
 {
-    const float s = sigmoid(g);
+    const f2 s = sig(g), left = fma2(s, both(-1.f), both(1.f));      // 1 - s
     if (silu) {
-        slope = fmaf(g * s, 1.f - s, s);
-        return g * s;
+        const f2 a = mul2(g, s);
+        slope = fma2(a, left, s);
+        return a;
     }
-    slope = s * (1.f - s);
+    slope = mul2(s, left);
     return s;
 }
 
 template <typename E, int LPR, int K, bool BWD, bool FIRST>
-__global__ void __launch_bounds__(NT, K > 2 ? (BWD ? 1 : 2) : BWD ? 2 : 4) gla_norm_gate_kernel(GateArgs a)
+__global__ void __launch_bounds__(NT, K > 2 ? 1 : K > 1 || BWD ? 2 : 4) gla_norm_gate_kernel(GateArgs a)
 {
     constexpr int RPB = NT / LPR, U = BWD || K > 1 ? 1 : 2;
-    __shared__ float red[BWD ? RPB : 1][BWD ? LPR * K * VEC : 1];
+    __shared__ __align__(16) float red[BWD ? RPB : 1][BWD ? LPR * K * VEC : 4];
     const int l = threadIdx.x % LPR, row = threadIdx.x / LPR;
-    float w[K][VEC], dw[K][VEC];
+    f2 w[K][4], dw[K][4];
     bool in[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int lo = (k * LPR + l) * VEC;
         in[k] = lo < a.d;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            w[k][j] = a.w && in[k] ? a.w[lo + j] : 1.f;
-            dw[k][j] = 0.f;
+        for (int j = 0; j < 4; ++j) {
+            w[k][j] = a.w && in[k] ? pk(a.w[lo + 2 * j], a.w[lo + 2 * j + 1]) : both(1.f);
+            dw[k][j] = 0ull;
         }
     }
     const float invn = a.norm == GLA_NORM_RMS ? 1.f / (float)a.d : 1.f;
-    for (long long r0 = (long long)blockIdx.x * RPB * U; r0 < a.rows; r0 += (long long)gridDim.x * RPB * U) {
-        typename Raw<E>::type xr[U][K], gr[U][K], yr[U][K];
-        long long xo[U], go[U], dxo[U], dgo[U], yo[U];
-        bool on[U];
+    const int h0 = blockIdx.y * a.hsplit, h1 = min(a.H, h0 + a.hsplit);
+    for (long long t0 = (long long)blockIdx.x * RPB; t0 < a.tokens; t0 += (long long)gridDim.x * RPB) {
+        const bool on = t0 + row < a.tokens;
+        const long long tok = on ? t0 + row : 0;
+        const long long b = a.tokens <= 0x7fffffff ? (unsigned)tok / (unsigned)a.T : tok / a.T, t = tok - b * a.T;
+        const E* xp = static_cast<const E*>(a.x) + b * a.sx[0] + h0 * a.sx[1] + t * a.sx[2] + l * VEC;
+        const E* gp = a.g ? static_cast<const E*>(a.g) + b * a.sg[0] + h0 * a.sg[1] + t * a.sg[2] + l * VEC : nullptr;
+        const long long yo = (tok * a.H + h0) * a.d + l * VEC;
+        E* yp = BWD ? nullptr : static_cast<E*>(a.y) + yo;
+        const E* dyp = BWD ? static_cast<const E*>(a.dy) + yo : nullptr;
+        E* dxp = BWD ? static_cast<E*>(a.dx) + b * a.sdx[0] + h0 * a.sdx[1] + t * a.sdx[2] + l * VEC : nullptr;
+        E* dgp = BWD && a.g ? static_cast<E*>(a.dg) + b * a.sdg[0] + h0 * a.sdg[1] + t * a.sdg[2] + l * VEC : nullptr;
+        for (int h = h0; h < h1; h += U) {
+            typename Raw<E>::type xr[U][K], gr[U][K], yr[U][K];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long r = r0 + u * RPB + row;
-            on[u] = r < a.rows;
-            const long long q = on[u] ? r : 0;
-            long long bt, b;
-            int h, t;
-            if (a.rows <= 0x7fffffff) {
-                const unsigned n = (unsigned)q / (unsigned)a.H;
-                h = (int)((unsigned)q - n * (unsigned)a.H);
-                b = n / (unsigned)a.T;
-                t = (int)(n - (unsigned)b * (unsigned)a.T);
-            } else {
-                bt = q / a.H;
-                h = (int)(q - bt * a.H);
-                b = bt / a.T;
-                t = (int)(bt - b * a.T);
-            }
-            xo[u] = b * a.sx[0] + h * a.sx[1] + t * a.sx[2];
-            go[u] = b * a.sg[0] + h * a.sg[1] + t * a.sg[2];
-            yo[u] = q * a.d;
-            if constexpr (BWD) {
-                dxo[u] = b * a.sdx[0] + h * a.sdx[1] + t * a.sdx[2];
-                dgo[u] = b * a.sdg[0] + h * a.sdg[1] + t * a.sdg[2];
-            }
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int lo = (k * LPR + l) * VEC;
-                const bool ok = on[u] && in[k];
-                xr[u][k] = fetch(ok ? static_cast<const E*>(a.x) + xo[u] + lo : nullptr);
-                gr[u][k] = fetch(ok && a.g ? static_cast<const E*>(a.g) + go[u] + lo : nullptr);
-                if constexpr (BWD) yr[u][k] = fetch(ok ? static_cast<const E*>(a.dy) + yo[u] + lo : nullptr);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float x[K][VEC], ac[K][VEC], sl[K][VEC], xin[K][VEC];
-            float s = 0.f;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                unpack(xr[u][k], x[k]);
-                unpack(gr[u][k], ac[k]);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    if (a.g) ac[k][j] = act_of(ac[k][j], a.act == GLA_ACT_SILU, sl[k][j]);
-                    else { ac[k][j] = 1.f; sl[k][j] = 0.f; }
-                    if constexpr (BWD) xin[k][j] = x[k][j];
-                    if (FIRST) x[k][j] *= ac[k][j];
-                    s = fmaf(x[k][j], x[k][j], s);
-                }
-            }
-            float inv = 1.f;
-            if (a.norm != GLA_NORM_NONE) {
-                inv = rsqrtf(fmaf(row_sum<LPR>(s), invn, a.eps));
-                if (BWD && !on[u]) inv = 0.f;      // a row that is none holds zeros: with eps = 0, 1 / 0
-            }
-            if constexpr (!BWD) {
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        x[k][j] *= inv * w[k][j];
-                        if (!FIRST) x[k][j] *= ac[k][j];
-                    }
-                    if (on[u] && in[k]) save8(static_cast<E*>(a.y) + yo[u] + (k * LPR + l) * VEC, x[k]);
+                    const bool ok = on && in[k] && h + u < h1;
+                    const int lo = k * LPR * VEC;
+                    xr[u][k] = fetch(ok ? xp + u * a.sx[1] + lo : nullptr);
+                    gr[u][k] = fetch(ok && gp ? gp + u * a.sg[1] + lo : nullptr);
+                    if constexpr (BWD) yr[u][k] = fetch(ok ? dyp + u * a.d + lo : nullptr);
                 }
-            } else {
-                float z[K][VEC], m = 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool row_on = on && h + u < h1;
+                f2 x[K][4], ac[K][4], sl[K][4], s2 = 0ull;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    unpack(yr[u][k], z[k]);
+                    wide(xr[u][k], x[k]);
+                    wide(gr[u][k], ac[k]);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        x[k][j] *= inv;                                        // x^
-                        const float dyx = z[k][j] * x[k][j];
-                        dw[k][j] = fmaf(dyx, FIRST ? 1.f : ac[k][j], dw[k][j]);
-                        sl[k][j] *= FIRST ? xin[k][j] : dyx * w[k][j];       // dg, or what du is multiplied by
-                        z[k][j] *= FIRST ? w[k][j] : w[k][j] * ac[k][j];
-                        m = fmaf(z[k][j], x[k][j], m);
+                    for (int j = 0; j < 4; ++j) {
+                        if (gp) ac[k][j] = act_of(ac[k][j], a.act == GLA_ACT_SILU, sl[k][j]);
+                        else { ac[k][j] = both(1.f); sl[k][j] = 0ull; }
+                        if (FIRST) x[k][j] = mul2(x[k][j], ac[k][j]);
+                        s2 = fma2(x[k][j], x[k][j], s2);
                     }
                 }
-                if (a.norm != GLA_NORM_NONE) m = row_sum<LPR>(m) * invn;
-                else m = 0.f;
+                float inv = 1.f;
+                if (a.norm != GLA_NORM_NONE) {
+                    inv = rsqrtf(fmaf(row_sum<LPR>(sum2(s2)), invn, a.eps));
+                    if (BWD && !row_on) inv = 0.f;      // a row that is none holds zeros: with eps = 0, 1 / 0
+                }
+                if constexpr (!BWD) {
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const int lo = (k * LPR + l) * VEC;
+                    for (int k = 0; k < K; ++k) {
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        z[k][j] = inv * fmaf(-x[k][j], m, z[k][j]);
-                        if (FIRST) {
-                            sl[k][j] *= z[k][j];
-                            z[k][j] *= ac[k][j];
+                        for (int j = 0; j < 4; ++j) {
+                            x[k][j] = mul2(x[k][j], mul2(w[k][j], both(inv)));
+                            if (!FIRST) x[k][j] = mul2(x[k][j], ac[k][j]);
+                        }
+                        if (row_on && in[k]) keep8(yp + u * a.d + k * LPR * VEC, x[k]);
+                    }
+                } else {
+                    f2 z[K][4], m2 = 0ull;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        f2 xin[4];
+                        wide(yr[u][k], z[k]);
+                        if (FIRST) wide(xr[u][k], xin);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            x[k][j] = mul2(x[k][j], both(inv));                     // x^
+                            const f2 dyx = mul2(z[k][j], x[k][j]);
+                            dw[k][j] = FIRST ? add2(dw[k][j], dyx) : fma2(dyx, ac[k][j], dw[k][j]);
+                            // dg, or what du is multiplied by
+                            sl[k][j] = mul2(sl[k][j], FIRST ? xin[j] : mul2(dyx, w[k][j]));
+                            z[k][j] = mul2(z[k][j], FIRST ? w[k][j] : mul2(w[k][j], ac[k][j]));
+                            m2 = fma2(z[k][j], x[k][j], m2);
                         }
                     }
-                    if (on[u] && in[k]) {
-                        save8(static_cast<E*>(a.dx) + dxo[u] + lo, z[k]);
-                        if (a.g) save8(static_cast<E*>(a.dg) + dgo[u] + lo, sl[k]);
+                    const float m = a.norm != GLA_NORM_NONE ? row_sum<LPR>(sum2(m2)) * invn : 0.f;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            z[k][j] = mul2(both(inv), fma2(x[k][j], both(-m), z[k][j]));
+                            if (FIRST) {
+                                sl[k][j] = mul2(sl[k][j], z[k][j]);
+                                z[k][j] = mul2(z[k][j], ac[k][j]);
+                            }
+                        }
+                        if (row_on && in[k]) {
+                            keep8(dxp + k * LPR * VEC, z[k]);
+                            if (gp) keep8(dgp + k * LPR * VEC, sl[k]);
+                        }
                     }
                 }
+            }
+            xp += U * a.sx[1];
+            if (gp) gp += U * a.sg[1];
+            if constexpr (BWD) {
+                dyp += U * a.d;
+                dxp += U * a.sdx[1];
+                if (gp) dgp += U * a.sdg[1];
+            } else {
+                yp += U * a.d;
             }
         }
     }
     if constexpr (BWD) {
         if (!a.part) return;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) red[row][(k * LPR + l) * VEC + j] = dw[k][j];
+        for (int k = 0; k < K; ++k) keep8(&red[row][(k * LPR + l) * VEC], dw[k]);
         __syncthreads();
+        const size_t blk = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
         for (int i = threadIdx.x; i < a.d; i += NT) {
             float s = 0.f;
             for (int k = 0; k < RPB; ++k) s += red[k][i];
-            a.part[(size_t)blockIdx.x * a.d + i] = s;
+            a.part[blk * a.d + i] = s;
         }
     }
 }
 
-long long blocks_of(const GateArgs& a, int sms, bool bwd)
+// The heads are spread over blocks until every SM has its eight; backward: as many blocks as are resident, few partials.
+dim3 grid_of(GateArgs& a, int sms, bool bwd)
 {
-    const int lpr = a.d <= 64 ? 8 : a.d <= 128 ? 16 : 32, u = bwd || a.d > 256 ? 1 : 2;
-    const long long per = NT / lpr * u, n = (a.rows + per - 1) / per;
-    const long long most = bwd ? 4LL * sms : 1LL << 30;    // backward: few blocks, few partials
-    return n < most ? n : most;
+    const int lpr = a.d <= 64 ? 8 : a.d <= 128 ? 16 : 32, rows = NT / lpr;
+    const long long tg = (a.tokens + rows - 1) / rows;
+    const long long want = (bwd ? 2LL : 8LL) * sms;
+    int split = 1;
+    while (split < a.H && tg * split < want) split *= 2;
+    if (split > a.H) split = a.H;
+    a.hsplit = (a.H + split - 1) / split;
+    const int gy = (a.H + a.hsplit - 1) / a.hsplit;
+    long long gx = tg;
+    const long long most = bwd ? (want + gy - 1) / gy : 1LL << 30;
+    if (gx > most) gx = most;
+    return dim3((unsigned)gx, gy);
 }
 
 template <typename E, bool BWD, bool FIRST>
-cudaError_t launch(const GateArgs& a, int sms, cudaStream_t s)
+cudaError_t launch(GateArgs a, int sms, cudaStream_t s)
 {
-    const unsigned g = (unsigned)blocks_of(a, sms, BWD);
+    const dim3 g = grid_of(a, sms, BWD);
     if (a.d <= 64) gla_norm_gate_kernel<E, 8, 1, BWD, FIRST><<<g, NT, 0, s>>>(a);
     else if (a.d <= 128) gla_norm_gate_kernel<E, 16, 1, BWD, FIRST><<<g, NT, 0, s>>>(a);
     else if (a.d <= 256) gla_norm_gate_kernel<E, 32, 1, BWD, FIRST><<<g, NT, 0, s>>>(a);
@@ -217,7 +225,7 @@ gla_status check(const gla_norm_gate_params* p)
     if (p->activation != GLA_ACT_SILU && p->activation != GLA_ACT_SIGMOID) return GLA_ERR_INVALID_ARG;
     if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return GLA_ERR_INVALID_ARG;
     if (p->T > 0 && !p->x) return GLA_ERR_INVALID_ARG;
-    if ((long long)p->B * p->T > (1LL << 40) / p->H) return GLA_ERR_INVALID_ARG;
+    if ((long long)p->B * p->T > (1LL << 40) / p->H || p->H > 65535) return GLA_ERR_INVALID_ARG;
     const size_t e = p->dtype == GLA_BF16 ? 2 : 4;
     for (int i = 0; i < 3; ++i)
         if (p->x_stride[i] * (long long)e % 16 != 0 || p->gate_stride[i] * (long long)e % 16 != 0) return GLA_ERR_INVALID_ARG;
@@ -234,7 +242,7 @@ GateArgs common(const gla_norm_gate_params* p)
     std::memset(&a, 0, sizeof(a));
     a.x = p->x; a.g = p->gate; a.w = p->w;
     for (int i = 0; i < 3; ++i) { a.sx[i] = p->x_stride[i]; a.sg[i] = p->gate_stride[i]; }
-    a.rows = (long long)p->B * p->H * p->T;
+    a.tokens = (long long)p->B * p->T;
     a.H = p->H; a.T = p->T; a.d = p->d; a.norm = p->norm; a.act = p->activation; a.first = p->gate_first != 0;
     a.eps = p->eps;
     return a;
@@ -271,7 +279,9 @@ size_t gla_norm_gate_bwd_workspace_size(const gla_norm_gate_params* p)
     int sms = 0;
     if (check(p) != GLA_OK || p->T == 0 || !p->w) return 0;
     if (device_ready(&sms) != GLA_OK) sms = 152;
-    return (size_t)blocks_of(common(p), sms, true) * p->d * 4;
+    GateArgs a = common(p);
+    const dim3 g = grid_of(a, sms, true);
+    return (size_t)g.x * g.y * p->d * 4;
 }
 
 gla_status gla_norm_gate_bwd(const gla_norm_gate_params* p, const gla_norm_gate_grads* g, void* workspace,
@@ -311,7 +321,8 @@ gla_status gla_norm_gate_bwd(const gla_norm_gate_params* p, const gla_norm_gate_
         return r == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
     }
     GateArgs a = common(p);
-    const long long blocks = blocks_of(a, sms, true);
+    const dim3 grid = grid_of(a, sms, true);
+    const long long blocks = (long long)grid.x * grid.y;
     if (g->grad_w && (!workspace || workspace_bytes < (size_t)blocks * p->d * 4)) return GLA_ERR_WORKSPACE;
     a.dy = g->grad_y; a.dx = g->grad_x; a.dg = g->grad_gate;
     for (int i = 0; i < 3; ++i) { a.sdx[i] = g->x_stride[i]; a.sdg[i] = g->gate_stride[i]; }

@@ -37,48 +37,65 @@ struct ResArgs {
     float alpha, eps;
 };
 
-// The sum of up to two values over the row's threads, in every one of them.
-template <int NTR>
-__device__ __forceinline__ void sum_row(float& a, float& b, float (*red)[2][NTR / 32 + 1], int& turn)
+// The sum of a value, or of two, over the row's threads, in every one of them.
+template <int NTR, bool TWO>
+__device__ __forceinline__ void sum_row(float& a, float& b, float2 (*red)[NTR / 32 + 1], int& turn)
 {
     a = row_sum<32>(a);
-    b = row_sum<32>(b);
+    if (TWO) b = row_sum<32>(b);
     if constexpr (NTR > 32) {
         // two buffers in turn: a warp may be one sum ahead of another, not two
-        if (threadIdx.x % 32 == 0) {
-            red[turn][0][threadIdx.x / 32] = a;
-            red[turn][1][threadIdx.x / 32] = b;
-        }
+        if (threadIdx.x % 32 == 0) red[turn][threadIdx.x / 32] = make_float2(a, b);
         __syncthreads();
-        a = b = 0.f;
+        a = 0.f;
+        if (TWO) b = 0.f;
 #pragma unroll
         for (int i = 0; i < NTR / 32; ++i) {
-            a += red[turn][0][i];
-            b += red[turn][1][i];
+            const float2 v = red[turn][i];
+            a += v.x;
+            if (TWO) b += v.y;
         }
         turn ^= 1;
     }
 }
 
 template <typename E, typename R, int NTR, int K, bool BWD>
-__global__ void __launch_bounds__(NTR == 32 ? 32 * kWarps : NTR) gla_residual_norm_kernel(ResArgs a)
+__global__ void __launch_bounds__(NTR == 32 ? 32 * kWarps : NTR, NTR == 32 ? 1 : BWD && K < 4 ? 512 / NTR : 1)
+gla_residual_norm_kernel(ResArgs a)
 {
-    __shared__ float red[2][2][NTR / 32 + 1];
+    __shared__ float2 red[2][NTR / 32 + 1];
     int turn = 0;
     constexpr int RPB = NTR == 32 ? kWarps : 1;
     const int l = threadIdx.x % NTR;
     const float invn = 1.f / (float)a.D;
     bool in[K];
-    float dw[BWD ? K : 1][VEC], ds[BWD ? K : 1][VEC];
+    f2 dw[BWD ? K : 1][4], ds[BWD ? K : 1][4];
 #pragma unroll
     for (int k = 0; k < K; ++k) in[k] = (k * NTR + l) * VEC < a.D;
     if constexpr (BWD)
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) dw[k][j] = ds[k][j] = 0.f;
+            for (int j = 0; j < 4; ++j) dw[k][j] = ds[k][j] = 0ull;
+    // eight values of a vector (1 without it), times c
+    auto vec = [&](const float* p, int k, float c, f2 (&f)[4]) {
+        const float* q = p + (k * NTR + l) * VEC;
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            if (p && in[k]) {
+                const ulonglong2 v = __ldg(reinterpret_cast<const ulonglong2*>(q + 2 * j));
+                f[j] = v.x; f[j + 1] = v.y;
+            } else {
+                f[j] = f[j + 1] = both(1.f);
+            }
+        }
+        if (c != 1.f)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], both(c));
+    };
 
-    for (long long row = (long long)blockIdx.x * RPB + (NTR == 32 ? threadIdx.x / 32 : 0); row < a.rows; row += (long long)gridDim.x * RPB) {
+    const long long step = (long long)gridDim.x * RPB;
+    for (long long row = (long long)blockIdx.x * RPB + (NTR == 32 ? threadIdx.x / 32 : 0); row < a.rows; row += step) {
         const long long at = row * a.D + l * VEC;
         typename Raw<E>::type xr[K], yr[K];
         typename Raw<R>::type rr[K], hr[K];
@@ -92,117 +109,118 @@ __global__ void __launch_bounds__(NTR == 32 ? 32 * kWarps : NTR) gla_residual_no
                 hr[k] = fetch(in[k] && a.dh ? static_cast<const R*>(a.dh) + o : nullptr);
             }
         }
-        float x[K][VEC], h[K][VEC], invx = 1.f, s = 0.f, none = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            unpack(xr[k], x[k]);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) s = fmaf(x[k][j], x[k][j], s);
-        }
+        float invx = 1.f, none = 0.f;
         if (a.post) {
-            sum_row<NTR>(s, none, red, turn);
-            invx = rsqrtf(fmaf(s, invn, a.eps));
-        }
-        auto vec = [&](const float* p, int k, float (&f)[VEC]) {
-            const int c = (k * NTR + l) * VEC;
+            f2 s = 0ull;
 #pragma unroll
-            for (int j = 0; j < VEC; j += 4) {
-                const float4 q = p && in[k] ? __ldg(reinterpret_cast<const float4*>(p + c + j)) : make_float4(1.f, 1.f, 1.f, 1.f);
-                f[j] = q.x; f[j + 1] = q.y; f[j + 2] = q.z; f[j + 3] = q.w;
+            for (int k = 0; k < K; ++k) {
+                f2 x[4];
+                wide(xr[k], x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s = fma2(x[j], x[j], s);
             }
-        };
-        float m = 0.f;
-        s = 0.f;
+            float t = sum2(s);
+            sum_row<NTR, false>(t, none, red, turn);
+            invx = rsqrtf(fmaf(t, invn, a.eps));
+        }
+        // h, its squares' sum and (backward) that of dy w h
+        f2 h[K][4], s2 = 0ull, m2 = 0ull;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float sc[VEC], wv[VEC], g[VEC];
-            unpack(rr[k], h[k]);
-            vec(a.scale, k, sc);
-            if constexpr (BWD) {
-                vec(a.w, k, wv);
-                unpack(yr[k], g);
-            }
+            f2 x[4], sc[4];
+            wide(xr[k], x);
+            wide(rr[k], h[k]);
+            vec(a.scale, k, a.alpha * invx, sc);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                h[k][j] = fmaf(x[k][j] * invx, a.alpha * sc[j], h[k][j]);
-                s = fmaf(h[k][j], h[k][j], s);
-                if constexpr (BWD) m = fmaf(g[j] * wv[j], h[k][j], m);
+            for (int j = 0; j < 4; ++j) {
+                h[k][j] = fma2(x[j], sc[j], h[k][j]);
+                s2 = fma2(h[k][j], h[k][j], s2);
+            }
+            if constexpr (BWD) {
+                f2 wv[4], g[4];
+                vec(a.w, k, 1.f, wv);
+                wide(yr[k], g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m2 = fma2(mul2(g[j], wv[j]), h[k][j], m2);
             }
         }
-        sum_row<NTR>(s, m, red, turn);
+        float s = sum2(s2), m = sum2(m2);
+        sum_row<NTR, BWD>(s, m, red, turn);
         const float inv = rsqrtf(fmaf(s, invn, a.eps));
         if constexpr (!BWD) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (!in[k]) continue;
                 const long long o = at + k * NTR * VEC;
-                if (a.h) save8(static_cast<R*>(a.h) + o, h[k]);
-                float wv[VEC];
-                vec(a.w, k, wv);
+                if (a.h) keep8(static_cast<R*>(a.h) + o, h[k]);
+                f2 wv[4];
+                vec(a.w, k, inv, wv);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) h[k][j] *= inv * wv[j];
-                save8(static_cast<E*>(a.y) + o, h[k]);
+                for (int j = 0; j < 4; ++j) h[k][j] = mul2(h[k][j], wv[j]);
+                keep8(static_cast<E*>(a.y) + o, h[k]);
             }
         } else {
-            m *= inv * invn;                     // mean(dy w h^)
-            float q = 0.f;
+            const f2 i2 = both(inv), mm = both(-m * inv * invn);        // -mean(dy w h^)
+            f2 q2 = 0ull;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                float sc[VEC], wv[VEC], g[VEC], d[VEC];
-                unpack(yr[k], g);
-                unpack(hr[k], d);
-                vec(a.w, k, wv);
-                vec(a.scale, k, sc);
+                f2 x[4], sc[4], wv[4], g[4], d[4];
+                wide(xr[k], x);
+                wide(yr[k], g);
+                wide(hr[k], d);
+                vec(a.w, k, 1.f, wv);
+                vec(a.scale, k, 1.f, sc);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float hh = h[k][j] * inv;
-                    dw[k][j] = fmaf(g[j], hh, dw[k][j]);
-                    h[k][j] = fmaf(inv, fmaf(-hh, m, g[j] * wv[j]), d[j]);        // dr
-                    x[k][j] *= invx;                                             // u
-                    ds[k][j] = fmaf(h[k][j], x[k][j], ds[k][j]);
-                    q = fmaf(h[k][j] * sc[j], x[k][j], q);
+                for (int j = 0; j < 4; ++j) {
+                    const f2 hh = mul2(h[k][j], i2);
+                    dw[k][j] = fma2(g[j], hh, dw[k][j]);
+                    h[k][j] = fma2(i2, fma2(hh, mm, mul2(g[j], wv[j])), d[j]);        // dr
+                    const f2 p = mul2(h[k][j], x[j]);
+                    ds[k][j] = fma2(p, both(invx), ds[k][j]);
+                    q2 = fma2(p, sc[j], q2);
                 }
-                if (in[k] && a.dr) save8(static_cast<R*>(a.dr) + at + k * NTR * VEC, h[k]);
+                if (in[k] && a.dr) keep8(static_cast<R*>(a.dr) + at + k * NTR * VEC, h[k]);
             }
+            float q = 0.f;
             if (a.post) {
-                sum_row<NTR>(q, none, red, turn);
-                q *= invn;
-            } else {
-                q = 0.f;
+                q = sum2(q2);
+                sum_row<NTR, false>(q, none, red, turn);
+                q *= invx * invx * invn;                               // mean(du u^) / n(x)
             }
             if (a.dx) {
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     if (!in[k]) continue;
-                    float sc[VEC];
-                    vec(a.scale, k, sc);
+                    f2 x[4], sc[4];
+                    wide(xr[k], x);
+                    vec(a.scale, k, 1.f, sc);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) x[k][j] = a.alpha * invx * fmaf(-x[k][j], q, h[k][j] * sc[j]);
-                    save8(static_cast<E*>(a.dx) + at + k * NTR * VEC, x[k]);
+                    for (int j = 0; j < 4; ++j) x[j] = mul2(both(a.alpha * invx), fma2(x[j], both(-q), mul2(h[k][j], sc[j])));
+                    keep8(static_cast<E*>(a.dx) + at + k * NTR * VEC, x);
                 }
             }
         }
     }
     if constexpr (BWD) {
         if (!a.part) return;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ds[k][j] = mul2(ds[k][j], both(a.alpha));
         if constexpr (NTR > 32) {
             float* p = a.part + (size_t)blockIdx.x * 2 * a.D;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (!in[k]) continue;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) ds[k][j] *= a.alpha;
-                save8(p + (k * NTR + l) * VEC, dw[k]);
-                save8(p + a.D + (k * NTR + l) * VEC, ds[k]);
+                keep8(p + (k * NTR + l) * VEC, dw[k]);
+                keep8(p + a.D + (k * NTR + l) * VEC, ds[k]);
             }
         } else {
             __shared__ float sums[kWarps][K * 32 * VEC];
             for (int z = 0; z < 2; ++z) {
                 __syncthreads();
 #pragma unroll
-                for (int k = 0; k < K; ++k)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) sums[threadIdx.x / 32][(k * 32 + l) * VEC + j] = z ? a.alpha * ds[k][j] : dw[k][j];
+                for (int k = 0; k < K; ++k) keep8(&sums[threadIdx.x / 32][(k * 32 + l) * VEC], z ? ds[k] : dw[k]);
                 __syncthreads();
                 for (int i = threadIdx.x; i < a.D; i += 32 * kWarps) {
                     float t = 0.f;
@@ -218,7 +236,7 @@ long long blocks_of(long long rows, int D, int sms, bool bwd)
 {
     const long long n = D <= kWarpD ? (rows + kWarps - 1) / kWarps : rows;
     // backward: as many blocks as are resident, a partial row of both sums each
-    const long long per = D <= kWarpD ? 2 : D <= 1024 ? 12 : D <= 2048 ? 6 : D <= 4096 ? 3 : 1;
+    const long long per = D <= kWarpD ? 2 : D <= 1024 ? 8 : D <= 2048 ? 4 : D <= 4096 ? 2 : 1;
     const long long most = bwd ? per * sms : 0x7fffffff;
     return n < most ? n : most;
 }
@@ -229,9 +247,9 @@ cudaError_t launch(const ResArgs& a, int sms, cudaStream_t s)
     const unsigned g = (unsigned)blocks_of(a.rows, a.D, sms, BWD);
     if (a.D <= 256) gla_residual_norm_kernel<E, R, 32, 1, BWD><<<g, 32 * kWarps, 0, s>>>(a);
     else if (a.D <= 512) gla_residual_norm_kernel<E, R, 32, 2, BWD><<<g, 32 * kWarps, 0, s>>>(a);
-    else if (a.D <= 1024) gla_residual_norm_kernel<E, R, 128, 1, BWD><<<g, 128, 0, s>>>(a);
-    else if (a.D <= 2048) gla_residual_norm_kernel<E, R, 256, 1, BWD><<<g, 256, 0, s>>>(a);
-    else if (a.D <= 4096) gla_residual_norm_kernel<E, R, 512, 1, BWD><<<g, 512, 0, s>>>(a);
+    else if (a.D <= 1024) gla_residual_norm_kernel<E, R, 64, 2, BWD><<<g, 64, 0, s>>>(a);
+    else if (a.D <= 2048) gla_residual_norm_kernel<E, R, 128, 2, BWD><<<g, 128, 0, s>>>(a);
+    else if (a.D <= 4096) gla_residual_norm_kernel<E, R, 256, 2, BWD><<<g, 256, 0, s>>>(a);
     else if (a.D <= 8192) gla_residual_norm_kernel<E, R, 512, 2, BWD><<<g, 512, 0, s>>>(a);
     else gla_residual_norm_kernel<E, R, 512, 4, BWD><<<g, 512, 0, s>>>(a);
     return cudaGetLastError();

@@ -53,7 +53,60 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// 1 / (1 + exp(-x)): 0 and 1 at the infinities.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) { float r; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x)); return r; }
+__device__ __forceinline__ float rcp(float x) { float r; asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x)); return r; }
+
+// 1 / (1 + exp(-x)); the argument's rounding leaves |x| 2^-24 of it. 0 and 1 at the infinities.
+__device__ __forceinline__ float sig(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
+
+// Pairs of fp32 values, as the packed instructions take them.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pk(float a, float b) { f2 r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b)); return r; }
+__device__ __forceinline__ void up(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) { f2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { f2 r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c)); return r; }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) { f2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+__device__ __forceinline__ f2 ex2_2(f2 v) { float a, b; up(v, a, b); return pk(ex2(a), ex2(b)); }
+
+__device__ __forceinline__ f2 both(float c) { return pk(c, c); }
+// sig of a pair.
+__device__ __forceinline__ f2 sig(f2 x)
+{
+    float a, b;
+    up(add2(ex2_2(mul2(x, both(-kLog2e))), both(1.f)), a, b);
+    return pk(rcp(a), rcp(b));
+}
+__device__ __forceinline__ uint32_t bf16x2(f2 v)
+{
+    float a, b;
+    uint32_t u;
+    up(v, a, b);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(b), "f"(a));
+    return u;
+}
+// Eight values to p, rounded to its type.
+__device__ __forceinline__ void keep8(float* p, const f2 (&r)[4])
+{
+    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(r[0], r[1]);
+    *(reinterpret_cast<ulonglong2*>(p) + 1) = make_ulonglong2(r[2], r[3]);
+}
+__device__ __forceinline__ void keep8(__nv_bfloat16* p, const f2 (&r)[4])
+{
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(r[0]), bf16x2(r[1]), bf16x2(r[2]), bf16x2(r[3]));
+}
+// Eight loaded values as pairs.
+__device__ __forceinline__ void wide(const uint4& w, f2 (&x)[4])
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = pk(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
+}
+__device__ __forceinline__ void wide(const Raw<float>::type& w, f2 (&x)[4])
+{
+    x[0] = pk(w.a.x, w.a.y); x[1] = pk(w.a.z, w.a.w); x[2] = pk(w.b.x, w.b.y); x[3] = pk(w.b.z, w.b.w);
+}
+__device__ __forceinline__ float sum2(f2 v) { float a, b; up(v, a, b); return a + b; }
 
 }  // namespace gla

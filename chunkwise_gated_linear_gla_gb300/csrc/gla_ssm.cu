@@ -15,7 +15,6 @@
 // (the decay across the segment is exp(A sum)), gla_ssm_scan the states entering them, a second walk y.
 //
 // gla_ssm_step: single and few tokens, bound by the states' bytes: a thread holds four states of a channel.
-#include "gla_rows.cuh"
 #include "gla_ssm.cuh"
 
 namespace gla {
@@ -85,9 +84,9 @@ __global__ void __launch_bounds__(kStepNT) gla_ssm_step_kernel(SsmArgs a)
 // ------------------------------------------------------------------ the walk
 
 constexpr int kS = 8, kC = 1;      // states and channels of a thread
-constexpr int kWalkWarps = 4;
+template <int N> constexpr int kWalkWarps = N >= 64 ? 4 : N == 32 ? 2 : 2;
 
-template <int N> constexpr int kWalkChannels = kWalkWarps * 32 * kS * kC / N;
+template <int N> constexpr int kWalkChannels = kWalkWarps<N> * 32 * kS * kC / N;
 
 template <typename E, int N, int MODE>
 struct WalkShared {
@@ -96,16 +95,16 @@ struct WalkShared {
     E raw[2][3][kSsmTile][CB];        // x, dt, z (REV: dy, dt, z)
     E bc[2][HAS_B + HAS_C][kSsmTile][N];
     float wide[HAS_B + HAS_C][kSsmTile][N];   // B, C of the tile in fp32
-    float2 work[kSsmTile][CB];        // delta, delta x (REV: dy silu(z))
+    float delta[kSsmTile][CB], dx[kSsmTile][CB];   // delta, delta x (REV: dy silu(z))
     // C . h, over each of a channel's Q threads' states; the next Q's 64 bytes on, so that a warp's stores meet no bank twice
     float yw[MODE == kSsmOut ? Q : 1][kSsmTile * CB + 16];
 };
 
 template <typename E, int N, int MODE>
-__global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a)
+__global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArgs a)
 {
     typedef WalkShared<E, N, MODE> Shared;
-    constexpr int NT = kWalkWarps * 32, CB = kWalkChannels<N>, Q = N / kS, TT = kSsmTile;
+    constexpr int NT = kWalkWarps<N> * 32, CB = kWalkChannels<N>, Q = N / kS, TT = kSsmTile;
     constexpr bool REV = MODE == kSsmRev, OUT = MODE == kSsmOut;
     constexpr int IC = Shared::HAS_B ? 1 : 0;      // where C lies beside B
     extern __shared__ __align__(16) char smem_raw[];
@@ -158,14 +157,12 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
     // the vectors of eight channels that this thread prepares and finishes: always the same channels
     constexpr int COLS = CB / VEC, VPT = TT * COLS;
     const int vc = threadIdx.x % COLS * VEC;
-    float bias[VEC], Dk[VEC], sumd[VEC];
+    const bool vin = c0 + vc < c1;
+    f2 bias[4], Dk[4], sumd[4];
+    params8(a.bias ? a.bias + c0 + vc : nullptr, vin, bias);
+    params8(OUT && a.Dk ? a.Dk + c0 + vc : nullptr, vin, Dk);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const bool in = c0 + vc < c1;
-        bias[j] = a.bias && in ? a.bias[c0 + vc + j] : 0.f;
-        Dk[j] = OUT && a.Dk && in ? a.Dk[c0 + vc + j] : 0.f;
-        sumd[j] = 0.f;
-    }
+    for (int j = 0; j < 4; ++j) sumd[j] = 0ull;
 
     for (int tile = 0; tile < tiles; ++tile) {
         const int stage = tile & 1, t0 = s0 + (REV ? tiles - 1 - tile : tile) * TT;
@@ -179,27 +176,25 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
         }
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
-            float x[VEC], d[VEC];
-            unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][0][tok][vc]), x);
-            unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][1][tok][vc]), d);
+            f2 x[4], d[4], z[4];
+            states<8>(&sm.raw[stage][0][tok][vc], x);
+            states<8>(&sm.raw[stage][1][tok][vc], d);
             const bool ok = t0 + tok < s1;
-            float z[VEC];
-            if (REV && a.z) unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][2][tok][vc]), z);
+            if (REV && a.z) states<8>(&sm.raw[stage][2][tok][vc], z);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                d[j] += bias[j];
+            for (int j = 0; j < 4; ++j) {
+                d[j] = add2(d[j], bias[j]);
                 if (a.softplus) d[j] = softplus(d[j]);
-                if (!ok) d[j] = 0.f;
-                if (MODE == kSsmState) sumd[j] += d[j];
+                if (!ok) d[j] = 0ull;
+                if (MODE == kSsmState) sumd[j] = add2(sumd[j], d[j]);
                 if (REV) {
-                    if (a.z) x[j] *= z[j] * sig(z[j]);
+                    if (a.z) x[j] = mul2(x[j], mul2(z[j], sig(z[j])));
                 } else {
-                    x[j] *= d[j];
+                    x[j] = mul2(x[j], d[j]);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < VEC; j += 2)
-                *reinterpret_cast<float4*>(&sm.work[tok][vc + j]) = make_float4(d[j], x[j], d[j + 1], x[j + 1]);
+            keep8(&sm.delta[tok][vc], d);
+            keep8(&sm.dx[tok][vc], x);
         }
         __syncthreads();
         if (MODE == kSsmKeep && on) {
@@ -219,62 +214,80 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
 #pragma unroll
             for (int j = 0; j < kS / 2; ++j) {
                 in[i][j] = h[i][j];
-                hl[i][j] = pk(0.f, 0.f);
+                hl[i][j] = 0ull;
             }
         }
-#pragma unroll 4
-        for (int n = 0; n < TT; ++n) {
+        // decays and inputs of a token; those of the next are formed while this one's are used
+        struct Ahead { f2 e[kC][kS / 2], u[kC][kS / 2]; };
+        auto prepare = [&](int n, Ahead& p) {
             const int tok = REV ? TT - 1 - n : n;
-            f2 Bv[kS / 2], Cv[kS / 2];
+            f2 Bv[kS / 2];
             states<kS>(&sm.wide[0][tok][sg * kS], Bv);
-            if (OUT) states<kS>(&sm.wide[IC][tok][sg * kS], Cv);
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
-                const float2 w = sm.work[tok][cl + i];
-                const f2 d2 = pk(w.x, w.x), x2 = pk(w.y, w.y);
-                sd[i] += w.x;
-                f2 s = pk(0.f, 0.f);
+                const float d = sm.delta[tok][cl + i], x = sm.dx[tok][cl + i];
+                sd[i] += d;
 #pragma unroll
                 for (int j = 0; j < kS / 2; ++j) {
-                    const f2 e = ex2_2(mul2(d2, A[i][j]));
-                    f2 u = mul2(x2, Bv[j]);
-                    if (REV) u = mul2(e, u);
-                    if (OUT) h[i][j] = fma2(e, h[i][j], u);
-                    hl[i][j] = fma2(e, hl[i][j], u);
+                    p.e[i][j] = ex2_2(mul2(both(d), A[i][j]));
+                    p.u[i][j] = mul2(both(x), Bv[j]);
+                    if (REV) p.u[i][j] = mul2(p.e[i][j], p.u[i][j]);
+                }
+            }
+        };
+        auto use = [&](int n, const Ahead& p) {
+            f2 Cv[kS / 2];
+            if (OUT) states<kS>(&sm.wide[IC][n][sg * kS], Cv);
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                f2 s = 0ull;
+#pragma unroll
+                for (int j = 0; j < kS / 2; ++j) {
+                    if (OUT) h[i][j] = fma2(p.e[i][j], h[i][j], p.u[i][j]);
+                    hl[i][j] = fma2(p.e[i][j], hl[i][j], p.u[i][j]);
                     if (OUT) s = fma2(h[i][j], Cv[j], s);
                 }
                 if (OUT) {
-                    float p, q;
-                    up(s, p, q);
-                    sm.yw[sg][tok * CB + cl + i] = p + q;
+                    float v, w;
+                    up(s, v, w);
+                    sm.yw[sg][n * CB + cl + i] = v + w;
                 }
             }
+        };
+        Ahead even, odd;
+        prepare(0, even);
+#pragma unroll
+        for (int n = 0; n < TT; n += 2) {
+            prepare(n + 1, odd);
+            use(n, even);
+            if (n + 2 < TT) prepare(n + 2, even);
+            use(n + 1, odd);
         }
 #pragma unroll
         for (int i = 0; i < kC; ++i)
 #pragma unroll
-            for (int j = 0; j < kS / 2; ++j) h[i][j] = fma2(ex2_2(mul2(pk(sd[i], sd[i]), A[i][j])), in[i][j], hl[i][j]);
+            for (int j = 0; j < kS / 2; ++j) h[i][j] = fma2(ex2_2(mul2(both(sd[i]), A[i][j])), in[i][j], hl[i][j]);
         if (!OUT) continue;
         __syncthreads();
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
-            if (t0 + tok >= s1 || c0 + vc >= c1) continue;
-            float x[VEC], z[VEC], y[VEC];
-            unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][0][tok][vc]), x);
-            if (a.z) unpack(*reinterpret_cast<const typename Raw<E>::type*>(&sm.raw[stage][2][tok][vc]), z);
+            if (t0 + tok >= s1 || !vin) continue;
+            f2 y[4], z[4];
+            states<8>(&sm.raw[stage][0][tok][vc], y);
+            if (a.z) states<8>(&sm.raw[stage][2][tok][vc], z);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) y[j] = Dk[j] * x[j];
+            for (int j = 0; j < 4; ++j) y[j] = mul2(Dk[j], y[j]);
 #pragma unroll
-            for (int q = 0; q < Q; ++q)
+            for (int q = 0; q < Q; ++q) {
+                f2 v[4];
+                states<8>(&sm.yw[q][tok * CB + vc], v);
 #pragma unroll
-                for (int j = 0; j < VEC; j += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(&sm.yw[q][tok * CB + vc + j]);
-                    y[j] += v.x; y[j + 1] += v.y; y[j + 2] += v.z; y[j + 3] += v.w;
-                }
+                for (int j = 0; j < 4; ++j) y[j] = add2(y[j], v[j]);
+            }
             if (a.z)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) y[j] *= z[j] * sig(z[j]);
-            save8(static_cast<E*>(a.y) + ((size_t)b * a.T + t0 + tok) * a.D + c0 + vc, y);
+                for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], mul2(z[j], sig(z[j])));
+            keep8(static_cast<E*>(a.y) + ((size_t)b * a.T + t0 + tok) * a.D + c0 + vc, y);
         }
     }
 
@@ -291,11 +304,9 @@ __global__ void __launch_bounds__(kWalkWarps * 32) gla_ssm_walk_kernel(SsmArgs a
     if (MODE == kSsmState) {
         // the sums of delta over the threads that prepared the same channels, in order
         __syncthreads();
-        float* sums = reinterpret_cast<float*>(&sm.work[0][0]);
+        float* sums = &sm.delta[0][0];
         constexpr int ROWS = (NT < VPT ? NT : VPT) / COLS;
-        if (threadIdx.x < ROWS * COLS)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) sums[threadIdx.x / COLS * CB + vc + j] = sumd[j];
+        if (threadIdx.x < ROWS * COLS) keep8(sums + threadIdx.x / COLS * CB + vc, sumd);
         __syncthreads();
         for (int c = threadIdx.x; c < CB; c += NT) {
             float s = 0.f;
@@ -336,7 +347,7 @@ cudaError_t walk(const SsmArgs& a0, cudaStream_t s)
     const cudaError_t r = cudaFuncSetAttribute(gla_ssm_walk_kernel<E, N, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
     if (r != cudaSuccess) return r;
     const dim3 g((unsigned)((long long)a.B * a.G * a.ctiles), MODE == kSsmState || MODE == kSsmRev ? a.nseg - 1 : a.nseg);
-    gla_ssm_walk_kernel<E, N, MODE><<<g, kWalkWarps * 32, n, s>>>(a);
+    gla_ssm_walk_kernel<E, N, MODE><<<g, kWalkWarps<N> * 32, n, s>>>(a);
     return cudaGetLastError();
 }
 template <typename E, int N>
@@ -366,7 +377,7 @@ cudaError_t step(const SsmArgs& a, cudaStream_t s)
 
 }  // namespace
 
-int ssm_walk_channels(int N) { return kWalkWarps * 32 * kS * kC / N; }
+int ssm_walk_channels(int N) { return N == 8 ? kWalkChannels<8> : N == 16 ? kWalkChannels<16> : N == 32 ? kWalkChannels<32> : kWalkChannels<64>; }
 
 cudaError_t launch_ssm_step(const SsmArgs& a, gla_dtype dtype, cudaStream_t s)
 {

@@ -6,6 +6,9 @@
 #include <cstdint>
 
 #include "gla_internal.h"
+#ifdef __CUDACC__
+#include "gla_rows.cuh"
+#endif
 
 namespace gla {
 
@@ -50,23 +53,6 @@ int ssm_bwd_channels(int N);
 
 #ifdef __CUDACC__
 
-// Pairs of fp32 values, as the packed instructions take them.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pk(float a, float b) { f2 r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b)); return r; }
-__device__ __forceinline__ void up(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) { f2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { f2 r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c)); return r; }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) { f2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
-__device__ __forceinline__ float ex2(float x) { float r; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x)); return r; }
-__device__ __forceinline__ f2 ex2_2(f2 v) { float a, b; up(v, a, b); return pk(ex2(a), ex2(b)); }
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float rcp(float x) { float r; asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x)); return r; }
-
-// 1 / (1 + exp(-x)); the argument's rounding leaves |x| 2^-24 of it. 0 and 1 at the infinities. It is softplus' slope, too.
-__device__ __forceinline__ float sig(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
-
 // log(1 + exp(v)): log(1 + u) = 2 atanh(s), s = u / (2 + u) <= 1/3, u = exp(-|v|), so that small steps keep their digits (a
 // logarithm of the rounded 1 + u would lose them). atanh(s) / s in s^2 by Chebyshev interpolation at five points of [0, 1/9]: good to
 // 8e-9 with its coefficients rounded. -inf gives 0.
@@ -78,6 +64,22 @@ __device__ __forceinline__ float softplus(float v)
     p = fmaf(p, q, 0.3333316147327423f);
     p = fmaf(p, q, 1.f);
     return fmaf(2.f * s, p, fmaxf(v, 0.f));
+}
+
+// The same for a pair.
+__device__ __forceinline__ f2 softplus(f2 v)
+{
+    float a, b, c, d;
+    up(mul2(v, both(kLog2e)), a, b);
+    const f2 u = pk(ex2(-fabsf(a)), ex2(-fabsf(b)));
+    up(add2(u, both(2.f)), c, d);
+    const f2 s = mul2(u, pk(rcp(c), rcp(d))), q = mul2(s, s);
+    f2 p = fma2(q, both(2 * 0.14078889787197113f), both(2 * 0.13982579112052917f));
+    p = fma2(p, q, both(2 * 0.20012298226356506f));
+    p = fma2(p, q, both(2 * 0.3333316147327423f));
+    p = fma2(p, q, both(2.f));
+    up(v, a, b);
+    return fma2(s, p, pk(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
 
 // S states from p, as fp32 pairs.
@@ -104,6 +106,13 @@ __device__ __forceinline__ void states(const float* p, f2 (&r)[S / 2])
         r[2 * i] = q.x;
         r[2 * i + 1] = q.y;
     }
+}
+
+// Eight parameters of channels c .. from p, zeros without.
+__device__ __forceinline__ void params8(const float* p, bool in, f2 (&r)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = p && in ? pk(__ldg(p + 2 * i), __ldg(p + 2 * i + 1)) : 0ull;
 }
 
 __device__ __forceinline__ void copy16(void* smem, const void* g, bool ok)

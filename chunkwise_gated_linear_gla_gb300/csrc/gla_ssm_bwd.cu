@@ -15,7 +15,6 @@
 //
 // Bound by issue: per token, channel and state 9 products or multiply-adds back, 4 for h again and 4.5 for the states kept,
 // with 2.5 exponentials.
-#include "gla_rows.cuh"
 #include "gla_ssm.cuh"
 
 namespace gla {
