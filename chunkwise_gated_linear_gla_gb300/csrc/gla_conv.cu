@@ -10,7 +10,7 @@
 //     dbias = sum da_t.
 //
 // Bound by HBM: x read and y written once (backward: x and dy read, dx written). A thread takes four channels
-// (eight bytes in bf16; with eight the weights, windows and sums do not fit the registers: 69 us against XX for the layer below) and
+// (eight bytes in bf16; with eight the weights, windows and sums do not fit the registers: 69 us against 36 for the layer of 8 x 2048 tokens of 2048 channels) and
 // walks a run of tokens with the window in registers; a run's first W - 1 rows are read again, from L2. A warp is 128 channels of a run
 // of one batch row, a block eight warps, runs of all rows in one order, so that single tokens of many rows fill it
 // too. Reads go through strides (a projection's slice, head by head), writes are dense. Sums are fp32; S_T is a copy of inputs.

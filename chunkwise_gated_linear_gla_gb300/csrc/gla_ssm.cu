@@ -83,28 +83,29 @@ __global__ void __launch_bounds__(kStepNT) gla_ssm_step_kernel(SsmArgs a)
 
 // ------------------------------------------------------------------ the walk
 
-constexpr int kS = 8, kC = 1;      // states and channels of a thread
-template <int N> constexpr int kWalkWarps = N >= 64 ? 4 : N == 32 ? 2 : 2;
-
-template <int N> constexpr int kWalkChannels = kWalkWarps<N> * 32 * kS * kC / N;
+constexpr int kS = 8;              // states of a thread
+constexpr int kWalkTile = 32;      // tokens per tile of loads: two of the kept states' tiles
+template <int N> constexpr int kWalkWarps = N >= 64 ? 4 : 2;
+template <int N> constexpr int kWalkChannels = kWalkWarps<N> * 32 * kS / N;
 
 template <typename E, int N, int MODE>
 struct WalkShared {
     static constexpr int CB = kWalkChannels<N>, Q = N / kS;
-    static constexpr bool HAS_B = MODE != kSsmRev, HAS_C = MODE == kSsmOut || MODE == kSsmRev;
-    E raw[2][3][kSsmTile][CB];        // x, dt, z (REV: dy, dt, z)
-    E bc[2][HAS_B + HAS_C][kSsmTile][N];
-    float wide[HAS_B + HAS_C][kSsmTile][N];   // B, C of the tile in fp32
-    float delta[kSsmTile][CB], dx[kSsmTile][CB];   // delta, delta x (REV: dy silu(z))
-    // C . h, over each of a channel's Q threads' states; the next Q's 64 bytes on, so that a warp's stores meet no bank twice
-    float yw[MODE == kSsmOut ? Q : 1][kSsmTile * CB + 16];
+    static constexpr bool HAS_B = MODE != kSsmRev, HAS_C = MODE == kSsmOut || MODE == kSsmRev, HAS_Z = HAS_C;
+    E raw[2][HAS_Z ? 3 : 2][kWalkTile][CB];   // x, dt, z (REV: dy, dt, z)
+    E bc[2][HAS_B + HAS_C][kWalkTile][N];
+    float wide[HAS_B + HAS_C][kWalkTile][N];  // B, C of the tile in fp32
+    // delta, delta x (REV: dy silu(z)); a token's places take the two halves of its C . h once it has been walked
+    // (rows four values further on each time, the second half 64 bytes: no store meets a bank twice)
+    static constexpr int P = CB + 4;
+    float work[2][kWalkTile * P + 16];
 };
 
 template <typename E, int N, int MODE>
 __global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArgs a)
 {
     typedef WalkShared<E, N, MODE> Shared;
-    constexpr int NT = kWalkWarps<N> * 32, CB = kWalkChannels<N>, Q = N / kS, TT = kSsmTile;
+    constexpr int NT = kWalkWarps<N> * 32, CB = kWalkChannels<N>, P = Shared::P, Q = N / kS, TT = kWalkTile, SUB = kSsmTile;
     constexpr bool REV = MODE == kSsmRev, OUT = MODE == kSsmOut;
     constexpr int IC = Shared::HAS_B ? 1 : 0;      // where C lies beside B
     extern __shared__ __align__(16) char smem_raw[];
@@ -114,28 +115,32 @@ __global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArg
     const int b = (int)(bg / a.G), g = (int)(bg % a.G);
     const int c0 = g * Dg + ct * CB, c1 = g * Dg + Dg;           // this block's channels end at c1
     const int seg = blockIdx.y + (REV ? 1 : 0), s0 = seg * a.seg, s1 = min(a.T, s0 + a.seg);
-    const int tiles = (s1 - s0 + TT - 1) / TT;
+    const int tiles = (s1 - s0 + TT - 1) / TT, first = REV ? s0 + (tiles - 1) * TT : s0;
 
-    const E* src[3] = {REV ? static_cast<const E*>(a.dy) + (size_t)b * a.T * a.D : static_cast<const E*>(a.x) + b * a.sx[0],
-                       static_cast<const E*>(a.dt) + b * a.sdt[0], a.z ? static_cast<const E*>(a.z) + b * a.sz[0] : nullptr};
-    const long long st[3] = {REV ? (long long)a.D : a.sx[1], a.sdt[1], a.sz[1]};
-    const E* Bp = static_cast<const E*>(a.Bm) + b * a.sB[0] + g * N;
-    const E* Cp = static_cast<const E*>(a.Cm) + b * a.sC[0] + g * N;
-    auto load = [&](int tile) {
-        const int stage = tile & 1, t0 = s0 + (REV ? tiles - 1 - tile : tile) * TT;
-        copy_rows<E, CB, NT>(&sm.raw[stage][0][0][0], src[0], st[0], t0, s1, c0, c1);
-        copy_rows<E, CB, NT>(&sm.raw[stage][1][0][0], src[1], st[1], t0, s1, c0, c1);
-        if ((OUT || REV) && a.z) copy_rows<E, CB, NT>(&sm.raw[stage][2][0][0], src[2], st[2], t0, s1, c0, c1);
-        if (Shared::HAS_B) copy_states<E, N, NT>(&sm.bc[stage][0][0][0], Bp, a.sB[1], t0, s1);
-        if (Shared::HAS_C) copy_states<E, N, NT>(&sm.bc[stage][IC][0][0], Cp, a.sC[1], t0, s1);
+    const E* const zp = a.z && Shared::HAS_Z ? static_cast<const E*>(a.z) + b * a.sz[0] + c0 : nullptr;
+    TileCopy<E, TT, CB, NT> cx, cd, cz;
+    TileCopy<E, TT, N, NT> cB, cC;
+    if (REV) cx.start(static_cast<const E*>(a.dy) + (size_t)b * a.T * a.D + c0, a.D, first, c1 - c0);
+    else cx.start(static_cast<const E*>(a.x) + b * a.sx[0] + c0, a.sx[1], first, c1 - c0);
+    cd.start(static_cast<const E*>(a.dt) + b * a.sdt[0] + c0, a.sdt[1], first, c1 - c0);
+    if (zp) cz.start(zp, a.sz[1], first, c1 - c0);
+    if (Shared::HAS_B) cB.start(static_cast<const E*>(a.Bm) + b * a.sB[0] + g * N, a.sB[1], first, N);
+    if (Shared::HAS_C) cC.start(static_cast<const E*>(a.Cm) + b * a.sC[0] + g * N, a.sC[1], first, N);
+    auto load = [&](int stage) {
+        constexpr int step = REV ? -TT : TT;
+        cx.go(&sm.raw[stage][0][0][0], s1, step);
+        cd.go(&sm.raw[stage][1][0][0], s1, step);
+        if (zp) cz.go(&sm.raw[stage][Shared::HAS_Z ? 2 : 0][0][0], s1, step);
+        if (Shared::HAS_B) cB.go(&sm.bc[stage][0][0][0], s1, step);
+        if (Shared::HAS_C) cC.go(&sm.bc[stage][IC][0][0], s1, step);
         copies_end();
     };
     load(0);
 
-    // this thread's channels (cl ..) and eight states
-    const int sg = threadIdx.x % Q, cl = threadIdx.x / Q * kC;
+    // this thread's channel and eight states
+    const int sg = threadIdx.x % Q, cl = threadIdx.x / Q;
     const bool on = c0 + cl < c1;
-    f2 h[kC][kS / 2], A[kC][kS / 2];
+    f2 h[kS / 2], A[kS / 2];
     const size_t per = (size_t)a.D * N, so = (size_t)(on ? c0 + cl : c0) * N + sg * kS;
     const float* from = nullptr;          // this batch row's states, [D][N]
     if (REV) {
@@ -144,16 +149,13 @@ __global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArg
         if (seg > 0) from = a.segS + ((size_t)b * (a.nseg - 1) + seg - 1) * per;
         else if (a.S0) from = a.S0 + b * per;
     }
+    states<kS>(a.A + so, A);
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-        states<kS>(a.A + so + (on ? i * N : 0), A[i]);
-#pragma unroll
-        for (int j = 0; j < kS / 2; ++j) {
-            A[i][j] = mul2(A[i][j], pk(kLog2e, kLog2e));
-            h[i][j] = pk(0.f, 0.f);
-        }
-        if (from) states<kS>(from + so + (on ? i * N : 0), h[i]);
+    for (int j = 0; j < kS / 2; ++j) {
+        A[j] = mul2(A[j], both(kLog2e));
+        h[j] = 0ull;
     }
+    if (from) states<kS>(from + so, h);
     // the vectors of eight channels that this thread prepares and finishes: always the same channels
     constexpr int COLS = CB / VEC, VPT = TT * COLS;
     const int vc = threadIdx.x % COLS * VEC;
@@ -168,7 +170,8 @@ __global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArg
         const int stage = tile & 1, t0 = s0 + (REV ? tiles - 1 - tile : tile) * TT;
         copies_wait<0>();
         __syncthreads();
-        if (tile + 1 < tiles) load(tile + 1);
+        if (tile + 1 < tiles) load(stage ^ 1);
+#pragma unroll 2
         for (int i = threadIdx.x; i < (Shared::HAS_B + Shared::HAS_C) * TT * N / 4; i += NT) {
             f2 v[2];
             states<4>(&sm.bc[stage][0][0][0] + i * 4, v);
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArg
             states<8>(&sm.raw[stage][0][tok][vc], x);
             states<8>(&sm.raw[stage][1][tok][vc], d);
             const bool ok = t0 + tok < s1;
-            if (REV && a.z) states<8>(&sm.raw[stage][2][tok][vc], z);
+            if (REV && zp) states<8>(&sm.raw[stage][Shared::HAS_Z ? 2 : 0][tok][vc], z);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 d[j] = add2(d[j], bias[j]);
@@ -188,105 +191,102 @@ __global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArg
                 if (!ok) d[j] = 0ull;
                 if (MODE == kSsmState) sumd[j] = add2(sumd[j], d[j]);
                 if (REV) {
-                    if (a.z) x[j] = mul2(x[j], mul2(z[j], sig(z[j])));
+                    if (zp) x[j] = mul2(x[j], mul2(z[j], sig(z[j])));
                 } else {
                     x[j] = mul2(x[j], d[j]);
                 }
             }
-            keep8(&sm.delta[tok][vc], d);
-            keep8(&sm.dx[tok][vc], x);
+            keep8(&sm.work[0][tok * P + vc], d);
+            keep8(&sm.work[1][tok * P + vc], x);
         }
         __syncthreads();
-        if (MODE == kSsmKeep && on) {
-            float* k = a.keep + ((size_t)b * ((a.T + TT - 1) / TT) + t0 / TT) * per + so;
+#pragma unroll 1
+        for (int sub = 0; sub < TT; sub += SUB) {
+            const int base = REV ? TT - SUB - sub : sub;
+            if (MODE == kSsmKeep && on && t0 + base < s1) {
+                float* k = a.keep + ((size_t)b * ((a.T + SUB - 1) / SUB) + (t0 + base) / SUB) * per + so;
 #pragma unroll
-            for (int i = 0; i < kC; ++i)
-#pragma unroll
-                for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(k + i * N + 2 * j) = make_ulonglong2(h[i][j], h[i][j + 1]);
-        }
-        // What the tile itself adds runs beside the states (hl, from zero); at its end the state that entered takes the tile's
-        // whole decay at once. So a long memory is rounded once per tile, not at every token.
-        f2 in[kC][kS / 2], hl[kC][kS / 2];
-        float sd[kC];
-#pragma unroll
-        for (int i = 0; i < kC; ++i) {
-            sd[i] = 0.f;
+                for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(k + 2 * j) = make_ulonglong2(h[j], h[j + 1]);
+            }
+            // What these tokens themselves add runs beside the states (hl, from zero); at their end the state that entered takes
+            // their whole decay at once. So a long memory is rounded once per 16 tokens, not at every one.
+            f2 in[kS / 2], hl[kS / 2];
+            float sd = 0.f;
 #pragma unroll
             for (int j = 0; j < kS / 2; ++j) {
-                in[i][j] = h[i][j];
-                hl[i][j] = 0ull;
+                in[j] = h[j];
+                hl[j] = 0ull;
             }
-        }
-        // decays and inputs of a token; those of the next are formed while this one's are used
-        struct Ahead { f2 e[kC][kS / 2], u[kC][kS / 2]; };
-        auto prepare = [&](int n, Ahead& p) {
-            const int tok = REV ? TT - 1 - n : n;
-            f2 Bv[kS / 2];
-            states<kS>(&sm.wide[0][tok][sg * kS], Bv);
-#pragma unroll
-            for (int i = 0; i < kC; ++i) {
-                const float d = sm.delta[tok][cl + i], x = sm.dx[tok][cl + i];
-                sd[i] += d;
+            // A token in three steps, so that no wait for shared memory or an exponential is seen: its operands are fetched two
+            // tokens ahead, its decays and inputs formed one ahead.
+            struct Token { float d, x; f2 B[kS / 2], C[kS / 2], e[kS / 2], u[kS / 2]; };
+            auto fetch = [&](int n, Token& p) {
+                const int tok = base + (REV ? SUB - 1 - n : n);
+                p.d = sm.work[0][tok * P + cl];
+                p.x = sm.work[1][tok * P + cl];
+                states<kS>(&sm.wide[0][tok][sg * kS], p.B);
+                if (OUT) states<kS>(&sm.wide[IC][tok][sg * kS], p.C);
+            };
+            auto form = [&](Token& p) {
+                sd += p.d;
 #pragma unroll
                 for (int j = 0; j < kS / 2; ++j) {
-                    p.e[i][j] = ex2_2(mul2(both(d), A[i][j]));
-                    p.u[i][j] = mul2(both(x), Bv[j]);
-                    if (REV) p.u[i][j] = mul2(p.e[i][j], p.u[i][j]);
+                    p.e[j] = ex2_2(mul2(both(p.d), A[j]));
+                    p.u[j] = mul2(both(p.x), p.B[j]);
+                    if (REV) p.u[j] = mul2(p.e[j], p.u[j]);
                 }
-            }
-        };
-        auto use = [&](int n, const Ahead& p) {
-            f2 Cv[kS / 2];
-            if (OUT) states<kS>(&sm.wide[IC][n][sg * kS], Cv);
-#pragma unroll
-            for (int i = 0; i < kC; ++i) {
+            };
+            auto use = [&](int n, const Token& p) {
                 f2 s = 0ull;
 #pragma unroll
                 for (int j = 0; j < kS / 2; ++j) {
-                    if (OUT) h[i][j] = fma2(p.e[i][j], h[i][j], p.u[i][j]);
-                    hl[i][j] = fma2(p.e[i][j], hl[i][j], p.u[i][j]);
-                    if (OUT) s = fma2(h[i][j], Cv[j], s);
+                    if (OUT) h[j] = fma2(p.e[j], h[j], p.u[j]);
+                    hl[j] = fma2(p.e[j], hl[j], p.u[j]);
+                    if (OUT) s = fma2(h[j], p.C[j], s);
                 }
                 if (OUT) {
-                    float v, w;
-                    up(s, v, w);
-                    sm.yw[sg][n * CB + cl + i] = v + w;
+                    // into the places of the token's delta and delta x, which all of the channel's threads (of this warp) have read
+                    float v = sum2(s);
+#pragma unroll
+                    for (int o = 2; o < Q; o *= 2) v += __shfl_xor_sync(~0u, v, o);
+                    __syncwarp();
+                    if (Q <= 2 || sg < 2) sm.work[sg & 1][(base + n) * P + cl] = v;
                 }
+            };
+            Token p[3];
+            fetch(0, p[0]);
+            fetch(1, p[1]);
+            form(p[0]);
+#pragma unroll
+            for (int n = 0; n < SUB; ++n) {
+                if (n + 2 < SUB) fetch(n + 2, p[(n + 2) % 3]);
+                asm volatile("" ::: "memory");             // (the loads stay before what follows)
+                if (n + 1 < SUB) form(p[(n + 1) % 3]);
+                use(n, p[n % 3]);
             }
-        };
-        Ahead even, odd;
-        prepare(0, even);
 #pragma unroll
-        for (int n = 0; n < TT; n += 2) {
-            prepare(n + 1, odd);
-            use(n, even);
-            if (n + 2 < TT) prepare(n + 2, even);
-            use(n + 1, odd);
+            for (int j = 0; j < kS / 2; ++j) h[j] = fma2(ex2_2(mul2(both(sd), A[j])), in[j], hl[j]);
         }
-#pragma unroll
-        for (int i = 0; i < kC; ++i)
-#pragma unroll
-            for (int j = 0; j < kS / 2; ++j) h[i][j] = fma2(ex2_2(mul2(both(sd[i]), A[i][j])), in[i][j], hl[i][j]);
         if (!OUT) continue;
         __syncthreads();
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
             if (t0 + tok >= s1 || !vin) continue;
-            f2 y[4], z[4];
+            f2 y[4], v[4], z[4];
             states<8>(&sm.raw[stage][0][tok][vc], y);
-            if (a.z) states<8>(&sm.raw[stage][2][tok][vc], z);
+            if (zp) states<8>(&sm.raw[stage][Shared::HAS_Z ? 2 : 0][tok][vc], z);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = mul2(Dk[j], y[j]);
+            for (int q = 0; q < (Q < 2 ? 1 : 2); ++q) {
+                f2 u[4];
+                states<8>(&sm.work[q][tok * P + vc], u);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                f2 v[4];
-                states<8>(&sm.yw[q][tok * CB + vc], v);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = add2(y[j], v[j]);
+                for (int j = 0; j < 4; ++j) v[j] = q ? add2(v[j], u[j]) : u[j];
             }
-            if (a.z)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], mul2(z[j], sig(z[j])));
+            for (int j = 0; j < 4; ++j) {
+                y[j] = fma2(Dk[j], y[j], v[j]);
+                if (zp) y[j] = mul2(y[j], mul2(z[j], sig(z[j])));
+            }
             keep8(static_cast<E*>(a.y) + ((size_t)b * a.T + t0 + tok) * a.D + c0 + vc, y);
         }
     }
@@ -297,14 +297,12 @@ __global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArg
     if (REV) to = a.segG + ((size_t)b * (a.nseg - 1) + seg - 1) * per;
     if (to && on) {
 #pragma unroll
-        for (int i = 0; i < kC; ++i)
-#pragma unroll
-            for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(to + so + i * N + 2 * j) = make_ulonglong2(h[i][j], h[i][j + 1]);
+        for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(to + so + 2 * j) = make_ulonglong2(h[j], h[j + 1]);
     }
     if (MODE == kSsmState) {
         // the sums of delta over the threads that prepared the same channels, in order
         __syncthreads();
-        float* sums = &sm.delta[0][0];
+        float* sums = &sm.work[0][0];
         constexpr int ROWS = (NT < VPT ? NT : VPT) / COLS;
         if (threadIdx.x < ROWS * COLS) keep8(sums + threadIdx.x / COLS * CB + vc, sumd);
         __syncthreads();

@@ -125,28 +125,42 @@ __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_gro
 template <int LEFT>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
-// Rows [t0, t0 + kSsmTile) of channels [c0, c0 + CB) into smem [kSsmTile][CB]; tokens from t1 and channels from c1 on as zeros.
-template <typename E, int CB, int NT>
-__device__ __forceinline__ void copy_rows(E* smem, const E* src, long long st, int t0, int t1, int c0, int c1)
-{
-    constexpr int PER = 16 / sizeof(E), COLS = CB / PER;
-    for (int i = threadIdx.x; i < kSsmTile * COLS; i += NT) {
-        const int tok = i / COLS, c = i % COLS * PER;
-        const bool ok = t0 + tok < t1 && c0 + c < c1;
-        copy16(smem + tok * CB + c, ok ? src + (t0 + tok) * st + c0 + c : src, ok);
+// Copies of tiles of TT rows of W values each (a multiple of 16 bytes) by NT threads into shared memory [TT][W], tile after tile, forwards
+// or backwards. A thread's pieces lie in one column, so a tile costs it an addition and a comparison a piece. Rows from
+// t1 on and columns from `cols` on become zeros.
+template <typename E, int TT, int W, int NT>
+struct TileCopy {
+    static constexpr int PER = 16 / sizeof(E), COLS = W / PER, ROWS = NT / COLS < TT ? NT / COLS : TT;
+    static_assert(W % PER == 0 && (COLS >= NT || NT % COLS == 0) && TT % ROWS == 0, "whole pieces");
+    const E* p;
+    const E* any;                      // an address that can be read
+    long long st;
+    int row, col, t;
+    bool in;
+    // first: the first tile's first row
+    __device__ __forceinline__ void start(const E* src, long long stride, int first, int cols)
+    {
+        col = threadIdx.x % COLS * PER;
+        row = threadIdx.x / COLS;
+        in = col < cols && row < TT;
+        st = stride;
+        any = src;
+        t = first + row;
+        p = src + t * stride + col;
     }
-}
-// A tile's rows of one group of B or C, N values a token.
-template <typename E, int N, int NT>
-__device__ __forceinline__ void copy_states(E* smem, const E* src, long long st, int t0, int t1)
-{
-    constexpr int PER = 16 / sizeof(E), COLS = N / PER;
-    for (int i = threadIdx.x; i < kSsmTile * COLS; i += NT) {
-        const int tok = i / COLS, c = i % COLS * PER;
-        const bool ok = t0 + tok < t1;
-        copy16(smem + tok * N + c, ok ? src + (t0 + tok) * st + c : src, ok);
+    __device__ __forceinline__ void go(E* smem, int t1, int step)
+    {
+        if (row < TT) {
+#pragma unroll
+            for (int k = 0; k < TT; k += ROWS) {
+                const bool ok = in && t + k < t1;
+                copy16(smem + (row + k) * W + col, ok ? p + k * st : any, ok);
+            }
+        }
+        t += step;
+        p += step * st;
     }
-}
+};
 
 #endif
 }  // namespace gla

@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kS = 4, kC = 2;             // states and channels of a thread
 constexpr int kWarps = 4, NT = kWarps * 32;
-constexpr int TT = kSsmTile, HALF = TT / 2;
+constexpr int TT = kSsmTile, PART = 4;    // tokens per tile, and per part of it whose states are in registers at a time
 
 template <int N> constexpr int kBwdChannels = NT * kS * kC / N;
 
@@ -37,10 +37,11 @@ struct BwdShared {
     E raw[2][4][TT][CB];                      // x, dt, z, dy
     E bc[2][2][TT][N];
     float wide[2][kOrders][TT * N + 16];      // B, C
+    // the states entering the tile, and its parts but the first and the last, as each thread reads them
+    float keep[kC][NT * 4], mid[TT / PART - 2][kC][NT * 4];
     float delta[TT][CB], dx[TT][CB], r[TT][CB];
     float part[3][Q][TT * CB + 16];           // y, p, e over each thread's states
     float red[kWarps][TT][2 * N];             // dB, dC over each warp's channels
-    float sums[2][VEC][NT];                   // dD, ddt_bias over each thread's tokens
 };
 
 // Four values in the order n ^ m (which is its own inverse).
@@ -79,29 +80,44 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
     const int tiles = (s1 - s0 + TT - 1) / TT, alltiles = (a.T + TT - 1) / TT;
     const size_t per = (size_t)a.D * N;
 
-    const E* xp = static_cast<const E*>(a.x) + b * a.sx[0];
-    const E* dtp = static_cast<const E*>(a.dt) + b * a.sdt[0];
-    const E* zp = a.z ? static_cast<const E*>(a.z) + b * a.sz[0] : nullptr;
-    const E* dyp = static_cast<const E*>(a.dy) + (size_t)b * a.T * a.D;
-    const E* Bp = static_cast<const E*>(a.Bm) + b * a.sB[0] + g * N;
-    const E* Cp = static_cast<const E*>(a.Cm) + b * a.sC[0] + g * N;
-    auto load = [&](int tile) {                      // tiles from the last, stages in turn
-        const int stage = tile & 1, t0 = s0 + tile * TT;
-        copy_rows<E, CB, NT>(&sm.raw[stage][0][0][0], xp, a.sx[1], t0, s1, c0, c1);
-        copy_rows<E, CB, NT>(&sm.raw[stage][1][0][0], dtp, a.sdt[1], t0, s1, c0, c1);
-        if (zp) copy_rows<E, CB, NT>(&sm.raw[stage][2][0][0], zp, a.sz[1], t0, s1, c0, c1);
-        copy_rows<E, CB, NT>(&sm.raw[stage][3][0][0], dyp, a.D, t0, s1, c0, c1);
-        copy_states<E, N, NT>(&sm.bc[stage][0][0][0], Bp, a.sB[1], t0, s1);
-        copy_states<E, N, NT>(&sm.bc[stage][1][0][0], Cp, a.sC[1], t0, s1);
-        copies_end();
-    };
-    if (tiles > 0) load(tiles - 1);
-
     const int sg = threadIdx.x % Q, cl = threadIdx.x / Q * kC, warp = threadIdx.x / 32;
     const int gi = threadIdx.x % 32 / Q;             // the lane's place among those with the same states
     const int m = (gi & 1) * 2 + (GROUPS > 2 ? gi >> 1 & 1 : 0);
     const bool on = c0 + cl < c1;
     const size_t so = (size_t)(on ? c0 + cl : c0) * N + sg * kS;
+    const E* const zp = a.z ? static_cast<const E*>(a.z) + b * a.sz[0] + c0 : nullptr;
+    const int last = s0 + (tiles - 1) * TT;
+    TileCopy<E, TT, CB, NT> cx, cd, cz, cy;
+    TileCopy<E, TT, N, NT> cB, cC;
+    cx.start(static_cast<const E*>(a.x) + b * a.sx[0] + c0, a.sx[1], last, c1 - c0);
+    cd.start(static_cast<const E*>(a.dt) + b * a.sdt[0] + c0, a.sdt[1], last, c1 - c0);
+    if (zp) cz.start(zp, a.sz[1], last, c1 - c0);
+    cy.start(static_cast<const E*>(a.dy) + (size_t)b * a.T * a.D + c0, a.D, last, c1 - c0);
+    cB.start(static_cast<const E*>(a.Bm) + b * a.sB[0] + g * N, a.sB[1], last, N);
+    cC.start(static_cast<const E*>(a.Cm) + b * a.sC[0] + g * N, a.sC[1], last, N);
+    auto load = [&](int tile) {                      // tiles from the last, stages in turn
+        const int stage = tile & 1;
+        cx.go(&sm.raw[stage][0][0][0], s1, -TT);
+        cd.go(&sm.raw[stage][1][0][0], s1, -TT);
+        if (zp) cz.go(&sm.raw[stage][2][0][0], s1, -TT);
+        cy.go(&sm.raw[stage][3][0][0], s1, -TT);
+        cB.go(&sm.bc[stage][0][0][0], s1, -TT);
+        cC.go(&sm.bc[stage][1][0][0], s1, -TT);
+        copies_end();
+    };
+    // the state entering a tile: each thread copies what it reads itself
+    auto load_keep = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+            copy16(&sm.keep[i][threadIdx.x * 4], a.keep + ((size_t)b * alltiles + s0 / TT + tile) * per + so + (on ? i * N : 0), true);
+        copies_end();
+    };
+
+    if (tiles > 0) {
+        load(tiles - 1);
+        load_keep(tiles - 1);
+    }
+
     f2 A[kC][kS / 2], G[kC][kS / 2], dA[kC][kS / 2];
     const float* gfrom = seg < a.nseg - 1 ? a.segG + ((size_t)b * (a.nseg - 1) + seg) * per : a.dST ? a.dST + b * per : nullptr;
 #pragma unroll
@@ -116,19 +132,15 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
     }
     constexpr int COLS = CB / VEC, VPT = TT * COLS;
     const int vc = threadIdx.x % COLS * VEC;
+    f2 dD[4], db[4];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) sm.sums[0][j][threadIdx.x] = sm.sums[1][j][threadIdx.x] = 0.f;
-    auto vec = [&](const E* p, float (&f)[VEC]) { unpack(*reinterpret_cast<const typename Raw<E>::type*>(p), f); };
-    auto put = [&](float* p, const float (&f)[VEC]) { save8(p, f); };
-    auto shared = [&](const float* p, int j) -> float { return p && c0 + vc < c1 ? __ldg(p + c0 + vc + j) : 0.f; };
+    for (int j = 0; j < 4; ++j) dD[j] = db[j] = 0ull;
+    // this block's sums of dA, dD and ddt_bias
+    float* const part_p = a.part_p + ((size_t)b * a.nseg + seg) * (per + 2 * (size_t)a.D);
+    const bool vin = c0 + vc < c1;
 
     for (int tile = tiles - 1; tile >= 0; --tile) {
         const int stage = tile & 1, t0 = s0 + tile * TT;
-        // the state entering the tile; its loads are in flight during the preparation
-        f2 H[kC][kS / 2];
-#pragma unroll
-        for (int i = 0; i < kC; ++i)
-            load4(a.keep + ((size_t)b * alltiles + t0 / TT) * per + so + (on ? i * N : 0), m, H[i]);
         copies_wait<0>();
         __syncthreads();
         if (tile > 0) load(tile - 1);
@@ -139,40 +151,42 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
             float v[4];
             up(q[0], v[0], v[1]); up(q[1], v[2], v[3]);
             *reinterpret_cast<float4*>(&sm.wide[which][0][at]) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(&sm.wide[which][1][at]) = make_float4(v[1], v[0], v[3], v[2]);
-            *reinterpret_cast<float4*>(&sm.wide[which][2][at]) = make_float4(v[2], v[3], v[0], v[1]);
+            *reinterpret_cast<float4*>(&sm.wide[which][1][at]) = make_float4(v[2], v[3], v[0], v[1]);
+            *reinterpret_cast<float4*>(&sm.wide[which][2][at]) = make_float4(v[1], v[0], v[3], v[2]);
             *reinterpret_cast<float4*>(&sm.wide[which][3][at]) = make_float4(v[3], v[2], v[1], v[0]);
         }
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
-            float x[VEC], d[VEC], r[VEC];
-            vec(&sm.raw[stage][0][tok][vc], x);
-            vec(&sm.raw[stage][1][tok][vc], d);
-            vec(&sm.raw[stage][3][tok][vc], r);
+            f2 x[4], d[4], r[4], bias[4];
+            states<8>(&sm.raw[stage][0][tok][vc], x);
+            states<8>(&sm.raw[stage][1][tok][vc], d);
+            states<8>(&sm.raw[stage][3][tok][vc], r);
+            params8(a.bias ? a.bias + c0 + vc : nullptr, vin, bias);
             if (zp) {
-                float z[VEC];
-                vec(&sm.raw[stage][2][tok][vc], z);
+                f2 z[4];
+                states<8>(&sm.raw[stage][2][tok][vc], z);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) r[j] *= z[j] * sig(z[j]);
+                for (int j = 0; j < 4; ++j) r[j] = mul2(r[j], mul2(z[j], sig(z[j])));
             }
             const bool ok = t0 + tok < s1;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                d[j] += shared(a.bias, j);
+            for (int j = 0; j < 4; ++j) {
+                d[j] = add2(d[j], bias[j]);
                 if (a.softplus) d[j] = softplus(d[j]);
-                if (!ok) d[j] = 0.f;
-                x[j] *= d[j];
+                if (!ok) d[j] = 0ull;
+                x[j] = mul2(x[j], d[j]);
             }
-            put(&sm.delta[tok][vc], d);
-            put(&sm.dx[tok][vc], x);
-            put(&sm.r[tok][vc], r);
+            keep8(&sm.delta[tok][vc], d);
+            keep8(&sm.dx[tok][vc], x);
+            keep8(&sm.r[tok][vc], r);
         }
         __syncthreads();
 
         // h and a of a token from the state before it
-        f2 h[HALF][kC][kS / 2], ea[HALF][kC][kS / 2];
-        const float* Bw = &sm.wide[0][m][sg * kS];
-        const float* Cw = &sm.wide[1][m][sg * kS];
+        f2 h[PART][kC][kS / 2], ea[PART][kC][kS / 2];
+        const int slot = (m & 1) * 2 + (m >> 1);      // (neighbouring lanes read neighbouring places)
+        const float* Bw = &sm.wide[0][slot][sg * kS];
+        const float* Cw = &sm.wide[1][slot][sg * kS];
         auto ahead = [&](int tok, f2 (&hn)[kC][kS / 2], f2 (&an)[kC][kS / 2], const f2 (&hp)[kC][kS / 2]) {
             const float2 d = *reinterpret_cast<const float2*>(&sm.delta[tok][cl]), x = *reinterpret_cast<const float2*>(&sm.dx[tok][cl]);
             f2 Bv[kS / 2];
@@ -182,18 +196,23 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                 const float di = i ? d.y : d.x, xi = i ? x.y : x.x;
 #pragma unroll
                 for (int j = 0; j < kS / 2; ++j) {
-                    an[i][j] = ex2_2(mul2(pk(di, di), A[i][j]));
-                    hn[i][j] = fma2(an[i][j], hp[i][j], mul2(pk(xi, xi), Bv[j]));
+                    an[i][j] = ex2_2(mul2(both(di), A[i][j]));
+                    hn[i][j] = fma2(an[i][j], hp[i][j], mul2(both(xi), Bv[j]));
                 }
             }
         };
-        f2 M[kC][kS / 2], unused[kC][kS / 2];         // the state entering the second half
+        // the states entering the tile's parts; the first of them is the one that was kept, the last stays in registers
+        f2 in[kC][kS / 2];
 #pragma unroll
-        for (int i = 0; i < kC; ++i)
+        for (int i = 0; i < kC; ++i) load4(&sm.keep[i][threadIdx.x * 4], m, in[i]);
+#pragma unroll 1
+        for (int part = 0; part < TT / PART - 1; ++part) {
+            if (part > 0)
 #pragma unroll
-            for (int j = 0; j < kS / 2; ++j) M[i][j] = H[i][j];
+                for (int i = 0; i < kC; ++i) *reinterpret_cast<ulonglong2*>(&sm.mid[part - 1][i][threadIdx.x * 4]) = make_ulonglong2(in[i][0], in[i][1]);
 #pragma unroll
-        for (int n = 0; n < HALF; ++n) ahead(n, M, unused, M);
+            for (int n = 0; n < PART; ++n) ahead(part * PART + n, in, ea[0], in);
+        }
 
         // As the states in the walk, G takes the tile's decay at once: what the tile adds runs beside it (Gl, from zero).
         f2 Gin[kC][kS / 2], Gl[kC][kS / 2];
@@ -208,17 +227,19 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
             }
         }
 #pragma unroll 1
-        for (int half = 1; half >= 0; --half) {
-            f2 in[kC][kS / 2];
+        for (int part = TT / PART - 1; part >= 0; --part) {
+            const int tb = part * PART;
+            if (part == 0) {
 #pragma unroll
-            for (int i = 0; i < kC; ++i)
+                for (int i = 0; i < kC; ++i) load4(&sm.keep[i][threadIdx.x * 4], m, in[i]);
+            } else if (part < TT / PART - 1) {
 #pragma unroll
-                for (int j = 0; j < kS / 2; ++j) in[i][j] = half ? M[i][j] : H[i][j];
-            const int tb = half * HALF;
+                for (int i = 0; i < kC; ++i) states<kS>(&sm.mid[part - 1][i][threadIdx.x * 4], in[i]);
+            }
 #pragma unroll
-            for (int n = 0; n < HALF; ++n) ahead(tb + n, h[n], ea[n], n ? h[n - 1] : in);
+            for (int n = 0; n < PART; ++n) ahead(tb + n, h[n], ea[n], n ? h[n - 1] : in);
 #pragma unroll
-            for (int n = HALF - 1; n >= 0; --n) {
+            for (int n = PART - 1; n >= 0; --n) {
                 const int tok = tb + n;
                 const float2 d = *reinterpret_cast<const float2*>(&sm.delta[tok][cl]), x = *reinterpret_cast<const float2*>(&sm.dx[tok][cl]),
                              r = *reinterpret_cast<const float2*>(&sm.r[tok][cl]);
@@ -282,6 +303,22 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         for (int i = 0; i < kC; ++i)
 #pragma unroll
             for (int j = 0; j < kS / 2; ++j) G[i][j] = fma2(ex2_2(mul2(pk(sd[i], sd[i]), A[i][j])), Gin[i][j], Gl[i][j]);
+        if (tile > 0) load_keep(tile - 1);
+        // dA of four tiles at a time into the sum of all: a sum of few terms is added to one of many
+        if (on && tile % 4 == 0) {
+            const bool begun = tile / 4 != (tiles - 1) / 4;
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                f2 sum[kS / 2] = {0ull, 0ull};
+                if (begun) load4(part_p + so + i * N, m, sum);
+#pragma unroll
+                for (int j = 0; j < kS / 2; ++j) {
+                    sum[j] = add2(sum[j], dA[i][j]);
+                    dA[i][j] = 0ull;
+                }
+                store4(part_p + so + i * N, m, sum);
+            }
+        }
         __syncthreads();
         // (channels beyond the group's end have r = 0 and delta x = 0: they add nothing)
         for (int i = threadIdx.x; i < TT * 2 * N; i += NT) {
@@ -294,47 +331,48 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         }
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
-            if (t0 + tok >= s1 || c0 + vc >= c1) continue;
-            float x[VEC], dt[VEC], d[VEC], r[VEC], o[3][VEC];
-            vec(&sm.raw[stage][0][tok][vc], x);
-            vec(&sm.raw[stage][1][tok][vc], dt);
-            auto get = [&](const float* q, float (&f)[VEC]) { unpack(*reinterpret_cast<const Raw<float>::type*>(q), f); };
-            get(&sm.delta[tok][vc], d);
-            get(&sm.r[tok][vc], r);
+            if (t0 + tok >= s1 || !vin) continue;
+            f2 x[4], dt[4], d[4], r[4], bias[4], Dk[4], o[3][4];
+            states<8>(&sm.raw[stage][0][tok][vc], x);
+            states<8>(&sm.raw[stage][1][tok][vc], dt);
+            states<8>(&sm.delta[tok][vc], d);
+            states<8>(&sm.r[tok][vc], r);
+            params8(a.bias ? a.bias + c0 + vc : nullptr, true, bias);
+            params8(a.Dk ? a.Dk + c0 + vc : nullptr, true, Dk);
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-                get(&sm.part[k][0][tok * CB + vc], o[k]);
+                states<8>(&sm.part[k][0][tok * CB + vc], o[k]);
 #pragma unroll
                 for (int q = 1; q < Q; ++q) {
-                    float f[VEC];
-                    get(&sm.part[k][q][tok * CB + vc], f);
+                    f2 f[4];
+                    states<8>(&sm.part[k][q][tok * CB + vc], f);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) o[k][j] += f[j];
+                    for (int j = 0; j < 4; ++j) o[k][j] = add2(o[k][j], f[j]);
                 }
             }
             const size_t at = ((size_t)b * a.T + t0 + tok) * a.D + c0 + vc;
             if (zp) {
-                float z[VEC], dy[VEC];
-                vec(&sm.raw[stage][2][tok][vc], z);
-                vec(&sm.raw[stage][3][tok][vc], dy);
+                f2 z[4], dy[4];
+                states<8>(&sm.raw[stage][2][tok][vc], z);
+                states<8>(&sm.raw[stage][3][tok][vc], dy);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float s = sig(z[j]);
-                    z[j] = dy[j] * fmaf(shared(a.Dk, j), x[j], o[0][j]) * fmaf(z[j] * s, 1.f - s, s);
+                for (int j = 0; j < 4; ++j) {
+                    const f2 s = sig(z[j]), left = fma2(s, both(-1.f), both(1.f));
+                    z[j] = mul2(mul2(dy[j], fma2(Dk[j], x[j], o[0][j])), fma2(mul2(z[j], s), left, s));
                 }
-                save8(static_cast<E*>(a.dz) + at, z);
+                keep8(static_cast<E*>(a.dz) + at, z);
             }
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                sm.sums[0][j][threadIdx.x] += r[j] * x[j];
-                float ddt = fmaf(x[j], o[1][j], o[2][j] * kLn2);
-                if (a.softplus) ddt *= sig(dt[j] + shared(a.bias, j));
-                sm.sums[1][j][threadIdx.x] += ddt;
-                dt[j] = ddt;
-                x[j] = fmaf(d[j], o[1][j], shared(a.Dk, j) * r[j]);
+            for (int j = 0; j < 4; ++j) {
+                dD[j] = fma2(r[j], x[j], dD[j]);
+                f2 g = fma2(x[j], o[1][j], mul2(o[2][j], both(kLn2)));
+                if (a.softplus) g = mul2(g, sig(add2(dt[j], bias[j])));
+                db[j] = add2(db[j], g);
+                dt[j] = g;
+                x[j] = fma2(d[j], o[1][j], mul2(Dk[j], r[j]));
             }
-            save8(static_cast<E*>(a.dx) + at, x);
-            save8(static_cast<E*>(a.ddt) + at, dt);
+            keep8(static_cast<E*>(a.dx) + at, x);
+            keep8(static_cast<E*>(a.ddt) + at, dt);
         }
     }
 
@@ -342,22 +380,23 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
 #pragma unroll
         for (int i = 0; i < kC; ++i) store4(a.dS0 + b * per + so + i * N, m, G[i]);
     }
-    float* part = a.part_p + ((size_t)b * a.nseg + seg) * (per + 2 * (size_t)a.D);
-    if (on) {
-#pragma unroll
-        for (int i = 0; i < kC; ++i) store4(part + so + i * N, m, dA[i]);
-    }
     // dD and ddt_bias over the threads that finished the same channels, in order
+    __syncthreads();
+    constexpr int ROWS = (NT < VPT ? NT : VPT) / COLS;
+    if (threadIdx.x < ROWS * COLS) {
+        keep8(&sm.delta[0][0] + threadIdx.x / COLS * CB + vc, dD);
+        keep8(&sm.dx[0][0] + threadIdx.x / COLS * CB + vc, db);
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < CB; c += NT) {
         if (c0 + c >= c1) continue;
         float s = 0.f, q = 0.f;
-        for (int k = c / VEC; k < NT && k < VPT; k += COLS) {
-            s += sm.sums[0][c % VEC][k];
-            q += sm.sums[1][c % VEC][k];
+        for (int k = 0; k < ROWS; ++k) {
+            s += (&sm.delta[0][0])[k * CB + c];
+            q += (&sm.dx[0][0])[k * CB + c];
         }
-        part[per + c0 + c] = s;
-        part[per + a.D + c0 + c] = q;
+        part_p[per + c0 + c] = s;
+        part_p[per + a.D + c0 + c] = q;
     }
 }
 
