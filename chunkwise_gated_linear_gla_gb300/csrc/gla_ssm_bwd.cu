@@ -226,6 +226,52 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                 Gl[i][j] = pk(0.f, 0.f);
             }
         }
+        // dB, dC of a token over the warp's channels: the lanes with the same states (GROUPS of them) halve what they hold, giving
+        // away the second half of it: first pairs, then values, then B or C; lanes beyond that add up. It is done in three steps
+        // among the next token's products, whose waits they fill.
+        float vB[4], vC[4];
+        auto sum_begin = [&](const f2 (&dB)[kS / 2], const f2 (&dC)[kS / 2]) {
+            up(dB[0], vB[0], vB[1]); up(dB[1], vB[2], vB[3]);
+            up(dC[0], vC[0], vC[1]); up(dC[1], vC[2], vC[3]);
+            vB[2] = __shfl_xor_sync(~0u, vB[2], Q); vB[3] = __shfl_xor_sync(~0u, vB[3], Q);
+            vC[2] = __shfl_xor_sync(~0u, vC[2], Q); vC[3] = __shfl_xor_sync(~0u, vC[3], Q);
+        };
+        auto sum_middle = [&] {
+            vB[0] += vB[2]; vB[1] += vB[3]; vC[0] += vC[2]; vC[1] += vC[3];
+            if constexpr (GROUPS > 2) {
+                vB[1] = __shfl_xor_sync(~0u, vB[1], 2 * Q);
+                vC[1] = __shfl_xor_sync(~0u, vC[1], 2 * Q);
+            }
+        };
+        const bool isC = gi & 4;
+        auto sum_last = [&] {
+            if constexpr (GROUPS > 2) {
+                vB[0] += vB[1];
+                vC[0] += vC[1];
+                if constexpr (GROUPS > 4) vB[1] = __shfl_xor_sync(~0u, isC ? vB[0] : vC[0], 4 * Q);
+            }
+        };
+        auto sum_end = [&](int tok) {
+            float* red = &sm.red[warp][tok][sg * kS];
+            if constexpr (GROUPS == 2) {
+                red[m] = vB[0]; red[m ^ 1] = vB[1]; red[N + m] = vC[0]; red[N + (m ^ 1)] = vC[1];
+            } else if constexpr (GROUPS == 4) {
+                red[m] = vB[0]; red[N + m] = vC[0];
+            } else {
+                float v = (isC ? vC[0] : vB[0]) + vB[1];
+                if constexpr (GROUPS == 16) v += __shfl_xor_sync(~0u, v, 8 * Q);
+                if (GROUPS == 8 || gi < 8) red[(isC ? N : 0) + m] = v;
+            }
+        };
+        struct Token { float2 d, x, r; f2 B[kS / 2], C[kS / 2]; };
+        auto fetch = [&](int tok, Token& p) {
+            p.d = *reinterpret_cast<const float2*>(&sm.delta[tok][cl]);
+            p.x = *reinterpret_cast<const float2*>(&sm.dx[tok][cl]);
+            p.r = *reinterpret_cast<const float2*>(&sm.r[tok][cl]);
+            states<kS>(Bw + tok * N, p.B);
+            states<kS>(Cw + tok * N, p.C);
+        };
+        f2 dB[kS / 2], dC[kS / 2];
 #pragma unroll 1
         for (int part = TT / PART - 1; part >= 0; --part) {
             const int tb = part * PART;
@@ -238,66 +284,50 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
             }
 #pragma unroll
             for (int n = 0; n < PART; ++n) ahead(tb + n, h[n], ea[n], n ? h[n - 1] : in);
+            Token p[2];
+            fetch(tb + PART - 1, p[(PART - 1) % 2]);
 #pragma unroll
             for (int n = PART - 1; n >= 0; --n) {
                 const int tok = tb + n;
-                const float2 d = *reinterpret_cast<const float2*>(&sm.delta[tok][cl]), x = *reinterpret_cast<const float2*>(&sm.dx[tok][cl]),
-                             r = *reinterpret_cast<const float2*>(&sm.r[tok][cl]);
-                f2 Bv[kS / 2], Cv[kS / 2], dB[kS / 2], dC[kS / 2];
-                states<kS>(Bw + tok * N, Bv);
-                states<kS>(Cw + tok * N, Cv);
-                float2 out[3];                        // y, p, e of the two channels over this thread's states
+                const Token& t = p[n % 2];
+                if (n > 0) fetch(tok - 1, p[(n - 1) % 2]);
+                const bool before = n < PART - 1;              // the token after this one is of this part: its sums are due
+                if (before) sum_begin(dB, dC);
 #pragma unroll
                 for (int i = 0; i < kC; ++i) {
-                    const float di = i ? d.y : d.x;
-                    const f2 d2 = pk(di, di), x2 = i ? pk(x.y, x.y) : pk(x.x, x.x), r2 = i ? pk(r.y, r.y) : pk(r.x, r.x);
-                    f2 ys = pk(0.f, 0.f), ps = ys, es = ys;
+                    const float di = i ? t.d.y : t.d.x;
+                    const f2 d2 = both(di), x2 = both(i ? t.x.y : t.x.x), r2 = both(i ? t.r.y : t.r.x);
+                    f2 ys = 0ull, ps = 0ull, es = 0ull;
                     sd[i] += di;
 #pragma unroll
                     for (int j = 0; j < kS / 2; ++j) {
                         const f2 hp = n ? h[n - 1][i][j] : in[i][j];
-                        ys = fma2(h[n][i][j], Cv[j], ys);
+                        ys = fma2(h[n][i][j], t.C[j], ys);
                         dC[j] = i ? fma2(r2, h[n][i][j], dC[j]) : mul2(r2, h[n][i][j]);
-                        const f2 gg = fma2(r2, Cv[j], G[i][j]);
-                        Gl[i][j] = mul2(ea[n][i][j], fma2(r2, Cv[j], Gl[i][j]));
+                        const f2 gg = fma2(r2, t.C[j], G[i][j]);
+                        Gl[i][j] = mul2(ea[n][i][j], fma2(r2, t.C[j], Gl[i][j]));
                         dB[j] = i ? fma2(x2, gg, dB[j]) : mul2(x2, gg);
-                        ps = fma2(gg, Bv[j], ps);
+                        ps = fma2(gg, t.B[j], ps);
                         G[i][j] = mul2(ea[n][i][j], gg);      // what goes on to the token before
                         const f2 q = mul2(G[i][j], hp);
                         es = fma2(q, A[i][j], es);
                         dA[i][j] = fma2(q, d2, dA[i][j]);
                     }
-                    float u, v;
-                    up(ys, u, v); (i ? out[0].y : out[0].x) = u + v;
-                    up(ps, u, v); (i ? out[1].y : out[1].x) = u + v;
-                    up(es, u, v); (i ? out[2].y : out[2].x) = u + v;
-                }
-#pragma unroll
-                for (int k = 0; k < 3; ++k) *reinterpret_cast<float2*>(&sm.part[k][sg][tok * CB + cl]) = out[k];
-
-                // dB, dC over the warp's channels: the lanes with the same states (GROUPS of them) halve what they hold, giving
-                // away the second half of it: first pairs, then values, then B or C; lanes beyond that add up
-                float vB[4], vC[4];
-                up(dB[0], vB[0], vB[1]); up(dB[1], vB[2], vB[3]);
-                up(dC[0], vC[0], vC[1]); up(dC[1], vC[2], vC[3]);
-                vB[0] += __shfl_xor_sync(~0u, vB[2], Q); vB[1] += __shfl_xor_sync(~0u, vB[3], Q);
-                vC[0] += __shfl_xor_sync(~0u, vC[2], Q); vC[1] += __shfl_xor_sync(~0u, vC[3], Q);
-                float* red = &sm.red[warp][tok][sg * kS];
-                if constexpr (GROUPS == 2) {
-                    red[m] = vB[0]; red[m ^ 1] = vB[1]; red[N + m] = vC[0]; red[N + (m ^ 1)] = vC[1];
-                } else {
-                    vB[0] += __shfl_xor_sync(~0u, vB[1], 2 * Q);
-                    vC[0] += __shfl_xor_sync(~0u, vC[1], 2 * Q);
-                    if constexpr (GROUPS == 4) {
-                        red[m] = vB[0]; red[N + m] = vC[0];
-                    } else {
-                        const bool isC = gi & 4;
-                        float v = (isC ? vC[0] : vB[0]) + __shfl_xor_sync(~0u, isC ? vB[0] : vC[0], 4 * Q);
-                        if constexpr (GROUPS == 16) v += __shfl_xor_sync(~0u, v, 8 * Q);
-                        if (GROUPS == 8 || gi < 8) red[(isC ? N : 0) + m] = v;
+                    if (before) {
+                        if (i == 0) sum_middle();
+                        else sum_last();
                     }
+                    // y, p, e of the channel over this thread's states
+                    sm.part[0][sg][tok * CB + cl + i] = sum2(ys);
+                    sm.part[1][sg][tok * CB + cl + i] = sum2(ps);
+                    sm.part[2][sg][tok * CB + cl + i] = sum2(es);
                 }
+                if (before) sum_end(tok + 1);
             }
+            sum_begin(dB, dC);
+            sum_middle();
+            sum_last();
+            sum_end(tb);
         }
 #pragma unroll
         for (int i = 0; i < kC; ++i)
