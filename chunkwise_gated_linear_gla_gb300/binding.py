@@ -1119,21 +1119,28 @@ def _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments=0):
     import torch
     if x.dim() != 3 or B.dim() != 4 or A.dim() != 2:
         _refuse("x has three dimensions [B,T,D], B and C four [B,T,G,N], A two [D,N]")
-    nb, T, nd = x.shape
-    G, N = B.shape[2:]
-    t, dev, f32 = x.dtype, x.device, torch.float32
+    shape, groups, t, dev, f32 = x.shape, B.shape, x.dtype, x.device, torch.float32
+    nb, T, nd = shape
+    G, N = groups[2:]
     code = _dtype_code(x, "x")
     if G == 0 or nd % G:
         _refuse(f"{nd} channels do not divide over {G} groups of B and C")
-    _rows(x, (nb, T, nd), t, dev, "x")
-    _rows(dt, (nb, T, nd), t, dev, "dt")
-    if z is not None:
-        _rows(z, (nb, T, nd), t, dev, "z")
-    for m, what in ((B, "B"), (C, "C")):
-        _rows(m, (nb, T, G, N), t, dev, what)
-        if G > 1 and m.stride(2) != N:
-            _refuse(f"the groups of {what} do not lie side by side")
-    _dense(A, (nd, N), f32, dev, "A")
+    sx, sd, sB, sC, sz = x.stride(), dt.stride(), B.stride(), C.stride(), (0, 0, 1) if z is None else z.stride()
+    # one look at everything; what is wrong is told below
+    if not (dt.shape == shape and dt.dtype is t and dt.device == dev and groups == (nb, T, G, N) and B.dtype is t and
+            B.device == dev and C.shape == groups and C.dtype is t and C.device == dev and
+            (z is None or z.shape == shape and z.dtype is t and z.device == dev) and
+            sx[2] == sd[2] == sB[3] == sC[3] == sz[2] == 1 and (G == 1 or sB[2] == sC[2] == N) and
+            A.shape == (nd, N) and A.dtype is f32 and A.device == dev and A.is_contiguous()):
+        _rows(x, (nb, T, nd), t, dev, "x")
+        _rows(dt, (nb, T, nd), t, dev, "dt")
+        if z is not None:
+            _rows(z, (nb, T, nd), t, dev, "z")
+        for m, what in ((B, "B"), (C, "C")):
+            _rows(m, (nb, T, G, N), t, dev, what)
+            if G > 1 and m.stride(2) != N:
+                _refuse(f"the groups of {what} do not lie side by side")
+        _dense(A, (nd, N), f32, dev, "A")
     if D is not None:
         _dense(D, (nd,), f32, dev, "D")
     if dt_bias is not None:
@@ -1143,10 +1150,13 @@ def _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments=0):
     _on_gpu(x, "x")
     if nb == 0:
         _refuse("an empty batch")
-    steps = lambda m: _Steps2(0, 0) if m is None else _Steps2(m.stride(0) if nb > 1 else 0, m.stride(1) if T > 1 else 0)  # noqa: E731
-    return gla_ssm_params(_ptr(x), _ptr(dt), _ptr(z), _ptr(B), _ptr(C), steps(x), steps(dt), steps(z), steps(B), steps(C),
-                          _ptr(A), _ptr(D), _ptr(dt_bias), _ptr(S0), nb, T, nd, G, N, 1 if softplus else 0, code,
-                          force_segments)
+    # strides of dimensions of one are never stepped and count as 0
+    if nb > 1 and T > 1:
+        steps = [_Steps2(s[0], s[1]) for s in (sx, sd, sz, sB, sC)]
+    else:
+        steps = [_Steps2(s[0] if nb > 1 else 0, s[1] if T > 1 else 0) for s in (sx, sd, sz, sB, sC)]
+    return gla_ssm_params(_ptr(x), _ptr(dt), _ptr(z), _ptr(B), _ptr(C), *steps, _ptr(A), _ptr(D), _ptr(dt_bias), _ptr(S0),
+                          nb, T, nd, G, N, 1 if softplus else 0, code, force_segments)
 
 
 def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, softplus=True, want_state=True,

@@ -42,7 +42,7 @@ enum SsmMode {
     kSsmRev = 3,      // backwards: the gradient of the state before the segment, from zero (all but the first)
 };
 
-cudaError_t launch_ssm_step(const SsmArgs& a, gla_dtype dtype, cudaStream_t s);
+cudaError_t launch_ssm_step(const SsmArgs& a, gla_dtype dtype, int sms, cudaStream_t s);
 cudaError_t launch_ssm_walk(const SsmArgs& a, int mode, gla_dtype dtype, cudaStream_t s);
 // The states entering the segments from each segment's own, in place; `rev`: from the last, into segG.
 cudaError_t launch_ssm_scan(const SsmArgs& a, bool rev, int sms, cudaStream_t s);

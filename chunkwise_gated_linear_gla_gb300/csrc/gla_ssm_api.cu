@@ -152,7 +152,7 @@ gla_status gla_ssm_fwd(const gla_ssm_params* p, void* y, float* ST, void* worksp
     if (!step && pl.ws > 0 && (!workspace || workspace_bytes < pl.ws)) return GLA_ERR_WORKSPACE;
     SsmArgs a = common(p, pl, workspace);
     a.y = y; a.ST = ST;
-    if (step) return cuda(launch_ssm_step(a, p->dtype, stream));
+    if (step) return cuda(launch_ssm_step(a, p->dtype, sms, stream));
     cudaError_t r = cudaSuccess;
     if (pl.nseg > 1) {
         r = launch_ssm_walk(a, kSsmState, p->dtype, stream);
