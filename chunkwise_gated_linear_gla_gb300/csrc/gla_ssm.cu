@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArg
 #pragma unroll 1
         for (int sub = 0; sub < TT; sub += SUB) {
             const int base = REV ? TT - SUB - sub : sub;
-            if (MODE == kSsmKeep && on && t0 + base < s1) {
+            if (t0 + base >= s1) continue;                 // (a segment's last tile may hold one of the two)
+            if (MODE == kSsmKeep && on) {
                 float* k = a.keep + ((size_t)b * ((a.T + SUB - 1) / SUB) + (t0 + base) / SUB) * per + so;
 #pragma unroll
                 for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(k + 2 * j) = make_ulonglong2(h[j], h[j + 1]);
@@ -392,6 +393,7 @@ cudaError_t step(const SsmArgs& a, int sms, cudaStream_t s)
 
 }  // namespace
 
+int ssm_walk_warps(int N) { return N >= 64 ? kWalkWarps<64> : kWalkWarps<8>; }
 int ssm_walk_channels(int N) { return N == 8 ? kWalkChannels<8> : N == 16 ? kWalkChannels<16> : N == 32 ? kWalkChannels<32> : kWalkChannels<64>; }
 
 cudaError_t launch_ssm_step(const SsmArgs& a, gla_dtype dtype, int sms, cudaStream_t s)

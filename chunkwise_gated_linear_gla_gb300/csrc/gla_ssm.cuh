@@ -50,6 +50,7 @@ cudaError_t launch_ssm_bwd(const SsmArgs& a, gla_dtype dtype, cudaStream_t s);
 cudaError_t launch_ssm_bc_sum(const SsmArgs& a, void* dB, void* dC, gla_dtype dtype, int sms, cudaStream_t s);
 int ssm_walk_channels(int N);     // channels per block of the walk, and of the backward
 int ssm_bwd_channels(int N);
+int ssm_walk_warps(int N);
 
 #ifdef __CUDACC__
 

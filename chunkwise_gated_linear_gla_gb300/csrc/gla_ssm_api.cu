@@ -38,10 +38,14 @@ struct SsmPlan {
     size_t off_sumd = 0, off_segG = 0, off_keep = 0, off_bc = 0, off_p = 0, ws = 0;
 };
 
-// Segments of the sequence. A walk takes 0.11 us a token of 32 with up to 1.5 warps on a scheduler, 0.2 with the 3.4 that its
-// registers and shared memory admit; cut, it is walked twice. So a walk that fills a fourth of the places or less is cut
-// into as many segments as fill them (one row of 16421 tokens of 4096 channels: uncut 1850 us, XX in eight). The backward's blocks
-// take two places of an SM and the walks are a small part of it: it is cut as soon as two segments fit.
+// Segments of the sequence. A walk is serial over its tokens, so few blocks leave SMs idle; cut, they fill the chip evenly, but
+// the tokens are walked twice (backward: three times more in part). Uncut, a walk of up to 1.7 blocks an SM takes 0.09 us a token, 0.115 at
+// 2.5, 0.12 at 3.4; cut so that there are twenty blocks an SM in all, 2.8e-4 us a block: equal at 2.6 an SM (rows of
+// 4096 channels of 16 states, caches flushed: one of 16421 tokens 1450 us uncut, 641 in 8 segments, 600 in 23; three of 4096 472
+// uncut, 428 in 8). The backward's larger blocks take 0.37 us a token up to one an SM and 0.51 up to two, and 2.2e-3 us each when
+// cut so that there are seven an SM: equal at 1.5 an SM (one row of 2048 tokens 761 us uncut, 334 in 16; two 766 and 598). Segments
+// are four tiles or more (two rows of 2048 tokens of 1536 channels of 8 states: 62 us in 32 segments, 73 in 64), two where the chip
+// is not filled otherwise (one row of 256 tokens of 1024 channels: 26 us uncut, 14 in 8, 17 in 16).
 void split(const gla_ssm_params* p, int sms, bool bwd, SsmPlan& pl)
 {
     const int CB = bwd ? ssm_bwd_channels(p->N) : ssm_walk_channels(p->N);
@@ -49,14 +53,16 @@ void split(const gla_ssm_params* p, int sms, bool bwd, SsmPlan& pl)
     const long long tiles = ((long long)p->T + kSsmTile - 1) / kSsmTile;
     long long n = p->force_segments;
     if (n == 0) {
-        n = (bwd ? 2LL : 7LL) * sms / blocks;
-        if (n < (bwd ? 2 : 4)) n = 1;
-        if (n > tiles / 4) n = tiles / 4;
+        const long long units = bwd ? blocks : blocks * ssm_walk_warps(p->N) / 2;    // (blocks of two warps)
+        n = 10 * units < (bwd ? 15LL : 26LL) * sms ? (bwd ? 7LL : 20LL) * sms / units : 1;
+        const long long filled = 7LL * sms / units, most = tiles / 2 < filled ? tiles / 2 : filled;
+        if (n > tiles / 4) n = most > tiles / 4 ? most : tiles / 4;
     }
     if (n > kMaxSegments) n = kMaxSegments;
     if (n > tiles) n = tiles;
     if (n < 1) n = 1;
-    const long long per = (tiles + n - 1) / n;
+    long long per = (tiles + n - 1) / n;
+    if (per > 1 && per < tiles) per += per % 2;      // (the walks load two tiles at a time)
     pl.nseg = per > 0 ? (int)((tiles + per - 1) / per) : 1;
     if (pl.nseg < 1) pl.nseg = 1;
     pl.seg = per > 0 ? (int)(per * kSsmTile) : kSsmTile;
