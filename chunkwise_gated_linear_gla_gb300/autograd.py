@@ -309,7 +309,7 @@ def norm_gate(x, gate=None, w=None, norm="rms", eps=1e-6, activation="silu", gat
 def residual_norm(x, residual=None, w=None, scale=None, post_norm=False, eps=1e-6):
     """(h, y) of binding.residual_norm_forward, differentiable once in x, residual, w and a scale that is a tensor, in
     reverse mode."""
-    if _plain(x, residual, w, None if isinstance(scale, (int, float)) else scale):
+    if _plain(x, residual, w, scale if hasattr(scale, "requires_grad") else None):
         return _b.residual_norm_forward(x, residual, w, scale, post_norm, eps)
     global _RESIDUAL
     if _RESIDUAL is None:

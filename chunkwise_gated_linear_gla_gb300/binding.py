@@ -1063,7 +1063,7 @@ def causal_conv_forward(x, w, bias=None, S0=None, activation="silu", want_state=
     """The short causal convolution of every channel (gla_conv_fwd), outputs from torch.
 
     x [B,T,D] or, head by head, [B,H,T,d] (bf16 or fp32; strided views, the last dimension contiguous and every row from a
-    16-byte boundary); w fp32 [D,W] with D = H d and W 2 to 4, bias fp32 [D] or None; S0 [B,W-1,D] in x's type, the W - 1
+    16-byte boundary; d, or D, a multiple of 16); w fp32 [D,W] with D = H d and W 2 to 4, bias fp32 [D] or None; S0 [B,W-1,D] in x's type, the W - 1
     rows before the first token, oldest first, or None (zeros); activation "silu" or None. Returns (y, ST): y dense in
     x's shape, ST the last W - 1 rows of (S0, x) (None unless wanted). A decoding loop passes ST=S0 to carry the state
     in place; y and ST count as modified in place. A batch of unequal prompts is padded in front, with zeros.

@@ -250,6 +250,81 @@ def test_other_streams_and_two_at_once():
         assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+@pytest.mark.gpu
+def test_rows_beyond_32_bits():
+    """Rows 2^30 values apart in one tensor of 2^33 bytes: offsets pass 2^31 elements and 2^32 bytes."""
+    T, far = 4, 1 << 30
+    store = torch.empty(T * far, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(11)
+    rows = torch.randn(T, 256, generator=g).bfloat16().cuda()
+    wide = store.as_strided((T, 256), (far, 1))
+    wide.copy_(rows)
+    x, near = wide.unsqueeze(0), rows.unsqueeze(0)
+    w = torch.randn(256, 4, generator=g).cuda()
+    dy = torch.randn(1, T, 256, generator=g).bfloat16().cuda()
+    for a, b in ((gla.causal_conv(x, w), gla.causal_conv(near, w)),
+                 (gla.causal_conv_backward(x, w, None, None, dy), gla.causal_conv_backward(near, w, None, None, dy))):
+        assert all(p is q or torch.equal(p, q) for p, q in zip(a, b))
+    heads = lambda t: t.unflatten(2, (2, 128)).transpose(1, 2)  # noqa: E731
+    dg = dy.unflatten(2, (2, 128)).contiguous()
+    assert torch.equal(gla.norm_gate(heads(x), heads(x)), gla.norm_gate(heads(near), heads(near)))
+    for p, q in zip(gla.norm_gate_backward(heads(x), heads(x), None, dg), gla.norm_gate_backward(heads(near), heads(near), None, dg)):
+        assert p is q or torch.equal(p, q)
+    A, S0 = -torch.rand(64, 16, generator=g).cuda(), torch.randn(1, 64, 16, generator=g).cuda()
+    cut = lambda t: (t[..., :64], t[..., 64:128], A, t[..., 128:144].unflatten(2, (1, 16)), t[..., 144:160].unflatten(2, (1, 16)), None,  # noqa: E731
+                     t[..., 160:224], None, S0)
+    for kw in ({}, {"force_segments": 1}):
+        assert all(torch.equal(p, q) for p, q in zip(gla.selective_scan_forward(*cut(x), **kw), gla.selective_scan_forward(*cut(near), **kw)))
+    d = dy[..., :64].contiguous()
+    for p, q in zip(gla.selective_scan_backward(*cut(x), d), gla.selective_scan_backward(*cut(near), d)):
+        assert p is q or torch.equal(p, q)
+
+
+@pytest.mark.gpu
+def test_long_tensors_pass_32_bits():
+    """2^31 + values in one dense tensor: the last rows against the same rows alone."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    T, D = (1 << 20) + 40, 2048
+    x = torch.randn(64, D, generator=g, device="cuda").bfloat16().repeat((T + 63) // 64, 1)[:T]
+    w, tail = torch.randn(D, 4, generator=g, device="cuda"), slice(T - 70, T)
+    y, ST = gla.causal_conv(x.unsqueeze(0), w)
+    y2, ST2 = gla.causal_conv(x[tail].unsqueeze(0), w, S0=x[T - 73:T - 70].unsqueeze(0).contiguous())
+    assert torch.equal(y[0, tail], y2[0]) and torch.equal(ST, ST2)
+    del y, y2
+    h, n = gla.residual_norm(x, x, w[:, 0].contiguous())
+    h2, n2 = gla.residual_norm(x[tail].contiguous(), x[tail].contiguous(), w[:, 0].contiguous())
+    assert torch.equal(h[tail], h2) and torch.equal(n[tail], n2)
+    del h, n
+    v = x.unflatten(1, (16, 128)).transpose(0, 1).unsqueeze(0)
+    y = gla.norm_gate(v, v)
+    assert torch.equal(y[0, tail], gla.norm_gate(v[:, :, tail], v[:, :, tail])[0])
+    del y
+    # a step of a decay that forgets: the last tokens of a long scan are those of a short one
+    args = lambda t: (t, t, torch.full((D, 8), -8.0, device="cuda"), t[..., :8].unsqueeze(2), t[..., 8:16].unsqueeze(2))  # noqa: E731
+    y, S = gla.selective_scan(*args(x.unsqueeze(0)))
+    y2, S2 = gla.selective_scan(*args(x[T - 320:].unsqueeze(0)))
+    assert torch.allclose(S, S2, rtol=1e-4, atol=1e-4) and torch.allclose(y[0, tail].float(), y2[0, -70:].float(), rtol=2.0 ** -7, atol=1e-3)
+
+
+@pytest.mark.gpu
+def test_gradients_of_broadcast_inputs():
+    """B and C of one row for the whole batch, a gate and a convolved row shared by all tokens: their gradients are the sums."""
+    t, w, x4 = _scan_inputs(40, 10), torch.randn(64, 4, device="cuda"), torch.randn(2, 2, 40, 64, device="cuda")
+    one = {n: t[n][:1].detach().requires_grad_(True) for n in ("B", "C")}
+    full = {n: a.detach().expand(2, -1, -1, -1).contiguous().requires_grad_(True) for n, a in one.items()}
+    dy = torch.randn(2, 40, 64, device="cuda")
+    a = torch.autograd.grad(gla.selective_scan(**{**t, **{n: b.expand(2, -1, -1, -1) for n, b in one.items()}})[0], list(one.values()), dy)
+    b = torch.autograd.grad(gla.selective_scan(**{**t, **full})[0], list(full.values()), dy)
+    for p, q in zip(a, b):
+        assert torch.allclose(p, q.sum(0, keepdim=True), rtol=1e-5, atol=1e-5)
+    g1 = torch.randn(2, 2, 1, 64, device="cuda", requires_grad=True)
+    g2 = g1.detach().expand(2, 2, 40, 64).contiguous().requires_grad_(True)
+    do = torch.randn(2, 40, 2, 64, device="cuda")
+    p, = torch.autograd.grad(gla.norm_gate(x4, g1.expand(2, 2, 40, 64)), g1, do)
+    q, = torch.autograd.grad(gla.norm_gate(x4, g2), g2, do)
+    assert torch.allclose(p, q.sum(2, keepdim=True), rtol=1e-5, atol=1e-4)
+
+
 # ---------------------------------------------------------------- no GPU needed
 
 def test_given_outputs_that_require_grad_are_refused():
