@@ -101,7 +101,7 @@ template <int N> constexpr int kWalkChannels = kWalkWarps<N> * 32 * kS / N;
 
 template <typename E, int N, int MODE>
 struct WalkShared {
-    static constexpr int CB = kWalkChannels<N>, Q = N / kS;
+    static constexpr int CB = kWalkChannels<N>;
     static constexpr bool HAS_B = MODE != kSsmRev, HAS_C = MODE == kSsmOut || MODE == kSsmRev, HAS_Z = HAS_C;
     E raw[2][HAS_Z ? 3 : 2][kWalkTile][CB];   // x, dt, z (REV: dy, dt, z)
     E bc[2][HAS_B + HAS_C][kWalkTile][N];
@@ -211,10 +211,11 @@ __global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArg
             keep8(&sm.work[1][tok * P + vc], x);
         }
         __syncthreads();
+        // (a segment's last tile may hold one of the two parts)
+        const int parts = t0 + SUB < s1 ? TT : SUB;
 #pragma unroll 1
-        for (int sub = 0; sub < TT; sub += SUB) {
+        for (int sub = REV ? TT - parts : 0; sub < (REV ? TT : parts); sub += SUB) {
             const int base = REV ? TT - SUB - sub : sub;
-            if (t0 + base >= s1) continue;                 // (a segment's last tile may hold one of the two)
             if (MODE == kSsmKeep && on) {
                 float* k = a.keep + ((size_t)b * ((a.T + SUB - 1) / SUB) + (t0 + base) / SUB) * per + so;
 #pragma unroll

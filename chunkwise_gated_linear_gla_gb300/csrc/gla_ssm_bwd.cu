@@ -37,8 +37,12 @@ struct BwdShared {
     E raw[2][4][TT][CB];                      // x, dt, z, dy
     E bc[2][2][TT][N];
     float wide[2][kOrders][TT * N + 16];      // B, C
-    // the states entering the tile, and its parts but the first and the last, as each thread reads them
-    float keep[kC][NT * 4], mid[TT / PART - 2][kC][NT * 4];
+    // the states entering the tile (two tiles' in turn), and its parts but the first and the last, as each thread reads them
+    float keep[2][kC][NT * 4], mid[TT / PART - 2][kC][NT * 4];
+    // Rows of a value per channel: the first four of every eight channels, then the other four, with the eights 0 - 3 and 4 - 7
+    // exchanged. So a thread's eight channels are two reads of 16 bytes beside its neighbours', and a warp's channels, two
+    // neighbouring eights, still meet every bank once.
+    static constexpr int HALF = CB / 2, TURN = CB >= 64 ? 4 : 0;
     float delta[TT][CB], dx[TT][CB], r[TT][CB];
     float part[3][Q][TT * CB + 16];           // y, p, e over each thread's states
     float red[kWarps][TT][2 * N];             // dB, dC over each warp's channels
@@ -69,9 +73,10 @@ __device__ __forceinline__ void store4(float* p, int m, const f2 (&r)[2])
 template <typename E, int N>
 __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
 {
-    constexpr int CB = kBwdChannels<N>, Q = N / kS, GROUPS = 32 / Q;
+    typedef BwdShared<E, N> Shared;
+    constexpr int CB = kBwdChannels<N>, Q = N / kS, GROUPS = 32 / Q, HALF = Shared::HALF, TURN = Shared::TURN;
     extern __shared__ __align__(16) char smem_raw[];
-    auto& sm = *reinterpret_cast<BwdShared<E, N>*>(smem_raw);
+    auto& sm = *reinterpret_cast<Shared*>(smem_raw);
     const int Dg = a.D / a.G, ct = blockIdx.x % a.ctiles;
     const long long bg = blockIdx.x / a.ctiles;
     const int b = (int)(bg / a.G), g = (int)(bg % a.G);
@@ -103,20 +108,13 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         cy.go(&sm.raw[stage][3][0][0], s1, -TT);
         cB.go(&sm.bc[stage][0][0][0], s1, -TT);
         cC.go(&sm.bc[stage][1][0][0], s1, -TT);
-        copies_end();
-    };
-    // the state entering a tile: each thread copies what it reads itself
-    auto load_keep = [&](int tile) {
+        // (each thread copies the states that it reads itself)
 #pragma unroll
         for (int i = 0; i < kC; ++i)
-            copy16(&sm.keep[i][threadIdx.x * 4], a.keep + ((size_t)b * alltiles + s0 / TT + tile) * per + so + (on ? i * N : 0), true);
+            copy16(&sm.keep[stage][i][threadIdx.x * 4], a.keep + ((size_t)b * alltiles + s0 / TT + tile) * per + so + (on ? i * N : 0), true);
         copies_end();
     };
-
-    if (tiles > 0) {
-        load(tiles - 1);
-        load_keep(tiles - 1);
-    }
+    if (tiles > 0) load(tiles - 1);
 
     f2 A[kC][kS / 2], G[kC][kS / 2], dA[kC][kS / 2];
     const float* gfrom = seg < a.nseg - 1 ? a.segG + ((size_t)b * (a.nseg - 1) + seg) * per : a.dST ? a.dST + b * per : nullptr;
@@ -138,6 +136,19 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
     // this block's sums of dA, dD and ddt_bias
     float* const part_p = a.part_p + ((size_t)b * a.nseg + seg) * (per + 2 * (size_t)a.D);
     const bool vin = c0 + vc < c1;
+    // a thread's eight channels of a row, and its pair's place
+    auto put8 = [&](float* row, const f2 (&v)[4]) {
+        *reinterpret_cast<ulonglong2*>(row + vc / 2) = make_ulonglong2(v[0], v[1]);
+        *reinterpret_cast<ulonglong2*>(row + HALF + (vc / 2 ^ 4 * TURN)) = make_ulonglong2(v[2], v[3]);
+    };
+    auto get8 = [&](const float* row, f2 (&v)[4]) {
+        const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(row + vc / 2), q = *reinterpret_cast<const ulonglong2*>(row + HALF + (vc / 2 ^ 4 * TURN));
+        v[0] = p.x; v[1] = p.y; v[2] = q.x; v[3] = q.y;
+    };
+    const int cp = cl & 4 ? HALF + ((cl >> 3 ^ TURN) * 4) + (cl & 3) : (cl >> 3) * 4 + (cl & 3);
+    f2 bias[4], Dk[4];
+    params8(a.bias ? a.bias + c0 + vc : nullptr, vin, bias);
+    params8(a.Dk ? a.Dk + c0 + vc : nullptr, vin, Dk);
 
     for (int tile = tiles - 1; tile >= 0; --tile) {
         const int stage = tile & 1, t0 = s0 + tile * TT;
@@ -157,11 +168,10 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         }
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
-            f2 x[4], d[4], r[4], bias[4];
+            f2 x[4], d[4], r[4];
             states<8>(&sm.raw[stage][0][tok][vc], x);
             states<8>(&sm.raw[stage][1][tok][vc], d);
             states<8>(&sm.raw[stage][3][tok][vc], r);
-            params8(a.bias ? a.bias + c0 + vc : nullptr, vin, bias);
             if (zp) {
                 f2 z[4];
                 states<8>(&sm.raw[stage][2][tok][vc], z);
@@ -176,9 +186,9 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                 if (!ok) d[j] = 0ull;
                 x[j] = mul2(x[j], d[j]);
             }
-            keep8(&sm.delta[tok][vc], d);
-            keep8(&sm.dx[tok][vc], x);
-            keep8(&sm.r[tok][vc], r);
+            put8(sm.delta[tok], d);
+            put8(sm.dx[tok], x);
+            put8(sm.r[tok], r);
         }
         __syncthreads();
 
@@ -188,7 +198,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         const float* Bw = &sm.wide[0][slot][sg * kS];
         const float* Cw = &sm.wide[1][slot][sg * kS];
         auto ahead = [&](int tok, f2 (&hn)[kC][kS / 2], f2 (&an)[kC][kS / 2], const f2 (&hp)[kC][kS / 2]) {
-            const float2 d = *reinterpret_cast<const float2*>(&sm.delta[tok][cl]), x = *reinterpret_cast<const float2*>(&sm.dx[tok][cl]);
+            const float2 d = *reinterpret_cast<const float2*>(&sm.delta[tok][cp]), x = *reinterpret_cast<const float2*>(&sm.dx[tok][cp]);
             f2 Bv[kS / 2];
             states<kS>(Bw + tok * N, Bv);
 #pragma unroll
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         // the states entering the tile's parts; the first of them is the one that was kept, the last stays in registers
         f2 in[kC][kS / 2];
 #pragma unroll
-        for (int i = 0; i < kC; ++i) load4(&sm.keep[i][threadIdx.x * 4], m, in[i]);
+        for (int i = 0; i < kC; ++i) load4(&sm.keep[stage][i][threadIdx.x * 4], m, in[i]);
 #pragma unroll 1
         for (int part = 0; part < TT / PART - 1; ++part) {
             if (part > 0)
@@ -265,9 +275,9 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         };
         struct Token { float2 d, x, r; f2 B[kS / 2], C[kS / 2]; };
         auto fetch = [&](int tok, Token& p) {
-            p.d = *reinterpret_cast<const float2*>(&sm.delta[tok][cl]);
-            p.x = *reinterpret_cast<const float2*>(&sm.dx[tok][cl]);
-            p.r = *reinterpret_cast<const float2*>(&sm.r[tok][cl]);
+            p.d = *reinterpret_cast<const float2*>(&sm.delta[tok][cp]);
+            p.x = *reinterpret_cast<const float2*>(&sm.dx[tok][cp]);
+            p.r = *reinterpret_cast<const float2*>(&sm.r[tok][cp]);
             states<kS>(Bw + tok * N, p.B);
             states<kS>(Cw + tok * N, p.C);
         };
@@ -277,7 +287,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
             const int tb = part * PART;
             if (part == 0) {
 #pragma unroll
-                for (int i = 0; i < kC; ++i) load4(&sm.keep[i][threadIdx.x * 4], m, in[i]);
+                for (int i = 0; i < kC; ++i) load4(&sm.keep[stage][i][threadIdx.x * 4], m, in[i]);
             } else if (part < TT / PART - 1) {
 #pragma unroll
                 for (int i = 0; i < kC; ++i) states<kS>(&sm.mid[part - 1][i][threadIdx.x * 4], in[i]);
@@ -318,9 +328,9 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                         else sum_last();
                     }
                     // y, p, e of the channel over this thread's states
-                    sm.part[0][sg][tok * CB + cl + i] = sum2(ys);
-                    sm.part[1][sg][tok * CB + cl + i] = sum2(ps);
-                    sm.part[2][sg][tok * CB + cl + i] = sum2(es);
+                    sm.part[0][sg][tok * CB + cp + i] = sum2(ys);
+                    sm.part[1][sg][tok * CB + cp + i] = sum2(ps);
+                    sm.part[2][sg][tok * CB + cp + i] = sum2(es);
                 }
                 if (before) sum_end(tok + 1);
             }
@@ -333,7 +343,6 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         for (int i = 0; i < kC; ++i)
 #pragma unroll
             for (int j = 0; j < kS / 2; ++j) G[i][j] = fma2(ex2_2(mul2(pk(sd[i], sd[i]), A[i][j])), Gin[i][j], Gl[i][j]);
-        if (tile > 0) load_keep(tile - 1);
         // dA of four tiles at a time into the sum of all: a sum of few terms is added to one of many
         if (on && tile % 4 == 0) {
             const bool begun = tile / 4 != (tiles - 1) / 4;
@@ -362,20 +371,18 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
             if (t0 + tok >= s1 || !vin) continue;
-            f2 x[4], dt[4], d[4], r[4], bias[4], Dk[4], o[3][4];
+            f2 x[4], dt[4], d[4], r[4], o[3][4];
             states<8>(&sm.raw[stage][0][tok][vc], x);
             states<8>(&sm.raw[stage][1][tok][vc], dt);
-            states<8>(&sm.delta[tok][vc], d);
-            states<8>(&sm.r[tok][vc], r);
-            params8(a.bias ? a.bias + c0 + vc : nullptr, true, bias);
-            params8(a.Dk ? a.Dk + c0 + vc : nullptr, true, Dk);
+            get8(sm.delta[tok], d);
+            get8(sm.r[tok], r);
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-                states<8>(&sm.part[k][0][tok * CB + vc], o[k]);
+                get8(&sm.part[k][0][tok * CB], o[k]);
 #pragma unroll
                 for (int q = 1; q < Q; ++q) {
                     f2 f[4];
-                    states<8>(&sm.part[k][q][tok * CB + vc], f);
+                    get8(&sm.part[k][q][tok * CB], f);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[k][j] = add2(o[k][j], f[j]);
                 }
