@@ -49,9 +49,9 @@ __device__ __forceinline__ f2 act_of(f2 g, int silu, f2& slope)
 }
 
 template <typename E, int LPR, int K, bool BWD, bool FIRST>
-__global__ void __launch_bounds__(NT, K > 2 ? 1 : K > 1 || BWD ? 2 : 4) gla_norm_gate_kernel(GateArgs a)
+__global__ void __launch_bounds__(NT, K > 2 ? 1 : BWD || K > 1 ? 2 : 4) gla_norm_gate_kernel(GateArgs a)
 {
-    constexpr int RPB = NT / LPR, U = BWD || K > 1 ? 1 : 2;
+    constexpr int RPB = NT / LPR, U = BWD || K > 2 ? 1 : 2;
     __shared__ __align__(16) float red[BWD ? RPB : 1][BWD ? LPR * K * VEC : 4];
     const int l = threadIdx.x % LPR, row = threadIdx.x / LPR;
     f2 w[K][4], dw[K][4];
@@ -183,12 +183,13 @@ __global__ void __launch_bounds__(NT, K > 2 ? 1 : K > 1 || BWD ? 2 : 4) gla_norm
     }
 }
 
-// The heads are spread over blocks until every SM has its eight; backward: as many blocks as are resident, few partials.
+// The heads are spread over blocks until every SM has three (3 x 1531 tokens of 4 heads of 512: 13.7 us, with eight 27.7: a thread then has one
+// head, not the two whose loads it can have in flight); backward: as many blocks as are resident, few partials.
 dim3 grid_of(GateArgs& a, int sms, bool bwd)
 {
     const int lpr = a.d <= 64 ? 8 : a.d <= 128 ? 16 : 32, rows = NT / lpr;
     const long long tg = (a.tokens + rows - 1) / rows;
-    const long long want = (bwd ? 2LL : 8LL) * sms;
+    const long long want = (bwd ? 2LL : 3LL) * sms;
     int split = 1;
     while (split < a.H && tg * split < want) split *= 2;
     if (split > a.H) split = a.H;
