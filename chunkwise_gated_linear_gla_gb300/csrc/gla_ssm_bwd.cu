@@ -447,6 +447,7 @@ __global__ void gla_ssm_bc_sum_kernel(const float* part, long long rows, int N, 
         const long long row = i / q;
         const int k = (int)(i - row * q) * 4;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
         for (int c = 0; c < ctiles; ++c) {
             const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)c * rows + row) * (2 * N) + k);
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
