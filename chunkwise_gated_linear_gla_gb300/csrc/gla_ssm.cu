@@ -94,14 +94,16 @@ __global__ void __launch_bounds__(kStepNT) gla_ssm_step_kernel(SsmArgs a)
 
 // ------------------------------------------------------------------ the walk
 
-constexpr int kS = 8;              // states of a thread
 constexpr int kWalkTile = 32;      // tokens per tile of loads: two of the kept states' tiles
-template <int N> constexpr int kWalkWarps = N >= 64 ? 4 : 2;
-template <int N> constexpr int kWalkChannels = kWalkWarps<N> * 32 * kS / N;
+// States of a thread: B and C are read once for eight. The walk that keeps states runs uncut with the few blocks of a training batch, where
+// more warps count for more (4 x 2048 tokens of 4096 channels of 16 states: 157 us with four, 171 with eight).
+template <int MODE> constexpr int kStates = MODE == kSsmKeep ? 4 : 8;
+template <int N, int MODE> constexpr int kWalkWarps = N >= 64 || MODE == kSsmKeep ? 4 : 2;
+template <int N, int MODE> constexpr int kWalkChannels = kWalkWarps<N, MODE> * 32 * kStates<MODE> / N;
 
 template <typename E, int N, int MODE>
 struct WalkShared {
-    static constexpr int CB = kWalkChannels<N>;
+    static constexpr int CB = kWalkChannels<N, MODE>;
     static constexpr bool HAS_B = MODE != kSsmRev, HAS_C = MODE == kSsmOut || MODE == kSsmRev, HAS_Z = HAS_C;
     E raw[2][HAS_Z ? 3 : 2][kWalkTile][CB];   // x, dt, z (REV: dy, dt, z)
     E bc[2][HAS_B + HAS_C][kWalkTile][N];
@@ -113,10 +115,10 @@ struct WalkShared {
 };
 
 template <typename E, int N, int MODE>
-__global__ void __launch_bounds__(kWalkWarps<N> * 32) gla_ssm_walk_kernel(SsmArgs a)
+__global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32) gla_ssm_walk_kernel(SsmArgs a)
 {
     typedef WalkShared<E, N, MODE> Shared;
-    constexpr int NT = kWalkWarps<N> * 32, CB = kWalkChannels<N>, P = Shared::P, Q = N / kS, TT = kWalkTile, SUB = kSsmTile;
+    constexpr int NT = kWalkWarps<N, MODE> * 32, CB = kWalkChannels<N, MODE>, P = Shared::P, kS = kStates<MODE>, Q = N / kS, TT = kWalkTile, SUB = kSsmTile;
     constexpr bool REV = MODE == kSsmRev, OUT = MODE == kSsmOut;
     constexpr int IC = Shared::HAS_B ? 1 : 0;      // where C lies beside B
     extern __shared__ __align__(16) char smem_raw[];
@@ -352,13 +354,13 @@ template <typename E, int N, int MODE>
 cudaError_t walk(const SsmArgs& a0, cudaStream_t s)
 {
     SsmArgs a = a0;
-    constexpr int CB = kWalkChannels<N>;
+    constexpr int CB = kWalkChannels<N, MODE>;
     a.ctiles = (a.D / a.G + CB - 1) / CB;
     const int n = (int)sizeof(WalkShared<E, N, MODE>);
     const cudaError_t r = cudaFuncSetAttribute(gla_ssm_walk_kernel<E, N, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
     if (r != cudaSuccess) return r;
     const dim3 g((unsigned)((long long)a.B * a.G * a.ctiles), MODE == kSsmState || MODE == kSsmRev ? a.nseg - 1 : a.nseg);
-    gla_ssm_walk_kernel<E, N, MODE><<<g, kWalkWarps<N> * 32, n, s>>>(a);
+    gla_ssm_walk_kernel<E, N, MODE><<<g, kWalkWarps<N, MODE> * 32, n, s>>>(a);
     return cudaGetLastError();
 }
 template <typename E, int N>
@@ -394,8 +396,8 @@ cudaError_t step(const SsmArgs& a, int sms, cudaStream_t s)
 
 }  // namespace
 
-int ssm_walk_warps(int N) { return N >= 64 ? kWalkWarps<64> : kWalkWarps<8>; }
-int ssm_walk_channels(int N) { return N == 8 ? kWalkChannels<8> : N == 16 ? kWalkChannels<16> : N == 32 ? kWalkChannels<32> : kWalkChannels<64>; }
+int ssm_walk_warps(int N) { return N >= 64 ? kWalkWarps<64, kSsmOut> : kWalkWarps<8, kSsmOut>; }
+int ssm_walk_channels(int N) { return kWalkChannels<8, kSsmOut> * 8 / N * (N >= 64 ? 2 : 1); }
 
 cudaError_t launch_ssm_step(const SsmArgs& a, gla_dtype dtype, int sms, cudaStream_t s)
 {
