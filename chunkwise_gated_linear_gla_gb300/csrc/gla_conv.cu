@@ -9,12 +9,13 @@
 //     dx_s = sum_j w_j da_{s+W-1-j} (+ dS_T where row s is in S_T; s < 0: dS0),   dw_j = sum da_t x_{t-W+1+j},
 //     dbias = sum da_t.
 //
-// Bound by HBM: x read and y written once (backward: x and dy read, dx written). A thread takes four channels of bf16
-// (eight bytes; with eight channels the weights and windows do not fit the registers), two in the backward, whose sums and windows are
-// twice as many, and walks a run of tokens with
-// the window in registers; a run's first W - 1 rows are read again, from L2. A warp is 128 (64) channels of a run of one batch
-// row, a block eight warps, runs of all rows in one order, so that single tokens of many rows fill it too. Reads
-// go through strides (a projection's slice, head by head), writes are dense. Sums are fp32; S_T is a copy of inputs.
+// Bytes: x read and y written once (backward: x and dy read, dx written). A thread takes four channels of a row (with eight
+// the weights and windows do not fit the registers: 69 us for the layer below, 33 so), two in the backward, whose sums and
+// windows are twice as many (75 us, 85 with four), and walks a run of tokens with the window in registers; a run's first W - 1
+// rows are read again, from L2. A warp is 128 (64) channels of a run of one batch row, a block eight warps, runs of all rows in one
+// order, so that single tokens of many rows fill it too (128 rows of 4096 channels 5.5 us, 16 with a block to a row). Reads go through
+// strides (a projection's slice, head by head), writes are dense. Sums are fp32; S_T is a copy of inputs. 8 x 2048 tokens of
+// 2048 channels: 31.5 us, 4.3 TB/s, 0.63 of the copy rate, at 16 instructions a value; backward 71 us, 0.42, at 30.
 #include <cmath>
 #include <cstring>
 #include <type_traits>

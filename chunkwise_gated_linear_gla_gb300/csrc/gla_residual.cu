@@ -12,8 +12,10 @@
 // from r and x, so that no gradient carries that rounding.
 //
 // Bound by HBM: x and r read, h and y written once (backward: x, r, dh, dy read, dx and dr written). Rows of up to 512
-// values are a warp's, with shuffles for the sums; wider rows a block's, K pieces of eight values per thread. The
-// vectors' gradients are summed in fp32 over a thread's rows, then over the blocks, each in a fixed order.
+// values are a warp's, with shuffles for the sums; wider rows a block's, K pieces of eight values per thread: two pieces, as every sum
+// over the row costs a thread 60 instructions (with one piece 51 us for the rows below). The vectors' gradients are summed in
+// fp32 over a thread's rows, then over the blocks, each in a fixed order. 16384 bf16 rows of 2048 values, post norm and scale: 40 us,
+// 6.7 TB/s, 0.98 of the copy rate; backward 77 us, 0.77.
 #include <cmath>
 #include <cstring>
 

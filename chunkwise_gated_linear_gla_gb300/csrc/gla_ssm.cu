@@ -4,17 +4,22 @@
 //     y_t = (C_t . h_t + D x_t) silu(z_t).
 //
 // No product of matrices is in it: per token, channel and state one exponential, two products and two fused
-// multiply-adds, all fp32, the states in registers from the first token to the last. Bound by issue: at eight
-// rows of 2048 tokens of 4096 channels of 16 states 1.07e9 exponentials and 4.3e9 multiply-adds, against 0.54 GB.
+// multiply-adds, all fp32, the states in registers from the first token to the last.
 //
-// gla_ssm_walk: a thread holds eight states of a channel and walks the tokens, its products packed pairs of states. The block goes in tiles of 16 tokens: raw rows
-// arrive by asynchronous copies one tile ahead, delta and delta x are formed once per channel and token into shared
-// memory, the walk leaves C . h there, and y is formed from it eight channels at a time.
+// gla_ssm_walk: a thread holds eight states of a channel and walks the tokens, its products packed pairs of states. The block goes
+// in tiles of 32 tokens: raw rows arrive by asynchronous copies one tile ahead, delta and delta x are formed once per channel
+// and token into shared memory, B and C widened there, the walk leaves C . h in their places, and y is formed from it eight
+// channels at a time. Bound by issue: eight rows of 2048 tokens of 4096 channels of 16 states (1.07e9 of them, 0.54 GB) take
+// 401 us at 7.6 warp instructions a state, 59% of the issue slots and 70% on the schedulers that got four warps, not three; the bytes
+// would take 80, the exponentials 107. Two blocks of two warps measured better than one of four (411) and tiles of 32 better than 16
+// (414) and 64 (530).
 //
 // Few channels: the sequence is cut into segments. A first walk leaves each segment's state from zero and its sum of delta
-// (the decay across the segment is exp(A sum)), gla_ssm_scan the states entering them, a second walk y.
+// (the decay across the segment is exp(A sum)), gla_ssm_scan the states entering them, a second walk y (one row of 16421
+// tokens: 234 + 14 + 352 us in 23 segments).
 //
-// gla_ssm_step: single and few tokens, bound by the states' bytes: a thread holds four states of a channel.
+// gla_ssm_step: single and few tokens, bound by the states' bytes and their latency: a thread holds four states of a channel, of four
+// batch rows where there are many (the next token of 128 rows: 16 us, 4.4 TB/s).
 #include "gla_ssm.cuh"
 
 namespace gla {

@@ -7,14 +7,17 @@
 //     dz_t = dy_t (C_t . h_t + D x_t) silu'(z_t),   dD = sum r_t x_t,   ddt_bias = sum ddt_t,   dS0 = a_1 G_1.
 //
 // A walk over the tokens has left the state entering every tile of 16 (gla_ssm_walk). gla_ssm_bwd takes the tiles from
-// the last: a thread holds two channels by four states of h, a and G; the tile's two halves of eight tokens are
-// formed again with h and a in registers, then walked back. Products a h_{t-1} are formed as such: as h_t - delta x B they would
-// lose their digits where a decay is steep. Sums over states end in shared memory per channel and token, sums over channels
-// per token over the warp by halving exchanges, then over the block's warps; a block leaves them as partials per channel tile,
-// added in a fixed order by gla_ssm_bc_sum. No atomics: results are equal bit for bit from call to call.
+// the last: a thread holds two channels by four states of A, G and dA. It walks the tile's states once from the kept one, leaving those
+// that enter its parts of four tokens, then takes the parts from the last: h and a of the four again, in registers, and back.
+// Products a h_{t-1} are formed as such: as h_t - delta x B they would lose their digits where a decay is steep. Sums over
+// states end in shared memory per channel and token, sums over channels per token over the warp by halving exchanges, then over the
+// block's warps; a block leaves them as partials per channel tile, added in a fixed order by gla_ssm_bc_sum. No atomics: results are
+// equal bit for bit from call to call.
 //
-// Bound by issue: per token, channel and state 9 products or multiply-adds back, 4 for h again and 4.5 for the states kept,
-// with 2.5 exponentials.
+// Bound by the multiply-adds' register reads (a packed one of three different pairs takes three cycles) and by waits that two warps
+// a scheduler cannot hide (226 registers, 110 KB a block): four rows of 2048 tokens of 4096 channels of 16 states take 767 us, 24 warp
+// instructions a state at 45% of the issue slots; per token, channel and state 9 products or multiply-adds back, 4 for h and a again, 3 for
+// the tile's first walk. Preparing and finishing the tiles is 0.2 of it. One channel a thread (twice the warps) took 1.25 times as long.
 #include "gla_ssm.cuh"
 
 namespace gla {
