@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -183,6 +184,34 @@ class gla_residual_grads(ctypes.Structure):
         "grad_h", "grad_y", "grad_x", "grad_residual", "grad_w", "grad_scale")]
 
 
+# The layouts of the structs above for struct.pack: filling a ctypes structure costs a call of the Python functions below
+# more than everything else in it. "0q" ends a layout on eight bytes.
+_CONV = struct.Struct("@P3q3P7i0q")
+_CONV_GRADS = struct.Struct("@3P3q3P")
+_SSM = struct.Struct("@5P10q4P8i")
+_SSM_GRADS = struct.Struct("@11P")
+_GATE = struct.Struct("@2P6qP7ifi0q")
+_GATE_GRADS = struct.Struct("@3P6qP")
+_RESIDUAL = struct.Struct("@4Pfqiifii0q")
+_RESIDUAL_GRADS = struct.Struct("@6P")
+_LAYOUTS = {gla_conv_params: _CONV, gla_conv_grads: _CONV_GRADS, gla_ssm_params: _SSM, gla_ssm_grads: _SSM_GRADS,
+            gla_norm_gate_params: _GATE, gla_norm_gate_grads: _GATE_GRADS, gla_residual_params: _RESIDUAL,
+            gla_residual_grads: _RESIDUAL_GRADS}
+# name, arguments (n: a size, else a pointer), result
+_PACKED = (("gla_conv_fwd", "pppp", ctypes.c_int), ("gla_conv_bwd", "pppnp", ctypes.c_int),
+           ("gla_conv_bwd_workspace_size", "p", ctypes.c_size_t),
+           ("gla_ssm_fwd", "ppppnp", ctypes.c_int), ("gla_ssm_fwd_workspace_size", "p", ctypes.c_size_t),
+           ("gla_ssm_bwd", "pppnp", ctypes.c_int), ("gla_ssm_bwd_workspace_size", "p", ctypes.c_size_t),
+           ("gla_norm_gate", "ppp", ctypes.c_int), ("gla_norm_gate_bwd", "pppnp", ctypes.c_int),
+           ("gla_norm_gate_bwd_workspace_size", "p", ctypes.c_size_t),
+           ("gla_residual_norm", "pppp", ctypes.c_int), ("gla_residual_norm_bwd", "pppnp", ctypes.c_int),
+           ("gla_residual_norm_bwd_workspace_size", "p", ctypes.c_size_t))
+
+
+class _raw:
+    """The packed calls' functions, by name, once the library is loaded."""
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -194,6 +223,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load libgla.so. Raises if it is missing (unless build_if_missing) or unloadable."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -272,6 +303,14 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                 ("gla_residual_norm_bwd_workspace_size", ctypes.c_size_t, [R])):
             f = getattr(lib, name)
             f.restype, f.argtypes = restype, argtypes
+        # the same calls for parameters packed into bytes
+        for s, layout in _LAYOUTS.items():
+            if layout.size != ctypes.sizeof(s):
+                raise RuntimeError(f"{s.__name__}: {layout.size} bytes packed, {ctypes.sizeof(s)} in C")
+        for name, args, restype in _PACKED:
+            f = lib[name]
+            f.restype, f.argtypes = restype, [ctypes.c_size_t if a == "n" else vp for a in args]
+            setattr(_raw, name, f)
         _lib = lib
         return lib
 
@@ -1020,43 +1059,88 @@ def _rows(t, shape, dtype, device, what):
         _refuse(f"the last dimension of {what} is not contiguous")
 
 
-def _workspace(nbytes, device):
-    """(tensor or None, its pointer): torch hands out blocks of 512 bytes."""
+def _at(t):
+    """A tensor's address (0 for none, and for one without values)."""
+    return 0 if t is None else t.data_ptr()
+
+
+def _pack(layout, *values):
+    try:
+        return layout.pack(*values)
+    except (struct.error, OverflowError) as e:
+        _refuse(f"an argument does not fit its C type ({e})")
+
+
+def _call(name, device, stream, tensors, *args):
+    """_launch for a packed call: the function's arguments but the stream, which comes last."""
     import torch
-    if not nbytes:
-        return None, None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return ws, ws.data_ptr()
+    index = device.index
+    f = getattr(_raw, name)
+    if stream is None and torch._C._cuda_getDevice() == index:
+        s = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            if stream is None:
+                s = f(*args, torch._C._cuda_getCurrentRawStream(index))
+            else:
+                _used_on(stream, device, *tensors)
+                s = f(*args, _stream(stream))
+    if s != GLA_OK:
+        raise GlaError(s, name)
+
+
+def _workspace(name, packed, device):
+    """(tensor or None, its address, its bytes): torch hands out blocks from 512-byte boundaries. Sizes depend on the
+    device's multiprocessors."""
+    import torch
+    if torch._C._cuda_getDevice() == device.index:
+        n = getattr(_raw, name)(packed)
+    else:
+        with torch.cuda.device(device):
+            n = getattr(_raw, name)(packed)
+    if not n:
+        return None, 0, 0
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), n
+
+
+def _step3(s, B, H, T):
+    """(batch, head, token) strides; those of dimensions of one are never stepped and count as 0."""
+    return s[0] if B > 1 else 0, s[1] if H > 1 else 0, s[2] if T > 1 else 0
 
 
 def _conv_params(x, w, bias, S0, activation):
     import torch
     if activation not in (None, "silu"):
         _refuse(f"activation is None or 'silu', not {activation!r}")
-    if x.dim() == 3:
-        (B, T, d), H = x.shape, 1
+    shape, dt, dev, f32 = x.shape, x.dtype, x.device, torch.float32
+    if len(shape) == 3:
+        (B, T, d), H = shape, 1
         s = x.stride()
-        steps = _steps((s[0], 0, s[1]), B, 1, T)
-    elif x.dim() == 4:
-        B, H, T, d = x.shape
-        steps = _steps(x.stride(), B, H, T)
+        steps = s[0] if B > 1 else 0, 0, s[1] if T > 1 else 0
+    elif len(shape) == 4:
+        B, H, T, d = shape
+        s = x.stride()
+        steps = _step3(s, B, H, T)
     else:
         _refuse("x has three or four dimensions: [B,T,D] or [B,H,T,d]")
-    dt, dev, D = x.dtype, x.device, H * d
+    D = H * d
     code = _dtype_code(x, "x")
-    _rows(x, x.shape, dt, dev, "x")
+    if s[-1] != 1:
+        _rows(x, shape, dt, dev, "x")
     if w.dim() != 2:
         _refuse("w has two dimensions: [H d, W]")
     W = w.shape[1]
-    _dense(w, (D, W), torch.float32, dev, "w")
+    _dense(w, (D, W), f32, dev, "w")
     if bias is not None:
-        _dense(bias, (D,), torch.float32, dev, "bias")
+        _dense(bias, (D,), f32, dev, "bias")
     if S0 is not None:
         _dense(S0, (B, W - 1, D), dt, dev, "S0")
     _on_gpu(x, "x")
     if B == 0:
         _refuse("an empty batch")
-    return gla_conv_params(_ptr(x), steps, _ptr(w), _ptr(bias), _ptr(S0), B, H, T, d, W, _ACTS[activation], code), D
+    load()
+    return _pack(_CONV, x.data_ptr(), *steps, w.data_ptr(), _at(bias), _at(S0), B, H, T, d, W, _ACTS[activation], code), (B, W - 1, D)
 
 
 def causal_conv_forward(x, w, bias=None, S0=None, activation="silu", want_state=True, stream=None, y=None, ST=None):
@@ -1068,22 +1152,19 @@ def causal_conv_forward(x, w, bias=None, S0=None, activation="silu", want_state=
     x's shape, ST the last W - 1 rows of (S0, x) (None unless wanted). A decoding loop passes ST=S0 to carry the state
     in place; y and ST count as modified in place. A batch of unequal prompts is padded in front, with zeros.
     """
-    p, D = _conv_params(x, w, bias, S0, activation)
-    dev, shape = x.device, (p.B, p.W - 1, D)
-    if y is not None:
+    p, state = _conv_params(x, w, bias, S0, activation)
+    dev, given = x.device, (y, ST)
+    if y is None:
+        y = x.new_empty(x.shape)
+    else:
         _dense(y, x.shape, x.dtype, dev, "y")
         _given(y, "y")
     if ST is not None:
-        _dense(ST, shape, x.dtype, dev, "ST")
+        _dense(ST, state, x.dtype, dev, "ST")
         _given(ST, "ST")
-    given = y, ST
-    lib = _lib or load()
-    if y is None:
-        y = x.new_empty(x.shape)
-    if ST is None and want_state:
-        ST = x.new_empty(shape)
-    py, ps = _ptr(y), _ptr(ST)
-    _launch(lambda r, s: lib.gla_conv_fwd(r, py, ps, s), "gla_conv_fwd", p, dev, stream, y, ST)
+    elif want_state:
+        ST = x.new_empty(state)
+    _call("gla_conv_fwd", dev, stream, (y, ST), p, y.data_ptr(), _at(ST))
     _written(*given)
     return y, ST
 
@@ -1093,26 +1174,24 @@ def causal_conv_backward(x, w, bias, S0, dy, dST=None, activation="silu", want_d
     x's type, dw and dbias fp32; dw and dbias None unless wanted, dbias without a bias, dS0 unless wanted (it is defined
     without S0 too, zeros)."""
     import torch
-    p, D = _conv_params(x, w, bias, S0, activation)
+    p, state = _conv_params(x, w, bias, S0, activation)
     dev = x.device
     _dense(dy, x.shape, x.dtype, dev, "dy")
     if dST is not None:
-        _dense(dST, (p.B, p.W - 1, D), x.dtype, dev, "dST")
-    lib = _lib or load()
+        _dense(dST, state, x.dtype, dev, "dST")
     gx = x.new_empty(x.shape) if x.dim() == 3 else _rows_like(x)
     gw = torch.empty_like(w) if want_dw else None
     gb = torch.empty_like(bias) if want_dw and bias is not None else None
-    gs = x.new_empty((p.B, p.W - 1, D)) if want_dS0 else None
+    gs = x.new_empty(state) if want_dS0 else None
     s = gx.stride()
-    steps = _steps((s[0], 0, s[1]), p.B, 1, p.T) if x.dim() == 3 else _steps(s, p.B, p.H, p.T)
-    g = gla_conv_grads(_ptr(dy), _ptr(dST), _ptr(gx), steps, _ptr(gw), _ptr(gb), _ptr(gs))
-    n = _here_size(lib.gla_conv_bwd_workspace_size, p, dev) if want_dw else 0
-    ws, pw = _workspace(n, dev)
-    _launch(lambda r, s: lib.gla_conv_bwd(r, ctypes.byref(g), pw, n, s), "gla_conv_bwd", p, dev, stream, gx, gw, gb, gs, ws)
+    if x.dim() == 3:
+        steps = s[0] if x.shape[0] > 1 else 0, 0, s[1] if x.shape[1] > 1 else 0
+    else:
+        steps = _step3(s, *x.shape[:3])
+    g = _pack(_CONV_GRADS, dy.data_ptr(), _at(dST), gx.data_ptr(), *steps, _at(gw), _at(gb), _at(gs))
+    ws, pw, n = _workspace("gla_conv_bwd_workspace_size", p, dev) if want_dw else (None, 0, 0)
+    _call("gla_conv_bwd", dev, stream, (gx, gw, gb, gs, ws), p, g, pw, n)
     return gx, gw, gb, gs
-
-
-_Steps2 = ctypes.c_longlong * 2
 
 
 def _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments=0):
@@ -1150,13 +1229,12 @@ def _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments=0):
     _on_gpu(x, "x")
     if nb == 0:
         _refuse("an empty batch")
+    load()
     # strides of dimensions of one are never stepped and count as 0
-    if nb > 1 and T > 1:
-        steps = [_Steps2(s[0], s[1]) for s in (sx, sd, sz, sB, sC)]
-    else:
-        steps = [_Steps2(s[0] if nb > 1 else 0, s[1] if T > 1 else 0) for s in (sx, sd, sz, sB, sC)]
-    return gla_ssm_params(_ptr(x), _ptr(dt), _ptr(z), _ptr(B), _ptr(C), *steps, _ptr(A), _ptr(D), _ptr(dt_bias), _ptr(S0),
-                          nb, T, nd, G, N, 1 if softplus else 0, code, force_segments)
+    b, o = nb > 1, T > 1
+    return _pack(_SSM, x.data_ptr(), dt.data_ptr(), _at(z), B.data_ptr(), C.data_ptr(), b and sx[0], o and sx[1], b and sd[0],
+                 o and sd[1], b and sz[0], o and sz[1], b and sB[0], o and sB[1], b and sC[0], o and sC[1], A.data_ptr(),
+                 _at(D), _at(dt_bias), _at(S0), nb, T, nd, G, N, 1 if softplus else 0, code, force_segments), (nb, nd, N), T
 
 
 def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, softplus=True, want_state=True,
@@ -1170,24 +1248,21 @@ def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None
     as modified in place. A token is passed over where its dt is -inf (with softplus; its other values finite).
     """
     import torch
-    p = _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments)
-    dev, states = x.device, (p.B, p.D, p.N)
-    if y is not None:
+    p, states, T = _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments)
+    dev, given = x.device, (y, ST)
+    if y is None:
+        y = x.new_empty(x.shape)
+    else:
         _dense(y, x.shape, x.dtype, dev, "y")
         _given(y, "y")
     if ST is not None:
         _dense(ST, states, torch.float32, dev, "ST")
         _given(ST, "ST")
-    given = y, ST
-    lib = _lib or load()
-    if y is None:
-        y = x.new_empty(x.shape)
-    if ST is None and want_state:
+    elif want_state:
         ST = torch.empty(states, dtype=torch.float32, device=dev)
-    n = 0 if p.T <= 8 and not force_segments else _here_size(lib.gla_ssm_fwd_workspace_size, p, dev)
-    ws, pw = _workspace(n, dev)
-    py, ps = _ptr(y), _ptr(ST)
-    _launch(lambda r, s: lib.gla_ssm_fwd(r, py, ps, pw, n, s), "gla_ssm_fwd", p, dev, stream, y, ST, ws)
+    # (up to eight tokens are taken one by one, without a workspace)
+    ws, pw, n = (None, 0, 0) if T <= 8 and not force_segments else _workspace("gla_ssm_fwd_workspace_size", p, dev)
+    _call("gla_ssm_fwd", dev, stream, (y, ST, ws), p, y.data_ptr(), _at(ST), pw, n)
     _written(*given)
     return y, ST
 
@@ -1197,21 +1272,17 @@ def selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, S0, dy, dST=None, sof
     """Gradients of selective_scan_forward: (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dS0), dense; dx, ddt, dB, dC and dz in the
     inputs' type, the others fp32; None without the input, dS0 unless wanted (it is defined without S0 too, zero)."""
     import torch
-    p = _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments)
-    dev, states = x.device, (p.B, p.D, p.N)
+    p, states, _ = _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments)
+    dev = x.device
     _dense(dy, x.shape, x.dtype, dev, "dy")
     if dST is not None:
         _dense(dST, states, torch.float32, dev, "dST")
-    lib = _lib or load()
     like = lambda m: None if m is None else m.new_empty(m.shape)  # noqa: E731
     gx, gdt, gA, gB, gC, gD, gz, gb = (like(m) for m in (x, dt, A, B, C, D, z, dt_bias))
     gS = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
-    g = gla_ssm_grads(_ptr(dy), _ptr(dST), _ptr(gx), _ptr(gdt), _ptr(gz), _ptr(gB), _ptr(gC), _ptr(gA), _ptr(gD),
-                      _ptr(gb), _ptr(gS))
-    n = _here_size(lib.gla_ssm_bwd_workspace_size, p, dev)
-    ws, pw = _workspace(n, dev)
-    _launch(lambda r, s: lib.gla_ssm_bwd(r, ctypes.byref(g), pw, n, s), "gla_ssm_bwd", p, dev, stream,
-            gx, gdt, gA, gB, gC, gD, gz, gb, gS, ws)
+    g = _pack(_SSM_GRADS, *(_at(t) for t in (dy, dST, gx, gdt, gz, gB, gC, gA, gD, gb, gS)))
+    ws, pw, n = _workspace("gla_ssm_bwd_workspace_size", p, dev)
+    _call("gla_ssm_bwd", dev, stream, (gx, gdt, gA, gB, gC, gD, gz, gb, gS, ws), p, g, pw, n)
     return gx, gdt, gA, gB, gC, gD, gz, gb, gS
 
 
@@ -1221,35 +1292,36 @@ def _gate_params(x, gate, w, norm, eps, activation, gate_first):
         _refuse(f"norm is None, 'l2' or 'rms', not {norm!r}")
     if activation not in ("silu", "sigmoid"):
         _refuse(f"activation is 'silu' or 'sigmoid', not {activation!r}")
-    if x.dim() != 4:
+    shape, dev = x.shape, x.device
+    if len(shape) != 4:
         _refuse("x has four dimensions: [B,H,T,d]")
-    B, H, T, d = x.shape
-    dev = x.device
+    B, H, T, d = shape
     code = _dtype_code(x, "x")
-    _rows(x, x.shape, x.dtype, dev, "x")
+    sx, sg, pg = x.stride(), (0, 0, 0), 0
+    if sx[3] != 1:
+        _rows(x, shape, x.dtype, dev, "x")
     if gate is not None:
-        _rows(gate, x.shape, x.dtype, dev, "gate")
+        _rows(gate, shape, x.dtype, dev, "gate")
+        sg, pg = _step3(gate.stride(), B, H, T), gate.data_ptr()
     if w is not None:
         _dense(w, (d,), torch.float32, dev, "w")
     _on_gpu(x, "x")
-    return gla_norm_gate_params(_ptr(x), _ptr(gate), _steps(x.stride(), B, H, T),
-                                _NO_STEPS if gate is None else _steps(gate.stride(), B, H, T), _ptr(w), B, H, T, d,
-                                _NORMS[norm], _ACTS[activation], 1 if gate_first else 0, eps, code)
+    load()
+    return _pack(_GATE, x.data_ptr(), pg, *_step3(sx, B, H, T), *sg, _at(w), B, H, T, d, _NORMS[norm], _ACTS[activation],
+                 1 if gate_first else 0, eps, code)
 
 
 def norm_gate_forward(x, gate=None, w=None, norm="rms", eps=1e-6, activation="silu", gate_first=False, stream=None):
     """Norm, weight and gate of every row of x [B,H,T,d] (a recurrence's output) into the output projection's layout
-    (gla_norm_gate): y = w x / n(x) act(gate), or with gate_first w u / n(u) of u = x act(gate); returns dense [B,T,H,d].
+    (gla_norm_gate): y = w x / n(x) act(g), or with gate_first w u / n(u) of u = x act(gate); returns dense [B,T,H,d].
 
     x and gate (or None: no gate) may be strided views of [B,H,T,d] (bf16 or fp32, one type), the last dimension
     contiguous and every row from a 16-byte boundary; w fp32 [d] or None; norm "rms", "l2" or None; activation "silu" or
     "sigmoid"; d a multiple of 16 up to 1024."""
     p = _gate_params(x, gate, w, norm, eps, activation, gate_first)
-    lib, dev = _lib or load(), x.device
     B, H, T, d = x.shape
     y = x.new_empty((B, T, H, d))
-    py = _ptr(y)
-    _launch(lambda r, s: lib.gla_norm_gate(r, py, s), "gla_norm_gate", p, dev, stream, y)
+    _call("gla_norm_gate", x.device, stream, (y,), p, y.data_ptr())
     return y
 
 
@@ -1259,16 +1331,14 @@ def norm_gate_backward(x, gate, w, dy, norm="rms", eps=1e-6, activation="silu", 
     import torch
     p = _gate_params(x, gate, w, norm, eps, activation, gate_first)
     B, H, T, d = x.shape
-    _dense(dy, (B, T, H, d), x.dtype, x.device, "dy")
-    lib, dev = _lib or load(), x.device
+    dev = x.device
+    _dense(dy, (B, T, H, d), x.dtype, dev, "dy")
     gx, gg = _rows_like(x), None if gate is None else _rows_like(gate)
     gw = None if w is None else torch.empty_like(w)
-    g = gla_norm_gate_grads(_ptr(dy), _ptr(gx), _ptr(gg), _steps(gx.stride(), B, H, T),
-                            _NO_STEPS if gg is None else _steps(gg.stride(), B, H, T), _ptr(gw))
-    n = 0 if gw is None else _here_size(lib.gla_norm_gate_bwd_workspace_size, p, dev)
-    ws, pw = _workspace(n, dev)
-    _launch(lambda r, s: lib.gla_norm_gate_bwd(r, ctypes.byref(g), pw, n, s), "gla_norm_gate_bwd", p, dev, stream,
-            gx, gg, gw, ws)
+    g = _pack(_GATE_GRADS, dy.data_ptr(), gx.data_ptr(), _at(gg), *_step3(gx.stride(), B, H, T),
+              *((0, 0, 0) if gg is None else _step3(gg.stride(), B, H, T)), _at(gw))
+    ws, pw, n = (None, 0, 0) if gw is None else _workspace("gla_norm_gate_bwd_workspace_size", p, dev)
+    _call("gla_norm_gate_bwd", dev, stream, (gx, gg, gw, ws), p, g, pw, n)
     return gx, gg, gw
 
 
@@ -1276,26 +1346,27 @@ def _residual_params(x, residual, w, scale, post_norm, eps):
     import torch
     if x.dim() < 1:
         _refuse("x has rows: [..., D]")
-    D, dev, f32 = x.shape[-1], x.device, torch.float32
-    code, rcode = _dtype_code(x, "x"), _dtype_code(x, "x")
-    _dense(x, x.shape, x.dtype, dev, "x")
+    shape, dev, f32 = x.shape, x.device, torch.float32
+    D = shape[-1]
+    code = rcode = _dtype_code(x, "x")
+    _dense(x, shape, x.dtype, dev, "x")
     if residual is not None:
         rcode = _dtype_code(residual, "residual")
         if code == GLA_FP32 and rcode != GLA_FP32:
             _refuse("an fp32 x goes into an fp32 residual")
-        _dense(residual, x.shape, residual.dtype, dev, "residual")
-    alpha, vec = 1.0, None
+        _dense(residual, shape, residual.dtype, dev, "residual")
+    alpha, vec = 1.0, 0
     if isinstance(scale, torch.Tensor):
-        vec = scale
-        _dense(vec, (D,), f32, dev, "scale")
+        _dense(scale, (D,), f32, dev, "scale")
+        vec = scale.data_ptr()
     elif scale is not None:
         alpha = float(scale)
     if w is not None:
         _dense(w, (D,), f32, dev, "w")
     _on_gpu(x, "x")
-    rows = x.numel() // D if D else 0
-    return gla_residual_params(_ptr(x), _ptr(residual), _ptr(w), _ptr(vec), alpha, rows, D, 1 if post_norm else 0, eps,
-                               code, rcode)
+    load()
+    return _pack(_RESIDUAL, x.data_ptr(), _at(residual), _at(w), vec, alpha, x.numel() // D if D else 0, D,
+                 1 if post_norm else 0, eps, code, rcode)
 
 
 def residual_norm_forward(x, residual=None, w=None, scale=None, post_norm=False, eps=1e-6, stream=None, h=None):
@@ -1306,17 +1377,15 @@ def residual_norm_forward(x, residual=None, w=None, scale=None, post_norm=False,
     scale a number, fp32 [D] or None; D a multiple of 16 up to 16384, tensors from a 16-byte boundary. h has the residual's
     type and may be the residual itself (h=residual: in place); it counts as modified in place. The norm reads h before its rounding."""
     p = _residual_params(x, residual, w, scale, post_norm, eps)
-    lib, dev = _lib or load(), x.device
+    dev, given = x.device, h
     like = x if residual is None else residual
-    if h is not None:
-        _dense(h, x.shape, like.dtype, dev, "h")
-        _given(h, "h")
-    given = h
     if h is None:
         h = like.new_empty(like.shape)
+    else:
+        _dense(h, x.shape, like.dtype, dev, "h")
+        _given(h, "h")
     y = x.new_empty(x.shape)
-    ph, py = _ptr(h), _ptr(y)
-    _launch(lambda r, s: lib.gla_residual_norm(r, ph, py, s), "gla_residual_norm", p, dev, stream, h, y)
+    _call("gla_residual_norm", dev, stream, (h, y), p, h.data_ptr(), y.data_ptr())
     _written(given)
     return h, y
 
@@ -1328,20 +1397,17 @@ def residual_norm_backward(x, residual, w, scale, dh, dy, post_norm=False, eps=1
     equal (no scale, no post_norm, one type) they are one tensor."""
     import torch
     p = _residual_params(x, residual, w, scale, post_norm, eps)
-    like = x if residual is None else residual
+    like, dev = x if residual is None else residual, x.device
     if dh is not None:
-        _dense(dh, x.shape, like.dtype, x.device, "dh")
+        _dense(dh, x.shape, like.dtype, dev, "dh")
     if dy is not None:
-        _dense(dy, x.shape, x.dtype, x.device, "dy")
-    lib, dev = _lib or load(), x.device
+        _dense(dy, x.shape, x.dtype, dev, "dy")
     same = want_dx and want_dres and residual is not None and scale is None and not post_norm and residual.dtype == x.dtype
     gr = residual.new_empty(residual.shape) if want_dres and residual is not None else None
     gx = gr if same else x.new_empty(x.shape) if want_dx else None
     gw = None if w is None else torch.empty_like(w)
     gs = torch.empty_like(scale) if isinstance(scale, torch.Tensor) else None
-    g = gla_residual_grads(_ptr(dh), _ptr(dy), None if same else _ptr(gx), _ptr(gr), _ptr(gw), _ptr(gs))
-    n = 0 if gw is None and gs is None else _here_size(lib.gla_residual_norm_bwd_workspace_size, p, dev)
-    ws, pw = _workspace(n, dev)
-    _launch(lambda r, s: lib.gla_residual_norm_bwd(r, ctypes.byref(g), pw, n, s), "gla_residual_norm_bwd", p, dev, stream,
-            gx, gr, gw, gs, ws)
+    g = _pack(_RESIDUAL_GRADS, _at(dh), _at(dy), 0 if same else _at(gx), _at(gr), _at(gw), _at(gs))
+    ws, pw, n = (None, 0, 0) if gw is None and gs is None else _workspace("gla_residual_norm_bwd_workspace_size", p, dev)
+    _call("gla_residual_norm_bwd", dev, stream, (gx, gr, gw, gs, ws), p, g, pw, n)
     return gx, gr, gw, gs
