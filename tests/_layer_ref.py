@@ -80,3 +80,17 @@ def near(got, want, what, slack=2e-5):
         tol = half * want.abs() + slack * want.square().mean().sqrt()
         worst = float(((got - want).abs() / (tol + 1e-30)).max())
         assert worst <= 1, f"{what}: {worst:.2f} of its bound"
+
+
+def along(f, args, grads, seed=0, step=2.0 ** -7):
+    """Each gradient of the scalar f(*args) (fp32 tensors) along a random direction against the difference of f's own values a step
+    either way: off by the step's square times the third derivative (6e-5 of values of order one) and by the results' 2^-24
+    over the step (1e-5 of the terms); held to 2e-2 of the root of the direction's summed squares."""
+    g = torch.Generator().manual_seed(seed)
+    for i, (x, d) in enumerate(zip(args, grads)):
+        way = torch.randn(x.shape, generator=g).to(x.device)
+        at = lambda s: f(*args[:i], x + s * way, *args[i + 1:])  # noqa: E731
+        diff = (at(step) - at(-step)) / (2 * step)
+        each = d.double() * way.double()
+        want, size = float(each.sum()), float(each.square().sum().sqrt())
+        assert abs(diff - want) <= 2e-2 * size + 1e-4, f"argument {i}: {diff} {want}"

@@ -143,6 +143,18 @@ def test_not_finite_values_stay_in_their_channel_and_window():
     assert torch.equal(z[same], y[same]) and torch.isnan(z[0, 100:104, 5]).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [1, 2])
+def test_gradients_against_differences(H):
+    x, w, b, S0, dy, dST = ref.cuda(make(2, H, 9, 32, 4, torch.float32, 6))
+    x = x.contiguous()
+
+    def loss(*a):
+        y, ST = gla.causal_conv_forward(*a)
+        return float((y.double() * dy.double()).sum() + (ST.double() * dST.double()).sum())
+    ref.along(loss, (x, w, b, S0), gla.causal_conv_backward(x, w, b, S0, dy, dST))
+
+
 # ---------------------------------------------------------------- refusals, no GPU needed
 
 def _params(**kw):

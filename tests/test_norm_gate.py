@@ -97,6 +97,15 @@ def test_empty_sequence_and_broadcast_gate():
     assert full.shape == e.shape
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("first,act", [(False, "silu"), (True, "silu"), (True, "sigmoid")])
+def test_gradients_against_differences(first, act):
+    x, g, w, dy = ref.cuda(make(1, 2, 5, 64, torch.float32, 8))
+    kw = dict(activation=act, gate_first=first)
+    loss = lambda *a: float((gla.norm_gate_forward(*a, **kw).double() * dy.double()).sum())  # noqa: E731
+    ref.along(loss, (x, g.contiguous(), w), gla.norm_gate_backward(x, g.contiguous(), w, dy, **kw))
+
+
 # ---------------------------------------------------------------- refusals, no GPU needed
 
 def _params(**kw):

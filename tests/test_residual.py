@@ -106,6 +106,19 @@ def test_no_rows():
     assert not got[2].any() and not got[3].any()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("post", [False, True])
+def test_gradients_against_differences(post):
+    g = torch.Generator().manual_seed(3)
+    x, r, dh, dy = (torch.randn(6, 80, generator=g).cuda() for _ in range(4))
+    w, sc = (1 + 0.2 * torch.randn(80, generator=g).cuda() for _ in range(2))
+
+    def loss(x, r, w, sc):
+        h, y = gla.residual_norm_forward(x, r, w, sc, post_norm=post)
+        return float((h.double() * dh.double()).sum() + (y.double() * dy.double()).sum())
+    ref.along(loss, (x, r, w, sc), gla.residual_norm_backward(x, r, w, sc, dh, dy, post_norm=post))
+
+
 # ---------------------------------------------------------------- refusals, no GPU needed
 
 def _params(**kw):

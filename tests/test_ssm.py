@@ -185,6 +185,26 @@ def test_gradients_against_differences():
         assert abs(diff - want) <= 2e-2 * size, f"{n}: {diff} {want}"
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,segments", [(5, 0), (70, 1), (70, 3)])
+def test_not_finite_values_stay_in_their_channel_and_after_their_token(T, segments):
+    """A NaN or an infinity in one channel's x, dt or z, or in its state, reaches no other channel and no token before it."""
+    t, _, _ = make(1, T, 64, 16, 1, torch.float32, 14)
+    t = {n: a.contiguous() for n, a in t.items()}
+    y, ST = gla.selective_scan_forward(**t, force_segments=segments)
+    v = {n: a.clone() for n, a in t.items()}
+    at = T - 3
+    v["x"][0, at, 3], v["dt"][0, at, 17], v["z"][0, at, 33], v["S0"][0, 50, 2] = float("nan"), float("inf"), float("nan"), float("inf")
+    z, SZ = gla.selective_scan_forward(**v, force_segments=segments)
+    same = torch.ones_like(y, dtype=torch.bool)
+    same[0, at:, [3, 17, 33]] = False
+    same[0, :, 50] = False
+    assert torch.equal(z[same], y[same]) and torch.isnan(z[0, at:, 3]).all() and torch.isnan(z[0, at, 33])
+    assert torch.equal(z[0, at + 1:, 33], y[0, at + 1:, 33])
+    rows = [c for c in range(64) if c not in (3, 17, 50)]
+    assert torch.equal(SZ[0, rows], ST[0, rows])
+
+
 # ---------------------------------------------------------------- refusals, no GPU needed
 
 def _params(**kw):
