@@ -314,14 +314,15 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                     sd[i] += di;
 #pragma unroll
                     for (int j = 0; j < kS / 2; ++j) {
+                        // (multiply-adds with a common first operand side by side: it is read from the registers once)
                         const f2 hp = n ? h[n - 1][i][j] : in[i][j];
                         ys = fma2(h[n][i][j], t.C[j], ys);
-                        dC[j] = i ? fma2(r2, h[n][i][j], dC[j]) : mul2(r2, h[n][i][j]);
-                        const f2 gg = fma2(r2, t.C[j], G[i][j]);
-                        Gl[i][j] = mul2(ea[n][i][j], fma2(r2, t.C[j], Gl[i][j]));
-                        dB[j] = i ? fma2(x2, gg, dB[j]) : mul2(x2, gg);
+                        dC[j] = i ? fma2(h[n][i][j], r2, dC[j]) : mul2(h[n][i][j], r2);
+                        const f2 gg = fma2(r2, t.C[j], G[i][j]), gl = fma2(r2, t.C[j], Gl[i][j]);
                         ps = fma2(gg, t.B[j], ps);
+                        dB[j] = i ? fma2(gg, x2, dB[j]) : mul2(gg, x2);
                         G[i][j] = mul2(ea[n][i][j], gg);      // what goes on to the token before
+                        Gl[i][j] = mul2(ea[n][i][j], gl);
                         const f2 q = mul2(G[i][j], hp);
                         es = fma2(q, A[i][j], es);
                         dA[i][j] = fma2(q, d2, dA[i][j]);
