@@ -120,7 +120,7 @@ struct WalkShared {
 };
 
 template <typename E, int N, int MODE>
-__global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32) gla_ssm_walk_kernel(SsmArgs a)
+__global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14 / kWalkWarps<N, MODE> : 1) gla_ssm_walk_kernel(SsmArgs a)
 {
     typedef WalkShared<E, N, MODE> Shared;
     constexpr int NT = kWalkWarps<N, MODE> * 32, CB = kWalkChannels<N, MODE>, P = Shared::P, kS = kStates<MODE>, Q = N / kS, TT = kWalkTile, SUB = kSsmTile;
@@ -280,7 +280,6 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32) gla_ssm_walk_kernel(
 #pragma unroll
             for (int n = 0; n < SUB; ++n) {
                 if (n + 2 < SUB) fetch(n + 2, p[(n + 2) % 3]);
-                asm volatile("" ::: "memory");             // (the loads stay before what follows)
                 if (n + 1 < SUB) form(p[(n + 1) % 3]);
                 use(n, p[n % 3]);
             }
