@@ -32,14 +32,19 @@ template <int N> constexpr int kBwdChannels = NT * kS * kC / N;
 // A thread's four states of a channel are taken in the order n ^ m, m from its lane: then what the lanes exchange when they
 // sum over the warp's channels lies at the same place in all of them. B and C of a tile lie in shared memory once in each order,
 // 64 bytes further on each time, so that the orders' reads meet no bank twice.
-constexpr int kOrders = 4;
+template <int N> constexpr int kOrders = N >= 64 ? 2 : 4;      // (with two groups of lanes only pairs are exchanged)
+
+// Sums over states are left in shared memory by each of a channel's N / kS threads. Where two blocks would not fit an SM so, they are
+// halved first, once or twice, by exchanges between neighbouring lanes (fp32, 3 x 777 tokens of 1040 channels of 32 states: 174 us with
+// one block an SM, XX so).
+template <typename E, int N> constexpr int kHalvings = N >= 64 ? 2 : N == 16 && sizeof(E) == 2 ? 0 : 1;
 
 template <typename E, int N>
 struct BwdShared {
-    static constexpr int CB = kBwdChannels<N>, Q = N / kS;
+    static constexpr int CB = kBwdChannels<N>, Q = N / kS, PQ = Q >> kHalvings<E, N>;
     E raw[2][4][TT][CB];                      // x, dt, z, dy
     E bc[2][2][TT][N];
-    float wide[2][kOrders][TT * N + 16];      // B, C
+    float wide[2][kOrders<N>][TT * N + 16];   // B, C
     // the states entering the tile (two tiles' in turn), and its parts but the first and the last, as each thread reads them
     float keep[2][kC][NT * 4], mid[TT / PART - 2][kC][NT * 4];
     // Rows of a value per channel: the first four of every eight channels, then the other four, with the eights 0 - 3 and 4 - 7
@@ -47,7 +52,7 @@ struct BwdShared {
     // neighbouring eights, still meet every bank once.
     static constexpr int HALF = CB / 2, TURN = CB >= 64 ? 4 : 0;
     float delta[TT][CB], dx[TT][CB], r[TT][CB];
-    float part[3][Q][TT * CB + 16];           // y, p, e over each thread's states
+    float part[3][PQ][TT * CB + 256 / N];     // y, p, e over states
     float red[kWarps][TT][2 * N];             // dB, dC over each warp's channels
 };
 
@@ -77,7 +82,8 @@ template <typename E, int N>
 __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
 {
     typedef BwdShared<E, N> Shared;
-    constexpr int CB = kBwdChannels<N>, Q = N / kS, GROUPS = 32 / Q, HALF = Shared::HALF, TURN = Shared::TURN;
+    constexpr int CB = kBwdChannels<N>, Q = N / kS, GROUPS = 32 / Q, HALF = Shared::HALF, TURN = Shared::TURN, PQ = Shared::PQ,
+                  HALVINGS = kHalvings<E, N>;
     extern __shared__ __align__(16) char smem_raw[];
     auto& sm = *reinterpret_cast<Shared*>(smem_raw);
     const int Dg = a.D / a.G, ct = blockIdx.x % a.ctiles;
@@ -166,8 +172,10 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
             up(q[0], v[0], v[1]); up(q[1], v[2], v[3]);
             *reinterpret_cast<float4*>(&sm.wide[which][0][at]) = make_float4(v[0], v[1], v[2], v[3]);
             *reinterpret_cast<float4*>(&sm.wide[which][1][at]) = make_float4(v[2], v[3], v[0], v[1]);
-            *reinterpret_cast<float4*>(&sm.wide[which][2][at]) = make_float4(v[1], v[0], v[3], v[2]);
-            *reinterpret_cast<float4*>(&sm.wide[which][3][at]) = make_float4(v[3], v[2], v[1], v[0]);
+            if constexpr (kOrders<N> > 2) {
+                *reinterpret_cast<float4*>(&sm.wide[which][2][at]) = make_float4(v[1], v[0], v[3], v[2]);
+                *reinterpret_cast<float4*>(&sm.wide[which][3][at]) = make_float4(v[3], v[2], v[1], v[0]);
+            }
         }
         for (int i = threadIdx.x; i < VPT; i += NT) {
             const int tok = i / COLS;
@@ -306,6 +314,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                 if (n > 0) fetch(tok - 1, p[(n - 1) % 2]);
                 const bool before = n < PART - 1;              // the token after this one is of this part: its sums are due
                 if (before) sum_begin(dB, dC);
+                float of[3][kC];
 #pragma unroll
                 for (int i = 0; i < kC; ++i) {
                     const float di = i ? t.d.y : t.d.x;
@@ -332,9 +341,24 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                         else sum_last();
                     }
                     // y, p, e of the channel over this thread's states
-                    sm.part[0][sg][tok * CB + cp + i] = sum2(ys);
-                    sm.part[1][sg][tok * CB + cp + i] = sum2(ps);
-                    sm.part[2][sg][tok * CB + cp + i] = sum2(es);
+                    if constexpr (HALVINGS == 0) {
+                        sm.part[0][sg][tok * CB + cp + i] = sum2(ys);
+                        sm.part[1][sg][tok * CB + cp + i] = sum2(ps);
+                        sm.part[2][sg][tok * CB + cp + i] = sum2(es);
+                    } else {
+                        const float sums[3] = {sum2(ys), sum2(ps), sum2(es)};
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) of[k][i] = sums[k];
+                    }
+                }
+                if constexpr (HALVINGS > 0) {
+                    const bool odd = sg & 1;               // a pair of lanes keeps one channel each
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        float v = (odd ? of[k][1] : of[k][0]) + __shfl_xor_sync(~0u, odd ? of[k][0] : of[k][1], 1);
+                        if constexpr (HALVINGS > 1) v += __shfl_xor_sync(~0u, v, 2);
+                        if (HALVINGS < 2 || !(sg & 2)) sm.part[k][sg >> HALVINGS][tok * CB + cp + (sg & 1)] = v;
+                    }
                 }
                 if (before) sum_end(tok + 1);
             }
@@ -384,7 +408,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
             for (int k = 0; k < 3; ++k) {
                 get8(&sm.part[k][0][tok * CB], o[k]);
 #pragma unroll
-                for (int q = 1; q < Q; ++q) {
+                for (int q = 1; q < PQ; ++q) {
                     f2 f[4];
                     get8(&sm.part[k][q][tok * CB], f);
 #pragma unroll
