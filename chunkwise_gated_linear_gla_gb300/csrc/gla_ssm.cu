@@ -10,13 +10,13 @@
 // in tiles of 32 tokens: raw rows arrive by asynchronous copies one tile ahead, delta and delta x are formed once per channel
 // and token into shared memory, B and C widened there, the walk leaves C . h in their places, and y is formed from it eight
 // channels at a time. Bound by issue: eight rows of 2048 tokens of 4096 channels of 16 states (1.07e9 of them, 0.54 GB) take
-// 401 us at 7.6 warp instructions a state, 59% of the issue slots and 70% on the schedulers that got four warps, not three; the bytes
-// would take 80, the exponentials 107. Two blocks of two warps measured better than one of four (411) and tiles of 32 better than 16
+// 396 us at 7.7 warp instructions a state, 59% of the issue slots and 70% on the schedulers that got four warps, not three; the bytes
+// would take 80, the exponentials 107. Two blocks of two warps measured better than one of four (407 us) and tiles of 32 better than 16
 // (414) and 64 (530).
 //
 // Few channels: the sequence is cut into segments. A first walk leaves each segment's state from zero and its sum of delta
 // (the decay across the segment is exp(A sum)), gla_ssm_scan the states entering them, a second walk y (one row of 16421
-// tokens: 234 + 14 + 352 us in 23 segments).
+// tokens: 216 + 14 + 349 us in 23 segments).
 //
 // gla_ssm_step: single and few tokens, bound by the states' bytes and their latency: a thread holds four states of a channel, of four
 // batch rows where there are many (the next token of 128 rows: 16 us, 4.4 TB/s).
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kStepNT) gla_ssm_step_kernel(SsmArgs a)
 
 constexpr int kWalkTile = 32;      // tokens per tile of loads: two of the kept states' tiles
 // States of a thread: B and C are read once for eight. The walk that keeps states runs uncut with the few blocks of a training batch, where
-// more warps count for more (4 x 2048 tokens of 4096 channels of 16 states: 157 us with four, 171 with eight).
+// more warps count for more (4 x 2048 tokens of 4096 channels of 16 states: 144 us with four, 171 with eight).
 template <int MODE> constexpr int kStates = MODE == kSsmKeep ? 4 : 8;
 template <int N, int MODE> constexpr int kWalkWarps = N >= 64 || MODE == kSsmKeep ? 4 : 2;
 template <int N, int MODE> constexpr int kWalkChannels = kWalkWarps<N, MODE> * 32 * kStates<MODE> / N;

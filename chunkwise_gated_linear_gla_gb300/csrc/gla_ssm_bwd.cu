@@ -14,8 +14,8 @@
 // block's warps; a block leaves them as partials per channel tile, added in a fixed order by gla_ssm_bc_sum. No atomics: results are
 // equal bit for bit from call to call.
 //
-// Bound by the multiply-adds' register reads (a packed one of three different pairs takes three cycles) and by waits that two warps
-// a scheduler cannot hide (226 registers, 110 KB a block): four rows of 2048 tokens of 4096 channels of 16 states take 767 us, 24 warp
+// Bound by the multiply-adds' register reads (a packed one of three different pairs takes 3.75 cycles) and by waits that two warps
+// a scheduler cannot hide (226 registers, 110 KB a block): four rows of 2048 tokens of 4096 channels of 16 states take 756 us, 23 warp
 // instructions a state at 45% of the issue slots; per token, channel and state 9 products or multiply-adds back, 4 for h and a again, 3 for
 // the tile's first walk. Preparing and finishing the tiles is 0.2 of it. One channel a thread (twice the warps) took 1.25 times as long.
 #include "gla_ssm.cuh"
