@@ -35,7 +35,7 @@ gla_status check(const gla_ssm_params* p)
 
 struct SsmPlan {
     int nseg = 1, seg = 0;
-    size_t off_sumd = 0, off_segG = 0, off_keep = 0, off_bc = 0, off_p = 0, ws = 0;
+    size_t off_sumd = 0, off_s0 = 0, off_segG = 0, off_keep = 0, off_bc = 0, off_p = 0, ws = 0;
 };
 
 // Segments of the sequence. A walk is serial over its tokens, so few blocks leave SMs idle; cut, they fill the chip evenly, but
@@ -70,6 +70,10 @@ void split(const gla_ssm_params* p, int sms, bool bwd, SsmPlan& pl)
     if (pl.nseg > 1) {
         pl.off_sumd = pl.ws + align_up((pl.nseg - 1) * states);
         pl.ws = pl.off_sumd + align_up((size_t)(pl.nseg - 1) * p->B * p->D * 4);
+    }
+    if (!bwd && pl.nseg > 1) {
+        pl.off_s0 = pl.ws;
+        pl.ws += align_up(states);
     }
     if (bwd) {
         pl.off_segG = pl.ws;
@@ -161,7 +165,12 @@ gla_status gla_ssm_fwd(const gla_ssm_params* p, void* y, float* ST, void* worksp
     if (step) return cuda(launch_ssm_step(a, p->dtype, sms, stream));
     cudaError_t r = cudaSuccess;
     if (pl.nseg > 1) {
-        r = launch_ssm_walk(a, kSsmState, p->dtype, stream);
+        if (ST && ST == p->S0) {     // the last segment's blocks write ST beside the first's, that read S0: those get a copy
+            float* s0 = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.off_s0);
+            r = cudaMemcpyAsync(s0, p->S0, states, cudaMemcpyDeviceToDevice, stream);
+            a.S0 = s0;
+        }
+        if (r == cudaSuccess) r = launch_ssm_walk(a, kSsmState, p->dtype, stream);
         if (r == cudaSuccess && pl.nseg > 2) r = launch_ssm_scan(a, false, sms, stream);
     }
     if (r == cudaSuccess) r = launch_ssm_walk(a, kSsmOut, p->dtype, stream);

@@ -36,7 +36,7 @@ template <int N> constexpr int kOrders = N >= 64 ? 2 : 4;      // (with two grou
 
 // Sums over states are left in shared memory by each of a channel's N / kS threads. Where two blocks would not fit an SM so, they are
 // halved first, once or twice, by exchanges between neighbouring lanes (fp32, 3 x 777 tokens of 1040 channels of 32 states: 174 us with
-// one block an SM, XX so).
+// one block an SM, 114 so; of 8 fp32 states nothing more can be halved: one block).
 template <typename E, int N> constexpr int kHalvings = N >= 64 ? 2 : N == 16 && sizeof(E) == 2 ? 0 : 1;
 
 template <typename E, int N>

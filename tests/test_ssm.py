@@ -154,6 +154,18 @@ def test_decoding_carries_the_state_in_place():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("segments", [2, 3, 20])
+def test_state_in_place_over_segments(segments):
+    """The last segment's blocks write the state that the first's read, in one launch and in any order."""
+    t, _, _ = make(8, 320, 4096, 16, 1, torch.bfloat16, 14)
+    y, ST = gla.selective_scan_forward(**t, force_segments=segments)
+    for _ in range(3):
+        state = t["S0"].clone()
+        y2, _ = gla.selective_scan_forward(**{**t, "S0": state}, ST=state, force_segments=segments)
+        assert torch.equal(y2, y) and torch.equal(state, ST)
+
+
+@pytest.mark.gpu
 def test_empty_sequence_and_broadcast_rows():
     t, dy, dST = make(2, 4, 32, 16, 1, torch.float32, 12)
     none = {k: (a[:, :0] if k in ("x", "dt", "B", "C", "z") else a) for k, a in t.items()}
@@ -254,6 +266,8 @@ def test_workspaces():
     assert lib.gla_ssm_fwd_workspace_size(big) == 0                                # channels enough: one walk
     few = _params(T=2048, force_segments=4)
     assert lib.gla_ssm_fwd_workspace_size(few) >= 3 * 2 * 64 * 16 * 4
+    # three segments' states and sums, and a copy of S0 for the call that writes ST over it
+    assert lib.gla_ssm_fwd_workspace_size(few) >= (3 + 1) * 2 * 64 * 16 * 4 + 3 * 2 * 64 * 4
     assert lib.gla_ssm_fwd_workspace_size(_params()) == 0                          # eight tokens: the step form
     assert lib.gla_ssm_bwd_workspace_size(_params(T=17)) >= 2 * 2 * 64 * 16 * 4    # the states of two tiles
 
