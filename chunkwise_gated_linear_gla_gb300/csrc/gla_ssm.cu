@@ -106,6 +106,25 @@ template <int MODE> constexpr int kStates = MODE == kSsmKeep ? 4 : 8;
 template <int N, int MODE> constexpr int kWalkWarps = N >= 64 || MODE == kSsmKeep ? 4 : 2;
 template <int N, int MODE> constexpr int kWalkChannels = kWalkWarps<N, MODE> * 32 * kStates<MODE> / N;
 
+// A thread's states of a channel, from the first of them on: by fours N / 2 apart, so that neighbouring lanes read neighbouring 16
+// bytes.
+template <int N, int S>
+__device__ __forceinline__ void pick(const float* p, f2 (&r)[S / 2])
+{
+#pragma unroll
+    for (int i = 0; i < S / 4; ++i) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(p + i * (N / 2));
+        r[2 * i] = q.x;
+        r[2 * i + 1] = q.y;
+    }
+}
+template <int N, int S>
+__device__ __forceinline__ void drop(float* p, const f2 (&r)[S / 2])
+{
+#pragma unroll
+    for (int i = 0; i < S / 4; ++i) *reinterpret_cast<ulonglong2*>(p + i * (N / 2)) = make_ulonglong2(r[2 * i], r[2 * i + 1]);
+}
+
 template <typename E, int N, int MODE>
 struct WalkShared {
     static constexpr int CB = kWalkChannels<N, MODE>;
@@ -159,7 +178,7 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
     const int sg = threadIdx.x % Q, cl = threadIdx.x / Q;
     const bool on = c0 + cl < c1;
     f2 h[kS / 2], A[kS / 2];
-    const size_t per = (size_t)a.D * N, so = (size_t)(on ? c0 + cl : c0) * N + sg * kS;
+    const size_t per = (size_t)a.D * N, so = (size_t)(on ? c0 + cl : c0) * N + sg * 4;
     const float* from = nullptr;          // this batch row's states, [D][N]
     if (REV) {
         if (seg == a.nseg - 1 && a.dST) from = a.dST + b * per;
@@ -167,13 +186,13 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
         if (seg > 0) from = a.segS + ((size_t)b * (a.nseg - 1) + seg - 1) * per;
         else if (a.S0) from = a.S0 + b * per;
     }
-    states<kS>(a.A + so, A);
+    pick<N, kS>(a.A + so, A);
 #pragma unroll
     for (int j = 0; j < kS / 2; ++j) {
         A[j] = mul2(A[j], both(kLog2e));
         h[j] = 0ull;
     }
-    if (from) states<kS>(from + so, h);
+    if (from) pick<N, kS>(from + so, h);
     // the vectors of eight channels that this thread prepares and finishes: always the same channels
     constexpr int COLS = CB / VEC, VPT = TT * COLS;
     const int vc = threadIdx.x % COLS * VEC;
@@ -223,11 +242,8 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
 #pragma unroll 1
         for (int sub = REV ? TT - parts : 0; sub < (REV ? TT : parts); sub += SUB) {
             const int base = REV ? TT - SUB - sub : sub;
-            if (MODE == kSsmKeep && on) {
-                float* k = a.keep + ((size_t)b * ((a.T + SUB - 1) / SUB) + (t0 + base) / SUB) * per + so;
-#pragma unroll
-                for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(k + 2 * j) = make_ulonglong2(h[j], h[j + 1]);
-            }
+            if (MODE == kSsmKeep && on)
+                drop<N, kS>(a.keep + ((size_t)b * ((a.T + SUB - 1) / SUB) + (t0 + base) / SUB) * per + so, h);
             // What these tokens themselves add runs beside the states (hl, from zero); at their end the state that entered takes
             // their whole decay at once. So a long memory is rounded once per 16 tokens, not at every one.
             f2 in[kS / 2], hl[kS / 2];
@@ -244,8 +260,8 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
                 const int tok = base + (REV ? SUB - 1 - n : n);
                 p.d = sm.work[0][tok * P + cl];
                 p.x = sm.work[1][tok * P + cl];
-                states<kS>(&sm.wide[0][tok][sg * kS], p.B);
-                if (OUT) states<kS>(&sm.wide[IC][tok][sg * kS], p.C);
+                pick<N, kS>(&sm.wide[0][tok][sg * 4], p.B);
+                if (OUT) pick<N, kS>(&sm.wide[IC][tok][sg * 4], p.C);
             };
             auto form = [&](Token& p) {
                 sd += p.d;
@@ -260,8 +276,12 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
                 f2 s = 0ull;
 #pragma unroll
                 for (int j = 0; j < kS / 2; ++j) {
-                    if (OUT) h[j] = fma2(p.e[j], h[j], p.u[j]);
-                    hl[j] = fma2(p.e[j], hl[j], p.u[j]);
+                    if (OUT) {
+                        h[j] = fma2(p.e[j], h[j], p.u[j]);
+                        hl[j] = n ? mul2(hl[j], p.e[j]) : p.e[j];
+                    } else {
+                        hl[j] = n ? fma2(p.e[j], hl[j], p.u[j]) : p.u[j];
+                    }
                     if (OUT) s = fma2(h[j], p.C[j], s);
                 }
                 if (OUT) {
@@ -284,7 +304,10 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
                 use(n, p[n % 3]);
             }
 #pragma unroll
-            for (int j = 0; j < kS / 2; ++j) h[j] = fma2(ex2_2(mul2(both(sd), A[j])), in[j], hl[j]);
+            for (int j = 0; j < kS / 2; ++j) {
+                const f2 e = ex2_2(mul2(both(sd), A[j]));
+                h[j] = OUT ? fma2(fma2(hl[j], both(-1.f), e), in[j], h[j]) : fma2(e, in[j], hl[j]);
+            }
         }
         if (!OUT) continue;
         __syncthreads();
@@ -314,10 +337,7 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
     if (OUT && seg == a.nseg - 1 && a.ST) to = a.ST + b * per;
     if (MODE == kSsmState) to = a.segS + ((size_t)b * (a.nseg - 1) + seg) * per;
     if (REV) to = a.segG + ((size_t)b * (a.nseg - 1) + seg - 1) * per;
-    if (to && on) {
-#pragma unroll
-        for (int j = 0; j < kS / 2; j += 2) *reinterpret_cast<ulonglong2*>(to + so + 2 * j) = make_ulonglong2(h[j], h[j + 1]);
-    }
+    if (to && on) drop<N, kS>(to + so, h);
     if (MODE == kSsmState) {
         // the sums of delta over the threads that prepared the same channels, in order
         __syncthreads();

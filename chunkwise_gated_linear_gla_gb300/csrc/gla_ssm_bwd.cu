@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
 #pragma unroll
             for (int j = 0; j < kS / 2; ++j) {
                 Gin[i][j] = G[i][j];
-                Gl[i][j] = pk(0.f, 0.f);
+                Gl[i][j] = both(1.f);
             }
         }
         // dB, dC of a token over the warp's channels: the lanes with the same states (GROUPS of them) halve what they hold, giving
@@ -327,11 +327,11 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                         const f2 hp = n ? h[n - 1][i][j] : in[i][j];
                         ys = fma2(h[n][i][j], t.C[j], ys);
                         dC[j] = i ? fma2(h[n][i][j], r2, dC[j]) : mul2(h[n][i][j], r2);
-                        const f2 gg = fma2(r2, t.C[j], G[i][j]), gl = fma2(r2, t.C[j], Gl[i][j]);
+                        const f2 gg = fma2(r2, t.C[j], G[i][j]);
                         ps = fma2(gg, t.B[j], ps);
                         dB[j] = i ? fma2(gg, x2, dB[j]) : mul2(gg, x2);
                         G[i][j] = mul2(ea[n][i][j], gg);      // what goes on to the token before
-                        Gl[i][j] = mul2(ea[n][i][j], gl);
+                        Gl[i][j] = mul2(ea[n][i][j], Gl[i][j]);
                         const f2 q = mul2(G[i][j], hp);
                         es = fma2(q, A[i][j], es);
                         dA[i][j] = fma2(q, d2, dA[i][j]);
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
 #pragma unroll
         for (int i = 0; i < kC; ++i)
 #pragma unroll
-            for (int j = 0; j < kS / 2; ++j) G[i][j] = fma2(ex2_2(mul2(pk(sd[i], sd[i]), A[i][j])), Gin[i][j], Gl[i][j]);
+            for (int j = 0; j < kS / 2; ++j) G[i][j] = fma2(fma2(Gl[i][j], both(-1.f), ex2_2(mul2(both(sd[i]), A[i][j]))), Gin[i][j], G[i][j]);
         // dA of four tiles at a time into the sum of all: a sum of few terms is added to one of many
         if (on && tile % 4 == 0) {
             const bool begun = tile / 4 != (tiles - 1) / 4;
