@@ -7,9 +7,9 @@
 // multiply-adds, all fp32, the states in registers from the first token to the last.
 //
 // gla_ssm_walk: a thread holds eight states of a channel and walks the tokens, its products packed pairs of states. The block goes
-// in tiles of 32 tokens: raw rows arrive by asynchronous copies one tile ahead, delta and delta x are formed once per channel
-// and token into shared memory, B and C widened there, the walk leaves C . h in their places, and y is formed from it eight
-// channels at a time. Bound by issue: eight rows of 2048 tokens of 4096 channels of 16 states (1.07e9 of them, 0.54 GB) take
+// in tiles of 32 tokens (16 where they would take too much room): raw rows arrive by asynchronous copies one tile ahead, delta and
+// delta x are formed once per channel and token into shared memory, B and C widened there, the walk leaves C . h in their places, and y
+// is formed from it eight channels at a time. Bound by issue: eight rows of 2048 tokens of 4096 channels of 16 states (1.07e9 of them, 0.54 GB) take
 // 396 us at 7.7 warp instructions a state, 59% of the issue slots and 70% on the schedulers that got four warps, not three; the bytes
 // would take 80, the exponentials 107. Two blocks of two warps measured better than one of four (407 us) and tiles of 32 better than 16
 // (414) and 64 (530).
@@ -99,7 +99,10 @@ __global__ void __launch_bounds__(kStepNT) gla_ssm_step_kernel(SsmArgs a)
 
 // ------------------------------------------------------------------ the walk
 
-constexpr int kWalkTile = 32;      // tokens per tile of loads: two of the kept states' tiles
+// Tokens per tile of loads: two of the kept states' tiles, or one where the rows of so many channels would leave an SM half its blocks
+// (8 x 2048 tokens of 8192 channels of 8 states: 566 us with 32, 485 with 16, fp32 716 and 632; 4096 of 16 390 and 403, fp32 477 and
+// 411; 2048 of 32 402 and 442, fp32 482 and 461 but of half the rows 257 and 293).
+template <typename E, int N> constexpr int kWalkTile = N == 8 || (N == 16 && sizeof(E) == 4) ? 16 : 32;
 // States of a thread: B and C are read once for eight. The walk that keeps states runs uncut with the few blocks of a training batch, where
 // more warps count for more (4 x 2048 tokens of 4096 channels of 16 states: 144 us with four, 171 with eight).
 template <int MODE> constexpr int kStates = MODE == kSsmKeep ? 4 : 8;
@@ -127,22 +130,22 @@ __device__ __forceinline__ void drop(float* p, const f2 (&r)[S / 2])
 
 template <typename E, int N, int MODE>
 struct WalkShared {
-    static constexpr int CB = kWalkChannels<N, MODE>;
+    static constexpr int CB = kWalkChannels<N, MODE>, TT = kWalkTile<E, N>;
     static constexpr bool HAS_B = MODE != kSsmRev, HAS_C = MODE == kSsmOut || MODE == kSsmRev, HAS_Z = HAS_C;
-    E raw[2][HAS_Z ? 3 : 2][kWalkTile][CB];   // x, dt, z (REV: dy, dt, z)
-    E bc[2][HAS_B + HAS_C][kWalkTile][N];
-    float wide[HAS_B + HAS_C][kWalkTile][N];  // B, C of the tile in fp32
+    E raw[2][HAS_Z ? 3 : 2][TT][CB];   // x, dt, z (REV: dy, dt, z)
+    E bc[2][HAS_B + HAS_C][TT][N];
+    float wide[HAS_B + HAS_C][TT][N];  // B, C of the tile in fp32
     // delta, delta x (REV: dy silu(z)); a token's places take the two halves of its C . h once it has been walked
     // (rows four values further on each time, the second half 64 bytes: no store meets a bank twice)
     static constexpr int P = CB + 4;
-    float work[2][kWalkTile * P + 16];
+    float work[2][TT * P + 16];
 };
 
 template <typename E, int N, int MODE>
 __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14 / kWalkWarps<N, MODE> : 1) gla_ssm_walk_kernel(SsmArgs a)
 {
     typedef WalkShared<E, N, MODE> Shared;
-    constexpr int NT = kWalkWarps<N, MODE> * 32, CB = kWalkChannels<N, MODE>, P = Shared::P, kS = kStates<MODE>, Q = N / kS, TT = kWalkTile, SUB = kSsmTile;
+    constexpr int NT = kWalkWarps<N, MODE> * 32, CB = kWalkChannels<N, MODE>, P = Shared::P, kS = kStates<MODE>, Q = N / kS, TT = kWalkTile<E, N>, SUB = kSsmTile;
     constexpr bool REV = MODE == kSsmRev, OUT = MODE == kSsmOut;
     constexpr int IC = Shared::HAS_B ? 1 : 0;      // where C lies beside B
     extern __shared__ __align__(16) char smem_raw[];
@@ -244,14 +247,15 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
             const int base = REV ? TT - SUB - sub : sub;
             if (MODE == kSsmKeep && on)
                 drop<N, kS>(a.keep + ((size_t)b * ((a.T + SUB - 1) / SUB) + (t0 + base) / SUB) * per + so, h);
-            // What these tokens themselves add runs beside the states (hl, from zero); at their end the state that entered takes
-            // their whole decay at once. So a long memory is rounded once per 16 tokens, not at every one.
-            f2 in[kS / 2], hl[kS / 2];
+            // At the end of these tokens the state that entered takes their whole decay at once, so that a long memory is rounded once
+            // per 16 tokens, not at every one. Beside the states runs what they multiply it by, the product of the decays; where the states
+            // between are not wanted, only what the tokens themselves add (from zero).
+            f2 in[kS / 2], beside[kS / 2];
             float sd = 0.f;
 #pragma unroll
             for (int j = 0; j < kS / 2; ++j) {
                 in[j] = h[j];
-                hl[j] = 0ull;
+                beside[j] = 0ull;
             }
             // A token in three steps, so that no wait for shared memory or an exponential is seen: its operands are fetched two
             // tokens ahead, its decays and inputs formed one ahead.
@@ -278,9 +282,9 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
                 for (int j = 0; j < kS / 2; ++j) {
                     if (OUT) {
                         h[j] = fma2(p.e[j], h[j], p.u[j]);
-                        hl[j] = n ? mul2(hl[j], p.e[j]) : p.e[j];
+                        beside[j] = n ? mul2(beside[j], p.e[j]) : p.e[j];
                     } else {
-                        hl[j] = n ? fma2(p.e[j], hl[j], p.u[j]) : p.u[j];
+                        beside[j] = n ? fma2(p.e[j], beside[j], p.u[j]) : p.u[j];
                     }
                     if (OUT) s = fma2(h[j], p.C[j], s);
                 }
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
 #pragma unroll
             for (int j = 0; j < kS / 2; ++j) {
                 const f2 e = ex2_2(mul2(both(sd), A[j]));
-                h[j] = OUT ? fma2(fma2(hl[j], both(-1.f), e), in[j], h[j]) : fma2(e, in[j], hl[j]);
+                h[j] = OUT ? fma2(fma2(beside[j], both(-1.f), e), in[j], h[j]) : fma2(e, in[j], beside[j]);
             }
         }
         if (!OUT) continue;

@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
             for (int n = 0; n < PART; ++n) ahead(part * PART + n, in, ea[0], in);
         }
 
-        // As the states in the walk, G takes the tile's decay at once: what the tile adds runs beside it (Gl, from zero).
-        f2 Gin[kC][kS / 2], Gl[kC][kS / 2];
+        // As the states in the walk, G takes the tile's decay at once in the end: the product of the decays runs beside it.
+        f2 Gin[kC][kS / 2], run[kC][kS / 2];
         float sd[kC];
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
 #pragma unroll
             for (int j = 0; j < kS / 2; ++j) {
                 Gin[i][j] = G[i][j];
-                Gl[i][j] = both(1.f);
+                run[i][j] = both(1.f);
             }
         }
         // dB, dC of a token over the warp's channels: the lanes with the same states (GROUPS of them) halve what they hold, giving
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                         ps = fma2(gg, t.B[j], ps);
                         dB[j] = i ? fma2(gg, x2, dB[j]) : mul2(gg, x2);
                         G[i][j] = mul2(ea[n][i][j], gg);      // what goes on to the token before
-                        Gl[i][j] = mul2(ea[n][i][j], Gl[i][j]);
+                        run[i][j] = mul2(ea[n][i][j], run[i][j]);
                         const f2 q = mul2(G[i][j], hp);
                         es = fma2(q, A[i][j], es);
                         dA[i][j] = fma2(q, d2, dA[i][j]);
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
 #pragma unroll
         for (int i = 0; i < kC; ++i)
 #pragma unroll
-            for (int j = 0; j < kS / 2; ++j) G[i][j] = fma2(fma2(Gl[i][j], both(-1.f), ex2_2(mul2(both(sd[i]), A[i][j]))), Gin[i][j], G[i][j]);
+            for (int j = 0; j < kS / 2; ++j) G[i][j] = fma2(fma2(run[i][j], both(-1.f), ex2_2(mul2(both(sd[i]), A[i][j]))), Gin[i][j], G[i][j]);
         // dA of four tiles at a time into the sum of all: a sum of few terms is added to one of many
         if (on && tile % 4 == 0) {
             const bool begun = tile / 4 != (tiles - 1) / 4;
