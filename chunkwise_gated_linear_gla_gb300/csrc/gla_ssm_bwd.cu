@@ -52,7 +52,7 @@ struct BwdShared {
     // neighbouring eights, still meet every bank once.
     static constexpr int HALF = CB / 2, TURN = CB >= 64 ? 4 : 0;
     float delta[TT][CB], dx[TT][CB], r[TT][CB];
-    float part[3][PQ][TT * CB + 256 / N];     // y, p, e over states
+    float part[3][PQ][TT * CB + (N > 32 ? 4 : 128 / N)];     // y, p, e over states, 128 / N places further on each time: stores of a warp meet few banks twice
     float red[kWarps][TT][2 * N];             // dB, dC over each warp's channels
 };
 
