@@ -52,7 +52,7 @@ struct BwdShared {
     // neighbouring eights, still meet every bank once.
     static constexpr int HALF = CB / 2, TURN = CB >= 64 ? 4 : 0;
     float delta[TT][CB], dx[TT][CB], r[TT][CB];
-    float part[3][PQ][TT * CB + (N > 32 ? 4 : 128 / N)];     // y, p, e over states, 128 / N places further on each time: stores of a warp meet few banks twice
+    float part[3][PQ][TT * CB + (kHalvings<E, N> == 0 || N > 32 ? 4 : 128 / N)];     // y, p, e over states, rows so far apart that a warp's stores meet no bank twice
     float red[kWarps][TT][2 * N];             // dB, dC over each warp's channels
 };
 
@@ -341,17 +341,14 @@ __global__ void __launch_bounds__(NT, 2) gla_ssm_bwd_kernel(SsmArgs a)
                         else sum_last();
                     }
                     // y, p, e of the channel over this thread's states
-                    if constexpr (HALVINGS == 0) {
-                        sm.part[0][sg][tok * CB + cp + i] = sum2(ys);
-                        sm.part[1][sg][tok * CB + cp + i] = sum2(ps);
-                        sm.part[2][sg][tok * CB + cp + i] = sum2(es);
-                    } else {
-                        const float sums[3] = {sum2(ys), sum2(ps), sum2(es)};
+                    const float sums[3] = {sum2(ys), sum2(ps), sum2(es)};
 #pragma unroll
-                        for (int k = 0; k < 3; ++k) of[k][i] = sums[k];
-                    }
+                    for (int k = 0; k < 3; ++k) of[k][i] = sums[k];
                 }
-                if constexpr (HALVINGS > 0) {
+                if constexpr (HALVINGS == 0) {
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) *reinterpret_cast<float2*>(&sm.part[k][sg][tok * CB + cp]) = make_float2(of[k][0], of[k][1]);
+                } else {
                     const bool odd = sg & 1;               // a pair of lanes keeps one channel each
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
