@@ -31,7 +31,7 @@ template <int N> constexpr int kBwdChannels = NT * kS * kC / N;
 
 // A thread's four states of a channel are taken in the order n ^ m, m from its lane: then what the lanes exchange when they
 // sum over the warp's channels lies at the same place in all of them. B and C of a tile lie in shared memory once in each order,
-// 64 bytes further on each time, so that the orders' reads meet no bank twice.
+// 64 bytes (of 8 states 32) further on each time, so that the orders' reads meet no bank twice.
 template <int N> constexpr int kOrders = N >= 64 ? 2 : 4;      // (with two groups of lanes only pairs are exchanged)
 
 // Sums over states are left in shared memory by each of a channel's N / kS threads. Where two blocks would not fit an SM so, they are
@@ -44,7 +44,7 @@ struct BwdShared {
     static constexpr int CB = kBwdChannels<N>, Q = N / kS, PQ = Q >> kHalvings<E, N>;
     E raw[2][4][TT][CB];                      // x, dt, z, dy
     E bc[2][2][TT][N];
-    float wide[2][kOrders<N>][TT * N + 16];   // B, C
+    float wide[2][kOrders<N>][TT * N + (N == 8 ? 8 : 16)];   // B, C
     // the states entering the tile (two tiles' in turn), and its parts but the first and the last, as each thread reads them
     float keep[2][kC][NT * 4], mid[TT / PART - 2][kC][NT * 4];
     // Rows of a value per channel: the first four of every eight channels, then the other four, with the eights 0 - 3 and 4 - 7
