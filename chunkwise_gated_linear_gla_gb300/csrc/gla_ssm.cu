@@ -10,13 +10,12 @@
 // in tiles of 32 tokens (16 where they would take too much room): raw rows arrive by asynchronous copies one tile ahead, delta and
 // delta x are formed once per channel and token into shared memory, B and C widened there, the walk leaves C . h in their places, and y
 // is formed from it eight channels at a time. Bound by issue: eight rows of 2048 tokens of 4096 channels of 16 states (1.07e9 of them, 0.54 GB) take
-// 396 us at 7.7 warp instructions a state, 59% of the issue slots and 70% on the schedulers that got four warps, not three; the bytes
-// would take 80, the exponentials 107. Two blocks of two warps measured better than one of four (407 us) and tiles of 32 better than 16
-// (414) and 64 (530).
+// 389 us at 7.7 warp instructions a state, 61% of the issue slots and 70% on the schedulers that got four warps, not three; the bytes
+// would take 80, the exponentials 107. Two blocks of two warps measured better than one of four (by 3%).
 //
 // Few channels: the sequence is cut into segments. A first walk leaves each segment's state from zero and its sum of delta
 // (the decay across the segment is exp(A sum)), gla_ssm_scan the states entering them, a second walk y (one row of 16421
-// tokens: 216 + 14 + 349 us in 23 segments).
+// tokens: 213 + 14 + 341 us in 23 segments).
 //
 // gla_ssm_step: single and few tokens, bound by the states' bytes and their latency: a thread holds four states of a channel, of four
 // batch rows where there are many (the next token of 128 rows: 16 us, 4.4 TB/s).

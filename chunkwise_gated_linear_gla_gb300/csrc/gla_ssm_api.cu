@@ -39,13 +39,13 @@ struct SsmPlan {
 };
 
 // Segments of the sequence. A walk is serial over its tokens, so few blocks leave SMs idle; cut, they fill the chip evenly, but
-// the tokens are walked twice (backward: three times more in part). Uncut, a walk of up to 1.7 blocks an SM takes 0.09 us a token, 0.115 at
-// 2.5, 0.12 at 3.4; cut so that there are twenty blocks an SM in all, 2.8e-4 us a block: equal at 2.6 an SM (rows of
-// 4096 channels of 16 states, caches flushed: one of 16421 tokens 1450 us uncut, 641 in 8 segments, 600 in 23; three of 4096 472
-// uncut, 428 in 8). The backward's larger blocks take 0.37 us a token up to one an SM and 0.51 up to two, and 2.2e-3 us each when
-// cut so that there are seven an SM: equal at 1.5 an SM (one row of 2048 tokens 761 us uncut, 334 in 16; two 766 and 598). Segments
-// are four tiles or more (two rows of 2048 tokens of 1536 channels of 8 states: 62 us in 32 segments, 73 in 64), two where the chip
-// is not filled otherwise (one row of 256 tokens of 1024 channels: 26 us uncut, 14 in 8, 17 in 16).
+// the tokens are walked twice (backward: three times more in part). Uncut, a walk of up to 1.7 blocks an SM takes 0.08 us a token, 0.107 at
+// 2.5, 0.11 at 3.4; cut so that there are twenty blocks an SM in all, 2.6e-4 us a block: equal at 2.7 an SM (rows of
+// 4096 channels of 16 states: one of 16421 tokens 1292 us uncut, 582 in 8 segments, 562 in 23; three of 4096 439
+// uncut, 404 in 8). The backward's larger blocks take 0.28 us a token up to one an SM and 0.42 up to two, and 2e-3 us each when
+// cut so that there are seven an SM: equal at 1.4 an SM (one row of 2048 tokens 567 us uncut, 295 in 16; two 600 and 519). Segments
+// are four tiles or more (two rows of 2048 tokens of 1536 channels of 8 states: 52 us in 32 segments, 60 in 64), two where the chip
+// is not filled otherwise (one row of 256 tokens of 1024 channels: 24 us uncut, 13 in 8, 15 in 16).
 void split(const gla_ssm_params* p, int sms, bool bwd, SsmPlan& pl)
 {
     const int CB = bwd ? ssm_bwd_channels(p->N) : ssm_walk_channels(p->N);
@@ -54,7 +54,7 @@ void split(const gla_ssm_params* p, int sms, bool bwd, SsmPlan& pl)
     long long n = p->force_segments;
     if (n == 0) {
         const long long units = bwd ? blocks : blocks * ssm_walk_warps(p->N) / 2;    // (blocks of two warps)
-        n = 10 * units < (bwd ? 15LL : 26LL) * sms ? (bwd ? 7LL : 20LL) * sms / units : 1;
+        n = 10 * units < (bwd ? 14LL : 27LL) * sms ? (bwd ? 7LL : 20LL) * sms / units : 1;
         const long long filled = 7LL * sms / units, most = tiles / 2 < filled ? tiles / 2 : filled;
         if (n > tiles / 4) n = most > tiles / 4 ? most : tiles / 4;
     }

@@ -15,8 +15,8 @@
 // equal bit for bit from call to call.
 //
 // Bound by the multiply-adds' register reads (a packed one of three different pairs takes 3.75 cycles) and by waits that two warps
-// a scheduler cannot hide (226 registers, 110 KB a block): four rows of 2048 tokens of 4096 channels of 16 states take 756 us, 23 warp
-// instructions a state at 45% of the issue slots; per token, channel and state 9 products or multiply-adds back, 4 for h and a again, 3 for
+// a scheduler cannot hide (228 registers, 111 KB a block): four rows of 2048 tokens of 4096 channels of 16 states take 705 us, 22 warp
+// instructions a state at 47% of the issue slots; per token, channel and state 10 products or multiply-adds back, 4 for h and a again, 3 for
 // the tile's first walk. Preparing and finishing the tiles is 0.2 of it. One channel a thread (twice the warps) took 1.25 times as long.
 #include "gla_ssm.cuh"
 
@@ -36,7 +36,7 @@ template <int N> constexpr int kOrders = N >= 64 ? 2 : 4;      // (with two grou
 
 // Sums over states are left in shared memory by each of a channel's N / kS threads. Where two blocks would not fit an SM so, they are
 // halved first, once or twice, by exchanges between neighbouring lanes (fp32, 3 x 777 tokens of 1040 channels of 32 states: 174 us with
-// one block an SM, 114 so; of 8 fp32 states nothing more can be halved: one block).
+// one block an SM, 111 so; of 8 fp32 states nothing more can be halved: one block).
 template <typename E, int N> constexpr int kHalvings = N >= 64 ? 2 : N == 16 && sizeof(E) == 2 ? 0 : 1;
 
 template <typename E, int N>
