@@ -62,23 +62,36 @@ __device__ __forceinline__ void sum_row(float& a, float& b, float2 (*red)[NTR / 
 }
 
 template <typename E, typename R, int NTR, int K, bool BWD>
-__global__ void __launch_bounds__(NTR == 32 ? 32 * kWarps : NTR, NTR == 32 ? 1 : BWD && K < 4 ? 512 / NTR : 1)
+__global__ void __launch_bounds__(NTR == 32 ? 32 * kWarps : NTR, NTR == 32 ? 1 : BWD ? K < 4 ? 512 / NTR : 1 : NTR == 512 && K < 4 ? 2 : 1)
 gla_residual_norm_kernel(ResArgs a)
 {
     __shared__ float2 red[2][NTR / 32 + 1];
     int turn = 0;
     constexpr int RPB = NTR == 32 ? kWarps : 1;
+    // The widest rows have one block to an SM. Its registers take the next row as soon as h is formed, before the row's sum and stores
+    // (4096 bf16 rows of 16384 values 127 us a row at a time, 96 so); backward the vectors' sums lie in shared memory, each thread's
+    // in places of its own (326 us with what the registers do not hold spilled, 271 so). Clusters of two and four blocks to a row, each
+    // with 4096 values of it, wait longer for each other's sums: 194 and 594 us.
+    constexpr bool AHEAD = !BWD && K == 4, SHARED = BWD && K == 4;
+    extern __shared__ __align__(16) ulonglong2 sums_of[];         // [dw, ds][K][2][NTR]
     const int l = threadIdx.x % NTR;
     const float invn = 1.f / (float)a.D;
     bool in[K];
-    f2 dw[BWD ? K : 1][4], ds[BWD ? K : 1][4];
+    f2 dw[BWD && !SHARED ? K : 1][4], ds[BWD && !SHARED ? K : 1][4];
+    auto sums = [&](int which, int k, int half) -> ulonglong2& { return sums_of[((which * K + k) * 2 + half) * NTR + threadIdx.x]; };
 #pragma unroll
     for (int k = 0; k < K; ++k) in[k] = (k * NTR + l) * VEC < a.D;
-    if constexpr (BWD)
+    if constexpr (BWD) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            if constexpr (SHARED) {
+                sums(0, k, 0) = sums(0, k, 1) = sums(1, k, 0) = sums(1, k, 1) = make_ulonglong2(0ull, 0ull);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dw[k][j] = ds[k][j] = 0ull;
+                for (int j = 0; j < 4; ++j) dw[k][j] = ds[k][j] = 0ull;
+            }
+        }
+    }
     // eight values of a vector (1 without it), times c
     auto vec = [&](const float* p, int k, float c, f2 (&f)[4]) {
         const float* q = p + (k * NTR + l) * VEC;
@@ -97,19 +110,24 @@ gla_residual_norm_kernel(ResArgs a)
     };
 
     const long long step = (long long)gridDim.x * RPB;
-    for (long long row = (long long)blockIdx.x * RPB + (NTR == 32 ? threadIdx.x / 32 : 0); row < a.rows; row += step) {
-        const long long at = row * a.D + l * VEC;
-        typename Raw<E>::type xr[K], yr[K];
-        typename Raw<R>::type rr[K], hr[K];
+    long long row = (long long)blockIdx.x * RPB + (NTR == 32 ? threadIdx.x / 32 : 0);
+    typename Raw<E>::type xr[K], yr[BWD ? K : 1];
+    typename Raw<R>::type rr[K], hr[BWD ? K : 1];
+    auto load = [&](auto& to, const auto* from, long long of) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const long long o = at + k * NTR * VEC;
-            xr[k] = fetch(in[k] ? static_cast<const E*>(a.x) + o : nullptr);
-            rr[k] = fetch(in[k] && a.r ? static_cast<const R*>(a.r) + o : nullptr);
-            if constexpr (BWD) {
-                yr[k] = fetch(in[k] && a.dy ? static_cast<const E*>(a.dy) + o : nullptr);
-                hr[k] = fetch(in[k] && a.dh ? static_cast<const R*>(a.dh) + o : nullptr);
-            }
+        for (int k = 0; k < K; ++k) to[k] = fetch(from && in[k] && of < a.rows ? from + of * a.D + (k * NTR + l) * VEC : nullptr);
+    };
+    auto load_xr = [&](long long of) {
+        load(xr, static_cast<const E*>(a.x), of);
+        load(rr, static_cast<const R*>(a.r), of);
+    };
+    if (AHEAD) load_xr(row);
+    for (; row < a.rows; row += step) {
+        const long long at = row * a.D + l * VEC;
+        if (!AHEAD) load_xr(row);
+        if constexpr (BWD) {
+            load(yr, static_cast<const E*>(a.dy), row);
+            if (!SHARED) load(hr, static_cast<const R*>(a.dh), row);
         }
         float invx = 1.f, none = 0.f;
         if (a.post) {
@@ -146,6 +164,8 @@ gla_residual_norm_kernel(ResArgs a)
                 for (int j = 0; j < 4; ++j) m2 = fma2(mul2(g[j], wv[j]), h[k][j], m2);
             }
         }
+        if (AHEAD) load_xr(row + step);
+        if constexpr (SHARED) load(hr, static_cast<const R*>(a.dh), row);      // (into r's registers)
         float s = sum2(s2), m = sum2(m2);
         sum_row<NTR, BWD>(s, m, red, turn);
         const float inv = rsqrtf(fmaf(s, invn, a.eps));
@@ -172,14 +192,27 @@ gla_residual_norm_kernel(ResArgs a)
                 wide(hr[k], d);
                 vec(a.w, k, 1.f, wv);
                 vec(a.scale, k, 1.f, sc);
+                f2 dwk[4], dsk[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const f2 hh = mul2(h[k][j], i2);
-                    dw[k][j] = fma2(g[j], hh, dw[k][j]);
+                    if constexpr (SHARED) dwk[j] = mul2(g[j], hh);
+                    else dw[k][j] = fma2(g[j], hh, dw[k][j]);
                     h[k][j] = fma2(i2, fma2(hh, mm, mul2(g[j], wv[j])), d[j]);        // dr
                     const f2 p = mul2(h[k][j], x[j]);
-                    ds[k][j] = fma2(p, both(invx), ds[k][j]);
+                    if constexpr (SHARED) dsk[j] = mul2(p, both(invx));
+                    else ds[k][j] = fma2(p, both(invx), ds[k][j]);
                     q2 = fma2(p, sc[j], q2);
+                }
+                if constexpr (SHARED) {
+                    if (a.part) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            ulonglong2 &u = sums(0, k, half), &v = sums(1, k, half);
+                            u = make_ulonglong2(add2(u.x, dwk[2 * half]), add2(u.y, dwk[2 * half + 1]));
+                            v = make_ulonglong2(add2(v.x, dsk[2 * half]), add2(v.y, dsk[2 * half + 1]));
+                        }
+                    }
                 }
                 if (in[k] && a.dr) keep8(static_cast<R*>(a.dr) + at + k * NTR * VEC, h[k]);
             }
@@ -205,11 +238,24 @@ gla_residual_norm_kernel(ResArgs a)
     }
     if constexpr (BWD) {
         if (!a.part) return;
+        if constexpr (!SHARED) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+            for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) ds[k][j] = mul2(ds[k][j], both(a.alpha));
-        if constexpr (NTR > 32) {
+                for (int j = 0; j < 4; ++j) ds[k][j] = mul2(ds[k][j], both(a.alpha));
+        }
+        if constexpr (SHARED) {
+            float* p = a.part + (size_t)blockIdx.x * 2 * a.D;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!in[k]) continue;
+                const ulonglong2 u = sums(0, k, 0), v = sums(0, k, 1), y = sums(1, k, 0), z = sums(1, k, 1);
+                const f2 dwk[4] = {u.x, u.y, v.x, v.y}, al = both(a.alpha);
+                const f2 dsk[4] = {mul2(y.x, al), mul2(y.y, al), mul2(z.x, al), mul2(z.y, al)};
+                keep8(p + (k * NTR + l) * VEC, dwk);
+                keep8(p + a.D + (k * NTR + l) * VEC, dsk);
+            }
+        } else if constexpr (NTR > 32) {
             float* p = a.part + (size_t)blockIdx.x * 2 * a.D;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -239,10 +285,19 @@ long long blocks_of(long long rows, int D, int sms, bool bwd)
     const long long n = D <= kWarpD ? (rows + kWarps - 1) / kWarps : rows;
     // backward: as many blocks as are resident, a partial row of both sums each
     const long long per = D <= kWarpD ? 2 : D <= 1024 ? 8 : D <= 2048 ? 4 : D <= 4096 ? 2 : 1;
-    const long long most = bwd ? per * sms : 0x7fffffff;
+    const long long most = bwd ? per * sms : D > 8192 ? sms : 0x7fffffff;
     return n < most ? n : most;
 }
 
+template <typename E, typename R, bool BWD>
+cudaError_t launch_widest(const ResArgs& a, unsigned blocks, cudaStream_t s)
+{
+    constexpr int NTR = 512, K = 4, n = BWD ? 2 * K * 2 * NTR * (int)sizeof(ulonglong2) : 0;
+    const cudaError_t r = cudaFuncSetAttribute(gla_residual_norm_kernel<E, R, NTR, K, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+    if (r != cudaSuccess) return r;
+    gla_residual_norm_kernel<E, R, NTR, K, BWD><<<blocks, NTR, n, s>>>(a);
+    return cudaGetLastError();
+}
 template <typename E, typename R, bool BWD>
 cudaError_t launch(const ResArgs& a, int sms, cudaStream_t s)
 {
@@ -253,7 +308,7 @@ cudaError_t launch(const ResArgs& a, int sms, cudaStream_t s)
     else if (a.D <= 2048) gla_residual_norm_kernel<E, R, 128, 2, BWD><<<g, 128, 0, s>>>(a);
     else if (a.D <= 4096) gla_residual_norm_kernel<E, R, 256, 2, BWD><<<g, 256, 0, s>>>(a);
     else if (a.D <= 8192) gla_residual_norm_kernel<E, R, 512, 2, BWD><<<g, 512, 0, s>>>(a);
-    else gla_residual_norm_kernel<E, R, 512, 4, BWD><<<g, 512, 0, s>>>(a);
+    else return launch_widest<E, R, BWD>(a, g, s);
     return cudaGetLastError();
 }
 template <bool BWD>

@@ -31,6 +31,10 @@ CASES = [
     (3, 8192, (BF, BF), True, "vector", True, True),
     (2, 16384, (BF, FP), True, "vector", True, True),
     (1300, 48, (BF, BF), True, 2.0, True, True),
+    (325, 8208, (BF, BF), True, "vector", True, True),       # the widest kernel, several rows to a block
+    (160, 16384, (FP, FP), False, "vector", True, True),
+    (311, 11008, (BF, FP), True, 0.5, True, False),
+    (200, 6160, (FP, FP), True, "vector", False, True),
 ]
 
 
