@@ -62,7 +62,7 @@ __device__ __forceinline__ void sum_row(float& a, float& b, float2 (*red)[NTR / 
 }
 
 template <typename E, typename R, int NTR, int K, bool BWD>
-__global__ void __launch_bounds__(NTR == 32 ? 32 * kWarps : NTR, NTR == 32 ? 1 : BWD ? K < 4 ? 512 / NTR : 1 : NTR == 512 && K < 4 ? 2 : 1)
+__global__ void __launch_bounds__(NTR == 32 ? 32 * kWarps : NTR, NTR == 32 ? (BWD ? 2 : 1) : BWD ? K < 4 ? 512 / NTR : 1 : NTR == 512 && K < 4 ? 2 : 1)
 gla_residual_norm_kernel(ResArgs a)
 {
     __shared__ float2 red[2][NTR / 32 + 1];
