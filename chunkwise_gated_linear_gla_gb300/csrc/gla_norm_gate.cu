@@ -12,8 +12,9 @@
 // Bound by HBM: x and g read, y written once (backward: x, g and dy read, dx and dg written). A row is LPR lanes of
 // K pieces of eight values; a thread keeps its token and takes the token's heads one after the other, so that a row's address
 // is a sum (the division into batch row and token is done once; once per row it was a third of the instructions, 49 us for the
-// layer), two heads' loads in flight. 8 x 2048 tokens of 16 heads of 128: 33 us, 6.1 TB/s, 0.90 of the copy rate. The weight's
-// gradient is summed in fp32 over a thread's rows, its block, then the blocks, each in a fixed order.
+// layer), two heads' loads in flight (of heads above 256 one, but twice the blocks: 65536 rows of 512 47 us with two, 39 so). 8 x 2048 tokens
+// of 16 heads of 128: 33 us, 6.1 TB/s, 0.90 of the copy rate. The weight's gradient is summed in fp32 over a thread's rows, its
+// block, then the blocks, each in a fixed order.
 #include <cmath>
 #include <cstring>
 
@@ -50,9 +51,9 @@ __device__ __forceinline__ f2 act_of(f2 g, int silu, f2& slope)
 }
 
 template <typename E, int LPR, int K, bool BWD, bool FIRST>
-__global__ void __launch_bounds__(NT, K > 2 ? 1 : BWD || K > 1 ? 2 : 4) gla_norm_gate_kernel(GateArgs a)
+__global__ void __launch_bounds__(NT, BWD ? (K > 2 ? 1 : 2) : K > 2 ? 2 : 4) gla_norm_gate_kernel(GateArgs a)
 {
-    constexpr int RPB = NT / LPR, U = BWD || K > 2 ? 1 : 2;
+    constexpr int RPB = NT / LPR, U = BWD || K > 1 ? 1 : 2;
     __shared__ __align__(16) float red[BWD ? RPB : 1][BWD ? LPR * K * VEC : 4];
     const int l = threadIdx.x % LPR, row = threadIdx.x / LPR;
     f2 w[K][4], dw[K][4];
@@ -184,13 +185,13 @@ __global__ void __launch_bounds__(NT, K > 2 ? 1 : BWD || K > 1 ? 2 : 4) gla_norm
     }
 }
 
-// The heads are spread over blocks until every SM has three (3 x 1531 tokens of 4 heads of 512: 13.7 us, with eight 27.7: a thread then has one
-// head, not the two whose loads it can have in flight); backward: as many blocks as are resident, few partials.
+// The heads are spread over blocks until every SM has two (3 x 1531 tokens of 4 heads of 512: 10.5 us, with four 12.5, with eight 16.5: the weights
+// are read for one head, not two; 777 tokens of 16 heads of 256 4.8, 5.5 and 8.4); backward: as many blocks as are resident, few partials.
 dim3 grid_of(GateArgs& a, int sms, bool bwd)
 {
-    const int lpr = a.d <= 64 ? 8 : a.d <= 128 ? 16 : 32, rows = NT / lpr;
+    const int lpr = a.d <= 16 ? 2 : a.d <= 32 ? 4 : a.d <= 64 ? 8 : a.d <= 128 ? 16 : 32, rows = NT / lpr;
     const long long tg = (a.tokens + rows - 1) / rows;
-    const long long want = (bwd ? 2LL : 3LL) * sms;
+    const long long want = 2LL * sms;
     int split = 1;
     while (split < a.H && tg * split < want) split *= 2;
     if (split > a.H) split = a.H;
@@ -206,7 +207,9 @@ template <typename E, bool BWD, bool FIRST>
 cudaError_t launch(GateArgs a, int sms, cudaStream_t s)
 {
     const dim3 g = grid_of(a, sms, BWD);
-    if (a.d <= 64) gla_norm_gate_kernel<E, 8, 1, BWD, FIRST><<<g, NT, 0, s>>>(a);
+    if (a.d <= 16) gla_norm_gate_kernel<E, 2, 1, BWD, FIRST><<<g, NT, 0, s>>>(a);
+    else if (a.d <= 32) gla_norm_gate_kernel<E, 4, 1, BWD, FIRST><<<g, NT, 0, s>>>(a);
+    else if (a.d <= 64) gla_norm_gate_kernel<E, 8, 1, BWD, FIRST><<<g, NT, 0, s>>>(a);
     else if (a.d <= 128) gla_norm_gate_kernel<E, 16, 1, BWD, FIRST><<<g, NT, 0, s>>>(a);
     else if (a.d <= 256) gla_norm_gate_kernel<E, 32, 1, BWD, FIRST><<<g, NT, 0, s>>>(a);
     else if (a.d <= 512) gla_norm_gate_kernel<E, 32, 2, BWD, FIRST><<<g, NT, 0, s>>>(a);

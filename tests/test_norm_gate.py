@@ -35,6 +35,9 @@ CASES = [
     (1, 1, 300, 784, "rms", "silu", False, True, True),
     (2, 3, 9, 128, "rms", "silu", False, False, True),
     (1, 1, 3, 48, None, "sigmoid", True, True, False),
+    (2, 5, 700, 16, "rms", "silu", True, True, True),
+    (1, 7, 333, 32, "l2", "silu", False, True, True),
+    (1, 3, 2000, 512, "rms", "sigmoid", False, True, True),
 ]
 
 
