@@ -11,11 +11,11 @@
 //
 // Bytes: x read and y written once (backward: x and dy read, dx written). A thread takes four channels of a row (with eight
 // the weights and windows do not fit the registers: 69 us for the layer below, 33 so), two in the backward, whose sums and
-// windows are twice as many (75 us, 85 with four), and walks a run of tokens with the window in registers; a run's first W - 1
+// windows are twice as many (75 us then, 85 with four), and walks a run of tokens with the window in registers; a run's first W - 1
 // rows are read again, from L2. A warp is 128 (64) channels of a run of one batch row, a block eight warps, runs of all rows in one
 // order, so that single tokens of many rows fill it too (128 rows of 4096 channels 5.5 us, 16 with a block to a row). Reads go through
 // strides (a projection's slice, head by head), writes are dense. Sums are fp32; S_T is a copy of inputs. 8 x 2048 tokens of
-// 2048 channels: 31.5 us, 4.3 TB/s, 0.63 of the copy rate, at 16 instructions a value; backward 71 us, 0.42, at 30.
+// 2048 channels: 31.5 us, 4.3 TB/s, 0.63 of the copy rate, at 16 instructions a value; backward 61 us, 0.49.
 #include <cmath>
 #include <cstring>
 #include <type_traits>
@@ -31,7 +31,7 @@ constexpr int NT = 256;
 constexpr int LANES = 32;                // lanes across channels
 constexpr int RUNS = NT / LANES;         // runs of tokens per block
 constexpr int kFwdPairs = 2, kBwdPairs = 1;    // pairs of channels per thread
-constexpr int UNR = 4;                   // rows in flight per thread; the forward's long runs take eight
+constexpr int UNR = 4;                   // rows in flight per thread; long runs take eight
 
 struct ConvArgs {
     const void* x; const float* w; const float* bias; const void* S0;
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(NT, UNR > 4 && sizeof(E) > 2 ? 3 : 4) gla_conv
 
 // The backward walks W - 1 tokens past its run: dx of the run's rows needs their da. Weight sums are its own run's. A block
 // takes several groups of runs, so that it leaves one partial sum of them all.
-template <typename E, int W>
-__global__ void __launch_bounds__(NT, 3) gla_conv_bwd_kernel(ConvArgs a)
+template <typename E, int W, int UNR>
+__global__ void __launch_bounds__(NT, UNR > 4 && sizeof(E) > 2 ? 2 : 3) gla_conv_bwd_kernel(ConvArgs a)
 {
     constexpr int P = kBwdPairs, V = 2 * P;
     __shared__ float red[RUNS][LANES * V * (W + 1)];
@@ -330,30 +330,43 @@ __global__ void __launch_bounds__(NT, 3) gla_conv_bwd_kernel(ConvArgs a)
     }
 }
 
-// Tokens per run: long runs read fewer rows twice, short ones fill the chip. Backward: as many blocks as are resident.
-int grid_of(ConvArgs& a, int sms, bool bwd)
+// Tokens per run, and the groups of runs (the blocks of a channel tile). Long runs read fewer rows twice, short ones fill the chip.
+// Backward there are as many blocks as are resident, each with several groups one after the other, and the run is the one that ends first, a run of
+// its tokens and six more that start and end it (8 x 2048 tokens of 2048 channels: 75 us with 64 tokens in three rounds of
+// groups, 63 so; fp32 82 and 79).
+int grid_of(ConvArgs& a, int sms, bool bwd, bool fp32)
 {
     const int V = 2 * (bwd ? kBwdPairs : kFwdPairs);
     a.ctiles = (a.D + LANES * V - 1) / (LANES * V);
-    const long long want = (bwd ? 4LL : 8LL) * sms * RUNS;      // warps
-    int run = 32;
-    while (run > UNR && (long long)a.ctiles * a.B * (((long long)a.T + run - 1) / run) < want) run /= 2;
-    a.run = run;
-    const long long runs = ((long long)a.T + run - 1) / run;
-    a.runs = (int)(runs > 1 ? runs : 1);
-    long long groups = ((long long)a.B * a.runs + RUNS - 1) / RUNS;
-    if (bwd) {
-        const long long most = 3LL * sms / a.ctiles > 1 ? 3LL * sms / a.ctiles : 1;
-        if (groups > most) groups = (groups + (groups + most - 1) / most - 1) / ((groups + most - 1) / most);
+    auto groups_of = [&](int run) {
+        const long long runs = ((long long)a.T + run - 1) / run;
+        a.run = run;
+        a.runs = (int)(runs > 1 ? runs : 1);
+        return ((long long)a.B * a.runs + RUNS - 1) / RUNS;
+    };
+    if (!bwd) {
+        const long long want = 8LL * sms * RUNS;      // warps
+        int run = 32;
+        while (run > UNR && (long long)a.ctiles * a.B * (((long long)a.T + run - 1) / run) < want) run /= 2;
+        return (int)groups_of(run);
     }
-    return (int)groups;
+    long long best = 0, cost = -1;
+    int at = UNR;
+    for (int run = UNR; run <= 128; run += run < 8 ? 4 : 8) {
+        const long long sm = fp32 && run > 16 ? 2 : 3, resident = sm * sms / a.ctiles, most = resident > 1 ? resident : 1;
+        const long long groups = groups_of(run), rounds = (groups + most - 1) / most, c = rounds * (run + 6) * sm;
+        if (cost < 0 || c < cost) { cost = c; at = run; best = (groups + rounds - 1) / rounds; }
+    }
+    groups_of(at);
+    return (int)best;
 }
 
 template <typename E, int W>
 cudaError_t launch(ConvArgs a, int sms, bool bwd, cudaStream_t s)
 {
-    const unsigned g = (unsigned)((long long)grid_of(a, sms, bwd) * a.ctiles);
-    if (bwd) gla_conv_bwd_kernel<E, W><<<g, NT, 0, s>>>(a);
+    const unsigned g = (unsigned)((long long)grid_of(a, sms, bwd, sizeof(E) > 2) * a.ctiles);
+    if (bwd && a.run > 16) gla_conv_bwd_kernel<E, W, 2 * UNR><<<g, NT, 0, s>>>(a);  // (fp32, the layer: 99 us with four)
+    else if (bwd) gla_conv_bwd_kernel<E, W, UNR><<<g, NT, 0, s>>>(a);               // (3 x 777 tokens of 1040 channels: 18 us with eight, 15)
     else if (a.run > 8) gla_conv_fwd_kernel<E, W, 2 * UNR><<<g, NT, 0, s>>>(a);     // (the layer: 35 us with four)
     else gla_conv_fwd_kernel<E, W, UNR><<<g, NT, 0, s>>>(a);                        // (128 single tokens: 6.6 us with eight, 5.5)
     return cudaGetLastError();
@@ -395,7 +408,7 @@ ConvArgs common(const gla_conv_params* p)
 size_t part_bytes(const gla_conv_params* p, int sms, long long* blocks)
 {
     ConvArgs a = common(p);
-    *blocks = grid_of(a, sms, true);
+    *blocks = grid_of(a, sms, true, p->dtype == GLA_FP32);
     return (size_t)*blocks * a.D * (p->W + 1) * 4;
 }
 

@@ -42,6 +42,8 @@ CASES = [
     (1, 2, 130, 128, 2, "silu", False, False),
     (2, 1, 1031, 128, 4, "silu", True, True),
     (1, 5, 33, 16, 2, None, False, True),
+    (2, 1, 2500, 2048, 4, "silu", True, True),       # long runs
+    (3, 1, 1300, 2048, 3, None, True, False),
 ]
 
 
