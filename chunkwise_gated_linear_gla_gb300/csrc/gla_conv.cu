@@ -10,12 +10,12 @@
 //     dbias = sum da_t.
 //
 // Bytes: x read and y written once (backward: x and dy read, dx written). A thread takes four channels of a row (with eight
-// the weights and windows do not fit the registers: 69 us for the layer below, 33 so), two in the backward, whose sums and
+// the weights and windows do not fit the registers: 69 us for the layer below, 33 then), two in the backward, whose sums and
 // windows are twice as many (75 us then, 85 with four), and walks a run of tokens with the window in registers; a run's first W - 1
 // rows are read again, from L2. A warp is 128 (64) channels of a run of one batch row, a block eight warps, runs of all rows in one
 // order, so that single tokens of many rows fill it too (128 rows of 4096 channels 5.5 us, 16 with a block to a row). Reads go through
 // strides (a projection's slice, head by head), writes are dense. Sums are fp32; S_T is a copy of inputs. 8 x 2048 tokens of
-// 2048 channels: 31.5 us, 4.3 TB/s, 0.63 of the copy rate, at 16 instructions a value; backward 61 us, 0.49.
+// 2048 channels: 25.5 us, 5.3 TB/s, 0.78 of the copy rate; backward 61 us, 0.49.
 #include <cmath>
 #include <cstring>
 #include <type_traits>
@@ -330,10 +330,11 @@ __global__ void __launch_bounds__(NT, UNR > 4 && sizeof(E) > 2 ? 2 : 3) gla_conv
     }
 }
 
-// Tokens per run, and the groups of runs (the blocks of a channel tile). Long runs read fewer rows twice, short ones fill the chip.
-// Backward there are as many blocks as are resident, each with several groups one after the other, and the run is the one that ends first, a run of
-// its tokens and six more that start and end it (8 x 2048 tokens of 2048 channels: 75 us with 64 tokens in three rounds of
-// groups, 63 so; fp32 82 and 79).
+// Tokens per run, and the groups of runs (the blocks of a channel tile). Long runs read fewer rows twice, short ones fill the chip;
+// blocks come in rounds of as many as are resident, and the run is the one whose rounds end first, a run of
+// its tokens and a few more that start and end it. Backward a block takes its rounds' groups one after the other, for few partials
+// (8 x 2048 tokens of 2048 channels: 75 us with 64 tokens in three rounds, 63 so; fp32 82 and 77; forward 32.7 with 16 in four, 25.6 so).
+// Forward in fp32 it is bytes, and runs above 32 tokens lose a little (two taps: 42 us, 45 with more).
 int grid_of(ConvArgs& a, int sms, bool bwd, bool fp32)
 {
     const int V = 2 * (bwd ? kBwdPairs : kFwdPairs);
@@ -344,18 +345,20 @@ int grid_of(ConvArgs& a, int sms, bool bwd, bool fp32)
         a.runs = (int)(runs > 1 ? runs : 1);
         return ((long long)a.B * a.runs + RUNS - 1) / RUNS;
     };
-    if (!bwd) {
-        const long long want = 8LL * sms * RUNS;      // warps
-        int run = 32;
-        while (run > UNR && (long long)a.ctiles * a.B * (((long long)a.T + run - 1) / run) < want) run /= 2;
-        return (int)groups_of(run);
-    }
     long long best = 0, cost = -1;
     int at = UNR;
-    for (int run = UNR; run <= 128; run += run < 8 ? 4 : 8) {
-        const long long sm = fp32 && run > 16 ? 2 : 3, resident = sm * sms / a.ctiles, most = resident > 1 ? resident : 1;
-        const long long groups = groups_of(run), rounds = (groups + most - 1) / most, c = rounds * (run + 6) * sm;
-        if (cost < 0 || c < cost) { cost = c; at = run; best = (groups + rounds - 1) / rounds; }
+    for (int run = UNR; run <= (fp32 && !bwd ? 32 : 128); run += run < 8 ? 4 : 8) {
+        const long long sm = bwd ? (fp32 && run > 16 ? 2 : 3) : fp32 && run > 8 ? 3 : 4;
+        const long long groups = groups_of(run);
+        long long rounds;
+        if (bwd) {
+            const long long most = sm * sms / a.ctiles > 1 ? sm * sms / a.ctiles : 1;
+            rounds = (groups + most - 1) / most;
+        } else {
+            rounds = (groups * a.ctiles + sm * sms - 1) / (sm * sms);
+        }
+        const long long c = rounds * (run + (bwd ? 6 : 4)) * sm;
+        if (cost < 0 || c < cost) { cost = c; at = run; best = bwd ? (groups + rounds - 1) / rounds : groups; }
     }
     groups_of(at);
     return (int)best;
