@@ -371,3 +371,21 @@ def test_plain_calls_take_no_graph(name, _stand_ins):
     assert first(call(*x)).requires_grad
     with torch.no_grad():
         assert not first(call(*x)).requires_grad
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_second_derivatives_are_refused(name, _stand_ins, monkeypatch):
+    b = glue._b
+    monkeypatch.setattr(b, "causal_conv_backward", lambda x, w, bias, S0, dy, *a, **k: (dy * 2, None, None, None))
+    monkeypatch.setattr(b, "selective_scan_backward", lambda *a, **k: (a[9] * 2, *(None,) * 8))
+    monkeypatch.setattr(b, "norm_gate_backward", lambda x, gate, w, dy, *a: (dy * 2, None, None))
+    monkeypatch.setattr(b, "residual_norm_backward", lambda x, r, w, s, dh, dy, *a, **k: (dh * 2, None, None, None))
+    call, k = CALLS[name]
+    x = [torch.randn(2, 3, 16) for _ in range(k)]
+    x[0].requires_grad_(True)
+    first = lambda r: r[0] if isinstance(r, tuple) else r  # noqa: E731
+    (g,) = torch.autograd.grad(first(call(*x)).square().sum(), x[:1])
+    assert not g.requires_grad and torch.equal(g, 8 * x[0])
+    (g,) = torch.autograd.grad(first(call(*x)).square().sum(), x[:1], create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
