@@ -102,34 +102,32 @@ __global__ void __launch_bounds__(kStepNT) gla_ssm_step_kernel(SsmArgs a)
 // (8 x 2048 tokens of 8192 channels of 8 states: 566 us with 32, 485 with 16, fp32 716 and 632; 4096 of 16 390 and 403, fp32 477 and
 // 411; 2048 of 32 402 and 442, fp32 482 and 461 but of half the rows 257 and 293).
 template <typename E, int N> constexpr int kWalkTile = N == 8 || (N == 16 && sizeof(E) == 4) ? 16 : 32;
-// States of a thread: B and C are read once for eight. The walk that keeps states runs uncut with the few blocks of a training batch, where
-// more warps count for more (4 x 2048 tokens of 4096 channels of 16 states: 144 us with four, 171 with eight).
-template <int MODE> constexpr int kStates = MODE == kSsmKeep ? 4 : 8;
-template <int N, int MODE> constexpr int kWalkWarps = N >= 64 || MODE == kSsmKeep ? 4 : 2;
-template <int N, int MODE> constexpr int kWalkChannels = kWalkWarps<N, MODE> * 32 * kStates<MODE> / N;
+constexpr int kS = 8;              // states of a thread: B and C are read once for them
+template <int N> constexpr int kWalkWarps = N >= 64 ? 4 : 2;
+template <int N> constexpr int kWalkChannels = kWalkWarps<N> * 32 * kS / N;
 
 // A thread's states of a channel, from the first of them on: by fours N / 2 apart, so that neighbouring lanes read neighbouring 16
 // bytes.
-template <int N, int S>
-__device__ __forceinline__ void pick(const float* p, f2 (&r)[S / 2])
+template <int N>
+__device__ __forceinline__ void pick(const float* p, f2 (&r)[kS / 2])
 {
 #pragma unroll
-    for (int i = 0; i < S / 4; ++i) {
+    for (int i = 0; i < kS / 4; ++i) {
         const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(p + i * (N / 2));
         r[2 * i] = q.x;
         r[2 * i + 1] = q.y;
     }
 }
-template <int N, int S>
-__device__ __forceinline__ void drop(float* p, const f2 (&r)[S / 2])
+template <int N>
+__device__ __forceinline__ void drop(float* p, const f2 (&r)[kS / 2])
 {
 #pragma unroll
-    for (int i = 0; i < S / 4; ++i) *reinterpret_cast<ulonglong2*>(p + i * (N / 2)) = make_ulonglong2(r[2 * i], r[2 * i + 1]);
+    for (int i = 0; i < kS / 4; ++i) *reinterpret_cast<ulonglong2*>(p + i * (N / 2)) = make_ulonglong2(r[2 * i], r[2 * i + 1]);
 }
 
 template <typename E, int N, int MODE>
 struct WalkShared {
-    static constexpr int CB = kWalkChannels<N, MODE>, TT = kWalkTile<E, N>;
+    static constexpr int CB = kWalkChannels<N>, TT = kWalkTile<E, N>;
     static constexpr bool HAS_B = MODE != kSsmRev, HAS_C = MODE == kSsmOut || MODE == kSsmRev, HAS_Z = HAS_C;
     E raw[2][HAS_Z ? 3 : 2][TT][CB];   // x, dt, z (REV: dy, dt, z)
     E bc[2][HAS_B + HAS_C][TT][N];
@@ -141,10 +139,10 @@ struct WalkShared {
 };
 
 template <typename E, int N, int MODE>
-__global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14 / kWalkWarps<N, MODE> : 1) gla_ssm_walk_kernel(SsmArgs a)
+__global__ void __launch_bounds__(kWalkWarps<N> * 32, MODE == kSsmOut ? 14 / kWalkWarps<N> : 1) gla_ssm_walk_kernel(SsmArgs a)
 {
     typedef WalkShared<E, N, MODE> Shared;
-    constexpr int NT = kWalkWarps<N, MODE> * 32, CB = kWalkChannels<N, MODE>, P = Shared::P, kS = kStates<MODE>, Q = N / kS, TT = kWalkTile<E, N>, SUB = kSsmTile;
+    constexpr int NT = kWalkWarps<N> * 32, CB = kWalkChannels<N>, P = Shared::P, Q = N / kS, TT = kWalkTile<E, N>, SUB = kSsmTile;
     constexpr bool REV = MODE == kSsmRev, OUT = MODE == kSsmOut;
     constexpr int IC = Shared::HAS_B ? 1 : 0;      // where C lies beside B
     extern __shared__ __align__(16) char smem_raw[];
@@ -188,13 +186,13 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
         if (seg > 0) from = a.segS + ((size_t)b * (a.nseg - 1) + seg - 1) * per;
         else if (a.S0) from = a.S0 + b * per;
     }
-    pick<N, kS>(a.A + so, A);
+    pick<N>(a.A + so, A);
 #pragma unroll
     for (int j = 0; j < kS / 2; ++j) {
         A[j] = mul2(A[j], both(kLog2e));
         h[j] = 0ull;
     }
-    if (from) pick<N, kS>(from + so, h);
+    if (from) pick<N>(from + so, h);
     // the vectors of eight channels that this thread prepares and finishes: always the same channels
     constexpr int COLS = CB / VEC, VPT = TT * COLS;
     const int vc = threadIdx.x % COLS * VEC;
@@ -245,7 +243,7 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
         for (int sub = REV ? TT - parts : 0; sub < (REV ? TT : parts); sub += SUB) {
             const int base = REV ? TT - SUB - sub : sub;
             if (MODE == kSsmKeep && on)
-                drop<N, kS>(a.keep + ((size_t)b * ((a.T + SUB - 1) / SUB) + (t0 + base) / SUB) * per + so, h);
+                drop<N>(a.keep + ((size_t)b * ((a.T + SUB - 1) / SUB) + (t0 + base) / SUB) * per + so, h);
             // At the end of these tokens the state that entered takes their whole decay at once, so that a long memory is rounded once
             // per 16 tokens, not at every one. Beside the states runs what they multiply it by, the product of the decays; where the states
             // between are not wanted, only what the tokens themselves add (from zero).
@@ -263,8 +261,8 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
                 const int tok = base + (REV ? SUB - 1 - n : n);
                 p.d = sm.work[0][tok * P + cl];
                 p.x = sm.work[1][tok * P + cl];
-                pick<N, kS>(&sm.wide[0][tok][sg * 4], p.B);
-                if (OUT) pick<N, kS>(&sm.wide[IC][tok][sg * 4], p.C);
+                pick<N>(&sm.wide[0][tok][sg * 4], p.B);
+                if (OUT) pick<N>(&sm.wide[IC][tok][sg * 4], p.C);
             };
             auto form = [&](Token& p) {
                 sd += p.d;
@@ -340,7 +338,7 @@ __global__ void __launch_bounds__(kWalkWarps<N, MODE> * 32, MODE == kSsmOut ? 14
     if (OUT && seg == a.nseg - 1 && a.ST) to = a.ST + b * per;
     if (MODE == kSsmState) to = a.segS + ((size_t)b * (a.nseg - 1) + seg) * per;
     if (REV) to = a.segG + ((size_t)b * (a.nseg - 1) + seg - 1) * per;
-    if (to && on) drop<N, kS>(to + so, h);
+    if (to && on) drop<N>(to + so, h);
     if (MODE == kSsmState) {
         // the sums of delta over the threads that prepared the same channels, in order
         __syncthreads();
@@ -381,13 +379,13 @@ template <typename E, int N, int MODE>
 cudaError_t walk(const SsmArgs& a0, cudaStream_t s)
 {
     SsmArgs a = a0;
-    constexpr int CB = kWalkChannels<N, MODE>;
+    constexpr int CB = kWalkChannels<N>;
     a.ctiles = (a.D / a.G + CB - 1) / CB;
     const int n = (int)sizeof(WalkShared<E, N, MODE>);
     const cudaError_t r = cudaFuncSetAttribute(gla_ssm_walk_kernel<E, N, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
     if (r != cudaSuccess) return r;
     const dim3 g((unsigned)((long long)a.B * a.G * a.ctiles), MODE == kSsmState || MODE == kSsmRev ? a.nseg - 1 : a.nseg);
-    gla_ssm_walk_kernel<E, N, MODE><<<g, kWalkWarps<N, MODE> * 32, n, s>>>(a);
+    gla_ssm_walk_kernel<E, N, MODE><<<g, kWalkWarps<N> * 32, n, s>>>(a);
     return cudaGetLastError();
 }
 template <typename E, int N>
@@ -423,8 +421,8 @@ cudaError_t step(const SsmArgs& a, int sms, cudaStream_t s)
 
 }  // namespace
 
-int ssm_walk_warps(int N) { return N >= 64 ? kWalkWarps<64, kSsmOut> : kWalkWarps<8, kSsmOut>; }
-int ssm_walk_channels(int N) { return kWalkChannels<8, kSsmOut> * 8 / N * (N >= 64 ? 2 : 1); }
+int ssm_walk_warps(int N) { return N >= 64 ? kWalkWarps<64> : kWalkWarps<8>; }
+int ssm_walk_channels(int N) { return kWalkChannels<8> * 8 / N * (N >= 64 ? 2 : 1); }
 
 cudaError_t launch_ssm_step(const SsmArgs& a, gla_dtype dtype, int sms, cudaStream_t s)
 {
