@@ -15,7 +15,7 @@
 // equal bit for bit from call to call.
 //
 // Bound by the multiply-adds' register reads (a packed one of three different pairs takes 3.75 cycles) and by waits that two warps
-// a scheduler cannot hide (228 registers, 111 KB a block): four rows of 2048 tokens of 4096 channels of 16 states take 705 us, 22 warp
+// a scheduler cannot hide (228 registers, 111 KB a block): four rows of 2048 tokens of 4096 channels of 16 states take 703 us, 22 warp
 // instructions a state at 47% of the issue slots; per token, channel and state 10 products or multiply-adds back, 4 for h and a again, 3 for
 // the tile's first walk. Preparing and finishing the tiles is 0.2 of it. One channel a thread (twice the warps) took 1.25 times as long.
 #include "gla_ssm.cuh"
