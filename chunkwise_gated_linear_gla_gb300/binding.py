@@ -1245,7 +1245,8 @@ def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None
     boundary); A fp32 [D,N], D and dt_bias fp32 [D] or None, S0 fp32 [B,D,N] or None (zero). N is 8, 16, 32 or 64, D / G a
     multiple of 8. With softplus the steps are softplus(dt + dt_bias), else dt + dt_bias. Returns (y, ST): y dense
     [B,T,D], ST fp32 [B,D,N] (None unless wanted). A decoding loop passes ST=S0 to carry the state in place; y and ST count
-    as modified in place. A token is passed over where its dt is -inf (with softplus; its other values finite).
+    as modified in place. A token is passed over where its dt is -inf (with softplus; its other values finite). Where states grow
+    (A above zero), the growth over 16 tokens has to be an fp32 number.
     """
     import torch
     p, states, T = _ssm_params(x, dt, A, B, C, D, z, dt_bias, S0, softplus, force_segments)

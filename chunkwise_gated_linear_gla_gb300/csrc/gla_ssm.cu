@@ -354,6 +354,14 @@ __global__ void __launch_bounds__(kWalkWarps<N> * 32, MODE == kSsmOut ? 14 / kWa
     }
 }
 
+// 2^p x + o for large p, that of a long segment of states that grow: in two steps, as 2^p may be no fp32 number where 2^p x is
+// one. No state stays none.
+__device__ __forceinline__ float grow(float p, float x, float o)
+{
+    const float e = ex2(0.5f * p);
+    return x == 0.f ? o : fmaf(e, e * x, o);
+}
+
 // The states entering segments 1 .., in place of the segments' own: the first's own starts from S0, X_{s+1} = exp(A sum_s) X_s
 // + own_s. rev: the gradients of the states after segments .. nseg - 2, in place of what each next segment leaves of its
 // own (the last one's starts from dST).
@@ -367,10 +375,18 @@ __global__ void gla_ssm_scan_kernel(SsmArgs a, int rev)
         const float* sd = a.sumd + b * m * a.D + o / a.N;
         float* s = (rev ? a.segG : a.segS) + b * m * per + o;
         float X = s[rev ? (m - 1) * per : 0];
+        // (a step's sum and state are read before the one before it is stored, whose place the compiler cannot tell apart)
+        auto at = [&](int k) { return rev ? m - 1 - k : k; };
+        float p = 0.f, own = 0.f;
+        auto read = [&](int k) {
+            p = A * sd[(long long)(rev ? at(k) + 1 : at(k)) * a.D];
+            own = s[at(k) * per];
+        };
+        if (m > 1) read(1);
         for (int k = 1; k < m; ++k) {
-            const int n = rev ? m - 1 - k : k, d = rev ? n + 1 : n;
-            X = fmaf(ex2(A * sd[(long long)d * a.D]), X, s[n * per]);
-            s[n * per] = X;
+            X = p < 64.f ? fmaf(ex2(p), X, own) : grow(p, X, own);
+            if (k + 1 < m) read(k + 1);
+            s[at(k) * per] = X;
         }
     }
 }

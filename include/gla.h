@@ -587,7 +587,8 @@ size_t gla_conv_bwd_workspace_size(const gla_conv_params* p);
  *     delta_t = softplus(dt_t + dt_bias)  (or dt_t + dt_bias),
  *     h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,     y_t = (C_t . h_t + D_skip x_t) silu(z_t),
  * A [D,N] (negative for states that decay), B and C one row of N values for each of the G groups of D / G channels.
- * A dt of -inf (with softplus; or of 0 without it and the bias) passes a token over: the state stays as it is. Other inputs are finite.
+ * A dt of -inf (with softplus; or of 0 without it and the bias) passes a token over: the state stays as it is. Other inputs are
+ * finite, and where states grow (A above zero, or steps below) the growth over 16 tokens, exp of their sum of delta A, is an fp32 number.
  * x, dt, z, B and C are read through strides in elements (batch, token; a row contiguous), every row starting on 16 bytes;
  * strides may be zero or negative. D / G is a multiple of 8, N 8, 16, 32 or 64 (else GLA_ERR_UNSUPPORTED), D <= 2^20.
  * States and sums are fp32, y is rounded once; ST may equal S0. Up to eight tokens are taken one by one, longer calls in

@@ -217,6 +217,48 @@ def test_not_finite_values_stay_in_their_channel_and_after_their_token(T, segmen
     assert torch.equal(SZ[0, rows], ST[0, rows])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("tiny", [False, True])
+def test_states_that_grow_over_segments(tiny):
+    """exp(delta A) = e^2 a token: the growth of a segment of 64 tokens is no fp32 number, while the states are: none until the
+    last two tokens, or so small that they fit after 48 tokens of it. A token's growth is off by 2^-22 + 2 2^-23, so 48 tokens' by
+    below 48 2^-21 = 2.3e-5 if all erred one way; held to 2.5e-5."""
+    g = torch.Generator().manual_seed(21)
+    rnd = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    T, D, N = 256, 16, 16
+    x, dt, A, B, C, S0 = rnd(1, T, D), torch.full((1, T, D), 2.0), torch.ones(D, N), rnd(1, T, 1, N), rnd(1, T, 1, N), None
+    x[:, :T - 2] = 0
+    if tiny:
+        x, S0 = torch.zeros_like(x), 1e-30 * rnd(1, D, N)
+        dt[:, :64], dt[:, 112:] = 0, 0
+    args = (x, dt, A, B, C, None, None, None, S0)
+    want, last = ref.scan(*ref.double(args), False)
+    for segments in (1, 4):
+        y, ST = gla.selective_scan_forward(*ref.cuda(args), softplus=False, force_segments=segments)
+        ref.near(y, want, "y", 2.5e-5)
+        ref.near(ST, last, "ST", 2.5e-5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("segments", [1, 4])
+def test_gradients_across_growing_segments(segments):
+    """The gradients of the first four tokens' outputs and the states of the last four tokens, with growth between them that neither
+    meets and that is no fp32 number."""
+    g = torch.Generator().manual_seed(22)
+    rnd = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    T, D, N = 256, 16, 16
+    x, dt, A, B, C, dy = rnd(1, T, D), torch.full((1, T, D), 2.0), torch.ones(D, N), rnd(1, T, 1, N), rnd(1, T, 1, N), rnd(1, T, D)
+    x[:, :T - 4] = 0
+    dy[:, 4:] = 0
+    args = (x, dt, A, B, C, None, None, None, None)
+    leaves = ref.double(args)
+    want, _ = ref.scan(*leaves, False)
+    wg = torch.autograd.grad((want * dy.double()).sum(), leaves[:5])
+    got = gla.selective_scan_backward(*ref.cuda(args), dy.cuda(), softplus=False, force_segments=segments)
+    for n, a, b in zip(NAMES, got, wg):
+        ref.near(a, b, "d" + n)
+
+
 # ---------------------------------------------------------------- refusals, no GPU needed
 
 def _params(**kw):
