@@ -4,10 +4,11 @@ import pytest
 import torch
 
 import chunkwise_gated_linear_gla_gb300 as gla
+from chunkwise_gated_linear_gla_gb300 import binding as bnd
 from chunkwise_gated_linear_gla_gb300 import build as gbuild
 
 import _layer_ref as ref
-from test_ssm import make
+from test_ssm import NAMES, make
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -36,3 +37,29 @@ def test_few_tokens_of_many_rows(N, T, over, without, dtype):
         state = t["S0"].clone()
         y2, _ = gla.selective_scan_forward(**{**t, "S0": state}, ST=state)
         assert torch.equal(y2, y) and torch.equal(state, ST)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,D,N,G,dtype", [(1, 4099, 64, 16, 1, torch.float32), (1, 2600, 48, 8, 1, torch.bfloat16),
+                                             (2, 1500, 32, 64, 2, torch.float32), (1, 2053, 96, 32, 3, torch.bfloat16)])
+def test_long_prompts_of_few_channels(B, T, D, N, G, dtype):
+    """Cut into many segments by the planner, forward and backward. The states' decays are good to 4e-6 of their size (memories of
+    up to 200 tokens) and the sums add 30 roundings, each of terms of up to ten times a tensor's root mean square: 6e-5 of it; sums over
+    the tokens 1e-5 of their norm."""
+    t, dy, dST = make(B, T, D, N, G, dtype, T)
+    args = [t[n] for n in NAMES]
+    packed, _, _ = bnd._ssm_params(*args, True)
+    assert bnd._workspace("gla_ssm_fwd_workspace_size", packed, dy.device)[2] > 16 * B * D * N * 4      # 16 segments and more
+    y, ST = gla.selective_scan_forward(*args)
+    got = gla.selective_scan_backward(*args, dy, dST)
+    leaves = ref.double(args)
+    want, last = ref.scan(*leaves, True)
+    ref.near(y, want, "y", 6e-5)
+    ref.near(ST, last, "ST", 6e-5)
+    wg = torch.autograd.grad((want * dy.double().cpu()).sum() + (last * dST.double().cpu()).sum(), leaves)
+    for n, a, b in zip(NAMES, got, wg):
+        if n in ("A", "D", "dt_bias"):
+            e = float((a.double().cpu() - b).norm() / b.norm())
+            assert e <= 1e-5, f"d{n}: {e:.1e}"
+        else:
+            ref.near(a, b, "d" + n, 6e-5)
