@@ -10,6 +10,8 @@ from chunkwise_gated_linear_gla_gb300 import build as gbuild
 import _layer_ref as ref
 from test_ssm import NAMES, make
 
+U = 2.0 ** -24                 # half a step of fp32 at one
+
 
 @pytest.fixture(scope="module", autouse=True)
 def _built():
@@ -63,3 +65,31 @@ def test_long_prompts_of_few_channels(B, T, D, N, G, dtype):
             assert e <= 1e-5, f"d{n}: {e:.1e}"
         else:
             ref.near(a, b, "d" + n, 6e-5)
+
+
+@pytest.mark.gpu
+def test_memories_longer_than_the_call():
+    """States that only decay, by exp(-1e-3) or so a token, and the gradients of those that enter: S0 exp(A sum of delta), and dST
+    times the same. A walk multiplies by one decay every 16 tokens (2048 of them: 128 decays, each good to 2^-23, and a rounding:
+    2.3e-5 if all erred one way), a call of up to eight tokens by one a token, for which that is 3.7e-4. Roundings of a state at every
+    token are common to both, sqrt(2048) U = 2.7e-6 at most; what 16 times fewer decays add is a fourth if they err at random and a
+    sixteenth if not. So the walks' error is held to half of what the same tokens give in calls of eight."""
+    g = torch.Generator().manual_seed(31)
+    B, T, D, N = 1, 2048, 64, 16
+    rnd = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    dt, A = rnd(B, T, D) * 0.3 - 6.9, -(0.5 + torch.rand(D, N, generator=g))
+    S0, dST = rnd(B, D, N), rnd(B, D, N)
+    decay = torch.exp(A.double() * torch.nn.functional.softplus(dt.double()).sum(1).unsqueeze(2))
+    none, bc = torch.zeros(B, T, D), rnd(B, T, 1, N)
+    x, dt, A, bc, S0, dST = (t.cuda() for t in (none, dt, A, bc, S0, dST))
+    off = lambda got, start: float(((got.double() - start.double() * decay.cuda()).norm() / (start.double() * decay.cuda()).norm()))  # noqa: E731
+    state = S0.clone()
+    for t in range(0, T, 8):
+        p = slice(t, t + 8)
+        gla.selective_scan_forward(x[:, p], dt[:, p], A, bc[:, p], bc[:, p], S0=state, ST=state)
+    singly = off(state, S0)
+    for segments in (0, 1, 8):
+        _, ST = gla.selective_scan_forward(x, dt, A, bc, bc, S0=S0, force_segments=segments)
+        dS0 = gla.selective_scan_backward(x, dt, A, bc, bc, None, None, None, S0, x, dST, force_segments=segments)[8]
+        for n, e in (("ST", off(ST, S0)), ("dS0", off(dS0, dST))):
+            assert e <= min(2.3e-5, singly / 2), f"{n} in {segments} segments: {e:.1e}, {singly:.1e} in calls of eight tokens"
