@@ -93,3 +93,32 @@ def test_memories_longer_than_the_call():
         dS0 = gla.selective_scan_backward(x, dt, A, bc, bc, None, None, None, S0, x, dST, force_segments=segments)[8]
         for n, e in (("ST", off(ST, S0)), ("dS0", off(dS0, dST))):
             assert e <= min(2.3e-5, singly / 2), f"{n} in {segments} segments: {e:.1e}, {singly:.1e} in calls of eight tokens"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,segments", [(5, 0), (20, 1), (20, 2)])
+def test_small_steps_keep_their_digits(T, segments, dtype):
+    """dt from -20 to -6, steps of 2e-9 to 2.5e-3: every value relative to itself. All terms are positive, so a sum is as good as its
+    terms. exp(dt) is off by 4 U and |dt| (U + 1.3e-8) (its argument's rounding, and that of log2 e), softplus by 6 U more, a
+    decay by 6 U, of at most 20 tokens; products and sums over tokens and 8 states 30 U: 160 U + |dt| 7.3e-8 in all. A gradient holds
+    as much of its own side, and the sigmoid as much as exp(dt) again; what cancels is a twentieth (delta A of 20 tokens). A
+    logarithm of the rounded 1 + exp(dt) is off by 400 U at dt = -6 and by everything at -17."""
+    g = torch.Generator().manual_seed(T)
+    D, N = 64, 8
+    pos = lambda *s: (0.5 + torch.rand(s, generator=g)).to(dtype)  # noqa: E731
+    dt = (torch.linspace(-20, -6, D) + 0.05 * torch.rand(1, T, D, generator=g)).to(dtype)
+    x, A, Bm, C, dy = pos(1, T, D), -pos(D, N).float(), pos(1, T, 1, N), pos(1, T, 1, N), pos(1, T, D)
+    args = (x, dt, A, Bm, C, None, None, None, None)
+    y, ST = gla.selective_scan_forward(*ref.cuda(args), force_segments=segments)
+    got = gla.selective_scan_backward(*ref.cuda(args), dy.cuda(), force_segments=segments)
+    leaves = ref.double(args)
+    want, last = ref.scan(*leaves, True)
+    wg = torch.autograd.grad((want * dy.double()).sum(), leaves[:5])
+    v = 20.0 - (14.0 / (D - 1)) * torch.arange(D, dtype=torch.float64)      # |dt| of a channel, at most
+    one = 160 * U + 7.3e-8 * v
+    for n, a, b, tol in (("y", y, want, one), ("ST", ST, last, one[:, None]), ("dx", got[0], wg[0], 1.1 * one),
+                         ("ddt", got[1], wg[1], 1.1 * one + 20 * U + 7.3e-8 * v), ("dA", got[2], wg[2], 2.1 * one[:, None])):
+        tol = tol + (2.0 ** -8 if a.dtype == torch.bfloat16 else 0)
+        worst = float(((a.double().cpu() - b.detach()).abs() / (b.detach().abs() * tol)).max())
+        assert (b > 0).all() and worst <= 1, f"{n}: {worst:.2f} of its bound"
