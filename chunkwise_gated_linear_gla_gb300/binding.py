@@ -1131,6 +1131,8 @@ def _conv_params(x, w, bias, S0, activation):
     if w.dim() != 2:
         _refuse("w has two dimensions: [H d, W]")
     W = w.shape[1]
+    if W == 0:
+        _refuse("w has no taps")
     _dense(w, (D, W), f32, dev, "w")
     if bias is not None:
         _dense(bias, (D,), f32, dev, "bias")

@@ -169,6 +169,12 @@ def test_calls_under_the_c_names_tell_their_status():
             call(p, stream=0)
 
 
+def test_a_filter_without_taps_is_refused():
+    """Its state would have minus one row."""
+    with pytest.raises(gla.GlaError, match="no taps"):
+        gla.causal_conv(torch.randn(1, 3, 64), torch.empty(64, 0))
+
+
 # ---------------------------------------------------------------- the same results under both names
 
 def _ws(n):
