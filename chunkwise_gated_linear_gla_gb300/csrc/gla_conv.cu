@@ -15,7 +15,8 @@
 // rows are read again, from L2. A warp is 128 (64) channels of a run of one batch row, a block eight warps, runs of all rows in one
 // order, so that single tokens of many rows fill it too (128 rows of 4096 channels 5.5 us, 16 with a block to a row). Reads go through
 // strides (a projection's slice, head by head), writes are dense. Sums are fp32; S_T is a copy of inputs. 8 x 2048 tokens of
-// 2048 channels: 25.5 us, 5.3 TB/s, 0.78 of the copy rate; backward 61 us, 0.49.
+// 2048 channels: 25.5 us, 5.3 TB/s, 0.78 of the copy rate; backward 61 us, 0.49 (eight rows are loaded, then computed with none in flight; bf16
+// spills 92 bytes at its 80 registers), and 5 for the sums of the weights' partials.
 #include <cmath>
 #include <cstring>
 #include <type_traits>

@@ -13,7 +13,8 @@
 // K pieces of eight values; a thread keeps its token and takes the token's heads one after the other, so that a row's address
 // is a sum (the division into batch row and token is done once; once per row it was a third of the instructions, 49 us for the
 // layer), two heads' loads in flight (of heads above 256 one, but twice the blocks: 65536 rows of 512 47 us with two, 39 so). 8 x 2048 tokens
-// of 16 heads of 128: 33 us, 6.1 TB/s, 0.90 of the copy rate. The weight's gradient is summed in fp32 over a thread's rows, its
+// of 16 heads of 128: 33 us, 6.1 TB/s, 0.90 of the copy rate. The backward has one head in flight, asked for after the last one's stores, and two
+// blocks an SM: too few bytes, 3.1 to 3.9 TB/s in bf16 up to 256 values (3.6 at 128), 4.2 to 5.6 in fp32. The weight's gradient is summed in fp32 over a thread's rows, its
 // block, then the blocks, each in a fixed order.
 #include <cmath>
 #include <cstring>

@@ -15,7 +15,8 @@
 // values are a warp's, with shuffles for the sums; wider rows a block's, K pieces of eight values per thread: two pieces, as every sum
 // over the row costs a thread 60 instructions (with one piece 51 us for the rows below). The vectors' gradients are summed in
 // fp32 over a thread's rows, then over the blocks, each in a fixed order. 16384 bf16 rows of 2048 values, post norm and scale: 40 us,
-// 6.7 TB/s, 0.98 of the copy rate; backward 77 us, 0.77.
+// 6.7 TB/s, 0.98 of the copy rate; backward 77 us, 0.77, and above 4096 values, with a block an SM and no load between the row's sums, 2.7 to
+// 3.2 TB/s in bf16 (fp32 3.1 to 4.1).
 #include <cmath>
 #include <cstring>
 

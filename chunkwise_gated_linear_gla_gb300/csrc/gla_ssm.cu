@@ -9,16 +9,18 @@
 // gla_ssm_walk: a thread holds eight states of a channel and walks the tokens, its products packed pairs of states. The block goes
 // in tiles of 32 tokens (16 where they would take too much room): raw rows arrive by asynchronous copies one tile ahead, delta and
 // delta x are formed once per channel and token into shared memory, B and C widened there, the walk leaves C . h in their places, and y
-// is formed from it eight channels at a time. Bound by issue: eight rows of 2048 tokens of 4096 channels of 16 states (1.07e9 of them, 0.54 GB) take
-// 389 us at 7.7 warp instructions a state, 61% of the issue slots and 70% on the schedulers that got four warps, not three; the bytes
-// would take 80, the exponentials 107. Two blocks of two warps measured better than one of four (by 3%).
+// is formed from it eight channels at a time. Bound by waits, no pipe is full: eight rows of 2048 tokens of 4096 channels of 16 states (1.07e9 of
+// them, 0.54 GB) take 389 us at 7.7 warp instructions a state, with 61% of the issue slots taken (70% on the schedulers that got four warps, not
+// three), 54% of the shared-memory path, 47% of the multiply-adds' pipe and 38% of the exponentials'; a tile's preparing and finishing overlap
+// other blocks' walks only. The bytes would take 80, the exponentials 107. Two blocks of two warps measured better than one of four (by 3%).
 //
 // Few channels: the sequence is cut into segments. A first walk leaves each segment's state from zero and its sum of delta
 // (the decay across the segment is exp(A sum)), gla_ssm_scan the states entering them, a second walk y (one row of 16421
 // tokens: 213 + 14 + 341 us in 23 segments).
 //
-// gla_ssm_step: single and few tokens, bound by the states' bytes and their latency: a thread holds four states of a channel, of four
-// batch rows where there are many (the next token of 128 rows: 16 us, 4.4 TB/s).
+// gla_ssm_step: single and few tokens: a thread holds four states of a channel, of four batch rows where there are many. The next token of 128
+// rows of 4096 channels takes 17 us with cold caches (4.2 TB/s) and 14 call after call, when part of the states is still in L2: bound by the
+// states' latency and, with 67% of the issue slots taken, by instructions, as each of a channel's lanes forms its step and gate again.
 #include "gla_ssm.cuh"
 
 namespace gla {
@@ -428,7 +430,7 @@ cudaError_t step(const SsmArgs& a, cudaStream_t s)
     else gla_ssm_step_kernel<E, 64, ROWS><<<g, kStepNT, 0, s>>>(a);
     return cudaGetLastError();
 }
-// Four rows to a thread once that leaves every SM 1024 threads (128 rows of 4096 channels of 16 states: 22 us singly, 14 so).
+// Four rows to a thread once that leaves every SM 1024 threads (128 rows of 4096 channels of 16 states, call after call: 22 us singly, 14 so).
 template <typename E>
 cudaError_t step(const SsmArgs& a, int sms, cudaStream_t s)
 {

@@ -590,7 +590,8 @@ size_t gla_conv_bwd_workspace_size(const gla_conv_params* p);
  * A dt of -inf (with softplus; or of 0 without it and the bias) passes a token over: the state stays as it is. Other inputs are
  * finite, and where states grow (A above zero, or steps below) the growth over 16 tokens, exp of their sum of delta A, is an fp32 number.
  * x, dt, z, B and C are read through strides in elements (batch, token; a row contiguous), every row starting on 16 bytes;
- * strides may be zero or negative. D / G is a multiple of 8, N 8, 16, 32 or 64 (else GLA_ERR_UNSUPPORTED), D <= 2^20.
+ * strides may be zero or negative. A, S0, y, ST and the gradients of tokens' rows and states lie on 16 bytes too. D / G is a multiple of 8, N
+ * 8, 16, 32 or 64 (else GLA_ERR_UNSUPPORTED), D <= 2^20.
  * States and sums are fp32, y is rounded once; ST may equal S0. Up to eight tokens are taken one by one, longer calls in
  * tiles of 16; with few channels the sequence is cut into segments, whose states from zero come first. T = 0 copies S0 to
  * ST. Ownership and asynchrony are as for gla_fwd_ex.
@@ -609,7 +610,8 @@ typedef struct {
     int B, T, D, G, N;
     int softplus;
     gla_dtype dtype;
-    int force_segments;         /* 0: the planner chooses the sequence split; n >= 1: n segments (as many as there are tiles at most) */
+    int force_segments;         /* 0: the planner chooses the sequence split; n >= 1: n segments (at most 1024, and as many as there are
+                                   tiles; fewer where whole pairs of tiles make fewer) */
 } gla_ssm_params;
 
 /* y [B,T,D] dense, ST [B,D,N] or NULL (not written). The workspace is for the sequence split: gla_ssm_fwd_workspace_size()
